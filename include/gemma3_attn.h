@@ -324,6 +324,109 @@ int gemma3_cached_attention(const void* Q, const void* K_cache, const void* V_ca
                             int end_index, int H, int H_kv, int d_h, int window, void* workspace,
                             size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ 8-bit KV cache */
+
+/* A layer's KV cache in half the bytes: K' and V as e4m3 numbers, with one
+ * scale for each block of 64 slots and kv head, for K' and for V.
+ *   K8, V8            [B, S, H_kv, d_h] e4m3 (1 byte: sign, 4 exponent bits of
+ *                     bias 7, 3 mantissa bits; largest 448, 0x7F / 0xFF NaN),
+ *                     16-byte aligned
+ *   K_scale, V_scale  [B, ceil(S / 64), H_kv] fp32, a power of two in
+ *                     [2^-15, 2^8] wherever tokens were written
+ *   pos_cache         [B, S] int32 as in the fp16 cache (negative: no token)
+ * Slot s of head j holds the values K8[b, s, j, :] * K_scale[b, s / 64, j].
+ * A fresh cache has all positions negative and its other bytes zero.  Slots,
+ * positions, mask, padding and end_index as in the fp16 cache above: left
+ * aligned, the caller advances end_index, nothing wraps. */
+
+/* Slots of a scale block. */
+enum { GEMMA3_CACHE8_BLOCK = 64 };
+
+/* Writes T new tokens' K' / V rows (fp16, layout as gemma3_kv_cache_write) to
+ * slots [end_index, end_index + T) and their positions to pos_cache.
+ *   A block that held no slot below end_index gets the scale 2^e, the smallest
+ * with e >= -15 and |x| <= 448 * 2^e for every finite new value x of the
+ * block; a block that did gets the larger of that and its old scale, and if
+ * it grew, its numbers in slots below end_index are rounded again to the new
+ * one.  Numbers are value / scale rounded to e4m3, ties to even; infinities
+ * are stored as +-448, NaN as NaN.  Pad tokens (t >= T - pad_lens[b]) are
+ * stored as zeros with position -1.  Slots from end_index + T on keep their
+ * bytes, which stand for nothing until they are written (their block's scale
+ * may have changed). */
+int gemma3_kv_cache8_write(const void* K_rows, const void* V_rows, long ld_rows,
+                           const int32_t* segment_pos, const int32_t* pad_lens, int B, int T,
+                           int S, int end_index, int H_kv, int d_h, void* K8, void* V8,
+                           float* K_scale, float* V_scale, int32_t* pos_cache, void* stream);
+
+/* The values of slots [first, first + n) as fp16 rows: row b*n + i of K_rows
+ * and V_rows (row stride ld_rows elements, H_kv*d_h values each) gets slot
+ * first + i of batch row b, whatever its position (n = 0 is no work).  Exact,
+ * since a stored value is a multiple of 2^-24, but for values above 65504
+ * (fp16's largest; only inputs within half a step of it round there), which
+ * give 65504.  The rows suit gemma3_kv_cache_write. */
+int gemma3_kv_cache8_read(const void* K8, const void* V8, const float* K_scale,
+                          const float* V_scale, int B, int S, int first, int n, int H_kv, int d_h,
+                          void* K_rows, void* V_rows, long ld_rows, void* stream);
+
+/* Workspace of gemma3_cached8_attention (with_weights: weight_sum given). */
+int gemma3_cached8_attention_workspace_size(int B, int T, int S, int H, int H_kv, int d_h,
+                                            int with_weights, size_t* bytes);
+
+/* gemma3_cached_attention over an 8-bit cache: Q' [B, T, H, d_h] fp16 (query
+ * scale applied) of tokens already written to slots [end_index, end_index +
+ * T); O [B, T, H, d_h] in o_dtype (GEMMA3_BF16 | GEMMA3_F16; may alias Q'
+ * when weight_sum is NULL), rows that see no slot and pad rows 0; window <= 0
+ * means global.
+ *   weight_sum [B, S] fp32 or NULL: weight_sum[b, s] += the probabilities that
+ * the row's valid tokens and query heads gave slot s, in fp32 and always in
+ * the same order.  This is what gemma3_kv_cache8_evict ranks slots by.
+ *   What hidden slots hold (those that no token of the call sees) never
+ * matters, NaN included; a NaN in a slot that some token of the call sees may
+ * reach other tokens of the same call. */
+int gemma3_cached8_attention(const void* Q, const void* K8, const void* V8, const float* K_scale,
+                             const float* V_scale, const int32_t* pos_cache,
+                             const int32_t* segment_pos, const int32_t* pad_lens, void* O,
+                             int o_dtype, float* weight_sum, int B, int T, int S, int end_index,
+                             int H, int H_kv, int d_h, int window, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Eviction: of each batch row's slots [0, end_index) that hold a token, keeps
+ * those of the last `recent` slots and, up to `keep` in all, the others of
+ * the largest weight_sum (equal weights: the lower slot; -0 equals 0; NaN is
+ * below every number), and moves them in slot order to the slots 0, 1, ... of
+ * another cache of S_dst slots (a row with fewer tokens fills fewer).
+ *   0 <= recent <= keep, 1 <= keep <= S_dst, 0 <= end_index <= S.
+ *   kept [B, keep] int32: the slot that each place was filled from, -1 where
+ * a row had none; there pos_dst is -1 and the numbers and weight are zero.
+ *   Each block of the other cache gets the scale of its own values by the
+ * rule of gemma3_kv_cache8_write, numbers rounded again where it differs from
+ * the one they came with.  pos_dst and weight_dst [B, S_dst] take the kept
+ * slots' positions and weights.  Slots from `keep` on are left as they were;
+ * the next end_index is keep.  The two caches must not overlap. */
+int gemma3_kv_cache8_evict(const void* K8, const void* V8, const float* K_scale,
+                           const float* V_scale, const int32_t* pos_cache,
+                           const float* weight_sum, int B, int S, int end_index, int H_kv,
+                           int d_h, int keep, int recent, void* K8_dst, void* V8_dst,
+                           float* K_scale_dst, float* V_scale_dst, int32_t* pos_dst,
+                           float* weight_dst, int32_t* kept, int S_dst, void* stream);
+
+/* Workspace of gemma3_attn_forward_cached8. */
+int gemma3_attn_cached8_workspace_size(const gemma3_attn_dims* dims, int S, int with_weights,
+                                       size_t* bytes);
+
+/* gemma3_attn_forward_cached over an 8-bit cache: the new tokens' K' and V
+ * are stored as gemma3_kv_cache8_write does, and the tokens (a prompt's too)
+ * attend over what the cache then holds, as gemma3_cached8_attention does,
+ * weight_sum included (NULL: none). */
+int gemma3_attn_forward_cached8(const gemma3_attn_dims* dims, int S, int end_index, const void* x,
+                                const int32_t* segment_pos, const int32_t* pad_lens,
+                                const void* Wq, const void* Wkv, const void* Wo,
+                                const void* gamma_q, const void* gamma_k, int attn_type,
+                                int window, double rope_base, double rope_scale,
+                                float query_scale, void* K8, void* V8, float* K_scale,
+                                float* V_scale, int32_t* pos_cache, float* weight_sum, void* out,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------- stage entry points */
 
 /* C[M, N] = A[M, K] * W[N, K]^T (the projection einsums of [AB] How it

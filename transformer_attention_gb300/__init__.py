@@ -11,6 +11,9 @@ from ._lib import (  # noqa: F401  (re-exported C-ABI names)
     gemma3_attn_cached_workspace_size, gemma3_attn_check_status, gemma3_attn_forward,
     gemma3_attn_forward_cached, gemma3_attn_workspace_size, gemma3_cached_attention,
     gemma3_cached_attention_workspace_size, gemma3_kv_cache_write,
+    GEMMA3_CACHE8_BLOCK, gemma3_attn_cached8_workspace_size, gemma3_attn_forward_cached8,
+    gemma3_cached8_attention, gemma3_cached8_attention_workspace_size, gemma3_kv_cache8_evict,
+    gemma3_kv_cache8_read, gemma3_kv_cache8_write,
     gemma3_block_attn_forward, gemma3_block_attn_workspace_size, gemma3_block_ffn_forward,
     gemma3_block_ffn_workspace_size, gemma3_block_forward, gemma3_block_workspace_size,
     gemma3_cast_bf16_f16, gemma3_geglu,
@@ -21,8 +24,9 @@ from ._lib import (  # noqa: F401  (re-exported C-ABI names)
     gemma3_postnorm_residual, gemma3_qk_norm_rope, gemma3_query_scale, gemma3_rmsnorm,
     gemma3_selftest_wait_timeout, gemma3_set_gemm_tile_rows, lib)
 
-__all__ = ["attention_forward", "attention_forward_cached", "block_attention_forward",
-           "block_forward", "model_forward", "new_kv_cache", "linear", "lib"]
+__all__ = ["attention_forward", "attention_forward_cached", "attention_forward_cached8",
+           "block_attention_forward", "block_forward", "evict_kv_cache8", "model_forward",
+           "new_kv_cache", "new_kv_cache8", "linear", "lib"]
 
 
 def _empty_ws(nbytes: int, device):
@@ -84,6 +88,67 @@ def attention_forward_cached(x, segment_pos, pad_lens, cache, end_index, Wq, Wkv
                                query_scale, K_cache, V_cache, pos_cache, out, workspace,
                                workspace.numel(), stream)
     return out
+
+
+def new_kv_cache8(B, S, H_kv, d_h, device):
+    """An empty 8-bit KV cache of S slots per row: (K8, V8) [B, S, H_kv, d_h]
+    e4m3, (K_scale, V_scale) [B, ceil(S / 64), H_kv] fp32 and pos_cache [B, S]
+    int32, every stored position -1."""
+    import torch
+    nb = -(-S // GEMMA3_CACHE8_BLOCK)
+    K8 = torch.zeros((B, S, H_kv, d_h), dtype=torch.uint8, device=device)
+    V8 = torch.zeros_like(K8)
+    K_scale = torch.zeros((B, nb, H_kv), dtype=torch.float32, device=device)
+    pos = torch.full((B, S), -1, dtype=torch.int32, device=device)
+    return (K8.view(torch.float8_e4m3fn), V8.view(torch.float8_e4m3fn), K_scale,
+            torch.zeros_like(K_scale), pos)
+
+
+def attention_forward_cached8(x, segment_pos, pad_lens, cache, end_index, Wq, Wkv, Wo, gamma_q,
+                              gamma_k, *, H, H_kv, attn_type, window, rope_base, rope_scale,
+                              query_scale, weight_sum=None, out=None, workspace=None,
+                              stream=None):
+    """attention_forward_cached over an 8-bit cache from new_kv_cache8 (updated
+    in place).  weight_sum [B, S] fp32, if given, gains the probabilities that
+    every slot received.  Returns out [B,T,D] bf16."""
+    import torch
+    B, T, D = x.shape
+    d_h = gamma_q.shape[0]
+    K8, V8, K_scale, V_scale, pos_cache = cache
+    S = pos_cache.shape[1]
+    dims = (B, T, D, H, H_kv, d_h)
+    if workspace is None:
+        workspace = _empty_ws(gemma3_attn_cached8_workspace_size(dims, S, weight_sum is not None),
+                              x.device)
+    if out is None:
+        out = torch.empty((B, T, D), dtype=torch.bfloat16, device=x.device)
+    gemma3_attn_forward_cached8(dims, S, end_index, x, segment_pos, pad_lens, Wq, Wkv, Wo,
+                                gamma_q, gamma_k, attn_type, window, rope_base, rope_scale,
+                                query_scale, K8, V8, K_scale, V_scale, pos_cache, weight_sum, out,
+                                workspace, workspace.numel(), stream)
+    return out
+
+
+def evict_kv_cache8(cache, weight_sum, end_index, keep, recent, *, into=None, S=None,
+                    stream=None):
+    """The ``keep`` slots of an 8-bit cache that matter most: those of its last
+    ``recent`` slots and the heaviest others by weight_sum, moved in order to
+    the front of another cache.  Returns (cache, weight_sum [B, S], kept
+    [B, keep] int32, the slots they came from, -1 for none); the next
+    end_index is ``keep``.  ``into``: (cache, weight_sum) to fill, else new
+    ones of ``S`` slots (default: as many as before)."""
+    import torch
+    K8, V8, K_scale, V_scale, pos = cache
+    B, S0, H_kv, d_h = K8.shape
+    if into is None:
+        S = S0 if S is None else S
+        into = (new_kv_cache8(B, S, H_kv, d_h, K8.device),
+                torch.zeros((B, S), dtype=torch.float32, device=K8.device))
+    dst, w_dst = into
+    kept = torch.empty((B, keep), dtype=torch.int32, device=K8.device)
+    gemma3_kv_cache8_evict(K8, V8, K_scale, V_scale, pos, weight_sum, B, S0, end_index, H_kv, d_h,
+                           keep, recent, *dst, w_dst, kept, dst[4].shape[1], stream)
+    return dst, w_dst, kept
 
 
 def block_attention_forward(x, segment_pos, pad_lens, Wq, Wkv, Wo, gamma_q, gamma_k, gamma_pre,

@@ -20,6 +20,7 @@ GEMMA3_ERR_TIMEOUT = -5
 GEMMA3_ERR_BAD_INPUT = -7
 GEMMA3_LOCAL_SLIDING, GEMMA3_GLOBAL = 0, 1
 GEMMA3_BF16, GEMMA3_F16, GEMMA3_F32 = 0, 1, 2
+GEMMA3_CACHE8_BLOCK = 64
 MODEL_SIZES = {"270M": 0, "1B": 1, "4B": 2, "12B": 3, "27B": 4}
 
 
@@ -94,6 +95,20 @@ SIGNATURES = {
                                         c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
                                         c_int, c_int, c_int, c_int, c_void_p, c_size_t,
                                         c_void_p]),
+    "gemma3_kv_cache8_write": (c_int, [c_void_p, c_void_p, c_long, c_void_p, c_void_p] +
+                               [c_int] * 6 + [c_void_p] * 6),
+    "gemma3_kv_cache8_read": (c_int, [c_void_p] * 4 + [c_int] * 6 +
+                              [c_void_p, c_void_p, c_long, c_void_p]),
+    "gemma3_cached8_attention_workspace_size": (c_int, [c_int] * 7 + [ctypes.POINTER(c_size_t)]),
+    "gemma3_cached8_attention": (c_int, [c_void_p] * 9 + [c_int, c_void_p] + [c_int] * 8 +
+                                 [c_void_p, c_size_t, c_void_p]),
+    "gemma3_kv_cache8_evict": (c_int, [c_void_p] * 6 + [c_int] * 7 + [c_void_p] * 7 +
+                               [c_int, c_void_p]),
+    "gemma3_attn_cached8_workspace_size": (c_int, [ctypes.POINTER(gemma3_attn_dims), c_int, c_int,
+                                                   ctypes.POINTER(c_size_t)]),
+    "gemma3_attn_forward_cached8": (c_int, [ctypes.POINTER(gemma3_attn_dims), c_int, c_int] +
+                                    [c_void_p] * 8 + [c_int, c_int, c_double, c_double, c_float] +
+                                    [c_void_p] * 8 + [c_size_t, c_void_p]),
     "gemma3_geglu": (c_int, [c_void_p, c_long, c_void_p, c_long, c_void_p, c_long, c_int, c_int,
                              c_int, c_int, c_void_p]),
     "gemma3_linear": (c_int, [c_void_p, c_long, c_void_p, c_long, c_void_p, c_long, c_int, c_int,
@@ -357,6 +372,69 @@ def gemma3_cached_attention(Q, K_cache, V_cache, pos_cache, segment_pos, pad_len
         _ptr(Q), _ptr(K_cache), _ptr(V_cache), _ptr(pos_cache), _ptr(segment_pos),
         _ptr(pad_lens), _ptr(O), o_dtype, B, T, S, end_index, H, H_kv, d_h, window,
         _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def gemma3_kv_cache8_write(K_rows, V_rows, ld_rows, segment_pos, pad_lens, B, T, S, end_index,
+                           H_kv, d_h, K8, V8, K_scale, V_scale, pos_cache, stream=None):
+    return _check("gemma3_kv_cache8_write", lib().gemma3_kv_cache8_write(
+        _ptr(K_rows), _ptr(V_rows), ld_rows, _ptr(segment_pos), _ptr(pad_lens), B, T, S,
+        end_index, H_kv, d_h, _ptr(K8), _ptr(V8), _ptr(K_scale), _ptr(V_scale), _ptr(pos_cache),
+        _stream(stream)))
+
+
+def gemma3_kv_cache8_read(K8, V8, K_scale, V_scale, B, S, first, n, H_kv, d_h, K_rows, V_rows,
+                          ld_rows, stream=None):
+    return _check("gemma3_kv_cache8_read", lib().gemma3_kv_cache8_read(
+        _ptr(K8), _ptr(V8), _ptr(K_scale), _ptr(V_scale), B, S, first, n, H_kv, d_h,
+        _ptr(K_rows), _ptr(V_rows), ld_rows, _stream(stream)))
+
+
+def gemma3_cached8_attention_workspace_size(B, T, S, H, H_kv, d_h, with_weights=False) -> int:
+    n = c_size_t()
+    _check("gemma3_cached8_attention_workspace_size",
+           lib().gemma3_cached8_attention_workspace_size(B, T, S, H, H_kv, d_h,
+                                                         int(with_weights), ctypes.byref(n)))
+    return n.value
+
+
+def gemma3_cached8_attention(Q, K8, V8, K_scale, V_scale, pos_cache, segment_pos, pad_lens, O,
+                             o_dtype, weight_sum, B, T, S, end_index, H, H_kv, d_h, window,
+                             workspace, workspace_bytes, stream=None):
+    return _check("gemma3_cached8_attention", lib().gemma3_cached8_attention(
+        _ptr(Q), _ptr(K8), _ptr(V8), _ptr(K_scale), _ptr(V_scale), _ptr(pos_cache),
+        _ptr(segment_pos), _ptr(pad_lens), _ptr(O), o_dtype, _ptr(weight_sum), B, T, S,
+        end_index, H, H_kv, d_h, window, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def gemma3_kv_cache8_evict(K8, V8, K_scale, V_scale, pos_cache, weight_sum, B, S, end_index, H_kv,
+                           d_h, keep, recent, K8_dst, V8_dst, K_scale_dst, V_scale_dst, pos_dst,
+                           weight_dst, kept, S_dst, stream=None):
+    return _check("gemma3_kv_cache8_evict", lib().gemma3_kv_cache8_evict(
+        _ptr(K8), _ptr(V8), _ptr(K_scale), _ptr(V_scale), _ptr(pos_cache), _ptr(weight_sum), B, S,
+        end_index, H_kv, d_h, keep, recent, _ptr(K8_dst), _ptr(V8_dst), _ptr(K_scale_dst),
+        _ptr(V_scale_dst), _ptr(pos_dst), _ptr(weight_dst), _ptr(kept), S_dst, _stream(stream)))
+
+
+def gemma3_attn_cached8_workspace_size(dims, S, with_weights=False) -> int:
+    n = c_size_t()
+    d = _dims(*dims)
+    _check("gemma3_attn_cached8_workspace_size",
+           lib().gemma3_attn_cached8_workspace_size(ctypes.byref(d), S, int(with_weights),
+                                                    ctypes.byref(n)))
+    return n.value
+
+
+def gemma3_attn_forward_cached8(dims, S, end_index, x, segment_pos, pad_lens, Wq, Wkv, Wo,
+                                gamma_q, gamma_k, attn_type, window, rope_base, rope_scale,
+                                query_scale, K8, V8, K_scale, V_scale, pos_cache, weight_sum, out,
+                                workspace, workspace_bytes, stream=None):
+    d = _dims(*dims)
+    return _check("gemma3_attn_forward_cached8", lib().gemma3_attn_forward_cached8(
+        ctypes.byref(d), S, end_index, _ptr(x), _ptr(segment_pos), _ptr(pad_lens), _ptr(Wq),
+        _ptr(Wkv), _ptr(Wo), _ptr(gamma_q), _ptr(gamma_k), attn_type, window, rope_base,
+        rope_scale, query_scale, _ptr(K8), _ptr(V8), _ptr(K_scale), _ptr(V_scale),
+        _ptr(pos_cache), _ptr(weight_sum), _ptr(out), _ptr(workspace), workspace_bytes,
+        _stream(stream)))
 
 
 def gemma3_geglu(A, lda, W_gating, ldw, Z, ldz, M, D_ff, K, in_dtype, stream=None):

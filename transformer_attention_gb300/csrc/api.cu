@@ -772,6 +772,235 @@ int gemma3_cached_attention(const void* Q, const void* K_cache, const void* V_ca
                                            workspace, as_stream(stream), st));
 }
 
+// ------------------------------------------------------------ 8-bit KV cache
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Shapes and pointers of an 8-bit cache of which the slots [0, used) are named.
+int validate_cache8(int B, int S, long long used, int H_kv, int d_h, const void* K8,
+                    const void* V8, const float* K_scale, const float* V_scale) {
+  if (!K8 || !V8 || !K_scale || !V_scale) return GEMMA3_ERR_INVALID_ARG;
+  if (d_h != 128 && d_h != 256) return GEMMA3_ERR_UNSUPPORTED;
+  if (B < 1 || B > 65535 || H_kv < 1 || H_kv > 65535 || S < 1 || S > (1 << 30) || used < 0 ||
+      used > S)
+    return GEMMA3_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * S >= (1LL << 40) / (static_cast<long long>(H_kv) * d_h))
+    return GEMMA3_ERR_INVALID_ARG;
+  if (!aligned16(K8) || !aligned16(V8) || !aligned4(K_scale) || !aligned4(V_scale))
+    return GEMMA3_ERR_MISALIGNED;
+  return GEMMA3_OK;
+}
+
+int validate_rows8(const void* K_rows, const void* V_rows, long ld_rows, int H_kv, int d_h) {
+  if (!K_rows || !V_rows || ld_rows < static_cast<long>(H_kv) * d_h) return GEMMA3_ERR_INVALID_ARG;
+  if (!aligned16(K_rows) || !aligned16(V_rows) || (ld_rows * 2) % 16) return GEMMA3_ERR_MISALIGNED;
+  return GEMMA3_OK;
+}
+
+struct Span {
+  const void* p;
+  size_t n;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.n && y < x + a.n;
+}
+
+struct Cached8Ws {
+  size_t q, kv, o, attn, total;
+};
+
+Cached8Ws cached8_ws(const gemma3_attn_dims* d, int S, bool weights) {
+  const size_t M = static_cast<size_t>(d->B) * d->T;
+  Cached8Ws w;
+  w.q = round_up(M * d->H * d->d_h * 2, 256);
+  w.kv = round_up(M * 2 * d->H_kv * d->d_h * 2, 256);
+  w.o = weights ? w.q : 0;   // Q' is read again for the weights
+  w.attn = round_up(cached8_attention_ws_bytes(d->B, d->T, S, d->H, d->H_kv, d->d_h, weights), 256);
+  w.total = w.q + w.kv + w.o + w.attn;
+  return w;
+}
+
+}  // namespace
+
+int gemma3_kv_cache8_write(const void* K_rows, const void* V_rows, long ld_rows,
+                           const int32_t* segment_pos, const int32_t* pad_lens, int B, int T,
+                           int S, int end_index, int H_kv, int d_h, void* K8, void* V8,
+                           float* K_scale, float* V_scale, int32_t* pos_cache, void* stream) {
+  if (T < 1 || end_index < 0 || !segment_pos || !pos_cache) return GEMMA3_ERR_INVALID_ARG;
+  int rc = validate_cache8(B, S, static_cast<long long>(end_index) + T, H_kv, d_h, K8, V8, K_scale,
+                           V_scale);
+  if (rc != GEMMA3_OK) return rc;
+  rc = validate_rows8(K_rows, V_rows, ld_rows, H_kv, d_h);
+  if (rc != GEMMA3_OK) return rc;
+  if (!aligned4(segment_pos) || !aligned4(pad_lens) || !aligned4(pos_cache))
+    return GEMMA3_ERR_MISALIGNED;
+  rc = check_device();
+  if (rc != GEMMA3_OK) return rc;
+  return to_status(launch_cache8_write(K_rows, V_rows, ld_rows, segment_pos, pad_lens, B, T, S,
+                                       end_index, H_kv, d_h, K8, V8, K_scale, V_scale, pos_cache,
+                                       as_stream(stream)));
+}
+
+int gemma3_kv_cache8_read(const void* K8, const void* V8, const float* K_scale,
+                          const float* V_scale, int B, int S, int first, int n, int H_kv, int d_h,
+                          void* K_rows, void* V_rows, long ld_rows, void* stream) {
+  if (first < 0 || n < 0) return GEMMA3_ERR_INVALID_ARG;
+  int rc = validate_cache8(B, S, static_cast<long long>(first) + n, H_kv, d_h, K8, V8, K_scale,
+                           V_scale);
+  if (rc != GEMMA3_OK) return rc;
+  rc = validate_rows8(K_rows, V_rows, ld_rows, H_kv, d_h);
+  if (rc != GEMMA3_OK) return rc;
+  rc = check_device();
+  if (rc != GEMMA3_OK) return rc;
+  return to_status(launch_cache8_read(K8, V8, K_scale, V_scale, B, S, first, n, H_kv, d_h, K_rows,
+                                      V_rows, ld_rows, as_stream(stream)));
+}
+
+int gemma3_cached8_attention_workspace_size(int B, int T, int S, int H, int H_kv, int d_h,
+                                            int with_weights, size_t* bytes) {
+  if (bytes == nullptr || B < 1 || T < 1 || S < 1 || S > (1 << 30) || H < 1 || H_kv < 1 ||
+      H % H_kv)
+    return GEMMA3_ERR_INVALID_ARG;
+  const int G = H / H_kv;
+  if ((d_h != 128 && d_h != 256) || (G != 1 && G != 2 && G != 4)) return GEMMA3_ERR_UNSUPPORTED;
+  if (B > 65535 || static_cast<long long>(B) * T * H >= (1LL << 31)) return GEMMA3_ERR_INVALID_ARG;
+  *bytes = round_up(cached8_attention_ws_bytes(B, T, S, H, H_kv, d_h, with_weights != 0), 256);
+  return GEMMA3_OK;
+}
+
+int gemma3_cached8_attention(const void* Q, const void* K8, const void* V8, const float* K_scale,
+                             const float* V_scale, const int32_t* pos_cache,
+                             const int32_t* segment_pos, const int32_t* pad_lens, void* O,
+                             int o_dtype, float* weight_sum, int B, int T, int S, int end_index,
+                             int H, int H_kv, int d_h, int window, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  int rc = gemma3_cached8_attention_workspace_size(B, T, S, H, H_kv, d_h, weight_sum != nullptr,
+                                                   &need);
+  if (rc != GEMMA3_OK) return rc;
+  if (!Q || !O || !segment_pos || !pos_cache || !workspace || end_index < 0)
+    return GEMMA3_ERR_INVALID_ARG;
+  if (o_dtype != GEMMA3_BF16 && o_dtype != GEMMA3_F16) return GEMMA3_ERR_INVALID_ARG;
+  rc = validate_cache8(B, S, static_cast<long long>(end_index) + T, H_kv, d_h, K8, V8, K_scale,
+                       V_scale);
+  if (rc != GEMMA3_OK) return rc;
+  if (!aligned16(Q) || !aligned16(O) || !aligned4(segment_pos) || !aligned4(pad_lens) ||
+      !aligned4(pos_cache) || !aligned4(weight_sum) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return GEMMA3_ERR_MISALIGNED;
+  const size_t qn = static_cast<size_t>(B) * T * H * d_h * 2;
+  if (weight_sum != nullptr && overlap({Q, qn}, {O, qn})) return GEMMA3_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return GEMMA3_ERR_WORKSPACE;
+  rc = check_device();
+  if (rc != GEMMA3_OK) return rc;
+  int* st = status_ptr();
+  if (st == nullptr) return GEMMA3_ERR_CUDA;
+  return to_status(launch_cached8_attention(
+      Q, K8, V8, K_scale, V_scale, pos_cache, segment_pos, pad_lens, O,
+      o_dtype == GEMMA3_F16 ? kF16 : kBF16, weight_sum, B, T, S, end_index, H, H_kv, d_h,
+      window > 0 ? window : 0, workspace, as_stream(stream), st));
+}
+
+int gemma3_kv_cache8_evict(const void* K8, const void* V8, const float* K_scale,
+                           const float* V_scale, const int32_t* pos_cache,
+                           const float* weight_sum, int B, int S, int end_index, int H_kv,
+                           int d_h, int keep, int recent, void* K8_dst, void* V8_dst,
+                           float* K_scale_dst, float* V_scale_dst, int32_t* pos_dst,
+                           float* weight_dst, int32_t* kept, int S_dst, void* stream) {
+  if (!pos_cache || !weight_sum || !pos_dst || !weight_dst || !kept) return GEMMA3_ERR_INVALID_ARG;
+  int rc = validate_cache8(B, S, end_index, H_kv, d_h, K8, V8, K_scale, V_scale);
+  if (rc != GEMMA3_OK) return rc;
+  if (keep < 1 || recent < 0 || recent > keep) return GEMMA3_ERR_INVALID_ARG;
+  rc = validate_cache8(B, S_dst, keep, H_kv, d_h, K8_dst, V8_dst, K_scale_dst, V_scale_dst);
+  if (rc != GEMMA3_OK) return rc;
+  if (!aligned4(pos_cache) || !aligned4(weight_sum) || !aligned4(pos_dst) ||
+      !aligned4(weight_dst) || !aligned4(kept))
+    return GEMMA3_ERR_MISALIGNED;
+  const size_t src = static_cast<size_t>(B) * S, dst = static_cast<size_t>(B) * S_dst;
+  const size_t kvd = static_cast<size_t>(H_kv) * d_h;
+  const size_t sn = static_cast<size_t>(B) * c8_blocks(S) * H_kv * 4;
+  const size_t dn = static_cast<size_t>(B) * c8_blocks(S_dst) * H_kv * 4;
+  const Span in[] = {{K8, src * kvd}, {V8, src * kvd},   {K_scale, sn},
+                     {V_scale, sn},   {pos_cache, src * 4}, {weight_sum, src * 4}};
+  const Span outs[] = {{K8_dst, dst * kvd}, {V8_dst, dst * kvd},  {K_scale_dst, dn},
+                       {V_scale_dst, dn},   {pos_dst, dst * 4},   {weight_dst, dst * 4},
+                       {kept, static_cast<size_t>(B) * keep * 4}};
+  for (size_t i = 0; i < sizeof(outs) / sizeof(outs[0]); ++i) {
+    for (const Span& a : in)
+      if (overlap(a, outs[i])) return GEMMA3_ERR_INVALID_ARG;
+    for (size_t k = 0; k < i; ++k)
+      if (overlap(outs[k], outs[i])) return GEMMA3_ERR_INVALID_ARG;
+  }
+  rc = check_device();
+  if (rc != GEMMA3_OK) return rc;
+  return to_status(launch_cache8_evict(K8, V8, K_scale, V_scale, pos_cache, weight_sum, B, S,
+                                       end_index, H_kv, d_h, keep, recent, K8_dst, V8_dst,
+                                       K_scale_dst, V_scale_dst, pos_dst, weight_dst, kept, S_dst,
+                                       as_stream(stream)));
+}
+
+int gemma3_attn_cached8_workspace_size(const gemma3_attn_dims* dims, int S, int with_weights,
+                                       size_t* bytes) {
+  const int rc = validate_dims(dims);
+  if (rc != GEMMA3_OK) return rc;
+  if (bytes == nullptr || S < 1 || S > (1 << 30) || dims->B > 65535 ||
+      static_cast<long long>(dims->B) * dims->T * dims->H >= (1LL << 31))
+    return GEMMA3_ERR_INVALID_ARG;
+  *bytes = cached8_ws(dims, S, with_weights != 0).total;
+  return GEMMA3_OK;
+}
+
+int gemma3_attn_forward_cached8(const gemma3_attn_dims* dims, int S, int end_index, const void* x,
+                                const int32_t* segment_pos, const int32_t* pad_lens,
+                                const void* Wq, const void* Wkv, const void* Wo,
+                                const void* gamma_q, const void* gamma_k, int attn_type,
+                                int window, double rope_base, double rope_scale,
+                                float query_scale, void* K8, void* V8, float* K_scale,
+                                float* V_scale, int32_t* pos_cache, float* weight_sum, void* out,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = validate_layer_args(dims, x, segment_pos, Wq, Wkv, Wo, gamma_q, gamma_k, attn_type,
+                               window, rope_base, rope_scale, workspace);
+  if (rc != GEMMA3_OK) return rc;
+  const gemma3_attn_dims* d = dims;
+  if (!pos_cache || !out || end_index < 0) return GEMMA3_ERR_INVALID_ARG;
+  rc = validate_cache8(d->B, S, static_cast<long long>(end_index) + d->T, d->H_kv, d->d_h, K8, V8,
+                       K_scale, V_scale);
+  if (rc != GEMMA3_OK) return rc;
+  if (!aligned16(out) || !aligned4(segment_pos) || !aligned4(pad_lens) || !aligned4(pos_cache) ||
+      !aligned4(weight_sum))
+    return GEMMA3_ERR_MISALIGNED;
+  size_t need = 0;
+  rc = gemma3_attn_cached8_workspace_size(dims, S, weight_sum != nullptr, &need);
+  if (rc != GEMMA3_OK) return rc;
+  if (workspace_bytes < need) return GEMMA3_ERR_WORKSPACE;
+  const Cached8Ws w = cached8_ws(dims, S, weight_sum != nullptr);
+  int* st = status_ptr();
+  if (st == nullptr) return GEMMA3_ERR_CUDA;
+  const int M = d->B * d->T;
+  const int HD = d->H * d->d_h, KVD = d->H_kv * d->d_h;
+  uint8_t* qbuf = static_cast<uint8_t*>(workspace);       // Q' [M, H*d_h] fp16
+  uint8_t* kvbuf = qbuf + w.q;                            // [K'|V] fp16 [M, 2*KVD]
+  uint8_t* obuf = weight_sum != nullptr ? kvbuf + w.kv : qbuf;   // O bf16
+  uint8_t* aws = kvbuf + w.kv + w.o;
+  cudaStream_t s = as_stream(stream);
+  const int win = attn_type == GEMMA3_LOCAL_SLIDING ? window : 0;
+  if (project_qk(x, d->D, kBF16, Wq, Wkv, qbuf, kvbuf, gamma_q, gamma_k, segment_pos, M, d->D,
+                 d->H, d->H_kv, d->d_h, rope_base, rope_scale, query_scale, s,
+                 st) != cudaSuccess ||
+      launch_cache8_write(kvbuf, kvbuf + KVD * 2, 2 * KVD, segment_pos, pad_lens, d->B, d->T, S,
+                          end_index, d->H_kv, d->d_h, K8, V8, K_scale, V_scale, pos_cache,
+                          s) != cudaSuccess ||
+      launch_cached8_attention(qbuf, K8, V8, K_scale, V_scale, pos_cache, segment_pos, pad_lens,
+                               obuf, kBF16, weight_sum, d->B, d->T, S, end_index, d->H, d->H_kv,
+                               d->d_h, win, aws, s, st) != cudaSuccess)
+    return GEMMA3_ERR_CUDA;
+  return to_status(launch_linear(obuf, HD, Wo, HD, out, d->D, M, d->D, HD, kBF16, kBF16, s, st, 0));
+}
+
 int gemma3_geglu(const void* A, long lda, const void* W_gating, long ldw, void* Z, long ldz,
                  int M, int D_ff, int K, int in_dtype, void* stream) {
   if (!A || !W_gating || !Z || M < 0 || D_ff < 1 || K < 1) return GEMMA3_ERR_INVALID_ARG;

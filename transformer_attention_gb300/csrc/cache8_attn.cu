@@ -1,0 +1,760 @@
+// Attention of new tokens over the 8-bit KV cache (cache8.cuh), and the
+// weight that each slot received.
+//
+//   O[t, h] = sum_s p_s v_s,  p = softmax over the visible slots of q . k_s
+//   weight_sum[s] += sum over the row's valid tokens and heads of p_s
+//
+// Visible slots as in decode.cu: s <= end + t, a stored position >= 0 and, on
+// a local layer, within the window of the query's position.
+//
+// decode8_kernel (few query rows, T * G <= 16 of a kv head at a time).  Every
+// byte of the cache is read once and meets at most 16 query rows, so HBM
+// bounds it: d_h = 128 needs 256 bytes per slot and kv head.  The two
+// contractions run on mma.sync m16n8k16 with the slots (K) and the channels
+// (V) on the 16-row side and the query rows on the 8-wide side: at one byte
+// per number the fp32 CUDA cores would need 4 FMAs per byte for 4 rows, about
+// their whole rate at the HBM rate, while these MMAs take under a fifth of
+// theirs (measured 1024 fp16 FMA per clock and SM).  A tcgen05 tile has 128
+// rows for which there are no queries, and could take the e4m3 bytes as they
+// are only if the probabilities were split into 8-bit parts; many rows go to
+// the tcgen05 kernel (cache8_flash.cu).
+//   - The bytes go from the swizzled TMA tile straight into MMA fragments:
+//     the contraction over channels does not care for their order, so a
+//     thread's 4 consecutive channels serve as its k columns {2c, 2c+1, 2c+8,
+//     2c+9}, and Q's fragments are permuted alike.  V needs slots along k:
+//     ldmatrix.trans on byte pairs and one byte permutation give the
+//     fragments of 16 channels.
+//   - e4m3 numbers are exact in fp16; scales multiply the logits (K) and the
+//     fp32 accumulator (V) in fp32: the accumulator is kept in units of the
+//     current block's V scale and changes unit in the multiplication that the
+//     running maximum asks for anyway.
+//   - The probabilities are rounded to fp16 for the V product (relative error
+//     2^-11 each, averaged over slots; below the fp16 or bf16 output's own
+//     rounding); sums and maxima are fp32.
+// The slots of a (row, kv head) are split over CTAs, and a second launch
+// merges the parts and, for weight_sum, adds up exp2(logit - max) / sum from
+// the logits that the first one left in the workspace (4 bytes per query row
+// and slot, against 2 d_h for K' and V; reading K' again would cost d_h).
+#include <algorithm>
+#include <climits>
+
+#include "cache8.cuh"
+#include "decode_span.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace g3 {
+
+namespace {
+
+constexpr int kTile = kC8Block;      // slots per tile: one scale block
+constexpr int kCWarps = 4;           // consumer warps, 16 slots of each tile each
+constexpr int kThreads = (kCWarps + 1) * 32;
+constexpr int kMaxSplits = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum { kSiteFull = 50, kSiteEmpty = 51 };
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void named_barrier(int id, int nthreads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int DH, int NT>
+struct Cfg {
+  static constexpr int NCH = DH / 128;                  // 128-byte column boxes of a row
+  static constexpr int BOX = kTile * 128;
+  static constexpr int TILE = 2 * NCH * BOX;            // K' and V of one tile
+  static constexpr int NST = DH == 256 ? 3 : 6;         // ring stages (96 KB either way)
+  static constexpr int RING = NST * TILE;
+  static constexpr int NC = DH / 16;                    // 16-channel chunks
+  static constexpr int QF = NC * NT * 32 * 8;           // Q fragments
+  static constexpr int ROWS = NT * 8;
+  static constexpr int LDM = DH + 8;                    // merge record row, floats
+  static constexpr int MERGE = kCWarps * ROWS * LDM * 4;
+  static constexpr int SMEM = 1024 + RING + QF;
+  static_assert(MERGE <= RING, "merge records must fit in the ring");
+  static_assert(SMEM <= 112 * 1024, "two CTAs per SM");
+};
+
+struct Params {
+  const __half* Q;            // [B, T, H, DH], query scale applied
+  const float* K_scale;       // [B, nb, H_kv]
+  const float* V_scale;
+  const int32_t* posc;        // [B, S]
+  const int32_t* qpos;        // [B, T]
+  const int32_t* pad_lens;    // [B] or null
+  const int32_t* span_part;   // [B, nchunk] or null
+  float2* stat;               // [B*T*H, nsplit] (max, sum) of each part
+  float* part;                // [B*T*H, nsplit, DH] unnormalised, when nsplit > 1
+  float* logits;              // [B, H_kv, T*G, S64] base-2 logits, or null
+  void* O;
+  int o_f16, B, T, S, H, H_kv, nb, end, window, nsplit, nchunk, tq, ntg;
+  int* status;
+};
+
+__device__ __forceinline__ int first_visible(const int32_t* span_part, int nchunk, int b, int lane) {
+  int lo = 0;
+  if (span_part != nullptr) {
+    lo = INT_MAX;
+    for (int i = lane; i < nchunk; i += 32)
+      lo = min(lo, span_part[static_cast<size_t>(b) * nchunk + i]);
+    lo = span_warp_min(lo);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void store_o(void* O, int o_f16, size_t at, float v) {
+  if (o_f16)
+    static_cast<__half*>(O)[at] = __float2half_rn(v);
+  else
+    static_cast<__nv_bfloat16*>(O)[at] = __float2bfloat16_rn(v);
+}
+
+template <int DH, int NT>
+__global__ void __launch_bounds__(kThreads, 2)
+    decode8_kernel(const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const Params p) {
+  pdl_enter();
+  using C = Cfg<DH, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* ring = smem;
+  uint2* qf = reinterpret_cast<uint2*>(smem + C::RING);       // [NC][NT][32]
+  __shared__ __align__(8) uint64_t full[C::NST], empty[C::NST];
+  __shared__ int abort_flag;
+  __shared__ int rng[3];
+  __shared__ float2 mstat[kCWarps][C::ROWS];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int split = blockIdx.x, j = blockIdx.y;
+  const int b = blockIdx.z / p.ntg, tg = blockIdx.z % p.ntg;
+  const int G = p.H / p.H_kv;
+  const int t0 = tg * p.tq;
+  const int ntok = min(p.tq, p.T - t0);
+  const int R = ntok * G;
+  const int valid = p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0);
+
+  if (tid == 0) {
+#pragma unroll
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), kCWarps);
+    }
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kCWarps) {
+    // Visible slots of this CTA's rows lie in [lo, hi): whole tiles of them,
+    // evenly over the nsplit CTAs of (b, j, tg).
+    int lo = first_visible(p.span_part, p.nchunk, b, lane);
+    const int t_last = min(t0 + ntok, valid) - 1;
+    const int hi = t_last >= t0 ? p.end + t_last + 1 : 0;
+    lo = min(lo, hi);
+    const int k0 = lo / kTile, k1 = (hi + kTile - 1) / kTile;
+    const int per = (k1 - k0 + p.nsplit - 1) / p.nsplit;
+    const long long a = k0 + static_cast<long long>(split) * per;
+    if (lane == 0) {
+      rng[0] = static_cast<int>(min(a, static_cast<long long>(k1)));
+      rng[1] = static_cast<int>(min(a + per, static_cast<long long>(k1)));
+      rng[2] = hi;
+    }
+  }
+  // Q fragments: k columns {2c, 2c+1, 2c+8, 2c+9} of a 16-channel chunk are
+  // the channels 4c .. 4c+3, row n = lane / 4.
+  for (int i = tid; i < C::NC * NT * 32; i += kThreads) {
+    const int l = i & 31, nt = (i >> 5) % NT, ch = (i >> 5) / NT;
+    const int r = nt * 8 + (l >> 2);
+    uint2 q = make_uint2(0, 0);
+    if (r < R) {
+      const int t = t0 + r / G, h = j * G + r % G;
+      q = __ldg(reinterpret_cast<const uint2*>(
+          p.Q + ((static_cast<size_t>(b) * p.T + t) * p.H + h) * DH + ch * 16 + (l & 3) * 4));
+    }
+    qf[i] = q;
+  }
+  __syncthreads();
+  const int k_lo = rng[0], n_tiles = rng[1] - rng[0], hi = rng[2];
+
+  if (warp == kCWarps) {
+    // ---------------- producer: K'/V tiles of 64 slots into the ring
+    if (lane == 0 && n_tiles > 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      int issued = 0;
+      for (int i = 0; i < n_tiles; ++i) {
+        const int st = i % C::NST;
+        if (i >= C::NST && !mbar_wait(smem_u32(&empty[st]), ((i / C::NST) - 1) & 1, &abort_flag,
+                                      p.status, kSiteEmpty))
+          break;
+        const uint32_t bar = smem_u32(&full[st]);
+        mbar_arrive_expect_tx(bar, C::TILE);
+        uint8_t* kd = ring + st * C::TILE;
+        uint8_t* vd = kd + C::NCH * C::BOX;
+        const int s0 = (k_lo + i) * kTile;
+#pragma unroll
+        for (int ch = 0; ch < C::NCH; ++ch) {
+          tma_load_4d(smem_u32(kd + ch * C::BOX), &tmK, bar, ch * 128, j, s0, b);
+          tma_load_4d(smem_u32(vd + ch * C::BOX), &tmV, bar, ch * 128, j, s0, b);
+        }
+        issued = i + 1;
+      }
+      // Every issued load lands before the CTA may exit.
+      for (int i = max(0, issued - C::NST); i < issued; ++i)
+        mbar_wait_drain(smem_u32(&full[i % C::NST]), (i / C::NST) & 1);
+    }
+    return;
+  }
+
+  // ---------------- consumers: warp w takes slots 16w .. 16w+15 of every tile
+  // Rows of this thread: nt * 8 + 2c + e; slots g and g + 8 of the warp's 16.
+  int lim[NT][2], plo[NT][2], phi[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = nt * 8 + 2 * c + e;
+      lim[nt][e] = -1;
+      plo[nt][e] = 0;
+      phi[nt][e] = INT_MAX;
+      if (r < R && t0 + r / G < valid) {
+        const int t = t0 + r / G;
+        lim[nt][e] = p.end + t;
+        if (p.window > 0) {
+          const long long qp = p.qpos[static_cast<size_t>(b) * p.T + t];
+          plo[nt][e] = static_cast<int>(max(0LL, min(qp - p.window + 1, (long long)INT_MAX)));
+          phi[nt][e] = static_cast<int>(max(-1LL, min(qp + p.window - 1, (long long)INT_MAX)));
+        }
+      }
+    }
+  float m[NT][2], l[NT][2], o[C::NC][NT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int ch = 0; ch < C::NC; ++ch)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[ch][nt][e] = 0.f;
+  }
+  float unit = 1.f;                  // V scale that o is in units of
+  const float* ksp = p.K_scale + (static_cast<size_t>(b) * p.nb) * p.H_kv + j;
+  const float* vsp = p.V_scale + (static_cast<size_t>(b) * p.nb) * p.H_kv + j;
+  const int32_t* posr = p.posc + static_cast<size_t>(b) * p.S;
+  const int so = warp * 16 + g;      // this thread's first slot within a tile
+
+  // ldmatrix row addresses within a box: matrices (slots 0-7 | 8-15) x (two
+  // 16-byte chunks), chunk XORed with the slot's low bits by the TMA swizzle.
+  const int mrow = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+  const int mch = lane >> 4;
+  const uint32_t roff = mrow * 128, rxor = mrow & 7;
+
+  // the next tile's positions and scales are fetched a tile ahead
+  int pos0 = -1, pos1 = -1;
+  float ks = 0.f, vs = 0.f;
+  auto fetch = [&](int i) {
+    pos0 = pos1 = -1;
+    if (i < n_tiles) {
+      const int s = (k_lo + i) * kTile + so;
+      if (s < hi) pos0 = __ldg(posr + s);
+      if (s + 8 < hi) pos1 = __ldg(posr + s + 8);
+      ks = __ldg(ksp + static_cast<size_t>(k_lo + i) * p.H_kv);
+      vs = __ldg(vsp + static_cast<size_t>(k_lo + i) * p.H_kv);
+    }
+  };
+  fetch(0);
+  for (int i = 0; i < n_tiles; ++i) {
+    const int st = i % C::NST;
+    const int s = (k_lo + i) * kTile + so;
+    const int ps0 = pos0, ps1 = pos1;
+    const float kl = ks * kLog2e, vsc = vs;
+    fetch(i + 1);
+    // visible (row, slot) pairs, and per slot whether any row sees it
+    bool vis[NT][4];
+    bool any0 = false, any1 = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        vis[nt][e] = ps0 >= plo[nt][e] && ps0 <= phi[nt][e] && s <= lim[nt][e];
+        vis[nt][2 + e] = ps1 >= plo[nt][e] && ps1 <= phi[nt][e] && s + 8 <= lim[nt][e];
+        any0 |= vis[nt][e];
+        any1 |= vis[nt][2 + e];
+      }
+    const unsigned b0 = __ballot_sync(0xffffffffu, any0), b1 = __ballot_sync(0xffffffffu, any1);
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[st]), (i / C::NST) & 1,
+                                                      &abort_flag, p.status, kSiteFull));
+    if (!ok) break;
+    float* lg = nullptr;
+    if (p.logits != nullptr)
+      lg = p.logits + ((static_cast<size_t>(b) * p.H_kv + j) * (p.T * G) + t0 * G) *
+                          (static_cast<size_t>(p.nb) * kTile) + s;
+    if ((b0 | b1) != 0) {
+      const uint32_t kt = smem_u32(ring + st * C::TILE);
+      // S^T (16 slots x 8 rows): two accumulators shorten the chain
+      float acc[2][NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[0][nt][e] = acc[1][nt][e] = 0.f;
+#pragma unroll
+      for (int cp = 0; cp < C::NC / 2; ++cp) {
+        uint32_t r[4];
+        const int ch = cp * 2 + mch;
+        ldsm4(kt + (cp >> 2) * C::BOX + roff + (((ch & 7) ^ rxor) << 4), r);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t a0 = c8_half2(r[2 * u]), a2 = c8_half2_hi(r[2 * u]);
+          const uint32_t a1 = c8_half2(r[2 * u + 1]), a3 = c8_half2_hi(r[2 * u + 1]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 q = qf[((cp * 2 + u) * NT + nt) * 32 + lane];
+            mma16816(acc[u][nt], a0, a1, a2, a3, q.x, q.y);
+          }
+        }
+      }
+      // online softmax in base 2; o changes its unit to this block's V scale
+      uint32_t pb[NT][2];
+      float f[NT][2];
+      const float du = unit / vsc;
+      bool same = true;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = vis[nt][e] ? (acc[0][nt][e] + acc[1][nt][e]) * kl : -INFINITY;
+        if (lg != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = nt * 8 + 2 * c + (e & 1);
+            if (row < R)
+              lg[static_cast<size_t>(row) * (static_cast<size_t>(p.nb) * kTile) + (e >> 1) * 8] =
+                  x[e];
+          }
+        }
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(x[e], x[2 + e]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float mn = fmaxf(m[nt][e], mx);
+          const float ref = mn == -INFINITY ? 0.f : mn;
+          const float al = ex2(m[nt][e] - ref);     // 0 before the first visible slot
+          m[nt][e] = mn;
+          pr[e] = ex2(x[e] - ref);
+          pr[2 + e] = ex2(x[2 + e] - ref);
+          l[nt][e] = fmaf(l[nt][e], al, pr[e] + pr[2 + e]);
+          f[nt][e] = al * du;
+          same &= f[nt][e] == 1.f;
+        }
+        pb[nt][0] = transpose8x8(pack_half2(pr[0], pr[1]));
+        pb[nt][1] = transpose8x8(pack_half2(pr[2], pr[3]));
+      }
+      unit = vsc;
+      if (!__all_sync(0xffffffffu, same)) {
+#pragma unroll
+        for (int ch = 0; ch < C::NC; ++ch)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[ch][nt][e] *= f[nt][e & 1];
+      }
+      // slots that no row sees count as zero whatever they hold (a NaN there
+      // would survive its zero probability)
+      uint32_t v0 = 0xffffffffu, v1 = 0xffffffffu;
+      {
+        unsigned n0 = b0 | (b0 >> 1), n1 = b1 | (b1 >> 1);
+        n0 = (n0 | (n0 >> 2)) & 0x11111111u;
+        n1 = (n1 | (n1 >> 2)) & 0x11111111u;
+        if (n0 != 0x11111111u || n1 != 0x11111111u) {
+          v0 = ((n0 >> (8 * c)) & 1u ? 0xFFFFu : 0u) | ((n0 >> (8 * c + 4)) & 1u ? 0xFFFF0000u : 0u);
+          v1 = ((n1 >> (8 * c)) & 1u ? 0xFFFFu : 0u) | ((n1 >> (8 * c + 4)) & 1u ? 0xFFFF0000u : 0u);
+        }
+      }
+      const uint32_t vt = kt + C::NCH * C::BOX;
+#pragma unroll
+      for (int cp = 0; cp < C::NC / 2; ++cp) {
+        uint32_t r[4];
+        const int ch = cp * 2 + mch;
+        ldsm4_trans(vt + (cp >> 2) * C::BOX + roff + (((ch & 7) ^ rxor) << 4), r);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          // bytes (slot 2c: channels 2g, 2g+1; slot 2c+1: the same) to
+          // (channel 2g: slots 2c, 2c+1; channel 2g+1: the same)
+          const uint32_t w0 = __byte_perm(r[2 * u] & v0, 0, 0x3120);
+          const uint32_t w1 = __byte_perm(r[2 * u + 1] & v1, 0, 0x3120);
+          const uint32_t a0 = c8_half2(w0), a1 = c8_half2_hi(w0);
+          const uint32_t a2 = c8_half2(w1), a3 = c8_half2_hi(w1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(o[cp * 2 + u][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        }
+      }
+    } else if (lg != nullptr) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = nt * 8 + 2 * c + (e & 1);
+          if (row < R)
+            lg[static_cast<size_t>(row) * (static_cast<size_t>(p.nb) * kTile) + (e >> 1) * 8] =
+                -INFINITY;
+        }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
+  }
+
+  // ---------------- merge the four warps (records in the ring, which no copy
+  // writes any more once every warp is past its last tile)
+  named_barrier(1, kCWarps * 32);
+  float* mg = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float s = l[nt][e];
+      s += __shfl_xor_sync(0xffffffffu, s, 4);
+      s += __shfl_xor_sync(0xffffffffu, s, 8);
+      s += __shfl_xor_sync(0xffffffffu, s, 16);
+      const int row = nt * 8 + 2 * c + e;
+      if (g == 0) mstat[warp][row] = make_float2(m[nt][e], s);
+#pragma unroll
+      for (int ch = 0; ch < C::NC; ++ch)
+        *reinterpret_cast<float2*>(mg + (warp * C::ROWS + row) * C::LDM + ch * 16 + 2 * g) =
+            make_float2(o[ch][nt][e] * unit, o[ch][nt][2 + e] * unit);
+    }
+  named_barrier(1, kCWarps * 32);
+  for (int idx = tid; idx < R * DH; idx += kCWarps * 32) {
+    const int r = idx / DH, ch = idx % DH;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kCWarps; ++w) M = fmaxf(M, mstat[w][r].x);
+    float L = 0.f, acc = 0.f;
+    if (M != -INFINITY) {
+#pragma unroll
+      for (int w = 0; w < kCWarps; ++w) {
+        const float2 ms = mstat[w][r];
+        const float fw = ex2(ms.x - M);
+        L += fw * ms.y;
+        // (a warp that saw nothing holds zeros)
+        acc += fw * mg[(w * C::ROWS + r) * C::LDM + ch];
+      }
+    }
+    const int t = t0 + r / G, h = j * G + r % G;
+    const size_t orow = (static_cast<size_t>(b) * p.T + t) * p.H + h;
+    if (ch == 0 && p.stat != nullptr) p.stat[orow * p.nsplit + split] = make_float2(M, L);
+    if (p.nsplit == 1)
+      store_o(p.O, p.o_f16, orow * DH + ch, L != 0.f ? acc / L : 0.f);
+    else
+      p.part[(orow * p.nsplit + split) * DH + ch] = acc;
+  }
+}
+
+// Local layers: CTA (c, b) writes the first slot of chunk c that a valid
+// query of row b can see, or INT_MAX (decode_span.cuh).
+__global__ void __launch_bounds__(256) span8_kernel(const int32_t* __restrict__ posc,
+                                                    const int32_t* __restrict__ qpos,
+                                                    const int32_t* __restrict__ pad_lens, int T,
+                                                    int S, int end, int window, int nchunk,
+                                                    int32_t* __restrict__ span_part) {
+  pdl_enter();
+  kv_span_chunk(posc, qpos, pad_lens, T, S, end, window, nchunk, span_part, blockIdx.x,
+                blockIdx.y);
+}
+
+// ---------------------------------------------------------------- second launch
+// CTAs [0, n_rows): merge the parts of one query row.  The others: weights of
+// 256 slots of one batch row, every query row's logits once.
+struct FinishParams {
+  const float2* stat;
+  const float* part;
+  const float* logits;
+  float* weight_sum;
+  const int32_t* span_part;
+  const int32_t* pad_lens;
+  void* O;
+  int o_f16, n_rows, T, S, H, H_kv, nb, end, nsplit, nchunk, wchunks;
+};
+
+template <int DH>
+__global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
+  pdl_enter();
+  __shared__ float fw[kMaxSplits];
+  __shared__ float2 rs[256];
+  __shared__ float red[2][8];
+  __shared__ int lo_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x < static_cast<unsigned>(p.n_rows)) {
+    const size_t row = blockIdx.x;
+    const float2* st = p.stat + row * p.nsplit;
+    const float2 mine = tid < p.nsplit ? st[tid] : make_float2(-INFINITY, 0.f);
+    float M = mine.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) red[0][warp] = M;
+    __syncthreads();
+    M = red[0][0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) M = fmaxf(M, red[0][i]);
+    const float f = M == -INFINITY ? 0.f : ex2(mine.x - M);
+    fw[tid] = f;
+    float L = f * mine.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) red[1][warp] = L;
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) L += red[1][i];
+    const float* base = p.part + row * p.nsplit * DH;
+    for (int ch = tid; ch < DH; ch += 256) {
+      float acc = 0.f;
+#pragma unroll 8
+      for (int i = 0; i < p.nsplit; ++i)
+        acc = fmaf(fw[i], __ldg(base + static_cast<size_t>(i) * DH + ch), acc);
+      store_o(p.O, p.o_f16, row * DH + ch, L != 0.f ? acc / L : 0.f);
+    }
+    return;
+  }
+  const int wi = blockIdx.x - p.n_rows;
+  const int b = wi / p.wchunks, s = (wi % p.wchunks) * 256 + tid;
+  if (warp == 0) {
+    const int lo = first_visible(p.span_part, p.nchunk, b, lane);
+    if (lane == 0) lo_s = lo;
+  }
+  const int R = p.T * (p.H / p.H_kv), rows = p.T * p.H, G = p.H / p.H_kv;
+  const size_t S64 = static_cast<size_t>(p.nb) * kTile;
+  const int valid = p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0);
+  float acc = 0.f;
+  for (int r0 = 0; r0 < rows; r0 += 256) {
+    __syncthreads();
+    if (r0 + tid < rows) {
+      // (max, 1 / sum) of query row (t, h) over its parts
+      const float2* st = p.stat + (static_cast<size_t>(b) * rows + r0 + tid) * p.nsplit;
+      float M = -INFINITY, L = 0.f;
+      for (int i = 0; i < p.nsplit; ++i) M = fmaxf(M, st[i].x);
+      if (M != -INFINITY)
+        for (int i = 0; i < p.nsplit; ++i) L += ex2(st[i].x - M) * st[i].y;
+      rs[tid] = make_float2(M == -INFINITY ? 0.f : M, L != 0.f ? 1.f / L : 0.f);
+    }
+    __syncthreads();
+    // (the first launch wrote logits from the first visible tile up to a valid
+    // token's own slot)
+    if (s < p.end + p.T && s >= lo_s / kTile * kTile) {
+      const int n = min(256, rows - r0);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const int row = r0 + i, t = row / p.H, h = row % p.H;
+        if (t >= valid || s > p.end + t) continue;
+        const float x = __ldg(p.logits + ((static_cast<size_t>(b) * p.H_kv + h / G) * R + t * G +
+                                          h % G) * S64 + s);
+        acc = fmaf(ex2(x - rs[i].x), rs[i].y, acc);
+      }
+    }
+  }
+  if (s < p.end + p.T && acc != 0.f) p.weight_sum[static_cast<size_t>(b) * p.S + s] += acc;
+}
+
+// ---------------------------------------------------------------- planning
+struct Plan {
+  int nt, tq, ntg, units, max_splits;
+};
+
+Plan plan_rows(int B, int T, int S, int H, int H_kv) {
+  const int G = H / H_kv;
+  Plan d;
+  d.nt = static_cast<long long>(T) * G <= 8 ? 1 : 2;
+  d.tq = d.nt * 8 / G;
+  d.ntg = (T + d.tq - 1) / d.tq;
+  const long long u = static_cast<long long>(B) * H_kv * d.ntg;
+  d.units = static_cast<int>(std::min<long long>(u, INT_MAX));
+  const int by_cap = static_cast<int>(std::max<long long>(1, 1024 / u));
+  d.max_splits = std::min({kMaxSplits, by_cap, c8_blocks(S)});
+  return d;
+}
+
+struct Layout {
+  int32_t* span_part;
+  float2* stat;
+  float* part;
+  float* logits;
+  size_t bytes;
+};
+
+Layout layout(void* ws, int B, int T, int S, int H, int H_kv, int d_h, bool weights) {
+  const Plan d = plan_rows(B, T, S, H, H_kv);
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = static_cast<size_t>(B) * T * H;
+  const size_t span = up(static_cast<size_t>(B) * ((S + kSpanChunk - 1) / kSpanChunk) * 4);
+  const size_t stat = up(rows * d.max_splits * 8);
+  const size_t part = d.max_splits > 1 ? up(rows * d.max_splits * d_h * 4) : 0;
+  const size_t lg = weights ? up(rows * c8_blocks(S) * kTile * 4) : 0;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  Layout L;
+  L.span_part = reinterpret_cast<int32_t*>(w);
+  L.stat = reinterpret_cast<float2*>(w + span);
+  L.part = reinterpret_cast<float*>(w + span + stat);
+  L.logits = reinterpret_cast<float*>(w + span + stat + part);
+  L.bytes = span + stat + part + lg;
+  return L;
+}
+
+template <int DH, int NT>
+cudaError_t launch_cfg(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, dim3 grid,
+                       cudaStream_t stream) {
+  auto kern = decode8_kernel<DH, NT>;
+  if (cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), Cfg<DH, NT>::SMEM))
+    return e;
+  return launch_pdl(kern, grid, dim3(kThreads), Cfg<DH, NT>::SMEM, stream, tk, tv, p);
+}
+
+}  // namespace
+
+size_t cached8_attention_ws_bytes(int B, int T, int S, int H, int H_kv, int d_h, bool weights) {
+  return layout(nullptr, B, T, S, H, H_kv, d_h, weights).bytes;
+}
+
+cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* V8,
+                                     const float* K_scale, const float* V_scale,
+                                     const int32_t* pos_cache, const int32_t* qpos,
+                                     const int32_t* pad_lens, void* O, int o_dtype,
+                                     float* weight_sum, int B, int T, int S, int end, int H,
+                                     int H_kv, int d_h, int window, void* ws, cudaStream_t stream,
+                                     int* status) {
+  const Plan d = plan_rows(B, T, S, H, H_kv);
+  if (static_cast<long long>(B) * d.ntg > 65535 || B > 65535 || H_kv > 65535)
+    return cudaErrorInvalidValue;
+  const Layout lay = layout(ws, B, T, S, H, H_kv, d_h, weight_sum != nullptr);
+  const int hi = end + T, nb = c8_blocks(S);
+  const int nchunk = (hi + kSpanChunk - 1) / kSpanChunk;
+  if (window > 0) {
+    cudaError_t e = launch_pdl(span8_kernel, dim3(nchunk, B), dim3(256), 0, stream, pos_cache,
+                               qpos, pad_lens, T, S, end, window, nchunk, lay.span_part);
+    if (e != cudaSuccess) return e;
+  }
+  // Splits: two CTAs per SM; the count that ends first when a CTA's time is
+  // its tiles plus a start and a merge worth three of them.
+  const long long est = window > 0 ? std::min<long long>(hi, static_cast<long long>(window) + d.tq)
+                                   : static_cast<long long>(hi);
+  const int tiles = static_cast<int>((est + kTile - 1) / kTile) + (window > 0 ? 1 : 0);
+  const int slots = 2 * num_sms();
+  int nsplit = 1;
+  long long best = LLONG_MAX;
+  for (int n = 1; n <= std::min(d.max_splits, tiles); ++n) {
+    const long long waves = (static_cast<long long>(d.units) * n + slots - 1) / slots;
+    const long long cost = waves * ((tiles + n - 1) / n + 3);
+    if (cost < best) {
+      best = cost;
+      nsplit = n;
+    }
+  }
+
+  // caches [B, S, H_kv, d_h] of bytes: box {128 channels, 1 head, 64 slots, 1 row}
+  CUtensorMap tk, tv;
+  const uint64_t dims[4] = {static_cast<uint64_t>(d_h), static_cast<uint64_t>(H_kv),
+                            static_cast<uint64_t>(S), static_cast<uint64_t>(B)};
+  const uint64_t str[3] = {static_cast<uint64_t>(d_h), static_cast<uint64_t>(H_kv) * d_h,
+                           static_cast<uint64_t>(S) * H_kv * d_h};
+  const uint32_t box[4] = {128, 1, kTile, 1};
+  if (!encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, K8, dims, str, box) ||
+      !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, V8, dims, str, box))
+    return cudaErrorInvalidValue;
+
+  Params p;
+  p.Q = static_cast<const __half*>(Q);
+  p.K_scale = K_scale;
+  p.V_scale = V_scale;
+  p.posc = pos_cache;
+  p.qpos = qpos;
+  p.pad_lens = pad_lens;
+  p.span_part = window > 0 ? lay.span_part : nullptr;
+  p.stat = nsplit > 1 || weight_sum != nullptr ? lay.stat : nullptr;
+  p.part = lay.part;
+  p.logits = weight_sum != nullptr ? lay.logits : nullptr;
+  p.O = O;
+  p.o_f16 = o_dtype == kF16 ? 1 : 0;
+  p.B = B;
+  p.T = T;
+  p.S = S;
+  p.H = H;
+  p.H_kv = H_kv;
+  p.nb = nb;
+  p.end = end;
+  p.window = window;
+  p.nsplit = nsplit;
+  p.nchunk = nchunk;
+  p.tq = d.tq;
+  p.ntg = d.ntg;
+  p.status = status;
+  const dim3 grid(nsplit, H_kv, B * d.ntg);
+  cudaError_t e;
+  if (d_h == 256)
+    e = d.nt == 1 ? launch_cfg<256, 1>(tk, tv, p, grid, stream)
+                  : launch_cfg<256, 2>(tk, tv, p, grid, stream);
+  else
+    e = d.nt == 1 ? launch_cfg<128, 1>(tk, tv, p, grid, stream)
+                  : launch_cfg<128, 2>(tk, tv, p, grid, stream);
+  if (e != cudaSuccess || (nsplit == 1 && weight_sum == nullptr)) return e;
+
+  FinishParams q;
+  q.stat = lay.stat;
+  q.part = lay.part;
+  q.logits = lay.logits;
+  q.weight_sum = weight_sum;
+  q.span_part = p.span_part;
+  q.pad_lens = pad_lens;
+  q.O = O;
+  q.o_f16 = p.o_f16;
+  q.n_rows = nsplit > 1 ? B * T * H : 0;
+  q.T = T;
+  q.S = S;
+  q.H = H;
+  q.H_kv = H_kv;
+  q.nb = nb;
+  q.end = end;
+  q.nsplit = nsplit;
+  q.nchunk = nchunk;
+  q.wchunks = (hi + 255) / 256;
+  const long long ctas = q.n_rows + (weight_sum != nullptr ? static_cast<long long>(B) * q.wchunks : 0);
+  if (ctas > INT_MAX) return cudaErrorInvalidValue;
+  return launch_pdl(d_h == 256 ? finish8_kernel<256> : finish8_kernel<128>,
+                    dim3(static_cast<unsigned>(ctas)), dim3(256), 0, stream, q);
+}
+
+}  // namespace g3

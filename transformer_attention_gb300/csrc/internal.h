@@ -234,4 +234,42 @@ struct CachedAttnLayout {
 CachedAttnLayout cached_attention_layout(void* ws, int B, int T, int S, int H, int H_kv, int d_h);
 int cached_span_chunks(int T, int end);
 
+// ------------------------------------------------------------ 8-bit KV cache
+// Caches K8 / V8 [B, S, H_kv, d_h] of e4m3 bytes with scales [B, c8_blocks(S),
+// H_kv] fp32 and positions pos_cache [B, S] (cache8.cuh).
+constexpr int c8_blocks(int S) { return static_cast<int>((static_cast<long long>(S) + 63) / 64); }
+
+cudaError_t launch_cache8_write(const void* K_rows, const void* V_rows, long ld,
+                                const int32_t* segment_pos, const int32_t* pad_lens, int B, int T,
+                                int S, int end, int H_kv, int d_h, void* K8, void* V8,
+                                float* K_scale, float* V_scale, int32_t* pos_cache,
+                                cudaStream_t stream);
+
+// Slots [first, first + n) as fp16 rows b * n + t of stride ld.
+cudaError_t launch_cache8_read(const void* K8, const void* V8, const float* K_scale,
+                               const float* V_scale, int B, int S, int first, int n, int H_kv,
+                               int d_h, void* K_rows, void* V_rows, long ld, cudaStream_t stream);
+
+// Keeps `keep` of the slots [0, end) (the last `recent` and the heaviest) and
+// moves them to the front of the _dst cache of S_dst slots.
+cudaError_t launch_cache8_evict(const void* K8, const void* V8, const float* K_scale,
+                                const float* V_scale, const int32_t* pos_cache,
+                                const float* weight_sum, int B, int S, int end, int H_kv, int d_h,
+                                int keep, int recent, void* K8_dst, void* V8_dst,
+                                float* K_scale_dst, float* V_scale_dst, int32_t* pos_dst,
+                                float* weight_dst, int32_t* kept, int S_dst, cudaStream_t stream);
+
+// Workspace of launch_cached8_attention (depends only on the shapes and S).
+size_t cached8_attention_ws_bytes(int B, int T, int S, int H, int H_kv, int d_h, bool weights);
+
+// launch_cached_attention over an 8-bit cache; weight_sum [B, S] or null: the
+// probabilities of every slot are added to it.
+cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* V8,
+                                     const float* K_scale, const float* V_scale,
+                                     const int32_t* pos_cache, const int32_t* qpos,
+                                     const int32_t* pad_lens, void* O, int o_dtype,
+                                     float* weight_sum, int B, int T, int S, int end, int H,
+                                     int H_kv, int d_h, int window, void* ws, cudaStream_t stream,
+                                     int* status);
+
 }  // namespace g3
