@@ -7,7 +7,7 @@
 // Visible slots as in decode.cu: s <= end + t, a stored position >= 0 and, on
 // a local layer, within the window of the query's position.
 //
-// decode8_kernel (few query rows, T * G <= 16 of a kv head at a time).  Every
+// decode8_kernel (few query rows: T * G <= 16 per kv head).  Every
 // byte of the cache is read once and meets at most 16 query rows, so HBM
 // bounds it: d_h = 128 needs 256 bytes per slot and kv head.  The two
 // contractions run on mma.sync m16n8k16 with the slots (K) and the channels
@@ -39,6 +39,7 @@
 #include <climits>
 
 #include "cache8.cuh"
+#include "cache8_flash.cuh"
 #include "decode_span.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -51,9 +52,10 @@ constexpr int kTile = kC8Block;      // slots per tile: one scale block
 constexpr int kCWarps = 4;           // consumer warps, 16 slots of each tile each
 constexpr int kThreads = (kCWarps + 1) * 32;
 constexpr int kMaxSplits = 256;
+constexpr int kFewRows = 16;         // query rows of a kv head that decode8_kernel takes
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum { kSiteFull = 50, kSiteEmpty = 51 };
+enum { kSiteFull = 70, kSiteEmpty = 71 };
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -119,7 +121,7 @@ struct Params {
   float* part;                // [B*T*H, nsplit, DH] unnormalised, when nsplit > 1
   float* logits;              // [B, H_kv, T*G, S64] base-2 logits, or null
   void* O;
-  int o_f16, B, T, S, H, H_kv, nb, end, window, nsplit, nchunk, tq, ntg;
+  int o_f16, B, T, S, H, H_kv, nb, end, window, nsplit, nchunk;
   int* status;
 };
 
@@ -159,12 +161,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int split = blockIdx.x, j = blockIdx.y;
-  const int b = blockIdx.z / p.ntg, tg = blockIdx.z % p.ntg;
+  const int split = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
   const int G = p.H / p.H_kv;
-  const int t0 = tg * p.tq;
-  const int ntok = min(p.tq, p.T - t0);
-  const int R = ntok * G;
+  const int R = p.T * G;
   const int valid = p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0);
 
   if (tid == 0) {
@@ -178,10 +177,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (warp == kCWarps) {
     // Visible slots of this CTA's rows lie in [lo, hi): whole tiles of them,
-    // evenly over the nsplit CTAs of (b, j, tg).
+    // evenly over the nsplit CTAs of (b, j).
     int lo = first_visible(p.span_part, p.nchunk, b, lane);
-    const int t_last = min(t0 + ntok, valid) - 1;
-    const int hi = t_last >= t0 ? p.end + t_last + 1 : 0;
+    const int hi = valid > 0 ? p.end + min(valid, p.T) : 0;
     lo = min(lo, hi);
     const int k0 = lo / kTile, k1 = (hi + kTile - 1) / kTile;
     const int per = (k1 - k0 + p.nsplit - 1) / p.nsplit;
@@ -199,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int r = nt * 8 + (l >> 2);
     uint2 q = make_uint2(0, 0);
     if (r < R) {
-      const int t = t0 + r / G, h = j * G + r % G;
+      const int t = r / G, h = j * G + r % G;
       q = __ldg(reinterpret_cast<const uint2*>(
           p.Q + ((static_cast<size_t>(b) * p.T + t) * p.H + h) * DH + ch * 16 + (l & 3) * 4));
     }
@@ -249,13 +247,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       lim[nt][e] = -1;
       plo[nt][e] = 0;
       phi[nt][e] = INT_MAX;
-      if (r < R && t0 + r / G < valid) {
-        const int t = t0 + r / G;
+      if (r < R && r / G < valid) {
+        const int t = r / G;
         lim[nt][e] = p.end + t;
         if (p.window > 0) {
-          const long long qp = p.qpos[static_cast<size_t>(b) * p.T + t];
-          plo[nt][e] = static_cast<int>(max(0LL, min(qp - p.window + 1, (long long)INT_MAX)));
-          phi[nt][e] = static_cast<int>(max(-1LL, min(qp + p.window - 1, (long long)INT_MAX)));
+          const int qp = p.qpos[static_cast<size_t>(b) * p.T + t];
+          window_range(qp, qp, p.window, plo[nt][e], phi[nt][e]);
         }
       }
     }
@@ -319,8 +316,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!ok) break;
     float* lg = nullptr;
     if (p.logits != nullptr)
-      lg = p.logits + ((static_cast<size_t>(b) * p.H_kv + j) * (p.T * G) + t0 * G) *
-                          (static_cast<size_t>(p.nb) * kTile) + s;
+      lg = p.logits +
+           (static_cast<size_t>(b) * p.H_kv + j) * R * (static_cast<size_t>(p.nb) * kTile) + s;
     if ((b0 | b1) != 0) {
       const uint32_t kt = smem_u32(ring + st * C::TILE);
       // S^T (16 slots x 8 rows): two accumulators shorten the chain
@@ -476,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         acc += fw * mg[(w * C::ROWS + r) * C::LDM + ch];
       }
     }
-    const int t = t0 + r / G, h = j * G + r % G;
+    const int t = r / G, h = j * G + r % G;
     const size_t orow = (static_cast<size_t>(b) * p.T + t) * p.H + h;
     if (ch == 0 && p.stat != nullptr) p.stat[orow * p.nsplit + split] = make_float2(M, L);
     if (p.nsplit == 1)
@@ -592,46 +589,59 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
 }
 
 // ---------------------------------------------------------------- planning
+// Few rows (decode8_kernel) or many (the tcgen05 kernel), and how far the
+// slots may be split: as many CTAs as a few rounds of the SMs take.
 struct Plan {
-  int nt, tq, ntg, units, max_splits;
+  bool few;
+  int items;                  // query tiles of a (row, kv head)
+  long long units;            // (row, kv head, item)
+  int tile, max_splits;
 };
 
-Plan plan_rows(int B, int T, int S, int H, int H_kv) {
+Plan plan_rows(int B, int T, int S, int H, int H_kv, int d_h) {
   const int G = H / H_kv;
   Plan d;
-  d.nt = static_cast<long long>(T) * G <= 8 ? 1 : 2;
-  d.tq = d.nt * 8 / G;
-  d.ntg = (T + d.tq - 1) / d.tq;
-  const long long u = static_cast<long long>(B) * H_kv * d.ntg;
-  d.units = static_cast<int>(std::min<long long>(u, INT_MAX));
-  const int by_cap = static_cast<int>(std::max<long long>(1, 1024 / u));
-  d.max_splits = std::min({kMaxSplits, by_cap, c8_blocks(S)});
+  d.few = static_cast<long long>(T) * G <= kFewRows;
+  const int span = flash8_span(d_h, G);
+  d.items = d.few ? 1 : (T + span - 1) / span;
+  d.units = static_cast<long long>(B) * H_kv * d.items;
+  d.tile = d.few ? kTile : 2 * kTile;
+  const long long by_cap = std::max<long long>(1, (d.few ? 1024 : 512) / d.units);
+  const int tiles = (S + d.tile - 1) / d.tile;
+  d.max_splits = static_cast<int>(std::min<long long>({kMaxSplits, by_cap, tiles}));
   return d;
 }
 
 struct Layout {
-  int32_t* span_part;
+  int32_t* span_part;   // few: [B, chunks], many: [B, items]
   float2* stat;
   float* part;
-  float* logits;
+  float* logits;        // few rows with weights
+  float2* rowstat;      // many rows with weights
+  float* wpart;
   size_t bytes;
 };
 
 Layout layout(void* ws, int B, int T, int S, int H, int H_kv, int d_h, bool weights) {
-  const Plan d = plan_rows(B, T, S, H, H_kv);
-  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t rows = static_cast<size_t>(B) * T * H;
-  const size_t span = up(static_cast<size_t>(B) * ((S + kSpanChunk - 1) / kSpanChunk) * 4);
-  const size_t stat = up(rows * d.max_splits * 8);
-  const size_t part = d.max_splits > 1 ? up(rows * d.max_splits * d_h * 4) : 0;
-  const size_t lg = weights ? up(rows * c8_blocks(S) * kTile * 4) : 0;
+  const Plan d = plan_rows(B, T, S, H, H_kv, d_h);
   uint8_t* w = static_cast<uint8_t*>(ws);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    uint8_t* q = w + at;
+    at += (n + 255) / 256 * 256;
+    return q;
+  };
+  const size_t rows = static_cast<size_t>(B) * T * H;
+  const int spans = d.few ? (S + kSpanChunk - 1) / kSpanChunk : d.items;
   Layout L;
-  L.span_part = reinterpret_cast<int32_t*>(w);
-  L.stat = reinterpret_cast<float2*>(w + span);
-  L.part = reinterpret_cast<float*>(w + span + stat);
-  L.logits = reinterpret_cast<float*>(w + span + stat + part);
-  L.bytes = span + stat + part + lg;
+  L.span_part = reinterpret_cast<int32_t*>(take(static_cast<size_t>(B) * spans * 4));
+  L.stat = reinterpret_cast<float2*>(take(rows * d.max_splits * 8));
+  L.part = reinterpret_cast<float*>(take(d.max_splits > 1 ? rows * d.max_splits * d_h * 4 : 0));
+  L.logits = reinterpret_cast<float*>(
+      take(weights && d.few ? rows * c8_blocks(S) * kTile * 4 : 0));
+  L.rowstat = reinterpret_cast<float2*>(take(weights && !d.few ? rows * 8 : 0));
+  L.wpart = reinterpret_cast<float*>(take(weights && !d.few ? weights8_part_floats() * 4 : 0));
+  L.bytes = at;
   return L;
 }
 
@@ -657,34 +667,82 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
                                      float* weight_sum, int B, int T, int S, int end, int H,
                                      int H_kv, int d_h, int window, void* ws, cudaStream_t stream,
                                      int* status) {
-  const Plan d = plan_rows(B, T, S, H, H_kv);
-  if (static_cast<long long>(B) * d.ntg > 65535 || B > 65535 || H_kv > 65535)
-    return cudaErrorInvalidValue;
+  const Plan d = plan_rows(B, T, S, H, H_kv, d_h);
   const Layout lay = layout(ws, B, T, S, H, H_kv, d_h, weight_sum != nullptr);
-  const int hi = end + T, nb = c8_blocks(S);
-  const int nchunk = (hi + kSpanChunk - 1) / kSpanChunk;
-  if (window > 0) {
-    cudaError_t e = launch_pdl(span8_kernel, dim3(nchunk, B), dim3(256), 0, stream, pos_cache,
-                               qpos, pad_lens, T, S, end, window, nchunk, lay.span_part);
-    if (e != cudaSuccess) return e;
-  }
-  // Splits: two CTAs per SM; the count that ends first when a CTA's time is
-  // its tiles plus a start and a merge worth three of them.
-  const long long est = window > 0 ? std::min<long long>(hi, static_cast<long long>(window) + d.tq)
+  const int hi = end + T, nb = c8_blocks(S), o_f16 = o_dtype == kF16 ? 1 : 0;
+
+  // Splits: the count that ends first when a CTA's time is its tiles, a start
+  // and an end worth some more, and (many rows) the parts' bytes.
+  const int span = d.few ? T : flash8_span(d_h, H / H_kv);
+  const long long est = window > 0 ? std::min<long long>(hi, static_cast<long long>(window) + span)
                                    : static_cast<long long>(hi);
-  const int tiles = static_cast<int>((est + kTile - 1) / kTile) + (window > 0 ? 1 : 0);
-  const int slots = 2 * num_sms();
+  const int tiles = static_cast<int>((est + d.tile - 1) / d.tile) + (window > 0 ? 1 : 0);
+  const int slots = (d.few ? 2 : 1) * num_sms();
+  // (a part's 4 * d_h bytes per row go out and come back; a tile of the
+  // tcgen05 kernel takes about a microsecond, 6.5 MB of HBM time)
+  const double part_tiles =
+      d.few ? 0.0 : static_cast<double>(B) * T * H * d_h * 8.0 / 6.5e6;
   int nsplit = 1;
-  long long best = LLONG_MAX;
+  double best = 1e300;
   for (int n = 1; n <= std::min(d.max_splits, tiles); ++n) {
-    const long long waves = (static_cast<long long>(d.units) * n + slots - 1) / slots;
-    const long long cost = waves * ((tiles + n - 1) / n + 3);
+    const double waves = static_cast<double>((d.units * n + slots - 1) / slots);
+    const double cost = waves * ((tiles + n - 1) / n + 3) + (n > 1 ? n * part_tiles : 0.0);
     if (cost < best) {
       best = cost;
       nsplit = n;
     }
   }
+  cudaError_t e;
 
+  if (!d.few) {
+    Flash8Args a;
+    a.Q = Q;
+    a.K8 = K8;
+    a.V8 = V8;
+    a.K_scale = K_scale;
+    a.V_scale = V_scale;
+    a.posc = pos_cache;
+    a.qpos = qpos;
+    a.pad_lens = pad_lens;
+    a.first = lay.span_part;
+    a.stat = nsplit > 1 || weight_sum != nullptr ? lay.stat : nullptr;
+    a.part = lay.part;
+    a.O = O;
+    a.o_f16 = o_f16;
+    a.B = B;
+    a.T = T;
+    a.S = S;
+    a.end = end;
+    a.H = H;
+    a.H_kv = H_kv;
+    a.d_h = d_h;
+    a.window = window;
+    a.nsplit = nsplit;
+    a.status = status;
+    e = launch_flash8(a, stream);
+    if (e != cudaSuccess) return e;
+    if (nsplit > 1) {
+      FinishParams q = {};
+      q.stat = lay.stat;
+      q.part = lay.part;
+      q.O = O;
+      q.o_f16 = o_f16;
+      q.n_rows = B * T * H;
+      q.nsplit = nsplit;
+      e = launch_pdl(d_h == 256 ? finish8_kernel<256> : finish8_kernel<128>,
+                     dim3(static_cast<unsigned>(q.n_rows)), dim3(256), 0, stream, q);
+      if (e != cudaSuccess) return e;
+    }
+    return weight_sum != nullptr ? launch_weights8(a, lay.rowstat, lay.wpart, weight_sum, stream)
+                                 : cudaSuccess;
+  }
+
+  const int nchunk = (hi + kSpanChunk - 1) / kSpanChunk;
+  if (window > 0) {
+    e = launch_pdl(span8_kernel, dim3(nchunk, B), dim3(256), 0, stream, pos_cache, qpos, pad_lens, T,
+                   S, end, window, nchunk, lay.span_part);
+    if (e != cudaSuccess) return e;
+  }
   // caches [B, S, H_kv, d_h] of bytes: box {128 channels, 1 head, 64 slots, 1 row}
   CUtensorMap tk, tv;
   const uint64_t dims[4] = {static_cast<uint64_t>(d_h), static_cast<uint64_t>(H_kv),
@@ -708,7 +766,7 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   p.part = lay.part;
   p.logits = weight_sum != nullptr ? lay.logits : nullptr;
   p.O = O;
-  p.o_f16 = o_dtype == kF16 ? 1 : 0;
+  p.o_f16 = o_f16;
   p.B = B;
   p.T = T;
   p.S = S;
@@ -719,17 +777,15 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   p.window = window;
   p.nsplit = nsplit;
   p.nchunk = nchunk;
-  p.tq = d.tq;
-  p.ntg = d.ntg;
   p.status = status;
-  const dim3 grid(nsplit, H_kv, B * d.ntg);
-  cudaError_t e;
+  const dim3 grid(nsplit, H_kv, B);
+  const bool one = T * (H / H_kv) <= 8;
   if (d_h == 256)
-    e = d.nt == 1 ? launch_cfg<256, 1>(tk, tv, p, grid, stream)
-                  : launch_cfg<256, 2>(tk, tv, p, grid, stream);
+    e = one ? launch_cfg<256, 1>(tk, tv, p, grid, stream)
+            : launch_cfg<256, 2>(tk, tv, p, grid, stream);
   else
-    e = d.nt == 1 ? launch_cfg<128, 1>(tk, tv, p, grid, stream)
-                  : launch_cfg<128, 2>(tk, tv, p, grid, stream);
+    e = one ? launch_cfg<128, 1>(tk, tv, p, grid, stream)
+            : launch_cfg<128, 2>(tk, tv, p, grid, stream);
   if (e != cudaSuccess || (nsplit == 1 && weight_sum == nullptr)) return e;
 
   FinishParams q;
@@ -740,7 +796,7 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   q.span_part = p.span_part;
   q.pad_lens = pad_lens;
   q.O = O;
-  q.o_f16 = p.o_f16;
+  q.o_f16 = o_f16;
   q.n_rows = nsplit > 1 ? B * T * H : 0;
   q.T = T;
   q.S = S;
@@ -751,7 +807,8 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   q.nsplit = nsplit;
   q.nchunk = nchunk;
   q.wchunks = (hi + 255) / 256;
-  const long long ctas = q.n_rows + (weight_sum != nullptr ? static_cast<long long>(B) * q.wchunks : 0);
+  const long long ctas =
+      q.n_rows + (weight_sum != nullptr ? static_cast<long long>(B) * q.wchunks : 0);
   if (ctas > INT_MAX) return cudaErrorInvalidValue;
   return launch_pdl(d_h == 256 ? finish8_kernel<256> : finish8_kernel<128>,
                     dim3(static_cast<unsigned>(ctas)), dim3(256), 0, stream, q);

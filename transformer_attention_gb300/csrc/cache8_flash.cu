@@ -1,0 +1,687 @@
+// Attention of many new tokens (a prompt or a chunk of one) over the 8-bit KV
+// cache, on the tcgen05 tensor cores; what cache8_attn.cu computes for few.
+//
+// A CTA holds 128-row query tiles (TQ = 128 / G tokens x the G heads of kv
+// head j) and walks the visible slots in tiles of 128, with S = Q K^T and O +=
+// P V in fp16 with fp32 accumulators in TMEM.  The cache's bytes become the
+// swizzled fp16 tiles that the MMAs read in four or eight converter warps:
+// number x scale is an exact fp16 value (cache8.cuh), so the conversion costs
+// no precision, and kind::f8f6f4 would need Q and P in 8 bits.  Per 128-slot
+// tile and 128 channels that is 16384 two-number conversions, 270 clocks at the
+// 60 per clock and SM measured for cvt.f16x2.e4m3x2, against about 1100 clocks
+// of MMA for each query tile: d_h = 128 shares a conversion among two query
+// tiles.
+//
+// Warps (d_h = 128, two query tiles e = 0, 1):
+//   0      TMA of the Q tiles
+//   1      TMEM allocation and MMA issue
+//   2      positions: per tile a bit for each slot that holds a token, and the
+//          range of the stored positions
+//   4-7    converters: the K part, then the V part of each tile, fetched into
+//          registers one part ahead
+//   8-15   softmax of tile 0 and of tile 1, one thread per row
+// d_h = 256 has one query tile, converters of its own for K (4-7) and V
+// (8-11), softmax in 12-15.  Shared memory holds two 32 KB parts of K and two
+// of V: whole tiles of 128 slots x 128 channels, or for d_h = 256 the two
+// channel halves of one K tile and the two slot halves of one V tile.
+// TMEM: S_0 0-127, S_1 128-255 (d_h = 256: S of even and odd tiles), O from
+// 256; P (fp16 pairs) is written over the first 64 columns of its S.
+//
+// Slots hidden from the whole CTA become zeros in the conversion, so that
+// what they hold (a NaN, say) cannot reach O through a zero probability.
+// The slots of a query tile are split over CTAs when there are few tiles;
+// finish8_kernel (cache8_attn.cu) merges the parts.
+#include <algorithm>
+#include <climits>
+
+#include "attention_common.cuh"
+#include "cache8.cuh"
+#include "cache8_flash.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace g3 {
+
+namespace {
+
+using attn::ex2;
+
+constexpr int THREADS = 512;
+constexpr int BM = 128, BN = 128;
+constexpr uint32_t CHUNK = 128 * 128;       // 128 rows x 64 channels (128 B), swizzled
+constexpr uint32_t PART = 32768;
+constexpr uint32_t O_COL = 256;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float RESCALE_THRESHOLD = 8.0f;   // log2 units
+// Registers per thread: 512 threads launch with 128 each; control and
+// converter warpgroups give some to the softmax warpgroups.
+constexpr int REGS_LAUNCH = 128;
+constexpr int REGS_CTRL = 48, REGS_CONV = 80, REGS_SOFT = 192;
+static_assert(REGS_CTRL + REGS_CONV + 2 * REGS_SOFT <= 4 * REGS_LAUNCH &&
+                  REGS_CTRL + 2 * REGS_CONV + REGS_SOFT <= 4 * REGS_LAUNCH,
+              "register split above the launch allocation");
+
+enum : int {
+  kSiteQ = 80, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty, kSiteSFull, kSitePFull,
+  kSitePvDone, kSiteMetaFull, kSiteMetaEmpty, kSiteOFinal
+};
+
+struct Meta {
+  uint32_t ok[4];          // slots of the tile that hold a token below the CTA's last slot
+  int pmin, pmax;          // range of their positions
+  int pos[BN];
+};
+
+template <int DH, int G>
+struct Cfg {
+  static constexpr int NQ = DH == 128 ? 2 : 1;     // query tiles per CTA
+  static constexpr int TQ = BM / G;                // tokens per query tile
+  static constexpr int NCH = DH / 64;
+  static constexpr int PARTS = DH / 128;           // parts of a K or V tile
+  static constexpr uint32_t QT_BYTES = BM * DH * 2;
+  static constexpr uint32_t SMEM = NQ * QT_BYTES + 4 * PART + 1024;
+  static_assert(SMEM + 4096 <= 232448, "shared memory budget");
+};
+
+struct Params {
+  const uint8_t* K8;
+  const uint8_t* V8;
+  const float* K_scale;
+  const float* V_scale;
+  const int32_t* posc;
+  const int32_t* qpos;
+  const int32_t* pad_lens;
+  const int32_t* first;       // [B, items] first visible slot of each item (local layers) or null
+  float2* stat;
+  float* part;
+  void* O;
+  int o_f16, B, T, S, H, H_kv, nb, end, window, nsplit, items;
+  int* status;
+};
+
+// exp2(s log2 e - m) of 32 columns: packed fp16 pairs to p[0..15], sums to acc.
+__device__ __forceinline__ void exp_pack(const uint32_t (&s)[32], uint32_t* p, float2 (&acc)[4],
+                                         float2 l2e, float2 negm) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float2 x = __ffma2_rn(
+        make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), l2e, negm);
+    const float2 e = make_float2(ex2(x.x), ex2(x.y));
+    acc[k & 3] = __fadd2_rn(acc[k & 3], e);
+    p[k] = pack_half2(e.x, e.y);
+  }
+}
+
+__device__ __forceinline__ float mask_max(uint32_t (&r)[32], uint32_t keep) {
+  float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    if (!((keep >> c) & 1u)) r[c] = 0xff800000u;
+    if (!((keep >> (c + 1)) & 1u)) r[c + 1] = 0xff800000u;
+    a = fmaxf(a, __uint_as_float(r[c]));
+    b = fmaxf(b, __uint_as_float(r[c + 1]));
+  }
+  return fmaxf(a, b);
+}
+
+template <int DH, int G>
+__global__ void __launch_bounds__(THREADS, 1)
+    flash8_kernel(const __grid_constant__ CUtensorMap tmQ, const Params p) {
+  pdl_enter();
+  using C = Cfg<DH, G>;
+  if (*reinterpret_cast<volatile int*>(p.status) != 0) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + C::NQ * C::QT_BYTES;   // two parts
+  uint8_t* sV = sK + 2 * PART;                // two parts
+  __shared__ __align__(8) uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
+      p_full[2], pv_done[2], meta_full[2], meta_empty[2], o_final[2], drain;
+  __shared__ Meta meta[2];
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_flag;
+
+  // Item: latest tokens (most slots on a causal prompt) first, the items of a
+  // kv head next to each other so that they share its bytes in L2.
+  int idx = blockIdx.x;
+  const int item = p.items - 1 - idx % p.items;
+  idx /= p.items;
+  const int split = idx % p.nsplit;
+  idx /= p.nsplit;
+  const int j = idx % p.H_kv, b = idx / p.H_kv;
+  const int t0 = item * C::NQ * C::TQ;
+  const int valid = min(p.T, p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0));
+  const int t_end = min(t0 + C::NQ * C::TQ, valid);          // past the last valid token
+  const int nq = C::NQ == 2 && t0 + C::TQ < p.T ? 2 : 1;     // query tiles with tokens
+  const int hi = t_end > t0 ? p.end + t_end : 0;
+  int lo = p.first != nullptr ? p.first[static_cast<size_t>(b) * p.items + item] : 0;
+  lo = min(lo, hi) / kC8Block * kC8Block;
+  int n_tiles = (hi - lo + BN - 1) / BN;
+  const int per = (n_tiles + p.nsplit - 1) / p.nsplit;
+  const int first_tile = min(split * per, n_tiles);
+  n_tiles = min(per, n_tiles - first_tile);
+  const int s_base = lo + first_tile * BN;
+
+  if (tid == 0) {
+    mbar_init(smem_u32(&q_full), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&k_full[s]), 4);
+      mbar_init(smem_u32(&k_empty[s]), 1);
+      mbar_init(smem_u32(&v_full[s]), 4);
+      mbar_init(smem_u32(&v_empty[s]), 1);
+      mbar_init(smem_u32(&s_full[s]), 1);
+      mbar_init(smem_u32(&p_full[s]), 4);
+      mbar_init(smem_u32(&pv_done[s]), 1);
+      mbar_init(smem_u32(&meta_full[s]), 1);
+      mbar_init(smem_u32(&meta_empty[s]), 4 * nq);
+      mbar_init(smem_u32(&o_final[s]), 1);
+    }
+    mbar_init(smem_u32(&drain), 1);
+    abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmQ);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_sh), 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = tmem_sh;
+  auto wait_warp = [&](uint64_t& bar, int parity, int site) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, &abort_flag, p.status, site));
+  };
+
+  if (warp < 4) {
+    regs_decrease<REGS_CTRL>();
+    if (warp == 0 && lane == 0 && n_tiles > 0) {
+      // ---------------- Q
+      const uint32_t qb = smem_u32(&q_full);
+      mbar_arrive_expect_tx(qb, nq * C::QT_BYTES);
+      for (int e = 0; e < nq; ++e)
+        for (int ch = 0; ch < C::NCH; ++ch)
+          tma_load_4d(smem_u32(sQ + e * C::QT_BYTES + ch * CHUNK), &tmQ, qb, ch * 64, j * G,
+                      t0 + e * C::TQ, b);
+      mbar_wait_drain(qb, 0);
+    } else if (warp == 1 && n_tiles > 0) {
+      // ---------------- MMA issue (whole warp, one elected lane)
+      const uint32_t lead = elect_one();
+      constexpr uint32_t idesc_qk = idesc_f16(BM, BN, /*f16*/ 0, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_f16(BM, DH, /*f16*/ 0, 0, /*B MN-major*/ 1);
+      const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK), v_addr = smem_u32(sV);
+      bool ok = wait_warp(q_full, 0, kSiteQ);
+      if constexpr (C::NQ == 2) {
+        auto issue_s = [&](int e, int i) {
+          const uint32_t kb = k_addr + (i & 1) * PART;
+#pragma unroll
+          for (int k = 0; k < DH / 16; ++k) {
+            const uint32_t off = (k >> 2) * CHUNK + (k & 3) * 32;
+            mma_ss_lead(lead, tbase + e * 128, sdesc_sw128(q_addr + e * C::QT_BYTES + off, 16, 1024),
+                        sdesc_sw128(kb + off, 16, 1024), idesc_qk, k > 0 ? 1u : 0u);
+          }
+          mma_commit_lead(lead, smem_u32(&s_full[e]));
+        };
+        auto issue_pv = [&](int e, int i) -> bool {
+          if (!wait_warp(p_full[e], i & 1, kSitePFull)) return false;
+          if (e == 0 && !wait_warp(v_full[i & 1], (i >> 1) & 1, kSiteVFull)) return false;
+          tc_fence_after();
+          const uint32_t vb = v_addr + (i & 1) * PART;
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            mma_ts_lead(lead, tbase + O_COL + e * 128, tbase + e * 128 + k * 8,
+                        sdesc_sw128(vb + k * 2048, CHUNK, 1024), idesc_pv,
+                        (i > 0 || k > 0) ? 1u : 0u);
+          return true;
+        };
+        for (int i = 0; ok && i < n_tiles; ++i) {
+          ok = wait_warp(k_full[i & 1], (i >> 1) & 1, kSiteKFull);
+          if (!ok) break;
+          tc_fence_after();
+          for (int e = 0; ok && e < nq; ++e) {
+            // S_e reuses the columns of P_e of the tile before: the tensor
+            // pipe runs PV_e before it.
+            if (i > 0) ok = issue_pv(e, i - 1);
+            if (!ok) break;
+            if (i > 0 && e == nq - 1) mma_commit_lead(lead, smem_u32(&v_empty[(i - 1) & 1]));
+            issue_s(e, i);
+          }
+          if (!ok) break;
+          mma_commit_lead(lead, smem_u32(&k_empty[i & 1]));
+        }
+        for (int e = 0; ok && e < nq; ++e) {
+          ok = issue_pv(e, n_tiles - 1);
+          if (ok) mma_commit_lead(lead, smem_u32(&o_final[e]));
+        }
+      } else {
+        auto issue_pv = [&](int i) -> bool {
+          if (!wait_warp(p_full[i & 1], (i >> 1) & 1, kSitePFull)) return false;
+          for (int h = 0; h < 2; ++h) {
+            if (!wait_warp(v_full[h], i & 1, kSiteVFull)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts_lead(lead, tbase + O_COL, tbase + (i & 1) * 128 + (h * 4 + k) * 8,
+                          sdesc_sw128(v_addr + h * PART + k * 2048, CHUNK / 2, 1024), idesc_pv,
+                          (i > 0 || h > 0 || k > 0) ? 1u : 0u);
+            mma_commit_lead(lead, smem_u32(&v_empty[h]));
+          }
+          mma_commit_lead(lead, smem_u32(&pv_done[i & 1]));
+          return true;
+        };
+        for (int i = 0; ok && i < n_tiles; ++i) {
+          // S of tile i is issued before PV of tile i - 1 and after PV of
+          // tile i - 2, whose P its columns held.
+          for (int h = 0; ok && h < 2; ++h) {
+            ok = wait_warp(k_full[h], i & 1, kSiteKFull);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t off = (h * 2 + (k >> 2)) * CHUNK + (k & 3) * 32;
+              mma_ss_lead(lead, tbase + (i & 1) * 128, sdesc_sw128(q_addr + off, 16, 1024),
+                          sdesc_sw128(k_addr + off, 16, 1024), idesc_qk, (h > 0 || k > 0) ? 1u : 0u);
+            }
+            mma_commit_lead(lead, smem_u32(&k_empty[h]));
+          }
+          if (!ok) break;
+          mma_commit_lead(lead, smem_u32(&s_full[i & 1]));
+          if (i > 0) ok = issue_pv(i - 1);
+        }
+        if (ok) ok = issue_pv(n_tiles - 1);
+        if (ok) mma_commit_lead(lead, smem_u32(&o_final[0]));
+      }
+      mma_commit_lead(lead, smem_u32(&drain));
+      mbar_wait_drain(smem_u32(&drain), 0);
+    } else if (warp == 2) {
+      // ---------------- positions of each tile's slots
+      const int32_t* posr = p.posc + static_cast<size_t>(b) * p.S;
+      int nx[4];
+      auto fetch = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int s = s_base + i * BN + k * 32 + lane;
+          nx[k] = i < n_tiles && s < hi ? __ldg(posr + s) : -1;
+        }
+      };
+      fetch(0);
+      for (int i = 0; i < n_tiles; ++i) {
+        if (!wait_warp(meta_empty[i & 1], ((i >> 1) & 1) ^ 1, kSiteMetaEmpty)) break;
+        Meta& m = meta[i & 1];
+        int mn = INT_MAX, mx = INT_MIN;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool okk = nx[k] >= 0;
+          const uint32_t w = __ballot_sync(0xffffffffu, okk);
+          if (lane == 0) m.ok[k] = w;
+          m.pos[k * 32 + lane] = nx[k];
+          if (okk) {
+            mn = min(mn, nx[k]);
+            mx = max(mx, nx[k]);
+          }
+        }
+        mn = __reduce_min_sync(0xffffffffu, mn);
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        if (lane == 0) {
+          m.pmin = mn;
+          m.pmax = mx;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&meta_full[i & 1]));
+        fetch(i + 1);
+      }
+    }
+  } else if (warp < 4 + 4 * C::PARTS) {
+    // ---------------- converters
+    regs_decrease<REGS_CONV>();
+    const int ct = tid - 128 - (C::PARTS == 2 && warp >= 8 ? 128 : 0);   // thread of its warpgroup
+    // Which slots may count at all: of the window's reach of any valid token.
+    int plo = 0, phi = INT_MAX;
+    if (p.window > 0) {
+      int qn = INT_MAX, qx = INT_MIN;
+      for (int t = t0 + lane; t < t_end; t += 32) {
+        const int q = __ldg(p.qpos + static_cast<size_t>(b) * p.T + t);
+        qn = min(qn, q);
+        qx = max(qx, q);
+      }
+      qn = __reduce_min_sync(0xffffffffu, qn);
+      qx = __reduce_max_sync(0xffffffffu, qx);
+      window_range(qn, qx, p.window, plo, phi);
+    }
+    const Part8 src{p.posc + static_cast<size_t>(b) * p.S, s_base, hi, plo, phi, p.nb};
+    const size_t head = static_cast<size_t>(b) * p.S * p.H_kv * DH + static_cast<size_t>(j) * DH;
+    const size_t sc = static_cast<size_t>(b) * p.nb * p.H_kv + j;
+    const int n_parts = n_tiles * C::PARTS;
+    if constexpr (C::PARTS == 1) {
+      // K and V of each tile in turn
+      Fetched8 f;
+      fetch8<false>(f, src, p.K8 + head, p.K_scale + sc, p.H_kv * DH, p.H_kv, 0, 0, ct, n_tiles > 0);
+      for (int i = 0; i < n_tiles; ++i) {
+        if (!wait_warp(k_empty[i & 1], ((i >> 1) & 1) ^ 1, kSiteKEmpty)) break;
+        store8<false>(f, sK + (i & 1) * PART, ct);
+        publish8(k_full[i & 1], lane);
+        fetch8<false>(f, src, p.V8 + head, p.V_scale + sc, p.H_kv * DH, p.H_kv, i, 0, ct, true);
+        if (!wait_warp(v_empty[i & 1], ((i >> 1) & 1) ^ 1, kSiteVEmpty)) break;
+        store8<false>(f, sV + (i & 1) * PART, ct);
+        publish8(v_full[i & 1], lane);
+        fetch8<false>(f, src, p.K8 + head, p.K_scale + sc, p.H_kv * DH, p.H_kv, i + 1, 0, ct,
+                      i + 1 < n_tiles);
+      }
+    } else if (warp < 8) {
+      // K: channel halves
+      Fetched8 f;
+      fetch8<false>(f, src, p.K8 + head, p.K_scale + sc, p.H_kv * DH, p.H_kv, 0, 0, ct, n_tiles > 0);
+      for (int q = 0; q < n_parts; ++q) {
+        const int h = q & 1;
+        if (!wait_warp(k_empty[h], ((q >> 1) & 1) ^ 1, kSiteKEmpty)) break;
+        store8<false>(f, sK + h * PART, ct);
+        publish8(k_full[h], lane);
+        fetch8<false>(f, src, p.K8 + head + (h ^ 1) * 128, p.K_scale + sc, p.H_kv * DH, p.H_kv,
+                      (q + 1) >> 1, 0, ct, q + 1 < n_parts);
+      }
+    } else {
+      // V: slot halves
+      Fetched8 f;
+      fetch8<true>(f, src, p.V8 + head, p.V_scale + sc, p.H_kv * DH, p.H_kv, 0, 0, ct, n_tiles > 0);
+      for (int q = 0; q < n_parts; ++q) {
+        const int h = q & 1;
+        if (!wait_warp(v_empty[h], ((q >> 1) & 1) ^ 1, kSiteVEmpty)) break;
+        store8<true>(f, sV + h * PART, ct);
+        publish8(v_full[h], lane);
+        fetch8<true>(f, src, p.V8 + head, p.V_scale + sc, p.H_kv * DH, p.H_kv, (q + 1) >> 1, h ^ 1, ct,
+                     q + 1 < n_parts);
+      }
+    }
+  } else {
+    // ---------------- softmax of query tile e, thread r owns row r
+    regs_increase<REGS_SOFT>();
+    const int e = C::NQ == 2 ? (warp - 8) >> 2 : 0;
+    if (e < nq) {
+      const int q = warp & 3;                // TMEM lane quarter (= warp % 4)
+      const int r = q * 32 + lane;
+      const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+      const uint32_t o_base = tbase + lane_off + O_COL + e * 128;
+      const int t = t0 + e * C::TQ + r / G, h = j * G + r % G;
+      const bool row_valid = t < valid;
+      const int lim = row_valid ? p.end + t : -1;            // last visible slot
+      int plo = 0, phi = INT_MAX;
+      if (p.window > 0 && row_valid) {
+        const int qp = __ldg(p.qpos + static_cast<size_t>(b) * p.T + t);
+        window_range(qp, qp, p.window, plo, phi);
+      }
+      // over the warp's valid rows (the others are not stored)
+      const int w_lim = __reduce_min_sync(0xffffffffu, row_valid ? lim : INT_MAX);
+      const int w_plo = __reduce_max_sync(0xffffffffu, plo);
+      const int w_phi = __reduce_min_sync(0xffffffffu, phi);
+      float m_used = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int i = 0; i < n_tiles; ++i) {
+        const int sb = C::NQ == 2 ? e : (i & 1);
+        const uint32_t s_addr = tbase + lane_off + sb * 128;
+        ok = wait_warp(meta_full[i & 1], (i >> 1) & 1, kSiteMetaFull);
+        if (!ok) break;
+        const Meta& mt = meta[i & 1];
+        const int s_tile = s_base + i * BN;
+        const int pmin = mt.pmin, pmax = mt.pmax;
+        const bool win_ok = pmin >= w_plo && pmax <= w_phi;
+        const bool whole = (mt.ok[0] & mt.ok[1] & mt.ok[2] & mt.ok[3]) == 0xffffffffu &&
+                           s_tile + BN - 1 <= w_lim && win_ok;
+        ok = wait_warp(s_full[sb], C::NQ == 2 ? (i & 1) : ((i >> 1) & 1), kSiteSFull);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t ra[32], rb[32], rc[32], rd[32];
+        float m0, m1, m2, m3;
+        tmem_ld32_max(s_addr, ra, m0);
+        tmem_ld32_max(s_addr + 32, rb, m1);
+        tmem_ld32_max(s_addr + 64, rc, m2);
+        tmem_ld32_max(s_addr + 96, rd, m3);
+        tmem_ld_wait(ra);
+        tmem_ld_wait(rb);
+        tmem_ld_wait(rc);
+        tmem_ld_wait(rd);
+        tmem_ld_wait(m0);
+        tmem_ld_wait(m1);
+        tmem_ld_wait(m2);
+        tmem_ld_wait(m3);
+        if (!whole) {
+          uint32_t keep[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int c = lim - (s_tile + 32 * k);       // last visible column of the 32
+            keep[k] = mt.ok[k] & (c < 0 ? 0u : (c >= 31 ? 0xffffffffu : (2u << c) - 1u));
+          }
+          if (!win_ok) {
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w = 0;
+#pragma unroll 8
+              for (int c = 0; c < 32; ++c) {
+                const int ps = mt.pos[k * 32 + c];
+                w |= (ps >= plo && ps <= phi ? 1u : 0u) << c;
+              }
+              // (an index known at compile time keeps keep[] in registers)
+              keep[0] &= k == 0 ? w : 0xffffffffu;
+              keep[1] &= k == 1 ? w : 0xffffffffu;
+              keep[2] &= k == 2 ? w : 0xffffffffu;
+              keep[3] &= k == 3 ? w : 0xffffffffu;
+            }
+          }
+          m0 = mask_max(ra, keep[0]);
+          m1 = mask_max(rb, keep[1]);
+          m2 = mask_max(rc, keep[2]);
+          m3 = mask_max(rd, keep[3]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&meta_empty[i & 1]));
+        const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * LOG2E;
+        const bool grow = mx > m_used + RESCALE_THRESHOLD;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float m_new = grow ? mx : m_used;
+          const float factor = (m_new == m_used) ? 1.f : ex2(m_used - m_new);
+          if (i > 0) {
+            // O holds the PV of the tiles before: with two query tiles S_e of
+            // this tile was issued after them, with one PV may still run.
+            if constexpr (C::NQ == 1) {
+              ok = wait_warp(pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, kSitePvDone);
+              if (!ok) break;
+              tc_fence_after();
+            }
+#pragma unroll 1
+            for (int c = 0; c < DH / 32; ++c) {
+              uint32_t ro[32];
+              tmem_ld32(o_base + c * 32, ro);
+              tmem_ld_wait(ro);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                ro[k] = __float_as_uint(__uint_as_float(ro[k]) * factor);
+              tmem_st32(o_base + c * 32, ro);
+            }
+            tmem_st_wait();
+          }
+          l *= factor;
+          m_used = m_new;
+        }
+        const float mref = (m_used == -INFINITY) ? 0.f : m_used;
+        const float2 l2e = make_float2(LOG2E, LOG2E), negm = make_float2(-mref, -mref);
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                         make_float2(0.f, 0.f)};
+        {
+          uint32_t pk[32];
+          exp_pack(ra, pk, acc, l2e, negm);
+          exp_pack(rb, pk + 16, acc, l2e, negm);
+          tmem_st32(s_addr, pk);
+        }
+        {
+          uint32_t pk[32];
+          exp_pack(rc, pk, acc, l2e, negm);
+          exp_pack(rd, pk + 16, acc, l2e, negm);
+          tmem_st32(s_addr + 32, pk);
+        }
+        const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+        const float2 a = __fadd2_rn(a01, a23);
+        l += a.x + a.y;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[C::NQ == 2 ? e : (i & 1)]));
+      }
+      // ---------------- epilogue: this row of O
+      if (ok && n_tiles > 0) {
+        ok = wait_warp(o_final[e], 0, kSiteOFinal);
+        tc_fence_after();
+      }
+      const size_t orow = (static_cast<size_t>(b) * p.T + t) * p.H + h;
+      const bool have = row_valid && n_tiles > 0 && l != 0.f;
+      if (ok && t < p.T && p.stat != nullptr)
+        p.stat[orow * p.nsplit + split] = have ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
+      const float inv = have ? (p.nsplit == 1 ? 1.f / l : 1.f) : 0.f;
+      if (ok) {
+#pragma unroll 1
+        for (int c = 0; c < DH / 32; ++c) {
+          uint32_t ro[32];
+          if (n_tiles > 0) {
+            tmem_ld32(o_base + c * 32, ro);
+            tmem_ld_wait(ro);
+          }
+          if (t < p.T) {
+            if (p.nsplit == 1) {
+              store_row32(static_cast<uint16_t*>(p.O) + orow * DH + c * 32, ro, inv, have, p.o_f16);
+            } else {
+              float4* d = reinterpret_cast<float4*>(p.part + (orow * p.nsplit + split) * DH + c * 32);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                d[k] = have ? make_float4(__uint_as_float(ro[4 * k]), __uint_as_float(ro[4 * k + 1]),
+                                          __uint_as_float(ro[4 * k + 2]),
+                                          __uint_as_float(ro[4 * k + 3]))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
+        }
+        tc_fence_before();
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// First slot of batch row b that a valid token of an item (span tokens from
+// item * span) can see on a local layer, by its stored position; hi if none.
+__global__ void __launch_bounds__(1024) first8_kernel(const int32_t* __restrict__ posc,
+                                                      const int32_t* __restrict__ qpos,
+                                                      const int32_t* __restrict__ pad_lens, int T,
+                                                      int S, int end, int window, int span,
+                                                      int items, int32_t* __restrict__ first) {
+  pdl_enter();
+  __shared__ int found;
+  const int item = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int valid = min(T, T - (pad_lens != nullptr ? pad_lens[b] : 0));
+  const int t0 = item * span, t_end = min(t0 + span, valid);
+  const int hi = t_end > t0 ? end + t_end : 0;
+  int qn = INT_MAX, qx = INT_MIN;
+  for (int t = t0 + (tid & 31); t < t_end; t += 32) {
+    const int q = __ldg(qpos + static_cast<size_t>(b) * T + t);
+    qn = min(qn, q);
+    qx = max(qx, q);
+  }
+  qn = __reduce_min_sync(0xffffffffu, qn);
+  qx = __reduce_max_sync(0xffffffffu, qx);
+  int plo = 0, phi = INT_MAX;
+  window_range(qn, qx, window, plo, phi);
+  if (tid == 0) found = INT_MAX;
+  __syncthreads();
+  const int32_t* row = posc + static_cast<size_t>(b) * S;
+  for (int base = 0; base < hi; base += 8192) {
+    int best = INT_MAX;
+#pragma unroll
+    for (int k = 7; k >= 0; --k) {
+      const int s = base + k * 1024 + tid;
+      const int ps = s < hi ? __ldg(row + s) : -1;
+      if (ps >= plo && ps <= phi) best = s;
+    }
+    best = __reduce_min_sync(0xffffffffu, best);
+    if ((tid & 31) == 0 && best != INT_MAX) atomicMin(&found, best);
+    __syncthreads();
+    if (found != INT_MAX) break;
+    __syncthreads();
+  }
+  if (tid == 0) first[static_cast<size_t>(b) * items + item] = min(found, hi);
+}
+
+template <int DH, int G>
+cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
+  using C = Cfg<DH, G>;
+  CUtensorMap tq;
+  // Q' [B, T, H, d_h]: box {64 channels, the G heads of a kv head, TQ tokens, 1}
+  const uint64_t dims[4] = {static_cast<uint64_t>(DH), static_cast<uint64_t>(p.H),
+                            static_cast<uint64_t>(p.T), static_cast<uint64_t>(p.B)};
+  const uint64_t str[3] = {static_cast<uint64_t>(DH) * 2, static_cast<uint64_t>(p.H) * DH * 2,
+                           static_cast<uint64_t>(p.T) * p.H * DH * 2};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(C::TQ), 1};
+  if (!encode_tiled(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, Q, dims, str, box))
+    return cudaErrorInvalidValue;
+  auto kern = flash8_kernel<DH, G>;
+  int regs = 0;
+  if (cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, &regs)) return e;
+  // The softmax warpgroups' increases wait for what the others give up:
+  // launch only when the split fits the CTA's allocation.
+  if (regs < REGS_LAUNCH) return cudaErrorInvalidConfiguration;
+  const long long ctas = static_cast<long long>(p.items) * p.nsplit * p.H_kv * p.B;
+  if (ctas > INT_MAX) return cudaErrorInvalidValue;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), C::SMEM, stream, tq, p);
+}
+
+}  // namespace
+
+int flash8_span(int d_h, int G) { return (d_h == 128 ? 2 : 1) * (BM / G); }
+
+cudaError_t launch_flash8(const Flash8Args& a, cudaStream_t stream) {
+  const int G = a.H / a.H_kv;
+  const int span = flash8_span(a.d_h, G), items = (a.T + span - 1) / span;
+  if (a.window > 0) {
+    cudaError_t e = launch_pdl(first8_kernel, dim3(items, a.B), dim3(1024), 0, stream, a.posc,
+                               a.qpos, a.pad_lens, a.T, a.S, a.end, a.window, span, items, a.first);
+    if (e != cudaSuccess) return e;
+  }
+  Params p;
+  p.K8 = static_cast<const uint8_t*>(a.K8);
+  p.V8 = static_cast<const uint8_t*>(a.V8);
+  p.K_scale = a.K_scale;
+  p.V_scale = a.V_scale;
+  p.posc = a.posc;
+  p.qpos = a.qpos;
+  p.pad_lens = a.pad_lens;
+  p.first = a.window > 0 ? a.first : nullptr;
+  p.stat = a.stat;
+  p.part = a.part;
+  p.O = a.O;
+  p.o_f16 = a.o_f16;
+  p.B = a.B;
+  p.T = a.T;
+  p.S = a.S;
+  p.H = a.H;
+  p.H_kv = a.H_kv;
+  p.nb = c8_blocks(a.S);
+  p.end = a.end;
+  p.window = a.window;
+  p.nsplit = a.nsplit;
+  p.items = items;
+  p.status = a.status;
+#define G3_FLASH8_CASE(DH_, G_) \
+  if (a.d_h == DH_ && G == G_) return launch_cfg<DH_, G_>(a.Q, p, stream);
+  G3_FLASH8_CASE(128, 1)
+  G3_FLASH8_CASE(128, 2)
+  G3_FLASH8_CASE(128, 4)
+  G3_FLASH8_CASE(256, 1)
+  G3_FLASH8_CASE(256, 2)
+  G3_FLASH8_CASE(256, 4)
+#undef G3_FLASH8_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace g3
