@@ -13,12 +13,12 @@
 // tiles.
 //
 // Warps (d_h = 128, two query tiles e = 0, 1):
-//   0      TMA of the Q tiles
+//   0      TMA of the Q tiles (and for d_h = 256 of V's bytes)
 //   1      TMEM allocation and MMA issue
-//   2      positions: per tile a bit for each slot that holds a token, and the
-//          range of the stored positions
-//   4-7    converters: the K part, then the V part of each tile, fetched into
-//          registers one part ahead
+//   2      positions: per tile a bit for each slot that holds a token, the
+//          range of the stored positions, and the tile's scales
+//   3      TMA of the cache's bytes, 8 KB (64 slots x 128 channels) at a time
+//   4-7    converters: K, then V of each tile
 //   8-15   softmax of tile 0 and of tile 1, one thread per row
 // d_h = 256 has one query tile, converters of its own for K (4-7) and V
 // (8-11), softmax in 12-15.  Shared memory holds two 32 KB parts of K and two
@@ -63,13 +63,28 @@ static_assert(REGS_CTRL + REGS_CONV + 2 * REGS_SOFT <= 4 * REGS_LAUNCH &&
 
 enum : int {
   kSiteQ = 80, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty, kSiteSFull, kSitePFull,
-  kSitePvDone, kSiteMetaFull, kSiteMetaEmpty, kSiteOFinal
+  kSitePvDone, kSiteMetaFull, kSiteMetaEmpty, kSiteOFinal, kSiteRawFull,
+  kSiteRawEmpty
 };
+
+constexpr uint32_t RAW = 8192;              // bytes of a raw granule: 64 slots x 128 channels
+constexpr int NMETA = 4;
 
 struct Meta {
   uint32_t ok[4];          // slots of the tile that hold a token below the CTA's last slot
-  int pmin, pmax;          // range of their positions
+  uint32_t use[4];         // those of them in the windows' reach of some valid token
+  float ks[2], vs[2];      // scales of the two blocks
+  int pmin, pmax;          // range of the positions of the ok slots
+  int pad[2];
   int pos[BN];
+};
+
+struct Shared {
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2],
+      meta_full[NMETA], meta_empty[NMETA], raw_full[4], raw_empty[4], o_final[2], drain;
+  Meta meta[NMETA];
+  uint32_t tmem;
+  int abort_flag;
 };
 
 template <int DH, int G>
@@ -79,8 +94,11 @@ struct Cfg {
   static constexpr int NCH = DH / 64;
   static constexpr int PARTS = DH / 128;           // parts of a K or V tile
   static constexpr uint32_t QT_BYTES = BM * DH * 2;
-  static constexpr uint32_t SMEM = NQ * QT_BYTES + 4 * PART + 1024;
-  static_assert(SMEM + 4096 <= 232448, "shared memory budget");
+  // raw granules: d_h = 128 one ring of four for K and V in turn, d_h = 256
+  // a ring of two for each
+  static constexpr int RING = PARTS == 1 ? 4 : 2;
+  static constexpr uint32_t SMEM = NQ * QT_BYTES + 4 * PART + 4 * RAW + sizeof(Shared);
+  static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 struct Params {
@@ -126,23 +144,24 @@ __device__ __forceinline__ float mask_max(uint32_t (&r)[32], uint32_t keep) {
 
 template <int DH, int G>
 __global__ void __launch_bounds__(THREADS, 1)
-    flash8_kernel(const __grid_constant__ CUtensorMap tmQ, const Params p) {
+    flash8_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const Params p) {
   pdl_enter();
   using C = Cfg<DH, G>;
   if (*reinterpret_cast<volatile int*>(p.status) != 0) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  // (the swizzled tiles need 1024-byte alignment; there is no other shared memory)
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sK = smem + C::NQ * C::QT_BYTES;   // two parts
   uint8_t* sV = sK + 2 * PART;                // two parts
-  __shared__ __align__(8) uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
-      p_full[2], pv_done[2], meta_full[2], meta_empty[2], o_final[2], drain;
-  __shared__ Meta meta[2];
-  __shared__ uint32_t tmem_sh;
-  __shared__ int abort_flag;
+  uint8_t* sR = sV + 2 * PART;                // raw granules
+  Shared& sh = *reinterpret_cast<Shared*>(sR + 4 * RAW);
+  if ((smem_u32(smem) & 1023u) != 0) {        // (never, by the declaration above)
+    if (tid == 0) record_error(p.status, kDevErrTimeoutBase + kSiteQ);
+    return;
+  }
 
   // Item: latest tokens (most slots on a causal prompt) first, the items of a
   // kv head next to each other so that they share its bytes in L2.
@@ -166,53 +185,84 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int s_base = lo + first_tile * BN;
 
   if (tid == 0) {
-    mbar_init(smem_u32(&q_full), 1);
+    mbar_init(smem_u32(&sh.q_full), 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&k_full[s]), 4);
-      mbar_init(smem_u32(&k_empty[s]), 1);
-      mbar_init(smem_u32(&v_full[s]), 4);
-      mbar_init(smem_u32(&v_empty[s]), 1);
-      mbar_init(smem_u32(&s_full[s]), 1);
-      mbar_init(smem_u32(&p_full[s]), 4);
-      mbar_init(smem_u32(&pv_done[s]), 1);
-      mbar_init(smem_u32(&meta_full[s]), 1);
-      mbar_init(smem_u32(&meta_empty[s]), 4 * nq);
-      mbar_init(smem_u32(&o_final[s]), 1);
+      mbar_init(smem_u32(&sh.k_full[s]), 4);
+      mbar_init(smem_u32(&sh.k_empty[s]), 1);
+      mbar_init(smem_u32(&sh.v_full[s]), 4);
+      mbar_init(smem_u32(&sh.v_empty[s]), 1);
+      mbar_init(smem_u32(&sh.s_full[s]), 1);
+      mbar_init(smem_u32(&sh.p_full[s]), 4);
+      mbar_init(smem_u32(&sh.pv_done[s]), 1);
+      mbar_init(smem_u32(&sh.o_final[s]), 1);
     }
-    mbar_init(smem_u32(&drain), 1);
-    abort_flag = 0;
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(smem_u32(&sh.raw_full[s]), 1);
+      mbar_init(smem_u32(&sh.raw_empty[s]), 4);
+      mbar_init(smem_u32(&sh.meta_full[s]), 1);
+      mbar_init(smem_u32(&sh.meta_empty[s]), 4 * (nq + C::PARTS));   // softmax and converter warps
+    }
+    mbar_init(smem_u32(&sh.drain), 1);
+    sh.abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_sh), 512);
+    tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_relinquish();
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = tmem_sh;
+  const uint32_t tbase = sh.tmem;
   auto wait_warp = [&](uint64_t& bar, int parity, int site) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, &abort_flag, p.status, site));
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, &sh.abort_flag, p.status, site));
   };
 
   if (warp < 4) {
     regs_decrease<REGS_CTRL>();
+    // Raw granule n of a stream (RING slots from slot r0 on): of K, granule
+    // (channel half, slot half) of a tile, of V d_h = 256 (slot half, channel
+    // half); d_h = 128 has K's and V's two slot halves in one stream.
+    auto load_raw = [&](int r0, bool v, int n_granules) {
+      int n = 0;
+      for (; n < n_granules; ++n) {
+        const int r = r0 + n % C::RING;
+        if (!mbar_wait(smem_u32(&sh.raw_empty[r]), ((n / C::RING) & 1) ^ 1, &sh.abort_flag, p.status,
+                       kSiteRawEmpty))
+          break;
+        const int i = n >> 2, hh = (n >> 1) & 1, gg = n & 1;   // tile, part, granule of the part
+        const uint32_t bar = smem_u32(&sh.raw_full[r]);
+        mbar_arrive_expect_tx(bar, RAW);
+        if constexpr (C::PARTS == 1)
+          tma_load_4d(smem_u32(sR + r * RAW), hh ? &tmV : &tmK, bar, 0, j, s_base + i * BN + gg * 64, b);
+        else
+          tma_load_4d(smem_u32(sR + r * RAW), v ? &tmV : &tmK, bar, (v ? gg : hh) * 128, j,
+                      s_base + i * BN + (v ? hh : gg) * 64, b);
+      }
+      for (int k = max(0, n - C::RING); k < n; ++k)
+        mbar_wait_drain(smem_u32(&sh.raw_full[r0 + k % C::RING]), (k / C::RING) & 1);
+    };
     if (warp == 0 && lane == 0 && n_tiles > 0) {
       // ---------------- Q
-      const uint32_t qb = smem_u32(&q_full);
+      const uint32_t qb = smem_u32(&sh.q_full);
       mbar_arrive_expect_tx(qb, nq * C::QT_BYTES);
       for (int e = 0; e < nq; ++e)
         for (int ch = 0; ch < C::NCH; ++ch)
           tma_load_4d(smem_u32(sQ + e * C::QT_BYTES + ch * CHUNK), &tmQ, qb, ch * 64, j * G,
                       t0 + e * C::TQ, b);
+      if constexpr (C::PARTS == 2) load_raw(2, true, 4 * n_tiles);
       mbar_wait_drain(qb, 0);
+    } else if (warp == 3 && lane == 0) {
+      load_raw(0, false, 4 * n_tiles);
     } else if (warp == 1 && n_tiles > 0) {
       // ---------------- MMA issue (whole warp, one elected lane)
       const uint32_t lead = elect_one();
       constexpr uint32_t idesc_qk = idesc_f16(BM, BN, /*f16*/ 0, 0, 0);
       constexpr uint32_t idesc_pv = idesc_f16(BM, DH, /*f16*/ 0, 0, /*B MN-major*/ 1);
       const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK), v_addr = smem_u32(sV);
-      bool ok = wait_warp(q_full, 0, kSiteQ);
+      bool ok = wait_warp(sh.q_full, 0, kSiteQ);
       if constexpr (C::NQ == 2) {
         auto issue_s = [&](int e, int i) {
           const uint32_t kb = k_addr + (i & 1) * PART;
@@ -222,11 +272,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             mma_ss_lead(lead, tbase + e * 128, sdesc_sw128(q_addr + e * C::QT_BYTES + off, 16, 1024),
                         sdesc_sw128(kb + off, 16, 1024), idesc_qk, k > 0 ? 1u : 0u);
           }
-          mma_commit_lead(lead, smem_u32(&s_full[e]));
+          mma_commit_lead(lead, smem_u32(&sh.s_full[e]));
         };
         auto issue_pv = [&](int e, int i) -> bool {
-          if (!wait_warp(p_full[e], i & 1, kSitePFull)) return false;
-          if (e == 0 && !wait_warp(v_full[i & 1], (i >> 1) & 1, kSiteVFull)) return false;
+          if (!wait_warp(sh.p_full[e], i & 1, kSitePFull)) return false;
+          if (e == 0 && !wait_warp(sh.v_full[i & 1], (i >> 1) & 1, kSiteVFull)) return false;
           tc_fence_after();
           const uint32_t vb = v_addr + (i & 1) * PART;
 #pragma unroll
@@ -237,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           return true;
         };
         for (int i = 0; ok && i < n_tiles; ++i) {
-          ok = wait_warp(k_full[i & 1], (i >> 1) & 1, kSiteKFull);
+          ok = wait_warp(sh.k_full[i & 1], (i >> 1) & 1, kSiteKFull);
           if (!ok) break;
           tc_fence_after();
           for (int e = 0; ok && e < nq; ++e) {
@@ -245,37 +295,37 @@ __global__ void __launch_bounds__(THREADS, 1)
             // pipe runs PV_e before it.
             if (i > 0) ok = issue_pv(e, i - 1);
             if (!ok) break;
-            if (i > 0 && e == nq - 1) mma_commit_lead(lead, smem_u32(&v_empty[(i - 1) & 1]));
+            if (i > 0 && e == nq - 1) mma_commit_lead(lead, smem_u32(&sh.v_empty[(i - 1) & 1]));
             issue_s(e, i);
           }
           if (!ok) break;
-          mma_commit_lead(lead, smem_u32(&k_empty[i & 1]));
+          mma_commit_lead(lead, smem_u32(&sh.k_empty[i & 1]));
         }
         for (int e = 0; ok && e < nq; ++e) {
           ok = issue_pv(e, n_tiles - 1);
-          if (ok) mma_commit_lead(lead, smem_u32(&o_final[e]));
+          if (ok) mma_commit_lead(lead, smem_u32(&sh.o_final[e]));
         }
       } else {
         auto issue_pv = [&](int i) -> bool {
-          if (!wait_warp(p_full[i & 1], (i >> 1) & 1, kSitePFull)) return false;
+          if (!wait_warp(sh.p_full[i & 1], (i >> 1) & 1, kSitePFull)) return false;
           for (int h = 0; h < 2; ++h) {
-            if (!wait_warp(v_full[h], i & 1, kSiteVFull)) return false;
+            if (!wait_warp(sh.v_full[h], i & 1, kSiteVFull)) return false;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_ts_lead(lead, tbase + O_COL, tbase + (i & 1) * 128 + (h * 4 + k) * 8,
                           sdesc_sw128(v_addr + h * PART + k * 2048, CHUNK / 2, 1024), idesc_pv,
                           (i > 0 || h > 0 || k > 0) ? 1u : 0u);
-            mma_commit_lead(lead, smem_u32(&v_empty[h]));
+            mma_commit_lead(lead, smem_u32(&sh.v_empty[h]));
           }
-          mma_commit_lead(lead, smem_u32(&pv_done[i & 1]));
+          mma_commit_lead(lead, smem_u32(&sh.pv_done[i & 1]));
           return true;
         };
         for (int i = 0; ok && i < n_tiles; ++i) {
           // S of tile i is issued before PV of tile i - 1 and after PV of
           // tile i - 2, whose P its columns held.
           for (int h = 0; ok && h < 2; ++h) {
-            ok = wait_warp(k_full[h], i & 1, kSiteKFull);
+            ok = wait_warp(sh.k_full[h], i & 1, kSiteKFull);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -284,38 +334,62 @@ __global__ void __launch_bounds__(THREADS, 1)
               mma_ss_lead(lead, tbase + (i & 1) * 128, sdesc_sw128(q_addr + off, 16, 1024),
                           sdesc_sw128(k_addr + off, 16, 1024), idesc_qk, (h > 0 || k > 0) ? 1u : 0u);
             }
-            mma_commit_lead(lead, smem_u32(&k_empty[h]));
+            mma_commit_lead(lead, smem_u32(&sh.k_empty[h]));
           }
           if (!ok) break;
-          mma_commit_lead(lead, smem_u32(&s_full[i & 1]));
+          mma_commit_lead(lead, smem_u32(&sh.s_full[i & 1]));
           if (i > 0) ok = issue_pv(i - 1);
         }
         if (ok) ok = issue_pv(n_tiles - 1);
-        if (ok) mma_commit_lead(lead, smem_u32(&o_final[0]));
+        if (ok) mma_commit_lead(lead, smem_u32(&sh.o_final[0]));
       }
-      mma_commit_lead(lead, smem_u32(&drain));
-      mbar_wait_drain(smem_u32(&drain), 0);
+      mma_commit_lead(lead, smem_u32(&sh.drain));
+      mbar_wait_drain(smem_u32(&sh.drain), 0);
     } else if (warp == 2) {
-      // ---------------- positions of each tile's slots
+      // ---------------- positions and scales of each tile's slots
+      // Which slots may count at all: in the windows' reach of any valid token.
+      int plo = 0, phi = INT_MAX;
+      if (p.window > 0) {
+        int qn = INT_MAX, qx = INT_MIN;
+        for (int t = t0 + lane; t < t_end; t += 32) {
+          const int q = __ldg(p.qpos + static_cast<size_t>(b) * p.T + t);
+          qn = min(qn, q);
+          qx = max(qx, q);
+        }
+        qn = __reduce_min_sync(0xffffffffu, qn);
+        qx = __reduce_max_sync(0xffffffffu, qx);
+        window_range(qn, qx, p.window, plo, phi);
+      }
       const int32_t* posr = p.posc + static_cast<size_t>(b) * p.S;
+      // lanes 0, 1: K's scales of the tile's blocks, 2, 3: V's
+      const float* sc = (lane & 2 ? p.V_scale : p.K_scale) + static_cast<size_t>(b) * p.nb * p.H_kv + j;
       int nx[4];
+      float ns = 0.f;
       auto fetch = [&](int i) {
+        if (i >= n_tiles) return;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int s = s_base + i * BN + k * 32 + lane;
-          nx[k] = i < n_tiles && s < hi ? __ldg(posr + s) : -1;
+          nx[k] = s < hi ? __ldg(posr + s) : -1;
         }
+        if (lane < 4)
+          ns = __ldg(sc + static_cast<size_t>(min((s_base + i * BN) / kC8Block + (lane & 1), p.nb - 1)) *
+                              p.H_kv);
       };
       fetch(0);
       for (int i = 0; i < n_tiles; ++i) {
-        if (!wait_warp(meta_empty[i & 1], ((i >> 1) & 1) ^ 1, kSiteMetaEmpty)) break;
-        Meta& m = meta[i & 1];
+        if (!wait_warp(sh.meta_empty[i % NMETA], ((i / NMETA) & 1) ^ 1, kSiteMetaEmpty)) break;
+        Meta& m = sh.meta[i % NMETA];
         int mn = INT_MAX, mx = INT_MIN;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const bool okk = nx[k] >= 0;
           const uint32_t w = __ballot_sync(0xffffffffu, okk);
-          if (lane == 0) m.ok[k] = w;
+          const uint32_t u = __ballot_sync(0xffffffffu, nx[k] >= plo && nx[k] <= phi);
+          if (lane == 0) {
+            m.ok[k] = w;
+            m.use[k] = u;
+          }
           m.pos[k * 32 + lane] = nx[k];
           if (okk) {
             mn = min(mn, nx[k]);
@@ -324,74 +398,75 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         mn = __reduce_min_sync(0xffffffffu, mn);
         mx = __reduce_max_sync(0xffffffffu, mx);
+        if (lane < 4) (lane & 2 ? m.vs : m.ks)[lane & 1] = ns;
         if (lane == 0) {
           m.pmin = mn;
           m.pmax = mx;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&meta_full[i & 1]));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.meta_full[i % NMETA]));
         fetch(i + 1);
       }
     }
   } else if (warp < 4 + 4 * C::PARTS) {
     // ---------------- converters
     regs_decrease<REGS_CONV>();
-    const int ct = tid - 128 - (C::PARTS == 2 && warp >= 8 ? 128 : 0);   // thread of its warpgroup
-    // Which slots may count at all: of the window's reach of any valid token.
-    int plo = 0, phi = INT_MAX;
-    if (p.window > 0) {
-      int qn = INT_MAX, qx = INT_MIN;
-      for (int t = t0 + lane; t < t_end; t += 32) {
-        const int q = __ldg(p.qpos + static_cast<size_t>(b) * p.T + t);
-        qn = min(qn, q);
-        qx = max(qx, q);
+    const int ct = tid & 127;                  // thread of its warpgroup
+    const int col = ct & 7, row0 = ct >> 3;    // 16-channel group, slots row0 + 16 k of a granule
+    // Granule n of the warpgroup's stream (d_h = 128: K, V of each tile in
+    // turn; d_h = 256: warps 4-7 K, 8-11 V): two make a part of 32 KB of fp16.
+    // Wide parts are 128 slots x 128 channels, half parts (V of d_h = 256) 64
+    // slots x 256 channels.
+    const bool v256 = C::PARTS == 2 && warp >= 8;
+    const int r0 = v256 ? 2 : 0;
+#pragma unroll 1
+    for (int n = 0; n < 4 * n_tiles; ++n) {
+      const int i = n >> 2, hh = (n >> 1) & 1, gg = n & 1;
+      const bool v = C::PARTS == 1 ? hh : v256;
+      const int buf = C::PARTS == 1 ? (i & 1) : hh, use = C::PARTS == 1 ? (i >> 1) : i;
+      if ((n & 3) == 0 && !wait_warp(sh.meta_full[i % NMETA], (i / NMETA) & 1, kSiteMetaFull)) break;
+      const int r = r0 + n % C::RING;
+      if (!wait_warp(sh.raw_full[r], (n / C::RING) & 1, kSiteRawFull)) break;
+      const Meta& m = sh.meta[i % NMETA];
+      const int blk = v256 ? hh : gg;          // 64-slot block of the tile
+      const float s = (v ? m.vs : m.ks)[blk];
+      const uint32_t u0 = m.use[2 * blk], u1 = m.use[2 * blk + 1];
+      uint4 x[4];
+      uint32_t sc[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = row0 + 16 * k;
+        x[k] = *reinterpret_cast<const uint4*>(sR + r * RAW + row * 128 + ((col ^ (row & 7)) << 4));
+        sc[k] = pack_half2(s, s);
       }
-      qn = __reduce_min_sync(0xffffffffu, qn);
-      qx = __reduce_max_sync(0xffffffffu, qx);
-      window_range(qn, qx, p.window, plo, phi);
-    }
-    const Part8 src{p.posc + static_cast<size_t>(b) * p.S, s_base, hi, plo, phi, p.nb};
-    const size_t head = static_cast<size_t>(b) * p.S * p.H_kv * DH + static_cast<size_t>(j) * DH;
-    const size_t sc = static_cast<size_t>(b) * p.nb * p.H_kv + j;
-    const int n_parts = n_tiles * C::PARTS;
-    if constexpr (C::PARTS == 1) {
-      // K and V of each tile in turn
-      Fetched8 f;
-      fetch8<false>(f, src, p.K8 + head, p.K_scale + sc, p.H_kv * DH, p.H_kv, 0, 0, ct, n_tiles > 0);
-      for (int i = 0; i < n_tiles; ++i) {
-        if (!wait_warp(k_empty[i & 1], ((i >> 1) & 1) ^ 1, kSiteKEmpty)) break;
-        store8<false>(f, sK + (i & 1) * PART, ct);
-        publish8(k_full[i & 1], lane);
-        fetch8<false>(f, src, p.V8 + head, p.V_scale + sc, p.H_kv * DH, p.H_kv, i, 0, ct, true);
-        if (!wait_warp(v_empty[i & 1], ((i >> 1) & 1) ^ 1, kSiteVEmpty)) break;
-        store8<false>(f, sV + (i & 1) * PART, ct);
-        publish8(v_full[i & 1], lane);
-        fetch8<false>(f, src, p.K8 + head, p.K_scale + sc, p.H_kv * DH, p.H_kv, i + 1, 0, ct,
-                      i + 1 < n_tiles);
+      if ((u0 & u1) != 0xffffffffu) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (!(((k < 2 ? u0 : u1) >> ((row0 + 16 * k) & 31)) & 1u)) {
+            x[k] = make_uint4(0, 0, 0, 0);
+            sc[k] = 0u;
+          }
+        }
       }
-    } else if (warp < 8) {
-      // K: channel halves
-      Fetched8 f;
-      fetch8<false>(f, src, p.K8 + head, p.K_scale + sc, p.H_kv * DH, p.H_kv, 0, 0, ct, n_tiles > 0);
-      for (int q = 0; q < n_parts; ++q) {
-        const int h = q & 1;
-        if (!wait_warp(k_empty[h], ((q >> 1) & 1) ^ 1, kSiteKEmpty)) break;
-        store8<false>(f, sK + h * PART, ct);
-        publish8(k_full[h], lane);
-        fetch8<false>(f, src, p.K8 + head + (h ^ 1) * 128, p.K_scale + sc, p.H_kv * DH, p.H_kv,
-                      (q + 1) >> 1, 0, ct, q + 1 < n_parts);
+      if (gg == 0 && !wait_warp(v ? sh.v_empty[buf] : sh.k_empty[buf], (use & 1) ^ 1, kSiteKEmpty)) break;
+      uint8_t* base = (v ? sV : sK) + buf * PART +
+                      (v256 ? (gg * 2 + (col >> 2)) * (CHUNK / 2) : (col >> 2) * CHUNK + gg * (CHUNK / 2));
+      if (s > 128.f) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          store16_values<true>(x[k], sc[k], col, row0 + 16 * k, base + (row0 + 16 * k) * 128);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          store16_values<false>(x[k], sc[k], col, row0 + 16 * k, base + (row0 + 16 * k) * 128);
       }
-    } else {
-      // V: slot halves
-      Fetched8 f;
-      fetch8<true>(f, src, p.V8 + head, p.V_scale + sc, p.H_kv * DH, p.H_kv, 0, 0, ct, n_tiles > 0);
-      for (int q = 0; q < n_parts; ++q) {
-        const int h = q & 1;
-        if (!wait_warp(v_empty[h], ((q >> 1) & 1) ^ 1, kSiteVEmpty)) break;
-        store8<true>(f, sV + h * PART, ct);
-        publish8(v_full[h], lane);
-        fetch8<true>(f, src, p.V8 + head, p.V_scale + sc, p.H_kv * DH, p.H_kv, (q + 1) >> 1, h ^ 1, ct,
-                     q + 1 < n_parts);
+      // (the raw bytes are read: their values are stored)
+      if (gg == 1) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&sh.raw_empty[r]));
+        if (gg == 1) mbar_arrive(smem_u32(v ? &sh.v_full[buf] : &sh.k_full[buf]));
+        if ((n & 3) == 3) mbar_arrive(smem_u32(&sh.meta_empty[i % NMETA]));
       }
     }
   } else {
@@ -420,15 +495,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int i = 0; i < n_tiles; ++i) {
         const int sb = C::NQ == 2 ? e : (i & 1);
         const uint32_t s_addr = tbase + lane_off + sb * 128;
-        ok = wait_warp(meta_full[i & 1], (i >> 1) & 1, kSiteMetaFull);
+        ok = wait_warp(sh.meta_full[i % NMETA], (i / NMETA) & 1, kSiteMetaFull);
         if (!ok) break;
-        const Meta& mt = meta[i & 1];
+        const Meta& mt = sh.meta[i % NMETA];
         const int s_tile = s_base + i * BN;
         const int pmin = mt.pmin, pmax = mt.pmax;
         const bool win_ok = pmin >= w_plo && pmax <= w_phi;
         const bool whole = (mt.ok[0] & mt.ok[1] & mt.ok[2] & mt.ok[3]) == 0xffffffffu &&
                            s_tile + BN - 1 <= w_lim && win_ok;
-        ok = wait_warp(s_full[sb], C::NQ == 2 ? (i & 1) : ((i >> 1) & 1), kSiteSFull);
+        ok = wait_warp(sh.s_full[sb], C::NQ == 2 ? (i & 1) : ((i >> 1) & 1), kSiteSFull);
         if (!ok) break;
         tc_fence_after();
         uint32_t ra[32], rb[32], rc[32], rd[32];
@@ -474,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           m3 = mask_max(rd, keep[3]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&meta_empty[i & 1]));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.meta_empty[i % NMETA]));
         const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * LOG2E;
         const bool grow = mx > m_used + RESCALE_THRESHOLD;
         if (__any_sync(0xffffffffu, grow)) {
@@ -484,7 +559,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // O holds the PV of the tiles before: with two query tiles S_e of
             // this tile was issued after them, with one PV may still run.
             if constexpr (C::NQ == 1) {
-              ok = wait_warp(pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, kSitePvDone);
+              ok = wait_warp(sh.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, kSitePvDone);
               if (!ok) break;
               tc_fence_after();
             }
@@ -525,11 +600,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_full[C::NQ == 2 ? e : (i & 1)]));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[C::NQ == 2 ? e : (i & 1)]));
       }
       // ---------------- epilogue: this row of O
       if (ok && n_tiles > 0) {
-        ok = wait_warp(o_final[e], 0, kSiteOFinal);
+        ok = wait_warp(sh.o_final[e], 0, kSiteOFinal);
         tc_fence_after();
       }
       const size_t orow = (static_cast<size_t>(b) * p.T + t) * p.H + h;
@@ -616,7 +691,7 @@ __global__ void __launch_bounds__(1024) first8_kernel(const int32_t* __restrict_
 template <int DH, int G>
 cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
   using C = Cfg<DH, G>;
-  CUtensorMap tq;
+  CUtensorMap tq, tk, tv;
   // Q' [B, T, H, d_h]: box {64 channels, the G heads of a kv head, TQ tokens, 1}
   const uint64_t dims[4] = {static_cast<uint64_t>(DH), static_cast<uint64_t>(p.H),
                             static_cast<uint64_t>(p.T), static_cast<uint64_t>(p.B)};
@@ -624,6 +699,15 @@ cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
                            static_cast<uint64_t>(p.T) * p.H * DH * 2};
   const uint32_t box[4] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(C::TQ), 1};
   if (!encode_tiled(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, Q, dims, str, box))
+    return cudaErrorInvalidValue;
+  // caches [B, S, H_kv, d_h] of bytes: box {128 channels, 1 head, 64 slots, 1 row}
+  const uint64_t kdims[4] = {static_cast<uint64_t>(DH), static_cast<uint64_t>(p.H_kv),
+                             static_cast<uint64_t>(p.S), static_cast<uint64_t>(p.B)};
+  const uint64_t kstr[3] = {static_cast<uint64_t>(DH), static_cast<uint64_t>(p.H_kv) * DH,
+                            static_cast<uint64_t>(p.S) * p.H_kv * DH};
+  const uint32_t kbox[4] = {128, 1, 64, 1};
+  if (!encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.K8, kdims, kstr, kbox) ||
+      !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.V8, kdims, kstr, kbox))
     return cudaErrorInvalidValue;
   auto kern = flash8_kernel<DH, G>;
   int regs = 0;
@@ -633,7 +717,7 @@ cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
   if (regs < REGS_LAUNCH) return cudaErrorInvalidConfiguration;
   const long long ctas = static_cast<long long>(p.items) * p.nsplit * p.H_kv * p.B;
   if (ctas > INT_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), C::SMEM, stream, tq, p);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), C::SMEM, stream, tq, tk, tv, p);
 }
 
 }  // namespace

@@ -51,94 +51,36 @@ __device__ __forceinline__ void window_range(int qn, int qx, int window, int& pl
   phi = static_cast<int>(z < -1 ? -1 : (z > INT_MAX ? INT_MAX : z));
 }
 
-// A part: 16 KB of cache bytes as 32 KB of fp16, by one warpgroup, 128 bytes
-// per thread.  Wide parts (HALF false): 128 slots x 128 channels, 8 threads
-// per slot; half parts: 64 slots x 256 channels, 16 threads per slot.  Global
-// loads are whole 128-byte lines; the two 16-byte stores of a thread go out
-// in an order that puts eight neighbouring threads on eight bank groups.
-struct Part8 {
-  const int32_t* pos;   // the batch row's positions
-  int s_base, hi;       // first slot of tile 0; slots from hi on are hidden
-  int plo, phi;         // positions outside are hidden
-  int nb;               // blocks of the cache
-};
-
-struct Fetched8 {
-  uint4 x[8];
-  uint32_t ok;          // bit it: the slot of step it counts
-  float s0, s1;         // scales of the first and second 64 slots
-};
-
-// Fetch part `half` (slots 64 * half .. of a half part) of tile i: num, scale
-// point at the batch row's and head's first byte (plus a channel offset) and
-// scale; ld, lds: elements between slots and between blocks.
-template <bool HALF>
-__device__ __forceinline__ void fetch8(Fetched8& f, const Part8& src, const uint8_t* num,
-                                       const float* scale, int ld, int lds, int i, int half, int ct,
-                                       bool any) {
-  if (!any) return;
-  constexpr int TPS = HALF ? 16 : 8;
-  const int s0 = src.s_base + i * 128 + (HALF ? half * 64 : 0);
-  const int row = ct / TPS;
-  const uint8_t* a = num + (ct % TPS) * 16;
-  uint32_t ok = 0;
+// 16 cache bytes (one slot's channels 16 col .. 16 col + 15) as fp16 values in
+// a 128-byte-swizzled tile: base points at the slot's 128-byte row in the
+// chunk of 64 channels that holds them.  scale2: the block's as two fp16, or 0 with x = 0
+// for a hidden slot.  CLAMP for scales above 128, which can take a value past
+// fp16's largest; it becomes 65504 there.  The two 16-byte stores go out in an
+// order that puts eight neighbouring threads (col 0..7 of a slot) on eight
+// bank groups.
+template <bool CLAMP>
+__device__ __forceinline__ void store16_values(const uint4& x, uint32_t scale2, int col, int row,
+                                               uint8_t* base) {
+  const __half2 scale = *reinterpret_cast<const __half2*>(&scale2);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t o[8];
 #pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    const int s = s0 + row + it * (128 / TPS);
-    int ps = -1;
-    f.x[it] = make_uint4(0, 0, 0, 0);
-    if (s < src.hi) {
-      ps = __ldg(src.pos + s);
-      f.x[it] = __ldg(reinterpret_cast<const uint4*>(a + static_cast<size_t>(s) * ld));
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t lo = c8_half2(w[k]), hi = c8_half2_hi(w[k]);
+    __half2 v0 = __hmul2(*reinterpret_cast<const __half2*>(&lo), scale);
+    __half2 v1 = __hmul2(*reinterpret_cast<const __half2*>(&hi), scale);
+    if constexpr (CLAMP) {
+      const __half2 top = __float2half2_rn(65504.f);
+      v0 = __hmax2_nan(__hmin2_nan(v0, top), __hneg2(top));
+      v1 = __hmax2_nan(__hmin2_nan(v1, top), __hneg2(top));
     }
-    ok |= (ps >= src.plo && ps <= src.phi ? 1u : 0u) << it;
+    o[2 * k] = *reinterpret_cast<uint32_t*>(&v0);
+    o[2 * k + 1] = *reinterpret_cast<uint32_t*>(&v1);
   }
-  f.ok = ok;
-  const int blk = s0 / kC8Block;
-  f.s0 = __ldg(scale + static_cast<size_t>(min(blk, src.nb - 1)) * lds);
-  f.s1 = HALF ? f.s0 : __ldg(scale + static_cast<size_t>(min(blk + 1, src.nb - 1)) * lds);
-}
-
-// Its values in fp16, hidden slots as zeros, to the 128-byte-swizzled chunks
-// of 64 channels at dst.
-template <bool HALF>
-__device__ __forceinline__ void store8(const Fetched8& f, uint8_t* dst, int ct) {
-  constexpr int TPS = HALF ? 16 : 8;
-  constexpr uint32_t CH = HALF ? 64 * 128 : 128 * 128;
-  const int col = ct % TPS;                    // 16-channel group
-  const int u0 = (col & 3) * 2;
-  const bool swap = (col & 4) != 0;
-  const __half2 zero = __float2half2_rn(0.f);
-  // (a scale above 128 can take a value past fp16's largest: 65504 there)
-  const bool big = f.s0 > 128.f || f.s1 > 128.f;
-  const __half2 h0 = __float2half2_rn(f.s0), h1 = __float2half2_rn(f.s1);
-#pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    const int row = ct / TPS + it * (128 / TPS);
-    const bool ok = (f.ok >> it) & 1u;
-    const __half2 s = ok ? (!HALF && it >= 4 ? h1 : h0) : zero;
-    const uint32_t w[4] = {ok ? f.x[it].x : 0u, ok ? f.x[it].y : 0u, ok ? f.x[it].z : 0u,
-                           ok ? f.x[it].w : 0u};
-    uint32_t o[8];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t lo = c8_half2(w[k]), hi = c8_half2_hi(w[k]);
-      __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&lo), s);
-      __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&hi), s);
-      if (big) {
-        const __half2 top = __float2half2_rn(65504.f);
-        a = __hmax2_nan(__hmin2_nan(a, top), __hneg2(top));
-        b = __hmax2_nan(__hmin2_nan(b, top), __hneg2(top));
-      }
-      o[2 * k] = *reinterpret_cast<uint32_t*>(&a);
-      o[2 * k + 1] = *reinterpret_cast<uint32_t*>(&b);
-    }
-    uint8_t* base = dst + (col >> 2) * CH + row * 128;
-    const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-    const int r7 = row & 7;
-    *reinterpret_cast<uint4*>(base + (((u0 + (swap ? 1 : 0)) ^ r7) << 4)) = swap ? b : a;
-    *reinterpret_cast<uint4*>(base + (((u0 + (swap ? 0 : 1)) ^ r7) << 4)) = swap ? a : b;
-  }
+  const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
+  const int u0 = (col & 3) * 2, swap = (col >> 2) & 1, r7 = row & 7;
+  *reinterpret_cast<uint4*>(base + (((u0 + swap) ^ r7) << 4)) = swap ? b : a;
+  *reinterpret_cast<uint4*>(base + (((u0 + 1 - swap) ^ r7) << 4)) = swap ? a : b;
 }
 
 // A warp's stores visible to the tensor core, then its arrival.

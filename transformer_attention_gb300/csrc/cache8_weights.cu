@@ -223,24 +223,56 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp >= 4 && warp < 8) {
     // ---------------- converters: the tile's K, once per head
     const int ct = tid - 128;
-    const Part8 src{p.posc + static_cast<size_t>(b) * p.S, s_tile, hi, 0, INT_MAX, p.nb};
-    const uint8_t* num = p.K8 + static_cast<size_t>(b) * p.S * p.H_kv * DH;
+    const uint8_t* num = p.K8 + static_cast<size_t>(b) * p.S * p.H_kv * DH + (ct % 8) * 16;
     const float* sc = p.K_scale + static_cast<size_t>(b) * p.nb * p.H_kv;
+    const int32_t* posr = p.posc + static_cast<size_t>(b) * p.S;
     if (n_units > 0) {
       const int h_first = head_of(u0), n_parts = (head_of(u1 - 1) - h_first + 1) * C::PARTS;
-      Fetched8 f;
-      fetch8<false>(f, src, num + h_first * DH, sc + h_first, p.H_kv * DH, p.H_kv, 0, 0, ct, true);
+      const int row0 = ct / 8, blk = s_tile / kC8Block;
+      uint32_t ok = 0;
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        const int s = s_tile + row0 + it * 16;
+        ok |= (s < hi && __ldg(posr + s) >= 0 ? 1u : 0u) << it;
+      }
+      // a part: 128 slots x 128 channels, 128 bytes per thread
+      uint4 x[8];
+      float sc0 = 0.f, sc1 = 0.f;
+      auto fetch = [&](int q) {
+        const int h = h_first + q / C::PARTS;
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          x[it] = make_uint4(0, 0, 0, 0);
+          if ((ok >> it) & 1u)
+            x[it] = __ldg(reinterpret_cast<const uint4*>(
+                num + static_cast<size_t>(s_tile + row0 + it * 16) * p.H_kv * DH + h * DH +
+                (q % C::PARTS) * 128));
+        }
+        sc0 = __ldg(sc + static_cast<size_t>(blk) * p.H_kv + h);
+        sc1 = __ldg(sc + static_cast<size_t>(min(blk + 1, p.nb - 1)) * p.H_kv + h);
+      };
+      fetch(0);
       for (int q = 0; q < n_parts; ++q) {
         const int hh = q / C::PARTS, part = q % C::PARTS, kb = hh % C::KB;
         if (part == 0 && !wait_warp(k_empty[kb], ((hh / C::KB) & 1) ^ 1, kSiteKEmpty)) break;
-        store8<false>(f, sK + (kb * C::PARTS + part) * PART, ct);
+        uint8_t* dst = sK + (kb * C::PARTS + part) * PART + ((ct % 8) >> 2) * CHUNK;
+        const uint32_t h0 = pack_half2(sc0, sc0), h1 = pack_half2(sc1, sc1);
+        if (sc0 > 128.f || sc1 > 128.f) {
+#pragma unroll
+          for (int it = 0; it < 8; ++it)
+            store16_values<true>(x[it], (ok >> it) & 1u ? (it >= 4 ? h1 : h0) : 0u, ct % 8,
+                                 row0 + it * 16, dst + (row0 + it * 16) * 128);
+        } else {
+#pragma unroll
+          for (int it = 0; it < 8; ++it)
+            store16_values<false>(x[it], (ok >> it) & 1u ? (it >= 4 ? h1 : h0) : 0u, ct % 8,
+                                  row0 + it * 16, dst + (row0 + it * 16) * 128);
+        }
         if (part == C::PARTS - 1)
           publish8(k_full[kb], lane);
         else
           fence_proxy_async_smem();
-        const int nh = h_first + (q + 1) / C::PARTS;
-        fetch8<false>(f, src, num + nh * DH + ((q + 1) % C::PARTS) * 128, sc + nh, p.H_kv * DH, p.H_kv,
-                      0, 0, ct, q + 1 < n_parts);
+        if (q + 1 < n_parts) fetch(q + 1);
       }
     }
   } else if (warp >= 8) {
