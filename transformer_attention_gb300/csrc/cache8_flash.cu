@@ -413,60 +413,73 @@ __global__ void __launch_bounds__(THREADS, 1)
     regs_decrease<REGS_CONV>();
     const int ct = tid & 127;                  // thread of its warpgroup
     const int col = ct & 7, row0 = ct >> 3;    // 16-channel group, slots row0 + 16 k of a granule
-    // Granule n of the warpgroup's stream (d_h = 128: K, V of each tile in
-    // turn; d_h = 256: warps 4-7 K, 8-11 V): two make a part of 32 KB of fp16.
-    // Wide parts are 128 slots x 128 channels, half parts (V of d_h = 256) 64
-    // slots x 256 channels.
+    // Part q of the warpgroup's stream (d_h = 128: K, V of each tile in turn;
+    // d_h = 256: warps 4-7 the channel halves of K, 8-11 the slot halves of V):
+    // two granules to 32 KB of fp16.  Wide parts are 128 slots x 128 channels,
+    // half parts (V of d_h = 256) 64 slots x 256 channels.  All of a part's
+    // loads are in flight before the first conversion, and its granules are
+    // free for the next copies by then.
     const bool v256 = C::PARTS == 2 && warp >= 8;
     const int r0 = v256 ? 2 : 0;
 #pragma unroll 1
-    for (int n = 0; n < 4 * n_tiles; ++n) {
-      const int i = n >> 2, hh = (n >> 1) & 1, gg = n & 1;
+    for (int q = 0; q < 2 * n_tiles; ++q) {
+      const int i = q >> 1, hh = q & 1;
       const bool v = C::PARTS == 1 ? hh : v256;
       const int buf = C::PARTS == 1 ? (i & 1) : hh, use = C::PARTS == 1 ? (i >> 1) : i;
-      if ((n & 3) == 0 && !wait_warp(sh.meta_full[i % NMETA], (i / NMETA) & 1, kSiteMetaFull)) break;
-      const int r = r0 + n % C::RING;
-      if (!wait_warp(sh.raw_full[r], (n / C::RING) & 1, kSiteRawFull)) break;
+      if (hh == 0 && !wait_warp(sh.meta_full[i % NMETA], (i / NMETA) & 1, kSiteMetaFull)) break;
       const Meta& m = sh.meta[i % NMETA];
-      const int blk = v256 ? hh : gg;          // 64-slot block of the tile
-      const float s = (v ? m.vs : m.ks)[blk];
-      const uint32_t u0 = m.use[2 * blk], u1 = m.use[2 * blk + 1];
-      uint4 x[4];
-      uint32_t sc[4];
+      // scales and counted slots of granule 0 and 1
+      const float* msc = v ? m.vs : m.ks;
+      const float s0 = msc[v256 ? hh : 0], s1 = msc[v256 ? hh : 1];
+      const uint2 u0 = *reinterpret_cast<const uint2*>(m.use + (v256 ? 2 * hh : 0));
+      const uint2 u1 = *reinterpret_cast<const uint2*>(m.use + (v256 ? 2 * hh : 2));
+      uint4 x[8];
+      uint32_t sc[8];
+      bool ok = true;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int row = row0 + 16 * k;
-        x[k] = *reinterpret_cast<const uint4*>(sR + r * RAW + row * 128 + ((col ^ (row & 7)) << 4));
-        sc[k] = pack_half2(s, s);
-      }
-      if ((u0 & u1) != 0xffffffffu) {
+      for (int g = 0; g < 2; ++g) {
+        const int n = 2 * q + g, r = r0 + n % C::RING;
+        ok = ok && wait_warp(sh.raw_full[r], (n / C::RING) & 1, kSiteRawFull);
+        if (!ok) break;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if (!(((k < 2 ? u0 : u1) >> ((row0 + 16 * k) & 31)) & 1u)) {
+          const int row = row0 + 16 * k;
+          x[4 * g + k] =
+              *reinterpret_cast<const uint4*>(sR + r * RAW + row * 128 + ((col ^ (row & 7)) << 4));
+          sc[4 * g + k] = g ? pack_half2(s1, s1) : pack_half2(s0, s0);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[r]));
+      }
+      ok = ok && wait_warp(v ? sh.v_empty[buf] : sh.k_empty[buf], (use & 1) ^ 1, kSiteKEmpty);
+      if (!ok) break;
+      if ((u0.x & u0.y & u1.x & u1.y) != 0xffffffffu) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t u = k < 2 ? u0.x : (k < 4 ? u0.y : (k < 6 ? u1.x : u1.y));
+          if (!((u >> ((row0 + 16 * k) & 31)) & 1u)) {
             x[k] = make_uint4(0, 0, 0, 0);
             sc[k] = 0u;
           }
         }
       }
-      if (gg == 0 && !wait_warp(v ? sh.v_empty[buf] : sh.k_empty[buf], (use & 1) ^ 1, kSiteKEmpty)) break;
-      uint8_t* base = (v ? sV : sK) + buf * PART +
-                      (v256 ? (gg * 2 + (col >> 2)) * (CHUNK / 2) : (col >> 2) * CHUNK + gg * (CHUNK / 2));
-      if (s > 128.f) {
+      uint8_t* base = (v ? sV : sK) + buf * PART + (col >> 2) * (v256 ? CHUNK / 2 : CHUNK) + row0 * 128;
+      // granule 1: the other channel chunks of the same slots, or the next 64 slots
+      const uint32_t g1 = v256 ? CHUNK : CHUNK / 2;
+      if (s0 > 128.f || s1 > 128.f) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          store16_values<true>(x[k], sc[k], col, row0 + 16 * k, base + (row0 + 16 * k) * 128);
+        for (int k = 0; k < 8; ++k)
+          store16_values<true>(x[k], sc[k], col, row0, base + (k & 3) * 2048 + (k >> 2) * g1);
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          store16_values<false>(x[k], sc[k], col, row0 + 16 * k, base + (row0 + 16 * k) * 128);
+        for (int k = 0; k < 8; ++k)
+          store16_values<false>(x[k], sc[k], col, row0, base + (k & 3) * 2048 + (k >> 2) * g1);
       }
-      // (the raw bytes are read: their values are stored)
-      if (gg == 1) fence_proxy_async_smem();
+      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(smem_u32(&sh.raw_empty[r]));
-        if (gg == 1) mbar_arrive(smem_u32(v ? &sh.v_full[buf] : &sh.k_full[buf]));
-        if ((n & 3) == 3) mbar_arrive(smem_u32(&sh.meta_empty[i % NMETA]));
+        mbar_arrive(smem_u32(v ? &sh.v_full[buf] : &sh.k_full[buf]));
+        if (hh == 1) mbar_arrive(smem_u32(&sh.meta_empty[i % NMETA]));
       }
     }
   } else {
