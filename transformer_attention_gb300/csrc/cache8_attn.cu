@@ -503,6 +503,7 @@ struct FinishParams {
   const float* part;
   const float* logits;
   float* weight_sum;
+  float2* rowstat;            // many rows: [B, H_kv, T*G] of the merged rows, or null
   const int32_t* span_part;
   const int32_t* pad_lens;
   void* O;
@@ -539,6 +540,12 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
     L = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) L += red[1][i];
+    if (tid == 0 && p.rowstat != nullptr) {
+      const int h = row % p.H, G = p.H / p.H_kv;
+      const size_t t = row / p.H % p.T, b = row / p.H / p.T;
+      p.rowstat[((b * p.H_kv + h / G) * p.T + t) * G + h % G] =
+          row_stat(M, L, M != -INFINITY && L != 0.f);
+    }
     const float* base = p.part + row * p.nsplit * DH;
     for (int ch = tid; ch < DH; ch += 256) {
       float acc = 0.f;
@@ -705,8 +712,9 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
     a.qpos = qpos;
     a.pad_lens = pad_lens;
     a.first = lay.span_part;
-    a.stat = nsplit > 1 || weight_sum != nullptr ? lay.stat : nullptr;
+    a.stat = lay.stat;
     a.part = lay.part;
+    a.rowstat = weight_sum != nullptr ? lay.rowstat : nullptr;
     a.O = O;
     a.o_f16 = o_f16;
     a.B = B;
@@ -729,11 +737,15 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
       q.o_f16 = o_f16;
       q.n_rows = B * T * H;
       q.nsplit = nsplit;
+      q.rowstat = a.rowstat;
+      q.T = T;
+      q.H = H;
+      q.H_kv = H_kv;
       e = launch_pdl(d_h == 256 ? finish8_kernel<256> : finish8_kernel<128>,
                      dim3(static_cast<unsigned>(q.n_rows)), dim3(256), 0, stream, q);
       if (e != cudaSuccess) return e;
     }
-    return weight_sum != nullptr ? launch_weights8(a, lay.rowstat, lay.wpart, weight_sum, stream)
+    return weight_sum != nullptr ? launch_weights8(a, lay.wpart, weight_sum, stream)
                                  : cudaSuccess;
   }
 
@@ -788,7 +800,7 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
             : launch_cfg<128, 2>(tk, tv, p, grid, stream);
   if (e != cudaSuccess || (nsplit == 1 && weight_sum == nullptr)) return e;
 
-  FinishParams q;
+  FinishParams q = {};
   q.stat = lay.stat;
   q.part = lay.part;
   q.logits = lay.logits;

@@ -112,10 +112,18 @@ struct Params {
   const int32_t* first;       // [B, items] first visible slot of each item (local layers) or null
   float2* stat;
   float* part;
+  float2* rowstat;
   void* O;
   int o_f16, B, T, S, H, H_kv, nb, end, window, nsplit, items;
   int* status;
 };
+
+__device__ __forceinline__ void prefetch_4d(const void* tmap, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
 
 // exp2(s log2 e - m) of 32 columns: packed fp16 pairs to p[0..15], sums to acc.
 __device__ __forceinline__ void exp_pack(const uint32_t (&s)[32], uint32_t* p, float2 (&acc)[4],
@@ -224,22 +232,36 @@ __global__ void __launch_bounds__(THREADS, 1)
     regs_decrease<REGS_CTRL>();
     // Raw granule n of a stream (RING slots from slot r0 on): of K, granule
     // (channel half, slot half) of a tile, of V d_h = 256 (slot half, channel
-    // half); d_h = 128 has K's and V's two slot halves in one stream.
+    // half); d_h = 128 has K's and V's two slot halves in one stream.  For
+    // d_h = 256, whose rings are shorter, granules are pulled into L2 AHEAD
+    // turns before: its rings cover a copy from L2, not one from HBM.
+    constexpr int AHEAD = C::PARTS == 1 ? 0 : 12;
     auto load_raw = [&](int r0, bool v, int n_granules) {
-      int n = 0;
+      auto coord = [&](int n, bool& vv, int& c, int& s) {
+        const int hh = (n >> 1) & 1, gg = n & 1;   // part, granule of the part
+        vv = C::PARTS == 1 ? hh : v;
+        c = C::PARTS == 1 ? 0 : (v ? gg : hh) * 128;
+        s = s_base + (n >> 2) * BN + (C::PARTS == 1 ? gg : (v ? hh : gg)) * 64;
+      };
+      bool vv;
+      int c, s, n = 0;
+      for (int k = 0; k < min(AHEAD, n_granules); ++k) {
+        coord(k, vv, c, s);
+        prefetch_4d(vv ? &tmV : &tmK, c, j, s, b);
+      }
       for (; n < n_granules; ++n) {
         const int r = r0 + n % C::RING;
         if (!mbar_wait(smem_u32(&sh.raw_empty[r]), ((n / C::RING) & 1) ^ 1, &sh.abort_flag, p.status,
                        kSiteRawEmpty))
           break;
-        const int i = n >> 2, hh = (n >> 1) & 1, gg = n & 1;   // tile, part, granule of the part
+        coord(n, vv, c, s);
         const uint32_t bar = smem_u32(&sh.raw_full[r]);
         mbar_arrive_expect_tx(bar, RAW);
-        if constexpr (C::PARTS == 1)
-          tma_load_4d(smem_u32(sR + r * RAW), hh ? &tmV : &tmK, bar, 0, j, s_base + i * BN + gg * 64, b);
-        else
-          tma_load_4d(smem_u32(sR + r * RAW), v ? &tmV : &tmK, bar, (v ? gg : hh) * 128, j,
-                      s_base + i * BN + (v ? hh : gg) * 64, b);
+        tma_load_4d(smem_u32(sR + r * RAW), vv ? &tmV : &tmK, bar, c, j, s, b);
+        if (AHEAD > 0 && n + AHEAD < n_granules) {
+          coord(n + AHEAD, vv, c, s);
+          prefetch_4d(vv ? &tmV : &tmK, c, j, s, b);
+        }
       }
       for (int k = max(0, n - C::RING); k < n; ++k)
         mbar_wait_drain(smem_u32(&sh.raw_full[r0 + k % C::RING]), (k / C::RING) & 1);
@@ -622,8 +644,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       const size_t orow = (static_cast<size_t>(b) * p.T + t) * p.H + h;
       const bool have = row_valid && n_tiles > 0 && l != 0.f;
-      if (ok && t < p.T && p.stat != nullptr)
-        p.stat[orow * p.nsplit + split] = have ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
+      if (ok && t < p.T) {
+        if (p.nsplit > 1)
+          p.stat[orow * p.nsplit + split] =
+              have ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
+        else if (p.rowstat != nullptr)
+          p.rowstat[((static_cast<size_t>(b) * p.H_kv + j) * p.T + t) * G + r % G] =
+              row_stat(m_used, l, have);
+      }
       const float inv = have ? (p.nsplit == 1 ? 1.f / l : 1.f) : 0.f;
       if (ok) {
 #pragma unroll 1
@@ -756,6 +784,7 @@ cudaError_t launch_flash8(const Flash8Args& a, cudaStream_t stream) {
   p.first = a.window > 0 ? a.first : nullptr;
   p.stat = a.stat;
   p.part = a.part;
+  p.rowstat = a.rowstat;
   p.O = a.O;
   p.o_f16 = a.o_f16;
   p.B = a.B;

@@ -22,8 +22,9 @@ struct Flash8Args {
   const int32_t* qpos;
   const int32_t* pad_lens;
   int32_t* first;             // [B, items] scratch of local layers
-  float2* stat;               // [B*T*H, nsplit] (max, sum) of each part, or null
+  float2* stat;               // [B*T*H, nsplit] (max, sum) of each part when nsplit > 1
   float* part;                // [B*T*H, nsplit, d_h] when nsplit > 1
+  float2* rowstat;            // [B, H_kv, T*G] (max, 1 / sum) of every row, or null
   void* O;
   int o_f16, B, T, S, end, H, H_kv, d_h, window, nsplit;
   int* status;
@@ -33,11 +34,11 @@ int flash8_span(int d_h, int G);
 cudaError_t launch_flash8(const Flash8Args& a, cudaStream_t stream);
 
 // The probabilities that every slot received from the call's rows, added to
-// weight_sum [B, S] (cache8_weights.cu).  rowstat [B*T*H] and wpart
-// (weights8_part_floats() floats) are scratch.
+// weight_sum [B, S] (cache8_weights.cu), from a.rowstat.  wpart: scratch of
+// weights8_part_floats() floats.
 constexpr int kWeights8MaxCtas = 1024;
 constexpr size_t weights8_part_floats() { return static_cast<size_t>(kWeights8MaxCtas) * 128; }
-cudaError_t launch_weights8(const Flash8Args& a, float2* rowstat, float* wpart, float* weight_sum,
+cudaError_t launch_weights8(const Flash8Args& a, float* wpart, float* weight_sum,
                             cudaStream_t stream);
 
 #ifdef __CUDACC__
@@ -81,6 +82,12 @@ __device__ __forceinline__ void store16_values(const uint4& x, uint32_t scale2, 
   const int u0 = (col & 3) * 2, swap = (col >> 2) & 1, r7 = row & 7;
   *reinterpret_cast<uint4*>(base + (((u0 + swap) ^ r7) << 4)) = swap ? b : a;
   *reinterpret_cast<uint4*>(base + (((u0 + 1 - swap) ^ r7) << 4)) = swap ? a : b;
+}
+
+// A query row's entry of rowstat: (max, 1 / sum), or (inf, 0) for a row that
+// saw nothing, whose weights come out as zeros.
+__device__ __forceinline__ float2 row_stat(float m, float l, bool any) {
+  return any ? make_float2(m, 1.f / l) : make_float2(INFINITY, 0.f);
 }
 
 // A warp's stores visible to the tensor core, then its arrival.

@@ -281,6 +281,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int s = s_tile + r;
     const int ps = s < hi ? __ldg(p.posc + static_cast<size_t>(b) * p.S + s) : -1;
+    // query positions that see this slot on a local layer, and the range of
+    // the warp's slots' positions
+    int qlo = INT_MIN, qhi = INT_MAX;
+    if (p.window > 0) window_range(ps, ps, p.window, qlo, qhi);
+    const int wmin = __reduce_min_sync(0xffffffffu, ps >= 0 ? ps : INT_MAX);
+    const int wmax = __reduce_max_sync(0xffffffffu, ps);
     const size_t rows = static_cast<size_t>(p.T) * G;
     float2 nx = make_float2(INFINITY, 0.f);
     int nq = 0;
@@ -309,7 +315,21 @@ __global__ void __launch_bounds__(THREADS, 1)
       // columns [c0, c1) are valid tokens at or behind this slot
       const int c0 = max(0, min(C::TQ, s - p.end - t0)) * G;
       const int c1 = max(0, min(C::TQ, valid - t0)) * G;
-      const bool masked = __any_sync(0xffffffffu, c0 > 0) || c1 < BN || p.window > 0;
+      bool masked = __any_sync(0xffffffffu, c0 > 0) || c1 < BN;
+      if (p.window > 0 && !masked) {
+        // every slot of the warp within the window of every token of the tile?
+        int qn = INT_MAX, qx = INT_MIN;
+        for (int k = lane; k < C::TQ; k += 32) {
+          qn = min(qn, sq[wg][par][k]);
+          qx = max(qx, sq[wg][par][k]);
+        }
+        qn = __reduce_min_sync(0xffffffffu, qn);
+        qx = __reduce_max_sync(0xffffffffu, qx);
+        int plo, phi, a, z;
+        window_range(qx, qx, p.window, plo, a);
+        window_range(qn, qn, p.window, z, phi);
+        masked = wmax >= 0 && (wmin < plo || wmax > phi);
+      }
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       const float4* st4 = reinterpret_cast<const float4*>(rs[wg][par]);
 #pragma unroll 1
@@ -320,12 +340,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (masked) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            bool see = c + k >= c0 && c + k < c1;
-            if (p.window > 0) {
-              // (positions and the window are below 2^31: 64-bit differences)
-              const long long d = static_cast<long long>(sq[wg][par][(c + k) / G]) - ps;
-              see = see && d < p.window && -d < p.window;
-            }
+            const int qp = sq[wg][par][(c + k) / G];
+            const bool see = c + k >= c0 && c + k < c1 && qp >= qlo && qp <= qhi;
             if (!see) x[k] = 0xff800000u;   // -inf
           }
         }
@@ -366,26 +382,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// (max, 1 / sum) of every query row over the attention's parts, rows of a kv
-// head together.
-__global__ void __launch_bounds__(256) rowstat8_kernel(const float2* __restrict__ stat, int nsplit,
-                                                       long rows, int T, int H, int G,
-                                                       float2* __restrict__ rowstat) {
-  pdl_enter();
-  const long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;   // (b * T + t) * H + h
-  if (i >= rows) return;
-  const float2* st = stat + i * nsplit;
-  float M = -INFINITY, L = 0.f;
-  for (int k = 0; k < nsplit; ++k) M = fmaxf(M, st[k].x);
-  if (M != -INFINITY)
-    for (int k = 0; k < nsplit; ++k) L = fmaf(ex2(st[k].x - M), st[k].y, L);
-  const int h = static_cast<int>(i % H), t = static_cast<int>(i / H % T);
-  const long b = i / H / T;
-  const bool any = M != -INFINITY && L != 0.f;
-  rowstat[((b * (H / G) + h / G) * T + t) * G + h % G] =
-      any ? make_float2(M, 1.f / L) : make_float2(INFINITY, 0.f);
-}
-
 __global__ void __launch_bounds__(256) wadd8_kernel(const float* __restrict__ wpart, int usplit,
                                                     int B, int ld, int hi, int S,
                                                     float* __restrict__ weight_sum) {
@@ -417,21 +413,17 @@ cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_weights8(const Flash8Args& a, float2* rowstat, float* wpart, float* weight_sum,
+cudaError_t launch_weights8(const Flash8Args& a, float* wpart, float* weight_sum,
                             cudaStream_t stream) {
   const int G = a.H / a.H_kv;
-  const long rows = static_cast<long>(a.B) * a.T * a.H;
-  cudaError_t e = launch_pdl(rowstat8_kernel, dim3(static_cast<unsigned>((rows + 255) / 256)),
-                             dim3(256), 0, stream, static_cast<const float2*>(a.stat), a.nsplit, rows,
-                             a.T, a.H, G, rowstat);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaErrorInvalidValue;
   Params p;
   p.K8 = static_cast<const uint8_t*>(a.K8);
   p.K_scale = a.K_scale;
   p.posc = a.posc;
   p.qpos = a.qpos;
   p.pad_lens = a.pad_lens;
-  p.rowstat = rowstat;
+  p.rowstat = a.rowstat;
   p.weight_sum = weight_sum;
   p.wpart = wpart;
   p.B = a.B;
@@ -444,15 +436,14 @@ cudaError_t launch_weights8(const Flash8Args& a, float2* rowstat, float* wpart, 
   p.window = a.window;
   p.status = a.status;
   p.tiles = (a.end + a.T + BM - 1) / BM;
-  // CTAs on one slot tile: enough for two rounds of the SMs, while their parts
-  // fit the scratch.
+  // CTAs on one slot tile: as many as two rounds of the SMs take, while their
+  // parts fit the scratch.
   const long long n = static_cast<long long>(p.tiles) * a.B;
-  const long long want = (2LL * num_sms() + n - 1) / n;
+  const long long want = 2LL * num_sms() / n;
   p.usplit = static_cast<int>(std::max<long long>(
       1, std::min<long long>(want, std::min<long long>(kWeights8MaxCtas / n, 64))));
 #define G3_WEIGHTS8_CASE(DH_, G_) \
   if (a.d_h == DH_ && G == G_) e = launch_cfg<DH_, G_>(a.Q, p, stream);
-  e = cudaErrorInvalidValue;
   G3_WEIGHTS8_CASE(128, 1)
   G3_WEIGHTS8_CASE(128, 2)
   G3_WEIGHTS8_CASE(128, 4)
