@@ -184,11 +184,48 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _stream(stream) -> int:
+_raw_stream = None       # () -> the current stream's cudaStream_t
+_device = None           # () -> the current device's index
+
+
+def _bind_torch():
+    """The current stream and device by the calls that torch's own generated
+    code uses (0.2 us where building a Stream object takes 3.3, more than the
+    launch of a small kernel), or by the public ones where those are missing."""
+    global _raw_stream, _device
     import torch
+    torch.cuda.current_stream()              # initialises CUDA
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    dev = getattr(torch._C, "_cuda_getDevice", None)
+    _device = dev or torch.cuda.current_device
+    if raw is None:
+        _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    else:
+        _raw_stream = lambda: raw(_device())  # noqa: E731
+
+
+def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            _bind_torch()
+        return _raw_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _here(*tensors):
+    """Device pointers of the tensors (None and integers as they are), which
+    must all live on the current device: the kernels run there."""
+    if _device is None:
+        _bind_torch()
+    dev, out = _device(), []
+    for t in tensors:
+        if t is None or t.__class__ is int:
+            out.append(t)
+        elif t.get_device() != dev:
+            raise ValueError("tensor arguments must live on the current GPU")
+        else:
+            out.append(t.data_ptr())
+    return out
 
 
 def _dims(B, T, D, H, H_kv, d_h):
@@ -376,17 +413,17 @@ def gemma3_cached_attention(Q, K_cache, V_cache, pos_cache, segment_pos, pad_len
 
 def gemma3_kv_cache8_write(K_rows, V_rows, ld_rows, segment_pos, pad_lens, B, T, S, end_index,
                            H_kv, d_h, K8, V8, K_scale, V_scale, pos_cache, stream=None):
+    kr, vr, sp, pl, *cache = _here(K_rows, V_rows, segment_pos, pad_lens, K8, V8, K_scale, V_scale,
+                                   pos_cache)
     return _check("gemma3_kv_cache8_write", lib().gemma3_kv_cache8_write(
-        _ptr(K_rows), _ptr(V_rows), ld_rows, _ptr(segment_pos), _ptr(pad_lens), B, T, S,
-        end_index, H_kv, d_h, _ptr(K8), _ptr(V8), _ptr(K_scale), _ptr(V_scale), _ptr(pos_cache),
-        _stream(stream)))
+        kr, vr, ld_rows, sp, pl, B, T, S, end_index, H_kv, d_h, *cache, _stream(stream)))
 
 
 def gemma3_kv_cache8_read(K8, V8, K_scale, V_scale, B, S, first, n, H_kv, d_h, K_rows, V_rows,
                           ld_rows, stream=None):
+    k8, v8, ks, vs, kr, vr = _here(K8, V8, K_scale, V_scale, K_rows, V_rows)
     return _check("gemma3_kv_cache8_read", lib().gemma3_kv_cache8_read(
-        _ptr(K8), _ptr(V8), _ptr(K_scale), _ptr(V_scale), B, S, first, n, H_kv, d_h,
-        _ptr(K_rows), _ptr(V_rows), ld_rows, _stream(stream)))
+        k8, v8, ks, vs, B, S, first, n, H_kv, d_h, kr, vr, ld_rows, _stream(stream)))
 
 
 def gemma3_cached8_attention_workspace_size(B, T, S, H, H_kv, d_h, with_weights=False) -> int:
@@ -400,19 +437,20 @@ def gemma3_cached8_attention_workspace_size(B, T, S, H, H_kv, d_h, with_weights=
 def gemma3_cached8_attention(Q, K8, V8, K_scale, V_scale, pos_cache, segment_pos, pad_lens, O,
                              o_dtype, weight_sum, B, T, S, end_index, H, H_kv, d_h, window,
                              workspace, workspace_bytes, stream=None):
+    *ins, w, ws = _here(Q, K8, V8, K_scale, V_scale, pos_cache, segment_pos, pad_lens, O,
+                        weight_sum, workspace)
     return _check("gemma3_cached8_attention", lib().gemma3_cached8_attention(
-        _ptr(Q), _ptr(K8), _ptr(V8), _ptr(K_scale), _ptr(V_scale), _ptr(pos_cache),
-        _ptr(segment_pos), _ptr(pad_lens), _ptr(O), o_dtype, _ptr(weight_sum), B, T, S,
-        end_index, H, H_kv, d_h, window, _ptr(workspace), workspace_bytes, _stream(stream)))
+        *ins, o_dtype, w, B, T, S, end_index, H, H_kv, d_h, window, ws, workspace_bytes,
+        _stream(stream)))
 
 
 def gemma3_kv_cache8_evict(K8, V8, K_scale, V_scale, pos_cache, weight_sum, B, S, end_index, H_kv,
                            d_h, keep, recent, K8_dst, V8_dst, K_scale_dst, V_scale_dst, pos_dst,
                            weight_dst, kept, S_dst, stream=None):
+    src = _here(K8, V8, K_scale, V_scale, pos_cache, weight_sum)
+    dst = _here(K8_dst, V8_dst, K_scale_dst, V_scale_dst, pos_dst, weight_dst, kept)
     return _check("gemma3_kv_cache8_evict", lib().gemma3_kv_cache8_evict(
-        _ptr(K8), _ptr(V8), _ptr(K_scale), _ptr(V_scale), _ptr(pos_cache), _ptr(weight_sum), B, S,
-        end_index, H_kv, d_h, keep, recent, _ptr(K8_dst), _ptr(V8_dst), _ptr(K_scale_dst),
-        _ptr(V_scale_dst), _ptr(pos_dst), _ptr(weight_dst), _ptr(kept), S_dst, _stream(stream)))
+        *src, B, S, end_index, H_kv, d_h, keep, recent, *dst, S_dst, _stream(stream)))
 
 
 def gemma3_attn_cached8_workspace_size(dims, S, with_weights=False) -> int:
@@ -429,12 +467,11 @@ def gemma3_attn_forward_cached8(dims, S, end_index, x, segment_pos, pad_lens, Wq
                                 query_scale, K8, V8, K_scale, V_scale, pos_cache, weight_sum, out,
                                 workspace, workspace_bytes, stream=None):
     d = _dims(*dims)
+    ins = _here(x, segment_pos, pad_lens, Wq, Wkv, Wo, gamma_q, gamma_k)
+    outs = _here(K8, V8, K_scale, V_scale, pos_cache, weight_sum, out, workspace)
     return _check("gemma3_attn_forward_cached8", lib().gemma3_attn_forward_cached8(
-        ctypes.byref(d), S, end_index, _ptr(x), _ptr(segment_pos), _ptr(pad_lens), _ptr(Wq),
-        _ptr(Wkv), _ptr(Wo), _ptr(gamma_q), _ptr(gamma_k), attn_type, window, rope_base,
-        rope_scale, query_scale, _ptr(K8), _ptr(V8), _ptr(K_scale), _ptr(V_scale),
-        _ptr(pos_cache), _ptr(weight_sum), _ptr(out), _ptr(workspace), workspace_bytes,
-        _stream(stream)))
+        ctypes.byref(d), S, end_index, *ins, attn_type, window, rope_base, rope_scale,
+        query_scale, *outs, workspace_bytes, _stream(stream)))
 
 
 def gemma3_geglu(A, lda, W_gating, ldw, Z, ldz, M, D_ff, K, in_dtype, stream=None):

@@ -568,14 +568,19 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
   float acc = 0.f;
   for (int r0 = 0; r0 < rows; r0 += 256) {
     __syncthreads();
-    if (r0 + tid < rows) {
-      // (max, 1 / sum) of query row (t, h) over its parts
-      const float2* st = p.stat + (static_cast<size_t>(b) * rows + r0 + tid) * p.nsplit;
+    // (max, 1 / sum) of the query rows over their parts, a warp each
+    for (int i = warp; i < min(256, rows - r0); i += 8) {
+      const float2* st = p.stat + (static_cast<size_t>(b) * rows + r0 + i) * p.nsplit;
       float M = -INFINITY, L = 0.f;
-      for (int i = 0; i < p.nsplit; ++i) M = fmaxf(M, st[i].x);
+      for (int k = lane; k < p.nsplit; k += 32) M = fmaxf(M, st[k].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       if (M != -INFINITY)
-        for (int i = 0; i < p.nsplit; ++i) L += ex2(st[i].x - M) * st[i].y;
-      rs[tid] = make_float2(M == -INFINITY ? 0.f : M, L != 0.f ? 1.f / L : 0.f);
+        for (int k = lane; k < p.nsplit; k += 32) L = fmaf(ex2(st[k].x - M), st[k].y, L);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      if (lane == 0)
+        rs[i] = make_float2(M == -INFINITY ? 0.f : M, M != -INFINITY && L != 0.f ? 1.f / L : 0.f);
     }
     __syncthreads();
     // (the first launch wrote logits from the first visible tile up to a valid
@@ -617,6 +622,45 @@ Plan plan_rows(int B, int T, int S, int H, int H_kv, int d_h) {
   const int tiles = (S + d.tile - 1) / d.tile;
   d.max_splits = static_cast<int>(std::min<long long>({kMaxSplits, by_cap, tiles}));
   return d;
+}
+
+// Splits of few rows, bound by HBM: counted in the time a tile takes at the
+// full rate of HBM (2.6 ns for d_h = 128, 5.1 for 256), the tiles all
+// together, or those of one CTA at the pace of one among 256 (the CTAs that
+// saturate HBM), whichever is longer, and about 2 us per round of two CTAs
+// per SM to start and merge.  (12B-shaped batch of 16 over 7777 slots: 896
+// CTAs in three rounds 88 us, 256 CTAs in one 84 us.)
+int splits_few(const Plan& d, int tiles, int d_h) {
+  const int slots = 2 * num_sms(), start = d_h == 256 ? 400 : 800;
+  int nsplit = 1;
+  long long best = LLONG_MAX;
+  for (int n = 1; n <= std::min(d.max_splits, tiles); ++n) {
+    const long long waves = (d.units * n + slots - 1) / slots, per = (tiles + n - 1) / n;
+    const long long cost = std::max(d.units * tiles, waves * per * 256) + waves * start;
+    if (cost < best) {
+      best = cost;
+      nsplit = n;
+    }
+  }
+  return nsplit;
+}
+
+// Splits of many rows, bound by the tensor cores: a CTA's tiles (about a
+// microsecond each, 6.5 MB of HBM time), a start and an end worth three, and
+// the parts' bytes (4 per element out and back).
+int splits_many(const Plan& d, int tiles, long long elements) {
+  const double part_tiles = static_cast<double>(elements) * 8.0 / 6.5e6;
+  int nsplit = 1;
+  double best = 1e300;
+  for (int n = 1; n <= std::min(d.max_splits, tiles); ++n) {
+    const double waves = static_cast<double>((d.units * n + num_sms() - 1) / num_sms());
+    const double cost = waves * ((tiles + n - 1) / n + 3) + (n > 1 ? n * part_tiles : 0.0);
+    if (cost < best) {
+      best = cost;
+      nsplit = n;
+    }
+  }
+  return nsplit;
 }
 
 struct Layout {
@@ -678,27 +722,11 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   const Layout lay = layout(ws, B, T, S, H, H_kv, d_h, weight_sum != nullptr);
   const int hi = end + T, nb = c8_blocks(S), o_f16 = o_dtype == kF16 ? 1 : 0;
 
-  // Splits: the count that ends first when a CTA's time is its tiles, a start
-  // and an end worth some more, and (many rows) the parts' bytes.
   const int span = d.few ? T : flash8_span(d_h, H / H_kv);
   const long long est = window > 0 ? std::min<long long>(hi, static_cast<long long>(window) + span)
                                    : static_cast<long long>(hi);
   const int tiles = static_cast<int>((est + d.tile - 1) / d.tile) + (window > 0 ? 1 : 0);
-  const int slots = (d.few ? 2 : 1) * num_sms();
-  // (a part's 4 * d_h bytes per row go out and come back; a tile of the
-  // tcgen05 kernel takes about a microsecond, 6.5 MB of HBM time)
-  const double part_tiles =
-      d.few ? 0.0 : static_cast<double>(B) * T * H * d_h * 8.0 / 6.5e6;
-  int nsplit = 1;
-  double best = 1e300;
-  for (int n = 1; n <= std::min(d.max_splits, tiles); ++n) {
-    const double waves = static_cast<double>((d.units * n + slots - 1) / slots);
-    const double cost = waves * ((tiles + n - 1) / n + 3) + (n > 1 ? n * part_tiles : 0.0);
-    if (cost < best) {
-      best = cost;
-      nsplit = n;
-    }
-  }
+  const int nsplit = d.few ? splits_few(d, tiles, d_h) : splits_many(d, tiles, B * 1LL * T * H * d_h);
   cudaError_t e;
 
   if (!d.few) {
