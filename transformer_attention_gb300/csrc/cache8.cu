@@ -135,39 +135,58 @@ __global__ void __launch_bounds__(kRowThreads) cache8_write_kernel(const WritePa
 }
 
 // ---------------------------------------------------------------- read
-// Slots [first, first + n) of every row as fp16 rows: 16 numbers per thread.
+// Slots [first, first + n) of K (blockIdx.y even) or V of one batch row as
+// fp16 rows: 16 numbers per unit, four units per thread in flight.
+constexpr int kReadUnits = 4;
+
 __global__ void __launch_bounds__(256) cache8_read_kernel(
     const uint8_t* __restrict__ K8, const uint8_t* __restrict__ V8,
-    const float* __restrict__ K_scale, const float* __restrict__ V_scale, long total, int S,
-    int nb, int first, int n, int H_kv, int d_h, __half* K_rows, __half* V_rows, long ld) {
+    const float* __restrict__ K_scale, const float* __restrict__ V_scale, int S, int nb, int first,
+    int n, int H_kv, int d_h, unsigned chunks, __half* K_rows, __half* V_rows, long ld) {
   pdl_enter();
-  const int units = H_kv * d_h / 16;           // 16-byte units of one slot
-  for (long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<long>(gridDim.x) * blockDim.x) {
-    const int u = static_cast<int>(i % units);
-    long q = i / units;
-    const bool isv = q & 1;
-    q >>= 1;                                   // output row b * n + t
-    const int t = static_cast<int>(q % n);
-    const long b = q / n;
-    const int slot = first + t, c = u * 16, j = c / d_h;
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(
-        (isv ? V8 : K8) + (static_cast<size_t>(b) * S + slot) * H_kv * d_h + c));
-    const float s = __ldg((isv ? V_scale : K_scale) +
-                          (static_cast<size_t>(b) * nb + slot / kC8Block) * H_kv + j);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const unsigned row_units = H_kv * d_h / 16, head_units = d_h / 16;
+  const unsigned chunk = blockIdx.x % chunks, bk = blockIdx.x / chunks;   // (batch row, K or V)
+  const bool isv = bk & 1;
+  const size_t b = bk >> 1;
+  const uint8_t* num = (isv ? V8 : K8) + (b * S + first) * static_cast<size_t>(H_kv) * d_h;
+  const float* scale = (isv ? V_scale : K_scale) + b * nb * H_kv;
+  __half* rows = (isv ? V_rows : K_rows) + b * n * ld;
+  // (slots x units per slot passes 2^32 only beyond any one row's 2^40 bytes / 16;
+  // 64-bit unit numbers, 32-bit within a chunk)
+  const size_t total = static_cast<size_t>(n) * row_units;
+  const size_t base = static_cast<size_t>(chunk) * (256 * kReadUnits);
+  const unsigned t0 = static_cast<unsigned>(base / row_units);
+  const unsigned u0 = static_cast<unsigned>(base - static_cast<size_t>(t0) * row_units);
+  uint4 v[kReadUnits];
+  float s[kReadUnits];
+  unsigned t[kReadUnits], u[kReadUnits];
+#pragma unroll
+  for (int k = 0; k < kReadUnits; ++k) {
+    const unsigned i = k * 256 + threadIdx.x;
+    const unsigned q = (u0 + i) / row_units;
+    t[k] = t0 + q;
+    u[k] = u0 + i - q * row_units;
+    if (base + i < total) {
+      v[k] = __ldg(reinterpret_cast<const uint4*>(num + (static_cast<size_t>(t[k]) * row_units + u[k]) * 16));
+      s[k] = __ldg(scale + static_cast<size_t>((first + t[k]) / kC8Block) * H_kv + u[k] / head_units);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kReadUnits; ++k) {
+    if (base + k * 256 + threadIdx.x >= total) break;
+    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
     uint32_t o[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float2 f = c8_float2(w[k >> 1] >> ((k & 1) * 16));
-      f.x *= s;
-      f.y *= s;
+    for (int e = 0; e < 8; ++e) {
+      float2 f = c8_float2(w[e >> 1] >> ((e & 1) * 16));
+      f.x *= s[k];
+      f.y *= s[k];
       // beyond fp16's largest (only 65504 itself rounds there): 65504; NaN passes
       f.x = f.x > 65504.f ? 65504.f : (f.x < -65504.f ? -65504.f : f.x);
       f.y = f.y > 65504.f ? 65504.f : (f.y < -65504.f ? -65504.f : f.y);
-      o[k] = pack_half2(f.x, f.y);
+      o[e] = pack_half2(f.x, f.y);
     }
-    uint4* d = reinterpret_cast<uint4*>((isv ? V_rows : K_rows) + q * ld + c);
+    uint4* d = reinterpret_cast<uint4*>(rows + static_cast<size_t>(t[k]) * ld + u[k] * 16);
     d[0] = make_uint4(o[0], o[1], o[2], o[3]);
     d[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
@@ -197,33 +216,46 @@ struct SelectParams {
 constexpr int kSelThreads = 1024;
 constexpr int kSelSlots = 8192;      // slots per CTA worth one more CTA in the cluster
 constexpr int kSelMaxCluster = 8;
+constexpr int kSelKeys = 48 * 1024;  // keys that a CTA keeps in shared memory
 
 // One cluster per batch row: the keep-th largest key by four rounds of 8-bit
 // digit counts (each CTA counts its run of slots, the counts are summed over
 // the cluster through distributed shared memory), then the slots above it,
-// and the first of those equal to it, are written out in slot order.  The
-// keys are read from L2 once per round: 8 bytes per slot.
+// and the first of those equal to it, are written out in slot order.  Weights
+// and positions are read once; the keys stay in shared memory between the
+// rounds (a run longer than kSelKeys is read from L2 again).  Bound by the
+// rounds' latency: 131072 slots 20 us on eight CTAs; their 1 MB takes 0.2 us.
 __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const SelectParams p) {
   pdl_enter();
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), C = cluster.num_blocks();
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ uint32_t keys[];
   __shared__ int hist[2][256];
   __shared__ int sum[256];
-  __shared__ int wsum[32];
+  __shared__ int wsum[2][32];
   __shared__ int counts[2];
-  __shared__ int found[2];           // digit, keys above it
+  __shared__ int found[2][2];        // by round parity: digit, keys above it
   const float* w = p.w + static_cast<size_t>(b) * p.S;
   const int32_t* pos = p.pos + static_cast<size_t>(b) * p.S;
   int run = (p.end + C - 1) / C;
   run = (run + kSelThreads - 1) / kSelThreads * kSelThreads;
-  const int lo = min(static_cast<long long>(p.end), static_cast<long long>(rank) * run);
+  const int lo = static_cast<int>(min(static_cast<long long>(p.end), static_cast<long long>(rank) * run));
   const int hi = static_cast<int>(min(static_cast<long long>(p.end), static_cast<long long>(lo) + run));
+  const bool kept_here = run <= kSelKeys;
+  auto fresh_key = [&](int s) { return evict_key(__ldg(w + s), __ldg(pos + s), s, p.first_recent); };
+  if (kept_here) {
+#pragma unroll 4
+    for (int s = lo + tid; s < hi; s += kSelThreads) keys[s - lo] = fresh_key(s);
+  }
+  auto key_at = [&](int s) { return kept_here ? keys[s - lo] : fresh_key(s); };
 
   uint32_t prefix = 0;
   int want = p.keep;                 // rank still to find among keys that match the prefix
   bool all = false;                  // fewer tokens than places: keep every one
+  int own_gt = 0;                    // (thread 0) keys of this CTA above the prefix
+  int own_eq = 0;
   for (int round = 0; round < 4; ++round) {
     const int shift = 24 - 8 * round;
     int* h = hist[round & 1];
@@ -231,82 +263,90 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
     __syncthreads();
     for (int base = lo; base < hi; base += kSelThreads) {
       const int s = base + tid;
-      uint32_t key = 0;
-      if (s < hi) key = evict_key(__ldg(w + s), __ldg(pos + s), s, p.first_recent);
+      const uint32_t key = s < hi ? key_at(s) : 0u;
       const bool in = key != 0 && (round == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8)));
-      const int digit = in ? static_cast<int>((key >> shift) & 255u) : 256;
-      // keys share digits (weights of one magnitude): one add per digit and warp
-      const unsigned same = __match_any_sync(0xffffffffu, digit);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&h[digit], __popc(same));
+      const int digit = static_cast<int>((key >> shift) & 255u);
+      // A warp whose keys all share a digit (equal weights) adds once.
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      if (m == 0) continue;
+      const int d0 = __shfl_sync(0xffffffffu, digit, __ffs(m) - 1);
+      if (__all_sync(0xffffffffu, !in || digit == d0)) {
+        if (lane == 0) atomicAdd(&h[d0], __popc(m));
+      } else if (in) {
+        atomicAdd(&h[digit], 1);
+      }
     }
     cluster.sync();
     if (tid < 256) {
       int n = 0;
-      for (int r = 0; r < C; ++r) n += cluster.map_shared_rank(h, r)[tid];
+#pragma unroll
+      for (int r = 0; r < kSelMaxCluster; ++r)
+        if (r < C) n += cluster.map_shared_rank(h, r)[tid];
       sum[tid] = n;
     }
     __syncthreads();
+    int* f = found[round & 1];
     if (warp == 0) {
       // lane l holds digits 255 - 8l .. 248 - 8l, largest first
       int mine = 0;
+#pragma unroll
       for (int i = 0; i < 8; ++i) mine += sum[255 - 8 * lane - i];
       int before = mine;
+#pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, before, o);
         if (lane >= o) before += v;
       }
       const int total = __shfl_sync(0xffffffffu, before, 31);
       before -= mine;
-      if (lane == 0) found[0] = -1;
+      if (lane == 0) f[0] = -1;
       __syncwarp();
       if (total >= want && before < want && before + mine >= want) {
         int above = before;
         for (int i = 0; i < 8; ++i) {
           const int d = 255 - 8 * lane - i;
           if (above + sum[d] >= want) {
-            found[0] = d;
-            found[1] = above;
+            f[0] = d;
+            f[1] = above;
             break;
           }
           above += sum[d];
         }
       }
+      // this CTA's own keys above the digit (or all its tokens), and on it
+      __syncwarp();
+      const int d = f[0];
+      int gt = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = 255 - 8 * lane - i;
+        if (k > d) gt += h[k];
+      }
+      gt = __reduce_add_sync(0xffffffffu, gt);
+      own_gt += gt;
+      own_eq = d >= 0 ? h[d] : 0;
     }
     __syncthreads();
-    if (found[0] < 0) {              // (only in round 0)
+    if (f[0] < 0) {                  // (only in round 0)
       all = true;
       break;
     }
-    prefix |= static_cast<uint32_t>(found[0]) << shift;
-    want -= found[1];
+    prefix |= static_cast<uint32_t>(f[0]) << shift;
+    want -= f[1];
   }
   // A slot stays if its key is above `prefix`, or equals it and is among the
   // first `want` that do.
   const uint32_t thr = all ? 0u : prefix;
   if (all) want = 0;
-  int gt = 0, eq = 0;
-  for (int base = lo; base < hi; base += kSelThreads) {
-    const int s = base + tid;
-    if (s < hi) {
-      const uint32_t key = evict_key(__ldg(w + s), __ldg(pos + s), s, p.first_recent);
-      gt += key > thr;
-      eq += key == thr;
-    }
-  }
-  if (tid < 2) counts[tid] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    gt += __shfl_xor_sync(0xffffffffu, gt, o);
-    eq += __shfl_xor_sync(0xffffffffu, eq, o);
-  }
-  if (lane == 0) {
-    atomicAdd(&counts[0], gt);
-    atomicAdd(&counts[1], eq);
+  if (tid == 0) {
+    counts[0] = own_gt;
+    counts[1] = own_eq;
   }
   cluster.sync();
   int gt0 = 0, eq0 = 0, n_kept = 0, n_eq = 0;
-  for (int r = 0; r < C; ++r) {
+#pragma unroll
+  for (int r = 0; r < kSelMaxCluster; ++r) {
+    if (r >= C) break;
     const int* q = cluster.map_shared_rank(counts, r);
     const int a = q[0], e = q[1];
     if (r < rank) {
@@ -322,22 +362,15 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
   int32_t* kept = p.kept + static_cast<size_t>(b) * p.keep;
   int32_t* pos_dst = p.pos_dst + static_cast<size_t>(b) * p.S_dst;
   float* w_dst = p.w_dst + static_cast<size_t>(b) * p.S_dst;
-  for (int base = lo; base < hi; base += kSelThreads) {
+  for (int base = lo, step = 0; base < hi; base += kSelThreads, ++step) {
     const int s = base + tid;
-    float ws = 0.f;
-    int ps = -1;
-    uint32_t key = 0;
-    if (s < hi) {
-      ws = __ldg(w + s);
-      ps = __ldg(pos + s);
-      key = evict_key(ws, ps, s, p.first_recent);
-    }
-    const bool g = s < hi && key > thr, e = s < hi && key == thr;
+    const uint32_t key = s < hi ? key_at(s) : 0u;
+    const bool g = s < hi && key > thr, e = s < hi && key == thr && want > 0;
     const unsigned bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
     // counts of (above, equal) in 16 bits each: at most 1024 per step
-    if (lane == 0) wsum[warp] = __popc(bg) | (__popc(be) << 16);
+    if (lane == 0) wsum[step & 1][warp] = __popc(bg) | (__popc(be) << 16);
     __syncthreads();
-    int v = wsum[lane];
+    int v = wsum[step & 1][lane];
     const int own = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -352,12 +385,11 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
     if (g || (e && ne < want)) {
       const int d = ng + min(ne, want);
       kept[d] = s;
-      pos_dst[d] = ps;
-      w_dst[d] = ws;
+      pos_dst[d] = __ldg(pos + s);
+      w_dst[d] = __ldg(w + s);
     }
     gt0 += total & 0xFFFF;
     eq0 += total >> 16;
-    __syncthreads();
   }
   for (int d = n_kept + rank * kSelThreads + tid; d < p.keep; d += C * kSelThreads) {
     kept[d] = -1;
@@ -379,78 +411,99 @@ struct MoveParams {
   float* V_scale_dst;
 };
 
-// One CTA per (block of 64 kept slots, kv head, K' or V, batch row), heads
-// fastest so that the CTAs at work at one time read whole slots.  The numbers
-// of the block stay in registers between the search for the largest value and
-// the move to the block's own scale.
-template <int DH>
+// One CTA per block of 64 kept slots, batch row and U neighbouring (kv head, K
+// or V) tiles, heads fastest so that the CTAs at work at one time read whole
+// slots.  The numbers stay in registers between the search for the largest
+// value and the move to the block's own scale; a chain of three memory round
+// trips (which slots, their numbers, the stores) is paid once for U tiles.
+// (One tile per CTA: 115 us for 268 MB each way, four: 90 us.)
+template <int DH, int U>
 __global__ void __launch_bounds__(kRowThreads) cache8_move_kernel(const MoveParams p) {
   pdl_enter();
   constexpr int TPR = DH / 16;                 // threads per row, 16 channels each
   constexpr int RPP = kRowThreads / TPR;
   constexpr int NP = kTile / RPP;
-  __shared__ float red[kRowThreads / 32];
-  const int tid = threadIdx.x;
+  __shared__ float red[U][kRowThreads / 32];
+  const int tid = threadIdx.x, n_hk = 2 * p.H_kv, groups = (n_hk + U - 1) / U;
   unsigned idx = blockIdx.x;
-  const int hk = idx % (2 * p.H_kv);
-  idx /= 2 * p.H_kv;
+  const int hk0 = idx % groups * U;
+  idx /= groups;
   const int blk = idx % p.nblk, b = idx / p.nblk;
-  const int j = hk >> 1;
-  const bool isv = hk & 1;
   const int c = (tid % TPR) * 16;
   const size_t ldc = static_cast<size_t>(p.H_kv) * DH;
-  const uint8_t* src = (isv ? p.V8 : p.K8) + static_cast<size_t>(b) * p.S * ldc +
-                       static_cast<size_t>(j) * DH + c;
-  const float* src_scale =
-      (isv ? p.V_scale : p.K_scale) + static_cast<size_t>(b) * p.nb * p.H_kv + j;
+  const size_t src0 = static_cast<size_t>(b) * p.S * ldc, sc0 = static_cast<size_t>(b) * p.nb * p.H_kv;
 
-  uint4 n[NP];
-  float sc[NP], mx = 0.f;
+  int from[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int d = blk * kTile + i * RPP + tid / TPR;
-    const int s = d < p.keep ? __ldg(p.kept + static_cast<size_t>(b) * p.keep + d) : -1;
-    n[i] = make_uint4(0, 0, 0, 0);
-    sc[i] = 0.f;
-    if (s >= 0) {
-      n[i] = __ldg(reinterpret_cast<const uint4*>(src + static_cast<size_t>(s) * ldc));
-      sc[i] = __ldg(src_scale + static_cast<size_t>(s / kC8Block) * p.H_kv);
+    from[i] = d < p.keep ? __ldg(p.kept + static_cast<size_t>(b) * p.keep + d) : -1;
+  }
+  uint4 n[U][NP];
+  float sc[U][NP];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int hk = hk0 + u, j = hk >> 1;
+    const bool isv = hk & 1;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      n[u][i] = make_uint4(0, 0, 0, 0);
+      sc[u][i] = 0.f;
+      if (hk < n_hk && from[i] >= 0) {
+        n[u][i] = __ldg(reinterpret_cast<const uint4*>(
+            (isv ? p.V8 : p.K8) + src0 + static_cast<size_t>(from[i]) * ldc + j * DH + c));
+        sc[u][i] = __ldg((isv ? p.V_scale : p.K_scale) + sc0 +
+                         static_cast<size_t>(from[i] / kC8Block) * p.H_kv + j);
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    // e4m3 magnitudes order like their codes; 0x7f is NaN
-    const uint32_t w[4] = {n[i].x, n[i].y, n[i].z, n[i].w};
-    uint32_t m = 0;
+  for (int u = 0; u < U; ++u) {
+    float mx = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t a = w[k] & 0x7F7F7F7Fu;
-      a &= ~__vcmpeq4(a, 0x7F7F7F7Fu);
-      m = __vmaxu4(m, a);
+    for (int i = 0; i < NP; ++i) {
+      // e4m3 magnitudes order like their codes; 0x7f is NaN
+      const uint32_t w[4] = {n[u][i].x, n[u][i].y, n[u][i].z, n[u][i].w};
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t a = w[k] & 0x7F7F7F7Fu;
+        a &= ~__vcmpeq4(a, 0x7F7F7F7Fu);
+        m = __vmaxu4(m, a);
+      }
+      m = __vmaxu4(m, m >> 16);
+      m = max(m & 0xFFu, (m >> 8) & 0xFFu);
+      mx = fmaxf(mx, c8_float2(m).x * sc[u][i]);
     }
-    m = __vmaxu4(m, m >> 16);
-    m = max(m & 0xFFu, (m >> 8) & 0xFFu);
-    mx = fmaxf(mx, c8_float2(m).x * sc[i]);
-  }
-  mx = block_max(mx, red);
-  const float s = c8_scale_for(mx);
-  const float inv = 1.f / s;
-  uint8_t* dst = (isv ? p.V8_dst : p.K8_dst) + static_cast<size_t>(b) * p.S_dst * ldc +
-                 static_cast<size_t>(j) * DH + c;
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int d = blk * kTile + i * RPP + tid / TPR;
-    if (d < p.keep) {
-      const float ratio = sc[i] * inv;
-      uint4 v = n[i];
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if ((tid & 31) == 0) red[u][tid >> 5] = mx;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int hk = hk0 + u, j = hk >> 1;
+    if (hk >= n_hk) break;
+    const bool isv = hk & 1;
+    float mx = red[u][0];
+#pragma unroll
+    for (int i = 1; i < kRowThreads / 32; ++i) mx = fmaxf(mx, red[u][i]);
+    const float s = c8_scale_for(mx), inv = 1.f / s;
+    uint8_t* dst = (isv ? p.V8_dst : p.K8_dst) + static_cast<size_t>(b) * p.S_dst * ldc + j * DH + c;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int d = blk * kTile + i * RPP + tid / TPR;
+      if (d >= p.keep) continue;
+      const float ratio = sc[u][i] * inv;
+      uint4 v = n[u][i];
       if (ratio != 1.f)
         v = make_uint4(c8_rescale4(v.x, ratio), c8_rescale4(v.y, ratio), c8_rescale4(v.z, ratio),
                        c8_rescale4(v.w, ratio));
       *reinterpret_cast<uint4*>(dst + static_cast<size_t>(d) * ldc) = v;
     }
+    if (tid == 0)
+      (isv ? p.V_scale_dst : p.K_scale_dst)[(static_cast<size_t>(b) * p.nb_dst + blk) * p.H_kv + j] = s;
   }
-  if (tid == 0)
-    (isv ? p.V_scale_dst : p.K_scale_dst)[(static_cast<size_t>(b) * p.nb_dst + blk) * p.H_kv + j] = s;
 }
 
 }  // namespace
@@ -486,12 +539,13 @@ cudaError_t launch_cache8_write(const void* K_rows, const void* V_rows, long ld,
 cudaError_t launch_cache8_read(const void* K8, const void* V8, const float* K_scale,
                                const float* V_scale, int B, int S, int first, int n, int H_kv,
                                int d_h, void* K_rows, void* V_rows, long ld, cudaStream_t stream) {
-  const long total = static_cast<long>(B) * n * 2 * (H_kv * d_h / 16);
-  if (total <= 0) return cudaSuccess;
-  const long ctas = std::min<long>((total + 255) / 256, 64L * num_sms());
-  return launch_pdl(cache8_read_kernel, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, stream,
-                    static_cast<const uint8_t*>(K8), static_cast<const uint8_t*>(V8), K_scale,
-                    V_scale, total, S, c8_blocks(S), first, n, H_kv, d_h,
+  if (n <= 0) return cudaSuccess;
+  const size_t units = static_cast<size_t>(n) * (H_kv * d_h / 16);
+  const size_t chunks = (units + 256 * kReadUnits - 1) / (256 * kReadUnits);
+  if (chunks * B * 2 > INT_MAX) return cudaErrorInvalidValue;
+  return launch_pdl(cache8_read_kernel, dim3(static_cast<unsigned>(chunks * B * 2)), dim3(256), 0,
+                    stream, static_cast<const uint8_t*>(K8), static_cast<const uint8_t*>(V8), K_scale,
+                    V_scale, S, c8_blocks(S), first, n, H_kv, d_h, static_cast<unsigned>(chunks),
                     static_cast<__half*>(K_rows), static_cast<__half*>(V_rows), ld);
 }
 
@@ -515,8 +569,11 @@ cudaError_t launch_cache8_evict(const void* K8, const void* V8, const float* K_s
   q.w_dst = weight_dst;
   int cl = 1;
   while (cl < kSelMaxCluster && static_cast<long long>(cl) * kSelSlots < end) cl *= 2;
-  cudaError_t e = launch_pdl_cluster(cache8_select_kernel, dim3(cl, B), dim3(kSelThreads), 0, cl,
-                                     stream, q);
+  const int run = ((end + cl - 1) / cl + kSelThreads - 1) / kSelThreads * kSelThreads;
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(cache8_select_kernel), kSelKeys * 4);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl_cluster(cache8_select_kernel, dim3(cl, B), dim3(kSelThreads),
+                         run <= kSelKeys ? static_cast<size_t>(run) * 4 : 0, cl, stream, q);
   if (e != cudaSuccess) return e;
   MoveParams p;
   p.K8 = static_cast<const uint8_t*>(K8);
@@ -535,8 +592,9 @@ cudaError_t launch_cache8_evict(const void* K8, const void* V8, const float* K_s
   p.V8_dst = static_cast<uint8_t*>(V8_dst);
   p.K_scale_dst = K_scale_dst;
   p.V_scale_dst = V_scale_dst;
-  const dim3 grid(static_cast<unsigned>(static_cast<long long>(B) * p.nblk * H_kv * 2));
-  return launch_pdl(d_h == 256 ? cache8_move_kernel<256> : cache8_move_kernel<128>, grid,
+  const int u = d_h == 256 ? 2 : 4;
+  const dim3 grid(static_cast<unsigned>(static_cast<long long>(B) * p.nblk * ((2 * H_kv + u - 1) / u)));
+  return launch_pdl(d_h == 256 ? cache8_move_kernel<256, 2> : cache8_move_kernel<128, 4>, grid,
                     dim3(kRowThreads), 0, stream, p);
 }
 

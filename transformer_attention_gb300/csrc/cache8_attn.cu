@@ -97,7 +97,9 @@ struct Cfg {
   static constexpr int NCH = DH / 128;                  // 128-byte column boxes of a row
   static constexpr int BOX = kTile * 128;
   static constexpr int TILE = 2 * NCH * BOX;            // K' and V of one tile
-  static constexpr int NST = DH == 256 ? 3 : 6;         // ring stages (96 KB either way)
+  // CTAs per SM, and ring stages: 64 KB of tiles per CTA for three, 96 for two
+  static constexpr int CTAS = DH == 128 && NT == 1 ? 3 : 2;
+  static constexpr int NST = DH == 256 ? 3 : (CTAS == 3 ? 4 : 6);
   static constexpr int RING = NST * TILE;
   static constexpr int NC = DH / 16;                    // 16-channel chunks
   static constexpr int QF = NC * NT * 32 * 8;           // Q fragments
@@ -106,7 +108,7 @@ struct Cfg {
   static constexpr int MERGE = kCWarps * ROWS * LDM * 4;
   static constexpr int SMEM = 1024 + RING + QF;
   static_assert(MERGE <= RING, "merge records must fit in the ring");
-  static_assert(SMEM <= 112 * 1024, "two CTAs per SM");
+  static_assert((SMEM + 2048) * CTAS <= 228 * 1024, "CTAs per SM");
 };
 
 struct Params {
@@ -144,7 +146,7 @@ __device__ __forceinline__ void store_o(void* O, int o_f16, size_t at, float v) 
 }
 
 template <int DH, int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
     decode8_kernel(const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const Params p) {
   pdl_enter();
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   // Q fragments: k columns {2c, 2c+1, 2c+8, 2c+9} of a 16-channel chunk are
   // the channels 4c .. 4c+3, row n = lane / 4.
+#pragma unroll 4
   for (int i = tid; i < C::NC * NT * 32; i += kThreads) {
     const int l = i & 31, nt = (i >> 5) % NT, ch = (i >> 5) / NT;
     const int r = nt * 8 + (l >> 2);
@@ -457,29 +460,42 @@ __global__ void __launch_bounds__(kThreads, 2)
             make_float2(o[ch][nt][e] * unit, o[ch][nt][2 + e] * unit);
     }
   named_barrier(1, kCWarps * 32);
-  for (int idx = tid; idx < R * DH; idx += kCWarps * 32) {
-    const int r = idx / DH, ch = idx % DH;
+  for (int idx = tid; idx < R * (DH / 4); idx += kCWarps * 32) {
+    const int r = idx / (DH / 4), ch = idx % (DH / 4) * 4;
+    float2 ms[kCWarps];
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kCWarps; ++w) M = fmaxf(M, mstat[w][r].x);
-    float L = 0.f, acc = 0.f;
+    for (int w = 0; w < kCWarps; ++w) {
+      ms[w] = mstat[w][r];
+      M = fmaxf(M, ms[w].x);
+    }
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (M != -INFINITY) {
 #pragma unroll
       for (int w = 0; w < kCWarps; ++w) {
-        const float2 ms = mstat[w][r];
-        const float fw = ex2(ms.x - M);
-        L += fw * ms.y;
+        const float fw = ex2(ms[w].x - M);
+        L += fw * ms[w].y;
         // (a warp that saw nothing holds zeros)
-        acc += fw * mg[(w * C::ROWS + r) * C::LDM + ch];
+        const float4 v = *reinterpret_cast<const float4*>(mg + (w * C::ROWS + r) * C::LDM + ch);
+        acc.x += fw * v.x;
+        acc.y += fw * v.y;
+        acc.z += fw * v.z;
+        acc.w += fw * v.w;
       }
     }
     const int t = r / G, h = j * G + r % G;
     const size_t orow = (static_cast<size_t>(b) * p.T + t) * p.H + h;
     if (ch == 0 && p.stat != nullptr) p.stat[orow * p.nsplit + split] = make_float2(M, L);
-    if (p.nsplit == 1)
-      store_o(p.O, p.o_f16, orow * DH + ch, L != 0.f ? acc / L : 0.f);
-    else
-      p.part[(orow * p.nsplit + split) * DH + ch] = acc;
+    if (p.nsplit == 1) {
+      const float inv = L != 0.f ? 1.f / L : 0.f;
+      const float x0 = acc.x * inv, x1 = acc.y * inv, x2 = acc.z * inv, x3 = acc.w * inv;
+      const uint2 v = p.o_f16 ? make_uint2(pack_half2(x0, x1), pack_half2(x2, x3))
+                              : make_uint2(pack_bf162(x0, x1), pack_bf162(x2, x3));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * DH + ch) = v;
+    } else {
+      *reinterpret_cast<float4*>(p.part + (orow * p.nsplit + split) * DH + ch) = acc;
+    }
   }
 }
 
@@ -497,7 +513,9 @@ __global__ void __launch_bounds__(256) span8_kernel(const int32_t* __restrict__ 
 
 // ---------------------------------------------------------------- second launch
 // CTAs [0, n_rows): merge the parts of one query row.  The others: weights of
-// 256 slots of one batch row, every query row's logits once.
+// kWSlots slots of one batch row, every query row's logits once.
+constexpr int kWSlots = 512;
+
 struct FinishParams {
   const float2* stat;
   const float* part;
@@ -515,6 +533,7 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
   pdl_enter();
   __shared__ float fw[kMaxSplits];
   __shared__ float2 rs[256];
+  __shared__ int last[256];
   __shared__ float red[2][8];
   __shared__ int lo_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -557,20 +576,26 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
     return;
   }
   const int wi = blockIdx.x - p.n_rows;
-  const int b = wi / p.wchunks, s = (wi % p.wchunks) * 256 + tid;
+  const int b = wi / p.wchunks, s = (wi % p.wchunks) * kWSlots + 2 * tid;
   if (warp == 0) {
     const int lo = first_visible(p.span_part, p.nchunk, b, lane);
     if (lane == 0) lo_s = lo;
   }
-  const int R = p.T * (p.H / p.H_kv), rows = p.T * p.H, G = p.H / p.H_kv;
+  // Rows in the order of the logits: kv head, token, head of the group.
+  const int rows = p.T * p.H, G = p.H / p.H_kv, R = p.T * G;
   const size_t S64 = static_cast<size_t>(p.nb) * kTile;
   const int valid = p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0);
-  float acc = 0.f;
+  const float* lg = p.logits + static_cast<size_t>(b) * rows * S64 + s;
+  float2 acc = make_float2(0.f, 0.f);
   for (int r0 = 0; r0 < rows; r0 += 256) {
+    const int n = min(256, rows - r0);
     __syncthreads();
-    // (max, 1 / sum) of the query rows over their parts, a warp each
-    for (int i = warp; i < min(256, rows - r0); i += 8) {
-      const float2* st = p.stat + (static_cast<size_t>(b) * rows + r0 + i) * p.nsplit;
+    // (max, 1 / sum) of the query rows over their parts, a warp each, and the
+    // last slot whose logit the first launch wrote (a valid token's own)
+    for (int i = warp; i < n; i += 8) {
+      const int j = (r0 + i) / R, q = (r0 + i) % R, t = q / G;
+      const float2* st =
+          p.stat + ((static_cast<size_t>(b) * p.T + t) * p.H + j * G + q % G) * p.nsplit;
       float M = -INFINITY, L = 0.f;
       for (int k = lane; k < p.nsplit; k += 32) M = fmaxf(M, st[k].x);
 #pragma unroll
@@ -579,25 +604,28 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
         for (int k = lane; k < p.nsplit; k += 32) L = fmaf(ex2(st[k].x - M), st[k].y, L);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      if (lane == 0)
+      if (lane == 0) {
         rs[i] = make_float2(M == -INFINITY ? 0.f : M, M != -INFINITY && L != 0.f ? 1.f / L : 0.f);
+        last[i] = t < valid ? p.end + t : -1;
+      }
     }
     __syncthreads();
-    // (the first launch wrote logits from the first visible tile up to a valid
-    // token's own slot)
+    // (from the first visible tile on; two slots per thread, of one tile)
     if (s < p.end + p.T && s >= lo_s / kTile * kTile) {
-      const int n = min(256, rows - r0);
-#pragma unroll 4
+#pragma unroll 8
       for (int i = 0; i < n; ++i) {
-        const int row = r0 + i, t = row / p.H, h = row % p.H;
-        if (t >= valid || s > p.end + t) continue;
-        const float x = __ldg(p.logits + ((static_cast<size_t>(b) * p.H_kv + h / G) * R + t * G +
-                                          h % G) * S64 + s);
-        acc = fmaf(ex2(x - rs[i].x), rs[i].y, acc);
+        const int lim = last[i];
+        if (s > lim) continue;
+        const float2 x = __ldg(reinterpret_cast<const float2*>(lg + (r0 + i) * S64));
+        const float2 st = rs[i];
+        acc.x = fmaf(ex2(x.x - st.x), st.y, acc.x);
+        if (s + 1 <= lim) acc.y = fmaf(ex2(x.y - st.x), st.y, acc.y);
       }
     }
   }
-  if (s < p.end + p.T && acc != 0.f) p.weight_sum[static_cast<size_t>(b) * p.S + s] += acc;
+  float* out = p.weight_sum + static_cast<size_t>(b) * p.S;
+  if (acc.x != 0.f) out[s] += acc.x;
+  if (acc.y != 0.f) out[s + 1] += acc.y;
 }
 
 // ---------------------------------------------------------------- planning
@@ -626,17 +654,18 @@ Plan plan_rows(int B, int T, int S, int H, int H_kv, int d_h) {
 
 // Splits of few rows, bound by HBM: counted in the time a tile takes at the
 // full rate of HBM (2.6 ns for d_h = 128, 5.1 for 256), the tiles all
-// together, or those of one CTA at the pace of one among 256 (the CTAs that
-// saturate HBM), whichever is longer, and about 2 us per round of two CTAs
-// per SM to start and merge.  (12B-shaped batch of 16 over 7777 slots: 896
-// CTAs in three rounds 88 us, 256 CTAs in one 84 us.)
-int splits_few(const Plan& d, int tiles, int d_h) {
-  const int slots = 2 * num_sms(), start = d_h == 256 ? 400 : 800;
+// together, or those of one CTA at the pace of one among `full` (the CTAs
+// that saturate HBM), whichever is longer, and about 2 us per round of CTAs
+// to start and merge.  (12B-shaped batch of 16 over 7777 slots, d_h = 256: 896
+// CTAs in three rounds 88 us, 256 CTAs in one 82 us.)
+int splits_few(const Plan& d, int tiles, int d_h, int ctas_per_sm) {
+  const int slots = ctas_per_sm * num_sms(), start = d_h == 256 ? 400 : 800;
+  const int full = d_h == 256 ? 224 : slots;
   int nsplit = 1;
   long long best = LLONG_MAX;
   for (int n = 1; n <= std::min(d.max_splits, tiles); ++n) {
     const long long waves = (d.units * n + slots - 1) / slots, per = (tiles + n - 1) / n;
-    const long long cost = std::max(d.units * tiles, waves * per * 256) + waves * start;
+    const long long cost = std::max(d.units * tiles, waves * per * full) + waves * start;
     if (cost < best) {
       best = cost;
       nsplit = n;
@@ -696,6 +725,12 @@ Layout layout(void* ws, int B, int T, int S, int H, int H_kv, int d_h, bool weig
   return L;
 }
 
+// CTAs of decode8_kernel per SM for T * G = rows.
+int few_ctas(int d_h, int rows) {
+  if (d_h == 256) return rows <= 8 ? Cfg<256, 1>::CTAS : Cfg<256, 2>::CTAS;
+  return rows <= 8 ? Cfg<128, 1>::CTAS : Cfg<128, 2>::CTAS;
+}
+
 template <int DH, int NT>
 cudaError_t launch_cfg(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, dim3 grid,
                        cudaStream_t stream) {
@@ -726,7 +761,7 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   const long long est = window > 0 ? std::min<long long>(hi, static_cast<long long>(window) + span)
                                    : static_cast<long long>(hi);
   const int tiles = static_cast<int>((est + d.tile - 1) / d.tile) + (window > 0 ? 1 : 0);
-  const int nsplit = d.few ? splits_few(d, tiles, d_h) : splits_many(d, tiles, B * 1LL * T * H * d_h);
+  const int nsplit = d.few ? splits_few(d, tiles, d_h, few_ctas(d_h, T * (H / H_kv))) : splits_many(d, tiles, B * 1LL * T * H * d_h);
   cudaError_t e;
 
   if (!d.few) {
@@ -846,7 +881,7 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   q.end = end;
   q.nsplit = nsplit;
   q.nchunk = nchunk;
-  q.wchunks = (hi + 255) / 256;
+  q.wchunks = (hi + kWSlots - 1) / kWSlots;
   const long long ctas =
       q.n_rows + (weight_sum != nullptr ? static_cast<long long>(B) * q.wchunks : 0);
   if (ctas > INT_MAX) return cudaErrorInvalidValue;
