@@ -216,6 +216,7 @@ struct SelectParams {
 constexpr int kSelThreads = 1024;
 constexpr int kSelSlots = 8192;      // slots per CTA worth one more CTA in the cluster
 constexpr int kSelMaxCluster = 8;
+constexpr int kSelCopies = 4;
 constexpr int kSelKeys = 48 * 1024;  // keys that a CTA keeps in shared memory
 
 // One cluster per batch row: the keep-th largest key by four rounds of 8-bit
@@ -232,9 +233,9 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
   const int rank = cluster.block_rank(), C = cluster.num_blocks();
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   extern __shared__ uint32_t keys[];
-  __shared__ int hist[2][256];
-  __shared__ int sum[256];
-  __shared__ int wsum[2][32];
+  __shared__ int hist[2][kSelCopies][256];   // copies: lanes of one digit wait less for each other
+  __shared__ int sum[256], own[256];
+  __shared__ int wsum[32];
   __shared__ int counts[2];
   __shared__ int found[2][2];        // by round parity: digit, keys above it
   const float* w = p.w + static_cast<size_t>(b) * p.S;
@@ -245,9 +246,12 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
   const int hi = static_cast<int>(min(static_cast<long long>(p.end), static_cast<long long>(lo) + run));
   const bool kept_here = run <= kSelKeys;
   auto fresh_key = [&](int s) { return evict_key(__ldg(w + s), __ldg(pos + s), s, p.first_recent); };
+  // Warp w owns the slots w0 .. w1 of the CTA's run, 32 next to each other at
+  // a time (a thread reads back only keys that it stored).
+  const int seg = run / 32, w0 = lo + warp * seg, w1 = min(hi, w0 + seg);
   if (kept_here) {
-#pragma unroll 4
-    for (int s = lo + tid; s < hi; s += kSelThreads) keys[s - lo] = fresh_key(s);
+#pragma unroll 8
+    for (int s = w0 + lane; s < w1; s += 32) keys[s - lo] = fresh_key(s);
   }
   auto key_at = [&](int s) { return kept_here ? keys[s - lo] : fresh_key(s); };
 
@@ -258,30 +262,28 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
   int own_eq = 0;
   for (int round = 0; round < 4; ++round) {
     const int shift = 24 - 8 * round;
-    int* h = hist[round & 1];
-    if (tid < 256) h[tid] = 0;
+    int (*h)[256] = hist[round & 1];
+    for (int i = tid; i < kSelCopies * 256; i += kSelThreads) (&h[0][0])[i] = 0;
     __syncthreads();
-    for (int base = lo; base < hi; base += kSelThreads) {
-      const int s = base + tid;
-      const uint32_t key = s < hi ? key_at(s) : 0u;
-      const bool in = key != 0 && (round == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8)));
-      const int digit = static_cast<int>((key >> shift) & 255u);
-      // A warp whose keys all share a digit (equal weights) adds once.
-      const unsigned m = __ballot_sync(0xffffffffu, in);
-      if (m == 0) continue;
-      const int d0 = __shfl_sync(0xffffffffu, digit, __ffs(m) - 1);
-      if (__all_sync(0xffffffffu, !in || digit == d0)) {
-        if (lane == 0) atomicAdd(&h[d0], __popc(m));
-      } else if (in) {
-        atomicAdd(&h[digit], 1);
-      }
+#pragma unroll 4
+    for (int s = w0 + lane; s < w1; s += 32) {
+      const uint32_t key = key_at(s);
+      if (key != 0 && (round == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8))))
+        atomicAdd(&h[lane % kSelCopies][(key >> shift) & 255u], 1);
+    }
+    __syncthreads();
+    if (tid < 256) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kSelCopies; ++i) n += h[i][tid];
+      h[0][tid] = own[tid] = n;
     }
     cluster.sync();
     if (tid < 256) {
       int n = 0;
 #pragma unroll
       for (int r = 0; r < kSelMaxCluster; ++r)
-        if (r < C) n += cluster.map_shared_rank(h, r)[tid];
+        if (r < C) n += cluster.map_shared_rank(&h[0][0], r)[tid];
       sum[tid] = n;
     }
     __syncthreads();
@@ -320,11 +322,11 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int k = 255 - 8 * lane - i;
-        if (k > d) gt += h[k];
+        if (k > d) gt += own[k];
       }
       gt = __reduce_add_sync(0xffffffffu, gt);
       own_gt += gt;
-      own_eq = d >= 0 ? h[d] : 0;
+      own_eq = d >= 0 ? own[d] : 0;
     }
     __syncthreads();
     if (f[0] < 0) {                  // (only in round 0)
@@ -362,34 +364,39 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
   int32_t* kept = p.kept + static_cast<size_t>(b) * p.keep;
   int32_t* pos_dst = p.pos_dst + static_cast<size_t>(b) * p.S_dst;
   float* w_dst = p.w_dst + static_cast<size_t>(b) * p.S_dst;
-  for (int base = lo, step = 0; base < hi; base += kSelThreads, ++step) {
-    const int s = base + tid;
-    const uint32_t key = s < hi ? key_at(s) : 0u;
-    const bool g = s < hi && key > thr, e = s < hi && key == thr && want > 0;
+  // counts of (above, equal) of each warp's slots, and before them
+  int wg = 0, we = 0;
+#pragma unroll 4
+  for (int s = w0 + lane; s < w1; s += 32) {
+    const uint32_t key = key_at(s);
+    wg += key > thr;
+    we += key == thr;
+  }
+  wg = __reduce_add_sync(0xffffffffu, wg);
+  we = want > 0 ? __reduce_add_sync(0xffffffffu, we) : 0;
+  if (lane == 0) {
+    wsum[warp] = wg;
+    own[warp] = we;
+  }
+  __syncthreads();
+  gt0 += __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0);
+  eq0 += __reduce_add_sync(0xffffffffu, lane < warp ? own[lane] : 0);
+#pragma unroll 2
+  for (int base = w0; base < w1; base += 32) {
+    const int s = base + lane;
+    const uint32_t key = s < w1 ? key_at(s) : 0u;
+    const bool g = s < w1 && key > thr, e = s < w1 && key == thr && want > 0;
     const unsigned bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
-    // counts of (above, equal) in 16 bits each: at most 1024 per step
-    if (lane == 0) wsum[step & 1][warp] = __popc(bg) | (__popc(be) << 16);
-    __syncthreads();
-    int v = wsum[step & 1][lane];
-    const int own = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += up;
-    }
-    const int total = __shfl_sync(0xffffffffu, v, 31);
-    const int here = __shfl_sync(0xffffffffu, v - own, warp);
     const unsigned below = (1u << lane) - 1u;
-    const int ng = gt0 + (here & 0xFFFF) + __popc(bg & below);
-    const int ne = eq0 + (here >> 16) + __popc(be & below);
+    const int ng = gt0 + __popc(bg & below), ne = eq0 + __popc(be & below);
     if (g || (e && ne < want)) {
       const int d = ng + min(ne, want);
       kept[d] = s;
       pos_dst[d] = __ldg(pos + s);
       w_dst[d] = __ldg(w + s);
     }
-    gt0 += total & 0xFFFF;
-    eq0 += total >> 16;
+    gt0 += __popc(bg);
+    eq0 += __popc(be);
   }
   for (int d = n_kept + rank * kSelThreads + tid; d < p.keep; d += C * kSelThreads) {
     kept[d] = -1;

@@ -31,16 +31,20 @@
 //   - The probabilities are rounded to fp16 for the V product (relative error
 //     2^-11 each, averaged over slots; below the fp16 or bf16 output's own
 //     rounding); sums and maxima are fp32.
-// The slots of a (row, kv head) are split over CTAs, and a second launch
-// merges the parts and, for weight_sum, adds up exp2(logit - max) / sum from
-// the logits that the first one left in the workspace (4 bytes per query row
-// and slot, against 2 d_h for K' and V; reading K' again would cost d_h).
+// The slots of a (row, kv head) are split over CTAs: up to eight form a
+// cluster that merges its parts through distributed shared memory, more leave
+// them to a second launch.  For weight_sum a second launch adds up exp2(logit
+// - max) / sum from the logits that the first one left in the workspace (4
+// bytes per query row and slot, against 2 d_h for K' and V; reading K' again
+// would cost d_h).  On a local layer the CTAs take the last window's worth of
+// slots at once, and look through the positions of all earlier slots for ones
+// that a query still sees (positions may have gaps) while the first copies
+// are under way.
 #include <algorithm>
 #include <climits>
 
 #include "cache8.cuh"
 #include "cache8_flash.cuh"
-#include "decode_span.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -52,6 +56,7 @@ constexpr int kTile = kC8Block;      // slots per tile: one scale block
 constexpr int kCWarps = 4;           // consumer warps, 16 slots of each tile each
 constexpr int kThreads = (kCWarps + 1) * 32;
 constexpr int kMaxSplits = 256;
+constexpr int kMaxCluster = 8;
 constexpr int kFewRows = 16;         // query rows of a kv head that decode8_kernel takes
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -107,7 +112,7 @@ struct Cfg {
   static constexpr int LDM = DH + 8;                    // merge record row, floats
   static constexpr int MERGE = kCWarps * ROWS * LDM * 4;
   static constexpr int SMEM = 1024 + RING + QF;
-  static_assert(MERGE <= RING, "merge records must fit in the ring");
+  static_assert(MERGE + ROWS * DH * 4 <= RING, "merge records must fit in the ring");
   static_assert((SMEM + 2048) * CTAS <= 228 * 1024, "CTAs per SM");
 };
 
@@ -118,24 +123,29 @@ struct Params {
   const int32_t* posc;        // [B, S]
   const int32_t* qpos;        // [B, T]
   const int32_t* pad_lens;    // [B] or null
-  const int32_t* span_part;   // [B, nchunk] or null
-  float2* stat;               // [B*T*H, nsplit] (max, sum) of each part
-  float* part;                // [B*T*H, nsplit, DH] unnormalised, when nsplit > 1
+  int2* swept;                // [B, nsplit] tiles of each CTA's early slots that were
+                              // attended (local layers with weights), or null
+  float2* stat;               // [B*T*H, parts] (max, sum); parts = nsplit, or 1 of a cluster
+  float* part;                // [B*T*H, nsplit, DH] unnormalised, of parts > 1
   float* logits;              // [B, H_kv, T*G, S64] base-2 logits, or null
   void* O;
-  int o_f16, B, T, S, H, H_kv, nb, end, window, nsplit, nchunk;
+  int o_f16, B, T, S, H, H_kv, nb, end, window, nsplit, cluster, late;
   int* status;
 };
 
-__device__ __forceinline__ int first_visible(const int32_t* span_part, int nchunk, int b, int lane) {
-  int lo = 0;
-  if (span_part != nullptr) {
-    lo = INT_MAX;
-    for (int i = lane; i < nchunk; i += 32)
-      lo = min(lo, span_part[static_cast<size_t>(b) * nchunk + i]);
-    lo = span_warp_min(lo);
-  }
-  return lo;
+// Tiles [0, k0) of a batch row are its early ones, [k0, k1) the `late` last
+// (all of them on a global layer); `per` of each for one of nsplit CTAs.
+struct Tiles {
+  int hi, k0, k1, per_early, per_late;
+};
+__device__ __forceinline__ Tiles tiles_of(int end, int T, int valid, int late, int nsplit) {
+  Tiles t;
+  t.hi = valid > 0 ? end + min(valid, T) : 0;
+  t.k1 = (t.hi + kTile - 1) / kTile;
+  t.k0 = max(0, t.k1 - late);
+  t.per_early = (t.k0 + nsplit - 1) / nsplit;
+  t.per_late = (t.k1 - t.k0 + nsplit - 1) / nsplit;
+  return t;
 }
 
 __device__ __forceinline__ void store_o(void* O, int o_f16, size_t at, float v) {
@@ -143,6 +153,27 @@ __device__ __forceinline__ void store_o(void* O, int o_f16, size_t at, float v) 
     static_cast<__half*>(O)[at] = __float2half_rn(v);
   else
     static_cast<__nv_bfloat16*>(O)[at] = __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ void store_o4(void* O, int o_f16, size_t at, const float4& v, float f) {
+  const float x0 = v.x * f, x1 = v.y * f, x2 = v.z * f, x3 = v.w * f;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(O) + at) =
+      o_f16 ? make_uint2(pack_half2(x0, x1), pack_half2(x2, x3))
+            : make_uint2(pack_bf162(x0, x1), pack_bf162(x2, x3));
+}
+
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 template <int DH, int NT>
@@ -158,7 +189,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
   uint2* qf = reinterpret_cast<uint2*>(smem + C::RING);       // [NC][NT][32]
   __shared__ __align__(8) uint64_t full[C::NST], empty[C::NST];
   __shared__ int abort_flag;
-  __shared__ int rng[3];
+  __shared__ int early[2];             // first and last early tile with a visible slot
+  __shared__ float2 cstat[C::ROWS];    // this CTA's part, for its cluster
   __shared__ float2 mstat[kCWarps][C::ROWS];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -175,23 +207,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
       mbar_init(smem_u32(&empty[s]), kCWarps);
     }
     abort_flag = 0;
+    early[0] = INT_MAX;
+    early[1] = -1;
     fence_barrier_init();
   }
-  if (warp == kCWarps) {
-    // Visible slots of this CTA's rows lie in [lo, hi): whole tiles of them,
-    // evenly over the nsplit CTAs of (b, j).
-    int lo = first_visible(p.span_part, p.nchunk, b, lane);
-    const int hi = valid > 0 ? p.end + min(valid, p.T) : 0;
-    lo = min(lo, hi);
-    const int k0 = lo / kTile, k1 = (hi + kTile - 1) / kTile;
-    const int per = (k1 - k0 + p.nsplit - 1) / p.nsplit;
-    const long long a = k0 + static_cast<long long>(split) * per;
-    if (lane == 0) {
-      rng[0] = static_cast<int>(min(a, static_cast<long long>(k1)));
-      rng[1] = static_cast<int>(min(a + per, static_cast<long long>(k1)));
-      rng[2] = hi;
-    }
-  }
+  const Tiles tl = tiles_of(p.end, p.T, valid, p.late, p.nsplit);
+  const int hi = tl.hi;
+  const int late0 = min(tl.k1, tl.k0 + split * tl.per_late);
+  const int n_late = min(tl.k1, late0 + tl.per_late) - late0;
   // Q fragments: k columns {2c, 2c+1, 2c+8, 2c+9} of a 16-channel chunk are
   // the channels 4c .. 4c+3, row n = lane / 4.
 #pragma unroll 4
@@ -207,34 +230,56 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
     qf[i] = q;
   }
   __syncthreads();
-  const int k_lo = rng[0], n_tiles = rng[1] - rng[0], hi = rng[2];
+  // Tile i of this CTA: its late ones, then the early ones that it found.
+  int early0 = 0, n_tiles = n_late;
+  auto tile_at = [&](int i) { return i < n_late ? late0 + i : early0 + (i - n_late); };
+  auto take_early = [&]() {
+    if (early[1] >= 0) {
+      early0 = early[0];
+      n_tiles = n_late + early[1] - early0 + 1;
+    }
+  };
 
   if (warp == kCWarps) {
     // ---------------- producer: K'/V tiles of 64 slots into the ring
-    if (lane == 0 && n_tiles > 0) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-      int issued = 0;
-      for (int i = 0; i < n_tiles; ++i) {
-        const int st = i % C::NST;
-        if (i >= C::NST && !mbar_wait(smem_u32(&empty[st]), ((i / C::NST) - 1) & 1, &abort_flag,
-                                      p.status, kSiteEmpty))
-          break;
+    int issued = 0;
+    auto issue = [&](int upto) {
+      for (; issued < upto; ++issued) {
+        const int st = issued % C::NST;
+        if (issued >= C::NST && !mbar_wait(smem_u32(&empty[st]), ((issued / C::NST) - 1) & 1,
+                                           &abort_flag, p.status, kSiteEmpty))
+          return;
         const uint32_t bar = smem_u32(&full[st]);
         mbar_arrive_expect_tx(bar, C::TILE);
         uint8_t* kd = ring + st * C::TILE;
         uint8_t* vd = kd + C::NCH * C::BOX;
-        const int s0 = (k_lo + i) * kTile;
+        const int s0 = tile_at(issued) * kTile;
 #pragma unroll
         for (int ch = 0; ch < C::NCH; ++ch) {
           tma_load_4d(smem_u32(kd + ch * C::BOX), &tmK, bar, ch * 128, j, s0, b);
           tma_load_4d(smem_u32(vd + ch * C::BOX), &tmV, bar, ch * 128, j, s0, b);
         }
-        issued = i + 1;
       }
-      // Every issued load lands before the CTA may exit.
+    };
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      issue(p.window > 0 ? min(n_late, C::NST) : n_late);
+    }
+    if (p.window > 0) {
+      __syncwarp();
+      named_barrier(2, kThreads);
+      take_early();
+      if (lane == 0) issue(n_tiles);
+    }
+    // Every issued load lands before the CTA may exit.
+    if (lane == 0)
       for (int i = max(0, issued - C::NST); i < issued; ++i)
         mbar_wait_drain(smem_u32(&full[i % C::NST]), (i / C::NST) & 1);
+    __syncwarp();
+    if (p.cluster) {
+      cluster_sync();
+      cluster_sync();
     }
     return;
   }
@@ -259,6 +304,44 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
         }
       }
     }
+  if (p.window > 0) {
+    // early slots that some query of the row sees
+    int qn = INT_MAX, qx = INT_MIN;
+    for (int t = 0; t < min(valid, p.T); ++t) {
+      const int q = p.qpos[static_cast<size_t>(b) * p.T + t];
+      qn = min(qn, q);
+      qx = max(qx, q);
+    }
+    int lo, up, first = INT_MAX, last = -1;
+    window_range(qn, qx, p.window, lo, up);
+    const int32_t* row = p.posc + static_cast<size_t>(b) * p.S;
+    const int e0 = min(tl.k0, split * tl.per_early) * kTile;
+    const int e1 = min(tl.k0, (split + 1) * tl.per_early) * kTile;
+    for (int s = e0 + tid; s < e1; s += 8 * kCWarps * 32) {
+      int ps[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        ps[k] = s + k * kCWarps * 32 < e1 ? __ldg(row + s + k * kCWarps * 32) : -1;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (ps[k] >= lo && ps[k] <= up) {
+          first = min(first, (s + k * kCWarps * 32) / kTile);
+          last = (s + k * kCWarps * 32) / kTile;
+        }
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (lane == 0 && last >= 0) {
+      atomicMin(&early[0], first);
+      atomicMax(&early[1], last);
+    }
+    __threadfence_block();
+    named_barrier(2, kThreads);
+    take_early();
+    if (p.swept != nullptr && j == 0 && tid == 0)
+      p.swept[static_cast<size_t>(b) * p.nsplit + split] =
+          make_int2(early0, early0 + n_tiles - n_late);
+  }
   float m[NT][2], l[NT][2], o[C::NC][NT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -287,17 +370,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
   auto fetch = [&](int i) {
     pos0 = pos1 = -1;
     if (i < n_tiles) {
-      const int s = (k_lo + i) * kTile + so;
+      const int k = tile_at(i), s = k * kTile + so;
       if (s < hi) pos0 = __ldg(posr + s);
       if (s + 8 < hi) pos1 = __ldg(posr + s + 8);
-      ks = __ldg(ksp + static_cast<size_t>(k_lo + i) * p.H_kv);
-      vs = __ldg(vsp + static_cast<size_t>(k_lo + i) * p.H_kv);
+      ks = __ldg(ksp + static_cast<size_t>(k) * p.H_kv);
+      vs = __ldg(vsp + static_cast<size_t>(k) * p.H_kv);
     }
   };
   fetch(0);
   for (int i = 0; i < n_tiles; ++i) {
     const int st = i % C::NST;
-    const int s = (k_lo + i) * kTile + so;
+    const int s = tile_at(i) * kTile + so;
     const int ps0 = pos0, ps1 = pos1;
     const float kl = ks * kLog2e, vsc = vs;
     fetch(i + 1);
@@ -444,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
   // writes any more once every warp is past its last tile)
   named_barrier(1, kCWarps * 32);
   float* mg = reinterpret_cast<float*>(ring);
+  float* cacc = reinterpret_cast<float*>(ring + C::MERGE);     // [ROWS][DH]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -486,29 +570,57 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
     }
     const int t = r / G, h = j * G + r % G;
     const size_t orow = (static_cast<size_t>(b) * p.T + t) * p.H + h;
-    if (ch == 0 && p.stat != nullptr) p.stat[orow * p.nsplit + split] = make_float2(M, L);
-    if (p.nsplit == 1) {
-      const float inv = L != 0.f ? 1.f / L : 0.f;
-      const float x0 = acc.x * inv, x1 = acc.y * inv, x2 = acc.z * inv, x3 = acc.w * inv;
-      const uint2 v = p.o_f16 ? make_uint2(pack_half2(x0, x1), pack_half2(x2, x3))
-                              : make_uint2(pack_bf162(x0, x1), pack_bf162(x2, x3));
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * DH + ch) = v;
-    } else {
-      *reinterpret_cast<float4*>(p.part + (orow * p.nsplit + split) * DH + ch) = acc;
+    if (p.cluster) {
+      if (ch == 0) cstat[r] = make_float2(M, L);
+      *reinterpret_cast<float4*>(cacc + r * DH + ch) = acc;
+      continue;
     }
+    if (ch == 0 && p.stat != nullptr) p.stat[orow * p.nsplit + split] = make_float2(M, L);
+    if (p.nsplit == 1)
+      store_o4(p.O, p.o_f16, orow * DH + ch, acc, L != 0.f ? 1.f / L : 0.f);
+    else
+      *reinterpret_cast<float4*>(p.part + (orow * p.nsplit + split) * DH + ch) = acc;
   }
-}
-
-// Local layers: CTA (c, b) writes the first slot of chunk c that a valid
-// query of row b can see, or INT_MAX (decode_span.cuh).
-__global__ void __launch_bounds__(256) span8_kernel(const int32_t* __restrict__ posc,
-                                                    const int32_t* __restrict__ qpos,
-                                                    const int32_t* __restrict__ pad_lens, int T,
-                                                    int S, int end, int window, int nchunk,
-                                                    int32_t* __restrict__ span_part) {
-  pdl_enter();
-  kv_span_chunk(posc, qpos, pad_lens, T, S, end, window, nchunk, span_part, blockIdx.x,
-                blockIdx.y);
+  if (p.cluster) {
+    // The cluster's parts, read through distributed shared memory; each CTA
+    // writes its share of the rows' channels.
+    __syncwarp();
+    cluster_sync();
+    const uint32_t st = smem_u32(cstat), ac = smem_u32(cacc);
+    for (int idx = split * (kCWarps * 32) + tid; idx < R * (DH / 4);
+         idx += p.nsplit * kCWarps * 32) {
+      const int r = idx / (DH / 4), ch = idx % (DH / 4) * 4;
+      float2 ms[8];
+      float4 v[8];
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 8; ++w)
+        if (w < p.nsplit) {
+          ms[w] = ld_cluster_f2(mapa_shared(st + r * 8, w));
+          v[w] = ld_cluster_f4(mapa_shared(ac + (r * DH + ch) * 4, w));
+          M = fmaxf(M, ms[w].x);
+        }
+      float L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (M != -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+          if (w < p.nsplit) {
+            const float fw = ex2(ms[w].x - M);
+            L += fw * ms[w].y;
+            acc.x += fw * v[w].x;
+            acc.y += fw * v[w].y;
+            acc.z += fw * v[w].z;
+            acc.w += fw * v[w].w;
+          }
+      }
+      const size_t orow = (static_cast<size_t>(b) * p.T + r / G) * p.H + j * G + r % G;
+      if (ch == 0 && p.stat != nullptr) p.stat[orow] = make_float2(M, L);
+      store_o4(p.O, p.o_f16, orow * DH + ch, acc, L != 0.f ? 1.f / L : 0.f);
+    }
+    __syncwarp();
+    cluster_sync();     // no CTA leaves while another reads its shared memory
+  }
 }
 
 // ---------------------------------------------------------------- second launch
@@ -522,10 +634,10 @@ struct FinishParams {
   const float* logits;
   float* weight_sum;
   float2* rowstat;            // many rows: [B, H_kv, T*G] of the merged rows, or null
-  const int32_t* span_part;
+  const int2* swept;          // as in Params
   const int32_t* pad_lens;
   void* O;
-  int o_f16, n_rows, T, S, H, H_kv, nb, end, nsplit, nchunk, wchunks;
+  int o_f16, n_rows, T, S, H, H_kv, nb, end, nsplit, parts, late, wchunks;
 };
 
 template <int DH>
@@ -535,7 +647,6 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
   __shared__ float2 rs[256];
   __shared__ int last[256];
   __shared__ float red[2][8];
-  __shared__ int lo_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (blockIdx.x < static_cast<unsigned>(p.n_rows)) {
     const size_t row = blockIdx.x;
@@ -577,31 +688,35 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
   }
   const int wi = blockIdx.x - p.n_rows;
   const int b = wi / p.wchunks, s = (wi % p.wchunks) * kWSlots + 2 * tid;
-  if (warp == 0) {
-    const int lo = first_visible(p.span_part, p.nchunk, b, lane);
-    if (lane == 0) lo_s = lo;
-  }
   // Rows in the order of the logits: kv head, token, head of the group.
   const int rows = p.T * p.H, G = p.H / p.H_kv, R = p.T * G;
   const size_t S64 = static_cast<size_t>(p.nb) * kTile;
   const int valid = p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0);
+  // Did the first launch attend this slot's tile?
+  const Tiles tl = tiles_of(p.end, p.T, valid, p.late, p.nsplit);
+  const int k = s / kTile;
+  bool seen = s < tl.hi;
+  if (seen && k < tl.k0) {
+    const int2 e = p.swept[static_cast<size_t>(b) * p.nsplit + k / tl.per_early];
+    seen = k >= e.x && k < e.y;
+  }
   const float* lg = p.logits + static_cast<size_t>(b) * rows * S64 + s;
   float2 acc = make_float2(0.f, 0.f);
   for (int r0 = 0; r0 < rows; r0 += 256) {
     const int n = min(256, rows - r0);
-    __syncthreads();
+    if (r0 > 0) __syncthreads();
     // (max, 1 / sum) of the query rows over their parts, a warp each, and the
     // last slot whose logit the first launch wrote (a valid token's own)
     for (int i = warp; i < n; i += 8) {
       const int j = (r0 + i) / R, q = (r0 + i) % R, t = q / G;
       const float2* st =
-          p.stat + ((static_cast<size_t>(b) * p.T + t) * p.H + j * G + q % G) * p.nsplit;
+          p.stat + ((static_cast<size_t>(b) * p.T + t) * p.H + j * G + q % G) * p.parts;
       float M = -INFINITY, L = 0.f;
-      for (int k = lane; k < p.nsplit; k += 32) M = fmaxf(M, st[k].x);
+      for (int k = lane; k < p.parts; k += 32) M = fmaxf(M, st[k].x);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       if (M != -INFINITY)
-        for (int k = lane; k < p.nsplit; k += 32) L = fmaf(ex2(st[k].x - M), st[k].y, L);
+        for (int k = lane; k < p.parts; k += 32) L = fmaf(ex2(st[k].x - M), st[k].y, L);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
       if (lane == 0) {
@@ -610,16 +725,17 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
       }
     }
     __syncthreads();
-    // (from the first visible tile on; two slots per thread, of one tile)
-    if (s < p.end + p.T && s >= lo_s / kTile * kTile) {
+    // (two slots of one tile per thread; the logits are loaded without asking
+    // whether they count, so that eight rows' are in flight)
+    if (seen) {
 #pragma unroll 8
       for (int i = 0; i < n; ++i) {
-        const int lim = last[i];
-        if (s > lim) continue;
         const float2 x = __ldg(reinterpret_cast<const float2*>(lg + (r0 + i) * S64));
         const float2 st = rs[i];
-        acc.x = fmaf(ex2(x.x - st.x), st.y, acc.x);
-        if (s + 1 <= lim) acc.y = fmaf(ex2(x.y - st.x), st.y, acc.y);
+        const int lim = last[i];
+        const float e0 = ex2(x.x - st.x), e1 = ex2(x.y - st.x);
+        acc.x = fmaf(s <= lim ? e0 : 0.f, st.y, acc.x);
+        acc.y = fmaf(s + 1 <= lim ? e1 : 0.f, st.y, acc.y);
       }
     }
   }
@@ -655,23 +771,31 @@ Plan plan_rows(int B, int T, int S, int H, int H_kv, int d_h) {
 // Splits of few rows, bound by HBM: counted in the time a tile takes at the
 // full rate of HBM (2.6 ns for d_h = 128, 5.1 for 256), the tiles all
 // together, or those of one CTA at the pace of one among `full` (the CTAs
-// that saturate HBM), whichever is longer, and about 2 us per round of CTAs
-// to start and merge.  (12B-shaped batch of 16 over 7777 slots, d_h = 256: 896
-// CTAs in three rounds 88 us, 256 CTAs in one 82 us.)
-int splits_few(const Plan& d, int tiles, int d_h, int ctas_per_sm) {
-  const int slots = ctas_per_sm * num_sms(), start = d_h == 256 ? 400 : 800;
+// that saturate HBM), whichever is longer, about 2 us per round of CTAs, and
+// for a second launch 3.5 us and 50 ns per split, which up to eight CTAs of a
+// cluster save (with weights there is one anyway).  12B-shaped batch of 16 over 7777 slots,
+// d_h = 256: 896 CTAs in three rounds 88 us, 256 CTAs in one 82 us.
+struct Split {
+  int n;
+  bool cluster;
+};
+Split splits_few(const Plan& d, int tiles, int d_h, int ctas_per_sm) {
+  const int slots = ctas_per_sm * num_sms(), us = d_h == 256 ? 200 : 400;
   const int full = d_h == 256 ? 224 : slots;
-  int nsplit = 1;
+  Split best_of = {1, false};
   long long best = LLONG_MAX;
-  for (int n = 1; n <= std::min(d.max_splits, tiles); ++n) {
+  for (int n = 1; n <= std::max(std::min(d.max_splits, tiles), kMaxCluster); ++n) {
+    const bool cluster = n == 2 || n == 4 || n == kMaxCluster;
+    if (!cluster && n > std::min(d.max_splits, tiles)) continue;
     const long long waves = (d.units * n + slots - 1) / slots, per = (tiles + n - 1) / n;
-    const long long cost = std::max(d.units * tiles, waves * per * full) + waves * start;
+    const long long cost = std::max(d.units * tiles, waves * per * full) + waves * 2 * us +
+                           (n > 1 && !cluster ? 7 * us / 2 + n * us / 20 : 0);
     if (cost < best) {
       best = cost;
-      nsplit = n;
+      best_of = {n, cluster};
     }
   }
-  return nsplit;
+  return best_of;
 }
 
 // Splits of many rows, bound by the tensor cores: a CTA's tiles (about a
@@ -693,7 +817,8 @@ int splits_many(const Plan& d, int tiles, long long elements) {
 }
 
 struct Layout {
-  int32_t* span_part;   // few: [B, chunks], many: [B, items]
+  int2* swept;          // few: [B, splits]
+  int32_t* first;       // many: [B, items]
   float2* stat;
   float* part;
   float* logits;        // few rows with weights
@@ -712,9 +837,10 @@ Layout layout(void* ws, int B, int T, int S, int H, int H_kv, int d_h, bool weig
     return q;
   };
   const size_t rows = static_cast<size_t>(B) * T * H;
-  const int spans = d.few ? (S + kSpanChunk - 1) / kSpanChunk : d.items;
   Layout L;
-  L.span_part = reinterpret_cast<int32_t*>(take(static_cast<size_t>(B) * spans * 4));
+  L.swept = reinterpret_cast<int2*>(
+      take(weights && d.few ? static_cast<size_t>(B) * std::max(d.max_splits, kMaxCluster) * 8 : 0));
+  L.first = reinterpret_cast<int32_t*>(take(d.few ? 0 : static_cast<size_t>(B) * d.items * 4));
   L.stat = reinterpret_cast<float2*>(take(rows * d.max_splits * 8));
   L.part = reinterpret_cast<float*>(take(d.max_splits > 1 ? rows * d.max_splits * d_h * 4 : 0));
   L.logits = reinterpret_cast<float*>(
@@ -737,6 +863,9 @@ cudaError_t launch_cfg(const CUtensorMap& tk, const CUtensorMap& tv, const Param
   auto kern = decode8_kernel<DH, NT>;
   if (cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), Cfg<DH, NT>::SMEM))
     return e;
+  if (p.cluster)
+    return launch_pdl_cluster(kern, grid, dim3(kThreads), Cfg<DH, NT>::SMEM, p.nsplit, stream, tk, tv,
+                              p);
   return launch_pdl(kern, grid, dim3(kThreads), Cfg<DH, NT>::SMEM, stream, tk, tv, p);
 }
 
@@ -761,10 +890,10 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   const long long est = window > 0 ? std::min<long long>(hi, static_cast<long long>(window) + span)
                                    : static_cast<long long>(hi);
   const int tiles = static_cast<int>((est + d.tile - 1) / d.tile) + (window > 0 ? 1 : 0);
-  const int nsplit = d.few ? splits_few(d, tiles, d_h, few_ctas(d_h, T * (H / H_kv))) : splits_many(d, tiles, B * 1LL * T * H * d_h);
   cudaError_t e;
 
   if (!d.few) {
+    const int nsplit = splits_many(d, tiles, B * 1LL * T * H * d_h);
     Flash8Args a;
     a.Q = Q;
     a.K8 = K8;
@@ -774,7 +903,7 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
     a.posc = pos_cache;
     a.qpos = qpos;
     a.pad_lens = pad_lens;
-    a.first = lay.span_part;
+    a.first = lay.first;
     a.stat = lay.stat;
     a.part = lay.part;
     a.rowstat = weight_sum != nullptr ? lay.rowstat : nullptr;
@@ -812,12 +941,8 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
                                  : cudaSuccess;
   }
 
-  const int nchunk = (hi + kSpanChunk - 1) / kSpanChunk;
-  if (window > 0) {
-    e = launch_pdl(span8_kernel, dim3(nchunk, B), dim3(256), 0, stream, pos_cache, qpos, pad_lens, T,
-                   S, end, window, nchunk, lay.span_part);
-    if (e != cudaSuccess) return e;
-  }
+  const Split sp = splits_few(d, tiles, d_h, few_ctas(d_h, T * (H / H_kv)));
+  const int nsplit = sp.n, parts = sp.cluster ? 1 : nsplit;
   // caches [B, S, H_kv, d_h] of bytes: box {128 channels, 1 head, 64 slots, 1 row}
   CUtensorMap tk, tv;
   const uint64_t dims[4] = {static_cast<uint64_t>(d_h), static_cast<uint64_t>(H_kv),
@@ -836,8 +961,8 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   p.posc = pos_cache;
   p.qpos = qpos;
   p.pad_lens = pad_lens;
-  p.span_part = window > 0 ? lay.span_part : nullptr;
-  p.stat = nsplit > 1 || weight_sum != nullptr ? lay.stat : nullptr;
+  p.swept = window > 0 && weight_sum != nullptr ? lay.swept : nullptr;
+  p.stat = parts > 1 || weight_sum != nullptr ? lay.stat : nullptr;
   p.part = lay.part;
   p.logits = weight_sum != nullptr ? lay.logits : nullptr;
   p.O = O;
@@ -851,7 +976,9 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   p.end = end;
   p.window = window;
   p.nsplit = nsplit;
-  p.nchunk = nchunk;
+  p.cluster = sp.cluster ? 1 : 0;
+  // (the last slots that positions without gaps let a window's tokens see)
+  p.late = window > 0 ? tiles : INT_MAX;
   p.status = status;
   const dim3 grid(nsplit, H_kv, B);
   const bool one = T * (H / H_kv) <= 8;
@@ -861,18 +988,18 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   else
     e = one ? launch_cfg<128, 1>(tk, tv, p, grid, stream)
             : launch_cfg<128, 2>(tk, tv, p, grid, stream);
-  if (e != cudaSuccess || (nsplit == 1 && weight_sum == nullptr)) return e;
+  if (e != cudaSuccess || (parts == 1 && weight_sum == nullptr)) return e;
 
   FinishParams q = {};
   q.stat = lay.stat;
   q.part = lay.part;
   q.logits = lay.logits;
   q.weight_sum = weight_sum;
-  q.span_part = p.span_part;
+  q.swept = lay.swept;
   q.pad_lens = pad_lens;
   q.O = O;
   q.o_f16 = o_f16;
-  q.n_rows = nsplit > 1 ? B * T * H : 0;
+  q.n_rows = parts > 1 ? B * T * H : 0;
   q.T = T;
   q.S = S;
   q.H = H;
@@ -880,7 +1007,8 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   q.nb = nb;
   q.end = end;
   q.nsplit = nsplit;
-  q.nchunk = nchunk;
+  q.parts = parts;
+  q.late = p.late;
   q.wchunks = (hi + kWSlots - 1) / kWSlots;
   const long long ctas =
       q.n_rows + (weight_sum != nullptr ? static_cast<long long>(B) * q.wchunks : 0);
