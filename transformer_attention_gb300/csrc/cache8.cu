@@ -197,11 +197,11 @@ __global__ void __launch_bounds__(256) cache8_read_kernel(
 // ~0 for one of the last `recent` slots, in between the weight (NaN below
 // every number, -0 as 0).
 __device__ __forceinline__ uint32_t evict_key(float w, int pos, int s, int first_recent) {
-  if (pos < 0) return 0u;
-  if (s >= first_recent) return 0xFFFFFFFFu;
-  if (w != w) return 1u;
   const uint32_t u = __float_as_uint(w + 0.f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+  k = w != w ? 1u : k;
+  k = s >= first_recent ? 0xFFFFFFFFu : k;
+  return pos < 0 ? 0u : k;
 }
 
 struct SelectParams {
@@ -214,10 +214,10 @@ struct SelectParams {
 };
 
 constexpr int kSelThreads = 1024;
-constexpr int kSelSlots = 8192;      // slots per CTA worth one more CTA in the cluster
+constexpr int kSelSlots = 4096;      // slots per CTA worth one more CTA in the cluster
 constexpr int kSelMaxCluster = 8;
-constexpr int kSelCopies = 4;
-constexpr int kSelKeys = 48 * 1024;  // keys that a CTA keeps in shared memory
+constexpr int kSelKeys = 40 * 1024;  // keys that a CTA keeps in shared memory
+constexpr int kSelHist = 256 * 32;   // digit counts, each lane its own
 
 // One cluster per batch row: the keep-th largest key by four rounds of 8-bit
 // digit counts (each CTA counts its run of slots, the counts are summed over
@@ -226,15 +226,20 @@ constexpr int kSelKeys = 48 * 1024;  // keys that a CTA keeps in shared memory
 // and positions are read once; the keys stay in shared memory between the
 // rounds (a run longer than kSelKeys is read from L2 again).  Bound by the
 // rounds' latency: 131072 slots 20 us on eight CTAs; their 1 MB takes 0.2 us.
+template <bool KEPT>
 __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const SelectParams p) {
   pdl_enter();
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), C = cluster.num_blocks();
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  extern __shared__ uint32_t keys[];
-  __shared__ int hist[2][kSelCopies][256];   // copies: lanes of one digit wait less for each other
-  __shared__ int sum[256], own[256];
+  // Counts [digit][lane]: weights of one magnitude share their first digit,
+  // and lanes adding to one word would wait for each other (131072 slots: 38
+  // us with four copies of the counts).
+  extern __shared__ int hist[];
+  uint32_t* keys = reinterpret_cast<uint32_t*>(hist + kSelHist);
+  __shared__ int tot[2][256];        // this CTA's counts, for its cluster
+  __shared__ int sum[256], own[32];
   __shared__ int wsum[32];
   __shared__ int counts[2];
   __shared__ int found[2][2];        // by round parity: digit, keys above it
@@ -244,16 +249,26 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
   run = (run + kSelThreads - 1) / kSelThreads * kSelThreads;
   const int lo = static_cast<int>(min(static_cast<long long>(p.end), static_cast<long long>(rank) * run));
   const int hi = static_cast<int>(min(static_cast<long long>(p.end), static_cast<long long>(lo) + run));
-  const bool kept_here = run <= kSelKeys;
-  auto fresh_key = [&](int s) { return evict_key(__ldg(w + s), __ldg(pos + s), s, p.first_recent); };
   // Warp w owns the slots w0 .. w1 of the CTA's run, 32 next to each other at
   // a time (a thread reads back only keys that it stored).
   const int seg = run / 32, w0 = lo + warp * seg, w1 = min(hi, w0 + seg);
-  if (kept_here) {
-#pragma unroll 8
-    for (int s = w0 + lane; s < w1; s += 32) keys[s - lo] = fresh_key(s);
+  auto fresh_key = [&](int s) { return evict_key(__ldg(w + s), __ldg(pos + s), s, p.first_recent); };
+  if constexpr (KEPT) {
+    for (int base = w0 + lane; base < w1; base += 8 * 32) {
+      uint32_t k[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) k[i] = base + 32 * i < w1 ? fresh_key(base + 32 * i) : 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (base + 32 * i < w1) keys[base + 32 * i - lo] = k[i];
+    }
   }
-  auto key_at = [&](int s) { return kept_here ? keys[s - lo] : fresh_key(s); };
+  auto key_at = [&](int s) -> uint32_t {
+    if constexpr (KEPT)
+      return keys[s - lo];
+    else
+      return fresh_key(s);
+  };
 
   uint32_t prefix = 0;
   int want = p.keep;                 // rank still to find among keys that match the prefix
@@ -262,28 +277,28 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
   int own_eq = 0;
   for (int round = 0; round < 4; ++round) {
     const int shift = 24 - 8 * round;
-    int (*h)[256] = hist[round & 1];
-    for (int i = tid; i < kSelCopies * 256; i += kSelThreads) (&h[0][0])[i] = 0;
+    int* h = tot[round & 1];
+#pragma unroll
+    for (int i = 0; i < kSelHist / kSelThreads; ++i) hist[i * kSelThreads + tid] = 0;
     __syncthreads();
 #pragma unroll 4
     for (int s = w0 + lane; s < w1; s += 32) {
       const uint32_t key = key_at(s);
       if (key != 0 && (round == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8))))
-        atomicAdd(&h[lane % kSelCopies][(key >> shift) & 255u], 1);
+        atomicAdd(&hist[((key >> shift) & 255u) * 32 + lane], 1);
     }
     __syncthreads();
-    if (tid < 256) {
-      int n = 0;
 #pragma unroll
-      for (int i = 0; i < kSelCopies; ++i) n += h[i][tid];
-      h[0][tid] = own[tid] = n;
+    for (int i = 0; i < 8; ++i) {
+      const int d = warp * 8 + i, n = __reduce_add_sync(0xffffffffu, hist[d * 32 + lane]);
+      if (lane == 0) h[d] = n;
     }
     cluster.sync();
     if (tid < 256) {
       int n = 0;
 #pragma unroll
       for (int r = 0; r < kSelMaxCluster; ++r)
-        if (r < C) n += cluster.map_shared_rank(&h[0][0], r)[tid];
+        if (r < C) n += cluster.map_shared_rank(h, r)[tid];
       sum[tid] = n;
     }
     __syncthreads();
@@ -322,11 +337,11 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int k = 255 - 8 * lane - i;
-        if (k > d) gt += own[k];
+        if (k > d) gt += h[k];
       }
       gt = __reduce_add_sync(0xffffffffu, gt);
       own_gt += gt;
-      own_eq = d >= 0 ? own[d] : 0;
+      own_eq = d >= 0 ? h[d] : 0;
     }
     __syncthreads();
     if (f[0] < 0) {                  // (only in round 0)
@@ -381,22 +396,33 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
   __syncthreads();
   gt0 += __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0);
   eq0 += __reduce_add_sync(0xffffffffu, lane < warp ? own[lane] : 0);
-#pragma unroll 2
-  for (int base = w0; base < w1; base += 32) {
-    const int s = base + lane;
-    const uint32_t key = s < w1 ? key_at(s) : 0u;
-    const bool g = s < w1 && key > thr, e = s < w1 && key == thr && want > 0;
-    const unsigned bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
-    const unsigned below = (1u << lane) - 1u;
-    const int ng = gt0 + __popc(bg & below), ne = eq0 + __popc(be & below);
-    if (g || (e && ne < want)) {
-      const int d = ng + min(ne, want);
-      kept[d] = s;
-      pos_dst[d] = __ldg(pos + s);
-      w_dst[d] = __ldg(w + s);
+  const unsigned below = (1u << lane) - 1u;
+  for (int base = w0; base < w1; base += 4 * 32) {
+    // (positions and weights of four steps at once, kept or not)
+    float ws[4];
+    int ps[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = min(base + 32 * i + lane, w1 - 1);
+      ws[i] = __ldg(w + s);
+      ps[i] = __ldg(pos + s);
     }
-    gt0 += __popc(bg);
-    eq0 += __popc(be);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = base + 32 * i + lane;
+      const uint32_t key = s < w1 ? key_at(s) : 0u;
+      const bool g = s < w1 && key > thr, e = s < w1 && key == thr && want > 0;
+      const unsigned bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
+      const int ng = gt0 + __popc(bg & below), ne = eq0 + __popc(be & below);
+      if (g || (e && ne < want)) {
+        const int d = ng + min(ne, want);
+        kept[d] = s;
+        pos_dst[d] = ps[i];
+        w_dst[d] = ws[i];
+      }
+      gt0 += __popc(bg);
+      eq0 += __popc(be);
+    }
   }
   for (int d = n_kept + rank * kSelThreads + tid; d < p.keep; d += C * kSelThreads) {
     kept[d] = -1;
@@ -577,10 +603,12 @@ cudaError_t launch_cache8_evict(const void* K8, const void* V8, const float* K_s
   int cl = 1;
   while (cl < kSelMaxCluster && static_cast<long long>(cl) * kSelSlots < end) cl *= 2;
   const int run = ((end + cl - 1) / cl + kSelThreads - 1) / kSelThreads * kSelThreads;
-  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(cache8_select_kernel), kSelKeys * 4);
+  const bool kept_keys = run <= kSelKeys;
+  const auto kern = kept_keys ? cache8_select_kernel<true> : cache8_select_kernel<false>;
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), (kSelHist + kSelKeys) * 4);
   if (e != cudaSuccess) return e;
-  e = launch_pdl_cluster(cache8_select_kernel, dim3(cl, B), dim3(kSelThreads),
-                         run <= kSelKeys ? static_cast<size_t>(run) * 4 : 0, cl, stream, q);
+  e = launch_pdl_cluster(kern, dim3(cl, B), dim3(kSelThreads),
+                         static_cast<size_t>(kSelHist + (kept_keys ? run : 0)) * 4, cl, stream, q);
   if (e != cudaSuccess) return e;
   MoveParams p;
   p.K8 = static_cast<const uint8_t*>(K8);
