@@ -215,20 +215,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
   const int hi = tl.hi;
   const int late0 = min(tl.k1, tl.k0 + split * tl.per_late);
   const int n_late = min(tl.k1, late0 + tl.per_late) - late0;
-  // Q fragments: k columns {2c, 2c+1, 2c+8, 2c+9} of a 16-channel chunk are
-  // the channels 4c .. 4c+3, row n = lane / 4.
-#pragma unroll 4
-  for (int i = tid; i < C::NC * NT * 32; i += kThreads) {
-    const int l = i & 31, nt = (i >> 5) % NT, ch = (i >> 5) / NT;
-    const int r = nt * 8 + (l >> 2);
-    uint2 q = make_uint2(0, 0);
-    if (r < R) {
-      const int t = r / G, h = j * G + r % G;
-      q = __ldg(reinterpret_cast<const uint2*>(
-          p.Q + ((static_cast<size_t>(b) * p.T + t) * p.H + h) * DH + ch * 16 + (l & 3) * 4));
-    }
-    qf[i] = q;
-  }
   __syncthreads();
   // Tile i of this CTA: its late ones, then the early ones that it found.
   int early0 = 0, n_tiles = n_late;
@@ -284,7 +270,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
     return;
   }
 
-  // ---------------- consumers: warp w takes slots 16w .. 16w+15 of every tile
+  // ---------------- consumers
+  // Q fragments (while the first copies are under way): k columns {2c, 2c+1, 2c+8, 2c+9} of a 16-channel chunk are
+  // the channels 4c .. 4c+3, row n = lane / 4.
+#pragma unroll 4
+  for (int i = tid; i < C::NC * NT * 32; i += kCWarps * 32) {
+    const int l = i & 31, nt = (i >> 5) % NT, ch = (i >> 5) / NT;
+    const int r = nt * 8 + (l >> 2);
+    uint2 q = make_uint2(0, 0);
+    if (r < R) {
+      const int t = r / G, h = j * G + r % G;
+      q = __ldg(reinterpret_cast<const uint2*>(
+          p.Q + ((static_cast<size_t>(b) * p.T + t) * p.H + h) * DH + ch * 16 + (l & 3) * 4));
+    }
+    qf[i] = q;
+  }
+  named_barrier(1, kCWarps * 32);
+  // Warp w takes slots 16w .. 16w+15 of every tile
   // Rows of this thread: nt * 8 + 2c + e; slots g and g + 8 of the warp's 16.
   int lim[NT][2], plo[NT][2], phi[NT][2];
 #pragma unroll
@@ -627,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
 // CTAs [0, n_rows): merge the parts of one query row.  The others: weights of
 // kWSlots slots of one batch row, every query row's logits once.
 constexpr int kWSlots = 512;
+constexpr int kWRows = 16;
 
 struct FinishParams {
   const float2* stat;
@@ -644,8 +647,8 @@ template <int DH>
 __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
   pdl_enter();
   __shared__ float fw[kMaxSplits];
-  __shared__ float2 rs[256];
-  __shared__ int last[256];
+  __shared__ float2 rs[2][kWRows];
+  __shared__ int last[2][kWRows];
   __shared__ float red[2][8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (blockIdx.x < static_cast<unsigned>(p.n_rows)) {
@@ -701,47 +704,59 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
     seen = k >= e.x && k < e.y;
   }
   const float* lg = p.logits + static_cast<size_t>(b) * rows * S64 + s;
-  float2 acc = make_float2(0.f, 0.f);
-  for (int r0 = 0; r0 < rows; r0 += 256) {
-    const int n = min(256, rows - r0);
-    if (r0 > 0) __syncthreads();
-    // (max, 1 / sum) of the query rows over their parts, a warp each, and the
-    // last slot whose logit the first launch wrote (a valid token's own)
-    for (int i = warp; i < n; i += 8) {
-      const int j = (r0 + i) / R, q = (r0 + i) % R, t = q / G;
-      const float2* st =
-          p.stat + ((static_cast<size_t>(b) * p.T + t) * p.H + j * G + q % G) * p.parts;
+  float* out = p.weight_sum + static_cast<size_t>(b) * p.S;
+  float2 old = make_float2(0.f, 0.f), acc = make_float2(0.f, 0.f);
+  if (seen) {
+    old.x = out[s];
+    if (s + 1 < p.S) old.y = out[s + 1];
+  }
+  for (int r0 = 0, par = 0; r0 < rows; r0 += kWRows, par ^= 1) {
+    const int n = min(kWRows, rows - r0);
+    // The rows' logits (two slots of one tile per thread; loaded without
+    // asking whether they count) are under way while a warp each finds the
+    // rows' (max, 1 / sum) over their parts, and the last slot whose logit the
+    // first launch wrote (a valid token's own).
+    float2 x[kWRows];
+#pragma unroll
+    for (int i = 0; i < kWRows; ++i)
+      x[i] = seen && i < n ? __ldg(reinterpret_cast<const float2*>(lg + (r0 + i) * S64))
+                           : make_float2(0.f, 0.f);
+    for (int i = warp; i < kWRows; i += 8) {
       float M = -INFINITY, L = 0.f;
-      for (int k = lane; k < p.parts; k += 32) M = fmaxf(M, st[k].x);
+      int t = valid;
+      if (i < n) {
+        const int j = (r0 + i) / R, q = (r0 + i) % R;
+        t = q / G;
+        const float2* st =
+            p.stat + ((static_cast<size_t>(b) * p.T + t) * p.H + j * G + q % G) * p.parts;
+        for (int k = lane; k < p.parts; k += 32) M = fmaxf(M, st[k].x);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      if (M != -INFINITY)
-        for (int k = lane; k < p.parts; k += 32) L = fmaf(ex2(st[k].x - M), st[k].y, L);
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        if (M != -INFINITY)
+          for (int k = lane; k < p.parts; k += 32) L = fmaf(ex2(st[k].x - M), st[k].y, L);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      }
       if (lane == 0) {
-        rs[i] = make_float2(M == -INFINITY ? 0.f : M, M != -INFINITY && L != 0.f ? 1.f / L : 0.f);
-        last[i] = t < valid ? p.end + t : -1;
+        rs[par][i] =
+            make_float2(M == -INFINITY ? 0.f : M, M != -INFINITY && L != 0.f ? 1.f / L : 0.f);
+        last[par][i] = t < valid ? p.end + t : -1;
       }
     }
     __syncthreads();
-    // (two slots of one tile per thread; the logits are loaded without asking
-    // whether they count, so that eight rows' are in flight)
-    if (seen) {
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float2 x = __ldg(reinterpret_cast<const float2*>(lg + (r0 + i) * S64));
-        const float2 st = rs[i];
-        const int lim = last[i];
-        const float e0 = ex2(x.x - st.x), e1 = ex2(x.y - st.x);
-        acc.x = fmaf(s <= lim ? e0 : 0.f, st.y, acc.x);
-        acc.y = fmaf(s + 1 <= lim ? e1 : 0.f, st.y, acc.y);
-      }
+#pragma unroll
+    for (int i = 0; i < kWRows; ++i) {
+      const float2 st = rs[par][i];
+      const int lim = last[par][i];
+      const float e0 = ex2(x[i].x - st.x), e1 = ex2(x[i].y - st.x);
+      acc.x = fmaf(s <= lim ? e0 : 0.f, st.y, acc.x);
+      acc.y = fmaf(s + 1 <= lim ? e1 : 0.f, st.y, acc.y);
     }
   }
-  float* out = p.weight_sum + static_cast<size_t>(b) * p.S;
-  if (acc.x != 0.f) out[s] += acc.x;
-  if (acc.y != 0.f) out[s + 1] += acc.y;
+  if (seen) {
+    if (acc.x != 0.f) out[s] = old.x + acc.x;
+    if (acc.y != 0.f) out[s + 1] = old.y + acc.y;
+  }
 }
 
 // ---------------------------------------------------------------- planning
