@@ -636,7 +636,6 @@ struct FinishParams {
   const float* part;
   const float* logits;
   float* weight_sum;
-  float2* rowstat;            // many rows: [B, H_kv, T*G] of the merged rows, or null
   const int2* swept;          // as in Params
   const int32_t* pad_lens;
   void* O;
@@ -673,12 +672,6 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
     L = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) L += red[1][i];
-    if (tid == 0 && p.rowstat != nullptr) {
-      const int h = row % p.H, G = p.H / p.H_kv;
-      const size_t t = row / p.H % p.T, b = row / p.H / p.T;
-      p.rowstat[((b * p.H_kv + h / G) * p.T + t) * G + h % G] =
-          row_stat(M, L, M != -INFINITY && L != 0.f);
-    }
     const float* base = p.part + row * p.nsplit * DH;
     for (int ch = tid; ch < DH; ch += 256) {
       float acc = 0.f;
@@ -760,27 +753,14 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
 }
 
 // ---------------------------------------------------------------- planning
-// Few rows (decode8_kernel) or many (the tcgen05 kernel), and how far the
-// slots may be split: as many CTAs as a few rounds of the SMs take.
-struct Plan {
-  bool few;
-  int items;                  // query tiles of a (row, kv head)
-  long long units;            // (row, kv head, item)
-  int tile, max_splits;
-};
+// Few rows (decode8_kernel), whose slots are split over a bounded number of
+// CTAs, or many (launch_flash8).
+bool few_rows(int T, int G) { return static_cast<long long>(T) * G <= kFewRows; }
 
-Plan plan_rows(int B, int T, int S, int H, int H_kv, int d_h) {
-  const int G = H / H_kv;
-  Plan d;
-  d.few = static_cast<long long>(T) * G <= kFewRows;
-  const int span = flash8_span(d_h, G);
-  d.items = d.few ? 1 : (T + span - 1) / span;
-  d.units = static_cast<long long>(B) * H_kv * d.items;
-  d.tile = d.few ? kTile : 2 * kTile;
-  const long long by_cap = std::max<long long>(1, (d.few ? 1024 : 512) / d.units);
-  const int tiles = (S + d.tile - 1) / d.tile;
-  d.max_splits = static_cast<int>(std::min<long long>({kMaxSplits, by_cap, tiles}));
-  return d;
+int max_splits(int B, int S, int H_kv) {
+  const long long units = static_cast<long long>(B) * H_kv;
+  return static_cast<int>(std::min<long long>(
+      {kMaxSplits, std::max<long long>(1, 1024 / units), c8_blocks(S)}));
 }
 
 // Splits of few rows, bound by HBM: counted in the time a tile takes at the
@@ -794,16 +774,16 @@ struct Split {
   int n;
   bool cluster;
 };
-Split splits_few(const Plan& d, int tiles, int d_h, int ctas_per_sm) {
+Split splits_few(long long units, int most, int tiles, int d_h, int ctas_per_sm) {
   const int slots = ctas_per_sm * num_sms(), us = d_h == 256 ? 200 : 400;
   const int full = d_h == 256 ? 224 : slots;
   Split best_of = {1, false};
   long long best = LLONG_MAX;
-  for (int n = 1; n <= std::max(std::min(d.max_splits, tiles), kMaxCluster); ++n) {
+  for (int n = 1; n <= std::max(std::min(most, tiles), kMaxCluster); ++n) {
     const bool cluster = n == 2 || n == 4 || n == kMaxCluster;
-    if (!cluster && n > std::min(d.max_splits, tiles)) continue;
-    const long long waves = (d.units * n + slots - 1) / slots, per = (tiles + n - 1) / n;
-    const long long cost = std::max(d.units * tiles, waves * per * full) + waves * 2 * us +
+    if (!cluster && n > std::min(most, tiles)) continue;
+    const long long waves = (units * n + slots - 1) / slots, per = (tiles + n - 1) / n;
+    const long long cost = std::max(units * tiles, waves * per * full) + waves * 2 * us +
                            (n > 1 && !cluster ? 7 * us / 2 + n * us / 20 : 0);
     if (cost < best) {
       best = cost;
@@ -813,28 +793,10 @@ Split splits_few(const Plan& d, int tiles, int d_h, int ctas_per_sm) {
   return best_of;
 }
 
-// Splits of many rows, bound by the tensor cores: a CTA's tiles (about a
-// microsecond each, 6.5 MB of HBM time), a start and an end worth three, and
-// the parts' bytes (4 per element out and back).
-int splits_many(const Plan& d, int tiles, long long elements) {
-  const double part_tiles = static_cast<double>(elements) * 8.0 / 6.5e6;
-  int nsplit = 1;
-  double best = 1e300;
-  for (int n = 1; n <= std::min(d.max_splits, tiles); ++n) {
-    const double waves = static_cast<double>((d.units * n + num_sms() - 1) / num_sms());
-    const double cost = waves * ((tiles + n - 1) / n + 3) + (n > 1 ? n * part_tiles : 0.0);
-    if (cost < best) {
-      best = cost;
-      nsplit = n;
-    }
-  }
-  return nsplit;
-}
-
 struct Layout {
   int2* swept;          // few: [B, splits]
   int32_t* first;       // many: [B, items]
-  float2* stat;
+  float2* stat;         // few: [B*T*H, splits], many: parts of cut units
   float* part;
   float* logits;        // few rows with weights
   float2* rowstat;      // many rows with weights
@@ -843,25 +805,27 @@ struct Layout {
 };
 
 Layout layout(void* ws, int B, int T, int S, int H, int H_kv, int d_h, bool weights) {
-  const Plan d = plan_rows(B, T, S, H, H_kv, d_h);
+  const bool few = few_rows(T, H / H_kv);
   uint8_t* w = static_cast<uint8_t*>(ws);
   size_t at = 0;
-  auto take = [&](size_t n) {
+  auto take = [&](bool wanted, size_t n) {
     uint8_t* q = w + at;
-    at += (n + 255) / 256 * 256;
+    at += wanted ? (n + 255) / 256 * 256 : 0;
     return q;
   };
   const size_t rows = static_cast<size_t>(B) * T * H;
+  const int splits = max_splits(B, S, H_kv), span = flash8_span(d_h, H / H_kv);
+  const size_t items = (static_cast<size_t>(T) + span - 1) / span;
+  const size_t parts = few ? rows * splits : flash8_part_rows(B, T, S, H, H_kv, d_h);
   Layout L;
   L.swept = reinterpret_cast<int2*>(
-      take(weights && d.few ? static_cast<size_t>(B) * std::max(d.max_splits, kMaxCluster) * 8 : 0));
-  L.first = reinterpret_cast<int32_t*>(take(d.few ? 0 : static_cast<size_t>(B) * d.items * 4));
-  L.stat = reinterpret_cast<float2*>(take(rows * d.max_splits * 8));
-  L.part = reinterpret_cast<float*>(take(d.max_splits > 1 ? rows * d.max_splits * d_h * 4 : 0));
-  L.logits = reinterpret_cast<float*>(
-      take(weights && d.few ? rows * c8_blocks(S) * kTile * 4 : 0));
-  L.rowstat = reinterpret_cast<float2*>(take(weights && !d.few ? rows * 8 : 0));
-  L.wpart = reinterpret_cast<float*>(take(weights && !d.few ? weights8_part_floats() * 4 : 0));
+      take(few && weights, static_cast<size_t>(B) * std::max(splits, kMaxCluster) * 8));
+  L.first = reinterpret_cast<int32_t*>(take(!few, B * items * 4));
+  L.stat = reinterpret_cast<float2*>(take(true, parts * 8));
+  L.part = reinterpret_cast<float*>(take(!few || splits > 1, parts * d_h * 4));
+  L.logits = reinterpret_cast<float*>(take(few && weights, rows * c8_blocks(S) * kTile * 4));
+  L.rowstat = reinterpret_cast<float2*>(take(!few && weights, rows * 8));
+  L.wpart = reinterpret_cast<float*>(take(!few && weights, weights8_part_floats() * 4));
   L.bytes = at;
   return L;
 }
@@ -897,18 +861,11 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
                                      float* weight_sum, int B, int T, int S, int end, int H,
                                      int H_kv, int d_h, int window, void* ws, cudaStream_t stream,
                                      int* status) {
-  const Plan d = plan_rows(B, T, S, H, H_kv, d_h);
   const Layout lay = layout(ws, B, T, S, H, H_kv, d_h, weight_sum != nullptr);
   const int hi = end + T, nb = c8_blocks(S), o_f16 = o_dtype == kF16 ? 1 : 0;
-
-  const int span = d.few ? T : flash8_span(d_h, H / H_kv);
-  const long long est = window > 0 ? std::min<long long>(hi, static_cast<long long>(window) + span)
-                                   : static_cast<long long>(hi);
-  const int tiles = static_cast<int>((est + d.tile - 1) / d.tile) + (window > 0 ? 1 : 0);
   cudaError_t e;
 
-  if (!d.few) {
-    const int nsplit = splits_many(d, tiles, B * 1LL * T * H * d_h);
+  if (!few_rows(T, H / H_kv)) {
     Flash8Args a;
     a.Q = Q;
     a.K8 = K8;
@@ -919,9 +876,9 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
     a.qpos = qpos;
     a.pad_lens = pad_lens;
     a.first = lay.first;
-    a.stat = lay.stat;
-    a.part = lay.part;
     a.rowstat = weight_sum != nullptr ? lay.rowstat : nullptr;
+    a.pstat = lay.stat;
+    a.part = lay.part;
     a.O = O;
     a.o_f16 = o_f16;
     a.B = B;
@@ -932,31 +889,17 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
     a.H_kv = H_kv;
     a.d_h = d_h;
     a.window = window;
-    a.nsplit = nsplit;
     a.status = status;
     e = launch_flash8(a, stream);
-    if (e != cudaSuccess) return e;
-    if (nsplit > 1) {
-      FinishParams q = {};
-      q.stat = lay.stat;
-      q.part = lay.part;
-      q.O = O;
-      q.o_f16 = o_f16;
-      q.n_rows = B * T * H;
-      q.nsplit = nsplit;
-      q.rowstat = a.rowstat;
-      q.T = T;
-      q.H = H;
-      q.H_kv = H_kv;
-      e = launch_pdl(d_h == 256 ? finish8_kernel<256> : finish8_kernel<128>,
-                     dim3(static_cast<unsigned>(q.n_rows)), dim3(256), 0, stream, q);
-      if (e != cudaSuccess) return e;
-    }
-    return weight_sum != nullptr ? launch_weights8(a, lay.wpart, weight_sum, stream)
-                                 : cudaSuccess;
+    if (e != cudaSuccess || weight_sum == nullptr) return e;
+    return launch_weights8(a, lay.wpart, weight_sum, stream);
   }
 
-  const Split sp = splits_few(d, tiles, d_h, few_ctas(d_h, T * (H / H_kv)));
+  const long long est = window > 0 ? std::min<long long>(hi, static_cast<long long>(window) + T)
+                                   : static_cast<long long>(hi);
+  const int tiles = static_cast<int>((est + kTile - 1) / kTile) + (window > 0 ? 1 : 0);
+  const Split sp = splits_few(static_cast<long long>(B) * H_kv, max_splits(B, S, H_kv), tiles, d_h,
+                              few_ctas(d_h, T * (H / H_kv)));
   const int nsplit = sp.n, parts = sp.cluster ? 1 : nsplit;
   // caches [B, S, H_kv, d_h] of bytes: box {128 channels, 1 head, 64 slots, 1 row}
   CUtensorMap tk, tv;

@@ -29,8 +29,12 @@
 //
 // Slots hidden from the whole CTA become zeros in the conversion, so that
 // what they hold (a NaN, say) cannot reach O through a zero probability.
-// The slots of a query tile are split over CTAs when there are few tiles;
-// finish8_kernel (cache8_attn.cu) merges the parts.
+// A unit is a query tile (pair) of one kv head and batch row.  Whole rounds of
+// the SMs take a unit per CTA; the units left over, fewer than the SMs, are
+// cut along their slots (plan8), into equal parts where several fit, else into
+// a large part each and small ones that the remaining SMs take one after
+// another; flash8_merge_kernel adds the parts.  (128 units on 152 SMs: 410 us
+// uncut for a 1024-token chunk over 32768 slots, 27B-shaped.)
 #include <algorithm>
 #include <climits>
 
@@ -110,11 +114,13 @@ struct Params {
   const int32_t* qpos;
   const int32_t* pad_lens;
   const int32_t* first;       // [B, items] first visible slot of each item (local layers) or null
-  float2* stat;
-  float* part;
-  float2* rowstat;
+  float2* rowstat;            // [B, H_kv, T*G] (max, 1 / sum) of every row, or null
+  float2* pstat;              // [cut units, parts, NQ * 128] (max, sum)
+  float* part;                // [cut units, parts, NQ * 128, DH] unnormalised
   void* O;
-  int o_f16, B, T, S, H, H_kv, nb, end, window, nsplit, items;
+  int o_f16, B, T, S, H, H_kv, nb, end, window, items;
+  int whole, cut, parts;      // units in one piece, units cut, into how many parts
+  float first_part;           // share of a cut unit's tiles in its first part
   int* status;
 };
 
@@ -171,14 +177,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     return;
   }
 
-  // Item: latest tokens (most slots on a causal prompt) first, the items of a
-  // kv head next to each other so that they share its bytes in L2.
-  int idx = blockIdx.x;
-  const int item = p.items - 1 - idx % p.items;
-  idx /= p.items;
-  const int split = idx % p.nsplit;
-  idx /= p.nsplit;
-  const int j = idx % p.H_kv, b = idx / p.H_kv;
+  // CTAs: the whole units, the first parts of the cut ones, the other parts.
+  // Units: the items of a kv head next to each other, so that they share its
+  // bytes in L2, the latest tokens (most slots on a causal prompt) first.
+  const int head_units = p.whole + p.cut, rest = static_cast<int>(blockIdx.x) - head_units;
+  const int unit = rest < 0 ? blockIdx.x : p.whole + rest % p.cut;
+  const int pt = rest < 0 ? 0 : 1 + rest / p.cut;           // part
+  const bool whole = unit < p.whole;
+  const int item = p.items - 1 - unit % p.items;
+  const int bj = unit / p.items, j = bj % p.H_kv, b = bj / p.H_kv;
   const int t0 = item * C::NQ * C::TQ;
   const int valid = min(p.T, p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0));
   const int t_end = min(t0 + C::NQ * C::TQ, valid);          // past the last valid token
@@ -186,10 +193,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int hi = t_end > t0 ? p.end + t_end : 0;
   int lo = p.first != nullptr ? p.first[static_cast<size_t>(b) * p.items + item] : 0;
   lo = min(lo, hi) / kC8Block * kC8Block;
-  int n_tiles = (hi - lo + BN - 1) / BN;
-  const int per = (n_tiles + p.nsplit - 1) / p.nsplit;
-  const int first_tile = min(split * per, n_tiles);
-  n_tiles = min(per, n_tiles - first_tile);
+  int n_tiles = (hi - lo + BN - 1) / BN, first_tile = 0;
+  if (!whole) {
+    // part 0 has its share, the others the rest evenly
+    const int n0 = min(n_tiles, static_cast<int>(ceilf(p.first_part * n_tiles)));
+    const int left = n_tiles - n0, others = p.parts - 1;
+    first_tile = pt == 0 ? 0 : n0 + left * (pt - 1) / others;
+    n_tiles = pt == 0 ? n0 : left * pt / others - left * (pt - 1) / others;
+  }
   const int s_base = lo + first_tile * BN;
 
   if (tid == 0) {
@@ -643,16 +654,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
       }
       const size_t orow = (static_cast<size_t>(b) * p.T + t) * p.H + h;
+      const size_t prow = (static_cast<size_t>(unit - p.whole) * p.parts + pt) * (C::NQ * BM) + e * BM + r;
       const bool have = row_valid && n_tiles > 0 && l != 0.f;
-      if (ok && t < p.T) {
-        if (p.nsplit > 1)
-          p.stat[orow * p.nsplit + split] =
-              have ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
-        else if (p.rowstat != nullptr)
-          p.rowstat[((static_cast<size_t>(b) * p.H_kv + j) * p.T + t) * G + r % G] =
-              row_stat(m_used, l, have);
-      }
-      const float inv = have ? (p.nsplit == 1 ? 1.f / l : 1.f) : 0.f;
+      if (ok && !whole)
+        p.pstat[prow] = have ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
+      else if (ok && t < p.T && p.rowstat != nullptr)
+        p.rowstat[((static_cast<size_t>(b) * p.H_kv + j) * p.T + t) * G + r % G] =
+            row_stat(m_used, l, have);
+      const float inv = have ? 1.f / l : 0.f;
       if (ok) {
 #pragma unroll 1
         for (int c = 0; c < DH / 32; ++c) {
@@ -661,18 +670,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_ld32(o_base + c * 32, ro);
             tmem_ld_wait(ro);
           }
-          if (t < p.T) {
-            if (p.nsplit == 1) {
+          if (whole) {
+            if (t < p.T)
               store_row32(static_cast<uint16_t*>(p.O) + orow * DH + c * 32, ro, inv, have, p.o_f16);
-            } else {
-              float4* d = reinterpret_cast<float4*>(p.part + (orow * p.nsplit + split) * DH + c * 32);
+          } else {
+            float4* d = reinterpret_cast<float4*>(p.part + prow * DH + c * 32);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                d[k] = have ? make_float4(__uint_as_float(ro[4 * k]), __uint_as_float(ro[4 * k + 1]),
-                                          __uint_as_float(ro[4 * k + 2]),
-                                          __uint_as_float(ro[4 * k + 3]))
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+            for (int k = 0; k < 8; ++k)
+              d[k] = have ? make_float4(__uint_as_float(ro[4 * k]), __uint_as_float(ro[4 * k + 1]),
+                                        __uint_as_float(ro[4 * k + 2]),
+                                        __uint_as_float(ro[4 * k + 3]))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
           }
         }
         tc_fence_before();
@@ -683,6 +691,60 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
+  }
+}
+
+// The parts of the cut units: CTA (u, y) adds those of 16 rows of unit u.
+template <int DH, int G>
+__global__ void __launch_bounds__(256) flash8_merge_kernel(const Params p) {
+  pdl_enter();
+  using C = Cfg<DH, G>;
+  constexpr int ROWS = 16;
+  const int unit = p.whole + blockIdx.x;
+  const int item = p.items - 1 - unit % p.items;
+  const int bj = unit / p.items, j = bj % p.H_kv, b = bj / p.H_kv;
+  for (int i = threadIdx.x / 32; i < ROWS; i += 8) {
+    const int row = blockIdx.y * ROWS + i, lane = threadIdx.x & 31;   // of the query tiles
+    const int e = row / BM, r = row % BM;
+    const int t = item * C::NQ * C::TQ + e * C::TQ + r / G;
+    if (t >= p.T) continue;
+    auto at = [&](int c) -> size_t {
+      return (static_cast<size_t>(blockIdx.x) * p.parts + c) * (C::NQ * BM) + row;
+    };
+    float M = -INFINITY, L = 0.f;
+    for (int c = 0; c < p.parts; ++c) M = fmaxf(M, p.pstat[at(c)].x);
+    float4 acc[DH / 128];
+#pragma unroll
+    for (int v = 0; v < DH / 128; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (M != -INFINITY) {
+#pragma unroll 2
+      for (int c = 0; c < p.parts; ++c) {
+        const float2 st = p.pstat[at(c)];
+        const float f = ex2(st.x - M);
+        L = fmaf(f, st.y, L);
+        const float4* src = reinterpret_cast<const float4*>(p.part + at(c) * DH);
+#pragma unroll
+        for (int v = 0; v < DH / 128; ++v) {
+          const float4 o = __ldg(src + v * 32 + lane);
+          acc[v].x = fmaf(f, o.x, acc[v].x);
+          acc[v].y = fmaf(f, o.y, acc[v].y);
+          acc[v].z = fmaf(f, o.z, acc[v].z);
+          acc[v].w = fmaf(f, o.w, acc[v].w);
+        }
+      }
+    }
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    const size_t orow = (static_cast<size_t>(b) * p.T + t) * p.H + j * G + r % G;
+#pragma unroll
+    for (int v = 0; v < DH / 128; ++v) {
+      const float x0 = acc[v].x * inv, x1 = acc[v].y * inv, x2 = acc[v].z * inv, x3 = acc[v].w * inv;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * DH + v * 128 + lane * 4) =
+          p.o_f16 ? make_uint2(pack_half2(x0, x1), pack_half2(x2, x3))
+                  : make_uint2(pack_bf162(x0, x1), pack_bf162(x2, x3));
+    }
+    if (lane == 0 && p.rowstat != nullptr)
+      p.rowstat[((static_cast<size_t>(b) * p.H_kv + j) * p.T + t) * G + r % G] =
+          row_stat(M, L, L != 0.f);
   }
 }
 
@@ -756,23 +818,82 @@ cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
   // The softmax warpgroups' increases wait for what the others give up:
   // launch only when the split fits the CTA's allocation.
   if (regs < REGS_LAUNCH) return cudaErrorInvalidConfiguration;
-  const long long ctas = static_cast<long long>(p.items) * p.nsplit * p.H_kv * p.B;
+  const long long ctas = p.whole + static_cast<long long>(p.cut) * p.parts;
   if (ctas > INT_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), C::SMEM, stream, tq, tk, tv, p);
+  cudaError_t e =
+      launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), C::SMEM, stream, tq, tk, tv, p);
+  if (e != cudaSuccess || p.cut == 0) return e;
+  return launch_pdl(flash8_merge_kernel<DH, G>, dim3(p.cut, C::NQ * BM / 16), dim3(256), 0, stream, p);
+}
+
+// How many units stay whole, and the cut of the others (fewer than the SMs),
+// where the parts' rounds end earliest: counted in KV tiles, with a start and
+// an end of a CTA worth kStartTiles and the merge worth as much.
+constexpr int kStartTiles = 3;
+constexpr int kMaxCutParts = 320;            // parts that the workspace has room for
+
+struct Plan8 {
+  int whole, cut, parts;
+  float first_part;
+};
+
+Plan8 plan8(long long units, int tiles, int sms) {
+  const int rest = static_cast<int>(units % sms);
+  Plan8 uncut = {static_cast<int>(units), 0, 1, 1.f};
+  if (rest == 0) return uncut;
+  const int one = tiles + kStartTiles;                      // a round of whole units
+  int best = one, parts = 1;
+  float first = 1.f;
+  // equal parts, all in one round
+  const int k = std::min(sms / rest, tiles);
+  if (k >= 2 && (tiles + k - 1) / k + 2 * kStartTiles < best) {
+    best = (tiles + k - 1) / k + 2 * kStartTiles;
+    parts = k;
+    first = 1.f / k;
+  }
+  // a large part each, the small ones in q rounds on the other SMs
+  if (k < 2) {
+    const int q = (rest + sms - rest - 1) / (sms - rest);
+    const int small = std::max(1, (tiles - (q - 1) * kStartTiles) / (q + 1));
+    const int end = std::max(tiles - small + kStartTiles, q * (small + kStartTiles)) + kStartTiles;
+    if (small < tiles && end < best) {
+      best = end;
+      parts = 2;
+      first = static_cast<float>(tiles - small) / static_cast<float>(tiles);
+    }
+  }
+  if (parts == 1 || rest * parts > kMaxCutParts) return uncut;
+  return {static_cast<int>(units - rest), rest, parts, first};
 }
 
 }  // namespace
 
 int flash8_span(int d_h, int G) { return (d_h == 128 ? 2 : 1) * (BM / G); }
 
+size_t flash8_part_rows(int B, int T, int S, int H, int H_kv, int d_h) {
+  const int span = flash8_span(d_h, H / H_kv);
+  const long long units = static_cast<long long>(B) * H_kv * ((T + span - 1) / span);
+  const long long most = units * ((S + BN - 1) / BN);
+  return static_cast<size_t>(std::min<long long>(kMaxCutParts, most)) * (d_h == 128 ? 2 : 1) * BM;
+}
+
 cudaError_t launch_flash8(const Flash8Args& a, cudaStream_t stream) {
   const int G = a.H / a.H_kv;
   const int span = flash8_span(a.d_h, G), items = (a.T + span - 1) / span;
+  const int hi = a.end + a.T;
   if (a.window > 0) {
     cudaError_t e = launch_pdl(first8_kernel, dim3(items, a.B), dim3(1024), 0, stream, a.posc,
                                a.qpos, a.pad_lens, a.T, a.S, a.end, a.window, span, items, a.first);
     if (e != cudaSuccess) return e;
   }
+  const long long units = static_cast<long long>(a.B) * a.H_kv * items;
+  if (units > (1 << 30)) return cudaErrorInvalidValue;
+  // (a local item's slots: its window and its own tokens, from a block border)
+  int tiles = (hi + BN - 1) / BN;
+  if (a.window > 0)
+    tiles = static_cast<int>(std::min<long long>(
+        tiles, (static_cast<long long>(a.window) + span + kC8Block + BN - 1) / BN));
+  const Plan8 plan = plan8(units, tiles, num_sms());
   Params p;
   p.K8 = static_cast<const uint8_t*>(a.K8);
   p.V8 = static_cast<const uint8_t*>(a.V8);
@@ -782,9 +903,9 @@ cudaError_t launch_flash8(const Flash8Args& a, cudaStream_t stream) {
   p.qpos = a.qpos;
   p.pad_lens = a.pad_lens;
   p.first = a.window > 0 ? a.first : nullptr;
-  p.stat = a.stat;
-  p.part = a.part;
   p.rowstat = a.rowstat;
+  p.pstat = a.pstat;
+  p.part = a.part;
   p.O = a.O;
   p.o_f16 = a.o_f16;
   p.B = a.B;
@@ -795,8 +916,11 @@ cudaError_t launch_flash8(const Flash8Args& a, cudaStream_t stream) {
   p.nb = c8_blocks(a.S);
   p.end = a.end;
   p.window = a.window;
-  p.nsplit = a.nsplit;
   p.items = items;
+  p.whole = plan.whole;
+  p.cut = plan.cut;
+  p.parts = plan.parts;
+  p.first_part = plan.first_part;
   p.status = a.status;
 #define G3_FLASH8_CASE(DH_, G_) \
   if (a.d_h == DH_ && G == G_) return launch_cfg<DH_, G_>(a.Q, p, stream);

@@ -22,15 +22,16 @@ struct Flash8Args {
   const int32_t* qpos;
   const int32_t* pad_lens;
   int32_t* first;             // [B, items] scratch of local layers
-  float2* stat;               // [B*T*H, nsplit] (max, sum) of each part when nsplit > 1
-  float* part;                // [B*T*H, nsplit, d_h] when nsplit > 1
   float2* rowstat;            // [B, H_kv, T*G] (max, 1 / sum) of every row, or null
+  float2* pstat;              // [flash8_part_rows()] and
+  float* part;                // [flash8_part_rows(), d_h]: scratch of cut units
   void* O;
-  int o_f16, B, T, S, end, H, H_kv, d_h, window, nsplit;
+  int o_f16, B, T, S, end, H, H_kv, d_h, window;
   int* status;
 };
-// Tokens of one work item (one CTA per item, split, kv head and batch row).
+// Tokens of one work item.
 int flash8_span(int d_h, int G);
+size_t flash8_part_rows(int B, int T, int S, int H, int H_kv, int d_h);
 cudaError_t launch_flash8(const Flash8Args& a, cudaStream_t stream);
 
 // The probabilities that every slot received from the call's rows, added to
