@@ -53,8 +53,7 @@ namespace g3 {
 namespace {
 
 constexpr int kTile = kC8Block;      // slots per tile: one scale block
-constexpr int kCWarps = 4;           // consumer warps, 16 slots of each tile each
-constexpr int kThreads = (kCWarps + 1) * 32;
+constexpr int kSWarps = 4;           // warps along a tile's slots, 16 each
 constexpr int kMaxSplits = 256;
 constexpr int kMaxCluster = 8;
 constexpr int kFewRows = 16;         // query rows of a kv head that decode8_kernel takes
@@ -97,20 +96,28 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int DH, int NT>
+// NT n-tiles of 8 query rows per warp, RG groups of warps along the rows.
+// d_h = 256 with up to 16 rows takes two groups, whose V accumulators fit the
+// registers (one group of two n-tiles spilled: 9 rows of 66000 slots, T = 4, G =
+// 4, 132 us); each converts the cache's bytes for itself.
+template <int DH, int NT, int RG>
 struct Cfg {
+  static constexpr int CWARPS = kSWarps * RG;           // consumer warps
+  static constexpr int THREADS = (CWARPS + 1) * 32;
   static constexpr int NCH = DH / 128;                  // 128-byte column boxes of a row
   static constexpr int BOX = kTile * 128;
   static constexpr int TILE = 2 * NCH * BOX;            // K' and V of one tile
-  // CTAs per SM, and ring stages: 64 KB of tiles per CTA for three, 96 for two
-  static constexpr int CTAS = DH == 128 && NT == 1 ? 3 : 2;
-  static constexpr int NST = DH == 256 ? 3 : (CTAS == 3 ? 4 : 6);
+  // CTAs per SM, and ring stages: 64 KB of tiles per CTA for three, 96 for
+  // two, 192 for one
+  static constexpr int CTAS = RG == 2 ? 1 : (DH == 128 && NT == 1 ? 3 : 2);
+  static constexpr int NST = DH == 256 ? 3 * RG : (CTAS == 3 ? 4 : 6);
   static constexpr int RING = NST * TILE;
   static constexpr int NC = DH / 16;                    // 16-channel chunks
-  static constexpr int QF = NC * NT * 32 * 8;           // Q fragments
-  static constexpr int ROWS = NT * 8;
+  static constexpr int NN = NT * RG;                    // n-tiles of the CTA
+  static constexpr int QF = NC * NN * 32 * 8;           // Q fragments
+  static constexpr int ROWS = NN * 8;
   static constexpr int LDM = DH + 8;                    // merge record row, floats
-  static constexpr int MERGE = kCWarps * ROWS * LDM * 4;
+  static constexpr int MERGE = kSWarps * ROWS * LDM * 4;
   static constexpr int SMEM = 1024 + RING + QF;
   static_assert(MERGE + ROWS * DH * 4 <= RING, "merge records must fit in the ring");
   static_assert((SMEM + 2048) * CTAS <= 228 * 1024, "CTAs per SM");
@@ -176,12 +183,13 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-template <int DH, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
+template <int DH, int NT, int RG>
+__global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTAS)
     decode8_kernel(const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const Params p) {
   pdl_enter();
-  using C = Cfg<DH, NT>;
+  using C = Cfg<DH, NT, RG>;
+  constexpr int kConsumers = C::CWARPS * 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -191,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
   __shared__ int abort_flag;
   __shared__ int early[2];             // first and last early tile with a visible slot
   __shared__ float2 cstat[C::ROWS];    // this CTA's part, for its cluster
-  __shared__ float2 mstat[kCWarps][C::ROWS];
+  __shared__ float2 mstat[kSWarps][C::ROWS];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -204,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
 #pragma unroll
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), kCWarps);
+      mbar_init(smem_u32(&empty[s]), C::CWARPS);
     }
     abort_flag = 0;
     early[0] = INT_MAX;
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
     }
   };
 
-  if (warp == kCWarps) {
+  if (warp == C::CWARPS) {
     // ---------------- producer: K'/V tiles of 64 slots into the ring
     int issued = 0;
     auto issue = [&](int upto) {
@@ -254,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
     }
     if (p.window > 0) {
       __syncwarp();
-      named_barrier(2, kThreads);
+      named_barrier(2, C::THREADS);
       take_early();
       if (lane == 0) issue(n_tiles);
     }
@@ -274,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
   // Q fragments (while the first copies are under way): k columns {2c, 2c+1, 2c+8, 2c+9} of a 16-channel chunk are
   // the channels 4c .. 4c+3, row n = lane / 4.
 #pragma unroll 4
-  for (int i = tid; i < C::NC * NT * 32; i += kCWarps * 32) {
-    const int l = i & 31, nt = (i >> 5) % NT, ch = (i >> 5) / NT;
+  for (int i = tid; i < C::NC * C::NN * 32; i += kConsumers) {
+    const int l = i & 31, nt = (i >> 5) % C::NN, ch = (i >> 5) / C::NN;
     const int r = nt * 8 + (l >> 2);
     uint2 q = make_uint2(0, 0);
     if (r < R) {
@@ -285,15 +293,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
     }
     qf[i] = q;
   }
-  named_barrier(1, kCWarps * 32);
-  // Warp w takes slots 16w .. 16w+15 of every tile
-  // Rows of this thread: nt * 8 + 2c + e; slots g and g + 8 of the warp's 16.
+  named_barrier(1, kConsumers);
+  const int sw = warp % kSWarps, n0 = warp / kSWarps * NT;   // slots, first n-tile
+  // Warp sw takes slots 16sw .. 16sw + 15 of every tile
+  // Rows of this thread: (n0 + nt) * 8 + 2c + e; slots g and g + 8 of the warp's 16.
   int lim[NT][2], plo[NT][2], phi[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = nt * 8 + 2 * c + e;
+      const int r = (n0 + nt) * 8 + 2 * c + e;
       lim[nt][e] = -1;
       plo[nt][e] = 0;
       phi[nt][e] = INT_MAX;
@@ -319,16 +328,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
     const int32_t* row = p.posc + static_cast<size_t>(b) * p.S;
     const int e0 = min(tl.k0, split * tl.per_early) * kTile;
     const int e1 = min(tl.k0, (split + 1) * tl.per_early) * kTile;
-    for (int s = e0 + tid; s < e1; s += 8 * kCWarps * 32) {
+    for (int s = e0 + tid; s < e1; s += 8 * kConsumers) {
       int ps[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        ps[k] = s + k * kCWarps * 32 < e1 ? __ldg(row + s + k * kCWarps * 32) : -1;
+        ps[k] = s + k * kConsumers < e1 ? __ldg(row + s + k * kConsumers) : -1;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (ps[k] >= lo && ps[k] <= up) {
-          first = min(first, (s + k * kCWarps * 32) / kTile);
-          last = (s + k * kCWarps * 32) / kTile;
+          first = min(first, (s + k * kConsumers) / kTile);
+          last = (s + k * kConsumers) / kTile;
         }
     }
     first = __reduce_min_sync(0xffffffffu, first);
@@ -338,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
       atomicMax(&early[1], last);
     }
     __threadfence_block();
-    named_barrier(2, kThreads);
+    named_barrier(2, C::THREADS);
     take_early();
     if (p.swept != nullptr && j == 0 && tid == 0)
       p.swept[static_cast<size_t>(b) * p.nsplit + split] =
@@ -358,11 +367,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
   const float* ksp = p.K_scale + (static_cast<size_t>(b) * p.nb) * p.H_kv + j;
   const float* vsp = p.V_scale + (static_cast<size_t>(b) * p.nb) * p.H_kv + j;
   const int32_t* posr = p.posc + static_cast<size_t>(b) * p.S;
-  const int so = warp * 16 + g;      // this thread's first slot within a tile
+  const int so = sw * 16 + g;      // this thread's first slot within a tile
 
   // ldmatrix row addresses within a box: matrices (slots 0-7 | 8-15) x (two
   // 16-byte chunks), chunk XORed with the slot's low bits by the TMA swizzle.
-  const int mrow = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+  const int mrow = sw * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
   const int mch = lane >> 4;
   const uint32_t roff = mrow * 128, rxor = mrow & 7;
 
@@ -425,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
           const uint32_t a1 = c8_half2(r[2 * u + 1]), a3 = c8_half2_hi(r[2 * u + 1]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint2 q = qf[((cp * 2 + u) * NT + nt) * 32 + lane];
+            const uint2 q = qf[((cp * 2 + u) * C::NN + n0 + nt) * 32 + lane];
             mma16816(acc[u][nt], a0, a1, a2, a3, q.x, q.y);
           }
         }
@@ -444,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
         if (lg != nullptr) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int row = nt * 8 + 2 * c + (e & 1);
+            const int row = (n0 + nt) * 8 + 2 * c + (e & 1);
             if (row < R)
               lg[static_cast<size_t>(row) * (static_cast<size_t>(p.nb) * kTile) + (e >> 1) * 8] =
                   x[e];
@@ -515,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int row = nt * 8 + 2 * c + (e & 1);
+          const int row = (n0 + nt) * 8 + 2 * c + (e & 1);
           if (row < R)
             lg[static_cast<size_t>(row) * (static_cast<size_t>(p.nb) * kTile) + (e >> 1) * 8] =
                 -INFINITY;
@@ -525,9 +534,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
     if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
   }
 
-  // ---------------- merge the four warps (records in the ring, which no copy
+  // ---------------- merge the warps along the slots (records in the ring, which no copy
   // writes any more once every warp is past its last tile)
-  named_barrier(1, kCWarps * 32);
+  named_barrier(1, kConsumers);
   float* mg = reinterpret_cast<float*>(ring);
   float* cacc = reinterpret_cast<float*>(ring + C::MERGE);     // [ROWS][DH]
 #pragma unroll
@@ -538,20 +547,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
       s += __shfl_xor_sync(0xffffffffu, s, 4);
       s += __shfl_xor_sync(0xffffffffu, s, 8);
       s += __shfl_xor_sync(0xffffffffu, s, 16);
-      const int row = nt * 8 + 2 * c + e;
-      if (g == 0) mstat[warp][row] = make_float2(m[nt][e], s);
+      const int row = (n0 + nt) * 8 + 2 * c + e;
+      if (g == 0) mstat[sw][row] = make_float2(m[nt][e], s);
 #pragma unroll
       for (int ch = 0; ch < C::NC; ++ch)
-        *reinterpret_cast<float2*>(mg + (warp * C::ROWS + row) * C::LDM + ch * 16 + 2 * g) =
+        *reinterpret_cast<float2*>(mg + (sw * C::ROWS + row) * C::LDM + ch * 16 + 2 * g) =
             make_float2(o[ch][nt][e] * unit, o[ch][nt][2 + e] * unit);
     }
-  named_barrier(1, kCWarps * 32);
-  for (int idx = tid; idx < R * (DH / 4); idx += kCWarps * 32) {
+  named_barrier(1, kConsumers);
+  for (int idx = tid; idx < R * (DH / 4); idx += kConsumers) {
     const int r = idx / (DH / 4), ch = idx % (DH / 4) * 4;
-    float2 ms[kCWarps];
+    float2 ms[kSWarps];
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kCWarps; ++w) {
+    for (int w = 0; w < kSWarps; ++w) {
       ms[w] = mstat[w][r];
       M = fmaxf(M, ms[w].x);
     }
@@ -559,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (M != -INFINITY) {
 #pragma unroll
-      for (int w = 0; w < kCWarps; ++w) {
+      for (int w = 0; w < kSWarps; ++w) {
         const float fw = ex2(ms[w].x - M);
         L += fw * ms[w].y;
         // (a warp that saw nothing holds zeros)
@@ -589,8 +598,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
     __syncwarp();
     cluster_sync();
     const uint32_t st = smem_u32(cstat), ac = smem_u32(cacc);
-    for (int idx = split * (kCWarps * 32) + tid; idx < R * (DH / 4);
-         idx += p.nsplit * kCWarps * 32) {
+    for (int idx = split * kConsumers + tid; idx < R * (DH / 4);
+         idx += p.nsplit * kConsumers) {
       const int r = idx / (DH / 4), ch = idx % (DH / 4) * 4;
       float2 ms[8];
       float4 v[8];
@@ -625,65 +634,81 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH, NT>::CTAS)
   }
 }
 
-// ---------------------------------------------------------------- second launch
-// CTAs [0, n_rows): merge the parts of one query row.  The others: weights of
-// kWSlots slots of one batch row, every query row's logits once.
-constexpr int kWSlots = 512;
-constexpr int kWRows = 16;
-
-struct FinishParams {
+// ---------------------------------------------------------------- later launches
+// Merge of the parts of one query row per CTA; its (max, sum) to fstat, if
+// given.
+struct MergeParams {
   const float2* stat;
   const float* part;
+  float2* fstat;
+  void* O;
+  int o_f16, parts;
+};
+
+template <int DH>
+__global__ void __launch_bounds__(DH) merge8_kernel(const MergeParams p) {
+  pdl_enter();
+  __shared__ float fw[kMaxSplits];
+  __shared__ float red[2][DH / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const size_t row = blockIdx.x;
+  const float2* st = p.stat + row * p.parts;
+  float2 mine[kMaxSplits / DH];
+  float M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / DH; ++i) {
+    mine[i] = tid + i * DH < p.parts ? st[tid + i * DH] : make_float2(-INFINITY, 0.f);
+    M = fmaxf(M, mine[i].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[0][warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < DH / 32; ++i) M = fmaxf(M, red[0][i]);
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / DH; ++i) {
+    const float f = M == -INFINITY ? 0.f : ex2(mine[i].x - M);
+    fw[tid + i * DH] = f;
+    L = fmaf(f, mine[i].y, L);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane == 0) red[1][warp] = L;
+  __syncthreads();
+  L = 0.f;
+#pragma unroll
+  for (int i = 0; i < DH / 32; ++i) L += red[1][i];
+  const float* base = p.part + row * p.parts * DH + tid;
+  float acc = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < p.parts; ++i) acc = fmaf(fw[i], __ldg(base + static_cast<size_t>(i) * DH), acc);
+  store_o(p.O, p.o_f16, row * DH + tid, L != 0.f ? acc / L : 0.f);
+  if (tid == 0 && p.fstat != nullptr) p.fstat[row] = make_float2(M, L);
+}
+
+// Weights of 512 / RW slots of one batch row per CTA, every query row's logits
+// once, two slots per thread; RW groups of threads take every RW-th row (4
+// where a call has more than 16, which would otherwise come one batch after
+// another).
+struct WeighParams {
+  const float2* stat;         // [B*T*H] (max, sum)
   const float* logits;
   float* weight_sum;
   const int2* swept;          // as in Params
   const int32_t* pad_lens;
-  void* O;
-  int o_f16, n_rows, T, S, H, H_kv, nb, end, nsplit, parts, late, wchunks;
+  int T, S, H, H_kv, nb, end, nsplit, late, wchunks;
 };
 
-template <int DH>
-__global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
+template <int RW>
+__global__ void __launch_bounds__(256) weigh8_kernel(const WeighParams p) {
   pdl_enter();
-  __shared__ float fw[kMaxSplits];
-  __shared__ float2 rs[2][kWRows];
-  __shared__ int last[2][kWRows];
-  __shared__ float red[2][8];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (blockIdx.x < static_cast<unsigned>(p.n_rows)) {
-    const size_t row = blockIdx.x;
-    const float2* st = p.stat + row * p.nsplit;
-    const float2 mine = tid < p.nsplit ? st[tid] : make_float2(-INFINITY, 0.f);
-    float M = mine.x;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) red[0][warp] = M;
-    __syncthreads();
-    M = red[0][0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) M = fmaxf(M, red[0][i]);
-    const float f = M == -INFINITY ? 0.f : ex2(mine.x - M);
-    fw[tid] = f;
-    float L = f * mine.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (lane == 0) red[1][warp] = L;
-    __syncthreads();
-    L = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) L += red[1][i];
-    const float* base = p.part + row * p.nsplit * DH;
-    for (int ch = tid; ch < DH; ch += 256) {
-      float acc = 0.f;
-#pragma unroll 8
-      for (int i = 0; i < p.nsplit; ++i)
-        acc = fmaf(fw[i], __ldg(base + static_cast<size_t>(i) * DH + ch), acc);
-      store_o(p.O, p.o_f16, row * DH + ch, L != 0.f ? acc / L : 0.f);
-    }
-    return;
-  }
-  const int wi = blockIdx.x - p.n_rows;
-  const int b = wi / p.wchunks, s = (wi % p.wchunks) * kWSlots + 2 * tid;
+  constexpr int GT = 256 / RW, WROWS = 16 * RW;       // threads of a group, rows at a time
+  __shared__ float2 rs[2][WROWS];
+  __shared__ int last[2][WROWS];
+  __shared__ float2 wacc[RW > 1 ? RW - 1 : 1][GT];
+  const int tid = threadIdx.x, rg = tid / GT;
+  const int b = blockIdx.x / p.wchunks, s = (blockIdx.x % p.wchunks) * (2 * GT) + 2 * (tid % GT);
   // Rows in the order of the logits: kv head, token, head of the group.
   const int rows = p.T * p.H, G = p.H / p.H_kv, R = p.T * G;
   const size_t S64 = static_cast<size_t>(p.nb) * kTile;
@@ -699,54 +724,54 @@ __global__ void __launch_bounds__(256) finish8_kernel(const FinishParams p) {
   const float* lg = p.logits + static_cast<size_t>(b) * rows * S64 + s;
   float* out = p.weight_sum + static_cast<size_t>(b) * p.S;
   float2 old = make_float2(0.f, 0.f), acc = make_float2(0.f, 0.f);
-  if (seen) {
+  if (seen && rg == 0) {
     old.x = out[s];
     if (s + 1 < p.S) old.y = out[s + 1];
   }
-  for (int r0 = 0, par = 0; r0 < rows; r0 += kWRows, par ^= 1) {
-    const int n = min(kWRows, rows - r0);
-    // The rows' logits (two slots of one tile per thread; loaded without
-    // asking whether they count) are under way while a warp each finds the
-    // rows' (max, 1 / sum) over their parts, and the last slot whose logit the
-    // first launch wrote (a valid token's own).
-    float2 x[kWRows];
+  for (int r0 = 0, par = 0; r0 < rows; r0 += WROWS, par ^= 1) {
+    const int n = min(WROWS, rows - r0);
+    // The rows' logits (of one tile; loaded without asking whether they
+    // count) are under way while the rows' (max, 1 / sum) come, and the last
+    // slot whose logit the first launch wrote (a valid token's own).
+    float2 x[16];
 #pragma unroll
-    for (int i = 0; i < kWRows; ++i)
-      x[i] = seen && i < n ? __ldg(reinterpret_cast<const float2*>(lg + (r0 + i) * S64))
-                           : make_float2(0.f, 0.f);
-    for (int i = warp; i < kWRows; i += 8) {
-      float M = -INFINITY, L = 0.f;
-      int t = valid;
-      if (i < n) {
-        const int j = (r0 + i) / R, q = (r0 + i) % R;
-        t = q / G;
-        const float2* st =
-            p.stat + ((static_cast<size_t>(b) * p.T + t) * p.H + j * G + q % G) * p.parts;
-        for (int k = lane; k < p.parts; k += 32) M = fmaxf(M, st[k].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        if (M != -INFINITY)
-          for (int k = lane; k < p.parts; k += 32) L = fmaf(ex2(st[k].x - M), st[k].y, L);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    for (int i = 0; i < 16; ++i)
+      x[i] = seen && RW * i + rg < n
+                 ? __ldg(reinterpret_cast<const float2*>(lg + (r0 + RW * i + rg) * S64))
+                 : make_float2(0.f, 0.f);
+    if (tid < WROWS) {
+      float2 st = make_float2(0.f, 0.f);
+      int lim = -1;
+      if (tid < n) {
+        const int j = (r0 + tid) / R, e = (r0 + tid) % R, t = e / G;
+        st = __ldg(p.stat + (static_cast<size_t>(b) * p.T + t) * p.H + j * G + e % G);
+        lim = t < valid ? p.end + t : -1;
       }
-      if (lane == 0) {
-        rs[par][i] =
-            make_float2(M == -INFINITY ? 0.f : M, M != -INFINITY && L != 0.f ? 1.f / L : 0.f);
-        last[par][i] = t < valid ? p.end + t : -1;
-      }
+      rs[par][tid] = make_float2(st.x == -INFINITY ? 0.f : st.x, st.y != 0.f ? 1.f / st.y : 0.f);
+      last[par][tid] = lim;
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWRows; ++i) {
-      const float2 st = rs[par][i];
-      const int lim = last[par][i];
+    for (int i = 0; i < 16; ++i) {
+      const float2 st = rs[par][RW * i + rg];
+      const int lim = last[par][RW * i + rg];
       const float e0 = ex2(x[i].x - st.x), e1 = ex2(x[i].y - st.x);
       acc.x = fmaf(s <= lim ? e0 : 0.f, st.y, acc.x);
       acc.y = fmaf(s + 1 <= lim ? e1 : 0.f, st.y, acc.y);
     }
   }
-  if (seen) {
+  if constexpr (RW > 1) {
+    if (rg > 0) wacc[rg - 1][tid % GT] = acc;
+    __syncthreads();
+    if (rg == 0) {
+#pragma unroll
+      for (int i = 0; i < RW - 1; ++i) {
+        acc.x += wacc[i][tid].x;
+        acc.y += wacc[i][tid].y;
+      }
+    }
+  }
+  if (seen && rg == 0) {
     if (acc.x != 0.f) out[s] = old.x + acc.x;
     if (acc.y != 0.f) out[s + 1] = old.y + acc.y;
   }
@@ -776,7 +801,7 @@ struct Split {
 };
 Split splits_few(long long units, int most, int tiles, int d_h, int ctas_per_sm) {
   const int slots = ctas_per_sm * num_sms(), us = d_h == 256 ? 200 : 400;
-  const int full = d_h == 256 ? 224 : slots;
+  const int full = d_h == 256 && ctas_per_sm > 1 ? 224 : slots;
   Split best_of = {1, false};
   long long best = LLONG_MAX;
   for (int n = 1; n <= std::max(std::min(most, tiles), kMaxCluster); ++n) {
@@ -798,7 +823,8 @@ struct Layout {
   int32_t* first;       // many: [B, items]
   float2* stat;         // few: [B*T*H, splits], many: parts of cut units
   float* part;
-  float* logits;        // few rows with weights
+  float* logits;        // few rows with weights, and the merged (max, sum)
+  float2* fstat;
   float2* rowstat;      // many rows with weights
   float* wpart;
   size_t bytes;
@@ -824,6 +850,7 @@ Layout layout(void* ws, int B, int T, int S, int H, int H_kv, int d_h, bool weig
   L.stat = reinterpret_cast<float2*>(take(true, parts * 8));
   L.part = reinterpret_cast<float*>(take(!few || splits > 1, parts * d_h * 4));
   L.logits = reinterpret_cast<float*>(take(few && weights, rows * c8_blocks(S) * kTile * 4));
+  L.fstat = reinterpret_cast<float2*>(take(few && weights, rows * 8));
   L.rowstat = reinterpret_cast<float2*>(take(!few && weights, rows * 8));
   L.wpart = reinterpret_cast<float*>(take(!few && weights, weights8_part_floats() * 4));
   L.bytes = at;
@@ -832,20 +859,21 @@ Layout layout(void* ws, int B, int T, int S, int H, int H_kv, int d_h, bool weig
 
 // CTAs of decode8_kernel per SM for T * G = rows.
 int few_ctas(int d_h, int rows) {
-  if (d_h == 256) return rows <= 8 ? Cfg<256, 1>::CTAS : Cfg<256, 2>::CTAS;
-  return rows <= 8 ? Cfg<128, 1>::CTAS : Cfg<128, 2>::CTAS;
+  if (d_h == 256) return rows <= 8 ? Cfg<256, 1, 1>::CTAS : Cfg<256, 1, 2>::CTAS;
+  return rows <= 8 ? Cfg<128, 1, 1>::CTAS : Cfg<128, 2, 1>::CTAS;
 }
 
-template <int DH, int NT>
+template <int DH, int NT, int RG>
 cudaError_t launch_cfg(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, dim3 grid,
                        cudaStream_t stream) {
-  auto kern = decode8_kernel<DH, NT>;
-  if (cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), Cfg<DH, NT>::SMEM))
+  using C = Cfg<DH, NT, RG>;
+  auto kern = decode8_kernel<DH, NT, RG>;
+  if (cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM))
     return e;
   if (p.cluster)
-    return launch_pdl_cluster(kern, grid, dim3(kThreads), Cfg<DH, NT>::SMEM, p.nsplit, stream, tk, tv,
+    return launch_pdl_cluster(kern, grid, dim3(C::THREADS), C::SMEM, p.nsplit, stream, tk, tv,
                               p);
-  return launch_pdl(kern, grid, dim3(kThreads), Cfg<DH, NT>::SMEM, stream, tk, tv, p);
+  return launch_pdl(kern, grid, dim3(C::THREADS), C::SMEM, stream, tk, tv, p);
 }
 
 }  // namespace
@@ -941,23 +969,33 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   const dim3 grid(nsplit, H_kv, B);
   const bool one = T * (H / H_kv) <= 8;
   if (d_h == 256)
-    e = one ? launch_cfg<256, 1>(tk, tv, p, grid, stream)
-            : launch_cfg<256, 2>(tk, tv, p, grid, stream);
+    e = one ? launch_cfg<256, 1, 1>(tk, tv, p, grid, stream)
+            : launch_cfg<256, 1, 2>(tk, tv, p, grid, stream);
   else
-    e = one ? launch_cfg<128, 1>(tk, tv, p, grid, stream)
-            : launch_cfg<128, 2>(tk, tv, p, grid, stream);
-  if (e != cudaSuccess || (parts == 1 && weight_sum == nullptr)) return e;
+    e = one ? launch_cfg<128, 1, 1>(tk, tv, p, grid, stream)
+            : launch_cfg<128, 2, 1>(tk, tv, p, grid, stream);
+  if (e != cudaSuccess) return e;
 
-  FinishParams q = {};
-  q.stat = lay.stat;
-  q.part = lay.part;
+  if (parts > 1) {
+    MergeParams q;
+    q.stat = lay.stat;
+    q.part = lay.part;
+    q.fstat = weight_sum != nullptr ? lay.fstat : nullptr;
+    q.O = O;
+    q.o_f16 = o_f16;
+    q.parts = parts;
+    e = d_h == 256 ? launch_pdl(merge8_kernel<256>, dim3(B * T * H), dim3(256), 0, stream, q)
+                   : launch_pdl(merge8_kernel<128>, dim3(B * T * H), dim3(128), 0, stream, q);
+    if (e != cudaSuccess) return e;
+  }
+  if (weight_sum == nullptr) return cudaSuccess;
+  const bool many = T * H > 16;
+  WeighParams q;
+  q.stat = parts > 1 ? lay.fstat : lay.stat;
   q.logits = lay.logits;
   q.weight_sum = weight_sum;
   q.swept = lay.swept;
   q.pad_lens = pad_lens;
-  q.O = O;
-  q.o_f16 = o_f16;
-  q.n_rows = parts > 1 ? B * T * H : 0;
   q.T = T;
   q.S = S;
   q.H = H;
@@ -965,14 +1003,12 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   q.nb = nb;
   q.end = end;
   q.nsplit = nsplit;
-  q.parts = parts;
   q.late = p.late;
-  q.wchunks = (hi + kWSlots - 1) / kWSlots;
-  const long long ctas =
-      q.n_rows + (weight_sum != nullptr ? static_cast<long long>(B) * q.wchunks : 0);
+  q.wchunks = (hi + (many ? 128 : 512) - 1) / (many ? 128 : 512);
+  const long long ctas = static_cast<long long>(B) * q.wchunks;
   if (ctas > INT_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(d_h == 256 ? finish8_kernel<256> : finish8_kernel<128>,
-                    dim3(static_cast<unsigned>(ctas)), dim3(256), 0, stream, q);
+  return launch_pdl(many ? weigh8_kernel<4> : weigh8_kernel<1>, dim3(static_cast<unsigned>(ctas)),
+                    dim3(256), 0, stream, q);
 }
 
 }  // namespace g3

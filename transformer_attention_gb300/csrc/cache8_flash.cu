@@ -694,12 +694,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// The parts of the cut units: CTA (u, y) adds those of 16 rows of unit u.
+// The parts of the cut units: CTA (u, y) adds those of 8 rows of unit u, a
+// warp each.
 template <int DH, int G>
 __global__ void __launch_bounds__(256) flash8_merge_kernel(const Params p) {
   pdl_enter();
   using C = Cfg<DH, G>;
-  constexpr int ROWS = 16;
+  constexpr int ROWS = 8;
   const int unit = p.whole + blockIdx.x;
   const int item = p.items - 1 - unit % p.items;
   const int bj = unit / p.items, j = bj % p.H_kv, b = bj / p.H_kv;
@@ -711,25 +712,42 @@ __global__ void __launch_bounds__(256) flash8_merge_kernel(const Params p) {
     auto at = [&](int c) -> size_t {
       return (static_cast<size_t>(blockIdx.x) * p.parts + c) * (C::NQ * BM) + row;
     };
+    // (max, sum) of 32 parts at a time, one per lane, then their rows of O
     float M = -INFINITY, L = 0.f;
-    for (int c = 0; c < p.parts; ++c) M = fmaxf(M, p.pstat[at(c)].x);
     float4 acc[DH / 128];
 #pragma unroll
     for (int v = 0; v < DH / 128; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M != -INFINITY) {
-#pragma unroll 2
-      for (int c = 0; c < p.parts; ++c) {
-        const float2 st = p.pstat[at(c)];
-        const float f = ex2(st.x - M);
-        L = fmaf(f, st.y, L);
-        const float4* src = reinterpret_cast<const float4*>(p.part + at(c) * DH);
+    for (int c0 = 0; c0 < p.parts; c0 += 32) {
+      const int n = min(32, p.parts - c0);
+      const float2 st = lane < n ? p.pstat[at(c0 + lane)] : make_float2(-INFINITY, 0.f);
+      float m = st.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float mn = fmaxf(M, m), ref = mn == -INFINITY ? 0.f : mn;
+      const float old = ex2(M - ref), f = ex2(st.x - ref);
+      float l = f * st.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      L = fmaf(L, old, l);
+      M = mn;
+#pragma unroll
+      for (int v = 0; v < DH / 128; ++v) {
+        acc[v].x *= old;
+        acc[v].y *= old;
+        acc[v].z *= old;
+        acc[v].w *= old;
+      }
+#pragma unroll 4
+      for (int c = 0; c < n; ++c) {
+        const float fc = __shfl_sync(0xffffffffu, f, c);
+        const float4* src = reinterpret_cast<const float4*>(p.part + at(c0 + c) * DH);
 #pragma unroll
         for (int v = 0; v < DH / 128; ++v) {
           const float4 o = __ldg(src + v * 32 + lane);
-          acc[v].x = fmaf(f, o.x, acc[v].x);
-          acc[v].y = fmaf(f, o.y, acc[v].y);
-          acc[v].z = fmaf(f, o.z, acc[v].z);
-          acc[v].w = fmaf(f, o.w, acc[v].w);
+          acc[v].x = fmaf(fc, o.x, acc[v].x);
+          acc[v].y = fmaf(fc, o.y, acc[v].y);
+          acc[v].z = fmaf(fc, o.z, acc[v].z);
+          acc[v].w = fmaf(fc, o.w, acc[v].w);
         }
       }
     }
@@ -823,7 +841,7 @@ cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
   cudaError_t e =
       launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), C::SMEM, stream, tq, tk, tv, p);
   if (e != cudaSuccess || p.cut == 0) return e;
-  return launch_pdl(flash8_merge_kernel<DH, G>, dim3(p.cut, C::NQ * BM / 16), dim3(256), 0, stream, p);
+  return launch_pdl(flash8_merge_kernel<DH, G>, dim3(p.cut, C::NQ * BM / 8), dim3(256), 0, stream, p);
 }
 
 // How many units stay whole, and the cut of the others (fewer than the SMs),
