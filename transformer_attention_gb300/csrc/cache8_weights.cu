@@ -86,8 +86,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_flag;
 
-  const int st = blockIdx.x % p.tiles, b = (blockIdx.x / p.tiles) % p.B;
-  const int us = blockIdx.x / p.tiles / p.B;
+  // the latest slots first: on a local layer the early tiles have no work
+  const int us = blockIdx.x % p.usplit, b = (blockIdx.x / p.usplit) % p.B;
+  const int st = p.tiles - 1 - static_cast<int>(blockIdx.x) / p.usplit / p.B;
   const int valid = min(p.T, p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0));
   const int s_tile = st * BM, hi = valid > 0 ? p.end + valid : 0;
 
@@ -411,6 +412,36 @@ cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), C::SMEM, stream, tq, p);
 }
 
+// CTAs on one slot tile, while their parts fit the scratch: where the rounds
+// of the SMs end earliest, counted in units, with the start and the end of a
+// CTA worth kStart.  On a local layer without gaps only the slots of the
+// window and the new tokens have work, and of the row tiles those that a
+// window reaches.
+constexpr int kStart = 8;
+
+int split_units(const Flash8Args& a, int tiles) {
+  const long long all = static_cast<long long>(tiles) * a.B;
+  const int tq = BN / (a.H / a.H_kv);
+  long long busy = tiles, nrt = (a.T + tq - 1) / tq;
+  if (a.window > 0) {
+    busy = std::min<long long>(busy, (static_cast<long long>(a.window) + a.T + BM - 1) / BM + 1);
+    nrt = std::min<long long>(nrt, (static_cast<long long>(a.window) + BM + tq - 1) / tq + 1);
+  }
+  const long long units = nrt * a.H_kv, most = std::min({units, kWeights8MaxCtas / all, 64LL});
+  const int sms = num_sms();
+  long long best = LLONG_MAX;
+  int split = 1;
+  for (int n = 1; n <= most; ++n) {
+    const long long rounds = (busy * a.B * n + sms - 1) / sms;
+    const long long cost = rounds * (kStart + (units + n - 1) / n);
+    if (cost < best) {
+      best = cost;
+      split = n;
+    }
+  }
+  return split;
+}
+
 }  // namespace
 
 cudaError_t launch_weights8(const Flash8Args& a, float* wpart, float* weight_sum,
@@ -436,12 +467,7 @@ cudaError_t launch_weights8(const Flash8Args& a, float* wpart, float* weight_sum
   p.window = a.window;
   p.status = a.status;
   p.tiles = (a.end + a.T + BM - 1) / BM;
-  // CTAs on one slot tile: as many as two rounds of the SMs take, while their
-  // parts fit the scratch.
-  const long long n = static_cast<long long>(p.tiles) * a.B;
-  const long long want = 2LL * num_sms() / n;
-  p.usplit = static_cast<int>(std::max<long long>(
-      1, std::min<long long>(want, std::min<long long>(kWeights8MaxCtas / n, 64))));
+  p.usplit = split_units(a, p.tiles);
 #define G3_WEIGHTS8_CASE(DH_, G_) \
   if (a.d_h == DH_ && G == G_) e = launch_cfg<DH_, G_>(a.Q, p, stream);
   G3_WEIGHTS8_CASE(128, 1)
