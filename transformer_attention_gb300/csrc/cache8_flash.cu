@@ -20,8 +20,8 @@
 //   3      TMA of the cache's bytes, 8 KB (64 slots x 128 channels) at a time
 //   4-7    converters: K, then V of each tile
 //   8-15   softmax of tile 0 and of tile 1, one thread per row
-// d_h = 256 has one query tile, converters of its own for K (4-7) and V
-// (8-11), softmax in 12-15.  Shared memory holds two 32 KB parts of K and two
+// d_h = 256 has one query tile, converters of its own for K (4-11) and V
+// (12-19), softmax in 20-23.  Shared memory holds two 32 KB parts of K and two
 // of V: whole tiles of 128 slots x 128 channels, or for d_h = 256 the two
 // channel halves of one K tile and the two slot halves of one V tile.
 // TMEM: S_0 0-127, S_1 128-255 (d_h = 256: S of even and odd tiles), O from
@@ -50,21 +50,12 @@ namespace {
 
 using attn::ex2;
 
-constexpr int THREADS = 512;
 constexpr int BM = 128, BN = 128;
 constexpr uint32_t CHUNK = 128 * 128;       // 128 rows x 64 channels (128 B), swizzled
 constexpr uint32_t PART = 32768;
 constexpr uint32_t O_COL = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_THRESHOLD = 8.0f;   // log2 units
-// Registers per thread: 512 threads launch with 128 each; control and
-// converter warpgroups give some to the softmax warpgroups.
-constexpr int REGS_LAUNCH = 128;
-constexpr int REGS_CTRL = 48, REGS_CONV = 80, REGS_SOFT = 192;
-static_assert(REGS_CTRL + REGS_CONV + 2 * REGS_SOFT <= 4 * REGS_LAUNCH &&
-                  REGS_CTRL + 2 * REGS_CONV + REGS_SOFT <= 4 * REGS_LAUNCH,
-              "register split above the launch allocation");
-
 enum : int {
   kSiteQ = 80, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty, kSiteSFull, kSitePFull,
   kSitePvDone, kSiteMetaFull, kSiteMetaEmpty, kSiteOFinal, kSiteRawFull,
@@ -101,6 +92,19 @@ struct Cfg {
   // raw granules: d_h = 128 one ring of four for K and V in turn, d_h = 256
   // a ring of two for each
   static constexpr int RING = PARTS == 1 ? 4 : 2;
+  // Converter warpgroups: one for d_h = 128, for d_h = 256 two of K and two of
+  // V, each for one granule of a part.  (One of each: 0.9 us a part, which a
+  // prompt of 16384 tokens waited for: 937 us.)
+  static constexpr int SPLIT = PARTS;              // warpgroups of a part
+  static constexpr int CONV = PARTS * SPLIT;
+  static constexpr int THREADS = 128 * (1 + CONV + NQ);
+  // Registers per thread: control and converter warpgroups give some of the
+  // launch's to the softmax warpgroups.
+  static constexpr int REGS_LAUNCH = PARTS == 1 ? 128 : 80;
+  static constexpr int REGS_CTRL = PARTS == 1 ? 48 : 40, REGS_CONV = PARTS == 1 ? 80 : 56;
+  static constexpr int REGS_SOFT = PARTS == 1 ? 192 : 216;
+  static_assert(REGS_CTRL + CONV * REGS_CONV + NQ * REGS_SOFT <= (1 + CONV + NQ) * REGS_LAUNCH,
+                "register split above the launch allocation");
   static constexpr uint32_t SMEM = NQ * QT_BYTES + 4 * PART + 4 * RAW + sizeof(Shared);
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -157,7 +161,7 @@ __device__ __forceinline__ float mask_max(uint32_t (&r)[32], uint32_t keep) {
 }
 
 template <int DH, int G>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<DH, G>::THREADS, 1)
     flash8_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const Params p) {
   pdl_enter();
@@ -207,9 +211,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (tid == 0) {
     mbar_init(smem_u32(&sh.q_full), 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&sh.k_full[s]), 4);
+      mbar_init(smem_u32(&sh.k_full[s]), 4 * C::SPLIT);
       mbar_init(smem_u32(&sh.k_empty[s]), 1);
-      mbar_init(smem_u32(&sh.v_full[s]), 4);
+      mbar_init(smem_u32(&sh.v_full[s]), 4 * C::SPLIT);
       mbar_init(smem_u32(&sh.v_empty[s]), 1);
       mbar_init(smem_u32(&sh.s_full[s]), 1);
       mbar_init(smem_u32(&sh.p_full[s]), 4);
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&sh.raw_full[s]), 1);
       mbar_init(smem_u32(&sh.raw_empty[s]), 4);
       mbar_init(smem_u32(&sh.meta_full[s]), 1);
-      mbar_init(smem_u32(&sh.meta_empty[s]), 4 * (nq + C::PARTS));   // softmax and converter warps
+      mbar_init(smem_u32(&sh.meta_empty[s]), 4 * (nq + C::CONV));   // softmax and converter warps
     }
     mbar_init(smem_u32(&sh.drain), 1);
     sh.abort_flag = 0;
@@ -241,7 +245,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   if (warp < 4) {
-    regs_decrease<REGS_CTRL>();
+    regs_decrease<C::REGS_CTRL>();
     // Raw granule n of a stream (RING slots from slot r0 on): of K, granule
     // (channel half, slot half) of a tile, of V d_h = 256 (slot half, channel
     // half); d_h = 128 has K's and V's two slot halves in one stream.  For
@@ -442,19 +446,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         fetch(i + 1);
       }
     }
-  } else if (warp < 4 + 4 * C::PARTS) {
+  } else if (warp < 4 + 4 * C::CONV) {
     // ---------------- converters
-    regs_decrease<REGS_CONV>();
+    regs_decrease<C::REGS_CONV>();
     const int ct = tid & 127;                  // thread of its warpgroup
     const int col = ct & 7, row0 = ct >> 3;    // 16-channel group, slots row0 + 16 k of a granule
-    // Part q of the warpgroup's stream (d_h = 128: K, V of each tile in turn;
-    // d_h = 256: warps 4-7 the channel halves of K, 8-11 the slot halves of V):
-    // two granules to 32 KB of fp16.  Wide parts are 128 slots x 128 channels,
-    // half parts (V of d_h = 256) 64 slots x 256 channels.  All of a part's
-    // loads are in flight before the first conversion, and its granules are
-    // free for the next copies by then.
-    const bool v256 = C::PARTS == 2 && warp >= 8;
-    const int r0 = v256 ? 2 : 0;
+    // Part q of the stream (d_h = 128: K, V of each tile in turn; d_h = 256:
+    // warps 4-11 the channel halves of K, 12-19 the slot halves of V): two
+    // granules to 32 KB of fp16, each warpgroup both or its own.  Wide parts
+    // are 128 slots x 128 channels, half parts (V of d_h = 256) 64 slots x 256
+    // channels.  All loads are in flight before the first conversion, and the
+    // granules are free for the next copies by then.
+    const bool v256 = C::PARTS == 2 && warp >= 12;
+    const int r0 = v256 ? 2 : 0, g0 = C::SPLIT == 2 ? (warp >> 2 & 1) ^ 1 : 0;
+    constexpr int NG = 2 / C::SPLIT;
+    const int swap = swap8(col, row0) * 8;
 #pragma unroll 1
     for (int q = 0; q < 2 * n_tiles; ++q) {
       const int i = q >> 1, hh = q & 1;
@@ -462,52 +468,62 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int buf = C::PARTS == 1 ? (i & 1) : hh, use = C::PARTS == 1 ? (i >> 1) : i;
       if (hh == 0 && !wait_warp(sh.meta_full[i % NMETA], (i / NMETA) & 1, kSiteMetaFull)) break;
       const Meta& m = sh.meta[i % NMETA];
-      // scales and counted slots of granule 0 and 1
+      // scales and counted slots of the granules' 64-slot blocks (a block
+      // without any may have any scale)
       const float* msc = v ? m.vs : m.ks;
-      const float s0 = msc[v256 ? hh : 0], s1 = msc[v256 ? hh : 1];
-      const uint2 u0 = *reinterpret_cast<const uint2*>(m.use + (v256 ? 2 * hh : 0));
-      const uint2 u1 = *reinterpret_cast<const uint2*>(m.use + (v256 ? 2 * hh : 2));
-      uint4 x[8];
-      uint32_t sc[8];
+      float sc[NG];
+      uint2 u[NG];
+      bool whole_block = true;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int blk = v256 ? hh : g0 + g;
+        u[g] = *reinterpret_cast<const uint2*>(m.use + 2 * blk);
+        sc[g] = (u[g].x | u[g].y) != 0 ? msc[blk] : 0.f;
+        whole_block &= (u[g].x & u[g].y) == 0xffffffffu;
+      }
+      uint2 x[4 * NG][2];
       bool ok = true;
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int n = 2 * q + g, r = r0 + n % C::RING;
+      for (int g = 0; g < NG; ++g) {
+        const int n = 2 * q + g0 + g, r = r0 + n % C::RING;
         ok = ok && wait_warp(sh.raw_full[r], (n / C::RING) & 1, kSiteRawFull);
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int row = row0 + 16 * k;
-          x[4 * g + k] =
-              *reinterpret_cast<const uint4*>(sR + r * RAW + row * 128 + ((col ^ (row & 7)) << 4));
-          sc[4 * g + k] = g ? pack_half2(s1, s1) : pack_half2(s0, s0);
+          const uint8_t* src = sR + r * RAW + row * 128 + ((col ^ (row & 7)) << 4);
+          x[4 * g + k][0] = *reinterpret_cast<const uint2*>(src + swap);
+          x[4 * g + k][1] = *reinterpret_cast<const uint2*>(src + (swap ^ 8));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[r]));
       }
       ok = ok && wait_warp(v ? sh.v_empty[buf] : sh.k_empty[buf], (use & 1) ^ 1, kSiteKEmpty);
       if (!ok) break;
-      if ((u0.x & u0.y & u1.x & u1.y) != 0xffffffffu) {
+      if (!whole_block) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t u = k < 2 ? u0.x : (k < 4 ? u0.y : (k < 6 ? u1.x : u1.y));
-          if (!((u >> ((row0 + 16 * k) & 31)) & 1u)) {
-            x[k] = make_uint4(0, 0, 0, 0);
-            sc[k] = 0u;
-          }
+        for (int k = 0; k < 4 * NG; ++k) {
+          const uint32_t w = k & 2 ? u[k >> 2].y : u[k >> 2].x;
+          if (!((w >> ((row0 + 16 * k) & 31)) & 1u)) x[k][0] = x[k][1] = make_uint2(0, 0);
         }
       }
-      uint8_t* base = (v ? sV : sK) + buf * PART + (col >> 2) * (v256 ? CHUNK / 2 : CHUNK) + row0 * 128;
-      // granule 1: the other channel chunks of the same slots, or the next 64 slots
-      const uint32_t g1 = v256 ? CHUNK : CHUNK / 2;
-      if (s0 > 128.f || s1 > 128.f) {
+      // a part's second granule: the other channel chunks of the same slots,
+      // or the next 64 slots
+      const uint32_t chunk = v256 ? CHUNK / 2 : CHUNK, g1 = v256 ? CHUNK : CHUNK / 2;
+      uint8_t* base = (v ? sV : sK) + buf * PART + (col >> 2) * chunk + g0 * g1 + row0 * 128;
+      bool clamp = false;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          store16_values<true>(x[k], sc[k], col, row0, base + (k & 3) * 2048 + (k >> 2) * g1);
+      for (int g = 0; g < NG; ++g) clamp |= sc[g] > 128.f;
+      if (clamp) {
+#pragma unroll
+        for (int k = 0; k < 4 * NG; ++k)
+          store16_values<true>(x[k][0], x[k][1], pack_half2(sc[k >> 2], sc[k >> 2]), col, row0,
+                               base + (k & 3) * 2048 + (k >> 2) * g1);
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          store16_values<false>(x[k], sc[k], col, row0, base + (k & 3) * 2048 + (k >> 2) * g1);
+        for (int k = 0; k < 4 * NG; ++k)
+          store16_values<false>(x[k][0], x[k][1], pack_half2(sc[k >> 2], sc[k >> 2]), col, row0,
+                                base + (k & 3) * 2048 + (k >> 2) * g1);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -518,8 +534,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else {
     // ---------------- softmax of query tile e, thread r owns row r
-    regs_increase<REGS_SOFT>();
-    const int e = C::NQ == 2 ? (warp - 8) >> 2 : 0;
+    regs_increase<C::REGS_SOFT>();
+    const int e = C::NQ == 2 ? (warp - 4 - 4 * C::CONV) >> 2 : 0;
     if (e < nq) {
       const int q = warp & 3;                // TMEM lane quarter (= warp % 4)
       const int r = q * 32 + lane;
@@ -836,11 +852,11 @@ cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
   if (cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, &regs)) return e;
   // The softmax warpgroups' increases wait for what the others give up:
   // launch only when the split fits the CTA's allocation.
-  if (regs < REGS_LAUNCH) return cudaErrorInvalidConfiguration;
+  if (regs < C::REGS_LAUNCH) return cudaErrorInvalidConfiguration;
   const long long ctas = p.whole + static_cast<long long>(p.cut) * p.parts;
   if (ctas > INT_MAX) return cudaErrorInvalidValue;
   cudaError_t e =
-      launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), C::SMEM, stream, tq, tk, tv, p);
+      launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p);
   if (e != cudaSuccess || p.cut == 0) return e;
   return launch_pdl(flash8_merge_kernel<DH, G>, dim3(p.cut, C::NQ * BM / 8), dim3(256), 0, stream, p);
 }

@@ -59,16 +59,18 @@ __device__ __forceinline__ void window_range(int qn, int qx, int window, int& pl
 // for a hidden slot.  CLAMP for scales above 128, which can take a value past
 // fp16's largest; it becomes 65504 there.  The two 16-byte stores go out in an
 // order that puts eight neighbouring threads (col 0..7 of a slot) on eight
-// bank groups.
+// bank groups: a and b are the 8 bytes of the first and the second store, the
+// upper half first where swap8 is 1 (by the slot too, so that 8-byte loads of
+// two slots' bytes meet no conflict either).
+__device__ __forceinline__ int swap8(int col, int row) { return ((col >> 2) ^ row) & 1; }
+
 template <bool CLAMP>
-__device__ __forceinline__ void store16_values(const uint4& x, uint32_t scale2, int col, int row,
-                                               uint8_t* base) {
-  const __half2 scale = *reinterpret_cast<const __half2*>(&scale2);
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t o[8];
+__device__ __forceinline__ uint4 values8(uint2 w, __half2 scale) {
+  const uint32_t in[2] = {w.x, w.y};
+  uint32_t o[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t lo = c8_half2(w[k]), hi = c8_half2_hi(w[k]);
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t lo = c8_half2(in[k]), hi = c8_half2_hi(in[k]);
     __half2 v0 = __hmul2(*reinterpret_cast<const __half2*>(&lo), scale);
     __half2 v1 = __hmul2(*reinterpret_cast<const __half2*>(&hi), scale);
     if constexpr (CLAMP) {
@@ -79,10 +81,16 @@ __device__ __forceinline__ void store16_values(const uint4& x, uint32_t scale2, 
     o[2 * k] = *reinterpret_cast<uint32_t*>(&v0);
     o[2 * k + 1] = *reinterpret_cast<uint32_t*>(&v1);
   }
-  const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-  const int u0 = (col & 3) * 2, swap = (col >> 2) & 1, r7 = row & 7;
-  *reinterpret_cast<uint4*>(base + (((u0 + swap) ^ r7) << 4)) = swap ? b : a;
-  *reinterpret_cast<uint4*>(base + (((u0 + 1 - swap) ^ r7) << 4)) = swap ? a : b;
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <bool CLAMP>
+__device__ __forceinline__ void store16_values(uint2 a, uint2 b, uint32_t scale2, int col, int row,
+                                               uint8_t* base) {
+  const __half2 scale = *reinterpret_cast<const __half2*>(&scale2);
+  const int u0 = (col & 3) * 2, swap = swap8(col, row), r7 = row & 7;
+  *reinterpret_cast<uint4*>(base + (((u0 + swap) ^ r7) << 4)) = values8<CLAMP>(a, scale);
+  *reinterpret_cast<uint4*>(base + (((u0 + 1 - swap) ^ r7) << 4)) = values8<CLAMP>(b, scale);
 }
 
 // A query row's entry of rowstat: (max, 1 / sum), or (inf, 0) for a row that

@@ -237,17 +237,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok |= (s < hi && __ldg(posr + s) >= 0 ? 1u : 0u) << it;
       }
       // a part: 128 slots x 128 channels, 128 bytes per thread
-      uint4 x[8];
+      uint2 x[8][2];
+      const int swap = swap8(ct % 8, row0);
       float sc0 = 0.f, sc1 = 0.f;
       auto fetch = [&](int q) {
         const int h = h_first + q / C::PARTS;
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
-          x[it] = make_uint4(0, 0, 0, 0);
-          if ((ok >> it) & 1u)
-            x[it] = __ldg(reinterpret_cast<const uint4*>(
+          x[it][0] = x[it][1] = make_uint2(0, 0);
+          if ((ok >> it) & 1u) {
+            const uint2* src = reinterpret_cast<const uint2*>(
                 num + static_cast<size_t>(s_tile + row0 + it * 16) * p.H_kv * DH + h * DH +
-                (q % C::PARTS) * 128));
+                (q % C::PARTS) * 128);
+            x[it][0] = __ldg(src + swap);
+            x[it][1] = __ldg(src + 1 - swap);
+          }
         }
         sc0 = __ldg(sc + static_cast<size_t>(blk) * p.H_kv + h);
         sc1 = __ldg(sc + static_cast<size_t>(min(blk + 1, p.nb - 1)) * p.H_kv + h);
@@ -261,12 +265,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (sc0 > 128.f || sc1 > 128.f) {
 #pragma unroll
           for (int it = 0; it < 8; ++it)
-            store16_values<true>(x[it], (ok >> it) & 1u ? (it >= 4 ? h1 : h0) : 0u, ct % 8,
+            store16_values<true>(x[it][0], x[it][1], (ok >> it) & 1u ? (it >= 4 ? h1 : h0) : 0u, ct % 8,
                                  row0 + it * 16, dst + (row0 + it * 16) * 128);
         } else {
 #pragma unroll
           for (int it = 0; it < 8; ++it)
-            store16_values<false>(x[it], (ok >> it) & 1u ? (it >= 4 ? h1 : h0) : 0u, ct % 8,
+            store16_values<false>(x[it][0], x[it][1], (ok >> it) & 1u ? (it >= 4 ? h1 : h0) : 0u, ct % 8,
                                   row0 + it * 16, dst + (row0 + it * 16) * 128);
         }
         if (part == C::PARTS - 1)
