@@ -788,6 +788,8 @@ int validate_cache8(int B, int S, long long used, int H_kv, int d_h, const void*
     return GEMMA3_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * S >= (1LL << 40) / (static_cast<long long>(H_kv) * d_h))
     return GEMMA3_ERR_INVALID_ARG;
+  // (a CTA per 64-slot block, kv head, K' or V)
+  if (static_cast<long long>(B) * c8_blocks(S) * H_kv >= 1LL << 30) return GEMMA3_ERR_INVALID_ARG;
   if (!aligned16(K8) || !aligned16(V8) || !aligned4(K_scale) || !aligned4(V_scale))
     return GEMMA3_ERR_MISALIGNED;
   return GEMMA3_OK;
