@@ -380,9 +380,11 @@ int gemma3_cached8_attention_workspace_size(int B, int T, int S, int H, int H_kv
  *   weight_sum [B, S] fp32 or NULL: weight_sum[b, s] += the probabilities that
  * the row's valid tokens and query heads gave slot s, in fp32 and always in
  * the same order.  This is what gemma3_kv_cache8_evict ranks slots by.
- *   What hidden slots hold (those that no token of the call sees) never
- * matters, NaN included; a NaN in a slot that some token of the call sees may
- * reach other tokens of the same call. */
+ *   What a slot's numbers and scale hold never matters, NaN included, where
+ * the slot has no token, lies behind the row's last valid token, or on a
+ * local layer has a position outside the reach of all of the row's tokens
+ * (below the lowest one's window or above the highest one's).  A NaN in any
+ * other slot may reach every token of the call. */
 int gemma3_cached8_attention(const void* Q, const void* K8, const void* V8, const float* K_scale,
                              const float* V_scale, const int32_t* pos_cache,
                              const int32_t* segment_pos, const int32_t* pad_lens, void* O,

@@ -104,6 +104,28 @@ def new_kv_cache8(B, S, H_kv, d_h, device):
             torch.zeros_like(K_scale), pos)
 
 
+def _check_cache8(cache, B, H_kv, d_h, weight_sum):
+    """ValueError unless ``cache`` is an 8-bit cache of these sizes in the
+    layout of new_kv_cache8 (the kernels see addresses only), and weight_sum
+    None or [B, S] fp32.  Returns S."""
+    import torch
+    K8, V8, K_scale, V_scale, pos = cache
+    S = pos.shape[-1]
+    num, sc = (B, S, H_kv, d_h), (B, -(-S // GEMMA3_CACHE8_BLOCK), H_kv)
+    f32 = torch.float32
+    for name, t, shape, dtypes in (
+            ("K8", K8, num, (torch.float8_e4m3fn, torch.uint8)),
+            ("V8", V8, num, (torch.float8_e4m3fn, torch.uint8)),
+            ("K_scale", K_scale, sc, (f32,)), ("V_scale", V_scale, sc, (f32,)),
+            ("pos_cache", pos, (B, S), (torch.int32,)),
+            ("weight_sum", weight_sum, (B, S), (f32,))):
+        if t is None and name == "weight_sum":
+            continue
+        if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtypes[0]} tensor of shape {shape}")
+    return S
+
+
 def attention_forward_cached8(x, segment_pos, pad_lens, cache, end_index, Wq, Wkv, Wo, gamma_q,
                               gamma_k, *, H, H_kv, attn_type, window, rope_base, rope_scale,
                               query_scale, weight_sum=None, out=None, workspace=None,
@@ -115,7 +137,7 @@ def attention_forward_cached8(x, segment_pos, pad_lens, cache, end_index, Wq, Wk
     B, T, D = x.shape
     d_h = gamma_q.shape[0]
     K8, V8, K_scale, V_scale, pos_cache = cache
-    S = pos_cache.shape[1]
+    S = _check_cache8(cache, B, H_kv, d_h, weight_sum)
     dims = (B, T, D, H, H_kv, d_h)
     if workspace is None:
         workspace = _empty_ws(gemma3_attn_cached8_workspace_size(dims, S, weight_sum is not None),
@@ -140,11 +162,13 @@ def evict_kv_cache8(cache, weight_sum, end_index, keep, recent, *, into=None, S=
     import torch
     K8, V8, K_scale, V_scale, pos = cache
     B, S0, H_kv, d_h = K8.shape
+    _check_cache8(cache, B, H_kv, d_h, weight_sum)
     if into is None:
         S = S0 if S is None else S
         into = (new_kv_cache8(B, S, H_kv, d_h, K8.device),
                 torch.zeros((B, S), dtype=torch.float32, device=K8.device))
     dst, w_dst = into
+    _check_cache8(dst, B, H_kv, d_h, w_dst)
     kept = torch.empty((B, keep), dtype=torch.int32, device=K8.device)
     gemma3_kv_cache8_evict(K8, V8, K_scale, V_scale, pos, weight_sum, B, S0, end_index, H_kv, d_h,
                            keep, recent, *dst, w_dst, kept, dst[4].shape[1], stream)
