@@ -126,3 +126,25 @@ def test_keys_beyond_fp16(T, end):
     for t in range(T):
         want[:end + t + 1] += H / (end + t + 1)
     assert ((w[0].cpu().double() - want).abs() <= (T * H + 4) * 2.0 ** -23 * want).all()
+
+
+@pytest.mark.parametrize("T,d_h,stride", [(70, 128, 3), (150, 256, 2), (70, 256, 0), (9, 128, 3)])
+def test_windows_over_positions_that_skip(T, d_h, stride):
+    """Positions stride * slot (0: shuffled): neither a tile's slots nor its
+    tokens are at consecutive positions."""
+    import transformer_attention_gb300 as G3
+    B, S, end, H, H_kv, W = 2, 1500, 1200, 4, 2, 300
+    c, Q, seg = C._stage(B, T, S, end, H, H_kv, d_h, None, "plain", 21)
+    for b in range(B):
+        n = torch.arange(end + T)
+        p = n * stride + 5 if stride else torch.randperm(end + T, generator=C._gen(b))
+        c["pos"][b, :end + T] = p
+        seg[b] = p[end:]
+    ref, w, A, PV = C8.attend(Q, c, seg, None, end, W)
+    wsum = torch.zeros((B, S), device="cuda")
+    O = C._attend(G3, Q, C._to_dev(c), seg, None, T, end, H, H_kv, d_h, W, torch.float16, wsum)
+    assert G3.gemma3_attn_check_status() == 0
+    C._check_o(O, ref, A, PV, float(C8.values(c, "v").nan_to_num(0.0).abs().max()), end + T, d_h,
+               torch.float16)
+    d = 2 * ((d_h / 16 + 4) * 2.0 ** -22 * float(A.max()) + 2.0 ** -21)
+    assert ((wsum.cpu().double() - w).abs() <= (d + (T * H + 2) * 2.0 ** -23) * w).all()

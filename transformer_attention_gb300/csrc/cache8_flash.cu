@@ -70,7 +70,7 @@ struct Meta {
   uint32_t use[4];         // those of them in the windows' reach of some valid token
   float ks[2], vs[2];      // scales of the two blocks
   int pmin, pmax;          // range of the positions of the ok slots
-  int pad[2];
+  int seq, base;           // seq: each of them is at position base + its place in the tile
   int pos[BN];
 };
 
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(Cfg<DH, G>::THREADS, 1)
       for (int i = 0; i < n_tiles; ++i) {
         if (!wait_warp(sh.meta_empty[i % NMETA], ((i / NMETA) & 1) ^ 1, kSiteMetaEmpty)) break;
         Meta& m = sh.meta[i % NMETA];
-        int mn = INT_MAX, mx = INT_MIN;
+        int mn = INT_MAX, mx = INT_MIN, bn = INT_MAX, bx = INT_MIN;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const bool okk = nx[k] >= 0;
@@ -432,14 +432,22 @@ __global__ void __launch_bounds__(Cfg<DH, G>::THREADS, 1)
           if (okk) {
             mn = min(mn, nx[k]);
             mx = max(mx, nx[k]);
+            bn = min(bn, nx[k] - (k * 32 + lane));
+            bx = max(bx, nx[k] - (k * 32 + lane));
           }
         }
         mn = __reduce_min_sync(0xffffffffu, mn);
         mx = __reduce_max_sync(0xffffffffu, mx);
+        if (p.window > 0) {
+          bn = __reduce_min_sync(0xffffffffu, bn);
+          bx = __reduce_max_sync(0xffffffffu, bx);
+        }
         if (lane < 4) (lane & 2 ? m.vs : m.ks)[lane & 1] = ns;
         if (lane == 0) {
           m.pmin = mn;
           m.pmax = mx;
+          m.seq = bn == bx;
+          m.base = bn;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.meta_full[i % NMETA]));
@@ -590,7 +598,17 @@ __global__ void __launch_bounds__(Cfg<DH, G>::THREADS, 1)
             const int c = lim - (s_tile + 32 * k);       // last visible column of the 32
             keep[k] = mt.ok[k] & (c < 0 ? 0u : (c >= 31 ? 0xffffffffu : (2u << c) - 1u));
           }
-          if (!win_ok) {
+          if (!win_ok && mt.seq) {
+            const long long base = mt.base;
+            const int c0 = static_cast<int>(min(max(plo - base, 0LL), 128LL));
+            const int c1 = static_cast<int>(min(max(phi - base, -1LL), 127LL));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int a = c0 - 32 * k, z = c1 - 32 * k;   // columns [a, z] of the 32
+              const uint32_t from = a <= 0 ? 0xffffffffu : (a >= 32 ? 0u : 0xffffffffu << a);
+              keep[k] &= from & (z < 0 ? 0u : (z >= 31 ? 0xffffffffu : (2u << z) - 1u));
+            }
+          } else if (!win_ok) {
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
               uint32_t w = 0;

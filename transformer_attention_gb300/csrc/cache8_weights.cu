@@ -286,12 +286,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int s = s_tile + r;
     const int ps = s < hi ? __ldg(p.posc + static_cast<size_t>(b) * p.S + s) : -1;
-    // query positions that see this slot on a local layer, and the range of
-    // the warp's slots' positions
+    // query positions that see this slot on a local layer
     int qlo = INT_MIN, qhi = INT_MAX;
     if (p.window > 0) window_range(ps, ps, p.window, qlo, qhi);
-    const int wmin = __reduce_min_sync(0xffffffffu, ps >= 0 ? ps : INT_MAX);
-    const int wmax = __reduce_max_sync(0xffffffffu, ps);
     const size_t rows = static_cast<size_t>(p.T) * G;
     float2 nx = make_float2(INFINITY, 0.f);
     int nq = 0;
@@ -318,31 +315,44 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
       const int t0 = tile_of(u0 + n) * C::TQ;
       // columns [c0, c1) are valid tokens at or behind this slot
-      const int c0 = max(0, min(C::TQ, s - p.end - t0)) * G;
-      const int c1 = max(0, min(C::TQ, valid - t0)) * G;
-      bool masked = __any_sync(0xffffffffu, c0 > 0) || c1 < BN;
-      if (p.window > 0 && !masked) {
-        // every slot of the warp within the window of every token of the tile?
-        int qn = INT_MAX, qx = INT_MIN;
-        for (int k = lane; k < C::TQ; k += 32) {
-          qn = min(qn, sq[wg][par][k]);
-          qx = max(qx, sq[wg][par][k]);
+      const int n_tok = max(0, min(C::TQ, valid - t0));
+      int c0 = max(0, min(C::TQ, s - p.end - t0)) * G, c1 = n_tok * G;
+      bool runs = true;              // the columns that see the slot are a run
+      if (p.window > 0) {
+        const int q0 = sq[wg][par][0];
+        bool step = true;            // tokens at positions q0, q0 + 1, ..
+        for (int k = lane; k < n_tok; k += 32) step &= static_cast<unsigned>(sq[wg][par][k]) == static_cast<unsigned>(q0) + k;
+        runs = __all_sync(0xffffffffu, step);
+        if (runs && ps >= 0) {
+          const long long a = static_cast<long long>(qlo) - q0, z = static_cast<long long>(qhi) - q0 + 1;
+          c0 = max(c0, static_cast<int>(min(max(a, 0LL), static_cast<long long>(C::TQ))) * G);
+          c1 = min(c1, static_cast<int>(min(max(z, 0LL), static_cast<long long>(C::TQ))) * G);
         }
-        qn = __reduce_min_sync(0xffffffffu, qn);
-        qx = __reduce_max_sync(0xffffffffu, qx);
-        int plo, phi, a, z;
-        window_range(qx, qx, p.window, plo, a);
-        window_range(qn, qn, p.window, z, phi);
-        masked = wmax >= 0 && (wmin < plo || wmax > phi);
       }
+      // (a slot without a token: whatever it sums is dropped)
+      if (ps < 0) {
+        c0 = 0;
+        c1 = BN;
+      }
+      const int w0 = __reduce_max_sync(0xffffffffu, c0), w1 = __reduce_min_sync(0xffffffffu, c1);
+      const int any0 = __reduce_min_sync(0xffffffffu, ps < 0 ? BN : c0);
+      const int any1 = __reduce_max_sync(0xffffffffu, ps < 0 ? 0 : c1);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       const float4* st4 = reinterpret_cast<const float4*>(rs[wg][par]);
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
+        // (no column of the 32 counts for any slot of the warp)
+        if (c + 32 <= any0 || c >= any1) continue;
         uint32_t x[32];
         tmem_ld32(tbase + lane_off + sb * BN + c, x);
         tmem_ld_wait(x);
-        if (masked) {
+        if (runs) {
+          if (c < w0 || c + 32 > w1) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c + k < c0 || c + k >= c1) x[k] = 0xff800000u;   // -inf
+          }
+        } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             const int qp = sq[wg][par][(c + k) / G];
