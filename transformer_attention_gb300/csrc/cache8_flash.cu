@@ -20,6 +20,7 @@
 //   3      TMA of the cache's bytes, 8 KB (64 slots x 128 channels) at a time
 //   4-7    converters: K, then V of each tile
 //   8-15   softmax of tile 0 and of tile 1, one thread per row
+// One tile of d_h = 128: converters in 4-11, softmax in 12-15.
 // d_h = 256 has one query tile, converters of its own for K (4-11) and V
 // (12-19), softmax in 20-23.  Shared memory holds two 32 KB parts of K and two
 // of V: whole tiles of 128 slots x 128 channels, or for d_h = 256 the two
@@ -64,6 +65,7 @@ enum : int {
 
 constexpr uint32_t RAW = 8192;              // bytes of a raw granule: 64 slots x 128 channels
 constexpr int NMETA = 4;
+constexpr int MAX_RAW = 8;
 
 struct Meta {
   uint32_t ok[4];          // slots of the tile that hold a token below the CTA's last slot
@@ -76,26 +78,33 @@ struct Meta {
 
 struct Shared {
   uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2],
-      meta_full[NMETA], meta_empty[NMETA], raw_full[4], raw_empty[4], o_final[2], drain;
+      meta_full[NMETA], meta_empty[NMETA], raw_full[MAX_RAW], raw_empty[MAX_RAW], o_final[2], drain;
   Meta meta[NMETA];
   uint32_t tmem;
   int abort_flag;
 };
 
-template <int DH, int G>
+// NQ_ query tiles per CTA: two for d_h = 128, which share the conversion of a
+// tile's bytes, one where a call has no second: S is then double buffered, as
+// with d_h = 256, and two warpgroups convert (32 query rows over 65536 slots
+// of 8 kv heads 62 -> 58 us, 132 over 272 slots of 2 kv heads 19 -> 16 us).
+template <int DH, int G, int NQ_>
 struct Cfg {
-  static constexpr int NQ = DH == 128 ? 2 : 1;     // query tiles per CTA
+  static constexpr int NQ = NQ_;
+  static_assert(NQ == 1 || DH == 128, "TMEM columns");
   static constexpr int TQ = BM / G;                // tokens per query tile
   static constexpr int NCH = DH / 64;
   static constexpr int PARTS = DH / 128;           // parts of a K or V tile
   static constexpr uint32_t QT_BYTES = BM * DH * 2;
-  // raw granules: d_h = 128 one ring of four for K and V in turn, d_h = 256
-  // a ring of two for each
-  static constexpr int RING = PARTS == 1 ? 4 : 2;
-  // Converter warpgroups: one for d_h = 128, for d_h = 256 two of K and two of
-  // V, each for one granule of a part.  (One of each: 0.9 us a part, which a
-  // prompt of 16384 tokens waited for: 937 us.)
-  static constexpr int SPLIT = PARTS;              // warpgroups of a part
+  // raw granules: d_h = 128 one ring for K and V in turn, d_h = 256 a ring for each
+  static constexpr int RING = PARTS == 2 ? 2 : (NQ == 1 ? 8 : 4);
+  static constexpr int N_RAW = PARTS * RING;
+  static constexpr uint32_t SMEM = NQ * QT_BYTES + 4 * PART + N_RAW * RAW + sizeof(Shared);
+  static_assert(SMEM <= 232448 && N_RAW <= MAX_RAW, "shared memory budget");
+  // Converter warpgroups: one beside two of softmax, else two of K and (d_h =
+  // 256) two of V, each for one granule of a part.  (d_h = 256 with one of
+  // each: 0.9 us a part, which a prompt of 16384 tokens waited for: 937 us.)
+  static constexpr int SPLIT = NQ == 2 ? 1 : 2;    // warpgroups of a part
   static constexpr int CONV = PARTS * SPLIT;
   static constexpr int THREADS = 128 * (1 + CONV + NQ);
   // Registers per thread: control and converter warpgroups give some of the
@@ -105,8 +114,6 @@ struct Cfg {
   static constexpr int REGS_SOFT = PARTS == 1 ? 192 : 216;
   static_assert(REGS_CTRL + CONV * REGS_CONV + NQ * REGS_SOFT <= (1 + CONV + NQ) * REGS_LAUNCH,
                 "register split above the launch allocation");
-  static constexpr uint32_t SMEM = NQ * QT_BYTES + 4 * PART + 4 * RAW + sizeof(Shared);
-  static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 struct Params {
@@ -160,12 +167,12 @@ __device__ __forceinline__ float mask_max(uint32_t (&r)[32], uint32_t keep) {
   return fmaxf(a, b);
 }
 
-template <int DH, int G>
-__global__ void __launch_bounds__(Cfg<DH, G>::THREADS, 1)
+template <int DH, int G, int NQ>
+__global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
     flash8_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const Params p) {
   pdl_enter();
-  using C = Cfg<DH, G>;
+  using C = Cfg<DH, G, NQ>;
   if (*reinterpret_cast<volatile int*>(p.status) != 0) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -175,7 +182,7 @@ __global__ void __launch_bounds__(Cfg<DH, G>::THREADS, 1)
   uint8_t* sK = smem + C::NQ * C::QT_BYTES;   // two parts
   uint8_t* sV = sK + 2 * PART;                // two parts
   uint8_t* sR = sV + 2 * PART;                // raw granules
-  Shared& sh = *reinterpret_cast<Shared*>(sR + 4 * RAW);
+  Shared& sh = *reinterpret_cast<Shared*>(sR + C::N_RAW * RAW);
   if ((smem_u32(smem) & 1023u) != 0) {        // (never, by the declaration above)
     if (tid == 0) record_error(p.status, kDevErrTimeoutBase + kSiteQ);
     return;
@@ -220,9 +227,11 @@ __global__ void __launch_bounds__(Cfg<DH, G>::THREADS, 1)
       mbar_init(smem_u32(&sh.pv_done[s]), 1);
       mbar_init(smem_u32(&sh.o_final[s]), 1);
     }
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < C::N_RAW; ++s) {
       mbar_init(smem_u32(&sh.raw_full[s]), 1);
       mbar_init(smem_u32(&sh.raw_empty[s]), 4);
+    }
+    for (int s = 0; s < NMETA; ++s) {
       mbar_init(smem_u32(&sh.meta_full[s]), 1);
       mbar_init(smem_u32(&sh.meta_empty[s]), 4 * (nq + C::CONV));   // softmax and converter warps
     }
@@ -343,6 +352,38 @@ __global__ void __launch_bounds__(Cfg<DH, G>::THREADS, 1)
           ok = issue_pv(e, n_tiles - 1);
           if (ok) mma_commit_lead(lead, smem_u32(&sh.o_final[e]));
         }
+      } else if constexpr (C::PARTS == 1) {
+        // one query tile: S of even and of odd tiles
+        auto issue_pv = [&](int i) -> bool {
+          if (!wait_warp(sh.p_full[i & 1], (i >> 1) & 1, kSitePFull)) return false;
+          if (!wait_warp(sh.v_full[i & 1], (i >> 1) & 1, kSiteVFull)) return false;
+          tc_fence_after();
+          const uint32_t vb = v_addr + (i & 1) * PART;
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            mma_ts_lead(lead, tbase + O_COL, tbase + (i & 1) * 128 + k * 8,
+                        sdesc_sw128(vb + k * 2048, CHUNK, 1024), idesc_pv, (i > 0 || k > 0) ? 1u : 0u);
+          mma_commit_lead(lead, smem_u32(&sh.v_empty[i & 1]));
+          mma_commit_lead(lead, smem_u32(&sh.pv_done[i & 1]));
+          return true;
+        };
+        for (int i = 0; ok && i < n_tiles; ++i) {
+          ok = wait_warp(sh.k_full[i & 1], (i >> 1) & 1, kSiteKFull);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t kb = k_addr + (i & 1) * PART;
+#pragma unroll
+          for (int k = 0; k < DH / 16; ++k) {
+            const uint32_t off = (k >> 2) * CHUNK + (k & 3) * 32;
+            mma_ss_lead(lead, tbase + (i & 1) * 128, sdesc_sw128(q_addr + off, 16, 1024),
+                        sdesc_sw128(kb + off, 16, 1024), idesc_qk, k > 0 ? 1u : 0u);
+          }
+          mma_commit_lead(lead, smem_u32(&sh.k_empty[i & 1]));
+          mma_commit_lead(lead, smem_u32(&sh.s_full[i & 1]));
+          if (i > 0) ok = issue_pv(i - 1);
+        }
+        if (ok) ok = issue_pv(n_tiles - 1);
+        if (ok) mma_commit_lead(lead, smem_u32(&sh.o_final[0]));
       } else {
         auto issue_pv = [&](int i) -> bool {
           if (!wait_warp(sh.p_full[i & 1], (i >> 1) & 1, kSitePFull)) return false;
@@ -731,10 +772,10 @@ __global__ void __launch_bounds__(Cfg<DH, G>::THREADS, 1)
 
 // The parts of the cut units: CTA (u, y) adds those of 8 rows of unit u, a
 // warp each.
-template <int DH, int G>
+template <int DH, int G, int NQ>
 __global__ void __launch_bounds__(256) flash8_merge_kernel(const Params p) {
   pdl_enter();
-  using C = Cfg<DH, G>;
+  using C = Cfg<DH, G, NQ>;
   constexpr int ROWS = 8;
   const int unit = p.whole + blockIdx.x;
   const int bjs = p.B * p.H_kv, item = p.items - 1 - unit / bjs;
@@ -844,9 +885,9 @@ __global__ void __launch_bounds__(1024) first8_kernel(const int32_t* __restrict_
   if (tid == 0) first[static_cast<size_t>(b) * items + item] = min(found, hi);
 }
 
-template <int DH, int G>
+template <int DH, int G, int NQ>
 cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
-  using C = Cfg<DH, G>;
+  using C = Cfg<DH, G, NQ>;
   CUtensorMap tq, tk, tv;
   // Q' [B, T, H, d_h]: box {64 channels, the G heads of a kv head, TQ tokens, 1}
   const uint64_t dims[4] = {static_cast<uint64_t>(DH), static_cast<uint64_t>(p.H),
@@ -865,7 +906,7 @@ cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
   if (!encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.K8, kdims, kstr, kbox) ||
       !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.V8, kdims, kstr, kbox))
     return cudaErrorInvalidValue;
-  auto kern = flash8_kernel<DH, G>;
+  auto kern = flash8_kernel<DH, G, NQ>;
   int regs = 0;
   if (cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, &regs)) return e;
   // The softmax warpgroups' increases wait for what the others give up:
@@ -876,7 +917,7 @@ cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
   cudaError_t e =
       launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p);
   if (e != cudaSuccess || p.cut == 0) return e;
-  return launch_pdl(flash8_merge_kernel<DH, G>, dim3(p.cut, C::NQ * BM / 8), dim3(256), 0, stream, p);
+  return launch_pdl(flash8_merge_kernel<DH, G, NQ>, dim3(p.cut, C::NQ * BM / 8), dim3(256), 0, stream, p);
 }
 
 // How many units stay whole, and the cut of the others (fewer than the SMs),
@@ -980,14 +1021,19 @@ cudaError_t launch_flash8(const Flash8Args& a, cudaStream_t stream) {
   p.parts = plan.parts;
   p.first_part = plan.first_part;
   p.status = a.status;
-#define G3_FLASH8_CASE(DH_, G_) \
-  if (a.d_h == DH_ && G == G_) return launch_cfg<DH_, G_>(a.Q, p, stream);
-  G3_FLASH8_CASE(128, 1)
-  G3_FLASH8_CASE(128, 2)
-  G3_FLASH8_CASE(128, 4)
-  G3_FLASH8_CASE(256, 1)
-  G3_FLASH8_CASE(256, 2)
-  G3_FLASH8_CASE(256, 4)
+  // (a call with one query tile per kv head: its units stay one item each)
+  const bool two = a.d_h == 128 && a.T > BM / G;
+#define G3_FLASH8_CASE(DH_, G_, NQ_) \
+  if (a.d_h == DH_ && G == G_ && two == (NQ_ == 2)) return launch_cfg<DH_, G_, NQ_>(a.Q, p, stream);
+  G3_FLASH8_CASE(128, 1, 2)
+  G3_FLASH8_CASE(128, 2, 2)
+  G3_FLASH8_CASE(128, 4, 2)
+  G3_FLASH8_CASE(128, 1, 1)
+  G3_FLASH8_CASE(128, 2, 1)
+  G3_FLASH8_CASE(128, 4, 1)
+  G3_FLASH8_CASE(256, 1, 1)
+  G3_FLASH8_CASE(256, 2, 1)
+  G3_FLASH8_CASE(256, 4, 1)
 #undef G3_FLASH8_CASE
   return cudaErrorInvalidValue;
 }
