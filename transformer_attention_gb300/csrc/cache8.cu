@@ -225,7 +225,9 @@ constexpr int kSelHist = 256 * 32;   // digit counts, each lane its own
 // and the first of those equal to it, are written out in slot order.  Weights
 // and positions are read once; the keys stay in shared memory between the
 // rounds (a run longer than kSelKeys is read from L2 again).  Bound by the
-// rounds' latency: 131072 slots 20 us on eight CTAs; their 1 MB takes 0.2 us.
+// rounds' latency: 131072 slots 23 us on eight CTAs, 1000 slots 11 us on one;
+// their bytes take 0.2 us.  (A search bit by bit, one count over the CTA for
+// each, took 15 us for the 1000.)
 template <bool KEPT>
 __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const SelectParams p) {
   pdl_enter();
@@ -234,8 +236,7 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
   const int rank = cluster.block_rank(), C = cluster.num_blocks();
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // Counts [digit][lane]: weights of one magnitude share their first digit,
-  // and lanes adding to one word would wait for each other (131072 slots: 38
-  // us with four copies of the counts).
+  // and lanes adding to one word would wait for each other.
   extern __shared__ int hist[];
   uint32_t* keys = reinterpret_cast<uint32_t*>(hist + kSelHist);
   __shared__ int tot[2][256];        // this CTA's counts, for its cluster
@@ -449,7 +450,7 @@ struct MoveParams {
 // slots.  The numbers stay in registers between the search for the largest
 // value and the move to the block's own scale; a chain of three memory round
 // trips (which slots, their numbers, the stores) is paid once for U tiles.
-// (One tile per CTA: 115 us for 268 MB each way, four: 90 us.)
+// (One tile per CTA: 115 us for 268 MB each way, four: 105 us.)
 template <int DH, int U>
 __global__ void __launch_bounds__(kRowThreads) cache8_move_kernel(const MoveParams p) {
   pdl_enter();

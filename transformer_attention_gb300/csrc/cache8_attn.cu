@@ -11,7 +11,11 @@
 // byte of the cache is read once and meets at most 16 query rows, so HBM
 // bounds it: d_h = 128 needs 256 bytes per slot and kv head.  The two
 // contractions run on mma.sync m16n8k16 with the slots (K) and the channels
-// (V) on the 16-row side and the query rows on the 8-wide side: at one byte
+// (V) on the 16-row side and the query rows on the 8-wide side.  One token over
+// 131072 slots of 16 kv heads: 86 us, 6.3 TB/s; 9 to 16 rows double the
+// fragments and reach about 3 TB/s at d_h = 128 (16 rows over 65536 slots of 8
+// kv heads 50 us, 8 rows 35), bound by the latency of the dozen warps that fit
+// an SM.  At one byte
 // per number the fp32 CUDA cores would need 4 FMAs per byte for 4 rows, about
 // their whole rate at the HBM rate, while these MMAs take under a fifth of
 // theirs (measured 1024 fp16 FMA per clock and SM).  A tcgen05 tile has 128
@@ -33,13 +37,13 @@
 //     rounding); sums and maxima are fp32.
 // The slots of a (row, kv head) are split over CTAs: up to eight form a
 // cluster that merges its parts through distributed shared memory, more leave
-// them to a second launch.  For weight_sum a second launch adds up exp2(logit
-// - max) / sum from the logits that the first one left in the workspace (4
-// bytes per query row and slot, against 2 d_h for K' and V; reading K' again
-// would cost d_h).  On a local layer the CTAs take the last window's worth of
-// slots at once, and look through the positions of all earlier slots for ones
-// that a query still sees (positions may have gaps) while the first copies
-// are under way.
+// them to a second launch (merge8_kernel).  For weight_sum a last launch
+// (weigh8_kernel) adds up exp2(logit - max) / sum from the logits that the
+// first one left in the workspace (4 bytes per query row and slot, against 2
+// d_h for K' and V; reading K' again would cost d_h).  On a local layer the
+// CTAs take the last window's worth of slots at once, and look through the
+// positions of all earlier slots for ones that a query still sees (positions
+// may have gaps) while the first copies are under way.
 #include <algorithm>
 #include <climits>
 
@@ -279,8 +283,8 @@ __global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTA
   }
 
   // ---------------- consumers
-  // Q fragments (while the first copies are under way): k columns {2c, 2c+1, 2c+8, 2c+9} of a 16-channel chunk are
-  // the channels 4c .. 4c+3, row n = lane / 4.
+  // Q fragments (while the first copies are under way): k columns {2c, 2c+1,
+  // 2c+8, 2c+9} of a 16-channel chunk are the channels 4c .. 4c+3, row n = lane / 4.
 #pragma unroll 4
   for (int i = tid; i < C::NC * C::NN * 32; i += kConsumers) {
     const int l = i & 31, nt = (i >> 5) % C::NN, ch = (i >> 5) / C::NN;
@@ -792,9 +796,9 @@ int max_splits(int B, int S, int H_kv) {
 // full rate of HBM (2.6 ns for d_h = 128, 5.1 for 256), the tiles all
 // together, or those of one CTA at the pace of one among `full` (the CTAs
 // that saturate HBM), whichever is longer, about 2 us per round of CTAs, and
-// for a second launch 3.5 us and 50 ns per split, which up to eight CTAs of a
-// cluster save (with weights there is one anyway).  12B-shaped batch of 16 over 7777 slots,
-// d_h = 256: 896 CTAs in three rounds 88 us, 256 CTAs in one 82 us.
+// for a merging launch 3.5 us and 50 ns per split, which up to eight CTAs of a
+// cluster save.  12B-shaped batch of 16 over 7777 slots, d_h = 256: 896 CTAs
+// in three rounds 88 us, 256 CTAs in one 82 us.
 struct Split {
   int n;
   bool cluster;
