@@ -138,6 +138,7 @@ struct Params {
   int o_f16, B, T, S, H, H_kv, nb, end, window, items;
   int whole, cut, parts;      // units in one piece, units cut, into how many parts
   float first_part;           // share of a cut unit's tiles in its first part
+  uint32_t zero;              // 0, which the compiler does not know
   int* status;
 };
 
@@ -550,8 +551,21 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
           x[4 * g + k][0] = *reinterpret_cast<const uint2*>(src + swap);
           x[4 * g + k][1] = *reinterpret_cast<const uint2*>(src + (swap ^ 8));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[r]));
+      }
+      if (!ok) break;
+      // The copy that refills a granule may start once its barrier is arrived
+      // on: the address takes every lane's loaded words in, so that the
+      // arrival cannot overtake the loads (it did where nothing used them
+      // before it: calls back to back gave wrong rows).
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        uint32_t got = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          got |= (x[4 * g + k][0].x | x[4 * g + k][0].y) | (x[4 * g + k][1].x | x[4 * g + k][1].y);
+        got = __reduce_or_sync(0xffffffffu, got) & p.zero;
+        if (lane == 0)
+          mbar_arrive(smem_u32(&sh.raw_empty[r0 + (2 * q + g0 + g) % C::RING]) + got);
       }
       ok = ok && wait_warp(v ? sh.v_empty[buf] : sh.k_empty[buf], (use & 1) ^ 1, kSiteKEmpty);
       if (!ok) break;
@@ -676,9 +690,11 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
           m2 = mask_max(rc, keep[2]);
           m3 = mask_max(rd, keep[3]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.meta_empty[i % NMETA]));
         const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * LOG2E;
+        // (mx takes what was read of the tile's positions in, as above)
+        __syncwarp();
+        if (lane == 0)
+          mbar_arrive(smem_u32(&sh.meta_empty[i % NMETA]) + (__float_as_uint(mx) & p.zero));
         const bool grow = mx > m_used + RESCALE_THRESHOLD;
         if (__any_sync(0xffffffffu, grow)) {
           const float m_new = grow ? mx : m_used;
@@ -1026,6 +1042,7 @@ cudaError_t launch_flash8(const Flash8Args& a, cudaStream_t stream) {
   p.cut = plan.cut;
   p.parts = plan.parts;
   p.first_part = plan.first_part;
+  p.zero = 0;
   p.status = a.status;
   // (a call with one query tile per kv head: its units stay one item each)
   const bool two = a.d_h == 128 && a.T > BM / G;
