@@ -141,6 +141,7 @@ struct Params {
   float* logits;              // [B, H_kv, T*G, S64] base-2 logits, or null
   void* O;
   int o_f16, B, T, S, H, H_kv, nb, end, window, nsplit, cluster, late;
+  uint32_t zero;              // 0, which the compiler does not know
   int* status;
 };
 
@@ -419,6 +420,7 @@ __global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTA
     if (p.logits != nullptr)
       lg = p.logits +
            (static_cast<size_t>(b) * p.H_kv + j) * R * (static_cast<size_t>(p.nb) * kTile) + s;
+    uint32_t loaded = 0;             // words of the tile's last load
     if ((b0 | b1) != 0) {
       const uint32_t kt = smem_u32(ring + st * C::TILE);
       // S^T (16 slots x 8 rows): two accumulators shorten the chain
@@ -510,6 +512,7 @@ __global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTA
         uint32_t r[4];
         const int ch = cp * 2 + mch;
         ldsm4_trans(vt + (cp >> 2) * C::BOX + roff + (((ch & 7) ^ rxor) << 4), r);
+        if (cp == C::NC / 2 - 1) loaded = (r[0] | r[1]) | (r[2] | r[3]);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           // bytes (slot 2c: channels 2g, 2g+1; slot 2c+1: the same) to
@@ -534,8 +537,10 @@ __global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTA
                 -INFINITY;
         }
     }
+    // The next copy into the stage may start once this arrives: its address
+    // takes the last load's words in, so that it cannot overtake the loads.
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
+    if (lane == 0) mbar_arrive(smem_u32(&empty[st]) + (loaded & p.zero));
   }
 
   // ---------------- merge the warps along the slots (records in the ring, which no copy
@@ -969,6 +974,7 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   p.cluster = sp.cluster ? 1 : 0;
   // (the last slots that positions without gaps let a window's tokens see)
   p.late = window > 0 ? tiles : INT_MAX;
+  p.zero = 0;
   p.status = status;
   const dim3 grid(nsplit, H_kv, B);
   const bool one = T * (H / H_kv) <= 8;
