@@ -63,3 +63,93 @@ def test_calls_back_to_back(case):
     for o in outs:
         assert torch.equal(o[0], want[0])
     assert G3.gemma3_attn_check_status() == 0
+
+
+@pytest.mark.parametrize("H,H_kv,d_h,T", [(32, 16, 128, 1), (16, 8, 256, 2), (16, 16, 128, 20)])
+def test_steps_that_grow_scales(H, H_kv, d_h, T):
+    """Write and attend in turn without a gap, every step with larger values in
+    some heads, so that the block's scales of those grow: each step sees the
+    scales that its own write left."""
+    import transformer_attention_gb300 as G3
+    B, S, steps = 6, 2000, 40
+    g = torch.Generator(device="cuda").manual_seed(d_h + T)
+    kvd = H_kv * d_h
+    rows = (torch.randn((steps, B * T, 2, H_kv, d_h), generator=g, device="cuda") * 2.0 ** -6)
+    grow = torch.rand((steps, 1, 2, H_kv, 1), generator=g, device="cuda") < 0.3
+    rows *= 2.0 ** torch.cumsum(grow.float(), 0).clamp(max=18)
+    rows = rows.half().view(steps, B * T, 2 * kvd)
+    Q = (torch.randn((steps, B, T, H, d_h), generator=g, device="cuda") / 64).half()
+    n = G3.gemma3_cached8_attention_workspace_size(B, T, S, H, H_kv, d_h, True)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    seg = [torch.arange(300 + i * T, 300 + (i + 1) * T, device="cuda", dtype=torch.int32).repeat(B, 1)
+           for i in range(steps)]
+
+    def run(sync):
+        cache = G3.new_kv_cache8(B, S, H_kv, d_h, "cuda")
+        cache[4][:, :300] = torch.arange(300, device="cuda", dtype=torch.int32)
+        cache[2].fill_(2.0 ** -15)
+        cache[3].fill_(2.0 ** -15)
+        w = torch.zeros((B, S), device="cuda")
+        outs = [torch.empty((B, T, H, d_h), dtype=torch.float16, device="cuda") for _ in range(steps)]
+        torch.cuda.synchronize()
+        for i in range(steps):
+            end = 300 + i * T
+            G3.gemma3_kv_cache8_write(rows[i], rows[i][:, kvd:], 2 * kvd, seg[i], None, B, T, S, end,
+                                      H_kv, d_h, *cache)
+            if sync:
+                torch.cuda.synchronize()
+            G3.gemma3_cached8_attention(Q[i], *cache, seg[i], None, outs[i], G3.GEMMA3_F16, w, B, T, S,
+                                        end, H, H_kv, d_h, 0, ws, n)
+            if sync:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs + [w] + list(cache[2:4])
+
+    want = run(True)
+    for _ in range(6):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
+    assert G3.gemma3_attn_check_status() == 0
+
+
+@pytest.mark.parametrize("T,d_h", [(1, 128), (3, 256), (200, 128), (200, 256)])
+def test_two_inputs_in_turn(T, d_h):
+    """Two inputs in turn through one workspace, without a gap."""
+    import transformer_attention_gb300 as G3
+    B, S, end, H, H_kv = 2, 9000, 8000, 16, 8
+    g = torch.Generator(device="cuda").manual_seed(T)
+    ins = []
+    for _ in range(2):
+        cache = G3.new_kv_cache8(B, S, H_kv, d_h, "cuda")
+        for t in cache[:2]:
+            t.view(torch.uint8).copy_((torch.randn(t.shape, generator=g, device="cuda") * 60)
+                                      .to(torch.float8_e4m3fn).view(torch.uint8))
+        for t in cache[2:4]:
+            t.copy_(2.0 ** torch.randint(-8, -5, t.shape, generator=g, device="cuda"))
+        cache[4][:, :end + T] = torch.arange(end + T, device="cuda", dtype=torch.int32)
+        ins.append(((torch.randn((B, T, H, d_h), generator=g, device="cuda") / 8).half(), cache))
+    seg = torch.arange(end, end + T, device="cuda", dtype=torch.int32).repeat(B, 1)
+    n = G3.gemma3_cached8_attention_workspace_size(B, T, S, H, H_kv, d_h, True)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def call(i, O, w):
+        G3.gemma3_cached8_attention(ins[i][0], *ins[i][1], seg, None, O, G3.GEMMA3_BF16, w, B, T, S, end,
+                                    H, H_kv, d_h, 0, ws, n)
+
+    def outputs():
+        return (torch.empty((B, T, H, d_h), dtype=torch.bfloat16, device="cuda"),
+                torch.zeros((B, S), device="cuda"))
+
+    want = [outputs(), outputs()]
+    for i in (0, 1):
+        torch.cuda.synchronize()
+        call(i, *want[i])
+    torch.cuda.synchronize()
+    outs = [outputs() for _ in range(20)]
+    torch.cuda.synchronize()
+    for k, o in enumerate(outs):
+        call(k % 2, *o)
+    torch.cuda.synchronize()
+    for k, o in enumerate(outs):
+        assert torch.equal(o[0], want[k % 2][0]) and torch.equal(o[1], want[k % 2][1])
+    assert G3.gemma3_attn_check_status() == 0

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kRowThreads) cache8_write_kernel(const WritePa
   const int valid = p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0);
   const int s0 = blk * kTile, c = (tid % TPR) * 8;
   const bool held = s0 < p.end;                // the block holds earlier tokens
-  const float old = held ? *scale : 0.f;
+  const float old = held ? __ldcg(scale) : 0.f;
 
   uint4 x[NP];
   float mx = 0.f;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kRowThreads) cache8_write_kernel(const WritePa
     const int t = s0 + i * RPP + tid / TPR - p.end;
     x[i] = make_uint4(0, 0, 0, 0);
     if (t >= 0 && t < valid && t < p.T)
-      x[i] = __ldg(reinterpret_cast<const uint4*>(
+      x[i] = __ldcg(reinterpret_cast<const uint4*>(
           rows + (static_cast<size_t>(b) * p.T + t) * p.ld + static_cast<size_t>(j) * DH + c));
   }
 #pragma unroll
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kRowThreads) cache8_write_kernel(const WritePa
     if (t >= 0 && t < p.T) {
       *d = pack8(x[i], inv);
     } else if (t < 0 && s != old) {
-      const uint2 n = *d;
+      const uint2 n = __ldcg(d);
       *d = make_uint2(c8_rescale4(n.x, old * inv), c8_rescale4(n.y, old * inv));
     }
   }
@@ -167,8 +167,8 @@ __global__ void __launch_bounds__(256) cache8_read_kernel(
     t[k] = t0 + q;
     u[k] = u0 + i - q * row_units;
     if (base + i < total) {
-      v[k] = __ldg(reinterpret_cast<const uint4*>(num + (static_cast<size_t>(t[k]) * row_units + u[k]) * 16));
-      s[k] = __ldg(scale + static_cast<size_t>((first + t[k]) / kC8Block) * H_kv + u[k] / head_units);
+      v[k] = __ldcg(reinterpret_cast<const uint4*>(num + (static_cast<size_t>(t[k]) * row_units + u[k]) * 16));
+      s[k] = __ldcg(scale + static_cast<size_t>((first + t[k]) / kC8Block) * H_kv + u[k] / head_units);
     }
   }
 #pragma unroll
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
   // Warp w owns the slots w0 .. w1 of the CTA's run, 32 next to each other at
   // a time (a thread reads back only keys that it stored).
   const int seg = run / 32, w0 = lo + warp * seg, w1 = min(hi, w0 + seg);
-  auto fresh_key = [&](int s) { return evict_key(__ldg(w + s), __ldg(pos + s), s, p.first_recent); };
+  auto fresh_key = [&](int s) { return evict_key(__ldcg(w + s), __ldcg(pos + s), s, p.first_recent); };
   if constexpr (KEPT) {
     for (int base = w0 + lane; base < w1; base += 8 * 32) {
       uint32_t k[8];
@@ -405,8 +405,8 @@ __global__ void __launch_bounds__(kSelThreads) cache8_select_kernel(const Select
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int s = min(base + 32 * i + lane, w1 - 1);
-      ws[i] = __ldg(w + s);
-      ps[i] = __ldg(pos + s);
+      ws[i] = __ldcg(w + s);
+      ps[i] = __ldcg(pos + s);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kRowThreads) cache8_move_kernel(const MovePara
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int d = blk * kTile + i * RPP + tid / TPR;
-    from[i] = d < p.keep ? __ldg(p.kept + static_cast<size_t>(b) * p.keep + d) : -1;
+    from[i] = d < p.keep ? __ldcg(p.kept + static_cast<size_t>(b) * p.keep + d) : -1;
   }
   uint4 n[U][NP];
   float sc[U][NP];
@@ -484,9 +484,9 @@ __global__ void __launch_bounds__(kRowThreads) cache8_move_kernel(const MovePara
       n[u][i] = make_uint4(0, 0, 0, 0);
       sc[u][i] = 0.f;
       if (hk < n_hk && from[i] >= 0) {
-        n[u][i] = __ldg(reinterpret_cast<const uint4*>(
+        n[u][i] = __ldcg(reinterpret_cast<const uint4*>(
             (isv ? p.V8 : p.K8) + src0 + static_cast<size_t>(from[i]) * ldc + j * DH + c));
-        sc[u][i] = __ldg((isv ? p.V_scale : p.K_scale) + sc0 +
+        sc[u][i] = __ldcg((isv ? p.V_scale : p.K_scale) + sc0 +
                          static_cast<size_t>(from[i] / kC8Block) * p.H_kv + j);
       }
     }

@@ -9,6 +9,11 @@
 // number that stays normal exactly, and every value is an exact fp32 product.
 // With exponents from -15 up a value is a multiple of 2^-24, fp16's last
 // step, so reading a cache back as fp16 rounds nothing below fp16's largest.
+//
+// The kernels over this cache read what another launch may have written
+// (numbers, scales, positions, weights, scratch) past L1, by __ldcg: a kernel
+// starts while the one before it runs (pdl_enter), so that a line which that
+// one still reads into an SM's L1 may not be dropped again before this one.
 #pragma once
 
 #include <cstdint>

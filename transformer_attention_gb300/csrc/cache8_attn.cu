@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTA
     uint2 q = make_uint2(0, 0);
     if (r < R) {
       const int t = r / G, h = j * G + r % G;
-      q = __ldg(reinterpret_cast<const uint2*>(
+      q = __ldcg(reinterpret_cast<const uint2*>(
           p.Q + ((static_cast<size_t>(b) * p.T + t) * p.H + h) * DH + ch * 16 + (l & 3) * 4));
     }
     qf[i] = q;
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTA
       int ps[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        ps[k] = s + k * kConsumers < e1 ? __ldg(row + s + k * kConsumers) : -1;
+        ps[k] = s + k * kConsumers < e1 ? __ldcg(row + s + k * kConsumers) : -1;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (ps[k] >= lo && ps[k] <= up) {
@@ -387,10 +387,10 @@ __global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTA
     pos0 = pos1 = -1;
     if (i < n_tiles) {
       const int k = tile_at(i), s = k * kTile + so;
-      if (s < hi) pos0 = __ldg(posr + s);
-      if (s + 8 < hi) pos1 = __ldg(posr + s + 8);
-      ks = __ldg(ksp + static_cast<size_t>(k) * p.H_kv);
-      vs = __ldg(vsp + static_cast<size_t>(k) * p.H_kv);
+      if (s < hi) pos0 = __ldcg(posr + s);
+      if (s + 8 < hi) pos1 = __ldcg(posr + s + 8);
+      ks = __ldcg(ksp + static_cast<size_t>(k) * p.H_kv);
+      vs = __ldcg(vsp + static_cast<size_t>(k) * p.H_kv);
     }
   };
   fetch(0);
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(DH) merge8_kernel(const MergeParams p) {
   float M = -INFINITY, L = 0.f;
 #pragma unroll
   for (int i = 0; i < kMaxSplits / DH; ++i) {
-    mine[i] = tid + i * DH < p.parts ? st[tid + i * DH] : make_float2(-INFINITY, 0.f);
+    mine[i] = tid + i * DH < p.parts ? __ldcg(st + tid + i * DH) : make_float2(-INFINITY, 0.f);
     M = fmaxf(M, mine[i].x);
   }
 #pragma unroll
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(DH) merge8_kernel(const MergeParams p) {
   const float* base = p.part + row * p.parts * DH + tid;
   float acc = 0.f;
 #pragma unroll 8
-  for (int i = 0; i < p.parts; ++i) acc = fmaf(fw[i], __ldg(base + static_cast<size_t>(i) * DH), acc);
+  for (int i = 0; i < p.parts; ++i) acc = fmaf(fw[i], __ldcg(base + static_cast<size_t>(i) * DH), acc);
   store_o(p.O, p.o_f16, row * DH + tid, L != 0.f ? acc / L : 0.f);
   if (tid == 0 && p.fstat != nullptr) p.fstat[row] = make_float2(M, L);
 }
@@ -727,15 +727,15 @@ __global__ void __launch_bounds__(256) weigh8_kernel(const WeighParams p) {
   const int k = s / kTile;
   bool seen = s < tl.hi;
   if (seen && k < tl.k0) {
-    const int2 e = p.swept[static_cast<size_t>(b) * p.nsplit + k / tl.per_early];
+    const int2 e = __ldcg(p.swept + static_cast<size_t>(b) * p.nsplit + k / tl.per_early);
     seen = k >= e.x && k < e.y;
   }
   const float* lg = p.logits + static_cast<size_t>(b) * rows * S64 + s;
   float* out = p.weight_sum + static_cast<size_t>(b) * p.S;
   float2 old = make_float2(0.f, 0.f), acc = make_float2(0.f, 0.f);
   if (seen && rg == 0) {
-    old.x = out[s];
-    if (s + 1 < p.S) old.y = out[s + 1];
+    old.x = __ldcg(out + s);
+    if (s + 1 < p.S) old.y = __ldcg(out + s + 1);
   }
   for (int r0 = 0, par = 0; r0 < rows; r0 += WROWS, par ^= 1) {
     const int n = min(WROWS, rows - r0);
@@ -746,14 +746,14 @@ __global__ void __launch_bounds__(256) weigh8_kernel(const WeighParams p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       x[i] = seen && RW * i + rg < n
-                 ? __ldg(reinterpret_cast<const float2*>(lg + (r0 + RW * i + rg) * S64))
+                 ? __ldcg(reinterpret_cast<const float2*>(lg + (r0 + RW * i + rg) * S64))
                  : make_float2(0.f, 0.f);
     if (tid < WROWS) {
       float2 st = make_float2(0.f, 0.f);
       int lim = -1;
       if (tid < n) {
         const int j = (r0 + tid) / R, e = (r0 + tid) % R, t = e / G;
-        st = __ldg(p.stat + (static_cast<size_t>(b) * p.T + t) * p.H + j * G + e % G);
+        st = __ldcg(p.stat + (static_cast<size_t>(b) * p.T + t) * p.H + j * G + e % G);
         lim = t < valid ? p.end + t : -1;
       }
       rs[par][tid] = make_float2(st.x == -INFINITY ? 0.f : st.x, st.y != 0.f ? 1.f / st.y : 0.f);

@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
   const int t_end = min(t0 + C::NQ * C::TQ, valid);          // past the last valid token
   const int nq = C::NQ == 2 && t0 + C::TQ < p.T ? 2 : 1;     // query tiles with tokens
   const int hi = t_end > t0 ? p.end + t_end : 0;
-  int lo = p.first != nullptr ? p.first[static_cast<size_t>(b) * p.items + item] : 0;
+  int lo = p.first != nullptr ? __ldcg(p.first + static_cast<size_t>(b) * p.items + item) : 0;
   lo = min(lo, hi) / kC8Block * kC8Block;
   int n_tiles = (hi - lo + BN - 1) / BN, first_tile = 0;
   if (!whole) {
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
       if (p.window > 0) {
         int qn = INT_MAX, qx = INT_MIN;
         for (int t = t0 + lane; t < t_end; t += 32) {
-          const int q = __ldg(p.qpos + static_cast<size_t>(b) * p.T + t);
+          const int q = __ldcg(p.qpos + static_cast<size_t>(b) * p.T + t);
           qn = min(qn, q);
           qx = max(qx, q);
         }
@@ -456,10 +456,10 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int s = s_base + i * BN + k * 32 + lane;
-          nx[k] = s < hi ? __ldg(posr + s) : -1;
+          nx[k] = s < hi ? __ldcg(posr + s) : -1;
         }
         if (lane < 4)
-          ns = __ldg(sc + static_cast<size_t>(min((s_base + i * BN) / kC8Block + (lane & 1), p.nb - 1)) *
+          ns = __ldcg(sc + static_cast<size_t>(min((s_base + i * BN) / kC8Block + (lane & 1), p.nb - 1)) *
                               p.H_kv);
       };
       fetch(0);
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
       const int lim = row_valid ? p.end + t : -1;            // last visible slot
       int plo = 0, phi = INT_MAX;
       if (p.window > 0 && row_valid) {
-        const int qp = __ldg(p.qpos + static_cast<size_t>(b) * p.T + t);
+        const int qp = __ldcg(p.qpos + static_cast<size_t>(b) * p.T + t);
         window_range(qp, qp, p.window, plo, phi);
       }
       // over the warp's valid rows (the others are not stored)
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(256) flash8_merge_kernel(const Params p) {
     for (int v = 0; v < DH / 128; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c0 = 0; c0 < p.parts; c0 += 32) {
       const int n = min(32, p.parts - c0);
-      const float2 st = lane < n ? p.pstat[at(c0 + lane)] : make_float2(-INFINITY, 0.f);
+      const float2 st = lane < n ? __ldcg(p.pstat + at(c0 + lane)) : make_float2(-INFINITY, 0.f);
       float m = st.x;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(256) flash8_merge_kernel(const Params p) {
         const float4* src = reinterpret_cast<const float4*>(p.part + at(c0 + c) * DH);
 #pragma unroll
         for (int v = 0; v < DH / 128; ++v) {
-          const float4 o = __ldg(src + v * 32 + lane);
+          const float4 o = __ldcg(src + v * 32 + lane);
           acc[v].x = fmaf(fc, o.x, acc[v].x);
           acc[v].y = fmaf(fc, o.y, acc[v].y);
           acc[v].z = fmaf(fc, o.z, acc[v].z);
@@ -879,7 +879,7 @@ __global__ void __launch_bounds__(1024) first8_kernel(const int32_t* __restrict_
   const int hi = t_end > t0 ? end + t_end : 0;
   int qn = INT_MAX, qx = INT_MIN;
   for (int t = t0 + (tid & 31); t < t_end; t += 32) {
-    const int q = __ldg(qpos + static_cast<size_t>(b) * T + t);
+    const int q = __ldcg(qpos + static_cast<size_t>(b) * T + t);
     qn = min(qn, q);
     qx = max(qx, q);
   }
@@ -895,7 +895,7 @@ __global__ void __launch_bounds__(1024) first8_kernel(const int32_t* __restrict_
 #pragma unroll
     for (int k = 7; k >= 0; --k) {
       const int s = base + k * 1024 + tid;
-      const int ps = s < hi ? __ldg(row + s) : -1;
+      const int ps = s < hi ? __ldcg(row + s) : -1;
       if (ps >= plo && ps <= phi) best = s;
     }
     best = __reduce_min_sync(0xffffffffu, best);

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   if (warp < 4) {
     const int s = s_tile + tid;
-    const int ps = s < hi ? __ldg(p.posc + static_cast<size_t>(b) * p.S + s) : -1;
+    const int ps = s < hi ? __ldcg(p.posc + static_cast<size_t>(b) * p.S + s) : -1;
     const int mn = __reduce_min_sync(0xffffffffu, ps >= 0 ? ps : INT_MAX);
     const int mx = __reduce_max_sync(0xffffffffu, ps);
     if (lane == 0 && mx >= 0) {
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int t = max(0, s_tile - p.end) + tid; t < valid; t += THREADS) {
       bool see = true;
       if (p.window > 0) {
-        const int q = __ldg(p.qpos + static_cast<size_t>(b) * p.T + t);
+        const int q = __ldcg(p.qpos + static_cast<size_t>(b) * p.T + t);
         int plo, phi;
         window_range(q, q, p.window, plo, phi);
         see = plo <= pmax && phi >= pmin;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int it = 0; it < 8; ++it) {
         const int s = s_tile + row0 + it * 16;
-        ok |= (s < hi && __ldg(posr + s) >= 0 ? 1u : 0u) << it;
+        ok |= (s < hi && __ldcg(posr + s) >= 0 ? 1u : 0u) << it;
       }
       // a part: 128 slots x 128 channels, 128 bytes per thread
       uint2 x[8][2];
@@ -251,12 +251,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint2* src = reinterpret_cast<const uint2*>(
                 num + static_cast<size_t>(s_tile + row0 + it * 16) * p.H_kv * DH + h * DH +
                 (q % C::PARTS) * 128);
-            x[it][0] = __ldg(src + swap);
-            x[it][1] = __ldg(src + 1 - swap);
+            x[it][0] = __ldcg(src + swap);
+            x[it][1] = __ldcg(src + 1 - swap);
           }
         }
-        sc0 = __ldg(sc + static_cast<size_t>(blk) * p.H_kv + h);
-        sc1 = __ldg(sc + static_cast<size_t>(min(blk + 1, p.nb - 1)) * p.H_kv + h);
+        sc0 = __ldcg(sc + static_cast<size_t>(blk) * p.H_kv + h);
+        sc1 = __ldcg(sc + static_cast<size_t>(min(blk + 1, p.nb - 1)) * p.H_kv + h);
       };
       fetch(0);
       for (int q = 0; q < n_parts; ++q) {
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int wg = (warp - 8) >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int s = s_tile + r;
-    const int ps = s < hi ? __ldg(p.posc + static_cast<size_t>(b) * p.S + s) : -1;
+    const int ps = s < hi ? __ldcg(p.posc + static_cast<size_t>(b) * p.S + s) : -1;
     // query positions that see this slot on a local layer
     int qlo = INT_MIN, qhi = INT_MAX;
     if (p.window > 0) window_range(ps, ps, p.window, qlo, qhi);
@@ -298,10 +298,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (n >= n_units) return;
       const int j = head_of(u0 + n), t0 = tile_of(u0 + n) * C::TQ;
       const size_t row = static_cast<size_t>(t0) * G + r;
-      nx = row < rows ? __ldg(p.rowstat + (static_cast<size_t>(b) * p.H_kv + j) * rows + row)
+      nx = row < rows ? __ldcg(p.rowstat + (static_cast<size_t>(b) * p.H_kv + j) * rows + row)
                       : make_float2(INFINITY, 0.f);
       if (p.window > 0 && r < C::TQ && t0 + r < p.T)
-        nq = __ldg(p.qpos + static_cast<size_t>(b) * p.T + t0 + r);
+        nq = __ldcg(p.qpos + static_cast<size_t>(b) * p.T + t0 + r);
     };
     fetch(wg);
     bool ok = true;
@@ -391,8 +391,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     total += other[r];
     if (p.usplit > 1)
       p.wpart[(static_cast<size_t>(us) * p.B + b) * p.tiles * BM + s] = total;
-    else if (s < hi && total != 0.f)
-      p.weight_sum[static_cast<size_t>(b) * p.S + s] += total;
+    else if (s < hi && total != 0.f) {
+      float* w = p.weight_sum + static_cast<size_t>(b) * p.S + s;
+      *w = __ldcg(w) + total;
+    }
   }
   if (warp == 1) {
     tc_fence_after();
@@ -407,8 +409,9 @@ __global__ void __launch_bounds__(256) wadd8_kernel(const float* __restrict__ wp
   const int s = blockIdx.x * 256 + threadIdx.x, b = blockIdx.y;
   if (s >= hi) return;
   float a = 0.f;
-  for (int k = 0; k < usplit; ++k) a += __ldg(wpart + (static_cast<size_t>(k) * B + b) * ld + s);
-  if (a != 0.f) weight_sum[static_cast<size_t>(b) * S + s] += a;
+  for (int k = 0; k < usplit; ++k) a += __ldcg(wpart + (static_cast<size_t>(k) * B + b) * ld + s);
+  float* w = weight_sum + static_cast<size_t>(b) * S + s;
+  if (a != 0.f) *w = __ldcg(w) + a;
 }
 
 template <int DH, int G>
