@@ -15,7 +15,7 @@
 // 3500 clocks at 128 bytes each against 2050 of MMA; two query tiles of d_h =
 // 128 320 KB, 2500 against 2050.  (Without the conversion's arithmetic and
 // stores a prompt of 16384 tokens, d_h = 256, takes 603 us instead of 818.)
-// 1024 tokens over 32768 slots, 27B-shaped: 395 us, 1.37 PFLOP/s.
+// 1024 tokens over 32768 slots, 27B-shaped: 402 us, 1.35 PFLOP/s.
 //
 // Warps (d_h = 128, two query tiles e = 0, 1):
 //   0      TMA of the Q tiles (and for d_h = 256 of V's bytes)
@@ -39,8 +39,7 @@
 // the SMs take a unit per CTA; the units left over, fewer than the SMs, are
 // cut along their slots (plan8), into equal parts where several fit, else into
 // a large part each and small ones that the remaining SMs take one after
-// another; flash8_merge_kernel adds the parts.  (128 units on 152 SMs: 410 us
-// uncut for a 1024-token chunk over 32768 slots, 27B-shaped.)
+// another; flash8_merge_kernel adds the parts.
 #include <algorithm>
 #include <climits>
 
@@ -198,7 +197,8 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
   // CTAs: the whole units, the first parts of the cut ones, the other parts.
   // Units: the latest tokens of every batch row and kv head first, which have
   // the most slots on a causal prompt.  (A prompt of 4096 tokens, 27B-shaped:
-  // 150 us with the items of a head next to each other and the last ones cut.)
+  // 124 us, and 150 with the items of a head next to each other and the last
+  // ones cut.)
   const int head_units = p.whole + p.cut, rest = static_cast<int>(blockIdx.x) - head_units;
   const int unit = rest < 0 ? blockIdx.x : p.whole + rest % p.cut;
   const int pt = rest < 0 ? 0 : 1 + rest / p.cut;           // part
@@ -944,10 +944,13 @@ cudaError_t launch_cfg(const void* Q, const Params& p, cudaStream_t stream) {
 
 // How many units stay whole, and the cut of the others (fewer than the SMs),
 // where the parts' rounds end earliest: counted in KV tiles, with a start and
-// an end of a CTA worth kStartTiles and the merge worth as much.  `least` is
+// an end of a CTA worth kStartTiles, the merge as much and a tile more for
+// every kPartsPerTile parts, which pass through memory (256 units of 24 tiles:
+// 103 us cut, 89 uncut; 128 of 256 tiles 404 and 429; 8 of 9 tiles 21 and 29).
+// `least` is
 // the tiles of the shortest unit: where several rounds of units are as uneven
 // as on a causal prompt, the short last ones fill the gaps uncut.
-constexpr int kStartTiles = 3;
+constexpr int kStartTiles = 3, kPartsPerTile = 48;
 constexpr int kMaxCutParts = 320;            // parts that the workspace has room for
 
 struct Plan8 {
@@ -964,8 +967,10 @@ Plan8 plan8(long long units, int tiles, int least, int sms) {
   float first = 1.f;
   // equal parts, all in one round
   const int k = std::min(sms / rest, tiles);
-  if (k >= 2 && (tiles + k - 1) / k + 2 * kStartTiles < best) {
-    best = (tiles + k - 1) / k + 2 * kStartTiles;
+  auto merge = [&](int n) { return kStartTiles + rest * n / kPartsPerTile; };
+  const int even = (tiles + k - 1) / std::max(k, 1) + kStartTiles + merge(k);
+  if (k >= 2 && even < best) {
+    best = even;
     parts = k;
     first = 1.f / k;
   }
@@ -973,7 +978,7 @@ Plan8 plan8(long long units, int tiles, int least, int sms) {
   if (k < 2) {
     const int q = (rest + sms - rest - 1) / (sms - rest);
     const int small = std::max(1, (tiles - (q - 1) * kStartTiles) / (q + 1));
-    const int end = std::max(tiles - small + kStartTiles, q * (small + kStartTiles)) + kStartTiles;
+    const int end = std::max(tiles - small + kStartTiles, q * (small + kStartTiles)) + merge(2);
     if (small < tiles && end < best) {
       best = end;
       parts = 2;
