@@ -148,3 +148,18 @@ def test_windows_over_positions_that_skip(T, d_h, stride):
                torch.float16)
     d = 2 * ((d_h / 16 + 4) * 2.0 ** -22 * float(A.max()) + 2.0 ** -21)
     assert ((wsum.cpu().double() - w).abs() <= (d + (T * H + 2) * 2.0 ** -23) * w).all()
+
+
+CUT = [
+    (4, 256, 4300, 4000, 12, 12, 256, 0, [0, 256, 100, 1], "gaps"),
+    (4, 256, 4300, 4000, 24, 24, 256, 0, None, "plain"),
+    (4, 256, 4300, 4000, 31, 31, 256, 0, None, "stale"),
+    (4, 250, 4300, 4040, 24, 24, 128, 0, [0, 3, 200, 0], "gaps"),
+]
+
+
+@pytest.mark.parametrize("case", CUT, ids=C.IDS)
+def test_cut_units(case):
+    """Query tiles over slots enough to be cut into parts: 96, 192 and 248
+    units on 152 SMs, in equal parts and in large and small ones."""
+    _check(case)

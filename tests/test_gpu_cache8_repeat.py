@@ -153,3 +153,17 @@ def test_two_inputs_in_turn(T, d_h):
     for k, o in enumerate(outs):
         assert torch.equal(o[0], want[k % 2][0]) and torch.equal(o[1], want[k % 2][1])
     assert G3.gemma3_attn_check_status() == 0
+
+
+CUT = [
+    (4, 256, 4300, 4000, 12, 12, 256, 0),      # 96 units: a large part each and small ones
+    (4, 256, 4300, 4000, 24, 24, 256, 0),      # 192: one round of whole ones, then equal parts
+    (4, 256, 4300, 4000, 31, 31, 256, 0),      # 248: then large and small ones
+    (4, 256, 4300, 4000, 24, 24, 128, 0),
+    (5, 512, 9000, 8300, 48, 24, 128, 0),      # 480
+]
+
+
+@pytest.mark.parametrize("case", CUT, ids=lambda c: "B{}T{}S{}e{}H{}/{}d{}W{}".format(*c))
+def test_cut_units_back_to_back(case):
+    test_calls_back_to_back(case)
