@@ -163,3 +163,25 @@ def test_cut_units(case):
     """Query tiles over slots enough to be cut into parts: 96, 192 and 248
     units on 152 SMs, in equal parts and in large and small ones."""
     _check(case)
+
+
+@pytest.mark.parametrize("where", [0, 20000, 59000])
+@pytest.mark.parametrize("T", [40, 600])
+def test_window_behind_many_slots(T, where):
+    """A local layer far into a cache: the first visible slot lies early (a run
+    of slots at the queries' positions), in the middle, or just before."""
+    import transformer_attention_gb300 as G3
+    B, S, end, H, H_kv, d_h, W = 1, 61000, 60000, 2, 1, 128, 500
+    c, Q, seg = C._stage(B, T, S, end, H, H_kv, d_h, None, "plain", 33)
+    p = torch.arange(end + T) + 100000
+    p[where:where + 64] = torch.arange(end + 100000 - 100, end + 100000 - 36)
+    c["pos"][0, :end + T] = p
+    seg[0] = p[end:]
+    ref, w, A, PV = C8.attend(Q, c, seg, None, end, W)
+    wsum = torch.zeros((B, S), device="cuda")
+    O = C._attend(G3, Q, C._to_dev(c), seg, None, T, end, H, H_kv, d_h, W, torch.float16, wsum)
+    assert G3.gemma3_attn_check_status() == 0
+    C._check_o(O, ref, A, PV, float(C8.values(c, "v").nan_to_num(0.0).abs().max()), end + T, d_h,
+               torch.float16)
+    d = 2 * ((d_h / 16 + 4) * 2.0 ** -22 * float(A.max()) + 2.0 ** -21)
+    assert ((wsum.cpu().double() - w).abs() <= (d + (T * H + 2) * 2.0 ** -23) * w).all()

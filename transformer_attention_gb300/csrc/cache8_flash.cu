@@ -40,6 +40,8 @@
 // cut along their slots (plan8), into equal parts where several fit, else into
 // a large part each and small ones that the remaining SMs take one after
 // another; flash8_merge_kernel adds the parts.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <climits>
 
@@ -866,16 +868,22 @@ __global__ void __launch_bounds__(256) flash8_merge_kernel(const Params p) {
 
 // First slot of batch row b that a valid token of an item (span tokens from
 // item * span) can see on a local layer, by its stored position; hi if none.
-// 32 loads per thread in flight: 64 tokens behind 130000 slots 26 us in all, 29
-// with eight.
+// Up to eight CTAs per item, a cluster, while they fit the SMs: CTA r looks
+// through every C-th run of kFirstSlots slots (130000 slots: 20 us by one CTA
+// for 8192 at a time, 7 by eight).
+constexpr int kFirstSlots = 16384;
+
 __global__ void __launch_bounds__(1024) first8_kernel(const int32_t* __restrict__ posc,
                                                       const int32_t* __restrict__ qpos,
                                                       const int32_t* __restrict__ pad_lens, int T,
                                                       int S, int end, int window, int span,
                                                       int items, int32_t* __restrict__ first) {
   pdl_enter();
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank(), C = cluster.num_blocks();
   __shared__ int found;
-  const int item = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int item = blockIdx.x / C, b = blockIdx.y, tid = threadIdx.x;
   const int valid = min(T, T - (pad_lens != nullptr ? pad_lens[b] : 0));
   const int t0 = item * span, t_end = min(t0 + span, valid);
   const int hi = t_end > t0 ? end + t_end : 0;
@@ -892,11 +900,12 @@ __global__ void __launch_bounds__(1024) first8_kernel(const int32_t* __restrict_
   if (tid == 0) found = INT_MAX;
   __syncthreads();
   const int32_t* row = posc + static_cast<size_t>(b) * S;
-  for (int base = 0; base < hi; base += 32 * 1024) {
+  for (long long base = static_cast<long long>(rank) * kFirstSlots; base < hi;
+       base += static_cast<long long>(C) * kFirstSlots) {
     int best = INT_MAX;
 #pragma unroll
-    for (int k = 31; k >= 0; --k) {
-      const int s = base + k * 1024 + tid;
+    for (int k = kFirstSlots / 1024 - 1; k >= 0; --k) {
+      const int s = static_cast<int>(base) + k * 1024 + tid;
       const int ps = s < hi ? __ldcg(row + s) : -1;
       if (ps >= plo && ps <= phi) best = s;
     }
@@ -906,7 +915,13 @@ __global__ void __launch_bounds__(1024) first8_kernel(const int32_t* __restrict_
     if (found != INT_MAX) break;
     __syncthreads();
   }
-  if (tid == 0) first[static_cast<size_t>(b) * items + item] = min(found, hi);
+  if (C > 1) cluster.sync();
+  if (rank == 0 && tid == 0) {
+    int f = min(found, hi);
+    for (int r = 1; r < C; ++r) f = min(f, *cluster.map_shared_rank(&found, r));
+    first[static_cast<size_t>(b) * items + item] = f;
+  }
+  if (C > 1) cluster.sync();         // no CTA leaves before its minimum is read
 }
 
 template <int DH, int G, int NQ>
@@ -1007,8 +1022,16 @@ cudaError_t launch_flash8(const Flash8Args& a, cudaStream_t stream) {
   const int span = flash8_span(a.d_h, G), items = (a.T + span - 1) / span;
   const int hi = a.end + a.T;
   if (a.window > 0) {
-    cudaError_t e = launch_pdl(first8_kernel, dim3(items, a.B), dim3(1024), 0, stream, a.posc,
-                               a.qpos, a.pad_lens, a.T, a.S, a.end, a.window, span, items, a.first);
+    int cl = 1;
+    while (cl < 8 && static_cast<long long>(cl) * kFirstSlots < hi &&
+           2LL * cl * items * a.B <= num_sms())
+      cl *= 2;
+    const dim3 grid(items * cl, a.B), block(1024);
+    cudaError_t e =
+        cl > 1 ? launch_pdl_cluster(first8_kernel, grid, block, 0, cl, stream, a.posc, a.qpos, a.pad_lens,
+                                    a.T, a.S, a.end, a.window, span, items, a.first)
+               : launch_pdl(first8_kernel, grid, block, 0, stream, a.posc, a.qpos, a.pad_lens, a.T, a.S,
+                            a.end, a.window, span, items, a.first);
     if (e != cudaSuccess) return e;
   }
   const long long units = static_cast<long long>(a.B) * a.H_kv * items;
