@@ -6,6 +6,8 @@ the helpers below only allocate outputs and workspaces with torch and call it.
 """
 from __future__ import annotations
 
+import contextlib
+
 from ._lib import (  # noqa: F401  (re-exported C-ABI names)
     GEMMA3_BF16, GEMMA3_F16, GEMMA3_F32, GEMMA3_GLOBAL, GEMMA3_LOCAL_SLIDING, Gemma3Error,
     gemma3_attn_cached_workspace_size, gemma3_attn_check_status, gemma3_attn_forward,
@@ -27,6 +29,19 @@ from ._lib import (  # noqa: F401  (re-exported C-ABI names)
 __all__ = ["attention_forward", "attention_forward_cached", "attention_forward_cached8",
            "block_attention_forward", "block_forward", "evict_kv_cache8", "model_forward",
            "new_kv_cache", "new_kv_cache8", "linear", "lib"]
+
+
+def _on(stream):
+    """The context in which torch allocates and fills on ``stream``, as the
+    call launched on it will use it: memory of the current stream could still
+    be filled, or be handed out again, while that call runs."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _empty_ws(nbytes: int, device):
@@ -158,18 +173,20 @@ def evict_kv_cache8(cache, weight_sum, end_index, keep, recent, *, into=None, S=
     the front of another cache.  Returns (cache, weight_sum [B, S], kept
     [B, keep] int32, the slots they came from, -1 for none); the next
     end_index is ``keep``.  ``into``: (cache, weight_sum) to fill, else new
-    ones of ``S`` slots (default: as many as before)."""
+    ones of ``S`` slots (default: as many as before).  What it makes belongs
+    to ``stream`` (default: the current one)."""
     import torch
     K8, V8, K_scale, V_scale, pos = cache
     B, S0, H_kv, d_h = K8.shape
     _check_cache8(cache, B, H_kv, d_h, weight_sum)
-    if into is None:
-        S = S0 if S is None else S
-        into = (new_kv_cache8(B, S, H_kv, d_h, K8.device),
-                torch.zeros((B, S), dtype=torch.float32, device=K8.device))
-    dst, w_dst = into
-    _check_cache8(dst, B, H_kv, d_h, w_dst)
-    kept = torch.empty((B, keep), dtype=torch.int32, device=K8.device)
+    with _on(stream):
+        if into is None:
+            S = S0 if S is None else S
+            into = (new_kv_cache8(B, S, H_kv, d_h, K8.device),
+                    torch.zeros((B, S), dtype=torch.float32, device=K8.device))
+        dst, w_dst = into
+        _check_cache8(dst, B, H_kv, d_h, w_dst)
+        kept = torch.empty((B, keep), dtype=torch.int32, device=K8.device)
     gemma3_kv_cache8_evict(K8, V8, K_scale, V_scale, pos, weight_sum, B, S0, end_index, H_kv, d_h,
                            keep, recent, *dst, w_dst, kept, dst[4].shape[1], stream)
     return dst, w_dst, kept
