@@ -2,7 +2,8 @@
 
 The compute lives in libgemma3attn.so (CUDA kernels behind the C ABI of
 include/gemma3_attn.h).  ``_lib`` binds that ABI under the same names;
-the helpers below only allocate outputs and workspaces with torch and call it.
+the helpers below only allocate outputs and workspaces with torch, on the
+stream of the call, and call it.
 """
 from __future__ import annotations
 
@@ -61,10 +62,11 @@ def attention_forward(x, segment_pos, pad_lens, Wq, Wkv, Wo, gamma_q, gamma_k, *
     d_h = gamma_q.shape[0]
     dims = (B, T, D, H, H_kv, d_h)
     ws_bytes = gemma3_attn_workspace_size(*dims)
-    if workspace is None:
-        workspace = _empty_ws(ws_bytes, x.device)
-    if out is None:
-        out = torch.empty((B, T, D), dtype=torch.bfloat16, device=x.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = _empty_ws(ws_bytes, x.device)
+        if out is None:
+            out = torch.empty((B, T, D), dtype=torch.bfloat16, device=x.device)
     gemma3_attn_forward(dims, x, segment_pos, pad_lens, Wq, Wkv, Wo, gamma_q, gamma_k, attn_type,
                         window, rope_base, rope_scale, query_scale, out, workspace,
                         workspace.numel(), stream)
@@ -94,10 +96,11 @@ def attention_forward_cached(x, segment_pos, pad_lens, cache, end_index, Wq, Wkv
     S = pos_cache.shape[1]
     dims = (B, T, D, H, H_kv, d_h)
     ws_bytes = gemma3_attn_cached_workspace_size(dims, S)
-    if workspace is None:
-        workspace = _empty_ws(ws_bytes, x.device)
-    if out is None:
-        out = torch.empty((B, T, D), dtype=torch.bfloat16, device=x.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = _empty_ws(ws_bytes, x.device)
+        if out is None:
+            out = torch.empty((B, T, D), dtype=torch.bfloat16, device=x.device)
     gemma3_attn_forward_cached(dims, S, end_index, x, segment_pos, pad_lens, Wq, Wkv, Wo,
                                gamma_q, gamma_k, attn_type, window, rope_base, rope_scale,
                                query_scale, K_cache, V_cache, pos_cache, out, workspace,
@@ -154,11 +157,12 @@ def attention_forward_cached8(x, segment_pos, pad_lens, cache, end_index, Wq, Wk
     K8, V8, K_scale, V_scale, pos_cache = cache
     S = _check_cache8(cache, B, H_kv, d_h, weight_sum)
     dims = (B, T, D, H, H_kv, d_h)
-    if workspace is None:
-        workspace = _empty_ws(gemma3_attn_cached8_workspace_size(dims, S, weight_sum is not None),
-                              x.device)
-    if out is None:
-        out = torch.empty((B, T, D), dtype=torch.bfloat16, device=x.device)
+    ws_bytes = gemma3_attn_cached8_workspace_size(dims, S, weight_sum is not None)
+    with _on(stream):
+        if workspace is None:
+            workspace = _empty_ws(ws_bytes, x.device)
+        if out is None:
+            out = torch.empty((B, T, D), dtype=torch.bfloat16, device=x.device)
     gemma3_attn_forward_cached8(dims, S, end_index, x, segment_pos, pad_lens, Wq, Wkv, Wo,
                                 gamma_q, gamma_k, attn_type, window, rope_base, rope_scale,
                                 query_scale, K8, V8, K_scale, V_scale, pos_cache, weight_sum, out,
@@ -201,10 +205,11 @@ def block_attention_forward(x, segment_pos, pad_lens, Wq, Wkv, Wo, gamma_q, gamm
     d_h = gamma_q.shape[0]
     dims = (B, T, D, H, H_kv, d_h)
     ws_bytes = gemma3_block_attn_workspace_size(*dims)
-    if workspace is None:
-        workspace = _empty_ws(ws_bytes, x.device)
-    if y is None:
-        y = torch.empty((B, T, D), dtype=torch.float32, device=x.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = _empty_ws(ws_bytes, x.device)
+        if y is None:
+            y = torch.empty((B, T, D), dtype=torch.float32, device=x.device)
     x_dtype = GEMMA3_F32 if x.dtype == torch.float32 else GEMMA3_BF16
     gemma3_block_attn_forward(dims, x, x_dtype, y, segment_pos, pad_lens, Wq, Wkv, Wo, gamma_q,
                               gamma_k, gamma_pre, gamma_post, attn_type, window, rope_base,
@@ -224,10 +229,11 @@ def block_forward(x, segment_pos, pad_lens, Wq, Wkv, Wo, gamma_q, gamma_k, gamma
     D_ff = W_gating.shape[1]
     dims = (B, T, D, H, H_kv, d_h)
     ws_bytes = gemma3_block_workspace_size(dims, D_ff)
-    if workspace is None:
-        workspace = _empty_ws(ws_bytes, x.device)
-    if y is None:
-        y = torch.empty((B, T, D), dtype=torch.float32, device=x.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = _empty_ws(ws_bytes, x.device)
+        if y is None:
+            y = torch.empty((B, T, D), dtype=torch.float32, device=x.device)
     x_dtype = GEMMA3_F32 if x.dtype == torch.float32 else GEMMA3_BF16
     gemma3_block_forward(dims, D_ff, x, x_dtype, y, segment_pos, pad_lens, Wq, Wkv, Wo, gamma_q,
                          gamma_k, gamma_pre_attn, gamma_post_attn, gamma_pre_ffn, gamma_post_ffn,
@@ -248,10 +254,11 @@ def model_forward(tokens, segment_pos, pad_lens, E, layers, gamma_final, *, H, H
     d_h = layers[0]["gamma_q"].shape[0] if layers else 256
     dims = (B, T, D, H, H_kv, d_h)
     ws_bytes = gemma3_model_workspace_size(dims, D_ff, V)
-    if workspace is None:
-        workspace = _empty_ws(ws_bytes, tokens.device)
-    if logits is None:
-        logits = torch.empty((B, T, V), dtype=torch.float32, device=tokens.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = _empty_ws(ws_bytes, tokens.device)
+        if logits is None:
+            logits = torch.empty((B, T, V), dtype=torch.float32, device=tokens.device)
     gemma3_model_forward(dims, D_ff, V, len(layers), model_size, tokens, segment_pos, pad_lens,
                          E, layers, gamma_final, logits, workspace, workspace.numel(), stream)
     return logits
@@ -266,7 +273,8 @@ def linear(A, W, out_dtype=None, max_ctas=0, stream=None):
         raise ValueError("A and W must both be bf16 or both f16")
     M, K = A.shape
     N = W.shape[0]
-    C = torch.empty((M, N), dtype=out_dtype, device=A.device)
+    with _on(stream):
+        C = torch.empty((M, N), dtype=out_dtype, device=A.device)
     gemma3_linear(A, A.stride(0), W, W.stride(0), C, C.stride(0), M, N, K, code[A.dtype],
                   code[out_dtype], max_ctas, stream)
     return C
