@@ -379,7 +379,9 @@ int gemma3_cached8_attention_workspace_size(int B, int T, int S, int H, int H_kv
  * means global.
  *   weight_sum [B, S] fp32 or NULL: weight_sum[b, s] += the probabilities that
  * the row's valid tokens and query heads gave slot s, in fp32 and always in
- * the same order.  This is what gemma3_kv_cache8_evict ranks slots by.
+ * the same order.  This is what gemma3_kv_cache8_evict ranks slots by.  Once
+ * a wait has timed out on the device (until gemma3_attn_check_status) O is
+ * undefined and weights may be missing, but nothing else is added to them.
  *   What a slot's numbers and scale hold never matters, NaN included, where
  * the slot has no token, lies behind the row's last valid token, or on a
  * local layer has a position outside the reach of all of the row's tokens

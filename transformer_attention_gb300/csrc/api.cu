@@ -904,7 +904,7 @@ int gemma3_cached8_attention(const void* Q, const void* K8, const void* V8, cons
   return to_status(launch_cached8_attention(
       Q, K8, V8, K_scale, V_scale, pos_cache, segment_pos, pad_lens, O,
       o_dtype == GEMMA3_F16 ? kF16 : kBF16, weight_sum, B, T, S, end_index, H, H_kv, d_h,
-      window > 0 ? window : 0, workspace, as_stream(stream), st));
+      window > 0 ? window : 0, workspace, as_stream(stream), st, kLostWait));
 }
 
 int gemma3_kv_cache8_evict(const void* K8, const void* V8, const float* K_scale,
@@ -988,6 +988,9 @@ int gemma3_attn_forward_cached8(const gemma3_attn_dims* dims, int S, int end_ind
   uint8_t* kvbuf = qbuf + w.q;                            // [K'|V] fp16 [M, 2*KVD]
   uint8_t* obuf = weight_sum != nullptr ? kvbuf + w.kv : qbuf;   // O bf16
   uint8_t* aws = kvbuf + w.kv + w.o;
+  // More than kSkinnyMaxRows rows: the projections do not run after a recorded
+  // error of any kind.
+  const int lost = M > kSkinnyMaxRows ? kLostAny : kLostWait;
   cudaStream_t s = as_stream(stream);
   const int win = attn_type == GEMMA3_LOCAL_SLIDING ? window : 0;
   if (project_qk(x, d->D, kBF16, Wq, Wkv, qbuf, kvbuf, gamma_q, gamma_k, segment_pos, M, d->D,
@@ -998,7 +1001,7 @@ int gemma3_attn_forward_cached8(const gemma3_attn_dims* dims, int S, int end_ind
                           s) != cudaSuccess ||
       launch_cached8_attention(qbuf, K8, V8, K_scale, V_scale, pos_cache, segment_pos, pad_lens,
                                obuf, kBF16, weight_sum, d->B, d->T, S, end_index, d->H, d->H_kv,
-                               d->d_h, win, aws, s, st) != cudaSuccess)
+                               d->d_h, win, aws, s, st, lost) != cudaSuccess)
     return GEMMA3_ERR_CUDA;
   return to_status(launch_linear(obuf, HD, Wo, HD, out, d->D, M, d->D, HD, kBF16, kBF16, s, st, 0));
 }

@@ -707,6 +707,8 @@ struct WeighParams {
   const int2* swept;          // as in Params
   const int32_t* pad_lens;
   int T, S, H, H_kv, nb, end, nsplit, late, wchunks;
+  const int* status;
+  int lost;
 };
 
 template <int RW>
@@ -716,6 +718,7 @@ __global__ void __launch_bounds__(256) weigh8_kernel(const WeighParams p) {
   __shared__ float2 rs[2][WROWS];
   __shared__ int last[2][WROWS];
   __shared__ float2 wacc[RW > 1 ? RW - 1 : 1][GT];
+  const bool stop = lost_work(p.status, p.lost);      // logits may be missing
   const int tid = threadIdx.x, rg = tid / GT;
   const int b = blockIdx.x / p.wchunks, s = (blockIdx.x % p.wchunks) * (2 * GT) + 2 * (tid % GT);
   // Rows in the order of the logits: kv head, token, head of the group.
@@ -780,7 +783,7 @@ __global__ void __launch_bounds__(256) weigh8_kernel(const WeighParams p) {
       }
     }
   }
-  if (seen && rg == 0) {
+  if (seen && rg == 0 && !stop) {
     if (acc.x != 0.f) out[s] = old.x + acc.x;
     if (acc.y != 0.f) out[s + 1] = old.y + acc.y;
   }
@@ -897,7 +900,7 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
                                      const int32_t* pad_lens, void* O, int o_dtype,
                                      float* weight_sum, int B, int T, int S, int end, int H,
                                      int H_kv, int d_h, int window, void* ws, cudaStream_t stream,
-                                     int* status) {
+                                     int* status, int lost) {
   const Layout lay = layout(ws, B, T, S, H, H_kv, d_h, weight_sum != nullptr);
   const int hi = end + T, nb = c8_blocks(S), o_f16 = o_dtype == kF16 ? 1 : 0;
   cudaError_t e;
@@ -927,6 +930,7 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
     a.d_h = d_h;
     a.window = window;
     a.status = status;
+    a.lost = lost;
     e = launch_flash8(a, stream);
     if (e != cudaSuccess || weight_sum == nullptr) return e;
     return launch_weights8(a, lay.wpart, weight_sum, stream);
@@ -1014,6 +1018,8 @@ cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* 
   q.end = end;
   q.nsplit = nsplit;
   q.late = p.late;
+  q.status = status;
+  q.lost = lost;
   q.wchunks = (hi + (many ? 128 : 512) - 1) / (many ? 128 : 512);
   const long long ctas = static_cast<long long>(B) * q.wchunks;
   if (ctas > INT_MAX) return cudaErrorInvalidValue;

@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
                   const __grid_constant__ CUtensorMap tmV, const Params p) {
   pdl_enter();
   using C = Cfg<DH, G, NQ>;
-  if (*reinterpret_cast<volatile int*>(p.status) != 0) return;
+  if (__syncthreads_or(lost_work(p.status, kLostWait))) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // (the swizzled tiles need 1024-byte alignment; there is no other shared memory)
@@ -800,6 +800,7 @@ template <int DH, int G, int NQ>
 __global__ void __launch_bounds__(256) flash8_merge_kernel(const Params p) {
   pdl_enter();
   using C = Cfg<DH, G, NQ>;
+  if (lost_work(p.status, kLostWait)) return;   // parts may be missing
   constexpr int ROWS = 8;
   const int unit = p.whole + blockIdx.x;
   const int bjs = p.B * p.H_kv, item = p.items - 1 - unit / bjs;

@@ -28,6 +28,7 @@ struct Flash8Args {
   void* O;
   int o_f16, B, T, S, end, H, H_kv, d_h, window;
   int* status;
+  int lost;                   // errors (ptx.cuh) after which no weight is added
 };
 // Tokens of one work item.
 int flash8_span(int d_h, int G);

@@ -68,6 +68,7 @@ struct Params {
   float* wpart;               // [usplit, B, tiles * 128] when usplit > 1
   int B, T, S, H, H_kv, nb, end, window, usplit, tiles;
   int* status;
+  int lost;
 };
 
 template <int DH, int G>
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     weights8_kernel(const __grid_constant__ CUtensorMap tmQ, const Params p) {
   pdl_enter();
   using C = Cfg<DH, G>;
-  if (*reinterpret_cast<volatile int*>(p.status) != 0) return;
+  if (__syncthreads_or(lost_work(p.status, p.lost))) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     total += other[r];
     if (p.usplit > 1)
       p.wpart[(static_cast<size_t>(us) * p.B + b) * p.tiles * BM + s] = total;
-    else if (s < hi && total != 0.f) {
+    else if (s < hi && total != 0.f && !abort_flag) {
       float* w = p.weight_sum + static_cast<size_t>(b) * p.S + s;
       *w = __ldcg(w) + total;
     }
@@ -407,14 +408,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 __global__ void __launch_bounds__(256) wadd8_kernel(const float* __restrict__ wpart, int usplit,
                                                     int B, int ld, int hi, int S,
-                                                    float* __restrict__ weight_sum) {
+                                                    float* __restrict__ weight_sum,
+                                                    const int* status, int lost) {
   pdl_enter();
+  const bool stop = lost_work(status, lost);   // parts may be missing
   const int s = blockIdx.x * 256 + threadIdx.x, b = blockIdx.y;
   if (s >= hi) return;
   float a = 0.f;
   for (int k = 0; k < usplit; ++k) a += __ldcg(wpart + (static_cast<size_t>(k) * B + b) * ld + s);
   float* w = weight_sum + static_cast<size_t>(b) * S + s;
-  if (a != 0.f) *w = __ldcg(w) + a;
+  if (a != 0.f && !stop) *w = __ldcg(w) + a;
 }
 
 template <int DH, int G>
@@ -489,6 +492,7 @@ cudaError_t launch_weights8(const Flash8Args& a, float* wpart, float* weight_sum
   p.end = a.end;
   p.window = a.window;
   p.status = a.status;
+  p.lost = a.lost;
   p.tiles = (a.end + a.T + BM - 1) / BM;
   p.usplit = split_units(a, p.tiles);
 #define G3_WEIGHTS8_CASE(DH_, G_) \
@@ -503,7 +507,7 @@ cudaError_t launch_weights8(const Flash8Args& a, float* wpart, float* weight_sum
   if (e != cudaSuccess || p.usplit == 1) return e;
   return launch_pdl(wadd8_kernel, dim3((a.end + a.T + 255) / 256, a.B), dim3(256), 0, stream,
                     static_cast<const float*>(wpart), p.usplit, a.B, p.tiles * BM, a.end + a.T, a.S,
-                    weight_sum);
+                    weight_sum, static_cast<const int*>(a.status), a.lost);
 }
 
 }  // namespace g3

@@ -263,13 +263,14 @@ cudaError_t launch_cache8_evict(const void* K8, const void* V8, const float* K_s
 size_t cached8_attention_ws_bytes(int B, int T, int S, int H, int H_kv, int d_h, bool weights);
 
 // launch_cached_attention over an 8-bit cache; weight_sum [B, S] or null: the
-// probabilities of every slot are added to it.
+// probabilities of every slot are added to it, unless an error of the mask
+// `lost` (ptx.cuh) was recorded by then.
 cudaError_t launch_cached8_attention(const void* Q, const void* K8, const void* V8,
                                      const float* K_scale, const float* V_scale,
                                      const int32_t* pos_cache, const int32_t* qpos,
                                      const int32_t* pad_lens, void* O, int o_dtype,
                                      float* weight_sum, int B, int T, int S, int end, int H,
                                      int H_kv, int d_h, int window, void* ws, cudaStream_t stream,
-                                     int* status);
+                                     int* status, int lost);
 
 }  // namespace g3

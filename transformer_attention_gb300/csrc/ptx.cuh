@@ -21,6 +21,16 @@ enum : int {
   kDevErrBadToken = 0x2000,      // a token id outside [0, V)
 };
 
+// What a recorded error may have left undone, as masks of the status word: a
+// wait that gave up, the work behind it; any error, also what the kernels
+// skip that start with the word set (the GEMMs).
+enum : int { kLostWait = kDevErrTimeoutBase, kLostAny = kDevErrTimeoutBase | kDevErrBadToken };
+
+// Has an error of `mask` been recorded?
+__device__ __forceinline__ bool lost_work(const int* status, int mask) {
+  return (*reinterpret_cast<const volatile int*>(status) & mask) != 0;
+}
+
 // Programmatic dependent launch.  Every kernel of the library is launched
 // so that it may start while the kernel before it on the stream finishes
 // (launch_pdl, internal.h); its first statement waits until that kernel
