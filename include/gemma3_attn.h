@@ -421,7 +421,11 @@ int gemma3_attn_cached8_workspace_size(const gemma3_attn_dims* dims, int S, int 
 /* gemma3_attn_forward_cached over an 8-bit cache: the new tokens' K' and V
  * are stored as gemma3_kv_cache8_write does, and the tokens (a prompt's too)
  * attend over what the cache then holds, as gemma3_cached8_attention does,
- * weight_sum included (NULL: none). */
+ * weight_sum included (NULL: none).
+ *   After an error recorded on the device (by any call, until
+ * gemma3_attn_check_status) that leaves the projections without a result, the
+ * cache and weight_sum stay as they were and out is undefined: the call can
+ * be made again. */
 int gemma3_attn_forward_cached8(const gemma3_attn_dims* dims, int S, int end_index, const void* x,
                                 const int32_t* segment_pos, const int32_t* pad_lens,
                                 const void* Wq, const void* Wkv, const void* Wo,

@@ -1,10 +1,12 @@
 """The 8-bit cache after an error that another call recorded (a bad token id),
 before anybody has read it: calls whose own work is not lost give what they
-always give."""
+always give, and where the projections stop, a layer leaves its cache and its
+slot weights as they were."""
 import pytest
 import torch
 
 from tests import test_gpu_cache8 as C
+from transformer_attention_gb300 import workloads as WL
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +52,53 @@ def test_attention_after_a_recorded_error(T, window, d_h):
     got = call()
     _read_bad_token(G3)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("T", [1, 16, 64])
+def test_layer_after_a_recorded_error(T):
+    """Few tokens are unharmed.  Where the projections stop at a recorded
+    error (T = 16 and 64: more than 16 rows), the tokens are not written, so
+    that the block's scale and older numbers stay, and no weight is added; the
+    call made again gives what it would have given."""
+    import transformer_attention_gb300 as G3
+    w = WL.small(WL.WORKLOADS["tiny_local"], name="errors", B=2, T=128, D=256, H=4, H_kv=1, d_h=256,
+                 attn_type="global", window=0)
+    p = {k: v.cuda() for k, v in WL.weights(w).items()}
+    x = WL.x_full(w).cuda()
+    B, S, T0 = w.B, 200, 40
+    n = G3.gemma3_attn_cached8_workspace_size((B, 64, w.D, w.H, w.H_kv, w.d_h), S, True)
+
+    def layer(a, z, cache, weights):
+        ws = torch.full((n,), 0x7B, dtype=torch.uint8, device="cuda")     # 61280 in fp16
+        seg = torch.arange(a, z, dtype=torch.int32, device="cuda").repeat(B, 1)
+        out = torch.full((B, z - a, w.D), 5.0, dtype=torch.bfloat16, device="cuda")
+        return G3.attention_forward_cached8(
+            x[:, a:z].contiguous(), seg, None, cache, a, p["Wq"], p["Wkv"], p["Wo"], p["gamma_q"],
+            p["gamma_k"], H=w.H, H_kv=w.H_kv, attn_type=G3.GEMMA3_GLOBAL, window=0,
+            rope_base=w.rope_base, rope_scale=w.rope_scale, query_scale=w.query_scale,
+            weight_sum=weights, out=out, workspace=ws)
+
+    def state():
+        cache, weights = G3.new_kv_cache8(B, S, w.H_kv, w.d_h, "cuda"), torch.zeros((B, S), device="cuda")
+        layer(0, T0, cache, weights)
+        return cache, weights
+
+    def bits(cache, weights):
+        return [t.view(torch.uint8).clone() for t in (*cache, weights)]
+
+    clean = state()
+    want = layer(T0, T0 + T, *clean)
+    assert G3.gemma3_attn_check_status() == 0
+    mine = state()
+    before = bits(*mine)
+    _record_bad_token(G3)
+    got = layer(T0, T0 + T, *mine)
+    _read_bad_token(G3)
+    if B * T > 16:
+        for a, b in zip(bits(*mine), before):
+            assert torch.equal(a, b)
+        got = layer(T0, T0 + T, *mine)
+        assert G3.gemma3_attn_check_status() == 0
+    assert torch.equal(got, want)
+    for a, b in zip(bits(*mine), bits(*clean)):
+        assert torch.equal(a, b)

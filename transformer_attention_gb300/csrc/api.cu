@@ -989,7 +989,8 @@ int gemma3_attn_forward_cached8(const gemma3_attn_dims* dims, int S, int end_ind
   uint8_t* obuf = weight_sum != nullptr ? kvbuf + w.kv : qbuf;   // O bf16
   uint8_t* aws = kvbuf + w.kv + w.o;
   // More than kSkinnyMaxRows rows: the projections do not run after a recorded
-  // error of any kind.
+  // error of any kind, and rows that they did not write must not reach the
+  // cache (a block's scale would grow, its older numbers be rounded to it).
   const int lost = M > kSkinnyMaxRows ? kLostAny : kLostWait;
   cudaStream_t s = as_stream(stream);
   const int win = attn_type == GEMMA3_LOCAL_SLIDING ? window : 0;
@@ -997,8 +998,8 @@ int gemma3_attn_forward_cached8(const gemma3_attn_dims* dims, int S, int end_ind
                  d->H, d->H_kv, d->d_h, rope_base, rope_scale, query_scale, s,
                  st) != cudaSuccess ||
       launch_cache8_write(kvbuf, kvbuf + KVD * 2, 2 * KVD, segment_pos, pad_lens, d->B, d->T, S,
-                          end_index, d->H_kv, d->d_h, K8, V8, K_scale, V_scale, pos_cache,
-                          s) != cudaSuccess ||
+                          end_index, d->H_kv, d->d_h, K8, V8, K_scale, V_scale, pos_cache, s, st,
+                          lost) != cudaSuccess ||
       launch_cached8_attention(qbuf, K8, V8, K_scale, V_scale, pos_cache, segment_pos, pad_lens,
                                obuf, kBF16, weight_sum, d->B, d->T, S, end_index, d->H, d->H_kv,
                                d->d_h, win, aws, s, st, lost) != cudaSuccess)

@@ -19,11 +19,12 @@ namespace {
 constexpr int kTile = kC8Block;
 constexpr int kRowThreads = 256;
 
-__device__ __forceinline__ float block_max(float v, float* red) {
+// The block's largest v; -1 if `stop` for any thread.
+__device__ __forceinline__ float block_max(float v, float* red, bool stop) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
+  if (__syncthreads_or(stop)) return -1.f;
   v = red[0];
 #pragma unroll
   for (int i = 1; i < kRowThreads / 32; ++i) v = fmaxf(v, red[i]);
@@ -68,6 +69,8 @@ struct WriteParams {
   float* K_scale;
   float* V_scale;
   int32_t* posc;
+  const int* status;          // or null
+  int lost;
 };
 
 // One CTA per (block of 64 slots, kv head, K' or V, batch row): the block's
@@ -96,6 +99,7 @@ __global__ void __launch_bounds__(kRowThreads) cache8_write_kernel(const WritePa
   const int s0 = blk * kTile, c = (tid % TPR) * 8;
   const bool held = s0 < p.end;                // the block holds earlier tokens
   const float old = held ? __ldcg(scale) : 0.f;
+  const bool stop = p.status != nullptr && lost_work(p.status, p.lost);
 
   uint4 x[NP];
   float mx = 0.f;
@@ -109,7 +113,8 @@ __global__ void __launch_bounds__(kRowThreads) cache8_write_kernel(const WritePa
   }
 #pragma unroll
   for (int i = 0; i < NP; ++i) mx = fmaxf(mx, finite_max8(x[i]));
-  mx = block_max(mx, red);                     // (also: every thread has read the old scale)
+  mx = block_max(mx, red, stop);               // (also: every thread has read the old scale)
+  if (mx < 0.f) return;
   const float s = fmaxf(old, c8_scale_for(mx));
   const float inv = 1.f / s;
   const size_t ldc = static_cast<size_t>(p.H_kv) * DH;
@@ -546,7 +551,7 @@ cudaError_t launch_cache8_write(const void* K_rows, const void* V_rows, long ld,
                                 const int32_t* segment_pos, const int32_t* pad_lens, int B, int T,
                                 int S, int end, int H_kv, int d_h, void* K8, void* V8,
                                 float* K_scale, float* V_scale, int32_t* pos_cache,
-                                cudaStream_t stream) {
+                                cudaStream_t stream, const int* status, int lost) {
   WriteParams p;
   p.K_rows = static_cast<const __half*>(K_rows);
   p.V_rows = static_cast<const __half*>(V_rows);
@@ -565,6 +570,8 @@ cudaError_t launch_cache8_write(const void* K_rows, const void* V_rows, long ld,
   p.K_scale = K_scale;
   p.V_scale = V_scale;
   p.posc = pos_cache;
+  p.status = status;
+  p.lost = lost;
   const dim3 grid(static_cast<unsigned>(static_cast<long long>(B) * p.nblk * H_kv * 2));
   return launch_pdl(d_h == 256 ? cache8_write_kernel<256> : cache8_write_kernel<128>, grid,
                     dim3(kRowThreads), 0, stream, p);

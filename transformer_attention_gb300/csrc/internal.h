@@ -239,11 +239,13 @@ int cached_span_chunks(int T, int end);
 // H_kv] fp32 and positions pos_cache [B, S] (cache8.cuh).
 constexpr int c8_blocks(int S) { return static_cast<int>((static_cast<long long>(S) + 63) / 64); }
 
+// Writes nothing once an error of the mask `lost` (ptx.cuh) was recorded, if
+// `status` is given: the rows may be missing then.
 cudaError_t launch_cache8_write(const void* K_rows, const void* V_rows, long ld,
                                 const int32_t* segment_pos, const int32_t* pad_lens, int B, int T,
                                 int S, int end, int H_kv, int d_h, void* K8, void* V8,
                                 float* K_scale, float* V_scale, int32_t* pos_cache,
-                                cudaStream_t stream);
+                                cudaStream_t stream, const int* status = nullptr, int lost = 0);
 
 // Slots [first, first + n) as fp16 rows b * n + t of stride ld.
 cudaError_t launch_cache8_read(const void* K8, const void* V8, const float* K_scale,
