@@ -377,6 +377,9 @@ int gemma3_cached8_attention_workspace_size(int B, int T, int S, int H, int H_kv
  * T); O [B, T, H, d_h] in o_dtype (GEMMA3_BF16 | GEMMA3_F16; may alias Q'
  * when weight_sum is NULL), rows that see no slot and pad rows 0; window <= 0
  * means global.
+ *   Logits, sums and weights are fp32.  For the product with V a probability is
+ * rounded to fp16 as a multiple of its row's largest: off by 2^-11 relative,
+ * by 2^-32 absolute below 2^-21 (gemma3_cached_attention keeps fp32 there).
  *   weight_sum [B, S] fp32 or NULL: weight_sum[b, s] += the probabilities that
  * the row's valid tokens and query heads gave slot s, in fp32 and always in
  * the same order.  This is what gemma3_kv_cache8_evict ranks slots by.  Once

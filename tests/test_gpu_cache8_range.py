@@ -1,0 +1,59 @@
+"""The 8-bit cache attention over the range of its probabilities: keys far
+above many equal ones.
+
+Bounds as in test_gpu_cache8.py, with a tighter absolute term: probabilities
+are rounded to fp16 times 2^15 (few rows) or 2^7 at least (many), so that
+below fp16's normal range they are off by 2^-25 / 2^7 of the row's largest.
+"""
+import pytest
+import torch
+
+from oracle import cache8_oracle as C8
+from tests import test_gpu_cache8 as C
+
+pytestmark = pytest.mark.gpu
+
+F64 = torch.float64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from transformer_attention_gb300.build import build
+    build()
+    import transformer_attention_gb300 as G3
+    G3.lib()
+
+
+FORMS = [(1, 4, 2, 128), (3, 4, 1, 256), (40, 4, 2, 128), (300, 4, 2, 128), (70, 4, 2, 256)]
+
+
+@pytest.mark.parametrize("apart", [8, 64, 5000])
+@pytest.mark.parametrize("gap", [12.0, 16.0, 18.0, 20.0])
+@pytest.mark.parametrize("T,H,H_kv,d_h", FORMS)
+def test_sinks_far_above_equal_keys(T, H, H_kv, d_h, gap, apart):
+    """Every apart-th slot, of value zero, is e^gap times as likely as the
+    others, whose small shares still add up."""
+    import transformer_attention_gb300 as G3
+    B, S, end = 1, 5000, 4500
+    c, Q, seg = C._stage(B, T, S, end, H, H_kv, d_h, None, "plain", 7, (0, 0))
+    v = 100.0 + 30.0 * torch.randn(c["v8"].shape, generator=C._gen(5))
+    c["v8"][:, :end + T] = C8.encode(v.to(F64))[:, :end + T]
+    c["v8"][:, :end:apart] = 0
+    c["k8"][:, :end + T] = 0
+    c["k8"][:, :end:apart, :, 0] = C8.encode(torch.tensor(gap, dtype=F64))
+    Q = torch.zeros_like(Q)
+    Q[..., 0] = 1.0
+    ref, w, A, PV = C8.attend(Q, c, seg, None, end, 0)
+    wsum = torch.zeros((B, S), device="cuda")
+    O = C._attend(G3, Q, C._to_dev(c), seg, None, T, end, H, H_kv, d_h, 0, torch.float16, wsum)
+    assert G3.gemma3_attn_check_status() == 0
+    # (the largest probability is 1 / sinks: each of the others' is off by that share)
+    vmax = float(C8.values(c, "v").nan_to_num(0.0).abs().max())
+    sinks = -(-end // apart)
+    d = (d_h / 16 + 4) * 2.0 ** -22 * A + 2.0 ** -21
+    tol = ((2.0 ** -11 + 2 * d + 2.0 ** -18)[..., None] * PV + (end + T) / sinks * 2.0 ** -32 * vmax) * (
+        1 + 2.0 ** -11) + 2.0 ** -11 * ref.abs() + 2.0 ** -25
+    err = (O.cpu().to(F64) - ref).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+    dw = 2 * ((d_h / 16 + 4) * 2.0 ** -22 * float(A.max()) + 2.0 ** -21)
+    assert ((wsum.cpu().to(F64) - w).abs() <= (dw + (T * H + 2) * 2.0 ** -23) * w).all()

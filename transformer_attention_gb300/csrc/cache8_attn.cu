@@ -32,9 +32,11 @@
 //     fp32 accumulator (V) in fp32: the accumulator is kept in units of the
 //     current block's V scale and changes unit in the multiplication that the
 //     running maximum asks for anyway.
-//   - The probabilities are rounded to fp16 for the V product (relative error
-//     2^-11 each, averaged over slots; below the fp16 or bf16 output's own
-//     rounding); sums and maxima are fp32.
+//   - For the V product the probabilities, at most 1 against the running
+//     maximum, are rounded to fp16 times 2^15: off by 2^-11 relative each
+//     (averaged over slots; below the fp16 or bf16 output's own rounding) down
+//     to 2^-29, by 2^-40 absolute below that, so that a key far above
+//     thousands of others does not lose their sum.  Sums and maxima are fp32.
 // The slots of a (row, kv head) are split over CTAs: up to eight form a
 // cluster that merges its parts through distributed shared memory, more leave
 // them to a second launch (merge8_kernel).  For weight_sum a last launch
@@ -62,6 +64,7 @@ constexpr int kMaxSplits = 256;
 constexpr int kMaxCluster = 8;
 constexpr int kFewRows = 16;         // query rows of a kv head that decode8_kernel takes
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kPUnit = 32768.f;    // what the fp16 probabilities are multiplied by
 
 enum { kSiteFull = 70, kSiteEmpty = 71 };
 
@@ -482,8 +485,8 @@ __global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTA
           f[nt][e] = al * du;
           same &= f[nt][e] == 1.f;
         }
-        pb[nt][0] = transpose8x8(pack_half2(pr[0], pr[1]));
-        pb[nt][1] = transpose8x8(pack_half2(pr[2], pr[3]));
+        pb[nt][0] = transpose8x8(pack_half2(pr[0] * kPUnit, pr[1] * kPUnit));
+        pb[nt][1] = transpose8x8(pack_half2(pr[2] * kPUnit, pr[3] * kPUnit));
       }
       unit = vsc;
       if (!__all_sync(0xffffffffu, same)) {
@@ -548,6 +551,7 @@ __global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTA
   named_barrier(1, kConsumers);
   float* mg = reinterpret_cast<float*>(ring);
   float* cacc = reinterpret_cast<float*>(ring + C::MERGE);     // [ROWS][DH]
+  unit *= 1.f / kPUnit;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

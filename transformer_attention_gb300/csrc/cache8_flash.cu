@@ -62,7 +62,12 @@ constexpr uint32_t CHUNK = 128 * 128;       // 128 rows x 64 channels (128 B), s
 constexpr uint32_t PART = 32768;
 constexpr uint32_t O_COL = 256;
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float RESCALE_THRESHOLD = 8.0f;   // log2 units
+// A row's reference stays P_SHIFT below a past maximum while the present one
+// is less than RESCALE_THRESHOLD above that (log2 units): the probabilities
+// that are rounded to fp16 reach 2^15, so that those below its normal range, off
+// by 2^-25, are off by 2^-32 at most of the row's largest (a key far above
+// thousands of others does not lose their sum).
+constexpr float RESCALE_THRESHOLD = 8.0f, P_SHIFT = 7.0f;
 
 enum : int {
   kSiteQ = 80, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty, kSiteSFull, kSitePFull,
@@ -132,8 +137,8 @@ struct Params {
   const int32_t* qpos;
   const int32_t* pad_lens;
   const int32_t* first;       // [B, items] first visible slot of each item (local layers) or null
-  float2* rowstat;            // [B, H_kv, T*G] (max, 1 / sum) of every row, or null
-  float2* pstat;              // [cut units, parts, NQ * 128] (max, sum)
+  float2* rowstat;            // [B, H_kv, T*G] (reference, 1 / sum) of every row, or null
+  float2* pstat;              // [cut units, parts, NQ * 128] (reference, sum)
   float* part;                // [cut units, parts, NQ * 128, DH] unnormalised
   void* O;
   int o_f16, B, T, S, H, H_kv, nb, end, window, items;
@@ -697,9 +702,9 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
         __syncwarp();
         if (lane == 0)
           mbar_arrive(smem_u32(&sh.meta_empty[i % NMETA]) + (__float_as_uint(mx) & p.zero));
-        const bool grow = mx > m_used + RESCALE_THRESHOLD;
+        const bool grow = mx > m_used + (RESCALE_THRESHOLD + P_SHIFT);
         if (__any_sync(0xffffffffu, grow)) {
-          const float m_new = grow ? mx : m_used;
+          const float m_new = grow ? mx - P_SHIFT : m_used;
           const float factor = (m_new == m_used) ? 1.f : ex2(m_used - m_new);
           if (i > 0) {
             // O holds the PV of the tiles before: with two query tiles S_e of

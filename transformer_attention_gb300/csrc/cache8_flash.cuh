@@ -22,7 +22,7 @@ struct Flash8Args {
   const int32_t* qpos;
   const int32_t* pad_lens;
   int32_t* first;             // [B, items] scratch of local layers
-  float2* rowstat;            // [B, H_kv, T*G] (max, 1 / sum) of every row, or null
+  float2* rowstat;            // [B, H_kv, T*G] (reference, 1 / sum) of every row, or null
   float2* pstat;              // [flash8_part_rows()] and
   float* part;                // [flash8_part_rows(), d_h]: scratch of cut units
   void* O;
@@ -94,8 +94,8 @@ __device__ __forceinline__ void store16_values(uint2 a, uint2 b, uint32_t scale2
   *reinterpret_cast<uint4*>(base + (((u0 + 1 - swap) ^ r7) << 4)) = values8<CLAMP>(b, scale);
 }
 
-// A query row's entry of rowstat: (max, 1 / sum), or (inf, 0) for a row that
-// saw nothing, whose weights come out as zeros.
+// A query row's entry of rowstat: (reference, 1 / sum of exp2 against it), or
+// (inf, 0) for a row that saw nothing, whose weights come out as zeros.
 __device__ __forceinline__ float2 row_stat(float m, float l, bool any) {
   return any ? make_float2(m, 1.f / l) : make_float2(INFINITY, 0.f);
 }

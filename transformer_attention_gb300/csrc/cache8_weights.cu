@@ -1,8 +1,9 @@
 // The weight that each slot of the 8-bit cache received from many query rows
-// (a prompt or a chunk), after the attention has left every row's maximum and
-// sum: weight_sum[s] += sum over rows of exp2(l_s - max) / sum.  The logits
-// are computed again from K (half the attention's products and no V) because
-// keeping them would take 4 bytes per query row and slot.
+// (a prompt or a chunk), after the attention has left every row's reference
+// (near its maximum) and sum: weight_sum[s] += sum over rows of exp2(l_s -
+// reference) / sum.  The logits are computed again from K (half the attention's
+// products and no V) because keeping them would take 4 bytes per query row and
+// slot.
 //
 // The product is transposed, S^T = K Q^T with 128 slots on the tensor core's
 // 128 rows: a thread owns a slot and sums over the query rows in its own
@@ -63,7 +64,7 @@ struct Params {
   const int32_t* posc;
   const int32_t* qpos;
   const int32_t* pad_lens;
-  const float2* rowstat;      // [B, H_kv, T*G] (max, 1 / sum), (inf, 0) for a row of no weight
+  const float2* rowstat;      // [B, H_kv, T*G] (reference, 1 / sum), (inf, 0) for a row of no weight
   float* weight_sum;          // [B, S]
   float* wpart;               // [usplit, B, tiles * 128] when usplit > 1
   int B, T, S, H, H_kv, nb, end, window, usplit, tiles;
