@@ -376,7 +376,7 @@ int gemma3_cached8_attention_workspace_size(int B, int T, int S, int H, int H_kv
  * scale applied) of tokens already written to slots [end_index, end_index +
  * T); O [B, T, H, d_h] in o_dtype (GEMMA3_BF16 | GEMMA3_F16; may alias Q'
  * when weight_sum is NULL), rows that see no slot and pad rows 0; window <= 0
- * means global.
+ * means global.  A query's own position (segment_pos) may be negative here.
  *   Logits, sums and weights are fp32.  For the product with V a probability is
  * rounded to fp16 as a multiple of its row's largest: off by 2^-11 relative,
  * by 2^-32 absolute below 2^-21 (gemma3_cached_attention keeps fp32 there).

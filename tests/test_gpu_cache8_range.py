@@ -1,5 +1,5 @@
 """The 8-bit cache attention over the range of its probabilities: keys far
-above many equal ones.
+above many equal ones; and of query positions: negative ones.
 
 Bounds as in test_gpu_cache8.py, with a tighter absolute term: probabilities
 are rounded to fp16 times 2^15 (few rows) or 2^7 at least (many), so that
@@ -57,3 +57,25 @@ def test_sinks_far_above_equal_keys(T, H, H_kv, d_h, gap, apart):
     assert (err <= tol).all(), float((err / tol).max())
     dw = 2 * ((d_h / 16 + 4) * 2.0 ** -22 * float(A.max()) + 2.0 ** -21)
     assert ((wsum.cpu().to(F64) - w).abs() <= (dw + (T * H + 2) * 2.0 ** -23) * w).all()
+
+
+@pytest.mark.parametrize("T,H,H_kv,d_h", FORMS)
+def test_queries_at_negative_positions(T, H, H_kv, d_h):
+    """A query's own position may be negative: on a local layer it sees the
+    slots within its window, and they receive its weight."""
+    import transformer_attention_gb300 as G3
+    B, S, end, W = 2, 700, 350, 60
+    for shift in (-30, -T // 2 - 5, -2 ** 31):
+        c, Q, seg = C._stage(B, T, S, end, H, H_kv, d_h, None, "plain", 8)
+        seg = torch.arange(T).repeat(B, 1) + shift
+        c["pos"][:, end:end + T] = -1
+        ref, w, A, PV = C8.attend(Q, c, seg, None, end, W)
+        wsum = torch.zeros((B, S), device="cuda")
+        O = C._attend(G3, Q, C._to_dev(c), seg, None, T, end, H, H_kv, d_h, W, torch.float16, wsum)
+        assert G3.gemma3_attn_check_status() == 0
+        C._check_o(O, ref, A, PV, float(C8.values(c, "v").nan_to_num(0.0).abs().max()), end + T, d_h,
+                   torch.float16)
+        assert (w > 0).any() == (shift > -2 ** 31)
+        got = wsum.cpu().to(F64)
+        dw = 2 * ((d_h / 16 + 4) * 2.0 ** -22 * float(A.max()) + 2.0 ** -21)
+        assert ((got - w).abs() <= (dw + (T * H + 2) * 2.0 ** -23) * w).all()

@@ -293,9 +293,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int s = s_tile + r;
     const int ps = s < hi ? __ldcg(p.posc + static_cast<size_t>(b) * p.S + s) : -1;
-    // query positions that see this slot on a local layer
+    // query positions that see this slot on a local layer (negative ones too:
+    // only a stored position below 0 means that there is no token)
     int qlo = INT_MIN, qhi = INT_MAX;
-    if (p.window > 0) window_range(ps, ps, p.window, qlo, qhi);
+    if (p.window > 0 && ps >= 0) {
+      qlo = ps - (p.window - 1);
+      qhi = ps > INT_MAX - (p.window - 1) ? INT_MAX : ps + (p.window - 1);
+    }
     const size_t rows = static_cast<size_t>(p.T) * G;
     float2 nx = make_float2(INFINITY, 0.f);
     int nq = 0;
