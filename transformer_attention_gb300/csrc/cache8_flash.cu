@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
                   const __grid_constant__ CUtensorMap tmV, const Params p) {
   pdl_enter();
   using C = Cfg<DH, G, NQ>;
-  if (__syncthreads_or(lost_work(p.status, kLostWait))) return;
+  const bool lost = lost_work(p.status, kLostWait);   // (under way until the first barrier)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // (the swizzled tiles need 1024-byte alignment; there is no other shared memory)
@@ -260,9 +260,13 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
     tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_relinquish();
   }
-  __syncthreads();
+  const bool stop = __syncthreads_or(lost);
   tc_fence_after();
   const uint32_t tbase = sh.tmem;
+  if (stop) {
+    if (warp == 1) tmem_dealloc(tbase, 512);
+    return;
+  }
   auto wait_warp = [&](uint64_t& bar, int parity, int site) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, &sh.abort_flag, p.status, site));
   };

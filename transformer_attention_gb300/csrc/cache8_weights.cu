@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     weights8_kernel(const __grid_constant__ CUtensorMap tmQ, const Params p) {
   pdl_enter();
   using C = Cfg<DH, G>;
-  if (__syncthreads_or(lost_work(p.status, p.lost))) return;
+  const bool lost = lost_work(p.status, p.lost);      // (under way until the first barrier)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -125,7 +125,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(smem_u32(&tmem_sh), 512);
     tmem_relinquish();
   }
-  __syncthreads();
+  if (__syncthreads_or(lost)) {
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_sh, 512);
+    return;
+  }
   if (warp < 4) {
     const int s = s_tile + tid;
     const int ps = s < hi ? __ldcg(p.posc + static_cast<size_t>(b) * p.S + s) : -1;
