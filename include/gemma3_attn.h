@@ -335,6 +335,7 @@ int gemma3_cached_attention(const void* Q, const void* K_cache, const void* V_ca
  *                     [2^-15, 2^8] wherever tokens were written
  *   pos_cache         [B, S] int32 as in the fp16 cache (negative: no token)
  * Slot s of head j holds the values K8[b, s, j, :] * K_scale[b, s / 64, j].
+ * The attention computes with exactly these, up to 448 * 2^8 = 114688.
  * A fresh cache has all positions negative and its other bytes zero.  Slots,
  * positions, mask, padding and end_index as in the fp16 cache above: left
  * aligned, the caller advances end_index, nothing wraps. */

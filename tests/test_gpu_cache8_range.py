@@ -1,5 +1,6 @@
 """The 8-bit cache attention over the range of its probabilities: keys far
-above many equal ones; and of query positions: negative ones.
+above many equal ones; of query positions: negative ones; and of stored
+values: beyond fp16's largest.
 
 Bounds as in test_gpu_cache8.py, with a tighter absolute term: probabilities
 are rounded to fp16 times 2^15 (few rows) or 2^7 at least (many), so that
@@ -79,3 +80,32 @@ def test_queries_at_negative_positions(T, H, H_kv, d_h):
         got = wsum.cpu().to(F64)
         dw = 2 * ((d_h / 16 + 4) * 2.0 ** -22 * float(A.max()) + 2.0 ** -21)
         assert ((got - w).abs() <= (dw + (T * H + 2) * 2.0 ** -23) * w).all()
+
+
+@pytest.mark.parametrize("T,H,H_kv,d_h", FORMS)
+def test_stored_values_beyond_fp16(T, H, H_kv, d_h):
+    """A number that stands for 65536 or, from an infinity, for 114688 counts
+    as that in every form, in K and in V."""
+    import transformer_attention_gb300 as G3
+    B, S, end = 1, 700, 300
+    g = C._gen(9)
+    k = torch.zeros((B, end + T, H_kv, d_h)).half()
+    v = torch.zeros_like(k)
+    # K: 65504 (stored as 65536), an infinity or 57344 in one channel
+    pick = torch.randint(0, 3, (B, end + T, H_kv), generator=g)
+    top = torch.tensor([65504.0, float("inf"), 57344.0]).half()
+    k[..., 0] = top[pick]
+    sign = torch.randint(0, 2, v.shape, generator=g) * 2.0 - 1.0
+    v[:] = (top[torch.randint(0, 3, v.shape, generator=g)].float() * sign).half()
+    c = C8.write(C8.empty(B, S, H_kv, d_h), k, v, torch.arange(end + T)[None], None, 0)
+    assert float(C8.values(c, "k").max()) == 114688.0
+    Q = torch.zeros((B, T, H, d_h)).half()
+    Q[..., 0] = 2.0 ** -15
+    seg = torch.arange(end, end + T)[None]
+    ref, w, A, PV = C8.attend(Q, c, seg, None, end, 0)
+    wsum = torch.zeros((B, S), device="cuda")
+    O = C._attend(G3, Q, C._to_dev(c), seg, None, T, end, H, H_kv, d_h, 0, torch.bfloat16, wsum)
+    assert G3.gemma3_attn_check_status() == 0
+    C._check_o(O, ref, A, PV, 114688.0, end + T, d_h, torch.bfloat16)
+    dw = 2 * ((d_h / 16 + 4) * 2.0 ** -22 * float(A.max()) + 2.0 ** -21)
+    assert ((wsum.cpu().to(F64) - w).abs() <= (dw + (T * H + 2) * 2.0 ** -23) * w).all()

@@ -44,6 +44,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cstddef>
 
 #include "attention_common.cuh"
 #include "cache8.cuh"
@@ -79,14 +80,16 @@ constexpr uint32_t RAW = 8192;              // bytes of a raw granule: 64 slots 
 constexpr int NMETA = 4;
 constexpr int MAX_RAW = 8;
 
-struct Meta {
+struct alignas(16) Meta {  // (use is read in pairs)
   uint32_t ok[4];          // slots of the tile that hold a token below the CTA's last slot
   uint32_t use[4];         // those of them in the windows' reach of some valid token
-  float ks[2], vs[2];      // scales of the two blocks
+  __half2 ks[2], vs[2];    // scales of the two blocks in the tiles (tile_scale)
   int pmin, pmax;          // range of the positions of the ok slots
+  uint32_t halves;         // blocks whose tiles hold halves: K's in bits 0 and 1, V's 2 and 3
   int seq, base;           // seq: each of them is at position base + its place in the tile
   int pos[BN];
 };
+static_assert(sizeof(Meta) % 16 == 0 && offsetof(Meta, use) % 8 == 0, "pairs of use");
 
 struct Shared {
   uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2],
@@ -326,6 +329,33 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
       const uint32_t lead = elect_one();
       constexpr uint32_t idesc_qk = idesc_f16(BM, BN, /*f16*/ 0, 0, 0);
       constexpr uint32_t idesc_pv = idesc_f16(BM, DH, /*f16*/ 0, 0, /*B MN-major*/ 1);
+      // Blocks whose tiles hold halves (tile_scale) are multiplied twice, the
+      // second time onto the first: S of their 64 slots, their part of O.  (Here
+      // rather than in the softmax, whose registers and instructions every tile
+      // would pay for: 27B-shaped chunk 403 us, and 396 like this.)
+      constexpr uint32_t idesc_qk1 = idesc_f16(BM, kC8Block, /*f16*/ 0, 0, 0);
+      constexpr uint32_t KBLK = kC8Block * 128;               // a block's rows of a K chunk
+      uint32_t halves = 0, halves_pv = 0;                     // of the tiles of S and of PV
+      // S += Q K^T for channels [k0, k1) / 16 of the block's slots
+      auto again_s = [&](uint32_t d, uint32_t qa, uint32_t ka, int k0, int k1) {
+#pragma unroll 1
+        for (int blk = 0; blk < 2; ++blk) {
+          if (!((halves >> blk) & 1u)) continue;
+#pragma unroll 1
+          for (int k = k0; k < k1; ++k) {
+            const uint32_t off = (k >> 2) * CHUNK + (k & 3) * 32;
+            mma_ss_lead(lead, d + blk * kC8Block, sdesc_sw128(qa + off, 16, 1024),
+                        sdesc_sw128(ka + off + blk * KBLK, 16, 1024), idesc_qk1, 1u);
+          }
+        }
+      };
+      // O += P V for the block's slots, 16 at a time
+      auto again_pv = [&](int blk, uint32_t d, uint32_t pa, uint32_t va, uint32_t lbo) {
+        if (!((halves_pv >> (2 + blk)) & 1u)) return;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k)
+          mma_ts_lead(lead, d, pa + (blk * 4 + k) * 8, sdesc_sw128(va + k * 2048, lbo, 1024), idesc_pv, 1u);
+      };
       const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK), v_addr = smem_u32(sV);
       bool ok = wait_warp(sh.q_full, 0, kSiteQ);
       if constexpr (C::NQ == 2) {
@@ -337,6 +367,7 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
             mma_ss_lead(lead, tbase + e * 128, sdesc_sw128(q_addr + e * C::QT_BYTES + off, 16, 1024),
                         sdesc_sw128(kb + off, 16, 1024), idesc_qk, k > 0 ? 1u : 0u);
           }
+          if (halves & 3u) again_s(tbase + e * 128, q_addr + e * C::QT_BYTES, kb, 0, DH / 16);
           mma_commit_lead(lead, smem_u32(&sh.s_full[e]));
         };
         auto issue_pv = [&](int e, int i) -> bool {
@@ -349,12 +380,15 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
             mma_ts_lead(lead, tbase + O_COL + e * 128, tbase + e * 128 + k * 8,
                         sdesc_sw128(vb + k * 2048, CHUNK, 1024), idesc_pv,
                         (i > 0 || k > 0) ? 1u : 0u);
+          for (int blk = 0; halves_pv >= 4u && blk < 2; ++blk)
+            again_pv(blk, tbase + O_COL + e * 128, tbase + e * 128, vb + blk * 4 * 2048, CHUNK);
           return true;
         };
         for (int i = 0; ok && i < n_tiles; ++i) {
           ok = wait_warp(sh.k_full[i & 1], (i >> 1) & 1, kSiteKFull);
           if (!ok) break;
           tc_fence_after();
+          halves = sh.meta[i % NMETA].halves;   // (the converters have waited for it)
           for (int e = 0; ok && e < nq; ++e) {
             // S_e reuses the columns of P_e of the tile before: the tensor
             // pipe runs PV_e before it.
@@ -365,6 +399,7 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
           }
           if (!ok) break;
           mma_commit_lead(lead, smem_u32(&sh.k_empty[i & 1]));
+          halves_pv = halves;
         }
         for (int e = 0; ok && e < nq; ++e) {
           ok = issue_pv(e, n_tiles - 1);
@@ -381,6 +416,8 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
           for (int k = 0; k < BN / 16; ++k)
             mma_ts_lead(lead, tbase + O_COL, tbase + (i & 1) * 128 + k * 8,
                         sdesc_sw128(vb + k * 2048, CHUNK, 1024), idesc_pv, (i > 0 || k > 0) ? 1u : 0u);
+          for (int blk = 0; halves_pv >= 4u && blk < 2; ++blk)
+            again_pv(blk, tbase + O_COL, tbase + (i & 1) * 128, vb + blk * 4 * 2048, CHUNK);
           mma_commit_lead(lead, smem_u32(&sh.v_empty[i & 1]));
           mma_commit_lead(lead, smem_u32(&sh.pv_done[i & 1]));
           return true;
@@ -389,6 +426,7 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
           ok = wait_warp(sh.k_full[i & 1], (i >> 1) & 1, kSiteKFull);
           if (!ok) break;
           tc_fence_after();
+          halves = sh.meta[i % NMETA].halves;   // (the converters have waited for it)
           const uint32_t kb = k_addr + (i & 1) * PART;
 #pragma unroll
           for (int k = 0; k < DH / 16; ++k) {
@@ -396,9 +434,11 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
             mma_ss_lead(lead, tbase + (i & 1) * 128, sdesc_sw128(q_addr + off, 16, 1024),
                         sdesc_sw128(kb + off, 16, 1024), idesc_qk, k > 0 ? 1u : 0u);
           }
+          if (halves & 3u) again_s(tbase + (i & 1) * 128, q_addr, kb, 0, DH / 16);
           mma_commit_lead(lead, smem_u32(&sh.k_empty[i & 1]));
           mma_commit_lead(lead, smem_u32(&sh.s_full[i & 1]));
           if (i > 0) ok = issue_pv(i - 1);
+          halves_pv = halves;
         }
         if (ok) ok = issue_pv(n_tiles - 1);
         if (ok) mma_commit_lead(lead, smem_u32(&sh.o_final[0]));
@@ -413,6 +453,7 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
               mma_ts_lead(lead, tbase + O_COL, tbase + (i & 1) * 128 + (h * 4 + k) * 8,
                           sdesc_sw128(v_addr + h * PART + k * 2048, CHUNK / 2, 1024), idesc_pv,
                           (i > 0 || h > 0 || k > 0) ? 1u : 0u);
+            again_pv(h, tbase + O_COL, tbase + (i & 1) * 128, v_addr + h * PART, CHUNK / 2);
             mma_commit_lead(lead, smem_u32(&sh.v_empty[h]));
           }
           mma_commit_lead(lead, smem_u32(&sh.pv_done[i & 1]));
@@ -425,17 +466,20 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
             ok = wait_warp(sh.k_full[h], i & 1, kSiteKFull);
             if (!ok) break;
             tc_fence_after();
+            halves = sh.meta[i % NMETA].halves;   // (the converters have waited for it)
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const uint32_t off = (h * 2 + (k >> 2)) * CHUNK + (k & 3) * 32;
               mma_ss_lead(lead, tbase + (i & 1) * 128, sdesc_sw128(q_addr + off, 16, 1024),
                           sdesc_sw128(k_addr + off, 16, 1024), idesc_qk, (h > 0 || k > 0) ? 1u : 0u);
             }
+            if (halves & 3u) again_s(tbase + (i & 1) * 128, q_addr, k_addr, h * 8, h * 8 + 8);
             mma_commit_lead(lead, smem_u32(&sh.k_empty[h]));
           }
           if (!ok) break;
           mma_commit_lead(lead, smem_u32(&sh.s_full[i & 1]));
           if (i > 0) ok = issue_pv(i - 1);
+          halves_pv = halves;
         }
         if (ok) ok = issue_pv(n_tiles - 1);
         if (ok) mma_commit_lead(lead, smem_u32(&sh.o_final[0]));
@@ -501,8 +545,10 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
           bn = __reduce_min_sync(0xffffffffu, bn);
           bx = __reduce_max_sync(0xffffffffu, bx);
         }
-        if (lane < 4) (lane & 2 ? m.vs : m.ks)[lane & 1] = ns;
+        const uint32_t halves = __ballot_sync(0xffffffffu, lane < 4 && halved(ns));
+        if (lane < 4) (lane & 2 ? m.vs : m.ks)[lane & 1] = tile_scale(ns);
         if (lane == 0) {
+          m.halves = halves;
           m.pmin = mn;
           m.pmax = mx;
           m.seq = bn == bx;
@@ -537,15 +583,15 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
       const Meta& m = sh.meta[i % NMETA];
       // scales and counted slots of the granules' 64-slot blocks (a block
       // without any may have any scale)
-      const float* msc = v ? m.vs : m.ks;
-      float sc[NG];
+      const __half2* msc = v ? m.vs : m.ks;
+      __half2 sc[NG];
       uint2 u[NG];
       bool whole_block = true;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const int blk = v256 ? hh : g0 + g;
         u[g] = *reinterpret_cast<const uint2*>(m.use + 2 * blk);
-        sc[g] = (u[g].x | u[g].y) != 0 ? msc[blk] : 0.f;
+        sc[g] = (u[g].x | u[g].y) != 0 ? msc[blk] : __float2half2_rn(0.f);
         whole_block &= (u[g].x & u[g].y) == 0xffffffffu;
       }
       uint2 x[4 * NG][2];
@@ -591,20 +637,10 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
       // or the next 64 slots
       const uint32_t chunk = v256 ? CHUNK / 2 : CHUNK, g1 = v256 ? CHUNK : CHUNK / 2;
       uint8_t* base = (v ? sV : sK) + buf * PART + (col >> 2) * chunk + g0 * g1 + row0 * 128;
-      bool clamp = false;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) clamp |= sc[g] > 128.f;
-      if (clamp) {
-#pragma unroll
-        for (int k = 0; k < 4 * NG; ++k)
-          store16_values<true>(x[k][0], x[k][1], pack_half2(sc[k >> 2], sc[k >> 2]), col, row0,
-                               base + (k & 3) * 2048 + (k >> 2) * g1);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4 * NG; ++k)
-          store16_values<false>(x[k][0], x[k][1], pack_half2(sc[k >> 2], sc[k >> 2]), col, row0,
-                                base + (k & 3) * 2048 + (k >> 2) * g1);
-      }
+      for (int k = 0; k < 4 * NG; ++k)
+        store16_values(x[k][0], x[k][1], sc[k >> 2], col, row0,
+                       base + (k & 3) * 2048 + (k >> 2) * g1);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {

@@ -54,44 +54,43 @@ __device__ __forceinline__ void window_range(int qn, int qx, int window, int& pl
   phi = static_cast<int>(z < -1 ? -1 : (z > INT_MAX ? INT_MAX : z));
 }
 
+// A block's scale in the fp16 tiles.  At scales above 128 a value can pass
+// fp16's largest (a token's 65504 is stored as 65536, an infinity as 448 *
+// 256): the tiles take half of it there, and the products with it are doubled.
+__device__ __forceinline__ bool halved(float scale) { return scale > 128.f; }
+__device__ __forceinline__ __half2 tile_scale(float scale) {
+  return __float2half2_rn(halved(scale) ? 0.5f * scale : scale);
+}
+
 // 16 cache bytes (one slot's channels 16 col .. 16 col + 15) as fp16 values in
 // a 128-byte-swizzled tile: base points at the slot's 128-byte row in the
-// chunk of 64 channels that holds them.  scale2: the block's as two fp16, or 0 with x = 0
-// for a hidden slot.  CLAMP for scales above 128, which can take a value past
-// fp16's largest; it becomes 65504 there.  The two 16-byte stores go out in an
-// order that puts eight neighbouring threads (col 0..7 of a slot) on eight
-// bank groups: a and b are the 8 bytes of the first and the second store, the
-// upper half first where swap8 is 1 (by the slot too, so that 8-byte loads of
-// two slots' bytes meet no conflict either).
+// chunk of 64 channels that holds them.  scale: the block's as two fp16
+// (tile_scale), or 0 with a = b = 0 for a hidden slot.  The two 16-byte stores go out
+// in an order that puts eight neighbouring threads (col 0..7 of a slot) on
+// eight bank groups: a and b are the 8 bytes of the first and the second
+// store, the upper half first where swap8 is 1 (by the slot too, so that 8-byte
+// loads of two slots' bytes meet no conflict either).
 __device__ __forceinline__ int swap8(int col, int row) { return ((col >> 2) ^ row) & 1; }
 
-template <bool CLAMP>
 __device__ __forceinline__ uint4 values8(uint2 w, __half2 scale) {
   const uint32_t in[2] = {w.x, w.y};
   uint32_t o[4];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const uint32_t lo = c8_half2(in[k]), hi = c8_half2_hi(in[k]);
-    __half2 v0 = __hmul2(*reinterpret_cast<const __half2*>(&lo), scale);
-    __half2 v1 = __hmul2(*reinterpret_cast<const __half2*>(&hi), scale);
-    if constexpr (CLAMP) {
-      const __half2 top = __float2half2_rn(65504.f);
-      v0 = __hmax2_nan(__hmin2_nan(v0, top), __hneg2(top));
-      v1 = __hmax2_nan(__hmin2_nan(v1, top), __hneg2(top));
-    }
-    o[2 * k] = *reinterpret_cast<uint32_t*>(&v0);
-    o[2 * k + 1] = *reinterpret_cast<uint32_t*>(&v1);
+    const __half2 v0 = __hmul2(*reinterpret_cast<const __half2*>(&lo), scale);
+    const __half2 v1 = __hmul2(*reinterpret_cast<const __half2*>(&hi), scale);
+    o[2 * k] = *reinterpret_cast<const uint32_t*>(&v0);
+    o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&v1);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <bool CLAMP>
-__device__ __forceinline__ void store16_values(uint2 a, uint2 b, uint32_t scale2, int col, int row,
+__device__ __forceinline__ void store16_values(uint2 a, uint2 b, __half2 scale, int col, int row,
                                                uint8_t* base) {
-  const __half2 scale = *reinterpret_cast<const __half2*>(&scale2);
   const int u0 = (col & 3) * 2, swap = swap8(col, row), r7 = row & 7;
-  *reinterpret_cast<uint4*>(base + (((u0 + swap) ^ r7) << 4)) = values8<CLAMP>(a, scale);
-  *reinterpret_cast<uint4*>(base + (((u0 + 1 - swap) ^ r7) << 4)) = values8<CLAMP>(b, scale);
+  *reinterpret_cast<uint4*>(base + (((u0 + swap) ^ r7) << 4)) = values8(a, scale);
+  *reinterpret_cast<uint4*>(base + (((u0 + 1 - swap) ^ r7) << 4)) = values8(b, scale);
 }
 
 // A query row's entry of rowstat: (reference, 1 / sum of exp2 against it), or

@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ int sq[2][2][BN];               // query positions of the tile's tokens
   __shared__ float other[BM];
   __shared__ int pr[4];                      // min / max position, first / last token
+  __shared__ int any_halves;                 // does a K tile hold halves (tile_scale)?
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_flag;
 
@@ -118,6 +119,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     pr[1] = -1;
     pr[2] = INT_MAX;
     pr[3] = -1;
+    any_halves = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmQ);
   }
@@ -139,6 +141,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       atomicMin(&pr[0], mn);
       atomicMax(&pr[1], mx);
     }
+  } else {
+    // the scales of the tile's blocks, heads next to each other
+    const int n = (min(s_tile / kC8Block + 2, p.nb) - s_tile / kC8Block) * p.H_kv;
+    const float* sc = p.K_scale + (static_cast<size_t>(b) * p.nb + s_tile / kC8Block) * p.H_kv;
+    for (int i = tid - 128; i < n; i += THREADS - 128)
+      if (halved(__ldcg(sc + i))) any_halves = 1;
   }
   __syncthreads();
   // The tokens that may see a slot of the tile.
@@ -272,18 +280,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int hh = q / C::PARTS, part = q % C::PARTS, kb = hh % C::KB;
         if (part == 0 && !wait_warp(k_empty[kb], ((hh / C::KB) & 1) ^ 1, kSiteKEmpty)) break;
         uint8_t* dst = sK + (kb * C::PARTS + part) * PART + ((ct % 8) >> 2) * CHUNK;
-        const uint32_t h0 = pack_half2(sc0, sc0), h1 = pack_half2(sc1, sc1);
-        if (sc0 > 128.f || sc1 > 128.f) {
+        // (finite where a block holds no token: the bytes are zeros there)
+        const __half2 h0 = tile_scale(fminf(fabsf(sc0), 256.f)), h1 = tile_scale(fminf(fabsf(sc1), 256.f));
 #pragma unroll
-          for (int it = 0; it < 8; ++it)
-            store16_values<true>(x[it][0], x[it][1], (ok >> it) & 1u ? (it >= 4 ? h1 : h0) : 0u, ct % 8,
-                                 row0 + it * 16, dst + (row0 + it * 16) * 128);
-        } else {
-#pragma unroll
-          for (int it = 0; it < 8; ++it)
-            store16_values<false>(x[it][0], x[it][1], (ok >> it) & 1u ? (it >= 4 ? h1 : h0) : 0u, ct % 8,
-                                  row0 + it * 16, dst + (row0 + it * 16) * 128);
-        }
+        for (int it = 0; it < 8; ++it)
+          store16_values(x[it][0], x[it][1], it >= 4 ? h1 : h0, ct % 8, row0 + it * 16,
+                         dst + (row0 + it * 16) * 128);
         if (part == C::PARTS - 1)
           publish8(k_full[kb], lane);
         else
@@ -305,7 +307,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       qhi = ps > INT_MAX - (p.window - 1) ? INT_MAX : ps + (p.window - 1);
     }
     const size_t rows = static_cast<size_t>(p.T) * G;
+    // the slot's K scale of the unit's head: what its logits count (tile_scale)
+    const float* sc = p.K_scale + (static_cast<size_t>(b) * p.nb + min(s / kC8Block, p.nb - 1)) * p.H_kv;
     float2 nx = make_float2(INFINITY, 0.f);
+    const bool halves = any_halves != 0;
     int nq = 0;
     auto fetch = [&](int n) {
       if (n >= n_units) return;
@@ -329,6 +334,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) continue;
       tc_fence_after();
       const int t0 = tile_of(u0 + n) * C::TQ;
+      float by = LOG2E;
+      if (halves) by = halved(__ldcg(sc + head_of(u0 + n))) ? 2.f * LOG2E : LOG2E;
       // columns [c0, c1) are valid tokens at or behind this slot
       const int n_tok = max(0, min(C::TQ, valid - t0));
       int c0 = max(0, min(C::TQ, s - p.end - t0)) * G, c1 = n_tok * G;
@@ -379,8 +386,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
           const float4 a = st4[(c + k) >> 1];       // rows k and k + 1
-          const float e0 = ex2(fmaf(__uint_as_float(x[k]), LOG2E, -a.x));
-          const float e1 = ex2(fmaf(__uint_as_float(x[k + 1]), LOG2E, -a.z));
+          const float e0 = ex2(fmaf(__uint_as_float(x[k]), by, -a.x));
+          const float e1 = ex2(fmaf(__uint_as_float(x[k + 1]), by, -a.z));
           if (k & 2) {
             acc.z = fmaf(e0, a.y, acc.z);
             acc.w = fmaf(e1, a.w, acc.w);
