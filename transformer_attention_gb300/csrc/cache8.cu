@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kRowThreads) cache8_write_kernel(const WritePa
   const __half* rows = isv ? p.V_rows : p.K_rows;
   uint8_t* num = isv ? p.V8 : p.K8;
   float* scale = (isv ? p.V_scale : p.K_scale) + (static_cast<size_t>(b) * p.nb + blk) * p.H_kv + j;
-  const int valid = p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0);
+  const int valid = p.T - (p.pad_lens != nullptr ? __ldcg(p.pad_lens + b) : 0);
   const int s0 = blk * kTile, c = (tid % TPR) * 8;
   const bool held = s0 < p.end;                // the block holds earlier tokens
   const float old = held ? __ldcg(scale) : 0.f;
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kRowThreads) cache8_write_kernel(const WritePa
     const int t = s0 + tid - p.end;
     if (t >= 0 && t < p.T)
       p.posc[static_cast<size_t>(b) * p.S + s0 + tid] =
-          t < valid ? p.segment_pos[static_cast<size_t>(b) * p.T + t] : -1;
+          t < valid ? __ldcg(p.segment_pos + static_cast<size_t>(b) * p.T + t) : -1;
   }
 }
 

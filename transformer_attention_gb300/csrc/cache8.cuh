@@ -11,9 +11,10 @@
 // step, so reading a cache back as fp16 rounds nothing below fp16's largest.
 //
 // The kernels over this cache read what another launch may have written
-// (numbers, scales, positions, weights, scratch) past L1, by __ldcg: a kernel
-// starts while the one before it runs (pdl_enter), so that a line which that
-// one still reads into an SM's L1 may not be dropped again before this one.
+// (numbers, scales, weights, scratch, positions and padding of the slots and
+// of the queries) past L1, by __ldcg: a kernel starts while the one before it
+// runs (pdl_enter), so that a line which that one still reads into an SM's L1
+// may not be dropped again before this one.
 #pragma once
 
 #include <cstdint>

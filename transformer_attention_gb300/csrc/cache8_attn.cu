@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTA
   const int split = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
   const int G = p.H / p.H_kv;
   const int R = p.T * G;
-  const int valid = p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0);
+  const int valid = p.T - (p.pad_lens != nullptr ? __ldcg(p.pad_lens + b) : 0);
 
   if (tid == 0) {
 #pragma unroll
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTA
         const int t = r / G;
         lim[nt][e] = p.end + t;
         if (p.window > 0) {
-          const int qp = p.qpos[static_cast<size_t>(b) * p.T + t];
+          const int qp = __ldcg(p.qpos + static_cast<size_t>(b) * p.T + t);
           window_range(qp, qp, p.window, plo[nt][e], phi[nt][e]);
         }
       }
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(Cfg<DH, NT, RG>::THREADS, Cfg<DH, NT, RG>::CTA
     // early slots that some query of the row sees
     int qn = INT_MAX, qx = INT_MIN;
     for (int t = 0; t < min(valid, p.T); ++t) {
-      const int q = p.qpos[static_cast<size_t>(b) * p.T + t];
+      const int q = __ldcg(p.qpos + static_cast<size_t>(b) * p.T + t);
       qn = min(qn, q);
       qx = max(qx, q);
     }
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(256) weigh8_kernel(const WeighParams p) {
   // Rows in the order of the logits: kv head, token, head of the group.
   const int rows = p.T * p.H, G = p.H / p.H_kv, R = p.T * G;
   const size_t S64 = static_cast<size_t>(p.nb) * kTile;
-  const int valid = p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0);
+  const int valid = p.T - (p.pad_lens != nullptr ? __ldcg(p.pad_lens + b) : 0);
   // Did the first launch attend this slot's tile?
   const Tiles tl = tiles_of(p.end, p.T, valid, p.late, p.nsplit);
   const int k = s / kTile;

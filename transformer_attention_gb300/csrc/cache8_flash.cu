@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
   const int bjs = p.B * p.H_kv, item = p.items - 1 - unit / bjs;
   const int bj = unit % bjs, j = bj % p.H_kv, b = bj / p.H_kv;
   const int t0 = item * C::NQ * C::TQ;
-  const int valid = min(p.T, p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0));
+  const int valid = min(p.T, p.T - (p.pad_lens != nullptr ? __ldcg(p.pad_lens + b) : 0));
   const int t_end = min(t0 + C::NQ * C::TQ, valid);          // past the last valid token
   const int nq = C::NQ == 2 && t0 + C::TQ < p.T ? 2 : 1;     // query tiles with tokens
   const int hi = t_end > t0 ? p.end + t_end : 0;
@@ -930,7 +930,7 @@ __global__ void __launch_bounds__(1024) first8_kernel(const int32_t* __restrict_
   const int rank = cluster.block_rank(), C = cluster.num_blocks();
   __shared__ int found;
   const int item = blockIdx.x / C, b = blockIdx.y, tid = threadIdx.x;
-  const int valid = min(T, T - (pad_lens != nullptr ? pad_lens[b] : 0));
+  const int valid = min(T, T - (pad_lens != nullptr ? __ldcg(pad_lens + b) : 0));
   const int t0 = item * span, t_end = min(t0 + span, valid);
   const int hi = t_end > t0 ? end + t_end : 0;
   int qn = INT_MAX, qx = INT_MIN;

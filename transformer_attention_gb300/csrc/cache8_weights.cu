@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // the latest slots first: on a local layer the early tiles have no work
   const int us = blockIdx.x % p.usplit, b = (blockIdx.x / p.usplit) % p.B;
   const int st = p.tiles - 1 - static_cast<int>(blockIdx.x) / p.usplit / p.B;
-  const int valid = min(p.T, p.T - (p.pad_lens != nullptr ? p.pad_lens[b] : 0));
+  const int valid = min(p.T, p.T - (p.pad_lens != nullptr ? __ldcg(p.pad_lens + b) : 0));
   const int s_tile = st * BM, hi = valid > 0 ? p.end + valid : 0;
 
   if (tid == 0) {
