@@ -109,3 +109,35 @@ def test_stored_values_beyond_fp16(T, H, H_kv, d_h):
     C._check_o(O, ref, A, PV, 114688.0, end + T, d_h, torch.bfloat16)
     dw = 2 * ((d_h / 16 + 4) * 2.0 ** -22 * float(A.max()) + 2.0 ** -21)
     assert ((wsum.cpu().to(F64) - w).abs() <= (dw + (T * H + 2) * 2.0 ** -23) * w).all()
+
+
+@pytest.mark.parametrize("window", [0, 150])
+@pytest.mark.parametrize("T,H,H_kv,d_h", FORMS + [(600, 2, 1, 128), (200, 2, 2, 256)])
+def test_large_values_in_some_blocks(T, H, H_kv, d_h, window):
+    """Blocks of the largest scale, for K, for V or for both, next to others."""
+    import transformer_attention_gb300 as G3
+    B, S, end = 2, 1500, 800
+    n = end + T
+    g = C._gen(10 + T)
+    k = torch.randn((B, n, H_kv, d_h), generator=g)
+    v = 3000 * torch.randn((B, n, H_kv, d_h), generator=g)
+    kind = (torch.arange(n)[:, None] // 64 * 7 + torch.arange(H_kv)[None] * 3) % 5   # of a block and head
+    top = torch.tensor([65504.0, float("inf"), 57344.0])
+    pick = top[torch.randint(0, 3, (B, n, H_kv), generator=g)]
+    k[..., 0] = torch.where((kind % 2 == 0)[None], pick, k[..., 0])
+    sign = torch.randint(0, 2, v.shape, generator=g) * 2.0 - 1.0
+    big = top[torch.randint(0, 3, v.shape, generator=g)] * sign
+    v = torch.where((kind >= 2)[None, :, :, None] & (torch.rand(v.shape, generator=g) < 0.3), big, v)
+    c = C8.write(C8.empty(B, S, H_kv, d_h), k.half(), v.half(), torch.arange(n).repeat(B, 1), None, 0)
+    for w in ("ks", "vs"):
+        assert 256.0 in c[w] and 0 < float((c[w] == 256.0).double().mean()) < 1
+    Q = (torch.randn((B, T, H, d_h), generator=g) * 0.02).half()
+    Q[..., 0] = 2.0 ** -15
+    seg = torch.arange(end, n).repeat(B, 1)
+    ref, w, A, PV = C8.attend(Q, c, seg, None, end, window)
+    wsum = torch.zeros((B, S), device="cuda")
+    O = C._attend(G3, Q, C._to_dev(c), seg, None, T, end, H, H_kv, d_h, window, torch.bfloat16, wsum)
+    assert G3.gemma3_attn_check_status() == 0
+    C._check_o(O, ref, A, PV, 114688.0, n, d_h, torch.bfloat16)
+    dw = 2 * ((d_h / 16 + 4) * 2.0 ** -22 * float(A.max()) + 2.0 ** -21)
+    assert ((wsum.cpu().to(F64) - w).abs() <= (dw + (T * H + 2) * 2.0 ** -23) * w).all()
