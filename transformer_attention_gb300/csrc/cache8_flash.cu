@@ -845,7 +845,7 @@ template <int DH, int G, int NQ>
 __global__ void __launch_bounds__(256) flash8_merge_kernel(const Params p) {
   pdl_enter();
   using C = Cfg<DH, G, NQ>;
-  if (lost_work(p.status, kLostWait)) return;   // parts may be missing
+  const bool lost = lost_work(p.status, kLostWait);   // parts may be missing
   constexpr int ROWS = 8;
   const int unit = p.whole + blockIdx.x;
   const int bjs = p.B * p.H_kv, item = p.items - 1 - unit / bjs;
@@ -897,6 +897,7 @@ __global__ void __launch_bounds__(256) flash8_merge_kernel(const Params p) {
         }
       }
     }
+    if (lost) return;
     const float inv = L != 0.f ? 1.f / L : 0.f;
     const size_t orow = (static_cast<size_t>(b) * p.T + t) * p.H + j * G + r % G;
 #pragma unroll
