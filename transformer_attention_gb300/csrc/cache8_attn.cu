@@ -13,12 +13,12 @@
 // contractions run on mma.sync m16n8k16 with the slots (K) and the channels
 // (V) on the 16-row side and the query rows on the 8-wide side.  One token over
 // 131072 slots of 16 kv heads: 86 us, 6.3 TB/s; 9 to 16 rows double the
-// fragments and reach about 3 TB/s at d_h = 128 (16 rows over 65536 slots of 8
-// kv heads 50 us, 8 rows 35), bound by the latency of the dozen warps that fit
-// an SM.  At one byte
-// per number the fp32 CUDA cores would need 4 FMAs per byte for 4 rows, about
-// their whole rate at the HBM rate, while these MMAs take under a fifth of
-// theirs (measured 1024 fp16 FMA per clock and SM).  A tcgen05 tile has 128
+// fragments and reach about 3 TB/s (16 rows over 65536 slots, d_h = 128 and 8
+// kv heads 44 us, d_h = 256 and 4 kv heads 46; 8 rows 35), bound by the latency
+// of the ten warps that fit an SM.  At one byte per number the fp32 CUDA cores
+// would need 4 FMAs per byte for 4 rows, about their whole rate at the HBM rate,
+// while these MMAs take under a fifth of theirs (measured 1024 fp16 FMA per
+// clock and SM).  A tcgen05 tile has 128
 // rows for which there are no queries, and could take the e4m3 bytes as they
 // are only if the probabilities were split into 8-bit parts; many rows go to
 // the tcgen05 kernel (cache8_flash.cu).

@@ -15,7 +15,7 @@
 // 3500 clocks at 128 bytes each against 2050 of MMA; two query tiles of d_h =
 // 128 320 KB, 2500 against 2050.  (Without the conversion's arithmetic and
 // stores a prompt of 16384 tokens, d_h = 256, takes 603 us instead of 818.)
-// 1024 tokens over 32768 slots, 27B-shaped: 402 us, 1.35 PFLOP/s.
+// 1024 tokens over 32768 slots, 27B-shaped: 398 us, 1.36 PFLOP/s.
 //
 // Warps (d_h = 128, two query tiles e = 0, 1):
 //   0      TMA of the Q tiles (and for d_h = 256 of V's bytes)
@@ -206,9 +206,9 @@ __global__ void __launch_bounds__(Cfg<DH, G, NQ>::THREADS, 1)
 
   // CTAs: the whole units, the first parts of the cut ones, the other parts.
   // Units: the latest tokens of every batch row and kv head first, which have
-  // the most slots on a causal prompt.  (A prompt of 4096 tokens, 27B-shaped:
-  // 124 us, and 150 with the items of a head next to each other and the last
-  // ones cut.)
+  // the most slots on a causal prompt.  (A prompt of 4096 tokens, 27B-shaped, 119
+  // us; 124 when this was chosen, against 150 with the items of a head next to
+  // each other and the last ones cut.)
   const int head_units = p.whole + p.cut, rest = static_cast<int>(blockIdx.x) - head_units;
   const int unit = rest < 0 ? blockIdx.x : p.whole + rest % p.cut;
   const int pt = rest < 0 ? 0 : 1 + rest / p.cut;           // part

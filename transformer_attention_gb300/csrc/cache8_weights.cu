@@ -13,10 +13,10 @@
 // always in the same order; several CTAs on one slot tile write parts that a
 // last launch adds.  Bound by the way of a Q tile through the pipeline, copy,
 // MMA and sums, not by any one of them: 24 us for 515 tokens, 16 heads, window
-// 1024, whose products take 5, and 433 us for 1024 tokens over 32768 slots,
+// 1024, whose products take 5, and 429 us for 1024 tokens over 32768 slots,
 // 27B-shaped, whose products take 143 (without exponentials, row statistics
-// and MMA 260).  Four warpgroups of sums, or two slot tiles per CTA, bring the
-// long call to 370 us and cost short ones 2 us.
+// and MMA 260).  Four warpgroups of sums bring the long call to 390 us, two slot
+// tiles per CTA to 370; either costs short ones 2 us.
 //
 // Warps: 0 TMA of Q, 1 MMA issue, 4-7 converters, 8-11 and 12-15 the sums of
 // even and odd tiles.  TMEM: four S^T buffers of 128 columns.
