@@ -45,7 +45,8 @@ enum {
   GEMMA3_ERR_CUDA = -4,        /* a CUDA runtime call or kernel launch failed */
   GEMMA3_ERR_TIMEOUT = -5,     /* a kernel gave up on a bounded wait (device status word) */
   GEMMA3_ERR_WORKSPACE = -6,   /* workspace smaller than gemma3_*_workspace_size() */
-  GEMMA3_ERR_BAD_INPUT = -7    /* a kernel found invalid data (a token id outside [0, V)) */
+  GEMMA3_ERR_BAD_INPUT = -7    /* a kernel found invalid data (a token id outside [0, V), a paged
+                                  batch that does not fit itself) */
 };
 
 /* Attention types of [RT] How it works (AttentionType enum). */
@@ -439,6 +440,120 @@ int gemma3_attn_forward_cached8(const gemma3_attn_dims* dims, int S, int end_ind
                                 float* V_scale, int32_t* pos_cache, float* weight_sum, void* out,
                                 void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ paged KV cache */
+
+/* A layer's KV cache in pages, for sequences of lengths of their own:
+ *   K_pages, V_pages  [n_pages, page_size, H_kv, d_h] fp16, 16-byte aligned: K'
+ *                     and V; page_size a power of two from 16 to 256
+ * Slot s of sequence b is row s % page_size of page page_table[b, s /
+ * page_size].  Its slots [0, lens[b]) are filled, and a filled slot's position
+ * is its number.  Pages may be shared by sequences that only read them.
+ *   The new tokens of sequence b are the rows [row_start[b], row_start[b + 1])
+ * of packed arrays of M rows (none: the sequence has no part in the call); rows
+ * from row_start[B] on belong to no sequence.  Token i goes to slot lens[b] + i.
+ *   parents NULL: a step or a chunk, each token follows the one before it.
+ * Else a tree of drafted tokens: parents[row] is the number i of an earlier
+ * new token of the same sequence, or -1 for one that follows the filled slots.
+ * A token's position is lens[b] + its depth in the tree (the number of its
+ * ancestors among the new tokens).
+ *   The arrays lie on the device and are read when the kernels run, so that a
+ * captured call can be replayed with others.  The kernels check them: a
+ * sequence whose rows (not ascending, beyond M, more than T_max) or slots
+ * (negative, beyond max_pages * page_size) do not fit counts as one without
+ * new tokens, a parent that is not an earlier token as -1, a page outside the
+ * pool is neither written nor read, and GEMMA3_ERR_BAD_INPUT comes from
+ * gemma3_attn_check_status.  Entries of the page table behind a sequence's last
+ * slot are not looked at. */
+typedef struct {
+  int B, M, T_max;                     /* sequences, packed rows, most new tokens of a sequence */
+  int page_size, n_pages, max_pages;   /* max_pages: entries of a sequence in page_table */
+  const int32_t* lens;                 /* [B] */
+  const int32_t* row_start;            /* [B + 1] */
+  const int32_t* parents;              /* [M] or NULL; T_max <= GEMMA3_TREE_MAX if given */
+  const int32_t* page_table;           /* [B, max_pages] */
+} gemma3_paged_batch;
+
+/* Most new tokens of a sequence with parents. */
+enum { GEMMA3_TREE_MAX = 64 };
+
+/* segment_pos [M] int32: every row's position (0 behind the last sequence), as
+ * the projection entry points take them. */
+int gemma3_paged_positions(const gemma3_paged_batch* batch, int32_t* segment_pos, void* stream);
+
+/* The new tokens' K' and V to their slots, with the norm and the rotation on
+ * the way: RMSNorm over d_h with (1 + gamma_q) of the query heads of Q and (1 +
+ * gamma_k) of the key heads of K, RoPE at the token's position with (rope_base,
+ * rope_scale), Q' = query_scale * Q ([QK] How it works), as gemma3_qk_norm_rope.
+ *   Q       [M, ldq] fp16, H*d_h values per row; Q_out [M, ldqo] fp16 gets Q'
+ *           (it may be Q, with ldqo == ldq, and must not overlap it otherwise)
+ *   K, V    [M, ldkv] fp16, H_kv*d_h values per row; not changed
+ * gamma_q == gamma_k == NULL: the rows of K are K' already and go to the pages
+ * as they are; Q and Q_out are not looked at (H, rope_* and query_scale too).
+ * Rows of Q_out behind the last sequence are left as they were.  Positions
+ * below 2^24.  A page that two sequences of the batch write to holds what
+ * either wrote. */
+int gemma3_paged_append(const gemma3_paged_batch* batch, const void* Q, long ldq, void* Q_out,
+                        long ldqo, const void* K, const void* V, long ldkv, const void* gamma_q,
+                        const void* gamma_k, int H, int H_kv, int d_h, double rope_base,
+                        double rope_scale, float query_scale, void* K_pages, void* V_pages,
+                        void* stream);
+
+/* Workspace of gemma3_paged_attention (of B, M and the pages it is independent). */
+int gemma3_paged_attention_workspace_size(const gemma3_paged_batch* batch, int H, int H_kv, int d_h,
+                                          size_t* bytes);
+
+/* Attention of the new tokens, already in their slots, over the pages: Q' [M, H,
+ * d_h] fp16 (query scale applied); O [M, H, d_h] in o_dtype (GEMMA3_BF16 |
+ * GEMMA3_F16; may be Q').  A token sees the filled slots of its sequence, its
+ * ancestors among the new tokens and itself; with window > 0 (a local layer)
+ * those of them whose position is above its own - window.  Rows behind the last
+ * sequence are left as they were.
+ *   Logits, sums and the running output are fp32; for the product with V a
+ * probability is rounded to fp16 as a multiple of its row's largest (off by
+ * 2^-11 relative, by 2^-32 absolute below 2^-21).  The same call gives the same
+ * bits.
+ *   What slots hold never matters, NaN included, behind a sequence's last new
+ * token and, on a local layer, before the window of all of its new tokens.  A
+ * NaN in any other slot may reach every new token of its sequence. */
+int gemma3_paged_attention(const gemma3_paged_batch* batch, const void* Q, const void* K_pages,
+                           const void* V_pages, void* O, int o_dtype, int H, int H_kv, int d_h,
+                           int window, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Of each sequence's new tokens the accepted ones move to the slots from
+ * lens[b] on, in all of num_layers pools that lie one behind the other (K_pages,
+ * V_pages [num_layers, n_pages, page_size, H_kv, d_h]).
+ *   accepted  [B, T_max] int32: their numbers, ascending, the first counts[b]
+ *             of each row (the others are not looked at); NULL: the first ones,
+ *             nothing moves
+ *   counts    [B] int32, 0 <= counts[b] <= new tokens; NULL: all of them
+ *   new_lens  [B] int32, must not overlap batch->lens: lens[b] + counts[b]
+ * The accepted tokens should be a path from the root: a token's position then
+ * is its new slot.  A sequence whose accepted tokens do not ascend or lie
+ * outside its new ones is left as it is (GEMMA3_ERR_BAD_INPUT as above).
+ * batch->parents is not used. */
+int gemma3_paged_commit(const gemma3_paged_batch* batch, const int32_t* accepted,
+                        const int32_t* counts, int num_layers, int H_kv, int d_h, void* K_pages,
+                        void* V_pages, int32_t* new_lens, void* stream);
+
+/* Workspace of gemma3_attn_forward_paged. */
+int gemma3_attn_paged_workspace_size(const gemma3_paged_batch* batch, int D, int H, int H_kv,
+                                     int d_h, size_t* bytes);
+
+/* One attention layer over a paged batch: x [M, D] bf16 -> out [M, D] bf16.
+ * Projections, QK-norm, RoPE and query scale as gemma3_attn_forward at the
+ * positions above; K' and V go to the pages as gemma3_paged_append writes them;
+ * the tokens attend as gemma3_paged_attention does; output projection.  Rows of
+ * out behind the last sequence are 0.
+ *   After an error recorded on the device (by any call, until
+ * gemma3_attn_check_status) out is undefined, and the pages stay as they were
+ * if it left the projections without a result. */
+int gemma3_attn_forward_paged(const gemma3_paged_batch* batch, int D, int H, int H_kv, int d_h,
+                              const void* x, const void* Wq, const void* Wkv, const void* Wo,
+                              const void* gamma_q, const void* gamma_k, int attn_type, int window,
+                              double rope_base, double rope_scale, float query_scale,
+                              void* K_pages, void* V_pages, void* out, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------- stage entry points */
 
 /* C[M, N] = A[M, K] * W[N, K]^T (the projection einsums of [AB] How it
@@ -570,7 +685,8 @@ int gemma3_postnorm_residual(const float* a, const void* x, int x_dtype, const v
 int gemma3_attn_check_status(void* stream);
 
 /* Raw device status word of the last check (0 = none; 0x1000 + n = wait site
- * n; 0x2000 = a token id outside [0, V)). */
+ * n; 0x2000 = a token id outside [0, V); 0x4000 = a paged batch's row, length,
+ * page, parent or accepted token out of its range). */
 int gemma3_last_device_status(void);
 
 /* Human-readable text of a status code. */

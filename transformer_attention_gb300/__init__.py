@@ -17,6 +17,9 @@ from ._lib import (  # noqa: F401  (re-exported C-ABI names)
     GEMMA3_CACHE8_BLOCK, gemma3_attn_cached8_workspace_size, gemma3_attn_forward_cached8,
     gemma3_cached8_attention, gemma3_cached8_attention_workspace_size, gemma3_kv_cache8_evict,
     gemma3_kv_cache8_read, gemma3_kv_cache8_write,
+    GEMMA3_TREE_MAX, PagedBatch, gemma3_attn_forward_paged, gemma3_attn_paged_workspace_size,
+    gemma3_paged_append, gemma3_paged_attention, gemma3_paged_attention_workspace_size,
+    gemma3_paged_commit, gemma3_paged_positions,
     gemma3_block_attn_forward, gemma3_block_attn_workspace_size, gemma3_block_ffn_forward,
     gemma3_block_ffn_workspace_size, gemma3_block_forward, gemma3_block_workspace_size,
     gemma3_cast_bf16_f16, gemma3_geglu,
@@ -28,8 +31,9 @@ from ._lib import (  # noqa: F401  (re-exported C-ABI names)
     gemma3_selftest_wait_timeout, gemma3_set_gemm_tile_rows, lib)
 
 __all__ = ["attention_forward", "attention_forward_cached", "attention_forward_cached8",
-           "block_attention_forward", "block_forward", "evict_kv_cache8", "model_forward",
-           "new_kv_cache", "new_kv_cache8", "linear", "lib"]
+           "attention_forward_paged", "block_attention_forward", "block_forward",
+           "commit_paged_cache", "evict_kv_cache8", "model_forward", "new_kv_cache",
+           "new_kv_cache8", "new_paged_cache", "paged_batch", "linear", "lib"]
 
 
 def _on(stream):
@@ -194,6 +198,83 @@ def evict_kv_cache8(cache, weight_sum, end_index, keep, recent, *, into=None, S=
     gemma3_kv_cache8_evict(K8, V8, K_scale, V_scale, pos, weight_sum, B, S0, end_index, H_kv, d_h,
                            keep, recent, *dst, w_dst, kept, dst[4].shape[1], stream)
     return dst, w_dst, kept
+
+
+def new_paged_cache(num_layers, n_pages, page_size, H_kv, d_h, device):
+    """An empty paged KV cache of num_layers layers: (K_pages, V_pages)
+    [num_layers, n_pages, page_size, H_kv, d_h] fp16."""
+    import torch
+    K = torch.zeros((num_layers, n_pages, page_size, H_kv, d_h), dtype=torch.float16,
+                    device=device)
+    return K, torch.zeros_like(K)
+
+
+def paged_batch(lens, row_start, page_table, *, rows, T_max, page_size, n_pages, parents=None):
+    """The batch that the paged calls take (PagedBatch): sequence b's slots [0,
+    lens[b]) are filled, its new tokens are rows [row_start[b], row_start[b +
+    1]) of packed arrays of ``rows`` rows, at most ``T_max`` of them, and its
+    slots lie in the pages page_table[b] of a pool of ``n_pages``.  parents
+    [rows] (T_max <= 64): drafted trees."""
+    return PagedBatch(lens, row_start, page_table, rows=rows, T_max=T_max, page_size=page_size,
+                      n_pages=n_pages, parents=parents)
+
+
+def _check_pages(cache, layers, batch, H_kv, d_h):
+    """ValueError unless ``cache`` is a pair of contiguous fp16 pools of these sizes."""
+    import torch
+    _, _, _, page_size, n_pages, _ = batch.sizes
+    shape = layers + (n_pages, page_size, H_kv, d_h)
+    for name, t in zip(("K_pages", "V_pages"), cache):
+        if tuple(t.shape) != shape or t.dtype != torch.float16 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous fp16 tensor of shape {shape}")
+
+
+def attention_forward_paged(x, batch, cache, Wq, Wkv, Wo, gamma_q, gamma_k, *, H, H_kv, attn_type,
+                            window, rope_base, rope_scale, query_scale, out=None, workspace=None,
+                            stream=None):
+    """One attention layer over the packed rows x [rows, D] bf16 of a paged
+    batch.  ``cache``: the layer's (K_pages, V_pages) [n_pages, page_size,
+    H_kv, d_h], which gain the new tokens.  Returns out [rows, D] bf16, 0 in
+    rows behind the last sequence."""
+    import torch
+    M, D = x.shape
+    d_h = gamma_q.shape[0]
+    if M != batch.sizes[1]:
+        raise ValueError(f"x has {M} rows, the batch {batch.sizes[1]}")
+    _check_pages(cache, (), batch, H_kv, d_h)
+    ws_bytes = gemma3_attn_paged_workspace_size(batch, D, H, H_kv, d_h)
+    with _on(stream):
+        if workspace is None:
+            workspace = _empty_ws(ws_bytes, x.device)
+        if out is None:
+            out = torch.empty((M, D), dtype=torch.bfloat16, device=x.device)
+    gemma3_attn_forward_paged(batch, D, H, H_kv, d_h, x, Wq, Wkv, Wo, gamma_q, gamma_k, attn_type,
+                              window, rope_base, rope_scale, query_scale, *cache, out, workspace,
+                              workspace.numel(), stream)
+    return out
+
+
+def commit_paged_cache(batch, cache, accepted=None, counts=None, *, new_lens=None, stream=None):
+    """After a step over a paged batch: of each sequence's new tokens those
+    numbered accepted[b, :counts[b]] (ascending; default: the first counts[b],
+    or all) become its next filled slots in every layer of ``cache`` =
+    (K_pages, V_pages) [num_layers, n_pages, page_size, H_kv, d_h].  Returns
+    the new lens [B] int32, in a tensor that is not the batch's."""
+    import torch
+    K, V = cache
+    L, _, _, H_kv, d_h = K.shape
+    B, _, T_max = batch.sizes[:3]
+    _check_pages(cache, (L,), batch, H_kv, d_h)
+    for name, t, shape in (("accepted", accepted, (B, T_max)), ("counts", counts, (B,)),
+                           ("new_lens", new_lens, (B,))):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != torch.int32 or
+                              not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+    if new_lens is None:
+        with _on(stream):
+            new_lens = torch.empty(B, dtype=torch.int32, device=K.device)
+    gemma3_paged_commit(batch, accepted, counts, L, H_kv, d_h, K, V, new_lens, stream)
+    return new_lens
 
 
 def block_attention_forward(x, segment_pos, pad_lens, Wq, Wkv, Wo, gamma_q, gamma_k, gamma_pre,

@@ -21,6 +21,7 @@ GEMMA3_ERR_BAD_INPUT = -7
 GEMMA3_LOCAL_SLIDING, GEMMA3_GLOBAL = 0, 1
 GEMMA3_BF16, GEMMA3_F16, GEMMA3_F32 = 0, 1, 2
 GEMMA3_CACHE8_BLOCK = 64
+GEMMA3_TREE_MAX = 64
 MODEL_SIZES = {"270M": 0, "1B": 1, "4B": 2, "12B": 3, "27B": 4}
 
 
@@ -33,6 +34,11 @@ class gemma3_block_weights(ctypes.Structure):
     _fields_ = [(n, c_void_p) for n in (
         "Wq", "Wkv", "Wo", "gamma_q", "gamma_k", "gamma_pre_attn", "gamma_post_attn",
         "gamma_pre_ffn", "gamma_post_ffn", "W_gating", "W_down")]
+
+
+class gemma3_paged_batch(ctypes.Structure):
+    _fields_ = [(n, c_int) for n in ("B", "M", "T_max", "page_size", "n_pages", "max_pages")] + [
+        (n, c_void_p) for n in ("lens", "row_start", "parents", "page_table")]
 
 
 # name -> (restype, argtypes); mirrors include/gemma3_attn.h
@@ -109,6 +115,22 @@ SIGNATURES = {
     "gemma3_attn_forward_cached8": (c_int, [ctypes.POINTER(gemma3_attn_dims), c_int, c_int] +
                                     [c_void_p] * 8 + [c_int, c_int, c_double, c_double, c_float] +
                                     [c_void_p] * 8 + [c_size_t, c_void_p]),
+    "gemma3_paged_positions": (c_int, [ctypes.POINTER(gemma3_paged_batch), c_void_p, c_void_p]),
+    "gemma3_paged_append": (c_int, [ctypes.POINTER(gemma3_paged_batch), c_void_p, c_long, c_void_p,
+                                    c_long, c_void_p, c_void_p, c_long, c_void_p, c_void_p, c_int,
+                                    c_int, c_int, c_double, c_double, c_float, c_void_p, c_void_p,
+                                    c_void_p]),
+    "gemma3_paged_attention_workspace_size": (c_int, [ctypes.POINTER(gemma3_paged_batch), c_int,
+                                                      c_int, c_int, ctypes.POINTER(c_size_t)]),
+    "gemma3_paged_attention": (c_int, [ctypes.POINTER(gemma3_paged_batch)] + [c_void_p] * 4 +
+                               [c_int] * 5 + [c_void_p, c_size_t, c_void_p]),
+    "gemma3_paged_commit": (c_int, [ctypes.POINTER(gemma3_paged_batch), c_void_p, c_void_p, c_int,
+                                    c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "gemma3_attn_paged_workspace_size": (c_int, [ctypes.POINTER(gemma3_paged_batch)] +
+                                         [c_int] * 4 + [ctypes.POINTER(c_size_t)]),
+    "gemma3_attn_forward_paged": (c_int, [ctypes.POINTER(gemma3_paged_batch)] + [c_int] * 4 +
+                                  [c_void_p] * 6 + [c_int, c_int, c_double, c_double, c_float] +
+                                  [c_void_p] * 4 + [c_size_t, c_void_p]),
     "gemma3_geglu": (c_int, [c_void_p, c_long, c_void_p, c_long, c_void_p, c_long, c_int, c_int,
                              c_int, c_int, c_void_p]),
     "gemma3_linear": (c_int, [c_void_p, c_long, c_void_p, c_long, c_void_p, c_long, c_int, c_int,
@@ -472,6 +494,90 @@ def gemma3_attn_forward_cached8(dims, S, end_index, x, segment_pos, pad_lens, Wq
     return _check("gemma3_attn_forward_cached8", lib().gemma3_attn_forward_cached8(
         ctypes.byref(d), S, end_index, *ins, attn_type, window, rope_base, rope_scale,
         query_scale, *outs, workspace_bytes, _stream(stream)))
+
+
+class PagedBatch:
+    """A gemma3_paged_batch over device tensors, which it keeps alive: lens [B],
+    row_start [B + 1], page_table [B, max_pages] and parents [rows] or None,
+    all int32, contiguous and on one GPU.  Their contents may change between
+    calls; the sizes may not."""
+
+    def __init__(self, lens, row_start, page_table, *, rows, T_max, page_size, n_pages,
+                 parents=None):
+        import torch
+        B = lens.shape[0] if lens.dim() == 1 else -1
+        pages = page_table.shape[1] if page_table.dim() == 2 else -1
+        for name, t, shape in (("lens", lens, (B,)), ("row_start", row_start, (B + 1,)),
+                               ("page_table", page_table, (B, pages)), ("parents", parents, (rows,))):
+            if t is None and name == "parents":
+                continue
+            if tuple(t.shape) != shape or t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+        self.tensors = (lens, row_start, parents, page_table)
+        self.sizes = (B, rows, T_max, page_size, n_pages, pages)
+        self.struct = gemma3_paged_batch(*self.sizes, *(
+            None if t is None else t.data_ptr() for t in self.tensors))
+
+    def ref(self):
+        """A reference to the struct, its arrays on the current device."""
+        _here(*self.tensors)
+        return ctypes.byref(self.struct)
+
+    def sizes_ref(self):
+        return ctypes.byref(self.struct)
+
+
+def gemma3_paged_positions(batch, segment_pos, stream=None):
+    pos, = _here(segment_pos)
+    return _check("gemma3_paged_positions", lib().gemma3_paged_positions(
+        batch.ref(), pos, _stream(stream)))
+
+
+def gemma3_paged_append(batch, Q, ldq, Q_out, ldqo, K, V, ldkv, gamma_q, gamma_k, H, H_kv, d_h,
+                        rope_base, rope_scale, query_scale, K_pages, V_pages, stream=None):
+    q, qo, k, v, gq, gk, kp, vp = _here(Q, Q_out, K, V, gamma_q, gamma_k, K_pages, V_pages)
+    return _check("gemma3_paged_append", lib().gemma3_paged_append(
+        batch.ref(), q, ldq, qo, ldqo, k, v, ldkv, gq, gk, H, H_kv, d_h, rope_base, rope_scale,
+        query_scale, kp, vp, _stream(stream)))
+
+
+def gemma3_paged_attention_workspace_size(batch, H, H_kv, d_h) -> int:
+    n = c_size_t()
+    _check("gemma3_paged_attention_workspace_size", lib().gemma3_paged_attention_workspace_size(
+        batch.sizes_ref(), H, H_kv, d_h, ctypes.byref(n)))
+    return n.value
+
+
+def gemma3_paged_attention(batch, Q, K_pages, V_pages, O, o_dtype, H, H_kv, d_h, window, workspace,
+                           workspace_bytes, stream=None):
+    q, kp, vp, o, ws = _here(Q, K_pages, V_pages, O, workspace)
+    return _check("gemma3_paged_attention", lib().gemma3_paged_attention(
+        batch.ref(), q, kp, vp, o, o_dtype, H, H_kv, d_h, window, ws, workspace_bytes,
+        _stream(stream)))
+
+
+def gemma3_paged_commit(batch, accepted, counts, num_layers, H_kv, d_h, K_pages, V_pages, new_lens,
+                        stream=None):
+    ac, co, kp, vp, nl = _here(accepted, counts, K_pages, V_pages, new_lens)
+    return _check("gemma3_paged_commit", lib().gemma3_paged_commit(
+        batch.ref(), ac, co, num_layers, H_kv, d_h, kp, vp, nl, _stream(stream)))
+
+
+def gemma3_attn_paged_workspace_size(batch, D, H, H_kv, d_h) -> int:
+    n = c_size_t()
+    _check("gemma3_attn_paged_workspace_size", lib().gemma3_attn_paged_workspace_size(
+        batch.sizes_ref(), D, H, H_kv, d_h, ctypes.byref(n)))
+    return n.value
+
+
+def gemma3_attn_forward_paged(batch, D, H, H_kv, d_h, x, Wq, Wkv, Wo, gamma_q, gamma_k, attn_type,
+                              window, rope_base, rope_scale, query_scale, K_pages, V_pages, out,
+                              workspace, workspace_bytes, stream=None):
+    ins = _here(x, Wq, Wkv, Wo, gamma_q, gamma_k)
+    outs = _here(K_pages, V_pages, out, workspace)
+    return _check("gemma3_attn_forward_paged", lib().gemma3_attn_forward_paged(
+        batch.ref(), D, H, H_kv, d_h, *ins, attn_type, window, rope_base, rope_scale, query_scale,
+        *outs, workspace_bytes, _stream(stream)))
 
 
 def gemma3_geglu(A, lda, W_gating, ldw, Z, ldz, M, D_ff, K, in_dtype, stream=None):

@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "libgemma3attn.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cu", "gemm.cu", "attention.cu", "attention_pair.cu", "elementwise.cu", "decode.cu", "skinny_gemm.cu",
-           "cache8.cu", "cache8_attn.cu", "cache8_flash.cu", "cache8_weights.cu"]
+           "cache8.cu", "cache8_attn.cu", "cache8_flash.cu", "cache8_weights.cu",
+           "paged.cu", "paged_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "--expt-relaxed-constexpr", "-I", INCLUDE]

@@ -1007,6 +1007,266 @@ int gemma3_attn_forward_cached8(const gemma3_attn_dims* dims, int S, int end_ind
   return to_status(launch_linear(obuf, HD, Wo, HD, out, d->D, M, d->D, HD, kBF16, kBF16, s, st, 0));
 }
 
+// ------------------------------------------------------------ paged KV cache
+
+namespace {
+
+int validate_heads(int H, int H_kv, int d_h) {
+  if (H < 1 || H_kv < 1 || H % H_kv != 0) return GEMMA3_ERR_INVALID_ARG;
+  const int G = H / H_kv;
+  if ((d_h != 128 && d_h != 256) || (G != 1 && G != 2 && G != 4)) return GEMMA3_ERR_UNSUPPORTED;
+  if (static_cast<long long>(H) * d_h > (1 << 20)) return GEMMA3_ERR_INVALID_ARG;
+  return GEMMA3_OK;
+}
+
+// Sizes of a paged batch (its arrays: validate_paged).
+int validate_paged_sizes(const gemma3_paged_batch* b) {
+  if (b == nullptr || b->B < 1 || b->B > 65535 || b->M < 1 || b->M > (1 << 30) || b->T_max < 1)
+    return GEMMA3_ERR_INVALID_ARG;
+  if (b->page_size < 16 || b->page_size > 256 || (b->page_size & (b->page_size - 1)) != 0)
+    return GEMMA3_ERR_UNSUPPORTED;
+  // slots of a sequence and of the pool are 32-bit numbers
+  if (b->n_pages < 1 || static_cast<long long>(b->n_pages) * b->page_size > (1LL << 31) - 1024 ||
+      b->max_pages < 1 || static_cast<long long>(b->max_pages) * b->page_size > (1 << 30))
+    return GEMMA3_ERR_INVALID_ARG;
+  if (b->parents != nullptr && b->T_max > GEMMA3_TREE_MAX) return GEMMA3_ERR_UNSUPPORTED;
+  return GEMMA3_OK;
+}
+
+int validate_paged(const gemma3_paged_batch* b) {
+  const int rc = validate_paged_sizes(b);
+  if (rc != GEMMA3_OK) return rc;
+  if (!b->lens || !b->row_start || !b->page_table) return GEMMA3_ERR_INVALID_ARG;
+  if (!aligned4(b->lens) || !aligned4(b->row_start) || !aligned4(b->parents) || !aligned4(b->page_table))
+    return GEMMA3_ERR_MISALIGNED;
+  return GEMMA3_OK;
+}
+
+int validate_pools(const void* K_pages, const void* V_pages) {
+  if (!K_pages || !V_pages) return GEMMA3_ERR_INVALID_ARG;
+  return aligned16(K_pages) && aligned16(V_pages) ? GEMMA3_OK : GEMMA3_ERR_MISALIGNED;
+}
+
+PagedBatch as_batch(const gemma3_paged_batch* b) {
+  PagedBatch p;
+  p.B = b->B;
+  p.M = b->M;
+  p.T_max = b->T_max;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < b->page_size) ++p.page_shift;
+  p.n_pages = b->n_pages;
+  p.max_pages = b->max_pages;
+  p.lens = b->lens;
+  p.row_start = b->row_start;
+  p.parents = b->parents;
+  p.page_table = b->page_table;
+  return p;
+}
+
+struct PagedWs {
+  size_t q, kv, pos, attn, total;
+};
+
+PagedWs paged_ws(const gemma3_paged_batch* b, int H, int H_kv, int d_h) {
+  const size_t M = static_cast<size_t>(b->M);
+  PagedWs w;
+  w.q = round_up(M * H * d_h * 2, 256);
+  w.kv = round_up(M * 2 * H_kv * d_h * 2, 256);
+  w.pos = round_up(M * 4, 256);
+  w.attn = round_up(paged_attention_ws_bytes(b->T_max, H, H_kv, d_h), 256);
+  w.total = w.q + w.kv + w.pos + w.attn;
+  return w;
+}
+
+}  // namespace
+
+int gemma3_paged_positions(const gemma3_paged_batch* batch, int32_t* segment_pos, void* stream) {
+  int rc = validate_paged(batch);
+  if (rc != GEMMA3_OK) return rc;
+  if (segment_pos == nullptr) return GEMMA3_ERR_INVALID_ARG;
+  if (!aligned4(segment_pos)) return GEMMA3_ERR_MISALIGNED;
+  rc = check_device();
+  if (rc != GEMMA3_OK) return rc;
+  int* st = status_ptr();
+  if (st == nullptr) return GEMMA3_ERR_CUDA;
+  return to_status(launch_paged_positions(as_batch(batch), segment_pos, as_stream(stream), st));
+}
+
+int gemma3_paged_append(const gemma3_paged_batch* batch, const void* Q, long ldq, void* Q_out,
+                        long ldqo, const void* K, const void* V, long ldkv, const void* gamma_q,
+                        const void* gamma_k, int H, int H_kv, int d_h, double rope_base,
+                        double rope_scale, float query_scale, void* K_pages, void* V_pages,
+                        void* stream) {
+  int rc = validate_paged(batch);
+  if (rc != GEMMA3_OK) return rc;
+  const bool norm = gamma_k != nullptr;
+  rc = validate_heads(norm ? H : H_kv, H_kv, d_h);
+  if (rc != GEMMA3_OK) return rc;
+  if (!K || !V || (gamma_q != nullptr) != norm) return GEMMA3_ERR_INVALID_ARG;
+  if (ldkv < static_cast<long>(H_kv) * d_h) return GEMMA3_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V) || ldkv % 8 != 0) return GEMMA3_ERR_MISALIGNED;
+  if (norm) {
+    if (!Q || !Q_out || ldq < static_cast<long>(H) * d_h || ldqo < static_cast<long>(H) * d_h)
+      return GEMMA3_ERR_INVALID_ARG;
+    if (!(rope_base > 0.0) || !(rope_scale > 0.0) || !std::isfinite(rope_base) ||
+        !std::isfinite(rope_scale))
+      return GEMMA3_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned16(Q_out) || ldq % 8 != 0 || ldqo % 8 != 0 || !aligned16(gamma_q) ||
+        !aligned16(gamma_k))
+      return GEMMA3_ERR_MISALIGNED;
+    const size_t before = static_cast<size_t>(batch->M - 1), row = static_cast<size_t>(H) * d_h;
+    if ((Q != Q_out || ldq != ldqo) &&
+        overlap({Q, (before * ldq + row) * 2}, {Q_out, (before * ldqo + row) * 2}))
+      return GEMMA3_ERR_INVALID_ARG;
+  }
+  rc = validate_pools(K_pages, V_pages);
+  if (rc != GEMMA3_OK) return rc;
+  rc = check_device();
+  if (rc != GEMMA3_OK) return rc;
+  int* st = status_ptr();
+  if (st == nullptr) return GEMMA3_ERR_CUDA;
+  return to_status(launch_paged_append(as_batch(batch), Q, ldq, Q_out, ldqo, K, V, ldkv, gamma_q,
+                                       gamma_k, norm ? H : H_kv, H_kv, d_h, rope_base, rope_scale,
+                                       query_scale, K_pages, V_pages, /*zero_behind=*/false,
+                                       as_stream(stream), st, 0));
+}
+
+int gemma3_paged_attention_workspace_size(const gemma3_paged_batch* batch, int H, int H_kv, int d_h,
+                                          size_t* bytes) {
+  int rc = validate_paged_sizes(batch);
+  if (rc != GEMMA3_OK) return rc;
+  rc = validate_heads(H, H_kv, d_h);
+  if (rc != GEMMA3_OK) return rc;
+  if (bytes == nullptr) return GEMMA3_ERR_INVALID_ARG;
+  *bytes = round_up(paged_attention_ws_bytes(batch->T_max, H, H_kv, d_h), 256);
+  return GEMMA3_OK;
+}
+
+int gemma3_paged_attention(const gemma3_paged_batch* batch, const void* Q, const void* K_pages,
+                           const void* V_pages, void* O, int o_dtype, int H, int H_kv, int d_h,
+                           int window, void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  int rc = gemma3_paged_attention_workspace_size(batch, H, H_kv, d_h, &need);
+  if (rc != GEMMA3_OK) return rc;
+  rc = validate_paged(batch);
+  if (rc != GEMMA3_OK) return rc;
+  if (!Q || !O || !workspace) return GEMMA3_ERR_INVALID_ARG;
+  if (o_dtype != GEMMA3_BF16 && o_dtype != GEMMA3_F16) return GEMMA3_ERR_INVALID_ARG;
+  rc = validate_pools(K_pages, V_pages);
+  if (rc != GEMMA3_OK) return rc;
+  if (!aligned16(Q) || !aligned16(O) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return GEMMA3_ERR_MISALIGNED;
+  const size_t qn = static_cast<size_t>(batch->M) * H * d_h * 2;
+  if (Q != O && overlap({Q, qn}, {O, qn})) return GEMMA3_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return GEMMA3_ERR_WORKSPACE;
+  rc = check_device();
+  if (rc != GEMMA3_OK) return rc;
+  int* st = status_ptr();
+  if (st == nullptr) return GEMMA3_ERR_CUDA;
+  return to_status(launch_paged_attention(as_batch(batch), Q, K_pages, V_pages, O,
+                                          o_dtype == GEMMA3_F16 ? kF16 : kBF16, H, H_kv, d_h,
+                                          window > 0 ? window : 0, workspace, as_stream(stream), st));
+}
+
+int gemma3_paged_commit(const gemma3_paged_batch* batch, const int32_t* accepted,
+                        const int32_t* counts, int num_layers, int H_kv, int d_h, void* K_pages,
+                        void* V_pages, int32_t* new_lens, void* stream) {
+  int rc = validate_paged(batch);
+  if (rc != GEMMA3_OK) return rc;
+  rc = validate_heads(H_kv, H_kv, d_h);
+  if (rc != GEMMA3_OK) return rc;
+  if (num_layers < 1 || num_layers > 32767 || !new_lens) return GEMMA3_ERR_INVALID_ARG;
+  rc = validate_pools(K_pages, V_pages);
+  if (rc != GEMMA3_OK) return rc;
+  if (!aligned4(accepted) || !aligned4(counts) || !aligned4(new_lens)) return GEMMA3_ERR_MISALIGNED;
+  const size_t n = static_cast<size_t>(batch->B) * 4;
+  if (overlap({new_lens, n}, {batch->lens, n}) || overlap({new_lens, n}, {batch->row_start, n + 4}) ||
+      overlap({new_lens, n}, {batch->page_table, n * batch->max_pages}) ||
+      (accepted != nullptr && overlap({new_lens, n}, {accepted, n * batch->T_max})) ||
+      (counts != nullptr && overlap({new_lens, n}, {counts, n})))
+    return GEMMA3_ERR_INVALID_ARG;
+  rc = check_device();
+  if (rc != GEMMA3_OK) return rc;
+  int* st = status_ptr();
+  if (st == nullptr) return GEMMA3_ERR_CUDA;
+  return to_status(launch_paged_commit(as_batch(batch), accepted, counts, num_layers, H_kv, d_h,
+                                       K_pages, V_pages, new_lens, as_stream(stream), st));
+}
+
+int gemma3_attn_paged_workspace_size(const gemma3_paged_batch* batch, int D, int H, int H_kv,
+                                     int d_h, size_t* bytes) {
+  int rc = validate_paged_sizes(batch);
+  if (rc != GEMMA3_OK) return rc;
+  const gemma3_attn_dims dims = {1, batch->M, D, H, H_kv, d_h};
+  rc = validate_dims(&dims);
+  if (rc != GEMMA3_OK) return rc;
+  if (bytes == nullptr) return GEMMA3_ERR_INVALID_ARG;
+  *bytes = paged_ws(batch, H, H_kv, d_h).total;
+  return GEMMA3_OK;
+}
+
+int gemma3_attn_forward_paged(const gemma3_paged_batch* batch, int D, int H, int H_kv, int d_h,
+                              const void* x, const void* Wq, const void* Wkv, const void* Wo,
+                              const void* gamma_q, const void* gamma_k, int attn_type, int window,
+                              double rope_base, double rope_scale, float query_scale,
+                              void* K_pages, void* V_pages, void* out, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  int rc = validate_paged(batch);
+  if (rc != GEMMA3_OK) return rc;
+  const int M = batch->M;
+  const gemma3_attn_dims dims = {1, M, D, H, H_kv, d_h};
+  rc = validate_pools(K_pages, V_pages);
+  if (rc != GEMMA3_OK) return rc;
+  if (out == nullptr) return GEMMA3_ERR_INVALID_ARG;
+  if (!aligned16(out)) return GEMMA3_ERR_MISALIGNED;
+  rc = validate_layer_args(&dims, x, batch->lens, Wq, Wkv, Wo, gamma_q, gamma_k, attn_type, window,
+                           rope_base, rope_scale, workspace);
+  if (rc != GEMMA3_OK) return rc;
+  const PagedWs w = paged_ws(batch, H, H_kv, d_h);
+  if (workspace_bytes < w.total) return GEMMA3_ERR_WORKSPACE;
+  int* st = status_ptr();
+  if (st == nullptr) return GEMMA3_ERR_CUDA;
+  const int HD = H * d_h, KVD = H_kv * d_h;
+  uint8_t* qbuf = static_cast<uint8_t*>(workspace);      // Q, then Q', then O [M, H*d_h]
+  uint8_t* kvbuf = qbuf + w.q;                           // [K|V] or [K'|V] fp16 [M, 2*KVD]
+  int32_t* pos = reinterpret_cast<int32_t*>(kvbuf + w.kv);
+  uint8_t* aws = kvbuf + w.kv + w.pos;
+  cudaStream_t s = as_stream(stream);
+  const PagedBatch b = as_batch(batch);
+  // Rows that the projections did not write must not reach the pages: with
+  // more than kSkinnyMaxRows rows they do not run after an error of any kind.
+  const int lost = M > kSkinnyMaxRows ? kLostAny : kLostWait;
+  cudaError_t e;
+  if (linear_qknorm_fusable(M, HD, HD, d_h) && linear_qknorm_fusable(M, 2 * KVD, KVD, d_h)) {
+    // Norm and rotation in the projections' epilogue; the append only copies.
+    e = launch_paged_positions(b, pos, s, st);
+    if (e == cudaSuccess)
+      e = launch_qkv_qknorm(x, D, Wq, Wkv, D, qbuf, HD, kvbuf, 2 * KVD, M, HD, KVD, D, kBF16, gamma_q,
+                            gamma_k, pos, d_h, rope_base, rope_scale, query_scale, s, st);
+    if (e == cudaSuccess)
+      e = launch_paged_append(b, nullptr, 0, qbuf, HD, kvbuf, kvbuf + KVD * 2, 2 * KVD, nullptr, nullptr,
+                              H, H_kv, d_h, 0, 0, 0.f, K_pages, V_pages, /*zero_behind=*/true, s, st, lost);
+  } else {
+    if (M <= kSkinnyMaxRows) {
+      e = launch_linear_skinny2(x, D, Wq, D, qbuf, HD, HD, Wkv, D, kvbuf, 2 * KVD, 2 * KVD, M, D, kBF16,
+                                kF16, s, st);
+    } else {
+      e = launch_linear(x, D, Wq, D, qbuf, HD, M, HD, D, kBF16, kF16, s, st, 0);
+      if (e == cudaSuccess)
+        e = launch_linear(x, D, Wkv, D, kvbuf, 2 * KVD, M, 2 * KVD, D, kBF16, kF16, s, st, 0);
+    }
+    if (e == cudaSuccess)
+      e = launch_paged_append(b, qbuf, HD, qbuf, HD, kvbuf, kvbuf + KVD * 2, 2 * KVD, gamma_q, gamma_k, H,
+                              H_kv, d_h, rope_base, rope_scale, query_scale, K_pages, V_pages,
+                              /*zero_behind=*/true, s, st, lost);
+  }
+  if (e != cudaSuccess ||
+      launch_paged_attention(b, qbuf, K_pages, V_pages, qbuf, kBF16, H, H_kv, d_h,
+                             attn_type == GEMMA3_LOCAL_SLIDING ? window : 0, aws, s, st) != cudaSuccess)
+    return GEMMA3_ERR_CUDA;
+  return to_status(launch_linear(qbuf, HD, Wo, HD, out, D, M, D, HD, kBF16, kBF16, s, st, 0));
+}
+
 int gemma3_geglu(const void* A, long lda, const void* W_gating, long ldw, void* Z, long ldz,
                  int M, int D_ff, int K, int in_dtype, void* stream) {
   if (!A || !W_gating || !Z || M < 0 || D_ff < 1 || K < 1) return GEMMA3_ERR_INVALID_ARG;

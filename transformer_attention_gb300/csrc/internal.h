@@ -234,6 +234,46 @@ struct CachedAttnLayout {
 CachedAttnLayout cached_attention_layout(void* ws, int B, int T, int S, int H, int H_kv, int d_h);
 int cached_span_chunks(int T, int end);
 
+// ------------------------------------------------------------ paged KV cache
+// The sizes and device arrays of a paged batch (paged.cuh).
+struct PagedBatch {
+  int B, M, T_max;                      // sequences, packed rows, most new tokens of a sequence
+  int page_shift, n_pages, max_pages;   // log2 of the slots per page
+  const int32_t* lens;                  // [B]
+  const int32_t* row_start;             // [B + 1]
+  const int32_t* parents;               // [M] or null
+  const int32_t* page_table;            // [B, max_pages]
+};
+
+// pos[m] = lens[b] + depth of row m; 0 behind the last sequence.
+cudaError_t launch_paged_positions(const PagedBatch& batch, int32_t* pos, cudaStream_t stream,
+                                   int* status);
+
+// Q_out = the query rows and K pages = the key rows after RMSNorm, (1 +
+// gamma), RoPE (Q also times query_scale), or as they are without gammas
+// (Q and Q_out may be null then); V pages = the value rows.  zero_behind: the
+// rows of Q_out behind the last sequence become zeros, else they are left.
+// Writes nothing once an error of the mask `lost` was recorded.
+cudaError_t launch_paged_append(const PagedBatch& batch, const void* Q, long ldq, void* Q_out,
+                                long ldqo, const void* K, const void* V, long ldkv,
+                                const void* gamma_q, const void* gamma_k, int H, int H_kv, int d_h,
+                                double rope_base, double rope_scale, float query_scale,
+                                void* K_pages, void* V_pages, bool zero_behind,
+                                cudaStream_t stream, int* status, int lost);
+
+// Attention of a batch's new tokens over their pages; window 0: none.
+size_t paged_attention_ws_bytes(int T_max, int H, int H_kv, int d_h);
+cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const void* K_pages,
+                                   const void* V_pages, void* O, int o_dtype, int H, int H_kv,
+                                   int d_h, int window, void* ws, cudaStream_t stream, int* status);
+
+// Moves the accepted tokens of every sequence to the slots from lens[b] on, in
+// `layers` consecutive pools; new_lens[b] = lens[b] + count.
+cudaError_t launch_paged_commit(const PagedBatch& batch, const int32_t* accepted,
+                                const int32_t* counts, int layers, int H_kv, int d_h,
+                                void* K_pages, void* V_pages, int32_t* new_lens,
+                                cudaStream_t stream, int* status);
+
 // ------------------------------------------------------------ 8-bit KV cache
 // Caches K8 / V8 [B, S, H_kv, d_h] of e4m3 bytes with scales [B, c8_blocks(S),
 // H_kv] fp32 and positions pos_cache [B, S] (cache8.cuh).

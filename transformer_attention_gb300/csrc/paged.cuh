@@ -1,0 +1,171 @@
+// The paged KV cache: what its kernels share.
+//
+// A layer's cache is a pool of pages, K_pages and V_pages [n_pages, P, H_kv,
+// d_h] fp16, P a power of two.  Slot s of sequence b is row (s mod P) of page
+// page_table[b, s / P]; lens[b] slots are filled, and a filled slot's position
+// is its number.  The new tokens of sequence b are the rows [row_start[b],
+// row_start[b + 1]) of packed arrays; token i goes to slot lens[b] + i.  Its
+// parent is an earlier new token of the sequence or -1 (the filled slots), and
+// its position is lens[b] + its depth; without parents each token follows the
+// one before it.
+//
+// Everything of a batch but its sizes lies on the device, where the kernels
+// check it: a sequence whose rows, length or pages do not fit counts as one
+// without new tokens, a parent that is not earlier as -1, an entry of the page
+// table outside the pool as a page that is not there, and each records
+// kDevErrBadPaged.
+#pragma once
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace g3 {
+
+constexpr int kPagedTile = 128;     // slots per tile of the attention
+constexpr int kTreeMax = 64;        // new tokens of a sequence with parents: bits of a mask
+
+struct PagedSeq {
+  int row0, n, len;
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& p, int b, int* status) {
+  PagedSeq s;
+  s.row0 = __ldcg(p.row_start + b);
+  const int r1 = __ldcg(p.row_start + b + 1);
+  s.len = __ldcg(p.lens + b);
+  s.n = r1 - s.row0;
+  const long long slots = static_cast<long long>(p.max_pages) << p.page_shift;
+  if (s.row0 < 0 || r1 < s.row0 || r1 > p.M || s.n > p.T_max || s.len < 0 ||
+      static_cast<long long>(s.len) + s.n > slots) {
+    record_error(status, kDevErrBadPaged);
+    s.row0 = s.n = s.len = 0;
+  }
+  return s;
+}
+
+// Row of the pool that holds slot s of sequence b, or -1.
+__device__ __forceinline__ int paged_row(const PagedBatch& p, int b, int s, int* status) {
+  const int page = __ldcg(p.page_table + static_cast<size_t>(b) * p.max_pages + (s >> p.page_shift));
+  if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) {
+    record_error(status, kDevErrBadPaged);
+    return -1;
+  }
+  return (page << p.page_shift) + (s & ((1 << p.page_shift) - 1));
+}
+
+// The sequence whose rows hold row m (whole warp; -1: behind the last one).
+__device__ __forceinline__ int paged_find(const PagedBatch& p, int m, int lane) {
+  int b = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const bool before = b0 + lane < p.B && __ldcg(p.row_start + b0 + lane + 1) <= m;
+    b += __popc(__ballot_sync(0xffffffffu, before));
+  }
+  return b < p.B ? b : -1;
+}
+
+// The trees of a warp: lane l holds tokens l and 32 + l of one sequence.
+struct Ancestors {
+  uint32_t lo[2], hi[2];   // ancestors and the token itself, a bit each
+  int parent[2];
+
+  // Bits of token t (the same or another for every lane).
+  __device__ __forceinline__ uint64_t of(int t) const {
+    const uint32_t a = __shfl_sync(0xffffffffu, lo[0], t & 31), b = __shfl_sync(0xffffffffu, hi[0], t & 31);
+    const uint32_t c = __shfl_sync(0xffffffffu, lo[1], t & 31), d = __shfl_sync(0xffffffffu, hi[1], t & 31);
+    const uint32_t l = t & 32 ? c : a, h = t & 32 ? d : b;
+    return static_cast<uint64_t>(h) << 32 | l;
+  }
+  __device__ __forceinline__ int parent_of(int t) const {
+    const int a = __shfl_sync(0xffffffffu, parent[0], t & 31), b = __shfl_sync(0xffffffffu, parent[1], t & 31);
+    return t & 32 ? b : a;
+  }
+};
+
+// Ancestors of every new token of a sequence (whole warp), by pointer
+// doubling: after round k a token has those up to 2^k steps away.
+__device__ __forceinline__ Ancestors paged_ancestors(const PagedBatch& p, const PagedSeq& s, int lane,
+                                                     int* status) {
+  Ancestors a;
+  int ptr[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int i = lane + 32 * u;
+    int q = i < s.n ? __ldcg(p.parents + s.row0 + i) : -1;
+    if (q < -1 || q >= i) {
+      if (i < s.n) record_error(status, kDevErrBadPaged);
+      q = -1;
+    }
+    a.parent[u] = ptr[u] = q;
+    a.lo[u] = u == 0 ? 1u << lane : 0u;
+    a.hi[u] = u == 0 ? 0u : 1u << lane;
+  }
+  while (__any_sync(0xffffffffu, ptr[0] >= 0 || ptr[1] >= 0)) {
+    uint64_t up[2];
+    int next[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int q = max(ptr[u], 0);
+      const uint64_t m = a.of(q);
+      const int n0 = __shfl_sync(0xffffffffu, ptr[0], q & 31), n1 = __shfl_sync(0xffffffffu, ptr[1], q & 31);
+      up[u] = ptr[u] >= 0 ? m : 0;
+      next[u] = ptr[u] >= 0 ? (q & 32 ? n1 : n0) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      a.lo[u] |= static_cast<uint32_t>(up[u]);
+      a.hi[u] |= static_cast<uint32_t>(up[u] >> 32);
+      ptr[u] = next[u];
+    }
+  }
+  return a;
+}
+
+// ---------------------------------------------------------------- work units
+// A unit of the attention is a kv head of one sequence and `tq` of its new
+// tokens; its work are the 128-slot tiles from the first slot that one of
+// these tokens may see to the last.  window 0: none.  tq is 32, 64, 128 or 256.
+struct PagedUnit {
+  int lo, hi, tile0, tiles;   // visible slots [lo, hi), tiles [tile0, tile0 + tiles)
+};
+
+__host__ __device__ inline PagedUnit paged_unit(int len, int n, int window, bool tree, int tq, int q) {
+  PagedUnit u;
+  const int from = len + (tree ? 0 : q * tq) - window + 1;   // (a tree's tokens may have any depth)
+  const int end = (q + 1) * tq;
+  u.lo = window > 0 && from > 0 ? from : 0;
+  u.hi = len + (end < n ? end : n);
+  u.tile0 = u.lo / kPagedTile;
+  u.tiles = (u.hi + kPagedTile - 1) / kPagedTile - u.tile0;
+  return u;
+}
+
+// sum over i < N of floor((x + i tq) / 128), x >= 0
+__host__ __device__ inline long long paged_floor_sum(long long x, long long N, int tq) {
+  if (tq > kPagedTile) return N * (x / kPagedTile) + (tq / kPagedTile) * (N * (N - 1) / 2);
+  const long long k = kPagedTile / tq, c = x / tq;
+  const long long d1 = (c + N) / k, r1 = (c + N) % k, d0 = c / k, r0 = c % k;
+  return k * (d1 * (d1 - 1) / 2) + d1 * r1 - k * (d0 * (d0 - 1) / 2) - d0 * r0;
+}
+
+// Tiles of the first q units (of one kv head) of a sequence.
+__host__ __device__ inline long long paged_prefix(int len, int n, int window, bool tree, int tq, int q) {
+  if (q <= 0 || n <= 0) return 0;
+  const int nq = (n + tq - 1) / tq;
+  // last tiles, as if every unit were full
+  long long sum = paged_floor_sum(static_cast<long long>(len) + tq + kPagedTile - 1, q, tq);
+  if (q >= nq)   // the last unit ends at n
+    sum += (static_cast<long long>(len) + n + kPagedTile - 1) / kPagedTile -
+           (static_cast<long long>(len) + static_cast<long long>(nq) * tq + kPagedTile - 1) / kPagedTile;
+  if (window > 0) {
+    const long long from = static_cast<long long>(len) - window + 1;
+    if (tree) {
+      if (from > 0) sum -= q * (from / kPagedTile);
+    } else {
+      const long long i1 = from > 0 ? 0 : -from / tq + 1;   // first unit whose lo is above 0
+      if (i1 < q) sum -= paged_floor_sum(from + i1 * tq, q - i1, tq);
+    }
+  }
+  return sum;
+}
+
+}  // namespace g3

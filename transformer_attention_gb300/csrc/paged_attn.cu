@@ -1,0 +1,939 @@
+// Attention of a batch's new tokens (steps, drafted trees, chunks) over the
+// paged KV cache (paged.cuh), on the tcgen05 tensor cores.
+//
+//   O[i, h] = sum_s p_s v_s,  p = softmax of q . k_s over the slots s that token
+//   i sees: the filled ones within its window, its ancestors and itself
+//
+// A work unit is a kv head of one sequence and up to NQ query tiles of 128 rows
+// (128 / G tokens x the G heads); a step or a tree fills a few rows of one tile.
+// Below some 280 rows per kv head the cache's bytes bound the call, above them
+// the tensor cores, so one kernel serves both: the cache streams through a
+// ring of 32 KB parts, up to 192 KB in flight per SM, and each 128-slot tile costs 1100
+// (d_h = 128) or 2200 clocks of MMA however few its rows, against 2800 or 5600
+// for its bytes at the HBM rate.
+//
+// Sequences have lengths of their own, known on the device alone: each CTA adds
+// up the tiles of all units and takes an equal share of them, cut wherever it
+// falls (a unit's parts are then added by paged_merge_kernel, always in the
+// same order).
+//
+// Warps:
+//   0      TMA of K and V: a box for each page and 64 channels
+//   1      TMEM allocation and MMA issue
+//   2      the CTA's pieces of units, published through a ring
+//   3      TMA of Q
+//   4-7    softmax of query tile 0 (one thread per row), its epilogue
+//   8-11   the same of query tile 1 (NQ = 2)
+// TMEM: NQ = 1: S of even and odd tiles at 0 and 128; NQ = 2: S of query tile e
+// at 128 e.  P (fp16 pairs) is written over the first 64 columns of its S.  O
+// from column 256.
+// Slots outside [lo, hi) of a unit are zeroed in V's tile, so that what they
+// hold (a NaN, say) cannot reach O through a zero probability.
+#include <algorithm>
+
+#include "attention_common.cuh"
+#include "paged.cuh"
+
+namespace g3 {
+
+namespace {
+
+using attn::ex2;
+
+constexpr int BM = 128, BN = kPagedTile;
+constexpr uint32_t CHUNK = 128 * 128;       // 128 rows x 64 channels (128 B), swizzled
+constexpr uint32_t PART = 32768;
+constexpr uint32_t O_COL = 256;
+constexpr float LOG2E = 1.4426950408889634f;
+// A row's reference stays P_SHIFT below a past maximum while the present one
+// is less than RESCALE_THRESHOLD above that (log2 units): the probabilities
+// that are rounded to fp16 reach 2^15, so that those below its normal range, off
+// by 2^-25, are off by 2^-32 at most of the row's largest.
+constexpr float RESCALE_THRESHOLD = 8.0f, P_SHIFT = 7.0f;
+constexpr int kMaxCtas = 256;               // CTAs of a launch at most (workspace)
+constexpr int NPC = 4;                      // ring of pieces
+
+enum : int {
+  kSiteQFull = 100, kSiteQEmpty, kSitePartFull, kSitePartEmpty, kSiteSFull, kSitePFull, kSitePvDone,
+  kSiteOFinal, kSiteOFree, kSitePieceFull, kSitePieceEmpty
+};
+
+// A CTA's piece of a unit.  tiles 0: no more pieces.
+struct alignas(16) Piece {
+  int b, j, row0, ntok;     // packed row of the unit's first token, its tokens
+  int i0, n, len, lo;       // number of that token, the sequence's new tokens and length; visible slots
+  int hi, tile0, tiles, ends;   // ends: bit 0: the unit's first tile is in it, bit 1: its last
+};
+
+// The unit that starts in a CTA and ends in a later one (parts 0: none).
+struct alignas(16) Split {
+  int row0, ntok, j, parts;
+};
+
+struct Shared {
+  uint64_t q_full, q_empty, part_full[8], part_empty[8], s_full[2], p_full[2], pv_done[2],
+      o_final[2], o_free[2], piece_full[NPC], piece_empty[NPC], drain;
+  Piece piece[NPC];
+  long long warp_sum[12];
+  long long start_off;
+  int start_b;
+  uint32_t tmem;
+  int abort_flag;
+};
+
+template <int DH, int NQ_>
+struct Cfg {
+  static constexpr int NQ = NQ_;
+  static_assert(NQ == 1 || DH == 128, "TMEM columns");
+  static constexpr int NCH = DH / 64;
+  static constexpr int PARTS = DH / 128;          // parts of a K or V tile
+  static constexpr uint32_t QT_BYTES = BM * DH * 2;
+  static constexpr int NP = (7 * PART - NQ * QT_BYTES) / PART;   // ring: what Q leaves of 224 KB
+  static constexpr uint32_t SMEM = NQ * QT_BYTES + NP * PART + sizeof(Shared);
+  static_assert(SMEM <= 232448 && NP <= 8, "shared memory budget");
+  static constexpr int THREADS = 128 * (1 + NQ);
+  // two softmax warpgroups: the control warps give them registers
+  static constexpr int REGS_LAUNCH = 168, REGS_CTRL = 96, REGS_SOFT = 200;
+  static_assert(128 * REGS_CTRL + 256 * REGS_SOFT <= 384 * REGS_LAUNCH, "register split");
+};
+
+struct Params {
+  PagedBatch batch;
+  float2* pstat;          // [2 grid, rows] (reference, sum)
+  float* part;            // [2 grid, rows, DH] unnormalised
+  Split* split;           // [grid]
+  void* O;
+  int o_f16, H, H_kv, gshift, window, tq, tokbox, rows;
+  int* status;
+};
+
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  template <int N>
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// exp2(s log2 e - m) of 32 columns: packed fp16 pairs to p[0..15], sums to acc.
+__device__ __forceinline__ void exp_pack(const uint32_t (&s)[32], uint32_t* p, float2 (&acc)[4],
+                                         float2 l2e, float2 negm) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float2 x = __ffma2_rn(
+        make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), l2e, negm);
+    const float2 e = make_float2(ex2(x.x), ex2(x.y));
+    acc[k & 3] = __fadd2_rn(acc[k & 3], e);
+    p[k] = pack_half2(e.x, e.y);
+  }
+}
+
+__device__ __forceinline__ float mask_max(uint32_t (&r)[32], uint32_t keep) {
+  float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    if (!((keep >> c) & 1u)) r[c] = 0xff800000u;
+    if (!((keep >> (c + 1)) & 1u)) r[c + 1] = 0xff800000u;
+    a = fmaxf(a, __uint_as_float(r[c]));
+    b = fmaxf(b, __uint_as_float(r[c + 1]));
+  }
+  return fmaxf(a, b);
+}
+
+// Bits [a, z] of 32, for any a and z.
+__device__ __forceinline__ uint32_t bits_from_to(int a, int z) {
+  const uint32_t from = a <= 0 ? 0xffffffffu : (a >= 32 ? 0u : 0xffffffffu << a);
+  return from & (z < 0 ? 0u : (z >= 31 ? 0xffffffffu : (2u << z) - 1u));
+}
+
+// Bits [d, d + 32) of a mask, for any d.
+__device__ __forceinline__ uint32_t bits_at(uint64_t m, int d) {
+  if (d >= 0) return d < 64 ? static_cast<uint32_t>(m >> d) : 0u;
+  return d > -32 ? static_cast<uint32_t>(m << -d) : 0u;
+}
+
+template <int DH, int NQ>
+__global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const Params p) {
+  pdl_enter();
+  using C = Cfg<DH, NQ>;
+  const bool lost = lost_work(p.status, kLostWait);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const PagedBatch& batch = p.batch;
+  const bool tree = batch.parents != nullptr;
+
+  // (the swizzled tiles need 1024-byte alignment; there is no other shared memory)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem;
+  uint8_t* sP = smem + C::NQ * C::QT_BYTES;   // ring of parts
+  Shared& sh = *reinterpret_cast<Shared*>(sP + C::NP * PART);
+  if ((smem_u32(smem) & 1023u) != 0) {        // (never, by the declaration above)
+    if (tid == 0) record_error(p.status, kDevErrTimeoutBase + kSiteQFull);
+    return;
+  }
+
+  if (tid == 0) {
+    mbar_init(smem_u32(&sh.q_full), 1);
+    mbar_init(smem_u32(&sh.q_empty), 1);
+    for (int s = 0; s < C::NP; ++s) {
+      mbar_init(smem_u32(&sh.part_full[s]), 1);
+      mbar_init(smem_u32(&sh.part_empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sh.s_full[s]), 1);
+      mbar_init(smem_u32(&sh.p_full[s]), 4);
+      mbar_init(smem_u32(&sh.pv_done[s]), 1);
+      mbar_init(smem_u32(&sh.o_final[s]), 1);
+      mbar_init(smem_u32(&sh.o_free[s]), 4);
+    }
+    for (int s = 0; s < NPC; ++s) {
+      mbar_init(smem_u32(&sh.piece_full[s]), 1);
+      mbar_init(smem_u32(&sh.piece_empty[s]), 3 + 4 * C::NQ);   // K/V, MMA, Q, softmax warps
+    }
+    mbar_init(smem_u32(&sh.drain), 1);
+    sh.abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh.tmem), 512);
+    tmem_relinquish();
+  }
+
+  // ---------------- this CTA's share of all tiles
+  const int per = (batch.B + C::THREADS - 1) / C::THREADS;   // sequences per thread
+  auto seq_tiles = [&](const PagedSeq& s) -> long long {
+    return p.H_kv * paged_prefix(s.len, s.n, p.window, tree, p.tq, (s.n + p.tq - 1) / p.tq);
+  };
+  long long mine = 0;
+  for (int k = 0; k < per; ++k) {
+    const int b = tid * per + k;
+    if (b < batch.B) mine += seq_tiles(paged_seq(batch, b, p.status));
+  }
+  long long upto = mine;   // through this thread
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) sh.warp_sum[warp] = upto;
+  const bool stop = __syncthreads_or(lost);
+  tc_fence_after();
+  const uint32_t tbase = sh.tmem;
+  if (stop) {
+    if (warp == 1) tmem_dealloc(tbase, 512);
+    return;
+  }
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < C::THREADS / 32; ++w) {
+    if (w < warp) upto += sh.warp_sum[w];
+    total += sh.warp_sum[w];
+  }
+  // (no more CTAs than tiles: a unit's parts lie in consecutive ones)
+  const long long ctas = min(static_cast<long long>(gridDim.x), total);
+  const bool idle = static_cast<long long>(blockIdx.x) >= ctas;
+  const long long from = idle ? 0 : total * blockIdx.x / ctas;
+  const long long count = idle ? 0 : total * (blockIdx.x + 1) / ctas - from;
+  if (!idle && from < upto && from >= upto - mine) {
+    long long off = from - (upto - mine);
+    int b = tid * per;
+    while (true) {
+      const long long n = seq_tiles(paged_seq(batch, b, p.status));
+      if (off < n || b + 1 >= batch.B) break;
+      off -= n;
+      ++b;
+    }
+    sh.start_b = b;
+    sh.start_off = off;
+  }
+  __syncthreads();
+
+  auto wait_warp = [&](uint64_t& bar, uint32_t parity, int site) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, &sh.abort_flag, p.status, site));
+  };
+  // The next piece (whole warp); false at the end.
+  auto take = [&](int k, Piece& pc) -> bool {
+    if (!wait_warp(sh.piece_full[k % NPC], (k / NPC) & 1, kSitePieceFull)) return false;
+    pc = sh.piece[k % NPC];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.piece_empty[k % NPC]));
+    return pc.tiles > 0;
+  };
+
+  if (warp < 4) {
+    if constexpr (NQ == 2) regs_decrease<C::REGS_CTRL>();
+    if (warp == 2) {
+      // ---------------- pieces
+      Split split = {0, 0, 0, 0};
+      long long left = count, pos = from, off = idle ? 0 : sh.start_off;
+      int b = idle ? 0 : sh.start_b, k = 0, b0 = 0;
+      PagedSeq win = {0, 0, 0};   // of sequence b0 + lane
+      bool ok = true, have = false;
+      auto publish = [&](const Piece& pc) {
+        ok = k < NPC || wait_warp(sh.piece_empty[k % NPC], ((k / NPC) & 1) ^ 1, kSitePieceEmpty);
+        if (!ok) return;
+        if (lane == 0) {
+          sh.piece[k % NPC] = pc;
+          mbar_arrive(smem_u32(&sh.piece_full[k % NPC]));
+        }
+        ++k;
+      };
+      while (ok && left > 0 && b < batch.B) {
+        if (!have || b >= b0 + 32) {
+          b0 = b;
+          win = b0 + lane < batch.B ? paged_seq(batch, b0 + lane, p.status) : PagedSeq{0, 0, 0};
+          have = true;
+        }
+        PagedSeq s;
+        s.row0 = __shfl_sync(0xffffffffu, win.row0, b - b0);
+        s.n = __shfl_sync(0xffffffffu, win.n, b - b0);
+        s.len = __shfl_sync(0xffffffffu, win.len, b - b0);
+        const int nq = (s.n + p.tq - 1) / p.tq;
+        const long long head = paged_prefix(s.len, s.n, p.window, tree, p.tq, nq);
+        if (head == 0 || off >= head * p.H_kv) {
+          off = 0;
+          ++b;
+          continue;
+        }
+        int j = static_cast<int>(off / head), q = 0;
+        long long t = off - j * head;
+        if (nq > 1) {   // the unit of tile t: the last one that starts at or before it
+          int q1 = nq;
+          while (q1 - q > 1) {
+            const int mid = (q + q1) / 2;
+            if (paged_prefix(s.len, s.n, p.window, tree, p.tq, mid) <= t) q = mid;
+            else q1 = mid;
+          }
+          t -= paged_prefix(s.len, s.n, p.window, tree, p.tq, q);
+        }
+        while (ok && left > 0 && j < p.H_kv) {
+          const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.tq, q);
+          const int n = static_cast<int>(min(left, static_cast<long long>(u.tiles) - t));
+          Piece pc;
+          pc.b = b;
+          pc.j = j;
+          pc.i0 = q * p.tq;
+          pc.row0 = s.row0 + pc.i0;
+          pc.ntok = min(p.tq, s.n - pc.i0);
+          pc.n = s.n;
+          pc.len = s.len;
+          pc.lo = u.lo;
+          pc.hi = u.hi;
+          pc.tile0 = u.tile0 + static_cast<int>(t);
+          pc.tiles = n;
+          pc.ends = (t == 0 ? 1 : 0) | (t + n == u.tiles ? 2 : 0);
+          if (pc.ends == 1) {   // (pos is the unit's first tile)
+            const long long last = (((pos + u.tiles - 1) + 1) * ctas - 1) / total;
+            split = {pc.row0, pc.ntok, j, static_cast<int>(last) - static_cast<int>(blockIdx.x) + 1};
+          }
+          publish(pc);
+          left -= n;
+          pos += n;
+          t = 0;
+          if (++q == nq) {
+            q = 0;
+            ++j;
+          }
+        }
+        off = 0;
+        ++b;
+      }
+      if (lane == 0) p.split[blockIdx.x] = split;
+      if (ok) publish(Piece{});
+    } else if (warp == 0) {
+      // ---------------- K and V: K of a tile, then V of the tile before
+      const int ps = batch.page_shift, box = min(1 << ps, 64);   // slots per box
+      const int nbox = 256 / box;                                // boxes of a part
+      const int pool = batch.n_pages << ps;
+      Ring w;
+      int issued = 0;
+      // tile `tile` of a piece: lane k's `base` is the pool row of its page k
+      auto load_part = [&](bool v, int part, int j, int tile, int base) -> bool {
+        if (issued >= C::NP && !wait_warp(sh.part_empty[w.slot], w.phase ^ 1, kSitePartEmpty))
+          return false;
+        const uint32_t bar = smem_u32(&sh.part_full[w.slot]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, PART);
+        __syncwarp();
+        // the part's rows and 64-channel chunks: K (and V of d_h = 128) 128
+        // slots x 2 chunks, V of d_h = 256 64 slots x 4 chunks
+        const bool half = C::PARTS == 2 && v;
+        const int rows = half ? 64 : 128, per_chunk = rows / box;
+        const int ch = lane / per_chunk, r = lane % per_chunk * box;
+        const int so = r + (half ? part * 64 : 0);               // slot of the tile
+        const int page = ps < 7 ? so >> ps : 0;
+        const int row0 = __shfl_sync(0xffffffffu, base, page);
+        if (lane < nbox) {
+          const int row = row0 < 0 ? pool : row0 + ((tile * BN + so) & ((1 << ps) - 1));
+          const int c = (half || C::PARTS == 1 ? ch : part * 2 + ch) * 64;
+          tma_load_3d(smem_u32(sP + w.slot * PART + ch * rows * 128 + r * 128), v ? &tmV : &tmK, bar, c, j,
+                      row);
+        }
+        w.next<C::NP>();
+        ++issued;
+        return true;
+      };
+      bool ok = true;
+      int pj = 0, ptile = -1, pbase = 0;   // the tile whose V is still to come
+      Piece pc;
+      for (int k = 0; ok && take(k, pc); ++k) {
+        // page ids of the piece, 32 at a time: lane l holds entry first + l
+        const int32_t* table = batch.page_table + static_cast<size_t>(pc.b) * batch.max_pages;
+        const int p_end = ((pc.hi - 1) >> ps) + 1;               // pages that hold visible slots
+        auto entries = [&](int first) -> int {
+          const int at = first + lane;
+          if (at >= p_end) return -1;
+          const int id = __ldcg(table + at);
+          if (static_cast<unsigned>(id) >= static_cast<unsigned>(batch.n_pages)) {
+            record_error(p.status, kDevErrBadPaged);
+            return -1;
+          }
+          return id << ps;
+        };
+        int first = (pc.tile0 * BN) >> ps;
+        int cur = entries(first), ahead = entries(first + 32);
+        for (int i = 0; i < pc.tiles; ++i) {
+          const int tile = pc.tile0 + i, at = (tile * BN) >> ps;
+          if (at >= first + 32) {
+            first += 32;
+            cur = ahead;
+            ahead = entries(first + 32);
+          }
+          const int base = __shfl_sync(0xffffffffu, cur, (at - first + (lane & 7)) & 31);
+          for (int part = 0; ok && part < C::PARTS; ++part) ok = load_part(false, part, pc.j, tile, base);
+          for (int part = 0; ok && ptile >= 0 && part < C::PARTS; ++part)
+            ok = load_part(true, part, pj, ptile, pbase);
+          if (!ok) break;
+          pj = pc.j;
+          ptile = tile;
+          pbase = base;
+        }
+      }
+      for (int part = 0; ok && ptile >= 0 && part < C::PARTS; ++part)
+        ok = load_part(true, part, pj, ptile, pbase);
+      // Every issued load lands before the CTA may exit.
+      for (int n = max(0, issued - C::NP); n < issued; ++n)
+        mbar_wait_drain(smem_u32(&sh.part_full[n % C::NP]), (n / C::NP) & 1);
+    } else if (warp == 3) {
+      // ---------------- Q
+      int nload = 0;
+      Piece pc;
+      for (int k = 0; take(k, pc); ++k) {
+        if (nload > 0 && !wait_warp(sh.q_empty, (nload - 1) & 1, kSiteQEmpty)) break;
+        if (lane == 0) {
+          const int tq1 = BM >> p.gshift, nq = NQ == 2 && pc.ntok > tq1 ? 2 : 1;
+          const uint32_t bar = smem_u32(&sh.q_full);
+          mbar_arrive_expect_tx(bar, nq * C::NCH * ((p.tokbox * 128) << p.gshift));
+          for (int e = 0; e < nq; ++e)
+            for (int ch = 0; ch < C::NCH; ++ch)
+              tma_load_3d(smem_u32(sQ + e * C::QT_BYTES + ch * CHUNK), &tmQ, bar, ch * 64,
+                          pc.j << p.gshift, pc.row0 + e * tq1);
+        }
+        ++nload;
+      }
+      if (nload > 0) mbar_wait_drain(smem_u32(&sh.q_full), (nload - 1) & 1);
+    } else {
+      // ---------------- MMA issue (whole warp, one elected lane)
+      const uint32_t lead = elect_one();
+      constexpr uint32_t idesc_qk = idesc_f16(BM, BN, /*f16*/ 0, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_f16(BM, DH, /*f16*/ 0, 0, /*B MN-major*/ 1);
+      const uint32_t q_addr = smem_u32(sQ);
+      Ring r;
+      int g = 0;              // tiles whose S was issued
+      int ge[2] = {0, 0};     // NQ = 2: the same of each query tile
+      int pieces_e[2] = {0, 0};   // pieces whose first PV was issued
+      // S of a tile; for d_h = 256 its two parts are the channel halves.
+      auto issue_s = [&](int nq, bool last) -> bool {
+        for (int part = 0; part < C::PARTS; ++part) {
+          if (!wait_warp(sh.part_full[r.slot], r.phase, kSitePartFull)) return false;
+          tc_fence_after();
+          const uint32_t kb = smem_u32(sP + r.slot * PART);
+          for (int e = 0; e < nq; ++e) {
+            const uint32_t d = tbase + (NQ == 2 ? e : (g & 1)) * 128;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t off = (k >> 2) * CHUNK + (k & 3) * 32;
+              mma_ss_lead(lead, d, sdesc_sw128(q_addr + e * C::QT_BYTES + part * 2 * CHUNK + off, 16, 1024),
+                          sdesc_sw128(kb + off, 16, 1024), idesc_qk, part > 0 || k > 0 ? 1u : 0u);
+            }
+            if (NQ == 2 && e + 1 < nq) mma_commit_lead(lead, smem_u32(&sh.s_full[e]));
+          }
+          mma_commit_lead(lead, smem_u32(&sh.part_empty[r.slot]));
+          r.next<C::NP>();
+        }
+        mma_commit_lead(lead, smem_u32(&sh.s_full[NQ == 2 ? nq - 1 : (g & 1)]));
+        if (last) mma_commit_lead(lead, smem_u32(&sh.q_empty));
+        return true;
+      };
+      struct Pv {             // what the PV of a tile needs
+        int tile, lo, hi, nq, first, last;
+      };
+      // O += P V of query tile e, from `part` of V at `vb`.
+      auto mma_pv = [&](int e, int buf, uint32_t vb, int part, int first) {
+        constexpr int STEPS = 8 / C::PARTS;   // 16-slot steps of a part
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k)
+          mma_ts_lead(lead, tbase + O_COL + e * 128, tbase + buf * 128 + (part * STEPS + k) * 8,
+                      sdesc_sw128(vb + k * 2048, CHUNK / C::PARTS, 1024), idesc_pv,
+                      !first || part > 0 || k > 0 ? 1u : 0u);
+      };
+      // V of the part in slot r, zeroed outside [lo, hi).
+      auto v_ready = [&](const Pv& t, int part) -> bool {
+        if (!wait_warp(sh.part_full[r.slot], r.phase, kSitePartFull)) return false;
+        constexpr int ROWS = 128 / C::PARTS;
+        const int s0 = t.tile * BN + part * ROWS;
+        if (s0 < t.lo || s0 + ROWS > t.hi) {
+          uint8_t* base = sP + r.slot * PART;
+          const int z = min(max(t.lo - s0, 0), ROWS), a = min(max(t.hi - s0, 0), ROWS);
+          for (int c = 0; c < static_cast<int>(PART) / (ROWS * 128); ++c) {
+            uint4* rows = reinterpret_cast<uint4*>(base + c * ROWS * 128);
+            for (int i = lane; i < z * 8; i += 32) rows[i] = make_uint4(0, 0, 0, 0);
+            for (int i = a * 8 + lane; i < ROWS * 8; i += 32) rows[i] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        tc_fence_after();
+        return true;
+      };
+      // (before a piece's first PV: the piece before was read from O)
+      auto pv_begin = [&](const Pv& t, int e) -> bool {
+        if (!t.first) return true;
+        const bool ok = pieces_e[e] == 0 || wait_warp(sh.o_free[e], (pieces_e[e] - 1) & 1, kSiteOFree);
+        ++pieces_e[e];
+        return ok;
+      };
+      // NQ = 1: the PV of tile number n.
+      auto issue_pv1 = [&](const Pv& t, int n) -> bool {
+        if (!pv_begin(t, 0) || !wait_warp(sh.p_full[n & 1], (n >> 1) & 1, kSitePFull)) return false;
+        for (int part = 0; part < C::PARTS; ++part) {
+          if (!v_ready(t, part)) return false;
+          mma_pv(0, n & 1, smem_u32(sP + r.slot * PART), part, t.first);
+          mma_commit_lead(lead, smem_u32(&sh.part_empty[r.slot]));
+          r.next<C::NP>();
+        }
+        mma_commit_lead(lead, smem_u32(&sh.pv_done[n & 1]));
+        if (t.last) mma_commit_lead(lead, smem_u32(&sh.o_final[0]));
+        return true;
+      };
+      bool ok = true, pending = false;
+      Pv prev = {};
+      Piece pc;
+      for (int k = 0; ok && take(k, pc); ++k) {
+        const int nq = NQ == 2 && pc.ntok > (BM >> p.gshift) ? 2 : 1;
+        ok = wait_warp(sh.q_full, k & 1, kSiteQFull);
+        for (int i = 0; ok && i < pc.tiles; ++i) {
+          const Pv cur = {pc.tile0 + i, pc.lo, pc.hi, nq, i == 0, i + 1 == pc.tiles};
+          if constexpr (NQ == 1) {
+            ok = issue_s(1, cur.last);
+            ++g;
+            if (ok && pending) ok = issue_pv1(prev, g - 2);
+          } else {
+            // S_e reuses the columns of P_e of the tile before, whose V comes
+            // behind this tile's K in the ring: both are waited for first.
+            Ring kr = r;
+            if (!wait_warp(sh.part_full[kr.slot], kr.phase, kSitePartFull)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t kb = smem_u32(sP + kr.slot * PART);
+            r.next<C::NP>();
+            uint32_t vb = 0;
+            if (pending) {
+              ok = v_ready(prev, 0);
+              if (!ok) break;
+              vb = smem_u32(sP + r.slot * PART);
+            }
+            for (int e = 0; ok && e < 2; ++e) {
+              if (pending && e < prev.nq) {
+                ok = pv_begin(prev, e) && wait_warp(sh.p_full[e], (ge[e] - 1) & 1, kSitePFull);
+                if (!ok) break;
+                tc_fence_after();
+                mma_pv(e, e, vb, 0, prev.first);
+                if (prev.last) mma_commit_lead(lead, smem_u32(&sh.o_final[e]));
+              }
+              if (pending && e + 1 == prev.nq) mma_commit_lead(lead, smem_u32(&sh.part_empty[r.slot]));
+              if (e < nq) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  const uint32_t off = (c >> 2) * CHUNK + (c & 3) * 32;
+                  mma_ss_lead(lead, tbase + e * 128, sdesc_sw128(q_addr + e * C::QT_BYTES + off, 16, 1024),
+                              sdesc_sw128(kb + off, 16, 1024), idesc_qk, c > 0 ? 1u : 0u);
+                }
+                mma_commit_lead(lead, smem_u32(&sh.s_full[e]));
+                ++ge[e];
+              }
+              if (e + 1 == nq) {
+                mma_commit_lead(lead, smem_u32(&sh.part_empty[kr.slot]));
+                if (cur.last) mma_commit_lead(lead, smem_u32(&sh.q_empty));
+              }
+            }
+            if (pending) r.next<C::NP>();
+          }
+          prev = cur;
+          pending = true;
+        }
+      }
+      if (ok && pending) {
+        if constexpr (NQ == 1) {
+          ok = issue_pv1(prev, g - 1);
+        } else {
+          ok = v_ready(prev, 0);
+          for (int e = 0; ok && e < prev.nq; ++e) {
+            ok = pv_begin(prev, e) && wait_warp(sh.p_full[e], (ge[e] - 1) & 1, kSitePFull);
+            if (!ok) break;
+            tc_fence_after();
+            mma_pv(e, e, smem_u32(sP + r.slot * PART), 0, prev.first);
+            mma_commit_lead(lead, smem_u32(&sh.o_final[e]));
+          }
+        }
+      }
+      mma_commit_lead(lead, smem_u32(&sh.drain));
+      mbar_wait_drain(smem_u32(&sh.drain), 0);
+    }
+  } else {
+    // ---------------- softmax of query tile e: thread r owns row r
+    if constexpr (NQ == 2) regs_increase<C::REGS_SOFT>();
+    const int e = (warp - 4) >> 2;
+    const int q = warp & 3;                // TMEM lane quarter
+    const int r = q * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+    const uint32_t o_base = tbase + lane_off + O_COL + e * 128;
+    const int tq1 = BM >> p.gshift, tok = (e * BM + r) >> p.gshift;   // token of the unit
+    int g = 0, np = 0;                     // tiles and pieces of this query tile so far
+    bool ok = true;
+    Piece pc;
+    for (int k = 0; ok && take(k, pc); ++k) {
+      if (pc.ntok <= e * tq1) continue;    // no such query tile in the unit
+      const bool row_valid = tok < pc.ntok;
+      const bool live = __any_sync(0xffffffffu, row_valid);
+      const int i_tok = pc.i0 + tok;       // number among the sequence's new tokens
+      // Visible slots of the row: [v_lo, v_hi], and with a tree the ones of
+      // `family` from slot len on.
+      int v_lo = 0, v_hi = pc.len + i_tok;
+      uint64_t family = 0;
+      int t_lo = 0;                        // tiles from t_lo to t_hi are seen whole by every row
+      if (live && tree) {
+        const PagedSeq s = {pc.row0 - pc.i0, pc.n, pc.len};
+        const Ancestors a = paged_ancestors(batch, s, lane, p.status);
+        const int it = min(i_tok, kTreeMax - 1);
+        family = a.of(it);
+        const int at = pc.len + __popcll(family) - 1;            // position
+        v_hi = pc.len - 1;
+        if (p.window > 0) {
+          v_lo = at - p.window + 1;
+          if (p.window < kTreeMax) {       // ancestors fewer than `window` steps away
+            family = 1ull << it;
+            int up = a.parent_of(it);
+            for (int d = 1; d < p.window; ++d) {
+              if (up >= 0) family |= 1ull << up;
+              const int next = a.parent_of(max(up, 0));
+              up = up >= 0 ? next : -1;
+            }
+          }
+        }
+      } else if (p.window > 0) {
+        v_lo = pc.len + i_tok - p.window + 1;
+      }
+      t_lo = __reduce_max_sync(0xffffffffu, row_valid ? v_lo : 0);
+      const int t_hi = __reduce_min_sync(0xffffffffu, row_valid ? v_hi : 0x7fffffff);
+      float m_used = -INFINITY, l = 0.f;
+      for (int i = 0; i < pc.tiles; ++i, ++g) {
+        const int sb = NQ == 2 ? e : (g & 1);
+        const uint32_t s_addr = tbase + lane_off + sb * 128;
+        ok = wait_warp(sh.s_full[sb], NQ == 2 ? (g & 1) : ((g >> 1) & 1), kSiteSFull);
+        if (!ok) break;
+        if (live) {
+          tc_fence_after();
+          const int s_tile = (pc.tile0 + i) * BN;
+          uint32_t ra[32], rb[32], rc[32], rd[32];
+          float m0, m1, m2, m3;
+          tmem_ld32_max(s_addr, ra, m0);
+          tmem_ld32_max(s_addr + 32, rb, m1);
+          tmem_ld32_max(s_addr + 64, rc, m2);
+          tmem_ld32_max(s_addr + 96, rd, m3);
+          tmem_ld_wait(ra);
+          tmem_ld_wait(rb);
+          tmem_ld_wait(rc);
+          tmem_ld_wait(rd);
+          tmem_ld_wait(m0);
+          tmem_ld_wait(m1);
+          tmem_ld_wait(m2);
+          tmem_ld_wait(m3);
+          if (s_tile < t_lo || s_tile + BN - 1 > t_hi) {
+            uint32_t keep[4];
+            const int a = v_lo - s_tile, z = v_hi - s_tile, d = s_tile - pc.len;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              keep[c] = bits_from_to(a - 32 * c, z - 32 * c);
+              if (tree) keep[c] |= bits_at(family, d + 32 * c);
+            }
+            m0 = mask_max(ra, keep[0]);
+            m1 = mask_max(rb, keep[1]);
+            m2 = mask_max(rc, keep[2]);
+            m3 = mask_max(rd, keep[3]);
+          }
+          const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * LOG2E;
+          const bool grow = mx > m_used + (RESCALE_THRESHOLD + P_SHIFT);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float m_new = grow ? mx - P_SHIFT : m_used;
+            const float factor = (m_new == m_used) ? 1.f : ex2(m_used - m_new);
+            if (i > 0) {
+              // O holds the PV of the tiles before: with two query tiles S_e
+              // of this tile was issued after them, with one PV may still run.
+              if constexpr (NQ == 1) {
+                ok = wait_warp(sh.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, kSitePvDone);
+                if (!ok) break;
+                tc_fence_after();
+              }
+#pragma unroll 1
+              for (int c = 0; c < DH / 32; ++c) {
+                uint32_t ro[32];
+                tmem_ld32(o_base + c * 32, ro);
+                tmem_ld_wait(ro);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) ro[x] = __float_as_uint(__uint_as_float(ro[x]) * factor);
+                tmem_st32(o_base + c * 32, ro);
+              }
+              tmem_st_wait();
+            }
+            l *= factor;
+            m_used = m_new;
+          }
+          const float mref = (m_used == -INFINITY) ? 0.f : m_used;
+          const float2 l2e = make_float2(LOG2E, LOG2E), negm = make_float2(-mref, -mref);
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                           make_float2(0.f, 0.f)};
+          {
+            uint32_t pk[32];
+            exp_pack(ra, pk, acc, l2e, negm);
+            exp_pack(rb, pk + 16, acc, l2e, negm);
+            tmem_st32(s_addr, pk);
+          }
+          {
+            uint32_t pk[32];
+            exp_pack(rc, pk, acc, l2e, negm);
+            exp_pack(rd, pk + 16, acc, l2e, negm);
+            tmem_st32(s_addr + 32, pk);
+          }
+          const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+          const float2 a = __fadd2_rn(a01, a23);
+          l += a.x + a.y;
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[sb]));
+      }
+      // ---------------- epilogue: this row of O
+      if (ok) ok = wait_warp(sh.o_final[e], np & 1, kSiteOFinal);
+      ++np;
+      if (!ok) break;
+      if (live) {
+        tc_fence_after();
+        const bool whole = pc.ends == 3, have = row_valid && l != 0.f;
+        const size_t orow = static_cast<size_t>(pc.row0 + tok) * p.H + (pc.j << p.gshift) +
+                            (r & ((1 << p.gshift) - 1));
+        // parts: a CTA's first piece may begin inside a unit, its last end inside one
+        const size_t prow = static_cast<size_t>(2 * blockIdx.x + (pc.ends & 1)) * p.rows + e * BM + r;
+        if (!whole && row_valid)
+          p.pstat[prow] = have ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
+        const float inv = have ? 1.f / l : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < DH / 32; ++c) {
+          uint32_t ro[32];
+          tmem_ld32(o_base + c * 32, ro);
+          tmem_ld_wait(ro);
+          if (row_valid && whole) {
+            store_row32(static_cast<uint16_t*>(p.O) + orow * DH + c * 32, ro, inv, have, p.o_f16);
+          } else if (row_valid) {
+            float4* d = reinterpret_cast<float4*>(p.part + prow * DH + c * 32);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              d[x] = make_float4(__uint_as_float(ro[4 * x]), __uint_as_float(ro[4 * x + 1]),
+                                 __uint_as_float(ro[4 * x + 2]), __uint_as_float(ro[4 * x + 3]));
+          }
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.o_free[e]));
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// Adds the parts of the unit that starts in CTA blockIdx.x of the attention
+// and ends in a later one: CTA (x, y) takes rows y, y + gridDim.y, ...
+template <int DH>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const Params p) {
+  pdl_enter();
+  if (lost_work(p.status, kLostWait)) return;   // parts may be missing
+  const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.split) + blockIdx.x);
+  const Split u = {raw.x, raw.y, raw.z, raw.w};
+  constexpr int QUADS = DH / 4, GROUPS = 256 / QUADS;   // threads along the channels, along the parts
+  __shared__ float weight[kMaxCtas];
+  __shared__ float red[8], sum_sh;
+  __shared__ float4 acc_sh[GROUPS][QUADS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int quad = tid % QUADS, group = tid / QUADS;
+  const int rows = u.parts > 0 ? u.ntok << p.gshift : 0;
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    // part 0 ends CTA x, the others begin the CTAs behind it
+    auto slot = [&](int i) -> size_t {
+      return static_cast<size_t>(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * p.rows + r;
+    };
+    float2 st = make_float2(-INFINITY, 0.f);
+    if (tid < u.parts) st = __ldcg(p.pstat + slot(tid));
+    float m = st.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+    m = red[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) m = fmaxf(m, red[w]);
+    const float f = st.y == 0.f ? 0.f : ex2(st.x - m);
+    if (tid < u.parts) weight[tid] = f;
+    float l = f * st.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    __syncthreads();
+    if (lane == 0) red[warp] = l;
+    __syncthreads();
+    if (tid == 0) {
+      float s = 0.f;
+      for (int w = 0; w < 8; ++w) s += red[w];
+      sum_sh = s;
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = group; i < u.parts; i += GROUPS) {
+      const float w = weight[i];
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part + slot(i) * DH) + quad);
+      if (w != 0.f) {
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+      }
+    }
+    acc_sh[group][quad] = acc;
+    __syncthreads();
+    if (group == 0) {
+      for (int w = 1; w < GROUPS; ++w) {
+        const float4 v = acc_sh[w][quad];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+      }
+      const float inv = sum_sh != 0.f ? 1.f / sum_sh : 0.f;
+      const size_t orow = static_cast<size_t>(u.row0 + (r >> p.gshift)) * p.H + (u.j << p.gshift) +
+                          (r & ((1 << p.gshift) - 1));
+      uint2 w;
+      if (p.o_f16) w = make_uint2(pack_half2(acc.x * inv, acc.y * inv), pack_half2(acc.z * inv, acc.w * inv));
+      else w = make_uint2(pack_bf162(acc.x * inv, acc.y * inv), pack_bf162(acc.z * inv, acc.w * inv));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * DH + quad * 4) = w;
+    }
+    __syncthreads();
+  }
+}
+
+// Query tiles per unit: two where a unit of d_h = 128 can fill them.
+int query_tiles(int T_max, int G, int d_h) { return d_h == 128 && static_cast<long long>(T_max) * G > BM ? 2 : 1; }
+
+// Rows of a part in the workspace.
+int part_rows(int T_max, int G, int d_h) {
+  return static_cast<int>(std::min<long long>(static_cast<long long>(T_max) * G, query_tiles(T_max, G, d_h) * BM));
+}
+
+struct Layout {
+  size_t stat, part, split, total;
+};
+Layout layout(int T_max, int H, int H_kv, int d_h) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = static_cast<size_t>(2) * kMaxCtas * part_rows(T_max, H / H_kv, d_h);
+  Layout l;
+  l.stat = 0;
+  l.part = up(rows * sizeof(float2));
+  l.split = l.part + up(rows * d_h * 4);
+  l.total = l.split + up(kMaxCtas * sizeof(Split));
+  return l;
+}
+
+template <int DH, int NQ>
+cudaError_t launch_cfg(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                       const Params& p, cudaStream_t stream) {
+  using C = Cfg<DH, NQ>;
+  auto kern = paged_attn_kernel<DH, NQ>;
+  int regs = 0;
+  if (cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, &regs)) return e;
+  // The softmax warpgroups' register increase waits for the registers the
+  // other warpgroup gives up: launch only when the split fits.
+  if (NQ == 2 && regs * C::THREADS < 128 * C::REGS_CTRL + 256 * C::REGS_SOFT)
+    return cudaErrorInvalidConfiguration;
+  const int ctas = std::min(num_sms(), kMaxCtas);
+  if (cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p)) return e;
+  return launch_pdl(paged_merge_kernel<DH>, dim3(ctas, std::min(p.rows, 32)), dim3(256), 0, stream, p);
+}
+
+}  // namespace
+
+size_t paged_attention_ws_bytes(int T_max, int H, int H_kv, int d_h) {
+  return layout(T_max, H, H_kv, d_h).total;
+}
+
+cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const void* K_pages,
+                                   const void* V_pages, void* O, int o_dtype, int H, int H_kv,
+                                   int d_h, int window, void* ws, cudaStream_t stream, int* status) {
+  const int G = H / H_kv, nq = query_tiles(batch.T_max, G, d_h);
+  const Layout lay = layout(batch.T_max, H, H_kv, d_h);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  Params p;
+  p.batch = batch;
+  p.pstat = reinterpret_cast<float2*>(w + lay.stat);
+  p.part = reinterpret_cast<float*>(w + lay.part);
+  p.split = reinterpret_cast<Split*>(w + lay.split);
+  p.O = O;
+  p.o_f16 = o_dtype == kF16 ? 1 : 0;
+  p.H = H;
+  p.H_kv = H_kv;
+  p.gshift = G == 4 ? 2 : (G == 2 ? 1 : 0);
+  p.window = window;
+  p.tq = nq * BM / G;
+  p.tokbox = std::min(BM / G, batch.T_max);
+  p.rows = part_rows(batch.T_max, G, d_h);
+  p.status = status;
+  // Q [M, H, d_h]: box {64 channels, G heads, tokens}; rows behind M read as zeros.
+  CUtensorMap tq, tk, tv;
+  const uint64_t row = static_cast<uint64_t>(d_h) * 2;
+  const uint64_t qdims[3] = {static_cast<uint64_t>(d_h), static_cast<uint64_t>(H), static_cast<uint64_t>(batch.M)};
+  const uint64_t qstr[2] = {row, static_cast<uint64_t>(H) * row};
+  const uint32_t qbox[3] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(p.tokbox)};
+  // the pools as rows of slots: box {64 channels, 1 head, the slots of a page}
+  const uint64_t kdims[3] = {static_cast<uint64_t>(d_h), static_cast<uint64_t>(H_kv),
+                             static_cast<uint64_t>(batch.n_pages) << batch.page_shift};
+  const uint64_t kstr[2] = {row, static_cast<uint64_t>(H_kv) * row};
+  const uint32_t kbox[3] = {64, 1, static_cast<uint32_t>(std::min(1 << batch.page_shift, 64))};
+  if (!encode_tiled(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, Q, qdims, qstr, qbox) ||
+      !encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, K_pages, kdims, kstr, kbox) ||
+      !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, V_pages, kdims, kstr, kbox))
+    return cudaErrorInvalidValue;
+  if (d_h == 256) return launch_cfg<256, 1>(tq, tk, tv, p, stream);
+  return nq == 2 ? launch_cfg<128, 2>(tq, tk, tv, p, stream) : launch_cfg<128, 1>(tq, tk, tv, p, stream);
+}
+
+}  // namespace g3

@@ -19,12 +19,16 @@ constexpr unsigned long long kWaitTimeoutNs = 1000000000ull;  // 1 s per wait
 enum : int {
   kDevErrTimeoutBase = 0x1000,   // + wait-site id
   kDevErrBadToken = 0x2000,      // a token id outside [0, V)
+  kDevErrBadPaged = 0x4000,      // a paged batch's row, length, page or parent out of its range
 };
 
 // What a recorded error may have left undone, as masks of the status word: a
 // wait that gave up, the work behind it; any error, also what the kernels
 // skip that start with the word set (the GEMMs).
-enum : int { kLostWait = kDevErrTimeoutBase, kLostAny = kDevErrTimeoutBase | kDevErrBadToken };
+enum : int {
+  kLostWait = kDevErrTimeoutBase,
+  kLostAny = kDevErrTimeoutBase | kDevErrBadToken | kDevErrBadPaged
+};
 
 // Has an error of `mask` been recorded?
 __device__ __forceinline__ bool lost_work(const int* status, int mask) {
