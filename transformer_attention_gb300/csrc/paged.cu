@@ -4,12 +4,16 @@
 // append: x <- x / sqrt(mean(x^2) + 1e-6) * (1 + gamma), then RoPE at lens[b] +
 //   depth (rope.cuh), Q also times the query scale; K' and V rows go straight
 //   to their page slots.  Every number is read and written once: HBM bounds it
-//   for prompts, latency for a step.  A warp takes (row, up to 8 steps of head
-//   vectors), d_h / 8 lanes per vector and 16 bytes per lane, all loads first.
+//   for prompts, latency for a step.  A CTA takes a few rows, finds their
+//   sequences, positions and slots together, and its warps take up to 8 steps
+//   of a row's head vectors (Q, K and V), d_h / 8 lanes per vector and 16 bytes
+//   per lane, all loads first.
 // commit: token accepted[b, i] moves to slot lens[b] + i.  accepted ascends, so
 //   accepted[b, i] >= i, and a column of the rows is moved by one thread from
 //   the first token to the last: a slot is written only after the token that
 //   lay there was read.
+#include <algorithm>
+
 #include "paged.cuh"
 #include "rope.cuh"
 
@@ -18,7 +22,10 @@ namespace g3 {
 namespace {
 
 constexpr float kEps = 1e-6f;
-constexpr int kVecUnroll = 8;    // steps of head vectors per item
+constexpr int kVecUnroll = 8;        // steps of head vectors per item
+constexpr int kAppendRows = 32;      // rows of a CTA at a time
+constexpr int kAppendWarps = 8;
+constexpr int kStartsMax = 1024;     // row_start entries kept in shared memory
 
 // Token row m's sequence and position (whole warp); seq -1 behind the last one.
 struct PagedToken {
@@ -61,21 +68,24 @@ struct AppendParams {
   __half* Kp;
   __half* Vp;
   long ldq, ldqo, ldkv;
-  int H, H_kv, chunk_u, zero_behind, lost;
+  int H, H_kv, chunk_u, rows, zero_behind, lost;   // rows: of a CTA at a time
   float query_scale;
   int* status;
 };
 
 // NORM: norm and rotation; else the rows go to the pages as they are.
 template <int DH, bool NORM>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(32 * kAppendWarps, 2)
     paged_append_kernel(const PagedBatch p, const AppendParams a, const __grid_constant__ RopeFreqs freqs) {
   pdl_enter();
-  if (lost_work(a.status, a.lost)) return;
   constexpr int LPV = DH / 8;      // lanes per head vector
   constexpr int VPW = 32 / LPV;    // head vectors per warp step
   constexpr int HALF = LPV / 2;    // lane distance of the RoPE partner
-  const int lane = threadIdx.x & 31;
+  __shared__ int starts[kStartsMax + 1];
+  __shared__ int dst_sh[kAppendRows];      // pool row, -1: no page, -2: of no sequence
+  __shared__ float pos_sh[kAppendRows];
+  const bool lost = lost_work(a.status, a.lost);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int sub = lane / LPV, ll = lane % LPV;
   const bool second_half = ll >= HALF;
   const int c0 = (ll % HALF) * 8;
@@ -84,93 +94,136 @@ __global__ void __launch_bounds__(256, 2)
     gq_raw = *reinterpret_cast<const uint4*>(a.gq + ll * 8);
     gk_raw = *reinterpret_cast<const uint4*>(a.gk + ll * 8);
   }
-  const int warps_total = gridDim.x * (blockDim.x >> 5);
+  const bool in_smem = p.B <= kStartsMax;
+  if (in_smem)
+    for (int i = tid; i <= p.B; i += blockDim.x) starts[i] = __ldcg(p.row_start + i);
   const int h0 = NORM ? 0 : a.H;                   // Q is finished without gammas
-  const int nvec = a.H - h0 + a.H_kv;
+  const int hk = a.H + a.H_kv, end = hk + a.H_kv;  // head vectors: Q, K, V
   const int vpc = VPW * a.chunk_u;
-  const int nch = (nvec + vpc - 1) / vpc;
-  const long items = static_cast<long>(p.M) * nch;
+  const int nch = (end - h0 + vpc - 1) / vpc;      // items of a row
   const int KVD = a.H_kv * DH;
-  for (long item = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); item < items;
-       item += warps_total) {
-    const int m = static_cast<int>(item / nch);
-    const int base = h0 + static_cast<int>(item % nch) * vpc;
-    const int first = base + sub;
-    uint4 raw[kVecUnroll];
+
+  // This lane's 16 bytes of the item's vectors.
+  uint4 raw[kVecUnroll];
+  auto load = [&](int m0, int item) {
+    const int m = m0 + item / nch, first = h0 + item % nch * vpc + sub;
 #pragma unroll
     for (int u = 0; u < kVecUnroll; ++u) {
       const int hv = first + u * VPW;
-      const __half* src = hv < a.H ? a.Q + m * a.ldq + hv * DH : a.K + m * a.ldkv + (hv - a.H) * DH;
-      raw[u] = (u < a.chunk_u && hv < h0 + nvec) ? __ldcg(reinterpret_cast<const uint4*>(src + ll * 8))
-                                                 : make_uint4(0, 0, 0, 0);
+      const __half* src = hv < a.H ? a.Q + m * a.ldq + hv * DH
+                                   : (hv < hk ? a.K + m * a.ldkv + (hv - a.H) * DH
+                                              : a.V + m * a.ldkv + (hv - hk) * DH);
+      raw[u] = (u < a.chunk_u && hv < end) ? __ldcg(reinterpret_cast<const uint4*>(src + ll * 8))
+                                           : make_uint4(0, 0, 0, 0);
     }
-    const PagedToken t = paged_token(p, m, lane, a.status);
-    if (t.seq < 0) {
-      if (a.zero_behind && item % nch == 0)   // (its first item; the others write nothing)
-        for (int v = lane; v < a.H * LPV; v += 32)
-          *reinterpret_cast<uint4*>(a.Qo + m * a.ldqo + v * 8) = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    const int row = paged_row(p, t.seq, t.len + t.i, a.status);
-    float cs[8], sn[8];
-    if constexpr (NORM) {
-      const float pos = static_cast<float>(t.len + t.depth);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) rope_sincos(pos, freqs.f[c0 + e], sn[e], cs[e]);
-    }
-#pragma unroll
-    for (int u = 0; u < kVecUnroll; ++u) {
-      if (u >= a.chunk_u || base + u * VPW >= h0 + nvec) break;   // warp-uniform
-      const int hv = first + u * VPW;
-      const bool is_q = hv < a.H;
-      uint4 w = raw[u];
-      if constexpr (NORM) {
-        float x[8];
-        const __half2* h2 = reinterpret_cast<const __half2*>(&raw[u]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = __half22float2(h2[e]);
-          x[2 * e] = f.x;
-          x[2 * e + 1] = f.y;
-        }
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int off = HALF; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        const float rs = rsqrtf(ss * (1.f / DH) + kEps);
-        const uint4 graw = is_q ? gq_raw : gk_raw;
-        const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&graw);
-        float y[8], o[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 gf = __bfloat1622float2(g2[e]);
-          y[2 * e] = x[2 * e] * rs * (1.f + gf.x);
-          y[2 * e + 1] = x[2 * e + 1] * rs * (1.f + gf.y);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = __shfl_xor_sync(0xffffffffu, y[e], HALF);
-        const float sc = is_q ? a.query_scale : 1.f;
-        uint32_t* wp = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // first half: (x1 cos - x2 sin), second: (x2 cos + x1 sin)
-          const float s0 = second_half ? sn[2 * e] : -sn[2 * e];
-          const float s1 = second_half ? sn[2 * e + 1] : -sn[2 * e + 1];
-          const float r0 = y[2 * e] * cs[2 * e] + o[2 * e] * s0;
-          const float r1 = y[2 * e + 1] * cs[2 * e + 1] + o[2 * e + 1] * s1;
-          wp[e] = pack_half2(r0 * sc, r1 * sc);
+  };
+
+  for (int m0 = blockIdx.x * a.rows; m0 < p.M; m0 += gridDim.x * a.rows) {
+    const int rows = min(a.rows, p.M - m0), items = rows * nch;
+    int item = warp;
+    if (item < items) load(m0, item);
+    // ---------------- the rows' slots and positions
+    __syncthreads();       // (starts are there; the rows before are done)
+    if (tid < rows) {
+      const int m = m0 + tid;
+      auto start = [&](int i) { return in_smem ? starts[i] : __ldcg(p.row_start + i); };
+      // the first sequence that ends behind m
+      int b = 0, e = p.B;
+      while (b < e) {
+        const int mid = (b + e) / 2;
+        if (start(mid + 1) <= m) b = mid + 1;
+        else e = mid;
+      }
+      int dst = -2, pos = 0;
+      if (b < p.B) {
+        const PagedSeq s = paged_seq(p, b, a.status);
+        const int i = m - s.row0;
+        if (i >= 0 && i < s.n) {   // (a sequence that does not fit has none)
+          dst = paged_row(p, b, s.len + i, a.status);
+          pos = s.len + i;
         }
       }
-      if (hv >= h0 + nvec) continue;
-      if (is_q) {
-        *reinterpret_cast<uint4*>(a.Qo + m * a.ldqo + hv * DH + ll * 8) = w;
-      } else if (row >= 0) {
-        const int off = (hv - a.H) * DH + ll * 8;
-        const uint4 v = __ldcg(reinterpret_cast<const uint4*>(a.V + m * a.ldkv + off));
-        *reinterpret_cast<uint4*>(a.Kp + static_cast<size_t>(row) * KVD + off) = w;
-        *reinterpret_cast<uint4*>(a.Vp + static_cast<size_t>(row) * KVD + off) = v;
+      dst_sh[tid] = dst;
+      pos_sh[tid] = static_cast<float>(pos);
+    }
+    if (p.parents != nullptr) {    // a tree: positions by depth, a warp per row
+      __syncthreads();             // (behind the positions without one)
+      for (int r = warp; r < rows; r += kAppendWarps) {
+        const PagedToken t = paged_token(p, m0 + r, lane, a.status);
+        if (lane == 0 && t.seq >= 0) pos_sh[r] = static_cast<float>(t.len + t.depth);
       }
+    }
+    if (__syncthreads_or(lost)) return;
+
+    while (item < items) {
+      const int r = item / nch, m = m0 + r;
+      const int base = h0 + item % nch * vpc, first = base + sub;
+      const int dst = dst_sh[r];
+      if (dst == -2) {
+        if (a.zero_behind && item % nch == 0)   // (the row's first item; the others write nothing)
+          for (int v = lane; v < a.H * LPV; v += 32)
+            *reinterpret_cast<uint4*>(a.Qo + m * a.ldqo + v * 8) = make_uint4(0, 0, 0, 0);
+      } else {
+        float cs[8], sn[8];
+        if (NORM && base < hk) {
+          const float pos = pos_sh[r];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) rope_sincos(pos, freqs.f[c0 + e], sn[e], cs[e]);
+        }
+#pragma unroll
+        for (int u = 0; u < kVecUnroll; ++u) {
+          if (u >= a.chunk_u || base + u * VPW >= end) break;   // warp-uniform
+          const int hv = first + u * VPW;
+          const bool is_q = hv < a.H;
+          uint4 w = raw[u];
+          if (NORM && base + u * VPW < hk) {
+            float x[8];
+            const __half2* h2 = reinterpret_cast<const __half2*>(&raw[u]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = __half22float2(h2[e]);
+              x[2 * e] = f.x;
+              x[2 * e + 1] = f.y;
+            }
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int off = HALF; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+            const float rs = rsqrtf(ss * (1.f / DH) + kEps);
+            const uint4 graw = is_q ? gq_raw : gk_raw;
+            const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&graw);
+            float y[8], o[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 gf = __bfloat1622float2(g2[e]);
+              y[2 * e] = x[2 * e] * rs * (1.f + gf.x);
+              y[2 * e + 1] = x[2 * e + 1] * rs * (1.f + gf.y);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = __shfl_xor_sync(0xffffffffu, y[e], HALF);
+            const float sc = is_q ? a.query_scale : 1.f;
+            uint32_t rot[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // first half: (x1 cos - x2 sin), second: (x2 cos + x1 sin)
+              const float s0 = second_half ? sn[2 * e] : -sn[2 * e];
+              const float s1 = second_half ? sn[2 * e + 1] : -sn[2 * e + 1];
+              const float r0 = y[2 * e] * cs[2 * e] + o[2 * e] * s0;
+              const float r1 = y[2 * e + 1] * cs[2 * e + 1] + o[2 * e + 1] * s1;
+              rot[e] = pack_half2(r0 * sc, r1 * sc);
+            }
+            if (hv < hk) w = make_uint4(rot[0], rot[1], rot[2], rot[3]);
+          }
+          if (hv >= end) continue;
+          __half* to = is_q ? a.Qo + m * a.ldqo + hv * DH
+                            : (hv < hk ? a.Kp + static_cast<size_t>(dst) * KVD + (hv - a.H) * DH
+                                       : a.Vp + static_cast<size_t>(dst) * KVD + (hv - hk) * DH);
+          if (is_q || dst >= 0) *reinterpret_cast<uint4*>(to + ll * 8) = w;
+        }
+      }
+      item += kAppendWarps;
+      if (item < items) load(m0, item);
     }
   }
 }
@@ -240,17 +293,33 @@ template <int DH>
 cudaError_t launch_append_dh(const PagedBatch& batch, const AppendParams& p, bool norm,
                              const RopeFreqs& f, cudaStream_t stream) {
   AppendParams a = p;
-  const int vpw = 32 / (DH / 8);
-  const long nvec = (norm ? a.H : 0) + a.H_kv;
-  // Few rows: a step of head vectors per warp, so that they spread over the
-  // SMs; many: kVecUnroll, which share a row's angles.
-  const long steps = batch.M * ((nvec + vpw - 1) / vpw);
-  a.chunk_u = steps <= 16L * num_sms() ? 1 : kVecUnroll;
-  const long items = batch.M * ((nvec + vpw * a.chunk_u - 1) / (vpw * a.chunk_u));
-  const long blocks = (items + 7) / 8, most = 8L * num_sms();
-  const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));
-  return norm ? launch_pdl(paged_append_kernel<DH, true>, grid, dim3(256), 0, stream, batch, a, f)
-              : launch_pdl(paged_append_kernel<DH, false>, grid, dim3(256), 0, stream, batch, a, f);
+  constexpr int vpw = 32 / (DH / 8);
+  const int steps = ((norm ? a.H : 0) + 2 * a.H_kv + vpw - 1) / vpw;   // of a row
+  // Few rows: one per CTA, its steps spread over the warps; many: as many as
+  // share out the rows over two CTAs per SM.
+  const int slots = 2 * num_sms();
+  const int rounds = (batch.M + slots * kAppendRows - 1) / (slots * kAppendRows);
+  a.rows = (batch.M + slots * rounds - 1) / (slots * rounds);
+  a.chunk_u = std::min(kVecUnroll, std::max(1, steps * a.rows / kAppendWarps));
+  const int blocks = (batch.M + a.rows - 1) / a.rows;
+  const dim3 grid(std::min(blocks, slots)), block(32 * kAppendWarps);
+  return norm ? launch_pdl(paged_append_kernel<DH, true>, grid, block, 0, stream, batch, a, f)
+              : launch_pdl(paged_append_kernel<DH, false>, grid, block, 0, stream, batch, a, f);
+}
+
+// The frequencies of the thread's last call (128 powers in double take 6 us of
+// host time, more than a step's kernel).
+const RopeFreqs& rope_freqs(int d_h, double base, double scale) {
+  thread_local RopeFreqs f;
+  thread_local int at_d = 0;
+  thread_local double at_base = 0, at_scale = 0;
+  if (at_d != d_h || at_base != base || at_scale != scale) {
+    f = make_rope_freqs(d_h, base, scale);
+    at_d = d_h;
+    at_base = base;
+    at_scale = scale;
+  }
+  return f;
 }
 
 }  // namespace
@@ -286,8 +355,8 @@ cudaError_t launch_paged_append(const PagedBatch& batch, const void* Q, long ldq
   a.query_scale = query_scale;
   a.status = status;
   const bool norm = gamma_k != nullptr;
-  RopeFreqs f{};
-  if (norm) f = make_rope_freqs(d_h, rope_base, rope_scale);
+  static const RopeFreqs none{};
+  const RopeFreqs& f = norm ? rope_freqs(d_h, rope_base, rope_scale) : none;
   return d_h == 256 ? launch_append_dh<256>(batch, a, norm, f, stream)
                     : launch_append_dh<128>(batch, a, norm, f, stream);
 }

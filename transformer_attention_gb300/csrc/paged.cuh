@@ -121,48 +121,59 @@ __device__ __forceinline__ Ancestors paged_ancestors(const PagedBatch& p, const 
 }
 
 // ---------------------------------------------------------------- work units
-// A unit of the attention is a kv head of one sequence and `tq` of its new
+// A unit of the attention is a kv head of one sequence and 2^ts of its new
 // tokens; its work are the 128-slot tiles from the first slot that one of
-// these tokens may see to the last.  window 0: none.  tq is 32, 64, 128 or 256.
+// these tokens may see to the last.  window 0: none.  ts is 5 to 8.
+constexpr int kTileShift = 7;
+static_assert(1 << kTileShift == kPagedTile, "tile");
+
 struct PagedUnit {
   int lo, hi, tile0, tiles;   // visible slots [lo, hi), tiles [tile0, tile0 + tiles)
 };
 
-__host__ __device__ inline PagedUnit paged_unit(int len, int n, int window, bool tree, int tq, int q) {
+__host__ __device__ inline int paged_units(int n, int ts) { return (n + (1 << ts) - 1) >> ts; }
+
+__host__ __device__ inline PagedUnit paged_unit(int len, int n, int window, bool tree, int ts, int q) {
   PagedUnit u;
-  const int from = len + (tree ? 0 : q * tq) - window + 1;   // (a tree's tokens may have any depth)
-  const int end = (q + 1) * tq;
+  const int from = len + (tree ? 0 : q << ts) - window + 1;   // (a tree's tokens may have any depth)
+  const int end = (q + 1) << ts;
   u.lo = window > 0 && from > 0 ? from : 0;
   u.hi = len + (end < n ? end : n);
-  u.tile0 = u.lo / kPagedTile;
-  u.tiles = (u.hi + kPagedTile - 1) / kPagedTile - u.tile0;
+  u.tile0 = u.lo >> kTileShift;
+  u.tiles = ((u.hi + kPagedTile - 1) >> kTileShift) - u.tile0;
   return u;
 }
 
-// sum over i < N of floor((x + i tq) / 128), x >= 0
-__host__ __device__ inline long long paged_floor_sum(long long x, long long N, int tq) {
-  if (tq > kPagedTile) return N * (x / kPagedTile) + (tq / kPagedTile) * (N * (N - 1) / 2);
-  const long long k = kPagedTile / tq, c = x / tq;
-  const long long d1 = (c + N) / k, r1 = (c + N) % k, d0 = c / k, r0 = c % k;
-  return k * (d1 * (d1 - 1) / 2) + d1 * r1 - k * (d0 * (d0 - 1) / 2) - d0 * r0;
+// sum over i < N of floor((x + i 2^ts) / 128), x >= 0
+__host__ __device__ inline long long paged_floor_sum(long long x, long long N, int ts) {
+  if (ts > kTileShift) return N * (x >> kTileShift) + ((N * (N - 1) / 2) << (ts - kTileShift));
+  // with k = 128 / 2^ts: the sum of floor(i / k) from c = floor(x / 2^ts) to c + N
+  const int ks = kTileShift - ts;
+  auto upto = [ks](long long i) {
+    const long long d = i >> ks, r = i & ((1LL << ks) - 1);
+    return ((d * (d - 1) / 2) << ks) + d * r;
+  };
+  const long long c = x >> ts;
+  return upto(c + N) - upto(c);
 }
 
 // Tiles of the first q units (of one kv head) of a sequence.
-__host__ __device__ inline long long paged_prefix(int len, int n, int window, bool tree, int tq, int q) {
+__host__ __device__ inline long long paged_prefix(int len, int n, int window, bool tree, int ts, int q) {
   if (q <= 0 || n <= 0) return 0;
-  const int nq = (n + tq - 1) / tq;
+  if (n <= 1 << ts) return paged_unit(len, n, window, tree, ts, 0).tiles;
+  const int nq = paged_units(n, ts);
   // last tiles, as if every unit were full
-  long long sum = paged_floor_sum(static_cast<long long>(len) + tq + kPagedTile - 1, q, tq);
+  long long sum = paged_floor_sum(static_cast<long long>(len) + (1 << ts) + kPagedTile - 1, q, ts);
   if (q >= nq)   // the last unit ends at n
-    sum += (static_cast<long long>(len) + n + kPagedTile - 1) / kPagedTile -
-           (static_cast<long long>(len) + static_cast<long long>(nq) * tq + kPagedTile - 1) / kPagedTile;
+    sum += ((static_cast<long long>(len) + n + kPagedTile - 1) >> kTileShift) -
+           ((static_cast<long long>(len) + (static_cast<long long>(nq) << ts) + kPagedTile - 1) >> kTileShift);
   if (window > 0) {
     const long long from = static_cast<long long>(len) - window + 1;
     if (tree) {
-      if (from > 0) sum -= q * (from / kPagedTile);
+      if (from > 0) sum -= q * (from >> kTileShift);
     } else {
-      const long long i1 = from > 0 ? 0 : -from / tq + 1;   // first unit whose lo is above 0
-      if (i1 < q) sum -= paged_floor_sum(from + i1 * tq, q - i1, tq);
+      const long long i1 = from > 0 ? 0 : (-from >> ts) + 1;   // first unit whose lo is above 0
+      if (i1 < q) sum -= paged_floor_sum(from + (i1 << ts), q - i1, ts);
     }
   }
   return sum;

@@ -50,7 +50,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 // that are rounded to fp16 reach 2^15, so that those below its normal range, off
 // by 2^-25, are off by 2^-32 at most of the row's largest.
 constexpr float RESCALE_THRESHOLD = 8.0f, P_SHIFT = 7.0f;
-constexpr int kMaxCtas = 256;               // CTAs of a launch at most (workspace)
+constexpr int kMaxCtas = 160;               // CTAs of a launch at most (workspace)
 constexpr int NPC = 4;                      // ring of pieces
 
 enum : int {
@@ -77,6 +77,7 @@ struct Shared {
   long long warp_sum[12];
   long long start_off;
   int start_b;
+  PagedSeq start_seq;
   uint32_t tmem;
   int abort_flag;
 };
@@ -100,10 +101,10 @@ struct Cfg {
 struct Params {
   PagedBatch batch;
   float2* pstat;          // [2 grid, rows] (reference, sum)
-  float* part;            // [2 grid, rows, DH] unnormalised
+  float4* part;           // [2 grid, DH / 4, rows] unnormalised, 4 channels each
   Split* split;           // [grid]
   void* O;
-  int o_f16, H, H_kv, gshift, window, tq, tokbox, rows;
+  int o_f16, H, H_kv, gshift, window, ts, tokbox, rows, one;   // ts: log2 of a unit's tokens; one: T_max fits one unit
   int* status;
 };
 
@@ -160,9 +161,7 @@ template <int DH, int NQ>
 __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const Params p) {
-  pdl_enter();
   using C = Cfg<DH, NQ>;
-  const bool lost = lost_work(p.status, kLostWait);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedBatch& batch = p.batch;
   const bool tree = batch.parents != nullptr;
@@ -173,6 +172,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   uint8_t* sP = smem + C::NQ * C::QT_BYTES;   // ring of parts
   Shared& sh = *reinterpret_cast<Shared*>(sP + C::NP * PART);
   if ((smem_u32(smem) & 1023u) != 0) {        // (never, by the declaration above)
+    pdl_enter();
     if (tid == 0) record_error(p.status, kDevErrTimeoutBase + kSiteQFull);
     return;
   }
@@ -207,15 +207,24 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     tmem_relinquish();
   }
 
+  // (nothing before this reads or writes global memory)
+  pdl_enter();
+  const bool lost = lost_work(p.status, kLostWait);
+
   // ---------------- this CTA's share of all tiles
   const int per = (batch.B + C::THREADS - 1) / C::THREADS;   // sequences per thread
   auto seq_tiles = [&](const PagedSeq& s) -> long long {
-    return p.H_kv * paged_prefix(s.len, s.n, p.window, tree, p.tq, (s.n + p.tq - 1) / p.tq);
+    if (p.one)
+      return s.n > 0 ? static_cast<long long>(p.H_kv) * paged_unit(s.len, s.n, p.window, tree, p.ts, 0).tiles : 0;
+    return p.H_kv * paged_prefix(s.len, s.n, p.window, tree, p.ts, paged_units(s.n, p.ts));
   };
   long long mine = 0;
+  PagedSeq seq = {0, 0, 0};   // the thread's last one
   for (int k = 0; k < per; ++k) {
     const int b = tid * per + k;
-    if (b < batch.B) mine += seq_tiles(paged_seq(batch, b, p.status));
+    if (b >= batch.B) break;
+    seq = paged_seq(batch, b, p.status);
+    mine += seq_tiles(seq);
   }
   long long upto = mine;   // through this thread
 #pragma unroll
@@ -240,19 +249,26 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   // (no more CTAs than tiles: a unit's parts lie in consecutive ones)
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   const bool idle = static_cast<long long>(blockIdx.x) >= ctas;
-  const long long from = idle ? 0 : total * blockIdx.x / ctas;
-  const long long count = idle ? 0 : total * (blockIdx.x + 1) / ctas - from;
+  // first tile of CTA c (64-bit divisions cost some 100 clocks each)
+  auto share = [&](int c) -> long long {
+    if (total < 1 << 23) return static_cast<unsigned>(total) * static_cast<unsigned>(c) / static_cast<unsigned>(ctas);
+    return total * c / ctas;
+  };
+  const long long from = idle ? 0 : share(blockIdx.x);
+  const long long count = idle ? 0 : share(blockIdx.x + 1) - from;
   if (!idle && from < upto && from >= upto - mine) {
     long long off = from - (upto - mine);
     int b = tid * per;
-    while (true) {
-      const long long n = seq_tiles(paged_seq(batch, b, p.status));
+    while (per > 1) {
+      seq = paged_seq(batch, b, p.status);
+      const long long n = seq_tiles(seq);
       if (off < n || b + 1 >= batch.B) break;
       off -= n;
       ++b;
     }
     sh.start_b = b;
     sh.start_off = off;
+    sh.start_seq = seq;
   }
   __syncthreads();
 
@@ -274,9 +290,9 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       // ---------------- pieces
       Split split = {0, 0, 0, 0};
       long long left = count, pos = from, off = idle ? 0 : sh.start_off;
-      int b = idle ? 0 : sh.start_b, k = 0, b0 = 0;
+      int b = idle ? 0 : sh.start_b, k = 0, b0 = b + 1;
       PagedSeq win = {0, 0, 0};   // of sequence b0 + lane
-      bool ok = true, have = false;
+      bool ok = true, first = true, have = false;
       auto publish = [&](const Piece& pc) {
         ok = k < NPC || wait_warp(sh.piece_empty[k % NPC], ((k / NPC) & 1) ^ 1, kSitePieceEmpty);
         if (!ok) return;
@@ -287,42 +303,56 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         ++k;
       };
       while (ok && left > 0 && b < batch.B) {
-        if (!have || b >= b0 + 32) {
-          b0 = b;
-          win = b0 + lane < batch.B ? paged_seq(batch, b0 + lane, p.status) : PagedSeq{0, 0, 0};
-          have = true;
+        PagedSeq s = sh.start_seq;
+        if (!first) {
+          if (!have || b >= b0 + 32) {
+            b0 = b;
+            win = b0 + lane < batch.B ? paged_seq(batch, b0 + lane, p.status) : PagedSeq{0, 0, 0};
+            have = true;
+          }
+          s.row0 = __shfl_sync(0xffffffffu, win.row0, b - b0);
+          s.n = __shfl_sync(0xffffffffu, win.n, b - b0);
+          s.len = __shfl_sync(0xffffffffu, win.len, b - b0);
         }
-        PagedSeq s;
-        s.row0 = __shfl_sync(0xffffffffu, win.row0, b - b0);
-        s.n = __shfl_sync(0xffffffffu, win.n, b - b0);
-        s.len = __shfl_sync(0xffffffffu, win.len, b - b0);
-        const int nq = (s.n + p.tq - 1) / p.tq;
-        const long long head = paged_prefix(s.len, s.n, p.window, tree, p.tq, nq);
-        if (head == 0 || off >= head * p.H_kv) {
-          off = 0;
-          ++b;
-          continue;
-        }
-        int j = static_cast<int>(off / head), q = 0;
-        long long t = off - j * head;
-        if (nq > 1) {   // the unit of tile t: the last one that starts at or before it
-          int q1 = nq;
+        first = false;
+        int q = 0, j = 0, nq = 1;
+        long long t = off;
+        if (p.one) {        // every sequence is one unit per head
+          const int head = s.n > 0 ? paged_unit(s.len, s.n, p.window, tree, p.ts, 0).tiles : 0;
+          if (head == 0) {
+            ++b;
+            continue;
+          }
+          if (off > 0) {    // (inside the first sequence)
+            j = static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(head));
+            t = off - j * head;
+          }
+        } else {
+          nq = paged_units(s.n, p.ts);
+          const long long head = paged_prefix(s.len, s.n, p.window, tree, p.ts, nq);
+          if (head == 0) {
+            ++b;
+            continue;
+          }
+          j = static_cast<int>(off / head);
+          t = off - j * head;
+          int q1 = nq;      // the unit of tile t: the last one that starts at or before it
           while (q1 - q > 1) {
             const int mid = (q + q1) / 2;
-            if (paged_prefix(s.len, s.n, p.window, tree, p.tq, mid) <= t) q = mid;
+            if (paged_prefix(s.len, s.n, p.window, tree, p.ts, mid) <= t) q = mid;
             else q1 = mid;
           }
-          t -= paged_prefix(s.len, s.n, p.window, tree, p.tq, q);
+          t -= paged_prefix(s.len, s.n, p.window, tree, p.ts, q);
         }
         while (ok && left > 0 && j < p.H_kv) {
-          const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.tq, q);
+          const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, q);
           const int n = static_cast<int>(min(left, static_cast<long long>(u.tiles) - t));
           Piece pc;
           pc.b = b;
           pc.j = j;
-          pc.i0 = q * p.tq;
+          pc.i0 = q << p.ts;
           pc.row0 = s.row0 + pc.i0;
-          pc.ntok = min(p.tq, s.n - pc.i0);
+          pc.ntok = min(1 << p.ts, s.n - pc.i0);
           pc.n = s.n;
           pc.len = s.len;
           pc.lo = u.lo;
@@ -331,8 +361,10 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
           pc.tiles = n;
           pc.ends = (t == 0 ? 1 : 0) | (t + n == u.tiles ? 2 : 0);
           if (pc.ends == 1) {   // (pos is the unit's first tile)
-            const long long last = (((pos + u.tiles - 1) + 1) * ctas - 1) / total;
-            split = {pc.row0, pc.ntok, j, static_cast<int>(last) - static_cast<int>(blockIdx.x) + 1};
+            const long long end = pos + u.tiles;
+            const int last = total < 1 << 23 ? (static_cast<unsigned>(end) * static_cast<unsigned>(ctas) - 1) / static_cast<unsigned>(total)
+                                             : static_cast<int>((end * ctas - 1) / total);
+            split = {pc.row0, pc.ntok, j, last - static_cast<int>(blockIdx.x) + 1};
           }
           publish(pc);
           left -= n;
@@ -743,9 +775,10 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         const size_t orow = static_cast<size_t>(pc.row0 + tok) * p.H + (pc.j << p.gshift) +
                             (r & ((1 << p.gshift) - 1));
         // parts: a CTA's first piece may begin inside a unit, its last end inside one
-        const size_t prow = static_cast<size_t>(2 * blockIdx.x + (pc.ends & 1)) * p.rows + e * BM + r;
+        const size_t slot = 2 * blockIdx.x + (pc.ends & 1);
+        float4* pdst = p.part + slot * (DH / 4) * p.rows + e * BM + r;
         if (!whole && row_valid)
-          p.pstat[prow] = have ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
+          p.pstat[slot * p.rows + e * BM + r] = have ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
         const float inv = have ? 1.f / l : 0.f;
 #pragma unroll 1
         for (int c = 0; c < DH / 32; ++c) {
@@ -755,11 +788,12 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
           if (row_valid && whole) {
             store_row32(static_cast<uint16_t*>(p.O) + orow * DH + c * 32, ro, inv, have, p.o_f16);
           } else if (row_valid) {
-            float4* d = reinterpret_cast<float4*>(p.part + prow * DH + c * 32);
+            // (rows next to each other: the lanes' stores are)
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-              d[x] = make_float4(__uint_as_float(ro[4 * x]), __uint_as_float(ro[4 * x + 1]),
-                                 __uint_as_float(ro[4 * x + 2]), __uint_as_float(ro[4 * x + 3]));
+              pdst[static_cast<size_t>(c * 8 + x) * p.rows] =
+                  make_float4(__uint_as_float(ro[4 * x]), __uint_as_float(ro[4 * x + 1]),
+                              __uint_as_float(ro[4 * x + 2]), __uint_as_float(ro[4 * x + 3]));
           }
         }
         tc_fence_before();
@@ -775,81 +809,194 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   }
 }
 
-// Adds the parts of the unit that starts in CTA blockIdx.x of the attention
-// and ends in a later one: CTA (x, y) takes rows y, y + gridDim.y, ...
+// Adds the parts of the units that end in a later CTA than they start in.  A
+// task is up to 32 rows of such a unit and some of their channels: lanes along
+// the rows, which lie next to each other in a part, and where they are few
+// along 4-channel vectors too.  A lane has its row's sums to itself, so a task
+// is one warp's, or that of several where a unit has many parts.
+constexpr int kMergeWarps = 8;
+
+// A lane's running sums: reference, sum, VV vectors.
+template <int VV>
+struct MergeAcc {
+  float m = -INFINITY, l = 0.f;
+  float4 o[VV];
+
+  __device__ __forceinline__ void add(float2 st, const float4 (&x)[VV]) {
+    if (st.y == 0.f) return;                       // saw nothing
+    const float to = fmaxf(m, st.x);
+    const float fm = m == to ? 1.f : ex2(m - to), fx = ex2(st.x - to);
+    m = to;
+    l = l * fm + st.y * fx;
+#pragma unroll
+    for (int v = 0; v < VV; ++v) {
+      o[v].x = o[v].x * fm + x[v].x * fx;
+      o[v].y = o[v].y * fm + x[v].y * fx;
+      o[v].z = o[v].z * fm + x[v].z * fx;
+      o[v].w = o[v].w * fm + x[v].w * fx;
+    }
+  }
+};
+
+struct MergeShared {
+  int upto[kMaxCtas];            // tasks of the units that start in CTAs 0 .. i
+  Split split[kMaxCtas];
+  long long warp_sum[kMergeWarps];
+  int warp_max[kMergeWarps];
+  float2 st[kMergeWarps][32];
+  float4 o[kMergeWarps][2][32];
+};
+
+// Lanes along the rows of a unit of `all` rows: a power of two.
+__device__ __forceinline__ int merge_pad(int all) {
+  return all >= 32 ? 32 : 1 << (31 - __clz(2 * all - 1));
+}
+__device__ __forceinline__ int merge_warps(int parts) {   // warps of a task
+  return parts >= 32 ? 8 : (parts >= 16 ? 4 : (parts >= 8 ? 2 : 1));
+}
+
+// DIRECT: the tasks of the unit `one` that starts in CTA blockIdx.x, over
+// gridDim.y CTAs; else all tasks over all CTAs.
+template <int DH, int VV, bool DIRECT>
+__device__ __forceinline__ void merge_tasks(const Params& p, MergeShared& sh, const Split& one, int total,
+                                            int wp, int ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp & (wp - 1), per = kMergeWarps / wp;
+  const int stride = (DIRECT ? gridDim.y : gridDim.x) * per;
+  for (int t0 = (DIRECT ? blockIdx.y : blockIdx.x) * per; t0 < total; t0 += stride) {
+    const int task = t0 + warp / wp;
+    int cta = DIRECT ? blockIdx.x : 0;             // whose unit: the first with upto > task
+    if (!DIRECT)
+      for (int c0 = 0; c0 < ctas; c0 += 32)
+        cta += __popc(__ballot_sync(0xffffffffu, c0 + lane < ctas && sh.upto[c0 + lane] <= task));
+    const bool live = task < total;
+    MergeAcc<VV> acc;
+#pragma unroll
+    for (int v = 0; v < VV; ++v) acc.o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    size_t orow = 0;
+    int v0 = 0;
+    bool mine = false;
+    if (live) {
+      const Split u = DIRECT ? one : sh.split[cta];
+      const int all = u.ntok << p.gshift;          // rows of the unit
+      const int pad = merge_pad(all);
+      const int vecs = 32 / pad * VV;              // vectors of a task
+      const int chunks = (DH / 4 + vecs - 1) / vecs;
+      const int at = DIRECT ? task : task - (cta > 0 ? sh.upto[cta - 1] : 0);
+      const int r = at / chunks * 32 + (lane & (pad - 1));
+      v0 = at % chunks * vecs + lane / pad * VV;
+      mine = r < all && v0 < DH / 4;
+      orow = static_cast<size_t>(u.row0 + (r >> p.gshift)) * p.H + (u.j << p.gshift) + (r & ((1 << p.gshift) - 1));
+      if (mine) {
+        // this warp's parts: sub, sub + wp, ...; part 0 ends the CTA, the
+        // others begin those behind it
+        constexpr int AT_ONCE = 4;
+        for (int i0 = sub; i0 < u.parts; i0 += AT_ONCE * wp) {
+          float2 st[AT_ONCE];
+          float4 x[AT_ONCE][VV];
+#pragma unroll
+          for (int k = 0; k < AT_ONCE; ++k) {
+            const int i = i0 + k * wp;
+            st[k] = make_float2(0.f, 0.f);
+            if (i < u.parts) {
+              const size_t slot = i == 0 ? 2 * cta + 1 : 2 * (cta + i);
+              st[k] = __ldcg(p.pstat + slot * p.rows + r);
+#pragma unroll
+              for (int v = 0; v < VV; ++v) x[k][v] = __ldcg(p.part + (slot * (DH / 4) + v0 + v) * p.rows + r);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < AT_ONCE; ++k)
+            if (i0 + k * wp < u.parts) acc.add(st[k], x[k]);
+        }
+      }
+    }
+    if (wp > 1) {
+      sh.st[warp][lane] = make_float2(acc.m, acc.l);
+#pragma unroll
+      for (int v = 0; v < VV; ++v) sh.o[warp][v][lane] = acc.o[v];
+      __syncthreads();
+      if (sub == 0)
+        for (int k = 1; k < wp; ++k) {
+          float4 x[VV];
+#pragma unroll
+          for (int v = 0; v < VV; ++v) x[v] = sh.o[warp + k][v][lane];
+          acc.add(sh.st[warp + k][lane], x);
+        }
+      __syncthreads();
+    }
+    if (mine && sub == 0) {
+      const float inv = acc.l != 0.f ? 1.f / acc.l : 0.f;
+      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * DH) + v0;
+      uint2 w[VV];
+#pragma unroll
+      for (int v = 0; v < VV; ++v) {
+        const float a = acc.o[v].x * inv, b = acc.o[v].y * inv, c = acc.o[v].z * inv, d = acc.o[v].w * inv;
+        w[v] = p.o_f16 ? make_uint2(pack_half2(a, b), pack_half2(c, d))
+                       : make_uint2(pack_bf162(a, b), pack_bf162(c, d));
+      }
+      if constexpr (VV == 2) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+      else dst[0] = w[0];
+    }
+  }
+}
+
+// Few rows (at most kMergeDirect): CTAs of their own for each attention CTA,
+// which need not look at the others (step_local, 2 rows: 1.3 us less).
+constexpr int kMergeDirect = 8;
+
 template <int DH>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const Params p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_few_kernel(const Params p) {
   pdl_enter();
-  if (lost_work(p.status, kLostWait)) return;   // parts may be missing
+  const bool lost = lost_work(p.status, kLostWait);   // parts may be missing
+  __shared__ MergeShared sh;
   const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.split) + blockIdx.x);
   const Split u = {raw.x, raw.y, raw.z, raw.w};
-  constexpr int QUADS = DH / 4, GROUPS = 256 / QUADS;   // threads along the channels, along the parts
-  __shared__ float weight[kMaxCtas];
-  __shared__ float red[8], sum_sh;
-  __shared__ float4 acc_sh[GROUPS][QUADS];
+  if (lost || u.parts == 0) return;
+  merge_tasks<DH, 1, true>(p, sh, u, (DH / 4 * merge_pad(u.ntok << p.gshift) + 31) / 32, merge_warps(u.parts), 0);
+}
+
+template <int DH>
+__global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const Params p, int ctas) {
+  pdl_enter();
+  const bool lost = lost_work(p.status, kLostWait);   // parts may be missing
+  __shared__ MergeShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int quad = tid % QUADS, group = tid / QUADS;
-  const int rows = u.parts > 0 ? u.ntok << p.gshift : 0;
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    // part 0 ends CTA x, the others begin the CTAs behind it
-    auto slot = [&](int i) -> size_t {
-      return static_cast<size_t>(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * p.rows + r;
-    };
-    float2 st = make_float2(-INFINITY, 0.f);
-    if (tid < u.parts) st = __ldcg(p.pstat + slot(tid));
-    float m = st.x;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) red[warp] = m;
-    __syncthreads();
-    m = red[0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) m = fmaxf(m, red[w]);
-    const float f = st.y == 0.f ? 0.f : ex2(st.x - m);
-    if (tid < u.parts) weight[tid] = f;
-    float l = f * st.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    __syncthreads();
-    if (lane == 0) red[warp] = l;
-    __syncthreads();
-    if (tid == 0) {
-      float s = 0.f;
-      for (int w = 0; w < 8; ++w) s += red[w];
-      sum_sh = s;
-    }
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = group; i < u.parts; i += GROUPS) {
-      const float w = weight[i];
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part + slot(i) * DH) + quad);
-      if (w != 0.f) {
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
-      }
-    }
-    acc_sh[group][quad] = acc;
-    __syncthreads();
-    if (group == 0) {
-      for (int w = 1; w < GROUPS; ++w) {
-        const float4 v = acc_sh[w][quad];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-      }
-      const float inv = sum_sh != 0.f ? 1.f / sum_sh : 0.f;
-      const size_t orow = static_cast<size_t>(u.row0 + (r >> p.gshift)) * p.H + (u.j << p.gshift) +
-                          (r & ((1 << p.gshift) - 1));
-      uint2 w;
-      if (p.o_f16) w = make_uint2(pack_half2(acc.x * inv, acc.y * inv), pack_half2(acc.z * inv, acc.w * inv));
-      else w = make_uint2(pack_bf162(acc.x * inv, acc.y * inv), pack_bf162(acc.z * inv, acc.w * inv));
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * DH + quad * 4) = w;
-    }
-    __syncthreads();
+  Split u = {0, 0, 0, 0};                             // the unit that starts in CTA tid
+  if (tid < ctas) {
+    const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.split) + tid);
+    u = {raw.x, raw.y, raw.z, raw.w};
+    sh.split[tid] = u;
   }
+  // its tasks with one vector per lane and, packed above them, with two
+  const int all = u.parts > 0 ? u.ntok << p.gshift : 0;
+  const int groups = (all + 31) / 32, vecs = all > 0 ? DH / 4 * merge_pad(all) : 0;
+  long long tasks = static_cast<long long>(groups * ((vecs + 63) / 64)) << 32 | (groups * ((vecs + 31) / 32));
+  long long upto = tasks;
+  int most = u.parts;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
+  if (lane == 31) sh.warp_sum[warp] = upto;
+  if (lane == 0) sh.warp_max[warp] = most;
+  if (__syncthreads_or(lost)) return;
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    if (w < warp) upto += sh.warp_sum[w];
+    total += sh.warp_sum[w];
+    most = max(most, sh.warp_max[w]);
+  }
+  const int wp = merge_warps(most), ones = static_cast<int>(total), twos = static_cast<int>(total >> 32);
+  // Two vectors per lane where one leaves more tasks than warps.
+  const bool two = static_cast<long long>(ones) * wp > gridDim.x * kMergeWarps;
+  if (tid < ctas) sh.upto[tid] = static_cast<int>(two ? upto >> 32 : upto);
+  __syncthreads();
+  if (two) merge_tasks<DH, 2, false>(p, sh, u, twos, wp, ctas);
+  else merge_tasks<DH, 1, false>(p, sh, u, ones, wp, ctas);
 }
 
 // Query tiles per unit: two where a unit of d_h = 128 can fill them.
@@ -887,7 +1034,12 @@ cudaError_t launch_cfg(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
     return cudaErrorInvalidConfiguration;
   const int ctas = std::min(num_sms(), kMaxCtas);
   if (cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p)) return e;
-  return launch_pdl(paged_merge_kernel<DH>, dim3(ctas, std::min(p.rows, 32)), dim3(256), 0, stream, p);
+  if (p.rows <= kMergeDirect) {
+    const int tasks = (DH / 4 * kMergeDirect) / 32;   // at most
+    return launch_pdl(paged_merge_few_kernel<DH>, dim3(ctas, std::min(tasks, 4)), dim3(32 * kMergeWarps), 0,
+                      stream, p);
+  }
+  return launch_pdl(paged_merge_kernel<DH>, dim3(3 * ctas), dim3(32 * kMergeWarps), 0, stream, p, ctas);
 }
 
 }  // namespace
@@ -905,7 +1057,7 @@ cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const
   Params p;
   p.batch = batch;
   p.pstat = reinterpret_cast<float2*>(w + lay.stat);
-  p.part = reinterpret_cast<float*>(w + lay.part);
+  p.part = reinterpret_cast<float4*>(w + lay.part);
   p.split = reinterpret_cast<Split*>(w + lay.split);
   p.O = O;
   p.o_f16 = o_dtype == kF16 ? 1 : 0;
@@ -913,7 +1065,8 @@ cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const
   p.H_kv = H_kv;
   p.gshift = G == 4 ? 2 : (G == 2 ? 1 : 0);
   p.window = window;
-  p.tq = nq * BM / G;
+  p.ts = kTileShift + (nq - 1) - p.gshift;
+  p.one = batch.T_max <= 1 << p.ts ? 1 : 0;
   p.tokbox = std::min(BM / G, batch.T_max);
   p.rows = part_rows(batch.T_max, G, d_h);
   p.status = status;
