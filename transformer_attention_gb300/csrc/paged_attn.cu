@@ -22,8 +22,9 @@
 //   1      TMEM allocation and MMA issue
 //   2      the CTA's pieces of units, published through a ring
 //   3      TMA of Q
-//   4-7    softmax of query tile 0 (one thread per row), its epilogue
-//   8-11   the same of query tile 1 (NQ = 2)
+//   4-7    softmax of query tile 0, one thread per row (NQ = 2: its epilogue too)
+//   8-11   NQ = 2: the same of query tile 1; NQ = 1: the epilogue, so that the
+//          softmax goes on with the next piece
 // TMEM: NQ = 1: S of even and odd tiles at 0 and 128; NQ = 2: S of query tile e
 // at 128 e.  P (fp16 pairs) is written over the first 64 columns of its S.  O
 // from column 256.
@@ -43,6 +44,8 @@ using attn::ex2;
 constexpr int BM = 128, BN = kPagedTile;
 constexpr uint32_t CHUNK = 128 * 128;       // 128 rows x 64 channels (128 B), swizzled
 constexpr uint32_t PART = 32768;
+constexpr uint32_t QSMALL = 32 * 128;       // 32 rows of a chunk: Q of few rows (the MMA reads on behind them)
+constexpr int kTileCost = 2, kUnitCost = 1; // shares of the work
 constexpr uint32_t O_COL = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 // A row's reference stays P_SHIFT below a past maximum while the present one
@@ -55,7 +58,7 @@ constexpr int NPC = 4;                      // ring of pieces
 
 enum : int {
   kSiteQFull = 100, kSiteQEmpty, kSitePartFull, kSitePartEmpty, kSiteSFull, kSitePFull, kSitePvDone,
-  kSiteOFinal, kSiteOFree, kSitePieceFull, kSitePieceEmpty
+  kSiteOFinal, kSiteOFree, kSitePieceFull, kSitePieceEmpty, kSiteStatFull, kSiteStatEmpty
 };
 
 // A CTA's piece of a unit.  tiles 0: no more pieces.
@@ -71,16 +74,35 @@ struct alignas(16) Split {
 };
 
 struct Shared {
-  uint64_t q_full, q_empty, part_full[8], part_empty[8], s_full[2], p_full[2], pv_done[2],
-      o_final[2], o_free[2], piece_full[NPC], piece_empty[NPC], drain;
+  uint64_t q_full[2], q_empty[2], part_full[8], part_empty[8], s_full[2], p_full[2], pv_done[2],
+      o_final[2], o_free[2], stat_full[2], stat_empty[2], piece_full[NPC], piece_empty[NPC], drain;
   Piece piece[NPC];
+  float2 stat[2][BM];     // NQ = 1: (reference, sum) of a piece's rows
   long long warp_sum[12];
-  long long start_off;
-  int start_b;
+  long long start_off;    // of this CTA's share in its first sequence
+  int start_b, first_used, first_j;   // first_used: cost of the piece that is there already
   PagedSeq start_seq;
   uint32_t tmem;
   int abort_flag;
 };
+
+// Bounded wait for a phase; false after a timeout, whose site goes to *lost (it
+// is recorded once, when the role ends), or when another thread gave up.  The
+// roles share the instruction cache, so the waits are kept small.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int site,
+                                         int* lost) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > kWaitTimeoutNs) {
+      *lost = site;
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
 
 template <int DH, int NQ_>
 struct Cfg {
@@ -92,10 +114,12 @@ struct Cfg {
   static constexpr int NP = (7 * PART - NQ * QT_BYTES) / PART;   // ring: what Q leaves of 224 KB
   static constexpr uint32_t SMEM = NQ * QT_BYTES + NP * PART + sizeof(Shared);
   static_assert(SMEM <= 232448 && NP <= 8, "shared memory budget");
-  static constexpr int THREADS = 128 * (1 + NQ);
-  // two softmax warpgroups: the control warps give them registers
-  static constexpr int REGS_LAUNCH = 168, REGS_CTRL = 96, REGS_SOFT = 200;
-  static_assert(128 * REGS_CTRL + 256 * REGS_SOFT <= 384 * REGS_LAUNCH, "register split");
+  static constexpr int THREADS = 384;
+  // the control warps give registers to the others
+  static constexpr int REGS_LAUNCH = 168, REGS_CTRL = 96, REGS_SOFT = NQ == 2 ? 200 : 216;
+  static constexpr int REGS_OTHER = NQ == 2 ? 200 : 168;   // warps 8-11
+  static constexpr int REGS_SPLIT = 128 * (REGS_CTRL + REGS_SOFT + REGS_OTHER);
+  static_assert(REGS_SPLIT <= THREADS * REGS_LAUNCH, "register split");
 };
 
 struct Params {
@@ -104,7 +128,7 @@ struct Params {
   float4* part;           // [2 grid, DH / 4, rows] unnormalised, 4 channels each
   Split* split;           // [grid]
   void* O;
-  int o_f16, H, H_kv, gshift, window, ts, tokbox, rows, one;   // ts: log2 of a unit's tokens; one: T_max fits one unit
+  int o_f16, H, H_kv, gshift, window, ts, tokbox, rows, qsmall;   // ts: log2 of a unit's tokens
   int* status;
 };
 
@@ -120,6 +144,13 @@ struct Ring {
   }
 };
 
+__device__ __forceinline__ void prefetch_3d(const void* tmap, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
 // exp2(s log2 e - m) of 32 columns: packed fp16 pairs to p[0..15], sums to acc.
 __device__ __forceinline__ void exp_pack(const uint32_t (&s)[32], uint32_t* p, float2 (&acc)[4],
                                          float2 l2e, float2 negm) {
@@ -131,18 +162,6 @@ __device__ __forceinline__ void exp_pack(const uint32_t (&s)[32], uint32_t* p, f
     acc[k & 3] = __fadd2_rn(acc[k & 3], e);
     p[k] = pack_half2(e.x, e.y);
   }
-}
-
-__device__ __forceinline__ float mask_max(uint32_t (&r)[32], uint32_t keep) {
-  float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-  for (int c = 0; c < 32; c += 2) {
-    if (!((keep >> c) & 1u)) r[c] = 0xff800000u;
-    if (!((keep >> (c + 1)) & 1u)) r[c + 1] = 0xff800000u;
-    a = fmaxf(a, __uint_as_float(r[c]));
-    b = fmaxf(b, __uint_as_float(r[c + 1]));
-  }
-  return fmaxf(a, b);
 }
 
 // Bits [a, z] of 32, for any a and z.
@@ -157,7 +176,8 @@ __device__ __forceinline__ uint32_t bits_at(uint64_t m, int d) {
   return d > -32 ? static_cast<uint32_t>(m << -d) : 0u;
 }
 
-template <int DH, int NQ>
+// ONE: the new tokens of every sequence fit one unit per head.
+template <int DH, int NQ, bool ONE>
 __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const Params p) {
@@ -178,13 +198,15 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   }
 
   if (tid == 0) {
-    mbar_init(smem_u32(&sh.q_full), 1);
-    mbar_init(smem_u32(&sh.q_empty), 1);
     for (int s = 0; s < C::NP; ++s) {
       mbar_init(smem_u32(&sh.part_full[s]), 1);
       mbar_init(smem_u32(&sh.part_empty[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sh.q_full[s]), 1);
+      mbar_init(smem_u32(&sh.q_empty[s]), 1);
+      mbar_init(smem_u32(&sh.stat_full[s]), 4);
+      mbar_init(smem_u32(&sh.stat_empty[s]), 4);
       mbar_init(smem_u32(&sh.s_full[s]), 1);
       mbar_init(smem_u32(&sh.p_full[s]), 4);
       mbar_init(smem_u32(&sh.pv_done[s]), 1);
@@ -193,10 +215,11 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     }
     for (int s = 0; s < NPC; ++s) {
       mbar_init(smem_u32(&sh.piece_full[s]), 1);
-      mbar_init(smem_u32(&sh.piece_empty[s]), 3 + 4 * C::NQ);   // K/V, MMA, Q, softmax warps
+      mbar_init(smem_u32(&sh.piece_empty[s]), 11);   // all warps but 2
     }
     mbar_init(smem_u32(&sh.drain), 1);
     sh.abort_flag = 0;
+    sh.first_used = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
@@ -211,20 +234,28 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   pdl_enter();
   const bool lost = lost_work(p.status, kLostWait);
 
-  // ---------------- this CTA's share of all tiles
+  // ---------------- this CTA's share of all work
+  // A unit costs kTileCost for each tile and kUnitCost: what a piece costs
+  // besides its tiles.  Tile t of a unit is in the share that holds the unit's
+  // position kUnitCost + t kTileCost.
+  constexpr int TC = kTileCost, UC = kUnitCost;
   const int per = (batch.B + C::THREADS - 1) / C::THREADS;   // sequences per thread
-  auto seq_tiles = [&](const PagedSeq& s) -> long long {
-    if (p.one)
-      return s.n > 0 ? static_cast<long long>(p.H_kv) * paged_unit(s.len, s.n, p.window, tree, p.ts, 0).tiles : 0;
-    return p.H_kv * paged_prefix(s.len, s.n, p.window, tree, p.ts, paged_units(s.n, p.ts));
+  auto head_cost = [&](const PagedSeq& s) -> long long {     // of a kv head of a sequence
+    if constexpr (ONE) {
+      return s.n > 0 ? TC * paged_unit(s.len, s.n, p.window, tree, p.ts, 0).tiles + UC : 0;
+    } else {
+      const int nq = paged_units(s.n, p.ts);
+      return TC * paged_prefix(s.len, s.n, p.window, tree, p.ts, nq) + static_cast<long long>(UC) * nq;
+    }
   };
+  auto tile_at = [](int o) { return max(0, (o - UC + TC - 1) / TC); };   // first tile at or behind position o
   long long mine = 0;
   PagedSeq seq = {0, 0, 0};   // the thread's last one
   for (int k = 0; k < per; ++k) {
     const int b = tid * per + k;
     if (b >= batch.B) break;
     seq = paged_seq(batch, b, p.status);
-    mine += seq_tiles(seq);
+    mine += p.H_kv * head_cost(seq);
   }
   long long upto = mine;   // through this thread
 #pragma unroll
@@ -246,22 +277,43 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     if (w < warp) upto += sh.warp_sum[w];
     total += sh.warp_sum[w];
   }
-  // (no more CTAs than tiles: a unit's parts lie in consecutive ones)
-  const long long ctas = min(static_cast<long long>(gridDim.x), total);
-  const bool idle = static_cast<long long>(blockIdx.x) >= ctas;
-  // first tile of CTA c (64-bit divisions cost some 100 clocks each)
-  auto share = [&](int c) -> long long {
-    if (total < 1 << 23) return static_cast<unsigned>(total) * static_cast<unsigned>(c) / static_cast<unsigned>(ctas);
+  // (shares of a tile's cost or more: a unit's parts lie in consecutive CTAs)
+  const bool small = total < 1 << 23;   // (64-bit divisions cost some 100 clocks each)
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total / TC));
+  const bool idle = static_cast<int>(blockIdx.x) >= ctas;
+  auto share = [&](int c) -> long long {   // first position of CTA c
+    if (small) return static_cast<unsigned>(total) * static_cast<unsigned>(c) / static_cast<unsigned>(ctas);
     return total * c / ctas;
+  };
+  auto cta_of = [&](long long x) -> int {  // the CTA that holds position x
+    if (small) return (static_cast<unsigned>(x + 1) * static_cast<unsigned>(ctas) - 1) / static_cast<unsigned>(total);
+    return static_cast<int>(((x + 1) * ctas - 1) / total);
   };
   const long long from = idle ? 0 : share(blockIdx.x);
   const long long count = idle ? 0 : share(blockIdx.x + 1) - from;
+  // The piece of a unit's tiles [t0, t0 + n).
+  auto make_piece = [&](const PagedSeq& s, int b, int j, int q, const PagedUnit& u, int t0, int n) -> Piece {
+    Piece pc;
+    pc.b = b;
+    pc.j = j;
+    pc.i0 = q << p.ts;
+    pc.row0 = s.row0 + pc.i0;
+    pc.ntok = min(1 << p.ts, s.n - pc.i0);
+    pc.n = s.n;
+    pc.len = s.len;
+    pc.lo = u.lo;
+    pc.hi = u.hi;
+    pc.tile0 = u.tile0 + t0;
+    pc.tiles = n;
+    pc.ends = (t0 == 0 ? 1 : 0) | (t0 + n == u.tiles ? 2 : 0);
+    return pc;
+  };
   if (!idle && from < upto && from >= upto - mine) {
     long long off = from - (upto - mine);
     int b = tid * per;
     while (per > 1) {
       seq = paged_seq(batch, b, p.status);
-      const long long n = seq_tiles(seq);
+      const long long n = p.H_kv * head_cost(seq);
       if (off < n || b + 1 >= batch.B) break;
       off -= n;
       ++b;
@@ -269,11 +321,26 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     sh.start_b = b;
     sh.start_off = off;
     sh.start_seq = seq;
+    if constexpr (ONE) {   // the first piece at once: a step waits for it
+      const PagedUnit u = paged_unit(seq.len, seq.n, p.window, tree, p.ts, 0);
+      const int cost = u.tiles * TC + UC;
+      const int j = static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(cost));
+      const int o = static_cast<int>(off) - j * cost;
+      const int o1 = static_cast<int>(min(o + count, static_cast<long long>(cost)));
+      const int t0 = tile_at(o), n = tile_at(o1) - t0;
+      if (n > 0) {
+        sh.piece[0] = make_piece(seq, b, j, 0, u, t0, n);
+        sh.first_used = o1 - o;
+        sh.first_j = j;
+        mbar_arrive(smem_u32(&sh.piece_full[0]));
+      }
+    }
   }
   __syncthreads();
 
+  int lost_site = 0;
   auto wait_warp = [&](uint64_t& bar, uint32_t parity, int site) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, &sh.abort_flag, p.status, site));
+    return __all_sync(0xffffffffu, wait_bar(smem_u32(&bar), parity, &sh.abort_flag, site, &lost_site));
   };
   // The next piece (whole warp); false at the end.
   auto take = [&](int k, Piece& pc) -> bool {
@@ -285,7 +352,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   };
 
   if (warp < 4) {
-    if constexpr (NQ == 2) regs_decrease<C::REGS_CTRL>();
+    regs_decrease<C::REGS_CTRL>();
     if (warp == 2) {
       // ---------------- pieces
       Split split = {0, 0, 0, 0};
@@ -302,6 +369,10 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         }
         ++k;
       };
+      // A unit of this CTA that ends in another one (start: its position).
+      auto cut = [&](const Piece& pc, long long start, int tiles) {
+        split = {pc.row0, pc.ntok, pc.j, cta_of(start + UC + (tiles - 1) * TC) - static_cast<int>(blockIdx.x) + 1};
+      };
       while (ok && left > 0 && b < batch.B) {
         PagedSeq s = sh.start_seq;
         if (!first) {
@@ -314,62 +385,69 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
           s.n = __shfl_sync(0xffffffffu, win.n, b - b0);
           s.len = __shfl_sync(0xffffffffu, win.len, b - b0);
         }
-        first = false;
-        int q = 0, j = 0, nq = 1;
-        long long t = off;
-        if (p.one) {        // every sequence is one unit per head
-          const int head = s.n > 0 ? paged_unit(s.len, s.n, p.window, tree, p.ts, 0).tiles : 0;
-          if (head == 0) {
-            ++b;
-            continue;
-          }
-          if (off > 0) {    // (inside the first sequence)
-            j = static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(head));
-            t = off - j * head;
+        int q = 0, j = 0, nq = 1, o = 0;   // unit and position in it
+        if constexpr (ONE) {
+          if (first && sh.first_used > 0) {
+            // its first piece is there; it ends the unit or the CTA's share
+            const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, 0);
+            if (sh.piece[0].ends == 1)
+              cut(sh.piece[0], pos - off + static_cast<long long>(sh.first_j) * (u.tiles * TC + UC), u.tiles);
+            left -= sh.first_used;
+            pos += sh.first_used;
+            j = sh.first_j + 1;
+            k = 1;
+          } else {
+            if (s.n == 0) {
+              ++b;
+              continue;
+            }
+            if (off > 0) {    // (inside the first sequence)
+              const long long cost = head_cost(s);
+              j = static_cast<int>(off / cost);
+              o = static_cast<int>(off - j * cost);
+            }
           }
         } else {
+          // the unit of a head's position t: the last one that starts at or before it
           nq = paged_units(s.n, p.ts);
-          const long long head = paged_prefix(s.len, s.n, p.window, tree, p.ts, nq);
+          int q1 = nq, at = nq;
+          long long head = 0, start = 0, t = 0;
+#pragma unroll 1
+          while (true) {
+            const long long to = TC * paged_prefix(s.len, s.n, p.window, tree, p.ts, at) + static_cast<long long>(UC) * at;
+            if (head == 0) {
+              if (to == 0) break;
+              head = to;
+              j = static_cast<int>(off / head);
+              t = off - j * head;
+            } else if (to <= t) {
+              q = at;
+              start = to;
+            } else {
+              q1 = at;
+            }
+            if (q1 - q <= 1) break;
+            at = (q + q1) / 2;
+          }
           if (head == 0) {
             ++b;
             continue;
           }
-          j = static_cast<int>(off / head);
-          t = off - j * head;
-          int q1 = nq;      // the unit of tile t: the last one that starts at or before it
-          while (q1 - q > 1) {
-            const int mid = (q + q1) / 2;
-            if (paged_prefix(s.len, s.n, p.window, tree, p.ts, mid) <= t) q = mid;
-            else q1 = mid;
-          }
-          t -= paged_prefix(s.len, s.n, p.window, tree, p.ts, q);
+          o = static_cast<int>(t - start);
         }
+        first = false;
         while (ok && left > 0 && j < p.H_kv) {
           const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, q);
-          const int n = static_cast<int>(min(left, static_cast<long long>(u.tiles) - t));
-          Piece pc;
-          pc.b = b;
-          pc.j = j;
-          pc.i0 = q << p.ts;
-          pc.row0 = s.row0 + pc.i0;
-          pc.ntok = min(1 << p.ts, s.n - pc.i0);
-          pc.n = s.n;
-          pc.len = s.len;
-          pc.lo = u.lo;
-          pc.hi = u.hi;
-          pc.tile0 = u.tile0 + static_cast<int>(t);
-          pc.tiles = n;
-          pc.ends = (t == 0 ? 1 : 0) | (t + n == u.tiles ? 2 : 0);
-          if (pc.ends == 1) {   // (pos is the unit's first tile)
-            const long long end = pos + u.tiles;
-            const int last = total < 1 << 23 ? (static_cast<unsigned>(end) * static_cast<unsigned>(ctas) - 1) / static_cast<unsigned>(total)
-                                             : static_cast<int>((end * ctas - 1) / total);
-            split = {pc.row0, pc.ntok, j, last - static_cast<int>(blockIdx.x) + 1};
+          const int o1 = static_cast<int>(min(o + left, static_cast<long long>(u.tiles) * TC + UC));
+          const int t0 = tile_at(o), n = tile_at(o1) - t0;
+          if (n > 0) {
+            const Piece pc = make_piece(s, b, j, q, u, t0, n);
+            if (pc.ends == 1) cut(pc, pos - o, u.tiles);
+            publish(pc);
           }
-          publish(pc);
-          left -= n;
-          pos += n;
-          t = 0;
+          left -= o1 - o;
+          pos += o1 - o;
+          o = 0;
           if (++q == nq) {
             q = 0;
             ++j;
@@ -385,6 +463,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       const int ps = batch.page_shift, box = min(1 << ps, 64);   // slots per box
       const int nbox = 256 / box;                                // boxes of a part
       const int pool = batch.n_pages << ps;
+      constexpr int AHEAD = 3;                                   // tiles that are pulled into L2 before
       Ring w;
       int issued = 0;
       // tile `tile` of a piece: lane k's `base` is the pool row of its page k
@@ -412,96 +491,122 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         ++issued;
         return true;
       };
+      // K and V of a tile into L2, some tiles before the ring has room for them.
+      auto prefetch = [&](int j, int tile, int base) {
+        const int so = (lane >> 1) % (BN / box) * box;
+        const int row0 = __shfl_sync(0xffffffffu, base, ps < 7 ? so >> ps : 0);
+        if ((lane >> 1) < BN / box && row0 >= 0) {
+          const int row = row0 + ((tile * BN + so) & ((1 << ps) - 1));
+          for (int c = 0; c < DH; c += 64) prefetch_3d(lane & 1 ? &tmV : &tmK, c, j, row);
+        }
+      };
+      // A step: K of the next tile, then V of the one before (the first step
+      // has no V, the last no K).
       bool ok = true;
       int pj = 0, ptile = -1, pbase = 0;   // the tile whose V is still to come
       Piece pc;
-      for (int k = 0; ok && take(k, pc); ++k) {
-        // page ids of the piece, 32 at a time: lane l holds entry first + l
-        const int32_t* table = batch.page_table + static_cast<size_t>(pc.b) * batch.max_pages;
-        const int p_end = ((pc.hi - 1) >> ps) + 1;               // pages that hold visible slots
-        auto entries = [&](int first) -> int {
-          const int at = first + lane;
-          if (at >= p_end) return -1;
-          const int id = __ldcg(table + at);
-          if (static_cast<unsigned>(id) >= static_cast<unsigned>(batch.n_pages)) {
-            record_error(p.status, kDevErrBadPaged);
-            return -1;
-          }
-          return id << ps;
-        };
-        int first = (pc.tile0 * BN) >> ps;
-        int cur = entries(first), ahead = entries(first + 32);
-        for (int i = 0; i < pc.tiles; ++i) {
-          const int tile = pc.tile0 + i, at = (tile * BN) >> ps;
-          if (at >= first + 32) {
-            first += 32;
-            cur = ahead;
-            ahead = entries(first + 32);
-          }
-          const int base = __shfl_sync(0xffffffffu, cur, (at - first + (lane & 7)) & 31);
-          for (int part = 0; ok && part < C::PARTS; ++part) ok = load_part(false, part, pc.j, tile, base);
-          for (int part = 0; ok && ptile >= 0 && part < C::PARTS; ++part)
-            ok = load_part(true, part, pj, ptile, pbase);
-          if (!ok) break;
-          pj = pc.j;
-          ptile = tile;
-          pbase = base;
+      pc.tiles = 0;
+      int k = 0, i = 0, p_end = 0, first = 0, cur = 0, ahead = 0;
+      const int32_t* table = nullptr;
+      // page ids, 32 at a time: lane l holds entry first + l of the sequence
+      auto entries = [&](int from) -> int {
+        const int at = from + lane;
+        if (at >= p_end) return -1;
+        const int id = __ldcg(table + at);
+        if (static_cast<unsigned>(id) >= static_cast<unsigned>(batch.n_pages)) {
+          record_error(p.status, kDevErrBadPaged);
+          return -1;
         }
+        return id << ps;
+      };
+#pragma unroll 1
+      while (ok) {
+        bool more = true, fresh = false;
+        if (i == pc.tiles) {
+          more = take(k++, pc);
+          i = 0;
+          if (more) {
+            table = batch.page_table + static_cast<size_t>(pc.b) * batch.max_pages;
+            p_end = ((pc.hi - 1) >> ps) + 1;             // pages that hold visible slots
+            first = ((pc.tile0 * BN) >> ps) - 32;
+            fresh = true;
+          }
+        }
+        const int tile = pc.tile0 + i, at = (tile * BN) >> ps;
+        if (more && at >= first + 32) {
+          first += 32;
+          cur = fresh ? entries(first) : ahead;
+          ahead = entries(first + 32);
+        }
+        const int base = __shfl_sync(0xffffffffu, cur, (at - first + (lane & 7)) & 31);
+#pragma unroll 1
+        for (int x = more ? 0 : C::PARTS; ok && x < (ptile >= 0 ? 2 * C::PARTS : C::PARTS); ++x) {
+          const bool v = x >= C::PARTS;
+          ok = load_part(v, v ? x - C::PARTS : x, v ? pj : pc.j, v ? ptile : tile, v ? pbase : base);
+        }
+        if (!more) break;
+        if (!ONE && i + AHEAD < pc.tiles) {
+          const int to = (((tile + AHEAD) * BN) >> ps) - first + (lane & 7);   // (page ids are there for 32 to 63 entries)
+          const int a = __shfl_sync(0xffffffffu, cur, to & 31), z = __shfl_sync(0xffffffffu, ahead, to & 31);
+          prefetch(pc.j, tile + AHEAD, to < 32 ? a : z);
+        }
+        pj = pc.j;
+        ptile = tile;
+        pbase = base;
+        ++i;
       }
-      for (int part = 0; ok && ptile >= 0 && part < C::PARTS; ++part)
-        ok = load_part(true, part, pj, ptile, pbase);
       // Every issued load lands before the CTA may exit.
       for (int n = max(0, issued - C::NP); n < issued; ++n)
         mbar_wait_drain(smem_u32(&sh.part_full[n % C::NP]), (n / C::NP) & 1);
     } else if (warp == 3) {
-      // ---------------- Q
-      int nload = 0;
+      // ---------------- Q: few rows (qsmall) in two buffers, a piece ahead
+      int k = 0;
       Piece pc;
-      for (int k = 0; take(k, pc); ++k) {
-        if (nload > 0 && !wait_warp(sh.q_empty, (nload - 1) & 1, kSiteQEmpty)) break;
+      for (; take(k, pc); ++k) {
+        const int buf = p.qsmall ? k & 1 : 0, fill = p.qsmall ? k >> 1 : k;
+        if (fill > 0 && !wait_warp(sh.q_empty[buf], (fill - 1) & 1, kSiteQEmpty)) break;
         if (lane == 0) {
           const int tq1 = BM >> p.gshift, nq = NQ == 2 && pc.ntok > tq1 ? 2 : 1;
-          const uint32_t bar = smem_u32(&sh.q_full);
+          const uint32_t bar = smem_u32(&sh.q_full[buf]), dst = smem_u32(sQ) + buf * (C::QT_BYTES / 2);
           mbar_arrive_expect_tx(bar, nq * C::NCH * ((p.tokbox * 128) << p.gshift));
           for (int e = 0; e < nq; ++e)
             for (int ch = 0; ch < C::NCH; ++ch)
-              tma_load_3d(smem_u32(sQ + e * C::QT_BYTES + ch * CHUNK), &tmQ, bar, ch * 64,
+              tma_load_3d(dst + e * C::QT_BYTES + ch * (p.qsmall ? QSMALL : CHUNK), &tmQ, bar, ch * 64,
                           pc.j << p.gshift, pc.row0 + e * tq1);
         }
-        ++nload;
       }
-      if (nload > 0) mbar_wait_drain(smem_u32(&sh.q_full), (nload - 1) & 1);
+      // (every load that was issued lands before the CTA may exit)
+      for (int i = max(0, k - (p.qsmall ? 2 : 1)); i < k; ++i)
+        mbar_wait_drain(smem_u32(&sh.q_full[p.qsmall ? i & 1 : 0]), (p.qsmall ? i >> 1 : i) & 1);
     } else {
       // ---------------- MMA issue (whole warp, one elected lane)
       const uint32_t lead = elect_one();
       constexpr uint32_t idesc_qk = idesc_f16(BM, BN, /*f16*/ 0, 0, 0);
       constexpr uint32_t idesc_pv = idesc_f16(BM, DH, /*f16*/ 0, 0, /*B MN-major*/ 1);
-      const uint32_t q_addr = smem_u32(sQ);
+      const uint32_t q_stride = p.qsmall ? QSMALL : CHUNK;
       Ring r;
       int g = 0;              // tiles whose S was issued
       int ge[2] = {0, 0};     // NQ = 2: the same of each query tile
       int pieces_e[2] = {0, 0};   // pieces whose first PV was issued
-      // S of a tile; for d_h = 256 its two parts are the channel halves.
-      auto issue_s = [&](int nq, bool last) -> bool {
+      // NQ = 1: S of a tile; for d_h = 256 its two parts are the channel halves.
+      auto issue_s = [&](int g, uint32_t q_addr, uint64_t* q_done) -> bool {
+#pragma unroll 1
         for (int part = 0; part < C::PARTS; ++part) {
           if (!wait_warp(sh.part_full[r.slot], r.phase, kSitePartFull)) return false;
           tc_fence_after();
           const uint32_t kb = smem_u32(sP + r.slot * PART);
-          for (int e = 0; e < nq; ++e) {
-            const uint32_t d = tbase + (NQ == 2 ? e : (g & 1)) * 128;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t off = (k >> 2) * CHUNK + (k & 3) * 32;
-              mma_ss_lead(lead, d, sdesc_sw128(q_addr + e * C::QT_BYTES + part * 2 * CHUNK + off, 16, 1024),
-                          sdesc_sw128(kb + off, 16, 1024), idesc_qk, part > 0 || k > 0 ? 1u : 0u);
-            }
-            if (NQ == 2 && e + 1 < nq) mma_commit_lead(lead, smem_u32(&sh.s_full[e]));
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t off = (k >> 2) * CHUNK + (k & 3) * 32;
+            mma_ss_lead(lead, tbase + (g & 1) * 128,
+                        sdesc_sw128(q_addr + (part * 2 + (k >> 2)) * q_stride + (k & 3) * 32, 16, 1024),
+                        sdesc_sw128(kb + off, 16, 1024), idesc_qk, part > 0 || k > 0 ? 1u : 0u);
           }
           mma_commit_lead(lead, smem_u32(&sh.part_empty[r.slot]));
           r.next<C::NP>();
         }
-        mma_commit_lead(lead, smem_u32(&sh.s_full[NQ == 2 ? nq - 1 : (g & 1)]));
-        if (last) mma_commit_lead(lead, smem_u32(&sh.q_empty));
+        mma_commit_lead(lead, smem_u32(&sh.s_full[g & 1]));
+        if (q_done != nullptr) mma_commit_lead(lead, smem_u32(q_done));
         return true;
       };
       struct Pv {             // what the PV of a tile needs
@@ -517,16 +622,19 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
                       !first || part > 0 || k > 0 ? 1u : 0u);
       };
       // V of the part in slot r, zeroed outside [lo, hi).
-      auto v_ready = [&](const Pv& t, int part) -> bool {
+      auto v_ready = [&](const Pv& t, int part, const Ring& r) -> bool {
         if (!wait_warp(sh.part_full[r.slot], r.phase, kSitePartFull)) return false;
         constexpr int ROWS = 128 / C::PARTS;
         const int s0 = t.tile * BN + part * ROWS;
         if (s0 < t.lo || s0 + ROWS > t.hi) {
           uint8_t* base = sP + r.slot * PART;
           const int z = min(max(t.lo - s0, 0), ROWS), a = min(max(t.hi - s0, 0), ROWS);
+#pragma unroll 1
           for (int c = 0; c < static_cast<int>(PART) / (ROWS * 128); ++c) {
             uint4* rows = reinterpret_cast<uint4*>(base + c * ROWS * 128);
+#pragma unroll 1
             for (int i = lane; i < z * 8; i += 32) rows[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
             for (int i = a * 8 + lane; i < ROWS * 8; i += 32) rows[i] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
@@ -545,8 +653,9 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       // NQ = 1: the PV of tile number n.
       auto issue_pv1 = [&](const Pv& t, int n) -> bool {
         if (!pv_begin(t, 0) || !wait_warp(sh.p_full[n & 1], (n >> 1) & 1, kSitePFull)) return false;
+#pragma unroll 1
         for (int part = 0; part < C::PARTS; ++part) {
-          if (!v_ready(t, part)) return false;
+          if (!v_ready(t, part, r)) return false;
           mma_pv(0, n & 1, smem_u32(sP + r.slot * PART), part, t.first);
           mma_commit_lead(lead, smem_u32(&sh.part_empty[r.slot]));
           r.next<C::NP>();
@@ -555,220 +664,98 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         if (t.last) mma_commit_lead(lead, smem_u32(&sh.o_final[0]));
         return true;
       };
+      // A step: S of the next tile, then PV of the one before (the first step
+      // has no PV, the last no S).
       bool ok = true, pending = false;
       Pv prev = {};
       Piece pc;
-      for (int k = 0; ok && take(k, pc); ++k) {
-        const int nq = NQ == 2 && pc.ntok > (BM >> p.gshift) ? 2 : 1;
-        ok = wait_warp(sh.q_full, k & 1, kSiteQFull);
-        for (int i = 0; ok && i < pc.tiles; ++i) {
-          const Pv cur = {pc.tile0 + i, pc.lo, pc.hi, nq, i == 0, i + 1 == pc.tiles};
-          if constexpr (NQ == 1) {
-            ok = issue_s(1, cur.last);
+      int k = 0, i = 0;       // pieces taken, tiles of the present one done
+      int qbuf = 0;
+      pc.tiles = 0;
+#pragma unroll 1
+      while (ok) {
+        bool more = true;
+        if (i == pc.tiles) {
+          more = take(k, pc);
+          if (more) {
+            qbuf = p.qsmall ? k & 1 : 0;
+            ok = wait_warp(sh.q_full[qbuf], (p.qsmall ? k >> 1 : k) & 1, kSiteQFull);
+          }
+          ++k;
+          i = 0;
+        }
+        if (!ok || (!more && (!pending || sh.abort_flag))) break;
+        const int nq = more ? (NQ == 2 && pc.ntok > (BM >> p.gshift) ? 2 : 1) : 0;
+        const Pv cur = {pc.tile0 + i, pc.lo, pc.hi, nq, i == 0, i + 1 == pc.tiles};
+        if constexpr (NQ == 1) {
+          if (more) {
+            ok = issue_s(g, smem_u32(sQ) + qbuf * (C::QT_BYTES / 2), cur.last ? &sh.q_empty[qbuf] : nullptr);
+            if (!ok) break;
             ++g;
-            if (ok && pending) ok = issue_pv1(prev, g - 2);
-          } else {
-            // S_e reuses the columns of P_e of the tile before, whose V comes
-            // behind this tile's K in the ring: both are waited for first.
-            Ring kr = r;
-            if (!wait_warp(sh.part_full[kr.slot], kr.phase, kSitePartFull)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t kb = smem_u32(sP + kr.slot * PART);
-            r.next<C::NP>();
-            uint32_t vb = 0;
-            if (pending) {
-              ok = v_ready(prev, 0);
-              if (!ok) break;
-              vb = smem_u32(sP + r.slot * PART);
-            }
-            for (int e = 0; ok && e < 2; ++e) {
-              if (pending && e < prev.nq) {
-                ok = pv_begin(prev, e) && wait_warp(sh.p_full[e], (ge[e] - 1) & 1, kSitePFull);
-                if (!ok) break;
-                tc_fence_after();
-                mma_pv(e, e, vb, 0, prev.first);
-                if (prev.last) mma_commit_lead(lead, smem_u32(&sh.o_final[e]));
-              }
-              if (pending && e + 1 == prev.nq) mma_commit_lead(lead, smem_u32(&sh.part_empty[r.slot]));
-              if (e < nq) {
+          }
+          if (pending) ok = issue_pv1(prev, g - (more ? 2 : 1));
+        } else {
+          // S_e reuses the columns of P_e of the tile before, whose V comes
+          // behind this tile's K in the ring.
+          const Ring kr = r;
+          if (more) r.next<C::NP>();
+          if (pending) ok = v_ready(prev, 0, r);
+          if (!ok) break;
+          const uint32_t kb = smem_u32(sP + kr.slot * PART), vb = smem_u32(sP + r.slot * PART);
+          const uint32_t q_addr = smem_u32(sQ);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  const uint32_t off = (c >> 2) * CHUNK + (c & 3) * 32;
-                  mma_ss_lead(lead, tbase + e * 128, sdesc_sw128(q_addr + e * C::QT_BYTES + off, 16, 1024),
-                              sdesc_sw128(kb + off, 16, 1024), idesc_qk, c > 0 ? 1u : 0u);
-                }
-                mma_commit_lead(lead, smem_u32(&sh.s_full[e]));
-                ++ge[e];
+          for (int e = 0; e < 2; ++e) {
+            if (pending && e < prev.nq) {
+              ok = pv_begin(prev, e) && wait_warp(sh.p_full[e], (ge[e] - 1) & 1, kSitePFull);
+              if (!ok) break;
+              tc_fence_after();
+              mma_pv(e, e, vb, 0, prev.first);
+              if (prev.last) mma_commit_lead(lead, smem_u32(&sh.o_final[e]));
+              if (e + 1 == prev.nq) mma_commit_lead(lead, smem_u32(&sh.part_empty[r.slot]));
+            }
+            if (e == 0 && more) {
+              ok = wait_warp(sh.part_full[kr.slot], kr.phase, kSitePartFull);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            if (e < nq) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const uint32_t off = (c >> 2) * CHUNK + (c & 3) * 32;
+                mma_ss_lead(lead, tbase + e * 128, sdesc_sw128(q_addr + e * C::QT_BYTES + off, 16, 1024),
+                            sdesc_sw128(kb + off, 16, 1024), idesc_qk, c > 0 ? 1u : 0u);
               }
+              mma_commit_lead(lead, smem_u32(&sh.s_full[e]));
+              ++ge[e];
               if (e + 1 == nq) {
                 mma_commit_lead(lead, smem_u32(&sh.part_empty[kr.slot]));
-                if (cur.last) mma_commit_lead(lead, smem_u32(&sh.q_empty));
+                if (cur.last) mma_commit_lead(lead, smem_u32(&sh.q_empty[0]));
               }
             }
-            if (pending) r.next<C::NP>();
           }
-          prev = cur;
-          pending = true;
+          if (pending) r.next<C::NP>();
         }
-      }
-      if (ok && pending) {
-        if constexpr (NQ == 1) {
-          ok = issue_pv1(prev, g - 1);
-        } else {
-          ok = v_ready(prev, 0);
-          for (int e = 0; ok && e < prev.nq; ++e) {
-            ok = pv_begin(prev, e) && wait_warp(sh.p_full[e], (ge[e] - 1) & 1, kSitePFull);
-            if (!ok) break;
-            tc_fence_after();
-            mma_pv(e, e, smem_u32(sP + r.slot * PART), 0, prev.first);
-            mma_commit_lead(lead, smem_u32(&sh.o_final[e]));
-          }
-        }
+        if (!more) break;
+        prev = cur;
+        pending = true;
+        ++i;
       }
       mma_commit_lead(lead, smem_u32(&sh.drain));
       mbar_wait_drain(smem_u32(&sh.drain), 0);
     }
   } else {
-    // ---------------- softmax of query tile e: thread r owns row r
-    if constexpr (NQ == 2) regs_increase<C::REGS_SOFT>();
-    const int e = (warp - 4) >> 2;
+    // ---------------- softmax of query tile e (thread r owns row r), epilogue
+    const int e = NQ == 2 ? (warp - 4) >> 2 : 0;
     const int q = warp & 3;                // TMEM lane quarter
     const int r = q * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t o_base = tbase + lane_off + O_COL + e * 128;
     const int tq1 = BM >> p.gshift, tok = (e * BM + r) >> p.gshift;   // token of the unit
-    int g = 0, np = 0;                     // tiles and pieces of this query tile so far
-    bool ok = true;
-    Piece pc;
-    for (int k = 0; ok && take(k, pc); ++k) {
-      if (pc.ntok <= e * tq1) continue;    // no such query tile in the unit
+    // This row of a piece's O; np: the pieces before.
+    auto epilogue = [&](const Piece& pc, float m_used, float l, int np) -> bool {
+      if (!wait_warp(sh.o_final[e], np & 1, kSiteOFinal)) return false;
       const bool row_valid = tok < pc.ntok;
       const bool live = __any_sync(0xffffffffu, row_valid);
-      const int i_tok = pc.i0 + tok;       // number among the sequence's new tokens
-      // Visible slots of the row: [v_lo, v_hi], and with a tree the ones of
-      // `family` from slot len on.
-      int v_lo = 0, v_hi = pc.len + i_tok;
-      uint64_t family = 0;
-      int t_lo = 0;                        // tiles from t_lo to t_hi are seen whole by every row
-      if (live && tree) {
-        const PagedSeq s = {pc.row0 - pc.i0, pc.n, pc.len};
-        const Ancestors a = paged_ancestors(batch, s, lane, p.status);
-        const int it = min(i_tok, kTreeMax - 1);
-        family = a.of(it);
-        const int at = pc.len + __popcll(family) - 1;            // position
-        v_hi = pc.len - 1;
-        if (p.window > 0) {
-          v_lo = at - p.window + 1;
-          if (p.window < kTreeMax) {       // ancestors fewer than `window` steps away
-            family = 1ull << it;
-            int up = a.parent_of(it);
-            for (int d = 1; d < p.window; ++d) {
-              if (up >= 0) family |= 1ull << up;
-              const int next = a.parent_of(max(up, 0));
-              up = up >= 0 ? next : -1;
-            }
-          }
-        }
-      } else if (p.window > 0) {
-        v_lo = pc.len + i_tok - p.window + 1;
-      }
-      t_lo = __reduce_max_sync(0xffffffffu, row_valid ? v_lo : 0);
-      const int t_hi = __reduce_min_sync(0xffffffffu, row_valid ? v_hi : 0x7fffffff);
-      float m_used = -INFINITY, l = 0.f;
-      for (int i = 0; i < pc.tiles; ++i, ++g) {
-        const int sb = NQ == 2 ? e : (g & 1);
-        const uint32_t s_addr = tbase + lane_off + sb * 128;
-        ok = wait_warp(sh.s_full[sb], NQ == 2 ? (g & 1) : ((g >> 1) & 1), kSiteSFull);
-        if (!ok) break;
-        if (live) {
-          tc_fence_after();
-          const int s_tile = (pc.tile0 + i) * BN;
-          uint32_t ra[32], rb[32], rc[32], rd[32];
-          float m0, m1, m2, m3;
-          tmem_ld32_max(s_addr, ra, m0);
-          tmem_ld32_max(s_addr + 32, rb, m1);
-          tmem_ld32_max(s_addr + 64, rc, m2);
-          tmem_ld32_max(s_addr + 96, rd, m3);
-          tmem_ld_wait(ra);
-          tmem_ld_wait(rb);
-          tmem_ld_wait(rc);
-          tmem_ld_wait(rd);
-          tmem_ld_wait(m0);
-          tmem_ld_wait(m1);
-          tmem_ld_wait(m2);
-          tmem_ld_wait(m3);
-          if (s_tile < t_lo || s_tile + BN - 1 > t_hi) {
-            uint32_t keep[4];
-            const int a = v_lo - s_tile, z = v_hi - s_tile, d = s_tile - pc.len;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              keep[c] = bits_from_to(a - 32 * c, z - 32 * c);
-              if (tree) keep[c] |= bits_at(family, d + 32 * c);
-            }
-            m0 = mask_max(ra, keep[0]);
-            m1 = mask_max(rb, keep[1]);
-            m2 = mask_max(rc, keep[2]);
-            m3 = mask_max(rd, keep[3]);
-          }
-          const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * LOG2E;
-          const bool grow = mx > m_used + (RESCALE_THRESHOLD + P_SHIFT);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float m_new = grow ? mx - P_SHIFT : m_used;
-            const float factor = (m_new == m_used) ? 1.f : ex2(m_used - m_new);
-            if (i > 0) {
-              // O holds the PV of the tiles before: with two query tiles S_e
-              // of this tile was issued after them, with one PV may still run.
-              if constexpr (NQ == 1) {
-                ok = wait_warp(sh.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, kSitePvDone);
-                if (!ok) break;
-                tc_fence_after();
-              }
-#pragma unroll 1
-              for (int c = 0; c < DH / 32; ++c) {
-                uint32_t ro[32];
-                tmem_ld32(o_base + c * 32, ro);
-                tmem_ld_wait(ro);
-#pragma unroll
-                for (int x = 0; x < 32; ++x) ro[x] = __float_as_uint(__uint_as_float(ro[x]) * factor);
-                tmem_st32(o_base + c * 32, ro);
-              }
-              tmem_st_wait();
-            }
-            l *= factor;
-            m_used = m_new;
-          }
-          const float mref = (m_used == -INFINITY) ? 0.f : m_used;
-          const float2 l2e = make_float2(LOG2E, LOG2E), negm = make_float2(-mref, -mref);
-          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                           make_float2(0.f, 0.f)};
-          {
-            uint32_t pk[32];
-            exp_pack(ra, pk, acc, l2e, negm);
-            exp_pack(rb, pk + 16, acc, l2e, negm);
-            tmem_st32(s_addr, pk);
-          }
-          {
-            uint32_t pk[32];
-            exp_pack(rc, pk, acc, l2e, negm);
-            exp_pack(rd, pk + 16, acc, l2e, negm);
-            tmem_st32(s_addr + 32, pk);
-          }
-          const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
-          const float2 a = __fadd2_rn(a01, a23);
-          l += a.x + a.y;
-          tmem_st_wait();
-          tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[sb]));
-      }
-      // ---------------- epilogue: this row of O
-      if (ok) ok = wait_warp(sh.o_final[e], np & 1, kSiteOFinal);
-      ++np;
-      if (!ok) break;
       if (live) {
         tc_fence_after();
         const bool whole = pc.ends == 3, have = row_valid && l != 0.f;
@@ -800,8 +787,164 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.o_free[e]));
+      return true;
+    };
+    int g = 0, np = 0;                     // tiles and pieces of this query tile so far
+    bool ok = true;
+    Piece pc;
+    if (NQ == 1 && warp >= 8) {
+      regs_increase<C::REGS_OTHER>();
+      for (; ok && take(np, pc); ++np) {
+        ok = wait_warp(sh.stat_full[np & 1], (np >> 1) & 1, kSiteStatFull);
+        if (!ok) break;
+        const float2 st = sh.stat[np & 1][r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.stat_empty[np & 1]));
+        ok = epilogue(pc, st.x, st.y, np);
+      }
+    } else {
+      regs_increase<C::REGS_SOFT>();
+      for (int k = 0; ok && take(k, pc); ++k) {
+        if (pc.ntok <= e * tq1) continue;    // no such query tile in the unit
+        const bool row_valid = tok < pc.ntok;
+        const bool live = __any_sync(0xffffffffu, row_valid);
+        float m_used = -INFINITY, l = 0.f;
+        const int i_tok = pc.i0 + tok;       // number among the sequence's new tokens
+        // Visible slots of the row: [v_lo, v_hi], and with a tree the ones of
+        // `family` from slot len on.
+        int v_lo = 0, v_hi = pc.len + i_tok;
+        uint64_t family = 0;
+        if (live && tree) {
+          const PagedSeq s = {pc.row0 - pc.i0, pc.n, pc.len};
+          const Ancestors a = paged_ancestors(batch, s, lane, p.status);
+          const int it = min(i_tok, kTreeMax - 1);
+          family = a.of(it);
+          const int at = pc.len + __popcll(family) - 1;            // position
+          v_hi = pc.len - 1;
+          if (p.window > 0) {
+            v_lo = at - p.window + 1;
+            if (p.window < kTreeMax) {       // ancestors fewer than `window` steps away
+              family = 1ull << it;
+              int up = a.parent_of(it);
+              for (int d = 1; d < p.window; ++d) {
+                if (up >= 0) family |= 1ull << up;
+                const int next = a.parent_of(max(up, 0));
+                up = up >= 0 ? next : -1;
+              }
+            }
+          }
+        } else if (p.window > 0) {
+          v_lo = pc.len + i_tok - p.window + 1;
+        }
+        // tiles within [t_lo, t_hi] are seen whole by every row
+        const int t_lo = __reduce_max_sync(0xffffffffu, row_valid ? v_lo : 0);
+        const int t_hi = __reduce_min_sync(0xffffffffu, row_valid ? v_hi : 0x7fffffff);
+        for (int i = 0; i < pc.tiles; ++i, ++g) {
+          const int sb = NQ == 2 ? e : (g & 1);
+          const uint32_t s_addr = tbase + lane_off + sb * 128;
+          ok = wait_warp(sh.s_full[sb], NQ == 2 ? (g & 1) : ((g >> 1) & 1), kSiteSFull);
+          if (!ok) break;
+          if (live) {
+            tc_fence_after();
+            const int s_tile = (pc.tile0 + i) * BN;
+            if (s_tile < t_lo || s_tile + BN - 1 > t_hi) {
+              // hidden columns become -inf in place (rolled: a few tiles of a
+              // unit run this, and the softmax's own code stays small)
+#pragma unroll 1
+              for (int c = 0; c < BN; c += 32) {
+                uint32_t x[32];
+                tmem_ld32(s_addr + c, x);
+                uint32_t keep = bits_from_to(v_lo - s_tile - c, v_hi - s_tile - c);
+                if (tree) keep |= bits_at(family, s_tile + c - pc.len);
+                tmem_ld_wait(x);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (!((keep >> k) & 1u)) x[k] = 0xff800000u;
+                tmem_st32(s_addr + c, x);
+              }
+              tmem_st_wait();
+            }
+            uint32_t ra[32], rb[32], rc[32], rd[32];
+            float m0, m1, m2, m3;
+            tmem_ld32_max(s_addr, ra, m0);
+            tmem_ld32_max(s_addr + 32, rb, m1);
+            tmem_ld32_max(s_addr + 64, rc, m2);
+            tmem_ld32_max(s_addr + 96, rd, m3);
+            tmem_ld_wait(ra);
+            tmem_ld_wait(rb);
+            tmem_ld_wait(rc);
+            tmem_ld_wait(rd);
+            tmem_ld_wait(m0);
+            tmem_ld_wait(m1);
+            tmem_ld_wait(m2);
+            tmem_ld_wait(m3);
+            const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * LOG2E;
+            const bool grow = mx > m_used + (RESCALE_THRESHOLD + P_SHIFT);
+            if (__any_sync(0xffffffffu, grow)) {
+              const float m_new = grow ? mx - P_SHIFT : m_used;
+              const float factor = (m_new == m_used) ? 1.f : ex2(m_used - m_new);
+              if (i > 0) {
+                // O holds the PV of the tiles before: with two query tiles S_e
+                // of this tile was issued after them, with one PV may still run.
+                if constexpr (NQ == 1) {
+                  ok = wait_warp(sh.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, kSitePvDone);
+                  if (!ok) break;
+                  tc_fence_after();
+                }
+#pragma unroll 1
+                for (int c = 0; c < DH / 32; ++c) {
+                  uint32_t ro[32];
+                  tmem_ld32(o_base + c * 32, ro);
+                  tmem_ld_wait(ro);
+#pragma unroll
+                  for (int x = 0; x < 32; ++x) ro[x] = __float_as_uint(__uint_as_float(ro[x]) * factor);
+                  tmem_st32(o_base + c * 32, ro);
+                }
+                tmem_st_wait();
+              }
+              l *= factor;
+              m_used = m_new;
+            }
+            const float mref = (m_used == -INFINITY) ? 0.f : m_used;
+            const float2 l2e = make_float2(LOG2E, LOG2E), negm = make_float2(-mref, -mref);
+            float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                             make_float2(0.f, 0.f)};
+            {
+              uint32_t pk[32];
+              exp_pack(ra, pk, acc, l2e, negm);
+              exp_pack(rb, pk + 16, acc, l2e, negm);
+              tmem_st32(s_addr, pk);
+            }
+            {
+              uint32_t pk[32];
+              exp_pack(rc, pk, acc, l2e, negm);
+              exp_pack(rd, pk + 16, acc, l2e, negm);
+              tmem_st32(s_addr + 32, pk);
+            }
+            const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+            const float2 a = __fadd2_rn(a01, a23);
+            l += a.x + a.y;
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[sb]));
+        }
+        if (!ok) break;
+        if constexpr (NQ == 1) {             // to the epilogue's warps
+          ok = np < 2 || wait_warp(sh.stat_empty[np & 1], ((np >> 1) & 1) ^ 1, kSiteStatEmpty);
+          if (!ok) break;
+          sh.stat[np & 1][r] = make_float2(m_used, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.stat_full[np & 1]));
+        } else {
+          ok = epilogue(pc, m_used, l, np);
+        }
+        ++np;
+      }
     }
   }
+  if (lost_site != 0) record_error(p.status, kDevErrTimeoutBase + lost_site);
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -1021,17 +1164,16 @@ Layout layout(int T_max, int H, int H_kv, int d_h) {
   return l;
 }
 
-template <int DH, int NQ>
+template <int DH, int NQ, bool ONE>
 cudaError_t launch_cfg(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const Params& p, cudaStream_t stream) {
   using C = Cfg<DH, NQ>;
-  auto kern = paged_attn_kernel<DH, NQ>;
+  auto kern = paged_attn_kernel<DH, NQ, ONE>;
   int regs = 0;
   if (cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, &regs)) return e;
-  // The softmax warpgroups' register increase waits for the registers the
-  // other warpgroup gives up: launch only when the split fits.
-  if (NQ == 2 && regs * C::THREADS < 128 * C::REGS_CTRL + 256 * C::REGS_SOFT)
-    return cudaErrorInvalidConfiguration;
+  // The warpgroups' register increase waits for the registers the control
+  // warps give up: launch only when the split fits.
+  if (regs * C::THREADS < C::REGS_SPLIT) return cudaErrorInvalidConfiguration;
   const int ctas = std::min(num_sms(), kMaxCtas);
   if (cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p)) return e;
   if (p.rows <= kMergeDirect) {
@@ -1066,9 +1208,9 @@ cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const
   p.gshift = G == 4 ? 2 : (G == 2 ? 1 : 0);
   p.window = window;
   p.ts = kTileShift + (nq - 1) - p.gshift;
-  p.one = batch.T_max <= 1 << p.ts ? 1 : 0;
   p.tokbox = std::min(BM / G, batch.T_max);
   p.rows = part_rows(batch.T_max, G, d_h);
+  p.qsmall = nq == 1 && p.tokbox * G <= 32 ? 1 : 0;
   p.status = status;
   // Q [M, H, d_h]: box {64 channels, G heads, tokens}; rows behind M read as zeros.
   CUtensorMap tq, tk, tv;
@@ -1085,8 +1227,11 @@ cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const
       !encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, K_pages, kdims, kstr, kbox) ||
       !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, V_pages, kdims, kstr, kbox))
     return cudaErrorInvalidValue;
-  if (d_h == 256) return launch_cfg<256, 1>(tq, tk, tv, p, stream);
-  return nq == 2 ? launch_cfg<128, 2>(tq, tk, tv, p, stream) : launch_cfg<128, 1>(tq, tk, tv, p, stream);
+  if (d_h == 128)
+    return nq == 2 ? launch_cfg<128, 2, false>(tq, tk, tv, p, stream)
+                   : launch_cfg<128, 1, true>(tq, tk, tv, p, stream);
+  return batch.T_max <= 1 << p.ts ? launch_cfg<256, 1, true>(tq, tk, tv, p, stream)
+                                  : launch_cfg<256, 1, false>(tq, tk, tv, p, stream);
 }
 
 }  // namespace g3
