@@ -514,13 +514,19 @@ class PagedBatch:
             if tuple(t.shape) != shape or t.dtype != torch.int32 or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
         self.tensors = (lens, row_start, parents, page_table)
+        self.device = lens.get_device()
+        if any(t is not None and t.get_device() != self.device for t in self.tensors):
+            raise ValueError("a batch's tensors must live on one device")
         self.sizes = (B, rows, T_max, page_size, n_pages, pages)
         self.struct = gemma3_paged_batch(*self.sizes, *(
             None if t is None else t.data_ptr() for t in self.tensors))
 
     def ref(self):
         """A reference to the struct, its arrays on the current device."""
-        _here(*self.tensors)
+        if _device is None:
+            _bind_torch()
+        if self.device != _device():
+            raise ValueError("the batch's tensors must live on the current GPU")
         return ctypes.byref(self.struct)
 
     def sizes_ref(self):

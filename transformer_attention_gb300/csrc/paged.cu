@@ -6,8 +6,8 @@
 //   to their page slots.  Every number is read and written once: HBM bounds it
 //   for prompts, latency for a step.  A CTA takes a few rows, finds their
 //   sequences, positions and slots together, and its warps take up to 8 steps
-//   of a row's head vectors (Q, K and V), d_h / 8 lanes per vector and 16 bytes
-//   per lane, all loads first.
+//   of a row's head vectors (Q, K and V), all loads first; d_h / 8 lanes per
+//   vector, each with four channels of both halves, whose pairs it rotates alone.
 // commit: token accepted[b, i] moves to slot lens[b] + i.  accepted ascends, so
 //   accepted[b, i] >= i, and a column of the rows is moved by one thread from
 //   the first token to the last: a slot is written only after the token that
@@ -80,48 +80,67 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   pdl_enter();
   constexpr int LPV = DH / 8;      // lanes per head vector
   constexpr int VPW = 32 / LPV;    // head vectors per warp step
-  constexpr int HALF = LPV / 2;    // lane distance of the RoPE partner
   __shared__ int starts[kStartsMax + 1];
   __shared__ int dst_sh[kAppendRows];      // pool row, -1: no page, -2: of no sequence
   __shared__ float pos_sh[kAppendRows];
   const bool lost = lost_work(a.status, a.lost);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int sub = lane / LPV, ll = lane % LPV;
-  const bool second_half = ll >= HALF;
-  const int c0 = (ll % HALF) * 8;
-  uint4 gq_raw = make_uint4(0, 0, 0, 0), gk_raw = gq_raw;
+  const int sub = lane / LPV;
+  const int c0 = lane % LPV * 4;   // this lane's four pairs: channels c0 .. and c0 + d_h / 2 ..
+  // (1 + gamma) of them, for Q times the query scale
+  float2 gq[4], gk[4];
   if constexpr (NORM) {
-    gq_raw = *reinterpret_cast<const uint4*>(a.gq + ll * 8);
-    gk_raw = *reinterpret_cast<const uint4*>(a.gk + ll * 8);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = c0 + (e & 1) * 2 + (e >> 1) * (DH / 2);
+      const float2 q = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a.gq + c));
+      const float2 k = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a.gk + c));
+      gq[e] = make_float2((1.f + q.x) * a.query_scale, (1.f + q.y) * a.query_scale);
+      gk[e] = make_float2(1.f + k.x, 1.f + k.y);
+    }
   }
   const bool in_smem = p.B <= kStartsMax;
   if (in_smem)
     for (int i = tid; i <= p.B; i += blockDim.x) starts[i] = __ldcg(p.row_start + i);
-  const int h0 = NORM ? 0 : a.H;                   // Q is finished without gammas
-  const int hk = a.H + a.H_kv, end = hk + a.H_kv;  // head vectors: Q, K, V
-  const int vpc = VPW * a.chunk_u;
-  const int nch = (end - h0 + vpc - 1) / vpc;      // items of a row
+  // Items of a row: up to chunk_u steps of VPW heads of Q (finished without
+  // gammas), of K or of V.
+  const int iq = NORM ? ((a.H + VPW - 1) / VPW + a.chunk_u - 1) / a.chunk_u : 0;
+  const int ik = ((a.H_kv + VPW - 1) / VPW + a.chunk_u - 1) / a.chunk_u, nch = iq + 2 * ik;
   const int KVD = a.H_kv * DH;
+  struct Item {
+    int r, kind, head, left;   // row, 0 Q, 1 K, 2 V; this lane's first head, heads from it on
+  };
+  auto item_at = [&](int i) -> Item {
+    Item t;
+    t.r = i / nch;
+    const int c = i - t.r * nch;
+    t.kind = c < iq ? 0 : (c < iq + ik ? 1 : 2);
+    t.head = (t.kind == 0 ? c : (t.kind == 1 ? c - iq : c - iq - ik)) * a.chunk_u * VPW + sub;
+    t.left = min((t.kind == 0 ? a.H : a.H_kv) - t.head, a.chunk_u * VPW - sub);
+    return t;
+  };
 
-  // This lane's 16 bytes of the item's vectors.
-  uint4 raw[kVecUnroll];
-  auto load = [&](int m0, int item) {
-    const int m = m0 + item / nch, first = h0 + item % nch * vpc + sub;
+  // This lane's two times 8 bytes of the item's vectors.
+  uint2 raw[kVecUnroll][2];
+  auto load = [&](int m0, const Item& t) {
+    const long m = m0 + t.r;
+    const __half* src = (t.kind == 0 ? a.Q + m * a.ldq : (t.kind == 1 ? a.K : a.V) + m * a.ldkv) + t.head * DH + c0;
 #pragma unroll
     for (int u = 0; u < kVecUnroll; ++u) {
-      const int hv = first + u * VPW;
-      const __half* src = hv < a.H ? a.Q + m * a.ldq + hv * DH
-                                   : (hv < hk ? a.K + m * a.ldkv + (hv - a.H) * DH
-                                              : a.V + m * a.ldkv + (hv - hk) * DH);
-      raw[u] = (u < a.chunk_u && hv < end) ? __ldcg(reinterpret_cast<const uint4*>(src + ll * 8))
-                                           : make_uint4(0, 0, 0, 0);
+      if (u * VPW < t.left) {
+        raw[u][0] = __ldcg(reinterpret_cast<const uint2*>(src + u * VPW * DH));
+        raw[u][1] = __ldcg(reinterpret_cast<const uint2*>(src + u * VPW * DH + DH / 2));
+      } else {
+        raw[u][0] = raw[u][1] = make_uint2(0, 0);
+      }
     }
   };
 
   for (int m0 = blockIdx.x * a.rows; m0 < p.M; m0 += gridDim.x * a.rows) {
     const int rows = min(a.rows, p.M - m0), items = rows * nch;
     int item = warp;
-    if (item < items) load(m0, item);
+    Item t = item_at(item);
+    if (item < items) load(m0, t);
     // ---------------- the rows' slots and positions
     __syncthreads();       // (starts are there; the rows before are done)
     if (tid < rows) {
@@ -156,74 +175,63 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     if (__syncthreads_or(lost)) return;
 
     while (item < items) {
-      const int r = item / nch, m = m0 + r;
-      const int base = h0 + item % nch * vpc, first = base + sub;
-      const int dst = dst_sh[r];
+      const long m = m0 + t.r;
+      const int dst = dst_sh[t.r];
       if (dst == -2) {
-        if (a.zero_behind && item % nch == 0)   // (the row's first item; the others write nothing)
+        if (a.zero_behind && item == t.r * nch)   // (the row's first item; the others write nothing)
           for (int v = lane; v < a.H * LPV; v += 32)
             *reinterpret_cast<uint4*>(a.Qo + m * a.ldqo + v * 8) = make_uint4(0, 0, 0, 0);
       } else {
-        float cs[8], sn[8];
-        if (NORM && base < hk) {
-          const float pos = pos_sh[r];
+        __half* to = (t.kind == 0 ? a.Qo + m * a.ldqo
+                                  : (t.kind == 1 ? a.Kp : a.Vp) + static_cast<size_t>(max(dst, 0)) * KVD) +
+                     t.head * DH + c0;
+        const int left = t.kind != 0 && dst < 0 ? 0 : t.left;   // (no page: nothing is written)
+        if (NORM && t.kind != 2) {
+          float2 cs[2], sn[2], neg[2], g[4];
+          const float pos = pos_sh[t.r];
+          rope_sincos2(pos, freqs.f[c0], freqs.f[c0 + 1], sn[0], cs[0]);
+          rope_sincos2(pos, freqs.f[c0 + 2], freqs.f[c0 + 3], sn[1], cs[1]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) rope_sincos(pos, freqs.f[c0 + e], sn[e], cs[e]);
-        }
+          for (int e = 0; e < 4; ++e) g[e] = t.kind == 0 ? gq[e] : gk[e];
 #pragma unroll
-        for (int u = 0; u < kVecUnroll; ++u) {
-          if (u >= a.chunk_u || base + u * VPW >= end) break;   // warp-uniform
-          const int hv = first + u * VPW;
-          const bool is_q = hv < a.H;
-          uint4 w = raw[u];
-          if (NORM && base + u * VPW < hk) {
-            float x[8];
-            const __half2* h2 = reinterpret_cast<const __half2*>(&raw[u]);
+          for (int e = 0; e < 2; ++e) neg[e] = make_float2(-sn[e].x, -sn[e].y);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = __half22float2(h2[e]);
-              x[2 * e] = f.x;
-              x[2 * e + 1] = f.y;
-            }
-            float ss = 0.f;
+          for (int u = 0; u < kVecUnroll; ++u) {
+            if (u >= a.chunk_u) break;   // warp-uniform
+            float2 x[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+            for (int e = 0; e < 4; ++e)
+              x[e] = __half22float2(reinterpret_cast<const __half2*>(&raw[u][e >> 1])[e & 1]);
+            float2 s2 = __fmul2_rn(x[0], x[0]);
 #pragma unroll
-            for (int off = HALF; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+            for (int e = 1; e < 4; ++e) s2 = __ffma2_rn(x[e], x[e], s2);
+            float ss = s2.x + s2.y;
+#pragma unroll
+            for (int off = LPV / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
             const float rs = rsqrtf(ss * (1.f / DH) + kEps);
-            const uint4 graw = is_q ? gq_raw : gk_raw;
-            const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&graw);
-            float y[8], o[8];
+            const float2 rr = make_float2(rs, rs);
+            float2 o0[2], o1[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 gf = __bfloat1622float2(g2[e]);
-              y[2 * e] = x[2 * e] * rs * (1.f + gf.x);
-              y[2 * e + 1] = x[2 * e + 1] * rs * (1.f + gf.y);
+            for (int e = 0; e < 2; ++e) {
+              const float2 y0 = __fmul2_rn(__fmul2_rn(x[e], rr), g[e]);
+              const float2 y1 = __fmul2_rn(__fmul2_rn(x[2 + e], rr), g[2 + e]);
+              o0[e] = __ffma2_rn(y1, neg[e], __fmul2_rn(y0, cs[e]));
+              o1[e] = __ffma2_rn(y0, sn[e], __fmul2_rn(y1, cs[e]));
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __shfl_xor_sync(0xffffffffu, y[e], HALF);
-            const float sc = is_q ? a.query_scale : 1.f;
-            uint32_t rot[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // first half: (x1 cos - x2 sin), second: (x2 cos + x1 sin)
-              const float s0 = second_half ? sn[2 * e] : -sn[2 * e];
-              const float s1 = second_half ? sn[2 * e + 1] : -sn[2 * e + 1];
-              const float r0 = y[2 * e] * cs[2 * e] + o[2 * e] * s0;
-              const float r1 = y[2 * e + 1] * cs[2 * e + 1] + o[2 * e + 1] * s1;
-              rot[e] = pack_half2(r0 * sc, r1 * sc);
-            }
-            if (hv < hk) w = make_uint4(rot[0], rot[1], rot[2], rot[3]);
+            raw[u][0] = make_uint2(pack_half2(o0[0].x, o0[0].y), pack_half2(o0[1].x, o0[1].y));
+            raw[u][1] = make_uint2(pack_half2(o1[0].x, o1[0].y), pack_half2(o1[1].x, o1[1].y));
           }
-          if (hv >= end) continue;
-          __half* to = is_q ? a.Qo + m * a.ldqo + hv * DH
-                            : (hv < hk ? a.Kp + static_cast<size_t>(dst) * KVD + (hv - a.H) * DH
-                                       : a.Vp + static_cast<size_t>(dst) * KVD + (hv - hk) * DH);
-          if (is_q || dst >= 0) *reinterpret_cast<uint4*>(to + ll * 8) = w;
         }
+#pragma unroll
+        for (int u = 0; u < kVecUnroll; ++u)
+          if (u * VPW < left) {
+            *reinterpret_cast<uint2*>(to + u * VPW * DH) = raw[u][0];
+            *reinterpret_cast<uint2*>(to + u * VPW * DH + DH / 2) = raw[u][1];
+          }
       }
       item += kAppendWarps;
-      if (item < items) load(m0, item);
+      t = item_at(item);
+      if (item < items) load(m0, t);
     }
   }
 }
@@ -231,23 +239,29 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
 // ---------------------------------------------------------------- commit
 constexpr int kCommitThreads = 256;
 constexpr int kCommitAhead = 8;      // rows in flight per thread
-constexpr int kCommitChunk = 256;    // accepted tokens per round of shared memory
+constexpr int kCommitChunk = kCommitThreads;   // accepted tokens per round of shared memory
 
-// CTA (columns of 16 bytes, sequence, layer and K or V).
+// CTA (columns of 16 bytes, sequence, some of the layers' K and V): the slots
+// are looked up once for all its pools; the next rows' loads are under way
+// while a batch is stored (their slots lie behind it).
 __global__ void __launch_bounds__(kCommitThreads)
     paged_commit_kernel(const PagedBatch p, const int32_t* __restrict__ accepted,
-                        const int32_t* __restrict__ counts, int vecs, __half* Kp, __half* Vp,
+                        const int32_t* __restrict__ counts, int pools, int vecs, __half* Kp, __half* Vp,
                         int32_t* __restrict__ new_lens, int* status) {
   pdl_enter();
   const int b = blockIdx.y, tid = threadIdx.x;
-  const PagedSeq s = paged_seq(p, b, status);
-  const int count = counts != nullptr ? __ldcg(counts + b) : s.n;
   const int32_t* path = accepted != nullptr ? accepted + static_cast<size_t>(b) * p.T_max : nullptr;
+  // (the first accepted tokens are loaded beside the sequence)
+  const int at0 = path != nullptr && tid < p.T_max ? __ldcg(path + tid) : 0;
+  const int before0 = path != nullptr && tid > 0 && tid < p.T_max ? __ldcg(path + tid - 1) : -1;
+  const int given = counts != nullptr ? __ldcg(counts + b) : -1;
+  const PagedSeq s = paged_seq(p, b, status);
+  const int count = counts != nullptr ? given : s.n;
   bool bad = count < 0 || count > s.n;
   if (!bad && path != nullptr)
     for (int i = tid; i < count; i += kCommitThreads) {
-      const int at = __ldcg(path + i);
-      bad |= at >= s.n || at < (i > 0 ? __ldcg(path + i - 1) + 1 : 0);
+      const int at = i == tid ? at0 : __ldcg(path + i), before = i == tid ? before0 : __ldcg(path + i - 1);
+      bad |= at >= s.n || at <= before;
     }
   bad = __syncthreads_or(bad);
   const bool head = blockIdx.x == 0 && blockIdx.z == 0;
@@ -261,30 +275,39 @@ __global__ void __launch_bounds__(kCommitThreads)
   if (head && tid == 0) new_lens[b] = s.len + count;
   if (path == nullptr) return;
   const size_t pool = (static_cast<size_t>(p.n_pages) << p.page_shift) * vecs;   // 16-byte vectors
-  const int layer = blockIdx.z >> 1;
-  uint4* base = reinterpret_cast<uint4*>(blockIdx.z & 1 ? Vp : Kp) + layer * pool;
   const int c = blockIdx.x * kCommitThreads + tid;
   __shared__ int src[kCommitChunk], dst[kCommitChunk];
   for (int i0 = 0; i0 < count; i0 += kCommitChunk) {
     const int n = min(kCommitChunk, count - i0);
     __syncthreads();
     for (int i = tid; i < n; i += kCommitThreads) {
-      const int at = __ldcg(path + i0 + i);
+      const int at = i0 == 0 ? at0 : __ldcg(path + i0 + i);   // (kCommitChunk tokens, a thread each)
       // a token that lies where it belongs is not moved
-      src[i] = at == i0 + i ? -1 : paged_row(p, b, s.len + at, status);
-      dst[i] = at == i0 + i ? -1 : paged_row(p, b, s.len + i0 + i, status);
+      const int from = at == i0 + i ? -1 : paged_row(p, b, s.len + at, status);
+      const int to = at == i0 + i ? -1 : paged_row(p, b, s.len + i0 + i, status);
+      src[i] = to < 0 ? -1 : from;
+      dst[i] = to;
     }
     __syncthreads();
     if (c >= vecs) continue;
-    for (int i = 0; i < n; i += kCommitAhead) {
+    for (int z = blockIdx.z; z < pools; z += gridDim.z) {
+      uint4* base = reinterpret_cast<uint4*>(z & 1 ? Vp : Kp) + (z >> 1) * pool + c;
       uint4 v[kCommitAhead];
+      auto load = [&](int i) {
 #pragma unroll
-      for (int u = 0; u < kCommitAhead; ++u)
-        if (i + u < n && src[i + u] >= 0) v[u] = __ldcg(base + static_cast<size_t>(src[i + u]) * vecs + c);
+        for (int u = 0; u < kCommitAhead; ++u)
+          if (i + u < n && src[i + u] >= 0) v[u] = __ldcg(base + static_cast<size_t>(src[i + u]) * vecs);
+      };
+      load(0);
+      for (int i = 0; i < n; i += kCommitAhead) {
+        uint4 w[kCommitAhead];
 #pragma unroll
-      for (int u = 0; u < kCommitAhead; ++u)
-        if (i + u < n && src[i + u] >= 0 && dst[i + u] >= 0)
-          base[static_cast<size_t>(dst[i + u]) * vecs + c] = v[u];
+        for (int u = 0; u < kCommitAhead; ++u) w[u] = v[u];
+        load(i + kCommitAhead);
+#pragma unroll
+        for (int u = 0; u < kCommitAhead; ++u)
+          if (i + u < n && src[i + u] >= 0) base[static_cast<size_t>(dst[i + u]) * vecs] = w[u];
+      }
     }
   }
 }
@@ -294,7 +317,7 @@ cudaError_t launch_append_dh(const PagedBatch& batch, const AppendParams& p, boo
                              const RopeFreqs& f, cudaStream_t stream) {
   AppendParams a = p;
   constexpr int vpw = 32 / (DH / 8);
-  const int steps = ((norm ? a.H : 0) + 2 * a.H_kv + vpw - 1) / vpw;   // of a row
+  const int steps = (norm ? (a.H + vpw - 1) / vpw : 0) + 2 * ((a.H_kv + vpw - 1) / vpw);   // of a row
   // Few rows: one per CTA, its steps spread over the warps; many: as many as
   // share out the rows over two CTAs per SM.
   const int slots = 2 * num_sms();
@@ -366,8 +389,11 @@ cudaError_t launch_paged_commit(const PagedBatch& batch, const int32_t* accepted
                                 void* K_pages, void* V_pages, int32_t* new_lens,
                                 cudaStream_t stream, int* status) {
   const int vecs = H_kv * d_h / 8;
-  const dim3 grid((vecs + kCommitThreads - 1) / kCommitThreads, batch.B, accepted != nullptr ? 2 * layers : 1);
-  return launch_pdl(paged_commit_kernel, grid, dim3(kCommitThreads), 0, stream, batch, accepted, counts,
+  const int x = (vecs + kCommitThreads - 1) / kCommitThreads, pools = 2 * layers;
+  // as many CTAs as the SMs hold at once share the pools
+  const long long most = std::max(1LL, 6LL * num_sms() / (static_cast<long long>(x) * batch.B));
+  const dim3 grid(x, batch.B, accepted != nullptr ? static_cast<unsigned>(std::min<long long>(pools, most)) : 1);
+  return launch_pdl(paged_commit_kernel, grid, dim3(kCommitThreads), 0, stream, batch, accepted, counts, pools,
                     vecs, static_cast<__half*>(K_pages), static_cast<__half*>(V_pages), new_lens, status);
 }
 

@@ -18,10 +18,10 @@
 // same order).
 //
 // Warps:
-//   0      TMA of K and V: a box for each page and 64 channels
+//   0, 3   TMA of K and V, half of every part each: a copy costs its warp some
+//          100 clocks, and pages of 16 slots take 24 (d_h = 128) or 40 per tile
 //   1      TMEM allocation and MMA issue
-//   2      the CTA's pieces of units, published through a ring
-//   3      TMA of Q
+//   2      the CTA's pieces of units, published through a ring, and TMA of Q
 //   4-7    softmax of query tile 0, one thread per row (NQ = 2: its epilogue too)
 //   8-11   NQ = 2: the same of query tile 1; NQ = 1: the epilogue, so that the
 //          softmax goes on with the next piece
@@ -128,7 +128,7 @@ struct Params {
   float4* part;           // [2 grid, DH / 4, rows] unnormalised, 4 channels each
   Split* split;           // [grid]
   void* O;
-  int o_f16, H, H_kv, gshift, window, ts, tokbox, rows, qsmall;   // ts: log2 of a unit's tokens
+  int o_f16, H, H_kv, gshift, window, ts, tokbox, rows, qsmall, vshift;   // ts: log2 of a unit's tokens, vshift: of a V box's slots
   int* status;
 };
 
@@ -143,13 +143,6 @@ struct Ring {
     }
   }
 };
-
-__device__ __forceinline__ void prefetch_3d(const void* tmap, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                   reinterpret_cast<uint64_t>(tmap)),
-               "r"(c0), "r"(c1), "r"(c2)
-               : "memory");
-}
 
 // exp2(s log2 e - m) of 32 columns: packed fp16 pairs to p[0..15], sums to acc.
 __device__ __forceinline__ void exp_pack(const uint32_t (&s)[32], uint32_t* p, float2 (&acc)[4],
@@ -199,7 +192,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < C::NP; ++s) {
-      mbar_init(smem_u32(&sh.part_full[s]), 1);
+      mbar_init(smem_u32(&sh.part_full[s]), 2);   // both copying warps
       mbar_init(smem_u32(&sh.part_empty[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -360,6 +353,24 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       int b = idle ? 0 : sh.start_b, k = 0, b0 = b + 1;
       PagedSeq win = {0, 0, 0};   // of sequence b0 + lane
       bool ok = true, first = true, have = false;
+      // Q of piece k; few rows (qsmall) have two buffers.
+      auto load_q = [&](const Piece& pc) {
+        const int buf = p.qsmall ? k & 1 : 0, fill = p.qsmall ? k >> 1 : k;
+        ok = fill == 0 || wait_warp(sh.q_empty[buf], (fill - 1) & 1, kSiteQEmpty);
+        if (!ok) return;
+        if (lane == 0) {
+          const int tq1 = BM >> p.gshift, nt = NQ == 2 && pc.ntok > tq1 ? 2 : 1;
+          const uint32_t bar = smem_u32(&sh.q_full[buf]), dst = smem_u32(sQ) + buf * (C::QT_BYTES / 2);
+          mbar_arrive_expect_tx(bar, nt * C::NCH * ((p.tokbox * 128) << p.gshift));
+#pragma unroll 1
+          for (int x = 0; x < nt * C::NCH; ++x) {
+            const int e = x / C::NCH, ch = x % C::NCH;
+            tma_load_3d(dst + e * C::QT_BYTES + ch * (p.qsmall ? QSMALL : CHUNK), &tmQ, bar, ch * 64,
+                        pc.j << p.gshift, pc.row0 + e * tq1);
+          }
+        }
+        ++k;
+      };
       auto publish = [&](const Piece& pc) {
         ok = k < NPC || wait_warp(sh.piece_empty[k % NPC], ((k / NPC) & 1) ^ 1, kSitePieceEmpty);
         if (!ok) return;
@@ -367,7 +378,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
           sh.piece[k % NPC] = pc;
           mbar_arrive(smem_u32(&sh.piece_full[k % NPC]));
         }
-        ++k;
+        if (pc.tiles > 0) load_q(pc);
       };
       // A unit of this CTA that ends in another one (start: its position).
       auto cut = [&](const Piece& pc, long long start, int tiles) {
@@ -389,13 +400,13 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         if constexpr (ONE) {
           if (first && sh.first_used > 0) {
             // its first piece is there; it ends the unit or the CTA's share
+            load_q(sh.piece[0]);
             const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, 0);
             if (sh.piece[0].ends == 1)
               cut(sh.piece[0], pos - off + static_cast<long long>(sh.first_j) * (u.tiles * TC + UC), u.tiles);
             left -= sh.first_used;
             pos += sh.first_used;
             j = sh.first_j + 1;
-            k = 1;
           } else {
             if (s.n == 0) {
               ++b;
@@ -458,12 +469,14 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       }
       if (lane == 0) p.split[blockIdx.x] = split;
       if (ok) publish(Piece{});
-    } else if (warp == 0) {
-      // ---------------- K and V: K of a tile, then V of the tile before
-      const int ps = batch.page_shift, box = min(1 << ps, 64);   // slots per box
-      const int nbox = 256 / box;                                // boxes of a part
-      const int pool = batch.n_pages << ps;
-      constexpr int AHEAD = 3;                                   // tiles that are pulled into L2 before
+      // (every load that was issued lands before the CTA may exit)
+      for (int i = max(0, k - (p.qsmall ? 2 : 1)); i < k; ++i)
+        mbar_wait_drain(smem_u32(&sh.q_full[p.qsmall ? i & 1 : 0]), (p.qsmall ? i >> 1 : i) & 1);
+    } else if (warp != 1) {
+      // ---------------- K and V: K of a tile, then V of the tile before; of
+      // each part one half in each of two warps
+      const int half = warp == 3 ? 1 : 0;
+      const int ps = batch.page_shift, pool = batch.n_pages << ps, in_page = (1 << ps) - 1;
       Ring w;
       int issued = 0;
       // tile `tile` of a piece: lane k's `base` is the pool row of its page k
@@ -471,34 +484,24 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         if (issued >= C::NP && !wait_warp(sh.part_empty[w.slot], w.phase ^ 1, kSitePartEmpty))
           return false;
         const uint32_t bar = smem_u32(&sh.part_full[w.slot]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, PART);
+        if (lane == 0) mbar_arrive_expect_tx(bar, PART / 2);
         __syncwarp();
-        // the part's rows and 64-channel chunks: K (and V of d_h = 128) 128
-        // slots x 2 chunks, V of d_h = 256 64 slots x 4 chunks
-        const bool half = C::PARTS == 2 && v;
-        const int rows = half ? 64 : 128, per_chunk = rows / box;
-        const int ch = lane / per_chunk, r = lane % per_chunk * box;
-        const int so = r + (half ? part * 64 : 0);               // slot of the tile
-        const int page = ps < 7 ? so >> ps : 0;
-        const int row0 = __shfl_sync(0xffffffffu, base, page);
-        if (lane < nbox) {
-          const int row = row0 < 0 ? pool : row0 + ((tile * BN + so) & ((1 << ps) - 1));
-          const int c = (half || C::PARTS == 1 ? ch : part * 2 + ch) * 64;
-          tma_load_3d(smem_u32(sP + w.slot * PART + ch * rows * 128 + r * 128), v ? &tmV : &tmK, bar, c, j,
-                      row);
+        // K: 64 of the part's channels of all slots; V: all channels of half
+        // of its slots (d_h = 128 128, d_h = 256 64), a page's chunks together.
+        // A lane per box: 100 clocks each, 400 in a loop of one lane's.
+        constexpr int VS = 128 / C::PARTS / 2;
+        const int shift = v ? p.vshift : min(ps, kTileShift), at = lane << shift;   // slots of a box
+        const int so = v ? part * (2 * VS) + half * VS + at : at;
+        const int row0 = __shfl_sync(0xffffffffu, base, ps < kTileShift ? so >> ps : 0);
+        const int row = row0 < 0 ? pool : row0 + ((tile * BN + so) & in_page);
+        const uint32_t dst = smem_u32(sP + w.slot * PART) + half * (PART / 2) + at * (v ? DH * 2 : 128);
+        if (at < (v ? VS : BN)) {
+          if (v) tma_load_4d(dst, &tmV, bar, 0, row, 0, j);
+          else tma_load_3d(dst, &tmK, bar, (part * 2 + half) * 64, j, row);
         }
         w.next<C::NP>();
         ++issued;
         return true;
-      };
-      // K and V of a tile into L2, some tiles before the ring has room for them.
-      auto prefetch = [&](int j, int tile, int base) {
-        const int so = (lane >> 1) % (BN / box) * box;
-        const int row0 = __shfl_sync(0xffffffffu, base, ps < 7 ? so >> ps : 0);
-        if ((lane >> 1) < BN / box && row0 >= 0) {
-          const int row = row0 + ((tile * BN + so) & ((1 << ps) - 1));
-          for (int c = 0; c < DH; c += 64) prefetch_3d(lane & 1 ? &tmV : &tmK, c, j, row);
-        }
       };
       // A step: K of the next tile, then V of the one before (the first step
       // has no V, the last no K).
@@ -545,11 +548,6 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
           ok = load_part(v, v ? x - C::PARTS : x, v ? pj : pc.j, v ? ptile : tile, v ? pbase : base);
         }
         if (!more) break;
-        if (!ONE && i + AHEAD < pc.tiles) {
-          const int to = (((tile + AHEAD) * BN) >> ps) - first + (lane & 7);   // (page ids are there for 32 to 63 entries)
-          const int a = __shfl_sync(0xffffffffu, cur, to & 31), z = __shfl_sync(0xffffffffu, ahead, to & 31);
-          prefetch(pc.j, tile + AHEAD, to < 32 ? a : z);
-        }
         pj = pc.j;
         ptile = tile;
         pbase = base;
@@ -558,26 +556,6 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       // Every issued load lands before the CTA may exit.
       for (int n = max(0, issued - C::NP); n < issued; ++n)
         mbar_wait_drain(smem_u32(&sh.part_full[n % C::NP]), (n / C::NP) & 1);
-    } else if (warp == 3) {
-      // ---------------- Q: few rows (qsmall) in two buffers, a piece ahead
-      int k = 0;
-      Piece pc;
-      for (; take(k, pc); ++k) {
-        const int buf = p.qsmall ? k & 1 : 0, fill = p.qsmall ? k >> 1 : k;
-        if (fill > 0 && !wait_warp(sh.q_empty[buf], (fill - 1) & 1, kSiteQEmpty)) break;
-        if (lane == 0) {
-          const int tq1 = BM >> p.gshift, nq = NQ == 2 && pc.ntok > tq1 ? 2 : 1;
-          const uint32_t bar = smem_u32(&sh.q_full[buf]), dst = smem_u32(sQ) + buf * (C::QT_BYTES / 2);
-          mbar_arrive_expect_tx(bar, nq * C::NCH * ((p.tokbox * 128) << p.gshift));
-          for (int e = 0; e < nq; ++e)
-            for (int ch = 0; ch < C::NCH; ++ch)
-              tma_load_3d(dst + e * C::QT_BYTES + ch * (p.qsmall ? QSMALL : CHUNK), &tmQ, bar, ch * 64,
-                          pc.j << p.gshift, pc.row0 + e * tq1);
-        }
-      }
-      // (every load that was issued lands before the CTA may exit)
-      for (int i = max(0, k - (p.qsmall ? 2 : 1)); i < k; ++i)
-        mbar_wait_drain(smem_u32(&sh.q_full[p.qsmall ? i & 1 : 0]), (p.qsmall ? i >> 1 : i) & 1);
     } else {
       // ---------------- MMA issue (whole warp, one elected lane)
       const uint32_t lead = elect_one();
@@ -613,13 +591,17 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         int tile, lo, hi, nq, first, last;
       };
       // O += P V of query tile e, from `part` of V at `vb`.
+      // V lies in blocks of 2^vshift slots, a block's 64-channel chunks one
+      // behind the other.
+      const uint32_t v_chunk = 128u << p.vshift;
       auto mma_pv = [&](int e, int buf, uint32_t vb, int part, int first) {
         constexpr int STEPS = 8 / C::PARTS;   // 16-slot steps of a part
 #pragma unroll
-        for (int k = 0; k < STEPS; ++k)
+        for (int k = 0; k < STEPS; ++k) {
+          const uint32_t at = k * 2048 + ((k * 16) >> p.vshift) * (C::NCH - 1) * v_chunk;
           mma_ts_lead(lead, tbase + O_COL + e * 128, tbase + buf * 128 + (part * STEPS + k) * 8,
-                      sdesc_sw128(vb + k * 2048, CHUNK / C::PARTS, 1024), idesc_pv,
-                      !first || part > 0 || k > 0 ? 1u : 0u);
+                      sdesc_sw128(vb + at, v_chunk, 1024), idesc_pv, !first || part > 0 || k > 0 ? 1u : 0u);
+        }
       };
       // V of the part in slot r, zeroed outside [lo, hi).
       auto v_ready = [&](const Pv& t, int part, const Ring& r) -> bool {
@@ -629,13 +611,13 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         if (s0 < t.lo || s0 + ROWS > t.hi) {
           uint8_t* base = sP + r.slot * PART;
           const int z = min(max(t.lo - s0, 0), ROWS), a = min(max(t.hi - s0, 0), ROWS);
+          // (8 lanes to a row's 128 bytes)
 #pragma unroll 1
-          for (int c = 0; c < static_cast<int>(PART) / (ROWS * 128); ++c) {
-            uint4* rows = reinterpret_cast<uint4*>(base + c * ROWS * 128);
-#pragma unroll 1
-            for (int i = lane; i < z * 8; i += 32) rows[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-            for (int i = a * 8 + lane; i < ROWS * 8; i += 32) rows[i] = make_uint4(0, 0, 0, 0);
+          for (int i = lane >> 3; i < (z + ROWS - a) * C::NCH; i += 4) {
+            const int x = i / C::NCH, c = i % C::NCH, row = x < z ? x : a + x - z;
+            const int blk = row >> p.vshift, in = row & ((1 << p.vshift) - 1);
+            *reinterpret_cast<uint4*>(base + (blk * C::NCH + c) * v_chunk + in * 128 + (lane & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -1222,10 +1204,15 @@ cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const
   const uint64_t kdims[3] = {static_cast<uint64_t>(d_h), static_cast<uint64_t>(H_kv),
                              static_cast<uint64_t>(batch.n_pages) << batch.page_shift};
   const uint64_t kstr[2] = {row, static_cast<uint64_t>(H_kv) * row};
-  const uint32_t kbox[3] = {64, 1, static_cast<uint32_t>(std::min(1 << batch.page_shift, 64))};
+  const uint32_t kbox[3] = {64, 1, static_cast<uint32_t>(std::min(1 << batch.page_shift, BN))};
+  // V: box {64 channels, slots of a page, all 64-channel chunks, 1 head}
+  p.vshift = std::min(batch.page_shift, d_h == 128 ? 6 : 5);
+  const uint64_t vdims[4] = {64, kdims[2], static_cast<uint64_t>(d_h / 64), static_cast<uint64_t>(H_kv)};
+  const uint64_t vstr[3] = {static_cast<uint64_t>(H_kv) * row, 128, row};
+  const uint32_t vbox[4] = {64, 1u << p.vshift, static_cast<uint32_t>(d_h / 64), 1};
   if (!encode_tiled(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, Q, qdims, qstr, qbox) ||
       !encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, K_pages, kdims, kstr, kbox) ||
-      !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, V_pages, kdims, kstr, kbox))
+      !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, V_pages, vdims, vstr, vbox))
     return cudaErrorInvalidValue;
   if (d_h == 128)
     return nq == 2 ? launch_cfg<128, 2, false>(tq, tk, tv, p, stream)
