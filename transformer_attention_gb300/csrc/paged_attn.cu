@@ -13,9 +13,13 @@
 // for its bytes at the HBM rate.
 //
 // Sequences have lengths of their own, known on the device alone: each CTA adds
-// up the tiles of all units and takes an equal share of them, cut wherever it
+// up the work of all units and takes an equal share of it, cut wherever it
 // falls (a unit's parts are then added by paged_merge_kernel, always in the
-// same order).
+// same order).  Units of one kv head read the same slots: where units are longer
+// than a share, CTAs take whole shares from a unit's first tile on, so that the
+// units of a head run side by side and read their slots from L2 (1024 tokens
+// over 31744 slots, 27B-shaped: 2.1 GB from DRAM without this), and the other
+// CTAs share out what is left of the units.
 //
 // Warps:
 //   0, 3   TMA of K and V, half of every part each: a copy costs its warp some
@@ -45,7 +49,7 @@ constexpr int BM = 128, BN = kPagedTile;
 constexpr uint32_t CHUNK = 128 * 128;       // 128 rows x 64 channels (128 B), swizzled
 constexpr uint32_t PART = 32768;
 constexpr uint32_t QSMALL = 32 * 128;       // 32 rows of a chunk: Q of few rows (the MMA reads on behind them)
-constexpr int kTileCost = 2, kUnitCost = 1; // shares of the work
+constexpr int kTileCost = 2;                // shares of the work
 constexpr uint32_t O_COL = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 // A row's reference stays P_SHIFT below a past maximum while the present one
@@ -65,12 +69,26 @@ enum : int {
 struct alignas(16) Piece {
   int b, j, row0, ntok;     // packed row of the unit's first token, its tokens
   int i0, n, len, lo;       // number of that token, the sequence's new tokens and length; visible slots
-  int hi, tile0, tiles, ends;   // ends: bit 0: the unit's first tile is in it, bit 1: its last
+  int hi, tile0, tiles, slot;   // slot: of its part in the workspace, -1: the whole unit
 };
 
-// The unit that starts in a CTA and ends in a later one (parts 0: none).
+// Slots of parts: CTA c's first piece, if it begins inside a unit, has slot 2c,
+// its last, if it ends inside one, 2c + 1; what is left of a unit behind its
+// whole shares, the first of them CTA c's, has slot kRest + c if one piece
+// holds it.
+constexpr int kRest = 2 * kMaxCtas, kSlots = 3 * kMaxCtas;
+
+// The unit whose first piece is a CTA's and that has others (parts 0: none).
 struct alignas(16) Split {
   int row0, ntok, j, parts;
+  int cta, shares;          // whole shares, of CTAs cta ..
+  int rest, inside;         // the others: of CTAs rest .., or all in one piece
+
+  __device__ __forceinline__ int slot(int i) const {
+    if (i < shares) return 2 * (cta + i);
+    if (inside) return kRest + cta;
+    return i == shares ? 2 * rest + 1 : 2 * (rest + i - shares);
+  }
 };
 
 struct Shared {
@@ -79,7 +97,9 @@ struct Shared {
   Piece piece[NPC];
   float2 stat[2][BM];     // NQ = 1: (reference, sum) of a piece's rows
   long long warp_sum[12];
-  long long start_off;    // of this CTA's share in its first sequence
+  int warp_most[12];
+  long long start_off, start_base;   // of this CTA's share in its first sequence, which begins there
+  int start_taken;        // whole shares before that sequence
   int start_b, first_used, first_j;   // first_used: cost of the piece that is there already
   PagedSeq start_seq;
   uint32_t tmem;
@@ -114,9 +134,16 @@ struct Cfg {
   static constexpr int NP = (7 * PART - NQ * QT_BYTES) / PART;   // ring: what Q leaves of 224 KB
   static constexpr uint32_t SMEM = NQ * QT_BYTES + NP * PART + sizeof(Shared);
   static_assert(SMEM <= 232448 && NP <= 8, "shared memory budget");
+  // What a unit costs besides its tiles, in halves of a tile: of units of few
+  // rows alone, and where units of chunks and of steps meet (4B-shaped mixed
+  // batch: 103 us with 1, 81 with 4, 74 with 12).
+  static constexpr int UC1 = 3, UCG = NQ == 2 ? 5 : 10;
+  // Tiles that a CTA does rather than cutting every unit in two: what the parts
+  // of 128 rows and more cost, written and added.
+  [[maybe_unused]] static constexpr int WHOLE = NQ == 2 ? 16 : 8;
   static constexpr int THREADS = 384;
   // the control warps give registers to the others
-  static constexpr int REGS_LAUNCH = 168, REGS_CTRL = 96, REGS_SOFT = NQ == 2 ? 200 : 216;
+  static constexpr int REGS_LAUNCH = 168, REGS_CTRL = NQ == 2 ? 104 : 120, REGS_SOFT = NQ == 2 ? 200 : 216;
   static constexpr int REGS_OTHER = NQ == 2 ? 200 : 168;   // warps 8-11
   static constexpr int REGS_SPLIT = 128 * (REGS_CTRL + REGS_SOFT + REGS_OTHER);
   static_assert(REGS_SPLIT <= THREADS * REGS_LAUNCH, "register split");
@@ -124,8 +151,8 @@ struct Cfg {
 
 struct Params {
   PagedBatch batch;
-  float2* pstat;          // [2 grid, rows] (reference, sum)
-  float4* part;           // [2 grid, DH / 4, rows] unnormalised, 4 channels each
+  float2* pstat;          // [kSlots, rows] (reference, sum)
+  float4* part;           // [kSlots, DH / 4, rows] unnormalised, 4 channels each
   Split* split;           // [grid]
   void* O;
   int o_f16, H, H_kv, gshift, window, ts, tokbox, rows, qsmall, vshift;   // ts: log2 of a unit's tokens, vshift: of a V box's slots
@@ -172,7 +199,8 @@ __device__ __forceinline__ uint32_t bits_at(uint64_t m, int d) {
 // ONE: the new tokens of every sequence fit one unit per head.
 template <int DH, int NQ, bool ONE>
 __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
-    paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ32,
+                      const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const Params p) {
   using C = Cfg<DH, NQ>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -231,18 +259,46 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   // A unit costs kTileCost for each tile and kUnitCost: what a piece costs
   // besides its tiles.  Tile t of a unit is in the share that holds the unit's
   // position kUnitCost + t kTileCost.
-  constexpr int TC = kTileCost, UC = kUnitCost;
+  constexpr int TC = kTileCost, UC = ONE ? C::UC1 : C::UCG;
   const int per = (batch.B + C::THREADS - 1) / C::THREADS;   // sequences per thread
+  int S = 0;                  // tiles of a whole share (0: there are none)
+  bool uncut = false;         // every unit is one CTA's share
+  // whole shares of every unit of a sequence
+  auto shares_of = [&](const PagedSeq& s) -> int {
+    if (uncut) return s.n > 0 ? 1 : 0;
+    return ONE || S == 0 || s.n == 0 ? 0 : paged_unit(s.len, s.n, p.window, tree, p.ts, 0).tiles / S;
+  };
+  // cost of what is left of a kv head's first q units
+  auto cost_of = [&](const PagedSeq& s, int whole, int q) -> long long {
+    return TC * (paged_prefix(s.len, s.n, p.window, tree, p.ts, q) - static_cast<long long>(whole) * S * q) +
+           static_cast<long long>(UC) * q;
+  };
   auto head_cost = [&](const PagedSeq& s) -> long long {     // of a kv head of a sequence
-    if constexpr (ONE) {
+    if constexpr (ONE)
       return s.n > 0 ? TC * paged_unit(s.len, s.n, p.window, tree, p.ts, 0).tiles + UC : 0;
-    } else {
-      const int nq = paged_units(s.n, p.ts);
-      return TC * paged_prefix(s.len, s.n, p.window, tree, p.ts, nq) + static_cast<long long>(UC) * nq;
-    }
+    else
+      return cost_of(s, shares_of(s), paged_units(s.n, p.ts));
   };
   auto tile_at = [](int o) { return max(0, (o - UC + TC - 1) / TC); };   // first tile at or behind position o
-  long long mine = 0;
+  // Sum over the block's threads and, in upto, over those up to this one.
+  auto scan = [&](long long v, long long& upto, bool out) -> long long {
+    upto = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    if (lane == 31) sh.warp_sum[warp] = upto;
+    if (__syncthreads_or(out)) return -1;
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < C::THREADS / 32; ++w) {
+      if (w < warp) upto += sh.warp_sum[w];
+      total += sh.warp_sum[w];
+    }
+    return total;
+  };
+  long long mine = 0, upto;
   PagedSeq seq = {0, 0, 0};   // the thread's last one
   for (int k = 0; k < per; ++k) {
     const int b = tid * per + k;
@@ -250,41 +306,76 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     seq = paged_seq(batch, b, p.status);
     mine += p.H_kv * head_cost(seq);
   }
-  long long upto = mine;   // through this thread
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) sh.warp_sum[warp] = upto;
-  const bool stop = __syncthreads_or(lost);
+  long long total = scan(mine, upto, lost);
   tc_fence_after();
   const uint32_t tbase = sh.tmem;
-  if (stop) {
+  if (total < 0) {
     if (warp == 1) tmem_dealloc(tbase, 512);
     return;
   }
-  long long total = 0;
+  // Whole shares: CTAs 0 .. taken - 1.  (No window: a unit's tiles grow with
+  // its number.)  What all shares and units cost leaves at least one CTA over.
+  int taken = 0, grid = gridDim.x, taken_mine = 0, taken_upto = 0;
+  if constexpr (!ONE) {
+    const long long all = total;
+    // units, and the longest one's tiles
+    long long units = 0;
+    int longest = 0;
+    for (int k = 0; k < per; ++k) {
+      const int b = tid * per + k;
+      if (b >= batch.B) break;
+      if (per > 1) seq = paged_seq(batch, b, p.status);
+      if (seq.n == 0) continue;
+      const int nq = paged_units(seq.n, p.ts);
+      units += static_cast<long long>(p.H_kv) * nq;
+      // (with a window no unit has more than the slots that its tokens reach)
+      int t = (seq.len + seq.n + BN - 1) >> kTileShift;
+      if (p.window > 0) t = min(t, static_cast<int>((static_cast<long long>(p.window) + (tree ? seq.n : 1 << p.ts) + 2 * BN) >> kTileShift));
+      longest = max(longest, t);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) sh.warp_most[warp] = longest;
+    __syncthreads();          // (the sums are read)
+    units = scan(units, upto, false);
 #pragma unroll
-  for (int w = 0; w < C::THREADS / 32; ++w) {
-    if (w < warp) upto += sh.warp_sum[w];
-    total += sh.warp_sum[w];
+    for (int w = 0; w < C::THREADS / 32; ++w) longest = max(longest, sh.warp_most[w]);
+    const long long per_cta = (all + static_cast<long long>(grid) * TC - 1) / (static_cast<long long>(grid) * TC);
+    uncut = units <= grid && longest <= per_cta + C::WHOLE;
+    if (p.window == 0 && all > 0 && !uncut) S = static_cast<int>(per_cta);
+    mine = 0;
+    __syncthreads();
+    for (int k = 0; k < per; ++k) {
+      const int b = tid * per + k;
+      if (b >= batch.B) break;
+      if (per > 1) seq = paged_seq(batch, b, p.status);
+      if (!uncut) mine += p.H_kv * head_cost(seq);
+      taken_mine += p.H_kv * paged_units(seq.n, p.ts) * shares_of(seq);
+    }
+    // (at most kMaxCtas shares; costs below 2^48)
+    total = scan(static_cast<long long>(taken_mine) << 48 | mine, upto, false);
+    taken = static_cast<int>(total >> 48);
+    taken_upto = static_cast<int>(upto >> 48);
+    total &= (1LL << 48) - 1;
+    upto &= (1LL << 48) - 1;
+    grid -= taken;
   }
+  const bool sharing = static_cast<int>(blockIdx.x) < taken;   // this CTA has a whole share
+  const int me = blockIdx.x - taken;                           // its number among the others
   // (shares of a tile's cost or more: a unit's parts lie in consecutive CTAs)
   const bool small = total < 1 << 23;   // (64-bit divisions cost some 100 clocks each)
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total / TC));
-  const bool idle = static_cast<int>(blockIdx.x) >= ctas;
+  const int ctas = static_cast<int>(min(static_cast<long long>(grid), total / TC));
+  const bool idle = !sharing && me >= ctas;
   auto share = [&](int c) -> long long {   // first position of CTA c
     if (small) return static_cast<unsigned>(total) * static_cast<unsigned>(c) / static_cast<unsigned>(ctas);
     return total * c / ctas;
   };
   auto cta_of = [&](long long x) -> int {  // the CTA that holds position x
-    if (small) return (static_cast<unsigned>(x + 1) * static_cast<unsigned>(ctas) - 1) / static_cast<unsigned>(total);
-    return static_cast<int>(((x + 1) * ctas - 1) / total);
+    if (small) return taken + (static_cast<unsigned>(x + 1) * static_cast<unsigned>(ctas) - 1) / static_cast<unsigned>(total);
+    return taken + static_cast<int>(((x + 1) * ctas - 1) / total);
   };
-  const long long from = idle ? 0 : share(blockIdx.x);
-  const long long count = idle ? 0 : share(blockIdx.x + 1) - from;
-  // The piece of a unit's tiles [t0, t0 + n).
+  const long long from = idle || sharing ? 0 : share(me);
+  const long long count = idle || sharing ? 0 : share(me + 1) - from;
+  // The piece of a unit's tiles [t0, t0 + n); the part's slot is set by the caller.
   auto make_piece = [&](const PagedSeq& s, int b, int j, int q, const PagedUnit& u, int t0, int n) -> Piece {
     Piece pc;
     pc.b = b;
@@ -298,23 +389,33 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     pc.hi = u.hi;
     pc.tile0 = u.tile0 + t0;
     pc.tiles = n;
-    pc.ends = (t0 == 0 ? 1 : 0) | (t0 + n == u.tiles ? 2 : 0);
+    const int c2 = 2 * static_cast<int>(blockIdx.x);
+    pc.slot = t0 > 0 ? c2 : (n < u.tiles ? c2 + 1 : -1);
     return pc;
   };
-  if (!idle && from < upto && from >= upto - mine) {
-    long long off = from - (upto - mine);
-    int b = tid * per;
+  const bool finder = sharing ? static_cast<int>(blockIdx.x) < taken_upto &&
+                                    static_cast<int>(blockIdx.x) >= taken_upto - taken_mine
+                              : !idle && from < upto && from >= upto - mine;
+  if (finder) {
+    // the share's first sequence, and the position and share where that begins
+    long long base = upto - mine;
+    int b = tid * per, first = taken_upto - taken_mine;
     while (per > 1) {
       seq = paged_seq(batch, b, p.status);
-      const long long n = p.H_kv * head_cost(seq);
-      if (off < n || b + 1 >= batch.B) break;
-      off -= n;
+      const long long n = uncut ? 0 : p.H_kv * head_cost(seq);
+      const int t = ONE ? 0 : p.H_kv * paged_units(seq.n, p.ts) * shares_of(seq);
+      if ((sharing ? static_cast<int>(blockIdx.x) < first + t : from < base + n) || b + 1 >= batch.B) break;
+      base += n;
+      first += t;
       ++b;
     }
     sh.start_b = b;
-    sh.start_off = off;
+    sh.start_off = from - base;
+    sh.start_base = base;
+    sh.start_taken = first;
     sh.start_seq = seq;
     if constexpr (ONE) {   // the first piece at once: a step waits for it
+      const long long off = from - base;
       const PagedUnit u = paged_unit(seq.len, seq.n, p.window, tree, p.ts, 0);
       const int cost = u.tiles * TC + UC;
       const int j = static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(cost));
@@ -346,133 +447,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
 
   if (warp < 4) {
     regs_decrease<C::REGS_CTRL>();
-    if (warp == 2) {
-      // ---------------- pieces
-      Split split = {0, 0, 0, 0};
-      long long left = count, pos = from, off = idle ? 0 : sh.start_off;
-      int b = idle ? 0 : sh.start_b, k = 0, b0 = b + 1;
-      PagedSeq win = {0, 0, 0};   // of sequence b0 + lane
-      bool ok = true, first = true, have = false;
-      // Q of piece k; few rows (qsmall) have two buffers.
-      auto load_q = [&](const Piece& pc) {
-        const int buf = p.qsmall ? k & 1 : 0, fill = p.qsmall ? k >> 1 : k;
-        ok = fill == 0 || wait_warp(sh.q_empty[buf], (fill - 1) & 1, kSiteQEmpty);
-        if (!ok) return;
-        if (lane == 0) {
-          const int tq1 = BM >> p.gshift, nt = NQ == 2 && pc.ntok > tq1 ? 2 : 1;
-          const uint32_t bar = smem_u32(&sh.q_full[buf]), dst = smem_u32(sQ) + buf * (C::QT_BYTES / 2);
-          mbar_arrive_expect_tx(bar, nt * C::NCH * ((p.tokbox * 128) << p.gshift));
-#pragma unroll 1
-          for (int x = 0; x < nt * C::NCH; ++x) {
-            const int e = x / C::NCH, ch = x % C::NCH;
-            tma_load_3d(dst + e * C::QT_BYTES + ch * (p.qsmall ? QSMALL : CHUNK), &tmQ, bar, ch * 64,
-                        pc.j << p.gshift, pc.row0 + e * tq1);
-          }
-        }
-        ++k;
-      };
-      auto publish = [&](const Piece& pc) {
-        ok = k < NPC || wait_warp(sh.piece_empty[k % NPC], ((k / NPC) & 1) ^ 1, kSitePieceEmpty);
-        if (!ok) return;
-        if (lane == 0) {
-          sh.piece[k % NPC] = pc;
-          mbar_arrive(smem_u32(&sh.piece_full[k % NPC]));
-        }
-        if (pc.tiles > 0) load_q(pc);
-      };
-      // A unit of this CTA that ends in another one (start: its position).
-      auto cut = [&](const Piece& pc, long long start, int tiles) {
-        split = {pc.row0, pc.ntok, pc.j, cta_of(start + UC + (tiles - 1) * TC) - static_cast<int>(blockIdx.x) + 1};
-      };
-      while (ok && left > 0 && b < batch.B) {
-        PagedSeq s = sh.start_seq;
-        if (!first) {
-          if (!have || b >= b0 + 32) {
-            b0 = b;
-            win = b0 + lane < batch.B ? paged_seq(batch, b0 + lane, p.status) : PagedSeq{0, 0, 0};
-            have = true;
-          }
-          s.row0 = __shfl_sync(0xffffffffu, win.row0, b - b0);
-          s.n = __shfl_sync(0xffffffffu, win.n, b - b0);
-          s.len = __shfl_sync(0xffffffffu, win.len, b - b0);
-        }
-        int q = 0, j = 0, nq = 1, o = 0;   // unit and position in it
-        if constexpr (ONE) {
-          if (first && sh.first_used > 0) {
-            // its first piece is there; it ends the unit or the CTA's share
-            load_q(sh.piece[0]);
-            const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, 0);
-            if (sh.piece[0].ends == 1)
-              cut(sh.piece[0], pos - off + static_cast<long long>(sh.first_j) * (u.tiles * TC + UC), u.tiles);
-            left -= sh.first_used;
-            pos += sh.first_used;
-            j = sh.first_j + 1;
-          } else {
-            if (s.n == 0) {
-              ++b;
-              continue;
-            }
-            if (off > 0) {    // (inside the first sequence)
-              const long long cost = head_cost(s);
-              j = static_cast<int>(off / cost);
-              o = static_cast<int>(off - j * cost);
-            }
-          }
-        } else {
-          // the unit of a head's position t: the last one that starts at or before it
-          nq = paged_units(s.n, p.ts);
-          int q1 = nq, at = nq;
-          long long head = 0, start = 0, t = 0;
-#pragma unroll 1
-          while (true) {
-            const long long to = TC * paged_prefix(s.len, s.n, p.window, tree, p.ts, at) + static_cast<long long>(UC) * at;
-            if (head == 0) {
-              if (to == 0) break;
-              head = to;
-              j = static_cast<int>(off / head);
-              t = off - j * head;
-            } else if (to <= t) {
-              q = at;
-              start = to;
-            } else {
-              q1 = at;
-            }
-            if (q1 - q <= 1) break;
-            at = (q + q1) / 2;
-          }
-          if (head == 0) {
-            ++b;
-            continue;
-          }
-          o = static_cast<int>(t - start);
-        }
-        first = false;
-        while (ok && left > 0 && j < p.H_kv) {
-          const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, q);
-          const int o1 = static_cast<int>(min(o + left, static_cast<long long>(u.tiles) * TC + UC));
-          const int t0 = tile_at(o), n = tile_at(o1) - t0;
-          if (n > 0) {
-            const Piece pc = make_piece(s, b, j, q, u, t0, n);
-            if (pc.ends == 1) cut(pc, pos - o, u.tiles);
-            publish(pc);
-          }
-          left -= o1 - o;
-          pos += o1 - o;
-          o = 0;
-          if (++q == nq) {
-            q = 0;
-            ++j;
-          }
-        }
-        off = 0;
-        ++b;
-      }
-      if (lane == 0) p.split[blockIdx.x] = split;
-      if (ok) publish(Piece{});
-      // (every load that was issued lands before the CTA may exit)
-      for (int i = max(0, k - (p.qsmall ? 2 : 1)); i < k; ++i)
-        mbar_wait_drain(smem_u32(&sh.q_full[p.qsmall ? i & 1 : 0]), (p.qsmall ? i >> 1 : i) & 1);
-    } else if (warp != 1) {
+    if (warp != 1 && warp != 2) {
       // ---------------- K and V: K of a tile, then V of the tile before; of
       // each part one half in each of two warps
       const int half = warp == 3 ? 1 : 0;
@@ -556,7 +531,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       // Every issued load lands before the CTA may exit.
       for (int n = max(0, issued - C::NP); n < issued; ++n)
         mbar_wait_drain(smem_u32(&sh.part_full[n % C::NP]), (n / C::NP) & 1);
-    } else {
+    } else if (warp == 1) {
       // ---------------- MMA issue (whole warp, one elected lane)
       const uint32_t lead = elect_one();
       constexpr uint32_t idesc_qk = idesc_f16(BM, BN, /*f16*/ 0, 0, 0);
@@ -724,6 +699,163 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       }
       mma_commit_lead(lead, smem_u32(&sh.drain));
       mbar_wait_drain(smem_u32(&sh.drain), 0);
+    } else {
+      // ---------------- pieces
+      Split split = {0, 0, 0, 0, 0, 0, 0, 0};
+      long long left = count, pos = from, off = idle ? 0 : sh.start_off;
+      int b = idle ? 0 : sh.start_b, k = 0, b0 = b + 1;
+      PagedSeq win = {0, 0, 0};   // of sequence b0 + lane
+      bool ok = true, first = true, have = false;
+      // Q of piece k; few rows (qsmall) have two buffers.
+      auto load_q = [&](const Piece& pc) {
+        const int buf = p.qsmall ? k & 1 : 0, fill = p.qsmall ? k >> 1 : k;
+        ok = fill == 0 || wait_warp(sh.q_empty[buf], (fill - 1) & 1, kSiteQEmpty);
+        if (!ok) return;
+        if (lane == 0) {
+          const int tq1 = BM >> p.gshift, nt = NQ == 2 && pc.ntok > tq1 ? 2 : 1;
+          const uint32_t bar = smem_u32(&sh.q_full[buf]), dst = smem_u32(sQ) + buf * (C::QT_BYTES / 2);
+          // (a unit of few tokens does not read 128 rows)
+          const bool few = (pc.ntok << p.gshift) <= 32;
+          const int box = few ? min(p.tokbox << p.gshift, 32) : p.tokbox << p.gshift;   // rows
+          mbar_arrive_expect_tx(bar, nt * C::NCH * box * 128);
+#pragma unroll 1
+          for (int x = 0; x < nt * C::NCH; ++x) {
+            const int e = x / C::NCH, ch = x % C::NCH;
+            tma_load_3d(dst + e * C::QT_BYTES + ch * (p.qsmall ? QSMALL : CHUNK), few ? &tmQ32 : &tmQ, bar, ch * 64,
+                        pc.j << p.gshift, pc.row0 + e * tq1);
+          }
+        }
+        ++k;
+      };
+      auto publish = [&](const Piece& pc) {
+        ok = k < NPC || wait_warp(sh.piece_empty[k % NPC], ((k / NPC) & 1) ^ 1, kSitePieceEmpty);
+        if (!ok) return;
+        if (lane == 0) {
+          sh.piece[k % NPC] = pc;
+          mbar_arrive(smem_u32(&sh.piece_full[k % NPC]));
+        }
+        if (pc.tiles > 0) load_q(pc);
+      };
+      // A unit whose first piece is this CTA's, with others; what is left of it
+      // behind `whole` shares, `rest` tiles, begins at position `start`.
+      auto cut = [&](const Piece& pc, int whole, long long start, int rest) {
+        split = {pc.row0, pc.ntok, pc.j, whole, static_cast<int>(blockIdx.x), whole, 0, 0};
+        if (rest > 0) {
+          split.rest = cta_of(start + UC);
+          const int last = cta_of(start + UC + static_cast<long long>(rest - 1) * TC);
+          split.inside = whole > 0 && last == split.rest;
+          split.parts += last - split.rest + 1;
+        }
+      };
+      int passed = idle ? 0 : sh.start_taken;   // whole shares before the present sequence
+      if (!ONE && sharing) {
+        // ---- one whole share
+        const PagedSeq s = sh.start_seq;
+        const int whole = shares_of(s), nq = paged_units(s.n, p.ts), x = static_cast<int>(blockIdx.x) - passed;
+        const int unit = x / max(whole, 1), at = x - unit * whole, j = unit / nq, q = unit - j * nq;
+        const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, q);
+        Piece pc = make_piece(s, b, j, q, u, uncut ? 0 : at * S, uncut ? u.tiles : S);
+        if (pc.slot >= 0) pc.slot = 2 * blockIdx.x;
+        if (at == 0 && pc.slot >= 0)
+          cut(pc, whole, sh.start_base + j * cost_of(s, whole, nq) + cost_of(s, whole, q), u.tiles - whole * S);
+        publish(pc);
+      }
+      while (ok && left > 0 && b < batch.B) {
+        PagedSeq s = sh.start_seq;
+        if (!first) {
+          if (!have || b >= b0 + 32) {
+            b0 = b;
+            win = b0 + lane < batch.B ? paged_seq(batch, b0 + lane, p.status) : PagedSeq{0, 0, 0};
+            have = true;
+          }
+          s.row0 = __shfl_sync(0xffffffffu, win.row0, b - b0);
+          s.n = __shfl_sync(0xffffffffu, win.n, b - b0);
+          s.len = __shfl_sync(0xffffffffu, win.len, b - b0);
+        }
+        const int whole = shares_of(s);
+        int q = 0, j = 0, nq = 1, o = 0;   // unit and position in it
+        if constexpr (ONE) {
+          if (first && sh.first_used > 0) {
+            // its first piece is there; it ends the unit or the CTA's share
+            load_q(sh.piece[0]);
+            const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, 0);
+            if (sh.piece[0].slot == 2 * static_cast<int>(blockIdx.x) + 1)
+              cut(sh.piece[0], 0, sh.start_base + static_cast<long long>(sh.first_j) * (u.tiles * TC + UC), u.tiles);
+            left -= sh.first_used;
+            pos += sh.first_used;
+            j = sh.first_j + 1;
+          } else {
+            if (s.n == 0) {
+              ++b;
+              continue;
+            }
+            if (off > 0) {    // (inside the first sequence)
+              const long long cost = head_cost(s);
+              j = static_cast<int>(off / cost);
+              o = static_cast<int>(off - j * cost);
+            }
+          }
+        } else {
+          // the unit of a head's position t: the last one that starts at or before it
+          nq = paged_units(s.n, p.ts);
+          int q1 = nq, at = nq;
+          long long head = 0, start = 0, t = 0;
+#pragma unroll 1
+          while (true) {
+            const long long to = cost_of(s, whole, at);
+            if (head == 0) {
+              if (to == 0) break;
+              head = to;
+              j = static_cast<int>(off / head);
+              t = off - j * head;
+            } else if (to <= t) {
+              q = at;
+              start = to;
+            } else {
+              q1 = at;
+            }
+            if (q1 - q <= 1) break;
+            at = (q + q1) / 2;
+          }
+          if (head == 0) {
+            ++b;
+            continue;
+          }
+          o = static_cast<int>(t - start);
+        }
+        first = false;
+        while (ok && left > 0 && j < p.H_kv) {
+          const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, q);
+          const int skip = whole * S, rest = u.tiles - skip;
+          const int o1 = static_cast<int>(min(o + left, static_cast<long long>(rest) * TC + UC));
+          const int t0 = tile_at(o), n = tile_at(o1) - t0;
+          if (n > 0) {
+            Piece pc = make_piece(s, b, j, q, u, skip + t0, n);
+            if (t0 == 0 && n < rest) {
+              pc.slot = 2 * blockIdx.x + 1;
+              if (whole == 0) cut(pc, 0, pos - o, rest);
+            } else if (t0 == 0 && whole > 0) {
+              pc.slot = kRest + passed + (j * nq + q) * whole;
+            }
+            publish(pc);
+          }
+          left -= o1 - o;
+          pos += o1 - o;
+          o = 0;
+          if (++q == nq) {
+            q = 0;
+            ++j;
+          }
+        }
+        off = 0;
+        ++b;
+        passed += p.H_kv * nq * whole;
+      }
+      if (lane == 0) p.split[blockIdx.x] = split;   // (read by the merge)
+      if (ok) publish(Piece{});
+      // (every load that was issued lands before the CTA may exit)
+      for (int i = max(0, k - (p.qsmall ? 2 : 1)); i < k; ++i)
+        mbar_wait_drain(smem_u32(&sh.q_full[p.qsmall ? i & 1 : 0]), (p.qsmall ? i >> 1 : i) & 1);
     }
   } else {
     // ---------------- softmax of query tile e (thread r owns row r), epilogue
@@ -740,11 +872,10 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       const bool live = __any_sync(0xffffffffu, row_valid);
       if (live) {
         tc_fence_after();
-        const bool whole = pc.ends == 3, have = row_valid && l != 0.f;
+        const bool whole = pc.slot < 0, have = row_valid && l != 0.f;
         const size_t orow = static_cast<size_t>(pc.row0 + tok) * p.H + (pc.j << p.gshift) +
                             (r & ((1 << p.gshift) - 1));
-        // parts: a CTA's first piece may begin inside a unit, its last end inside one
-        const size_t slot = 2 * blockIdx.x + (pc.ends & 1);
+        const size_t slot = max(pc.slot, 0);
         float4* pdst = p.part + slot * (DH / 4) * p.rows + e * BM + r;
         if (!whole && row_valid)
           p.pstat[slot * p.rows + e * BM + r] = have ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
@@ -934,7 +1065,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   }
 }
 
-// Adds the parts of the units that end in a later CTA than they start in.  A
+// Adds the parts of the units that several CTAs have worked on.  A
 // task is up to 32 rows of such a unit and some of their channels: lanes along
 // the rows, which lie next to each other in a part, and where they are few
 // along 4-channel vectors too.  A lane has its row's sums to itself, so a task
@@ -971,6 +1102,11 @@ struct MergeShared {
   float2 st[kMergeWarps][32];
   float4 o[kMergeWarps][2][32];
 };
+
+__device__ __forceinline__ Split load_split(const Split* from) {
+  const int4 a = __ldcg(reinterpret_cast<const int4*>(from)), b = __ldcg(reinterpret_cast<const int4*>(from) + 1);
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
 
 // Lanes along the rows of a unit of `all` rows: a power of two.
 __device__ __forceinline__ int merge_pad(int all) {
@@ -1013,8 +1149,7 @@ __device__ __forceinline__ void merge_tasks(const Params& p, MergeShared& sh, co
       mine = r < all && v0 < DH / 4;
       orow = static_cast<size_t>(u.row0 + (r >> p.gshift)) * p.H + (u.j << p.gshift) + (r & ((1 << p.gshift) - 1));
       if (mine) {
-        // this warp's parts: sub, sub + wp, ...; part 0 ends the CTA, the
-        // others begin those behind it
+        // this warp's parts: sub, sub + wp, ...
         constexpr int AT_ONCE = 4;
         for (int i0 = sub; i0 < u.parts; i0 += AT_ONCE * wp) {
           float2 st[AT_ONCE];
@@ -1024,7 +1159,7 @@ __device__ __forceinline__ void merge_tasks(const Params& p, MergeShared& sh, co
             const int i = i0 + k * wp;
             st[k] = make_float2(0.f, 0.f);
             if (i < u.parts) {
-              const size_t slot = i == 0 ? 2 * cta + 1 : 2 * (cta + i);
+              const size_t slot = u.slot(i);
               st[k] = __ldcg(p.pstat + slot * p.rows + r);
 #pragma unroll
               for (int v = 0; v < VV; ++v) x[k][v] = __ldcg(p.part + (slot * (DH / 4) + v0 + v) * p.rows + r);
@@ -1075,8 +1210,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_few_kernel(const
   pdl_enter();
   const bool lost = lost_work(p.status, kLostWait);   // parts may be missing
   __shared__ MergeShared sh;
-  const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.split) + blockIdx.x);
-  const Split u = {raw.x, raw.y, raw.z, raw.w};
+  const Split u = load_split(p.split + blockIdx.x);
   if (lost || u.parts == 0) return;
   merge_tasks<DH, 1, true>(p, sh, u, (DH / 4 * merge_pad(u.ntok << p.gshift) + 31) / 32, merge_warps(u.parts), 0);
 }
@@ -1087,10 +1221,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const 
   const bool lost = lost_work(p.status, kLostWait);   // parts may be missing
   __shared__ MergeShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  Split u = {0, 0, 0, 0};                             // the unit that starts in CTA tid
+  Split u = {0, 0, 0, 0, 0, 0, 0, 0};                 // the unit that starts in CTA tid
   if (tid < ctas) {
-    const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.split) + tid);
-    u = {raw.x, raw.y, raw.z, raw.w};
+    u = load_split(p.split + tid);
     sh.split[tid] = u;
   }
   // its tasks with one vector per lane and, packed above them, with two
@@ -1137,7 +1270,7 @@ struct Layout {
 };
 Layout layout(int T_max, int H, int H_kv, int d_h) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t rows = static_cast<size_t>(2) * kMaxCtas * part_rows(T_max, H / H_kv, d_h);
+  const size_t rows = static_cast<size_t>(kSlots) * part_rows(T_max, H / H_kv, d_h);
   Layout l;
   l.stat = 0;
   l.part = up(rows * sizeof(float2));
@@ -1147,7 +1280,7 @@ Layout layout(int T_max, int H, int H_kv, int d_h) {
 }
 
 template <int DH, int NQ, bool ONE>
-cudaError_t launch_cfg(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+cudaError_t launch_cfg(const CUtensorMap& tq, const CUtensorMap& tq32, const CUtensorMap& tk, const CUtensorMap& tv,
                        const Params& p, cudaStream_t stream) {
   using C = Cfg<DH, NQ>;
   auto kern = paged_attn_kernel<DH, NQ, ONE>;
@@ -1157,7 +1290,7 @@ cudaError_t launch_cfg(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
   // warps give up: launch only when the split fits.
   if (regs * C::THREADS < C::REGS_SPLIT) return cudaErrorInvalidConfiguration;
   const int ctas = std::min(num_sms(), kMaxCtas);
-  if (cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p)) return e;
+  if (cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, tq, tq32, tk, tv, p)) return e;
   if (p.rows <= kMergeDirect) {
     const int tasks = (DH / 4 * kMergeDirect) / 32;   // at most
     return launch_pdl(paged_merge_few_kernel<DH>, dim3(ctas, std::min(tasks, 4)), dim3(32 * kMergeWarps), 0,
@@ -1195,11 +1328,12 @@ cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const
   p.qsmall = nq == 1 && p.tokbox * G <= 32 ? 1 : 0;
   p.status = status;
   // Q [M, H, d_h]: box {64 channels, G heads, tokens}; rows behind M read as zeros.
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tq32, tk, tv;   // tq32: units of few tokens, 32 rows at most
   const uint64_t row = static_cast<uint64_t>(d_h) * 2;
   const uint64_t qdims[3] = {static_cast<uint64_t>(d_h), static_cast<uint64_t>(H), static_cast<uint64_t>(batch.M)};
   const uint64_t qstr[2] = {row, static_cast<uint64_t>(H) * row};
   const uint32_t qbox[3] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(p.tokbox)};
+  const uint32_t qbox32[3] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(std::min(p.tokbox, 32 / G))};
   // the pools as rows of slots: box {64 channels, 1 head, the slots of a page}
   const uint64_t kdims[3] = {static_cast<uint64_t>(d_h), static_cast<uint64_t>(H_kv),
                              static_cast<uint64_t>(batch.n_pages) << batch.page_shift};
@@ -1211,14 +1345,15 @@ cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const
   const uint64_t vstr[3] = {static_cast<uint64_t>(H_kv) * row, 128, row};
   const uint32_t vbox[4] = {64, 1u << p.vshift, static_cast<uint32_t>(d_h / 64), 1};
   if (!encode_tiled(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, Q, qdims, qstr, qbox) ||
+      !encode_tiled(&tq32, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, Q, qdims, qstr, qbox32) ||
       !encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, K_pages, kdims, kstr, kbox) ||
       !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, V_pages, vdims, vstr, vbox))
     return cudaErrorInvalidValue;
   if (d_h == 128)
-    return nq == 2 ? launch_cfg<128, 2, false>(tq, tk, tv, p, stream)
-                   : launch_cfg<128, 1, true>(tq, tk, tv, p, stream);
-  return batch.T_max <= 1 << p.ts ? launch_cfg<256, 1, true>(tq, tk, tv, p, stream)
-                                  : launch_cfg<256, 1, false>(tq, tk, tv, p, stream);
+    return nq == 2 ? launch_cfg<128, 2, false>(tq, tq32, tk, tv, p, stream)
+                   : launch_cfg<128, 1, true>(tq, tq32, tk, tv, p, stream);
+  return batch.T_max <= 1 << p.ts ? launch_cfg<256, 1, true>(tq, tq32, tk, tv, p, stream)
+                                  : launch_cfg<256, 1, false>(tq, tq32, tk, tv, p, stream);
 }
 
 }  // namespace g3
