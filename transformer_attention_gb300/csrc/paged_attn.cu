@@ -124,6 +124,11 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   return true;
 }
 
+// Tiles that a CTA does rather than cutting every unit in two: what the parts of
+// 128 rows and more cost, written and added (128 units of 64 tiles, 27B-shaped:
+// 118 us cut, 115 whole; of 20 tiles 59 and 53).
+__host__ __device__ constexpr int uncut_tiles(int nq) { return nq == 2 ? 16 : 8; }
+
 template <int DH, int NQ_>
 struct Cfg {
   static constexpr int NQ = NQ_;
@@ -138,9 +143,6 @@ struct Cfg {
   // rows alone, and where units of chunks and of steps meet (4B-shaped mixed
   // batch: 103 us with 1, 81 with 4, 74 with 12).
   static constexpr int UC1 = 3, UCG = NQ == 2 ? 5 : 10;
-  // Tiles that a CTA does rather than cutting every unit in two: what the parts
-  // of 128 rows and more cost, written and added.
-  [[maybe_unused]] static constexpr int WHOLE = NQ == 2 ? 16 : 8;
   static constexpr int THREADS = 384;
   // the control warps give registers to the others
   static constexpr int REGS_LAUNCH = 168, REGS_CTRL = NQ == 2 ? 104 : 120, REGS_SOFT = NQ == 2 ? 200 : 216;
@@ -156,6 +158,7 @@ struct Params {
   Split* split;           // [grid]
   void* O;
   int o_f16, H, H_kv, gshift, window, ts, tokbox, rows, qsmall, vshift;   // ts: log2 of a unit's tokens, vshift: of a V box's slots
+  uint32_t zero;          // 0, which the compiler does not know
   int* status;
 };
 
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
 #pragma unroll
     for (int w = 0; w < C::THREADS / 32; ++w) longest = max(longest, sh.warp_most[w]);
     const long long per_cta = (all + static_cast<long long>(grid) * TC - 1) / (static_cast<long long>(grid) * TC);
-    uncut = units <= grid && longest <= per_cta + C::WHOLE;
+    uncut = units <= grid && longest <= per_cta + uncut_tiles(NQ);
     if (p.window == 0 && all > 0 && !uncut) S = static_cast<int>(per_cta);
     mine = 0;
     __syncthreads();
@@ -436,12 +439,15 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   auto wait_warp = [&](uint64_t& bar, uint32_t parity, int site) -> bool {
     return __all_sync(0xffffffffu, wait_bar(smem_u32(&bar), parity, &sh.abort_flag, site, &lost_site));
   };
-  // The next piece (whole warp); false at the end.
+  // The next piece (whole warp); false at the end.  The release takes in every
+  // word that was loaded (p.zero: 0, which the compiler does not know): it must
+  // not overtake the loads.
   auto take = [&](int k, Piece& pc) -> bool {
     if (!wait_warp(sh.piece_full[k % NPC], (k / NPC) & 1, kSitePieceFull)) return false;
     pc = sh.piece[k % NPC];
+    const int all = pc.b ^ pc.j ^ pc.row0 ^ pc.ntok ^ pc.i0 ^ pc.n ^ pc.len ^ pc.lo ^ pc.hi ^ pc.tile0 ^ pc.tiles ^ pc.slot;
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sh.piece_empty[k % NPC]));
+    if (lane == 0) mbar_arrive(smem_u32(&sh.piece_empty[k % NPC]) + (static_cast<uint32_t>(all) & p.zero));
     return pc.tiles > 0;
   };
 
@@ -912,7 +918,9 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         if (!ok) break;
         const float2 st = sh.stat[np & 1][r];
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.stat_empty[np & 1]));
+        if (lane == 0)   // (as in take)
+          mbar_arrive(smem_u32(&sh.stat_empty[np & 1]) +
+                      ((__float_as_uint(st.x) ^ __float_as_uint(st.y)) & p.zero));
         ok = epilogue(pc, st.x, st.y, np);
       }
     } else {
@@ -1326,6 +1334,7 @@ cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const
   p.tokbox = std::min(BM / G, batch.T_max);
   p.rows = part_rows(batch.T_max, G, d_h);
   p.qsmall = nq == 1 && p.tokbox * G <= 32 ? 1 : 0;
+  p.zero = 0;
   p.status = status;
   // Q [M, H, d_h]: box {64 channels, G heads, tokens}; rows behind M read as zeros.
   CUtensorMap tq, tq32, tk, tv;   // tq32: units of few tokens, 32 rows at most
