@@ -458,12 +458,14 @@ int gemma3_attn_forward_cached8(const gemma3_attn_dims* dims, int S, int end_ind
  * ancestors among the new tokens).
  *   The arrays lie on the device and are read when the kernels run, so that a
  * captured call can be replayed with others.  The kernels check them: a
- * sequence whose rows (not ascending, beyond M, more than T_max) or slots
- * (negative, beyond max_pages * page_size) do not fit counts as one without
- * new tokens, a parent that is not an earlier token as -1, a page outside the
- * pool is neither written nor read, and GEMMA3_ERR_BAD_INPUT comes from
- * gemma3_attn_check_status.  Entries of the page table behind a sequence's last
- * slot are not looked at. */
+ * sequence whose rows (beyond M, more than T_max) or slots (negative, beyond
+ * max_pages * page_size) do not fit counts as one without new tokens, a parent
+ * that is not an earlier token as -1, a page outside the pool is neither
+ * written nor read, and GEMMA3_ERR_BAD_INPUT comes from
+ * gemma3_attn_check_status (of what a call looks at: parents by the calls that
+ * use them, pages of the slots it reads or writes).  Where row_start falls, it
+ * is open besides which rows have a sequence.  Entries of the page table behind
+ * a sequence's last slot are not looked at. */
 typedef struct {
   int B, M, T_max;                     /* sequences, packed rows, most new tokens of a sequence */
   int page_size, n_pages, max_pages;   /* max_pages: entries of a sequence in page_table */

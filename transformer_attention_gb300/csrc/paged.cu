@@ -48,14 +48,23 @@ __device__ __forceinline__ PagedToken paged_token(const PagedBatch& p, int m, in
   return t;
 }
 
+// Rows find their sequence by the first rows alone: the sequences that no row
+// led to are checked here, by one CTA.
+__device__ __forceinline__ void check_sequences(const PagedBatch& p, int* status) {
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) paged_seq(p, b, status);
+}
+
 __global__ void __launch_bounds__(128)
     paged_positions_kernel(const PagedBatch p, int32_t* __restrict__ pos, int* status) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const int m = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (m >= p.M) return;
-  const PagedToken t = paged_token(p, m, lane, status);
-  if (lane == 0) pos[m] = t.seq >= 0 ? t.len + t.depth : 0;
+  if (m < p.M) {
+    const PagedToken t = paged_token(p, m, lane, status);
+    if (lane == 0) pos[m] = t.seq >= 0 ? t.len + t.depth : 0;
+  }
+  check_sequences(p, status);
 }
 
 struct AppendParams {
@@ -234,6 +243,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
       if (item < items) load(m0, t);
     }
   }
+  check_sequences(p, a.status);
 }
 
 // ---------------------------------------------------------------- commit
