@@ -35,6 +35,7 @@
 // Slots outside [lo, hi) of a unit are zeroed in V's tile, so that what they
 // hold (a NaN, say) cannot reach O through a zero probability.
 #include <algorithm>
+#include <mutex>
 
 #include "attention_common.cuh"
 #include "paged.cuh"
@@ -59,6 +60,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_THRESHOLD = 8.0f, P_SHIFT = 7.0f;
 constexpr int kMaxCtas = 160;               // CTAs of a launch at most (workspace)
 constexpr int NPC = 4;                      // ring of pieces
+constexpr int kMaxCluster = 8, kMergeTiles = 3;
 
 enum : int {
   kSiteQFull = 100, kSiteQEmpty, kSitePartFull, kSitePartEmpty, kSiteSFull, kSitePFull, kSitePvDone,
@@ -100,6 +102,7 @@ struct Shared {
   int warp_most[12];
   long long start_off, start_base;   // of this CTA's share in its first sequence, which begins there
   int start_taken;        // whole shares before that sequence
+  int unit_rows, unit_row0, unit_parts;   // of the cluster's unit
   int start_b, first_used, first_j;   // first_used: cost of the piece that is there already
   PagedSeq start_seq;
   uint32_t tmem;
@@ -199,13 +202,63 @@ __device__ __forceinline__ uint32_t bits_at(uint64_t m, int d) {
   return d > -32 ? static_cast<uint32_t>(m << -d) : 0u;
 }
 
-// ONE: the new tokens of every sequence fit one unit per head.
-template <int DH, int NQ, bool ONE>
+// A lane's running sums: reference, sum, VV vectors.
+template <int VV>
+struct MergeAcc {
+  float m = -INFINITY, l = 0.f;
+  float4 o[VV];
+
+  __device__ __forceinline__ void add(float2 st, const float4 (&x)[VV]) {
+    if (st.y == 0.f) return;                       // saw nothing
+    const float to = fmaxf(m, st.x);
+    const float fm = m == to ? 1.f : ex2(m - to), fx = ex2(st.x - to);
+    m = to;
+    l = l * fm + st.y * fx;
+#pragma unroll
+    for (int v = 0; v < VV; ++v) {
+      o[v].x = o[v].x * fm + x[v].x * fx;
+      o[v].y = o[v].y * fm + x[v].y * fx;
+      o[v].z = o[v].z * fm + x[v].z * fx;
+      o[v].w = o[v].w * fm + x[v].w * fx;
+    }
+  }
+
+  // A vector's four channels over the sum, packed.
+  __device__ __forceinline__ uint2 packed(int v, float inv, int f16) const {
+    const float a = o[v].x * inv, b = o[v].y * inv, c = o[v].z * inv, d = o[v].w * inv;
+    return f16 ? make_uint2(pack_half2(a, b), pack_half2(c, d)) : make_uint2(pack_bf162(a, b), pack_bf162(c, d));
+  }
+};
+
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// How a launch's CTAs take their work.
+enum : int {
+  kAnyUnits,      // equal shares of all units' work
+  kOneUnit,       // the same where the new tokens of every sequence fit one unit per head
+  kClusterUnit    // one unit per cluster, whose CTAs add their parts through distributed shared memory
+};
+
+template <int DH, int NQ, int MODE>
 __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ32,
                       const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const Params p) {
   using C = Cfg<DH, NQ>;
+  constexpr bool ONE = MODE != kAnyUnits, CLUSTER = MODE == kClusterUnit;
+  static_assert(NQ == 1 || !CLUSTER, "few rows");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedBatch& batch = p.batch;
   const bool tree = batch.parents != nullptr;
@@ -263,7 +316,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   // besides its tiles.  Tile t of a unit is in the share that holds the unit's
   // position kUnitCost + t kTileCost.
   constexpr int TC = kTileCost, UC = ONE ? C::UC1 : C::UCG;
-  const int per = (batch.B + C::THREADS - 1) / C::THREADS;   // sequences per thread
+  const int per = CLUSTER ? 0 : (batch.B + C::THREADS - 1) / C::THREADS;   // sequences per thread
   int S = 0;                  // tiles of a whole share (0: there are none)
   bool uncut = false;         // every unit is one CTA's share
   // whole shares of every unit of a sequence
@@ -309,7 +362,13 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     seq = paged_seq(batch, b, p.status);
     mine += p.H_kv * head_cost(seq);
   }
-  long long total = scan(mine, upto, lost);
+  long long total = 0;
+  if constexpr (CLUSTER) {
+    upto = 0;
+    __syncthreads();
+  } else {
+    total = scan(mine, upto, lost);
+  }
   tc_fence_after();
   const uint32_t tbase = sh.tmem;
   if (total < 0) {
@@ -433,7 +492,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       }
     }
   }
-  __syncthreads();
+  if constexpr (!CLUSTER) __syncthreads();
 
   int lost_site = 0;
   auto wait_warp = [&](uint64_t& bar, uint32_t parity, int site) -> bool {
@@ -753,6 +812,21 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
           split.parts += last - split.rest + 1;
         }
       };
+      if constexpr (CLUSTER) {
+        // ---- this CTA's part of the cluster's unit
+        const int cs = cluster_nctarank(), rank = cluster_ctarank(), unit = blockIdx.x / cs;
+        const int seq_b = unit / p.H_kv, j = unit - seq_b * p.H_kv;
+        const PagedSeq s = paged_seq(batch, seq_b, p.status);
+        const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, 0);
+        const int tiles = s.n > 0 && !lost ? u.tiles : 0, each = tiles / cs, more = tiles - each * cs;
+        const int n = each + (rank < more ? 1 : 0);
+        if (lane == 0) {
+          sh.unit_rows = s.n << p.gshift;
+          sh.unit_row0 = s.row0;
+          sh.unit_parts = min(tiles, cs);
+        }
+        if (n > 0) publish(make_piece(s, seq_b, j, 0, u, rank * each + min(rank, more), n));
+      }
       int passed = idle ? 0 : sh.start_taken;   // whole shares before the present sequence
       if (!ONE && sharing) {
         // ---- one whole share
@@ -857,7 +931,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         ++b;
         passed += p.H_kv * nq * whole;
       }
-      if (lane == 0) p.split[blockIdx.x] = split;   // (read by the merge)
+      if (!CLUSTER && lane == 0) p.split[blockIdx.x] = split;   // (read by the merge)
       if (ok) publish(Piece{});
       // (every load that was issued lands before the CTA may exit)
       for (int i = max(0, k - (p.qsmall ? 2 : 1)); i < k; ++i)
@@ -878,13 +952,15 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       const bool live = __any_sync(0xffffffffu, row_valid);
       if (live) {
         tc_fence_after();
-        const bool whole = pc.slot < 0, have = row_valid && l != 0.f;
+        const bool whole = !CLUSTER && pc.slot < 0, have = row_valid && l != 0.f;
         const size_t orow = static_cast<size_t>(pc.row0 + tok) * p.H + (pc.j << p.gshift) +
                             (r & ((1 << p.gshift) - 1));
         const size_t slot = max(pc.slot, 0);
-        float4* pdst = p.part + slot * (DH / 4) * p.rows + e * BM + r;
+        // (a cluster's parts lie where the ring was: its last copies are read)
+        float4* pdst = (CLUSTER ? reinterpret_cast<float4*>(sP) : p.part + slot * (DH / 4) * p.rows) + e * BM + r;
+        float2* sdst = (CLUSTER ? reinterpret_cast<float2*>(sP + p.rows * DH * 4) : p.pstat + slot * p.rows) + e * BM + r;
         if (!whole && row_valid)
-          p.pstat[slot * p.rows + e * BM + r] = have ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
+          *sdst = have ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
         const float inv = have ? 1.f / l : 0.f;
 #pragma unroll 1
         for (int c = 0; c < DH / 32; ++c) {
@@ -1066,6 +1142,41 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     }
   }
   if (lost_site != 0) record_error(p.status, kDevErrTimeoutBase + lost_site);
+  if constexpr (CLUSTER) {
+    // The cluster's parts: each CTA adds a share of the rows' 4-channel vectors.
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 4) {
+      const int cs = cluster_nctarank(), rank = cluster_ctarank(), unit = blockIdx.x / cs;
+      const int j = unit - unit / p.H_kv * p.H_kv, rows = sh.unit_rows, parts = sh.unit_parts;
+      const uint32_t o_at = smem_u32(sP), st_at = o_at + p.rows * DH * 4;
+      const int all = parts > 0 ? rows * (DH / 4) : 0;
+      for (int i = rank * 256 + tid - 128; i < all; i += cs * 256) {
+        const int c = i / rows, r = i - c * rows;
+        MergeAcc<1> acc;
+        acc.o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x0 = 0; x0 < parts; x0 += 4) {
+          float2 st[4];
+          float4 x[4][1];
+#pragma unroll
+          for (int x1 = 0; x1 < 4; ++x1)
+            if (x0 + x1 < parts) {
+              st[x1] = ld_cluster_f2(mapa_shared(st_at + r * 8, x0 + x1));
+              x[x1][0] = ld_cluster_f4(mapa_shared(o_at + (c * p.rows + r) * 16, x0 + x1));
+            }
+#pragma unroll
+          for (int x1 = 0; x1 < 4; ++x1)
+            if (x0 + x1 < parts) acc.add(st[x1], x[x1]);
+        }
+        const float inv = acc.l != 0.f ? 1.f / acc.l : 0.f;
+        const size_t orow = static_cast<size_t>(sh.unit_row0 + (r >> p.gshift)) * p.H + (j << p.gshift) +
+                            (r & ((1 << p.gshift) - 1));
+        reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * DH)[c] = acc.packed(0, inv, p.o_f16);
+      }
+    }
+    __syncwarp();
+    cluster_sync();       // no CTA leaves while another reads its shared memory
+  }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -1079,28 +1190,6 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
 // along 4-channel vectors too.  A lane has its row's sums to itself, so a task
 // is one warp's, or that of several where a unit has many parts.
 constexpr int kMergeWarps = 8;
-
-// A lane's running sums: reference, sum, VV vectors.
-template <int VV>
-struct MergeAcc {
-  float m = -INFINITY, l = 0.f;
-  float4 o[VV];
-
-  __device__ __forceinline__ void add(float2 st, const float4 (&x)[VV]) {
-    if (st.y == 0.f) return;                       // saw nothing
-    const float to = fmaxf(m, st.x);
-    const float fm = m == to ? 1.f : ex2(m - to), fx = ex2(st.x - to);
-    m = to;
-    l = l * fm + st.y * fx;
-#pragma unroll
-    for (int v = 0; v < VV; ++v) {
-      o[v].x = o[v].x * fm + x[v].x * fx;
-      o[v].y = o[v].y * fm + x[v].y * fx;
-      o[v].z = o[v].z * fm + x[v].z * fx;
-      o[v].w = o[v].w * fm + x[v].w * fx;
-    }
-  }
-};
 
 struct MergeShared {
   int upto[kMaxCtas];            // tasks of the units that start in CTAs 0 .. i
@@ -1198,11 +1287,7 @@ __device__ __forceinline__ void merge_tasks(const Params& p, MergeShared& sh, co
       uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * DH) + v0;
       uint2 w[VV];
 #pragma unroll
-      for (int v = 0; v < VV; ++v) {
-        const float a = acc.o[v].x * inv, b = acc.o[v].y * inv, c = acc.o[v].z * inv, d = acc.o[v].w * inv;
-        w[v] = p.o_f16 ? make_uint2(pack_half2(a, b), pack_half2(c, d))
-                       : make_uint2(pack_bf162(a, b), pack_bf162(c, d));
-      }
+      for (int v = 0; v < VV; ++v) w[v] = acc.packed(v, inv, p.o_f16);
       if constexpr (VV == 2) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
       else dst[0] = w[0];
     }
@@ -1287,24 +1372,91 @@ Layout layout(int T_max, int H, int H_kv, int d_h) {
   return l;
 }
 
-template <int DH, int NQ, bool ONE>
+template <int DH, int NQ, int MODE>
+cudaError_t prepare_cfg() {
+  using C = Cfg<DH, NQ>;
+  int regs = 0;
+  const void* kern = reinterpret_cast<const void*>(paged_attn_kernel<DH, NQ, MODE>);
+  if (cudaError_t e = prepare_kernel(kern, C::SMEM, &regs)) return e;
+  // The warpgroups' register increase waits for the registers the control
+  // warps give up: launch only when the split fits.
+  return regs * C::THREADS < C::REGS_SPLIT ? cudaErrorInvalidConfiguration : cudaSuccess;
+}
+
+template <int DH, int NQ, int MODE>
 cudaError_t launch_cfg(const CUtensorMap& tq, const CUtensorMap& tq32, const CUtensorMap& tk, const CUtensorMap& tv,
                        const Params& p, cudaStream_t stream) {
   using C = Cfg<DH, NQ>;
-  auto kern = paged_attn_kernel<DH, NQ, ONE>;
-  int regs = 0;
-  if (cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, &regs)) return e;
-  // The warpgroups' register increase waits for the registers the control
-  // warps give up: launch only when the split fits.
-  if (regs * C::THREADS < C::REGS_SPLIT) return cudaErrorInvalidConfiguration;
+  if (cudaError_t e = prepare_cfg<DH, NQ, MODE>()) return e;
   const int ctas = std::min(num_sms(), kMaxCtas);
-  if (cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, tq, tq32, tk, tv, p)) return e;
+  if (cudaError_t e = launch_pdl(paged_attn_kernel<DH, NQ, MODE>, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, tq,
+                                 tq32, tk, tv, p))
+    return e;
   if (p.rows <= kMergeDirect) {
     const int tasks = (DH / 4 * kMergeDirect) / 32;   // at most
     return launch_pdl(paged_merge_few_kernel<DH>, dim3(ctas, std::min(tasks, 4)), dim3(32 * kMergeWarps), 0,
                       stream, p);
   }
   return launch_pdl(paged_merge_kernel<DH>, dim3(3 * ctas), dim3(32 * kMergeWarps), 0, stream, p, ctas);
+}
+
+// Clusters of `size` CTAs that the device holds at once, asked once per device.
+template <int DH>
+int clusters_at_once(int size) {
+  constexpr int kDevices = 64;
+  static std::mutex mu;
+  static int known[kDevices][kMaxCluster + 1];   // plus one; 0: not asked
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  int& k = known[dev][size];
+  if (k == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(Cfg<DH, 1>::THREADS);
+    cfg.dynamicSmemBytes = Cfg<DH, 1>::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, paged_attn_kernel<DH, 1, kClusterUnit>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    k = n + 1;
+  }
+  return k - 1;
+}
+
+// CTAs of a unit's cluster, or 0: equal shares.  What a unit's tiles can be at
+// most is known here from the window and the page table's width; the equal
+// shares take fewer tiles per CTA and a merge, which costs kMergeTiles of them.
+template <int DH>
+int cluster_size(const Params& p) {
+  const PagedBatch& b = p.batch;
+  const long long units = static_cast<long long>(b.B) * p.H_kv;
+  long long most = (static_cast<long long>(b.max_pages) << b.page_shift) / BN + 1;
+  if (p.window > 0) most = std::min(most, (static_cast<long long>(p.window) + b.T_max) / BN + 2);
+  const int sms = num_sms();
+  if (units > sms || prepare_cfg<DH, 1, kClusterUnit>() != cudaSuccess) return 0;
+  for (int size = static_cast<int>(std::min<long long>(kMaxCluster, std::min(most, sms / units))); size >= 1; --size) {
+    if ((most + size - 1) / size > units * most / sms + kMergeTiles) return 0;
+    if (units <= clusters_at_once<DH>(size)) return size;
+  }
+  return 0;
+}
+
+template <int DH>
+cudaError_t launch_one(const CUtensorMap& tq, const CUtensorMap& tq32, const CUtensorMap& tk, const CUtensorMap& tv,
+                       const Params& p, cudaStream_t stream) {
+  using C = Cfg<DH, 1>;
+  const int size = cluster_size<DH>(p);
+  if (size == 0) return launch_cfg<DH, 1, kOneUnit>(tq, tq32, tk, tv, p, stream);
+  return launch_pdl_cluster(paged_attn_kernel<DH, 1, kClusterUnit>, dim3(p.batch.B * p.H_kv * size), dim3(C::THREADS),
+                            C::SMEM, size, stream, tq, tq32, tk, tv, p);
 }
 
 }  // namespace
@@ -1359,10 +1511,10 @@ cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const
       !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, V_pages, vdims, vstr, vbox))
     return cudaErrorInvalidValue;
   if (d_h == 128)
-    return nq == 2 ? launch_cfg<128, 2, false>(tq, tq32, tk, tv, p, stream)
-                   : launch_cfg<128, 1, true>(tq, tq32, tk, tv, p, stream);
-  return batch.T_max <= 1 << p.ts ? launch_cfg<256, 1, true>(tq, tq32, tk, tv, p, stream)
-                                  : launch_cfg<256, 1, false>(tq, tq32, tk, tv, p, stream);
+    return nq == 2 ? launch_cfg<128, 2, kAnyUnits>(tq, tq32, tk, tv, p, stream)
+                   : launch_one<128>(tq, tq32, tk, tv, p, stream);
+  return batch.T_max <= 1 << p.ts ? launch_one<256>(tq, tq32, tk, tv, p, stream)
+                                  : launch_cfg<256, 1, kAnyUnits>(tq, tq32, tk, tv, p, stream);
 }
 
 }  // namespace g3
