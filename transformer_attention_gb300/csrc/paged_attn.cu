@@ -60,7 +60,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_THRESHOLD = 8.0f, P_SHIFT = 7.0f;
 constexpr int kMaxCtas = 160;               // CTAs of a launch at most (workspace)
 constexpr int NPC = 4;                      // ring of pieces
-constexpr int kMaxCluster = 8, kMergeTiles = 3;
+constexpr int kMaxCluster = 16, kMergeTiles = 3;
 
 enum : int {
   kSiteQFull = 100, kSiteQEmpty, kSitePartFull, kSitePartEmpty, kSiteSFull, kSitePFull, kSitePvDone,
@@ -1411,6 +1411,8 @@ int clusters_at_once(int size) {
   std::lock_guard<std::mutex> lock(mu);
   int& k = known[dev][size];
   if (k == 0) {
+    // (more than 8 CTAs: as large a cluster as the device allows)
+    cudaFuncSetAttribute(paged_attn_kernel<DH, 1, kClusterUnit>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(size);
     cfg.blockDim = dim3(Cfg<DH, 1>::THREADS);
