@@ -60,7 +60,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_THRESHOLD = 8.0f, P_SHIFT = 7.0f;
 constexpr int kMaxCtas = 160;               // CTAs of a launch at most (workspace)
 constexpr int NPC = 4;                      // ring of pieces
-constexpr int kMaxCluster = 16, kMergeTiles = 3;
+constexpr int kMaxCluster = 16, kMergeTiles = 4;
 
 enum : int {
   kSiteQFull = 100, kSiteQEmpty, kSitePartFull, kSitePartEmpty, kSiteSFull, kSitePFull, kSitePvDone,
@@ -127,10 +127,11 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   return true;
 }
 
-// Tiles that a CTA does rather than cutting every unit in two: what the parts of
-// 128 rows and more cost, written and added (128 units of 64 tiles, 27B-shaped:
-// 118 us cut, 115 whole; of 20 tiles 59 and 53).
-__host__ __device__ constexpr int uncut_tiles(int nq) { return nq == 2 ? 16 : 8; }
+// Tiles that a CTA does rather than having the units cut into `parts`: a part of
+// 128 x 256 or 256 x 128 sums takes 65 ns of the device, written and added, a
+// tile 1.6 us (128 units of 64 tiles, 27B-shaped: 118 us cut, 115 whole; of 20
+// tiles 59 and 53).
+__host__ __device__ constexpr int uncut_tiles(int parts) { return 3 + parts / 24; }
 
 template <int DH, int NQ_>
 struct Cfg {
@@ -161,6 +162,7 @@ struct Params {
   Split* split;           // [grid]
   void* O;
   int o_f16, H, H_kv, gshift, window, ts, tokbox, rows, qsmall, vshift;   // ts: log2 of a unit's tokens, vshift: of a V box's slots
+  int units;              // of a head, where clusters take them
   uint32_t zero;          // 0, which the compiler does not know
   int* status;
 };
@@ -248,7 +250,8 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 enum : int {
   kAnyUnits,      // equal shares of all units' work
   kOneUnit,       // the same where the new tokens of every sequence fit one unit per head
-  kClusterUnit    // one unit per cluster, whose CTAs add their parts through distributed shared memory
+  kClusterUnit    // one unit of one query tile per cluster, whose CTAs add their parts through distributed
+                  // shared memory
 };
 
 template <int DH, int NQ, int MODE>
@@ -402,7 +405,8 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
 #pragma unroll
     for (int w = 0; w < C::THREADS / 32; ++w) longest = max(longest, sh.warp_most[w]);
     const long long per_cta = (all + static_cast<long long>(grid) * TC - 1) / (static_cast<long long>(grid) * TC);
-    uncut = units <= grid && longest <= per_cta + uncut_tiles(NQ);
+    uncut = units <= grid &&
+            longest <= per_cta + uncut_tiles(static_cast<int>(min(all / TC, grid + units)));
     if (p.window == 0 && all > 0 && !uncut) S = static_cast<int>(per_cta);
     mine = 0;
     __syncthreads();
@@ -815,17 +819,23 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       if constexpr (CLUSTER) {
         // ---- this CTA's part of the cluster's unit
         const int cs = cluster_nctarank(), rank = cluster_ctarank(), unit = blockIdx.x / cs;
-        const int seq_b = unit / p.H_kv, j = unit - seq_b * p.H_kv;
+        const int head = unit / p.units, q = unit - head * p.units;
+        const int seq_b = head / p.H_kv, j = head - seq_b * p.H_kv;
         const PagedSeq s = paged_seq(batch, seq_b, p.status);
-        const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, 0);
-        const int tiles = s.n > 0 && !lost ? u.tiles : 0, each = tiles / cs, more = tiles - each * cs;
+        const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, q);
+        const bool none = lost || q << p.ts >= s.n;    // no such unit in the sequence
+        const int tiles = none ? 0 : u.tiles, each = tiles / cs, more = tiles - each * cs;
         const int n = each + (rank < more ? 1 : 0);
         if (lane == 0) {
-          sh.unit_rows = s.n << p.gshift;
-          sh.unit_row0 = s.row0;
+          sh.unit_rows = min(1 << p.ts, s.n - (q << p.ts)) << p.gshift;
+          sh.unit_row0 = s.row0 + (q << p.ts);
           sh.unit_parts = min(tiles, cs);
         }
-        if (n > 0) publish(make_piece(s, seq_b, j, 0, u, rank * each + min(rank, more), n));
+        if (n > 0) {
+          Piece pc = make_piece(s, seq_b, j, q, u, rank * each + min(rank, more), n);
+          pc.slot = cs > 1 ? 0 : -1;
+          publish(pc);
+        }
       }
       int passed = idle ? 0 : sh.start_taken;   // whole shares before the present sequence
       if (!ONE && sharing) {
@@ -952,7 +962,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       const bool live = __any_sync(0xffffffffu, row_valid);
       if (live) {
         tc_fence_after();
-        const bool whole = !CLUSTER && pc.slot < 0, have = row_valid && l != 0.f;
+        const bool whole = pc.slot < 0, have = row_valid && l != 0.f;
         const size_t orow = static_cast<size_t>(pc.row0 + tok) * p.H + (pc.j << p.gshift) +
                             (r & ((1 << p.gshift) - 1));
         const size_t slot = max(pc.slot, 0);
@@ -1144,11 +1154,12 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   if (lost_site != 0) record_error(p.status, kDevErrTimeoutBase + lost_site);
   if constexpr (CLUSTER) {
     // The cluster's parts: each CTA adds a share of the rows' 4-channel vectors.
+    const int cs = cluster_nctarank();
     __syncwarp();
-    cluster_sync();
-    if (warp >= 4) {
-      const int cs = cluster_nctarank(), rank = cluster_ctarank(), unit = blockIdx.x / cs;
-      const int j = unit - unit / p.H_kv * p.H_kv, rows = sh.unit_rows, parts = sh.unit_parts;
+    if (cs > 1) cluster_sync();
+    if (warp >= 4 && cs > 1) {
+      const int rank = cluster_ctarank(), head = static_cast<int>(blockIdx.x) / cs / p.units;
+      const int j = head % p.H_kv, rows = sh.unit_rows, parts = sh.unit_parts;
       const uint32_t o_at = smem_u32(sP), st_at = o_at + p.rows * DH * 4;
       const int all = parts > 0 ? rows * (DH / 4) : 0;
       for (int i = rank * 256 + tid - 128; i < all; i += cs * 256) {
@@ -1175,7 +1186,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       }
     }
     __syncwarp();
-    cluster_sync();       // no CTA leaves while another reads its shared memory
+    if (cs > 1) cluster_sync();   // no CTA leaves while another reads its shared memory
   }
   __syncthreads();
   if (warp == 1) {
@@ -1439,26 +1450,37 @@ int clusters_at_once(int size) {
 template <int DH>
 int cluster_size(const Params& p) {
   const PagedBatch& b = p.batch;
-  const long long units = static_cast<long long>(b.B) * p.H_kv;
+  const long long units = static_cast<long long>(b.B) * p.H_kv * p.units;
   long long most = (static_cast<long long>(b.max_pages) << b.page_shift) / BN + 1;
-  if (p.window > 0) most = std::min(most, (static_cast<long long>(p.window) + b.T_max) / BN + 2);
+  if (p.window > 0) {
+    const int reach = b.parents != nullptr ? b.T_max : std::min(b.T_max, 1 << p.ts);
+    most = std::min(most, (static_cast<long long>(p.window) + reach) / BN + 2);
+  }
+  // What equal shares would take per CTA: of an uneven batch at most so many
+  // units have tokens, and where only the table bounds the lengths of several
+  // sequences, half of it is taken to be filled (8 steps over 100 to 6000 slots,
+  // 12B-shaped: 52 us by clusters, 28 shared out; over 3000 each 24 and 27).
+  const long long filled = std::min(units, ((b.M >> p.ts) + static_cast<long long>(b.B)) * p.H_kv);
+  const bool open = b.B > 1 && p.window == 0;
   const int sms = num_sms();
   if (units > sms || prepare_cfg<DH, 1, kClusterUnit>() != cudaSuccess) return 0;
   for (int size = static_cast<int>(std::min<long long>(kMaxCluster, std::min(most, sms / units))); size >= 1; --size) {
-    if ((most + size - 1) / size > units * most / sms + kMergeTiles) return 0;
+    if ((most + size - 1) / size > filled * most / (open ? 2 * sms : sms) + kMergeTiles) return 0;
     if (units <= clusters_at_once<DH>(size)) return size;
   }
   return 0;
 }
 
+// One query tile per unit: by clusters where that is faster; *done says so.
 template <int DH>
-cudaError_t launch_one(const CUtensorMap& tq, const CUtensorMap& tq32, const CUtensorMap& tk, const CUtensorMap& tv,
-                       const Params& p, cudaStream_t stream) {
+cudaError_t launch_clusters(const CUtensorMap& tq, const CUtensorMap& tq32, const CUtensorMap& tk,
+                            const CUtensorMap& tv, const Params& p, cudaStream_t stream, bool* done) {
   using C = Cfg<DH, 1>;
   const int size = cluster_size<DH>(p);
-  if (size == 0) return launch_cfg<DH, 1, kOneUnit>(tq, tq32, tk, tv, p, stream);
-  return launch_pdl_cluster(paged_attn_kernel<DH, 1, kClusterUnit>, dim3(p.batch.B * p.H_kv * size), dim3(C::THREADS),
-                            C::SMEM, size, stream, tq, tq32, tk, tv, p);
+  *done = size > 0;
+  if (size == 0) return cudaSuccess;
+  return launch_pdl_cluster(paged_attn_kernel<DH, 1, kClusterUnit>, dim3(p.batch.B * p.H_kv * p.units * size),
+                            dim3(C::THREADS), C::SMEM, size, stream, tq, tq32, tk, tv, p);
 }
 
 }  // namespace
@@ -1489,6 +1511,7 @@ cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const
   p.rows = part_rows(batch.T_max, G, d_h);
   p.qsmall = nq == 1 && p.tokbox * G <= 32 ? 1 : 0;
   p.zero = 0;
+  p.units = 1;
   p.status = status;
   // Q [M, H, d_h]: box {64 channels, G heads, tokens}; rows behind M read as zeros.
   CUtensorMap tq, tq32, tk, tv;   // tq32: units of few tokens, 32 rows at most
@@ -1512,10 +1535,19 @@ cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const
       !encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, K_pages, kdims, kstr, kbox) ||
       !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, V_pages, vdims, vstr, vbox))
     return cudaErrorInvalidValue;
+  // Clusters work on units of one query tile.
+  Params one = p;
+  one.ts = kTileShift - p.gshift;
+  one.rows = static_cast<int>(std::min<long long>(static_cast<long long>(batch.T_max) * G, BM));
+  one.units = paged_units(batch.T_max, one.ts);
+  bool done = false;
+  const cudaError_t e = d_h == 128 ? launch_clusters<128>(tq, tq32, tk, tv, one, stream, &done)
+                                   : launch_clusters<256>(tq, tq32, tk, tv, one, stream, &done);
+  if (e != cudaSuccess || done) return e;
   if (d_h == 128)
     return nq == 2 ? launch_cfg<128, 2, kAnyUnits>(tq, tq32, tk, tv, p, stream)
-                   : launch_one<128>(tq, tq32, tk, tv, p, stream);
-  return batch.T_max <= 1 << p.ts ? launch_one<256>(tq, tq32, tk, tv, p, stream)
+                   : launch_cfg<128, 1, kOneUnit>(tq, tq32, tk, tv, p, stream);
+  return batch.T_max <= 1 << p.ts ? launch_cfg<256, 1, kOneUnit>(tq, tq32, tk, tv, p, stream)
                                   : launch_cfg<256, 1, kAnyUnits>(tq, tq32, tk, tv, p, stream);
 }
 
