@@ -465,7 +465,8 @@ int gemma3_attn_forward_cached8(const gemma3_attn_dims* dims, int S, int end_ind
  * gemma3_attn_check_status (of what a call looks at: parents by the calls that
  * use them, pages of the slots it reads or writes).  Where row_start falls, it
  * is open besides which rows have a sequence.  Entries of the page table behind
- * a sequence's last slot are not looked at. */
+ * a sequence's last slot are not looked at, nor on a local layer those of pages
+ * that lie before the window of all of its new tokens. */
 typedef struct {
   int B, M, T_max;                     /* sequences, packed rows, most new tokens of a sequence */
   int page_size, n_pages, max_pages;   /* max_pages: entries of a sequence in page_table */
@@ -530,8 +531,9 @@ int gemma3_paged_attention(const gemma3_paged_batch* batch, const void* Q, const
  *   counts    [B] int32, 0 <= counts[b] <= new tokens; NULL: all of them
  *   new_lens  [B] int32, must not overlap batch->lens: lens[b] + counts[b]
  * The accepted tokens should be a path from the root: a token's position then
- * is its new slot.  A sequence whose accepted tokens do not ascend or lie
- * outside its new ones is left as it is (GEMMA3_ERR_BAD_INPUT as above).
+ * is its new slot.  A sequence that does not fit, or whose accepted tokens do
+ * not ascend or lie outside its new ones, is left as it is, new_lens[b] =
+ * lens[b] (GEMMA3_ERR_BAD_INPUT as above).
  * batch->parents is not used. */
 int gemma3_paged_commit(const gemma3_paged_batch* batch, const int32_t* accepted,
                         const int32_t* counts, int num_layers, int H_kv, int d_h, void* K_pages,

@@ -580,3 +580,88 @@ def test_layer_after_a_recorded_error(M):
 @pytest.mark.parametrize("window", [0, 700])
 def test_shares(H_, H_kv, d_h, lens, new, tree, window):
     T.check(T.make_batch(lens, new, 32, 130, tree=tree), H_, H_kv, d_h, window, torch.float16, 131)
+
+
+# ---------------------------------------------------------------- what a call may leave out
+@pytest.mark.parametrize("P", [16, 256])
+@pytest.mark.parametrize("H_kv,d_h,lens,new,tree", [
+    (2, 128, [700, 1300, 30], [6, 1, 3], True),
+    (2, 256, [700, 1300, 30], [6, 1, 3], False),
+    (4, 128, [1500, 700], [300, 1], False),
+    (2, 256, [1500, 700], [300, 1], False),
+])
+def test_pages_given_back(P, H_kv, d_h, lens, new, tree):
+    """Pages before every window may be gone from the table."""
+    import transformer_attention_gb300 as G3
+    W = 50
+    b = T.make_batch(lens, new, P, 70, tree=tree)
+    pools = T.make_pools(b, H_kv, d_h, 71)
+    Q = T.queries(b["M"], 2 * H_kv, d_h, 72)
+    gone = dict(b, table=b["table"].clone())
+    for s, length in enumerate(lens):
+        gone["table"][s, :max(0, length - W + 1) // P] = [-1, 2 ** 31 - 1, b["n_pages"]][s]
+    got = attend(T.dev_batch(gone), Q.cuda(), [p.cuda() for p in pools],
+                 torch.empty((b["M"], 2 * H_kv, d_h), dtype=torch.float16, device="cuda"), W)
+    assert G3.gemma3_attn_check_status() == 0
+    check_rows(got.cpu(), b, Q, pools, W, torch.float16)
+
+
+@pytest.mark.parametrize("what", ["row beyond M", "negative length", "beyond the table"])
+@pytest.mark.parametrize("count", [0, 1, None])
+def test_commit_of_sequences_that_do_not_fit(what, count):
+    """Their length and slots stay as they were, the others' tokens move."""
+    import transformer_attention_gb300 as G3
+    b = T.make_batch([30, 14, 3], [6, 4, 5], 16, 73)
+    g = torch.Generator().manual_seed(74)
+    pools = [torch.randn((2, b["n_pages"], 16, 1, 128), generator=g).half() for _ in range(2)]
+    bad = dict(b, lens=b["lens"].clone(), row_start=b["row_start"].clone())
+    if what == "row beyond M":
+        bad["row_start"][3] = b["M"] + 1
+    else:
+        bad["lens"][2] = -4 if what == "negative length" else 16 * b["table"].shape[1]
+    accepted = torch.tensor([[1, 4, 0, 0, 0, 0], [0, 2, 0, 0, 0, 0], [1, 2, 0, 0, 0, 0]], dtype=torch.int32)
+    dev = [p.cuda() for p in pools]
+    counts = None if count is None else torch.tensor([2, 2, count], dtype=torch.int32, device="cuda")
+    got = G3.commit_paged_cache(T.dev_batch(bad), dev, None if count is None else accepted.cuda(), counts)
+    expect_bad_input()
+    ref, lens = PO.commit(b, pools, None if count is None else accepted, [6, 4, 0] if count is None else [2, 2, 0])
+    assert got.tolist() == lens.tolist()[:2] + [int(bad["lens"][2])]
+    assert all(torch.equal(a.cpu(), r) for a, r in zip(dev, ref))
+
+
+@pytest.mark.parametrize("window", [2 ** 30, 2 ** 30 + 1, 2 ** 31 - 1])
+@pytest.mark.parametrize("new,tree", [(3, True), (300, False)])
+def test_the_widest_windows(window, new, tree):
+    """They hide nothing."""
+    b = T.make_batch([700, 9], [new, 2], 32, 75, tree=tree)
+    pools = T.make_pools(b, H_KV, 128, 76)
+    Q = T.queries(b["M"], H, 128, 77)
+    got = attend(T.dev_batch(b), Q.cuda(), [p.cuda() for p in pools],
+                 torch.empty((b["M"], H, 128), dtype=torch.float16, device="cuda"), window)
+    check_rows(got.cpu(), b, Q, pools, 0, torch.float16)
+
+
+@pytest.mark.parametrize("T_max", [10 ** 9, 2 ** 31 - 1])
+@pytest.mark.parametrize("d_h", [128, 256])
+def test_t_max_beyond_the_rows(T_max, d_h):
+    b = dict(T.make_batch([700, 9, 40], [1, 30, 2], 32, 78), T_max=T_max)
+    pools = T.make_pools(b, H_KV, d_h, 79)
+    Q = T.queries(b["M"], H, d_h, 80)
+    for window in (0, 33):
+        got = attend(T.dev_batch(b), Q.cuda(), [p.cuda() for p in pools],
+                     torch.empty((b["M"], H, d_h), dtype=torch.float16, device="cuda"), window)
+        check_rows(got.cpu(), b, Q, pools, window, torch.float16)
+
+
+@pytest.mark.parametrize("B", [31, 32, 33, 1025, 2500])
+def test_many_sequences(B):
+    """Rows find their sequence among many, some of them without new tokens."""
+    import transformer_attention_gb300 as G3
+    g = torch.Generator().manual_seed(81)
+    new = [0, 0] + torch.randint(0, 5, (B - 2,), generator=g).tolist()
+    lens = torch.randint(0, 40, (B,), generator=g).tolist()
+    b = T.make_batch(lens, new, 16, 82, tree=True, behind=3)
+    pos = torch.full((b["M"],), -5, dtype=torch.int32, device="cuda")
+    G3.gemma3_paged_positions(T.dev_batch(b), pos)
+    assert G3.gemma3_attn_check_status() == 0
+    assert torch.equal(pos.cpu().long(), PO.positions(b, b["M"]))

@@ -278,11 +278,12 @@ __global__ void __launch_bounds__(kCommitThreads)
   if (bad) {
     if (head && tid == 0) {
       record_error(status, kDevErrBadPaged);
-      new_lens[b] = s.len;
+      new_lens[b] = __ldcg(p.lens + b);
     }
     return;
   }
-  if (head && tid == 0) new_lens[b] = s.len + count;
+  // (a sequence that does not fit, without accepted tokens: as it was)
+  if (head && tid == 0) new_lens[b] = count > 0 ? s.len + count : __ldcg(p.lens + b);
   if (path == nullptr) return;
   const size_t pool = (static_cast<size_t>(p.n_pages) << p.page_shift) * vecs;   // 16-byte vectors
   const int c = blockIdx.x * kCommitThreads + tid;

@@ -53,12 +53,15 @@ __device__ __forceinline__ int paged_row(const PagedBatch& p, int b, int s, int*
   return (page << p.page_shift) + (s & ((1 << p.page_shift) - 1));
 }
 
-// The sequence whose rows hold row m (whole warp; -1: behind the last one).
+// The sequence whose rows hold row m (whole warp; -1: behind the last one): the
+// first that ends behind m, among [b, e], of which each round leaves a 32nd.
 __device__ __forceinline__ int paged_find(const PagedBatch& p, int m, int lane) {
-  int b = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const bool before = b0 + lane < p.B && __ldcg(p.row_start + b0 + lane + 1) <= m;
-    b += __popc(__ballot_sync(0xffffffffu, before));
+  int b = 0, e = p.B;
+  while (b < e) {
+    const int step = (e - b + 31) >> 5, at = b + (lane + 1) * step - 1;
+    const int k = __popc(__ballot_sync(0xffffffffu, at < e && __ldcg(p.row_start + at + 1) <= m));
+    b += k * step;
+    e = min(e, b + step - 1);
   }
   return b < p.B ? b : -1;
 }

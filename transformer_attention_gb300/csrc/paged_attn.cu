@@ -61,6 +61,7 @@ constexpr float RESCALE_THRESHOLD = 8.0f, P_SHIFT = 7.0f;
 constexpr int kMaxCtas = 160;               // CTAs of a launch at most (workspace)
 constexpr int NPC = 4;                      // ring of pieces
 constexpr int kMaxCluster = 16, kMergeTiles = 4;
+constexpr int kMaxSlots = 1 << 30;          // of a sequence (validate_paged_sizes)
 
 enum : int {
   kSiteQFull = 100, kSiteQEmpty, kSitePartFull, kSitePartEmpty, kSiteSFull, kSitePFull, kSitePvDone,
@@ -376,6 +377,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   const uint32_t tbase = sh.tmem;
   if (total < 0) {
     if (warp == 1) tmem_dealloc(tbase, 512);
+    if (tid == 0) p.split[blockIdx.x].parts = 0;   // (the error may be cleared before the merge starts)
     return;
   }
   // Whole shares: CTAs 0 .. taken - 1.  (No window: a unit's tiles grow with
@@ -553,12 +555,12 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       int pj = 0, ptile = -1, pbase = 0;   // the tile whose V is still to come
       Piece pc;
       pc.tiles = 0;
-      int k = 0, i = 0, p_end = 0, first = 0, cur = 0, ahead = 0;
+      int k = 0, i = 0, p_begin = 0, p_end = 0, first = 0, cur = 0, ahead = 0;
       const int32_t* table = nullptr;
       // page ids, 32 at a time: lane l holds entry first + l of the sequence
       auto entries = [&](int from) -> int {
         const int at = from + lane;
-        if (at >= p_end) return -1;
+        if (at < p_begin || at >= p_end) return -1;
         const int id = __ldcg(table + at);
         if (static_cast<unsigned>(id) >= static_cast<unsigned>(batch.n_pages)) {
           record_error(p.status, kDevErrBadPaged);
@@ -574,7 +576,8 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
           i = 0;
           if (more) {
             table = batch.page_table + static_cast<size_t>(pc.b) * batch.max_pages;
-            p_end = ((pc.hi - 1) >> ps) + 1;             // pages that hold visible slots
+            p_begin = pc.lo >> ps;                       // pages that hold visible slots
+            p_end = ((pc.hi - 1) >> ps) + 1;
             first = ((pc.tile0 * BN) >> ps) - 32;
             fresh = true;
           }
@@ -823,7 +826,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         const int seq_b = head / p.H_kv, j = head - seq_b * p.H_kv;
         const PagedSeq s = paged_seq(batch, seq_b, p.status);
         const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, q);
-        const bool none = lost || q << p.ts >= s.n;    // no such unit in the sequence
+        const bool none = __any_sync(0xffffffffu, lost) || q << p.ts >= s.n;   // no such unit in the sequence
         const int tiles = none ? 0 : u.tiles, each = tiles / cs, more = tiles - each * cs;
         const int n = each + (rank < more ? 1 : 0);
         if (lane == 0) {
@@ -1315,7 +1318,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_few_kernel(const
   const bool lost = lost_work(p.status, kLostWait);   // parts may be missing
   __shared__ MergeShared sh;
   const Split u = load_split(p.split + blockIdx.x);
-  if (lost || u.parts == 0) return;
+  if (__syncthreads_or(lost) || u.parts == 0) return;
   merge_tasks<DH, 1, true>(p, sh, u, (DH / 4 * merge_pad(u.ntok << p.gshift) + 31) / 32, merge_warps(u.parts), 0);
 }
 
@@ -1489,9 +1492,12 @@ size_t paged_attention_ws_bytes(int T_max, int H, int H_kv, int d_h) {
   return layout(T_max, H, H_kv, d_h).total;
 }
 
-cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const void* K_pages,
+cudaError_t launch_paged_attention(const PagedBatch& given, const void* Q, const void* K_pages,
                                    const void* V_pages, void* O, int o_dtype, int H, int H_kv,
                                    int d_h, int window, void* ws, cudaStream_t stream, int* status) {
+  PagedBatch batch = given;
+  batch.T_max = std::min(batch.T_max, batch.M);   // (no sequence has more; the workspace is enough for fewer)
+  if (window > kMaxSlots) window = 0;             // (hides nothing; the masks' differences stay in 32 bits)
   const int G = H / H_kv, nq = query_tiles(batch.T_max, G, d_h);
   const Layout lay = layout(batch.T_max, H, H_kv, d_h);
   uint8_t* w = static_cast<uint8_t*>(ws);
@@ -1531,10 +1537,11 @@ cudaError_t launch_paged_attention(const PagedBatch& batch, const void* Q, const
   const uint64_t vstr[3] = {static_cast<uint64_t>(H_kv) * row, 128, row};
   const uint32_t vbox[4] = {64, 1u << p.vshift, static_cast<uint32_t>(d_h / 64), 1};
   if (!encode_tiled(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, Q, qdims, qstr, qbox) ||
-      !encode_tiled(&tq32, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, Q, qdims, qstr, qbox32) ||
+      (qbox32[2] != qbox[2] && !encode_tiled(&tq32, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, Q, qdims, qstr, qbox32)) ||
       !encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, K_pages, kdims, kstr, kbox) ||
       !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, V_pages, vdims, vstr, vbox))
     return cudaErrorInvalidValue;
+  if (qbox32[2] == qbox[2]) tq32 = tq;
   // Clusters work on units of one query tile.
   Params one = p;
   one.ts = kTileShift - p.gshift;
