@@ -32,8 +32,9 @@
 // TMEM: NQ = 1: S of even and odd tiles at 0 and 128; NQ = 2: S of query tile e
 // at 128 e.  P (fp16 pairs) is written over the first 64 columns of its S.  O
 // from column 256.
-// Slots outside [lo, hi) of a unit are zeroed in V's tile, so that what they
-// hold (a NaN, say) cannot reach O through a zero probability.
+// Slots outside [lo, hi) of a unit are left out of the product with V, 16 at a
+// time, or zeroed in its tile, so that what they hold (a NaN, say) cannot reach
+// O through a zero probability.
 #include <algorithm>
 #include <mutex>
 
@@ -100,7 +101,7 @@ struct Shared {
   Piece piece[NPC];
   float2 stat[2][BM];     // NQ = 1: (reference, sum) of a piece's rows
   long long warp_sum[12];
-  int warp_most[12];
+  int warp_most[12], warp_units[12];
   long long start_off, start_base;   // of this CTA's share in its first sequence, which begins there
   int start_taken;        // whole shares before that sequence
   int unit_rows, unit_row0, unit_parts;   // of the cluster's unit
@@ -147,7 +148,7 @@ struct Cfg {
   // What a unit costs besides its tiles, in halves of a tile: of units of few
   // rows alone, and where units of chunks and of steps meet (4B-shaped mixed
   // batch: 103 us with 1, 81 with 4, 74 with 12).
-  static constexpr int UC1 = 3, UCG = NQ == 2 ? 5 : 10;
+  static constexpr int UC1 = 3, UCG = 5;
   static constexpr int THREADS = 384;
   // the control warps give registers to the others
   static constexpr int REGS_LAUNCH = 168, REGS_CTRL = NQ == 2 ? 104 : 120, REGS_SOFT = NQ == 2 ? 200 : 216;
@@ -245,6 +246,12 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+// The descriptor of a tile `bytes` (a multiple of 16) behind that of `base`: the
+// addresses stay below 2^18, so that their sum does not leave its field.
+__device__ __forceinline__ uint64_t sdesc_plus(uint64_t base, uint32_t bytes) {
+  return (base & 0xffffffff00000000ull) | (static_cast<uint32_t>(base) + (bytes >> 4));
 }
 
 // How a launch's CTAs take their work.
@@ -358,20 +365,51 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     }
     return total;
   };
-  long long mine = 0, upto;
+  long long mine = 0, upto = 0;
   PagedSeq seq = {0, 0, 0};   // the thread's last one
+  int units = 0, longest = 0; // (!ONE: units, and the longest one's tiles)
   for (int k = 0; k < per; ++k) {
     const int b = tid * per + k;
     if (b >= batch.B) break;
     seq = paged_seq(batch, b, p.status);
     mine += p.H_kv * head_cost(seq);
+    if constexpr (!ONE) {
+      if (seq.n == 0) continue;
+      // (units beyond a CTA's number count as so many; with a window no unit has
+      // more than the slots that its tokens reach)
+      units += min(p.H_kv * min(paged_units(seq.n, p.ts), kMaxCtas), kMaxCtas);
+      int t = (seq.len + seq.n + BN - 1) >> kTileShift;
+      if (p.window > 0) t = min(t, static_cast<int>((static_cast<long long>(p.window) + (tree ? seq.n : 1 << p.ts) + 2 * BN) >> kTileShift));
+      longest = max(longest, t);
+    }
   }
   long long total = 0;
   if constexpr (CLUSTER) {
-    upto = 0;
     __syncthreads();
-  } else {
+  } else if constexpr (ONE) {
     total = scan(mine, upto, lost);
+  } else {
+    // sums alone: what each CTA gets is settled below
+    units = __reduce_add_sync(0xffffffffu, units);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) {
+      sh.warp_sum[warp] = mine;
+      sh.warp_units[warp] = units;
+      sh.warp_most[warp] = longest;
+    }
+    if (__syncthreads_or(lost)) {
+      total = -1;
+    } else {
+      units = 0;
+#pragma unroll
+      for (int w = 0; w < C::THREADS / 32; ++w) {
+        total += sh.warp_sum[w];
+        units += sh.warp_units[w];
+        longest = max(longest, sh.warp_most[w]);
+      }
+    }
   }
   tc_fence_after();
   const uint32_t tbase = sh.tmem;
@@ -385,30 +423,11 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   int taken = 0, grid = gridDim.x, taken_mine = 0, taken_upto = 0;
   if constexpr (!ONE) {
     const long long all = total;
-    // units, and the longest one's tiles
-    long long units = 0;
-    int longest = 0;
-    for (int k = 0; k < per; ++k) {
-      const int b = tid * per + k;
-      if (b >= batch.B) break;
-      if (per > 1) seq = paged_seq(batch, b, p.status);
-      if (seq.n == 0) continue;
-      const int nq = paged_units(seq.n, p.ts);
-      units += static_cast<long long>(p.H_kv) * nq;
-      // (with a window no unit has more than the slots that its tokens reach)
-      int t = (seq.len + seq.n + BN - 1) >> kTileShift;
-      if (p.window > 0) t = min(t, static_cast<int>((static_cast<long long>(p.window) + (tree ? seq.n : 1 << p.ts) + 2 * BN) >> kTileShift));
-      longest = max(longest, t);
-    }
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    if (lane == 0) sh.warp_most[warp] = longest;
-    __syncthreads();          // (the sums are read)
-    units = scan(units, upto, false);
-#pragma unroll
-    for (int w = 0; w < C::THREADS / 32; ++w) longest = max(longest, sh.warp_most[w]);
-    const long long per_cta = (all + static_cast<long long>(grid) * TC - 1) / (static_cast<long long>(grid) * TC);
+    const long long per_cta =
+        all < 1 << 30 ? (static_cast<unsigned>(all) + static_cast<unsigned>(grid * TC) - 1) / static_cast<unsigned>(grid * TC)
+                      : (all + grid * TC - 1) / (grid * TC);
     uncut = units <= grid &&
-            longest <= per_cta + uncut_tiles(static_cast<int>(min(all / TC, grid + units)));
+            longest <= per_cta + uncut_tiles(static_cast<int>(min(all / TC, static_cast<long long>(grid + units))));
     if (p.window == 0 && all > 0 && !uncut) S = static_cast<int>(per_cta);
     mine = 0;
     __syncthreads();
@@ -558,15 +577,12 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       int k = 0, i = 0, p_begin = 0, p_end = 0, first = 0, cur = 0, ahead = 0;
       const int32_t* table = nullptr;
       // page ids, 32 at a time: lane l holds entry first + l of the sequence
-      auto entries = [&](int from) -> int {
-        const int at = from + lane;
-        if (at < p_begin || at >= p_end) return -1;
-        const int id = __ldcg(table + at);
-        if (static_cast<unsigned>(id) >= static_cast<unsigned>(batch.n_pages)) {
-          record_error(p.status, kDevErrBadPaged);
-          return -1;
-        }
-        return id << ps;
+      auto in_table = [&](int at) { return at >= p_begin && at < p_end; };
+      auto entry = [&](int at) { return in_table(at) ? __ldcg(table + at) : -1; };
+      auto pool_row = [&](int at, int id) -> int {
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(batch.n_pages)) return id << ps;
+        if (in_table(at)) record_error(p.status, kDevErrBadPaged);
+        return -1;
       };
 #pragma unroll 1
       while (ok) {
@@ -585,8 +601,9 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         const int tile = pc.tile0 + i, at = (tile * BN) >> ps;
         if (more && at >= first + 32) {
           first += 32;
-          cur = fresh ? entries(first) : ahead;
-          ahead = entries(first + 32);
+          const int id0 = fresh ? entry(first + lane) : 0, id1 = entry(first + 32 + lane);
+          cur = fresh ? pool_row(first + lane, id0) : ahead;
+          ahead = pool_row(first + 32 + lane, id1);
         }
         const int base = __shfl_sync(0xffffffffu, cur, (at - first + (lane & 7)) & 31);
 #pragma unroll 1
@@ -619,14 +636,12 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         for (int part = 0; part < C::PARTS; ++part) {
           if (!wait_warp(sh.part_full[r.slot], r.phase, kSitePartFull)) return false;
           tc_fence_after();
-          const uint32_t kb = smem_u32(sP + r.slot * PART);
+          const uint64_t kd = sdesc_sw128(smem_u32(sP + r.slot * PART), 16, 1024);
+          const uint64_t qd = sdesc_sw128(q_addr + part * 2 * q_stride, 16, 1024), qd1 = sdesc_plus(qd, q_stride);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t off = (k >> 2) * CHUNK + (k & 3) * 32;
-            mma_ss_lead(lead, tbase + (g & 1) * 128,
-                        sdesc_sw128(q_addr + (part * 2 + (k >> 2)) * q_stride + (k & 3) * 32, 16, 1024),
-                        sdesc_sw128(kb + off, 16, 1024), idesc_qk, part > 0 || k > 0 ? 1u : 0u);
-          }
+          for (int k = 0; k < 8; ++k)
+            mma_ss_lead(lead, tbase + (g & 1) * 128, sdesc_plus(k < 4 ? qd : qd1, (k & 3) * 32),
+                        sdesc_plus(kd, (k >> 2) * CHUNK + (k & 3) * 32), idesc_qk, part > 0 || k > 0 ? 1u : 0u);
           mma_commit_lead(lead, smem_u32(&sh.part_empty[r.slot]));
           r.next<C::NP>();
         }
@@ -641,30 +656,42 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       // V lies in blocks of 2^vshift slots, a block's 64-channel chunks one
       // behind the other.
       const uint32_t v_chunk = 128u << p.vshift;
-      auto mma_pv = [&](int e, int buf, uint32_t vb, int part, int first) {
-        constexpr int STEPS = 8 / C::PARTS;   // 16-slot steps of a part
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k) {
-          const uint32_t at = k * 2048 + ((k * 16) >> p.vshift) * (C::NCH - 1) * v_chunk;
+      constexpr int STEPS = 8 / C::PARTS;     // 16-slot steps of a part
+      int from = 0, to = 0;                   // those of the part in hand that hold visible slots
+      auto mma_pv = [&](int e, int buf, uint32_t vb, int part, bool first) {
+        const uint64_t vd = sdesc_sw128(vb, v_chunk, 1024);
+        auto step = [&](int k, bool sum) {
+          const uint32_t rows = k * 2048, blocks = rows & ~(v_chunk - 1);   // (whole ones before it)
           mma_ts_lead(lead, tbase + O_COL + e * 128, tbase + buf * 128 + (part * STEPS + k) * 8,
-                      sdesc_sw128(vb + at, v_chunk, 1024), idesc_pv, !first || part > 0 || k > 0 ? 1u : 0u);
+                      sdesc_plus(vd, rows + blocks * (C::NCH - 1)), idesc_pv, sum ? 1u : 0u);
+        };
+        if (NQ == 2 || (from == 0 && to == STEPS)) {
+#pragma unroll
+          for (int k = 0; k < STEPS; ++k) step(k, !first || k > 0);
+        } else {              // (a condition in each step instead: a tile 1.72 us, not 1.45)
+#pragma unroll 1
+          for (int k = from; k < to; ++k) step(k, !first || k > from);
         }
       };
-      // V of the part in slot r, zeroed outside [lo, hi).
+      // V of the part in slot r.  NQ = 1: the steps without a visible slot are
+      // left out, the slots outside [lo, hi) in the others zeroed; NQ = 2: all
+      // of them zeroed (a second loop of steps costs chunks more than it saves).
       auto v_ready = [&](const Pv& t, int part, const Ring& r) -> bool {
         if (!wait_warp(sh.part_full[r.slot], r.phase, kSitePartFull)) return false;
         constexpr int ROWS = 128 / C::PARTS;
         const int s0 = t.tile * BN + part * ROWS;
-        if (s0 < t.lo || s0 + ROWS > t.hi) {
-          uint8_t* base = sP + r.slot * PART;
-          const int z = min(max(t.lo - s0, 0), ROWS), a = min(max(t.hi - s0, 0), ROWS);
-          // (8 lanes to a row's 128 bytes)
+        const int z = min(max(t.lo - s0, 0), ROWS), a = min(max(t.hi - s0, 0), ROWS);
+        from = z >> 4;
+        to = z < a ? (a + 15) >> 4 : 0;       // 0: none
+        const int nz = NQ == 1 ? z & 15 : z, na = NQ == 1 ? -a & 15 : ROWS - a;
+        if ((nz | na) != 0) {
+          uint8_t* base = sP + r.slot * PART + (lane & 7) * 16;   // (8 lanes to a row's 128 bytes)
 #pragma unroll 1
-          for (int i = lane >> 3; i < (z + ROWS - a) * C::NCH; i += 4) {
-            const int x = i / C::NCH, c = i % C::NCH, row = x < z ? x : a + x - z;
-            const int blk = row >> p.vshift, in = row & ((1 << p.vshift) - 1);
-            *reinterpret_cast<uint4*>(base + (blk * C::NCH + c) * v_chunk + in * 128 + (lane & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
+          for (int i = lane >> 3; i < nz + na; i += 4) {
+            const int row = i < nz ? z - nz + i : a + i - nz;
+            uint8_t* at = base + row * 128 + (row >> p.vshift) * (C::NCH - 1) * v_chunk;
+#pragma unroll
+            for (int c = 0; c < C::NCH; ++c) *reinterpret_cast<uint4*>(at + c * v_chunk) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -682,10 +709,12 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       // NQ = 1: the PV of tile number n.
       auto issue_pv1 = [&](const Pv& t, int n) -> bool {
         if (!pv_begin(t, 0) || !wait_warp(sh.p_full[n & 1], (n >> 1) & 1, kSitePFull)) return false;
+        bool first = t.first;
 #pragma unroll 1
         for (int part = 0; part < C::PARTS; ++part) {
           if (!v_ready(t, part, r)) return false;
-          mma_pv(0, n & 1, smem_u32(sP + r.slot * PART), part, t.first);
+          mma_pv(0, n & 1, smem_u32(sP + r.slot * PART), part, first);
+          first = first && to == 0;
           mma_commit_lead(lead, smem_u32(&sh.part_empty[r.slot]));
           r.next<C::NP>();
         }
@@ -731,7 +760,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
           if (pending) ok = v_ready(prev, 0, r);
           if (!ok) break;
           const uint32_t kb = smem_u32(sP + kr.slot * PART), vb = smem_u32(sP + r.slot * PART);
-          const uint32_t q_addr = smem_u32(sQ);
+          const uint64_t kd = sdesc_sw128(kb, 16, 1024), qd = sdesc_sw128(smem_u32(sQ), 16, 1024);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             if (pending && e < prev.nq) {
@@ -751,8 +780,8 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
                 const uint32_t off = (c >> 2) * CHUNK + (c & 3) * 32;
-                mma_ss_lead(lead, tbase + e * 128, sdesc_sw128(q_addr + e * C::QT_BYTES + off, 16, 1024),
-                            sdesc_sw128(kb + off, 16, 1024), idesc_qk, c > 0 ? 1u : 0u);
+                mma_ss_lead(lead, tbase + e * 128, sdesc_plus(qd, e * C::QT_BYTES + off), sdesc_plus(kd, off), idesc_qk,
+                            c > 0 ? 1u : 0u);
               }
               mma_commit_lead(lead, smem_u32(&sh.s_full[e]));
               ++ge[e];
@@ -849,9 +878,9 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
         const PagedUnit u = paged_unit(s.len, s.n, p.window, tree, p.ts, q);
         Piece pc = make_piece(s, b, j, q, u, uncut ? 0 : at * S, uncut ? u.tiles : S);
         if (pc.slot >= 0) pc.slot = 2 * blockIdx.x;
+        publish(pc);
         if (at == 0 && pc.slot >= 0)
           cut(pc, whole, sh.start_base + j * cost_of(s, whole, nq) + cost_of(s, whole, q), u.tiles - whole * S);
-        publish(pc);
       }
       while (ok && left > 0 && b < batch.B) {
         PagedSeq s = sh.start_seq;
@@ -924,13 +953,11 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
           const int t0 = tile_at(o), n = tile_at(o1) - t0;
           if (n > 0) {
             Piece pc = make_piece(s, b, j, q, u, skip + t0, n);
-            if (t0 == 0 && n < rest) {
-              pc.slot = 2 * blockIdx.x + 1;
-              if (whole == 0) cut(pc, 0, pos - o, rest);
-            } else if (t0 == 0 && whole > 0) {
-              pc.slot = kRest + passed + (j * nq + q) * whole;
-            }
+            const bool begun = t0 == 0 && n < rest;   // its first piece of several
+            if (begun) pc.slot = 2 * blockIdx.x + 1;
+            else if (t0 == 0 && whole > 0) pc.slot = kRest + passed + (j * nq + q) * whole;
             publish(pc);
+            if (begun && whole == 0) cut(pc, 0, pos - o, rest);
           }
           left -= o1 - o;
           pos += o1 - o;
