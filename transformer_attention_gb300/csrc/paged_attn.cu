@@ -10,7 +10,10 @@
 // the tensor cores, so one kernel serves both: the cache streams through a
 // ring of 32 KB parts, up to 192 KB in flight per SM, and each 128-slot tile costs 1100
 // (d_h = 128) or 2200 clocks of MMA however few its rows, against 2800 or 5600
-// for its bytes at the HBM rate.
+// for its bytes at the HBM rate.  Measured: a token over 131071 slots, 27B-shaped,
+// 170 us (1.07 GB: 93% of the copy rate; 48 of the SMs, always the same, get
+// less of it and end 6% later); 1024 tokens over 31744 slots 383 us (1.41 PFLOP/s: of a tile pair's
+// 3100 clocks 2048 are MMA, as in attention_pair.cu).
 //
 // Sequences have lengths of their own, known on the device alone: each CTA adds
 // up the work of all units and takes an equal share of it, cut wherever it
@@ -37,6 +40,7 @@
 // O through a zero probability.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "attention_common.cuh"
 #include "paged.cuh"
@@ -146,8 +150,8 @@ struct Cfg {
   static constexpr uint32_t SMEM = NQ * QT_BYTES + NP * PART + sizeof(Shared);
   static_assert(SMEM <= 232448 && NP <= 8, "shared memory budget");
   // What a unit costs besides its tiles, in halves of a tile: of units of few
-  // rows alone, and where units of chunks and of steps meet (4B-shaped mixed
-  // batch: 103 us with 1, 81 with 4, 74 with 12).
+  // rows alone, and where units of chunks and of steps meet (eight mixed 4B-shaped
+  // batches: 56.7 us on average with 10, 54.2 with 6, 53.8 with 4).
   static constexpr int UC1 = 3, UCG = 5;
   static constexpr int THREADS = 384;
   // the control warps give registers to the others
@@ -1192,28 +1196,52 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       const int j = head % p.H_kv, rows = sh.unit_rows, parts = sh.unit_parts;
       const uint32_t o_at = smem_u32(sP), st_at = o_at + p.rows * DH * 4;
       const int all = parts > 0 ? rows * (DH / 4) : 0;
-      for (int i = rank * 256 + tid - 128; i < all; i += cs * 256) {
-        const int c = i / rows, r = i - c * rows;
-        MergeAcc<1> acc;
-        acc.o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int x0 = 0; x0 < parts; x0 += 4) {
-          float2 st[4];
-          float4 x[4][1];
+      // I vectors of a thread at once, A parts of each: the loads of a round trip
+      // (clusters of two: 21.5 us for 12B-shaped local trees with one vector at a
+      // time, 20.7 with four)
+      auto add_up = [&](auto items, auto at_once) {
+        constexpr int I = decltype(items)::value, A = decltype(at_once)::value;
+        const int stride = cs * 256;
+        for (int i0 = rank * 256 + tid - 128; i0 < all; i0 += I * stride) {
+          MergeAcc<1> acc[I];
+          int c[I], r[I];
 #pragma unroll
-          for (int x1 = 0; x1 < 4; ++x1)
-            if (x0 + x1 < parts) {
-              st[x1] = ld_cluster_f2(mapa_shared(st_at + r * 8, x0 + x1));
-              x[x1][0] = ld_cluster_f4(mapa_shared(o_at + (c * p.rows + r) * 16, x0 + x1));
-            }
+          for (int u = 0; u < I; ++u) {
+            acc[u].o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int i = min(i0 + u * stride, all - 1);
+            c[u] = i / rows;
+            r[u] = i - c[u] * rows;
+          }
+          for (int x0 = 0; x0 < parts; x0 += A) {
+            float2 st[I][A];
+            float4 x[I][A][1];
 #pragma unroll
-          for (int x1 = 0; x1 < 4; ++x1)
-            if (x0 + x1 < parts) acc.add(st[x1], x[x1]);
+            for (int u = 0; u < I; ++u)
+#pragma unroll
+              for (int k = 0; k < A; ++k)
+                if (x0 + k < parts) {
+                  st[u][k] = ld_cluster_f2(mapa_shared(st_at + r[u] * 8, x0 + k));
+                  x[u][k][0] = ld_cluster_f4(mapa_shared(o_at + (c[u] * p.rows + r[u]) * 16, x0 + k));
+                }
+#pragma unroll
+            for (int u = 0; u < I; ++u)
+#pragma unroll
+              for (int k = 0; k < A; ++k)
+                if (x0 + k < parts) acc[u].add(st[u][k], x[u][k]);
+          }
+#pragma unroll
+          for (int u = 0; u < I; ++u) {
+            if (i0 + u * stride >= all) break;
+            const float inv = acc[u].l != 0.f ? 1.f / acc[u].l : 0.f;
+            const size_t orow = static_cast<size_t>(sh.unit_row0 + (r[u] >> p.gshift)) * p.H + (j << p.gshift) +
+                                (r[u] & ((1 << p.gshift) - 1));
+            reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * DH)[c[u]] = acc[u].packed(0, inv, p.o_f16);
+          }
         }
-        const float inv = acc.l != 0.f ? 1.f / acc.l : 0.f;
-        const size_t orow = static_cast<size_t>(sh.unit_row0 + (r >> p.gshift)) * p.H + (j << p.gshift) +
-                            (r & ((1 << p.gshift) - 1));
-        reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * DH)[c] = acc.packed(0, inv, p.o_f16);
-      }
+      };
+      using std::integral_constant;
+      if (parts <= 2) add_up(integral_constant<int, 4>(), integral_constant<int, 2>());
+      else add_up(integral_constant<int, 1>(), integral_constant<int, 4>());
     }
     __syncwarp();
     if (cs > 1) cluster_sync();   // no CTA leaves while another reads its shared memory
@@ -1336,7 +1364,7 @@ __device__ __forceinline__ void merge_tasks(const Params& p, MergeShared& sh, co
 }
 
 // Few rows (at most kMergeDirect): CTAs of their own for each attention CTA,
-// which need not look at the others (step_local, 2 rows: 1.3 us less).
+// which need not look at the others (two rows: 1.3 us less than by the kernel below).
 constexpr int kMergeDirect = 8;
 
 template <int DH>
