@@ -8,11 +8,10 @@
 // (128 / G tokens x the G heads); a step or a tree fills a few rows of one tile.
 // Below some 280 rows per kv head the cache's bytes bound the call, above them
 // the tensor cores, so one kernel serves both: the cache streams through a
-// ring of 32 KB parts, up to 192 KB in flight per SM, and each 128-slot tile costs 1100
+// ring of 32 KB parts, 160 KB in flight per SM, and each 128-slot tile costs 1100
 // (d_h = 128) or 2200 clocks of MMA however few its rows, against 2800 or 5600
 // for its bytes at the HBM rate.  Measured: a token over 131071 slots, 27B-shaped,
-// 170 us (1.07 GB: 93% of the copy rate; 48 of the SMs, always the same, get
-// less of it and end 6% later); 1024 tokens over 31744 slots 383 us (1.41 PFLOP/s: of a tile pair's
+// 161.5 us (1.07 GB: 98% of the copy rate); 1024 tokens over 31744 slots 383 us (1.41 PFLOP/s: of a tile pair's
 // 3100 clocks 2048 are MMA, as in attention_pair.cu).
 //
 // Sequences have lengths of their own, known on the device alone: each CTA adds
@@ -146,9 +145,12 @@ struct Cfg {
   static constexpr int NCH = DH / 64;
   static constexpr int PARTS = DH / 128;          // parts of a K or V tile
   static constexpr uint32_t QT_BYTES = BM * DH * 2;
-  static constexpr int NP = (7 * PART - NQ * QT_BYTES) / PART;   // ring: what Q leaves of 224 KB
+  // Ring: five parts, 160 KB in flight.  The HBM serves some SMs worse the more
+  // all of them ask for at once (a token over 131071 slots, 27B-shaped: 169 us with
+  // six parts, 161.5 with five or four, 167 with three).
+  static constexpr int NP = 5;
   static constexpr uint32_t SMEM = NQ * QT_BYTES + NP * PART + sizeof(Shared);
-  static_assert(SMEM <= 232448 && NP <= 8, "shared memory budget");
+  static_assert(NQ * QT_BYTES + NP * PART <= 7 * PART && SMEM <= 232448, "shared memory budget");
   // What a unit costs besides its tiles, in halves of a tile: of units of few
   // rows alone, and where units of chunks and of steps meet (eight mixed 4B-shaped
   // batches: 56.7 us on average with 10, 54.2 with 6, 53.8 with 4).
