@@ -1255,106 +1255,82 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   }
 }
 
-// Adds the parts of the units that several CTAs have worked on.  A
-// task is up to 32 rows of such a unit and some of their channels: lanes along
-// the rows, which lie next to each other in a part, and where they are few
-// along 4-channel vectors too.  A lane has its row's sums to itself, so a task
-// is one warp's, or that of several where a unit has many parts.
+// Adds the parts of the units that several CTAs have worked on: the unit whose
+// first part is attention CTA blockIdx.x's, by gridDim.y CTAs, which need not
+// look at the other units (a list of all units' tasks, over CTAs of its own
+// number, took 2 to 3 us more: 4B-shaped mixed batches 43.9 -> 40.7 us).  A task
+// is up to 32 rows and some of their channels: lanes along the rows, which lie
+// next to each other in a part, and where they are few along 4-channel vectors
+// too, VV of them per lane.  A lane has its row's sums to itself, so a task is
+// one warp's, or that of several where a unit has many parts.
 constexpr int kMergeWarps = 8;
-
-struct MergeShared {
-  int upto[kMaxCtas];            // tasks of the units that start in CTAs 0 .. i
-  Split split[kMaxCtas];
-  long long warp_sum[kMergeWarps];
-  int warp_max[kMergeWarps];
-  float2 st[kMergeWarps][32];
-  float4 o[kMergeWarps][2][32];
-};
 
 __device__ __forceinline__ Split load_split(const Split* from) {
   const int4 a = __ldcg(reinterpret_cast<const int4*>(from)), b = __ldcg(reinterpret_cast<const int4*>(from) + 1);
   return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
-// Lanes along the rows of a unit of `all` rows: a power of two.
-__device__ __forceinline__ int merge_pad(int all) {
-  return all >= 32 ? 32 : 1 << (31 - __clz(2 * all - 1));
-}
-__device__ __forceinline__ int merge_warps(int parts) {   // warps of a task
-  return parts >= 32 ? 8 : (parts >= 16 ? 4 : (parts >= 8 ? 2 : 1));
-}
-
-// DIRECT: the tasks of the unit `one` that starts in CTA blockIdx.x, over
-// gridDim.y CTAs; else all tasks over all CTAs.
-template <int DH, int VV, bool DIRECT>
-__device__ __forceinline__ void merge_tasks(const Params& p, MergeShared& sh, const Split& one, int total,
-                                            int wp, int ctas) {
+template <int DH, int VV>
+__global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const Params p) {
+  pdl_enter();
+  const bool lost = lost_work(p.status, kLostWait);   // parts may be missing
+  __shared__ float2 sums[kMergeWarps][32];
+  __shared__ float4 rows[kMergeWarps][VV][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Split u = load_split(p.split + blockIdx.x);
+  if (__syncthreads_or(lost) || u.parts == 0) return;
+  const int all = u.ntok << p.gshift;          // rows of the unit
+  const int pad = all >= 32 ? 32 : 1 << (31 - __clz(2 * all - 1));   // lanes along them: a power of two
+  const int vecs = 32 / pad * VV;              // vectors of a task
+  const int chunks = (DH / 4 + vecs - 1) / vecs, total = (all + 31) / 32 * chunks;
+  const int wp = u.parts >= 32 ? 8 : (u.parts >= 16 ? 4 : (u.parts >= 8 ? 2 : 1));   // warps of a task
   const int sub = warp & (wp - 1), per = kMergeWarps / wp;
-  const int stride = (DIRECT ? gridDim.y : gridDim.x) * per;
-  for (int t0 = (DIRECT ? blockIdx.y : blockIdx.x) * per; t0 < total; t0 += stride) {
+  for (int t0 = blockIdx.y * per; t0 < total; t0 += gridDim.y * per) {
     const int task = t0 + warp / wp;
-    int cta = DIRECT ? blockIdx.x : 0;             // whose unit: the first with upto > task
-    if (!DIRECT)
-      for (int c0 = 0; c0 < ctas; c0 += 32)
-        cta += __popc(__ballot_sync(0xffffffffu, c0 + lane < ctas && sh.upto[c0 + lane] <= task));
-    const bool live = task < total;
+    const int r = task / chunks * 32 + (lane & (pad - 1)), v0 = task % chunks * vecs + lane / pad * VV;
+    const bool mine = task < total && r < all && v0 < DH / 4;
     MergeAcc<VV> acc;
 #pragma unroll
     for (int v = 0; v < VV; ++v) acc.o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    size_t orow = 0;
-    int v0 = 0;
-    bool mine = false;
-    if (live) {
-      const Split u = DIRECT ? one : sh.split[cta];
-      const int all = u.ntok << p.gshift;          // rows of the unit
-      const int pad = merge_pad(all);
-      const int vecs = 32 / pad * VV;              // vectors of a task
-      const int chunks = (DH / 4 + vecs - 1) / vecs;
-      const int at = DIRECT ? task : task - (cta > 0 ? sh.upto[cta - 1] : 0);
-      const int r = at / chunks * 32 + (lane & (pad - 1));
-      v0 = at % chunks * vecs + lane / pad * VV;
-      mine = r < all && v0 < DH / 4;
-      orow = static_cast<size_t>(u.row0 + (r >> p.gshift)) * p.H + (u.j << p.gshift) + (r & ((1 << p.gshift) - 1));
-      if (mine) {
-        // this warp's parts: sub, sub + wp, ...
-        constexpr int AT_ONCE = 4;
-        for (int i0 = sub; i0 < u.parts; i0 += AT_ONCE * wp) {
-          float2 st[AT_ONCE];
-          float4 x[AT_ONCE][VV];
+    if (mine) {
+      // this warp's parts: sub, sub + wp, ...
+      constexpr int AT_ONCE = 4;
+      for (int i0 = sub; i0 < u.parts; i0 += AT_ONCE * wp) {
+        float2 st[AT_ONCE];
+        float4 x[AT_ONCE][VV];
 #pragma unroll
-          for (int k = 0; k < AT_ONCE; ++k) {
-            const int i = i0 + k * wp;
-            st[k] = make_float2(0.f, 0.f);
-            if (i < u.parts) {
-              const size_t slot = u.slot(i);
-              st[k] = __ldcg(p.pstat + slot * p.rows + r);
+        for (int k = 0; k < AT_ONCE; ++k) {
+          const int i = i0 + k * wp;
+          st[k] = make_float2(0.f, 0.f);
+          if (i < u.parts) {
+            const size_t slot = u.slot(i);
+            st[k] = __ldcg(p.pstat + slot * p.rows + r);
 #pragma unroll
-              for (int v = 0; v < VV; ++v) x[k][v] = __ldcg(p.part + (slot * (DH / 4) + v0 + v) * p.rows + r);
-            }
+            for (int v = 0; v < VV; ++v) x[k][v] = __ldcg(p.part + (slot * (DH / 4) + v0 + v) * p.rows + r);
           }
-#pragma unroll
-          for (int k = 0; k < AT_ONCE; ++k)
-            if (i0 + k * wp < u.parts) acc.add(st[k], x[k]);
         }
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k)
+          if (i0 + k * wp < u.parts) acc.add(st[k], x[k]);
       }
     }
     if (wp > 1) {
-      sh.st[warp][lane] = make_float2(acc.m, acc.l);
+      sums[warp][lane] = make_float2(acc.m, acc.l);
 #pragma unroll
-      for (int v = 0; v < VV; ++v) sh.o[warp][v][lane] = acc.o[v];
+      for (int v = 0; v < VV; ++v) rows[warp][v][lane] = acc.o[v];
       __syncthreads();
       if (sub == 0)
         for (int k = 1; k < wp; ++k) {
           float4 x[VV];
 #pragma unroll
-          for (int v = 0; v < VV; ++v) x[v] = sh.o[warp + k][v][lane];
-          acc.add(sh.st[warp + k][lane], x);
+          for (int v = 0; v < VV; ++v) x[v] = rows[warp + k][v][lane];
+          acc.add(sums[warp + k][lane], x);
         }
       __syncthreads();
     }
     if (mine && sub == 0) {
       const float inv = acc.l != 0.f ? 1.f / acc.l : 0.f;
+      const size_t orow = static_cast<size_t>(u.row0 + (r >> p.gshift)) * p.H + (u.j << p.gshift) + (r & ((1 << p.gshift) - 1));
       uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * DH) + v0;
       uint2 w[VV];
 #pragma unroll
@@ -1363,62 +1339,6 @@ __device__ __forceinline__ void merge_tasks(const Params& p, MergeShared& sh, co
       else dst[0] = w[0];
     }
   }
-}
-
-// Few rows (at most kMergeDirect): CTAs of their own for each attention CTA,
-// which need not look at the others (two rows: 1.3 us less than by the kernel below).
-constexpr int kMergeDirect = 8;
-
-template <int DH>
-__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_few_kernel(const Params p) {
-  pdl_enter();
-  const bool lost = lost_work(p.status, kLostWait);   // parts may be missing
-  __shared__ MergeShared sh;
-  const Split u = load_split(p.split + blockIdx.x);
-  if (__syncthreads_or(lost) || u.parts == 0) return;
-  merge_tasks<DH, 1, true>(p, sh, u, (DH / 4 * merge_pad(u.ntok << p.gshift) + 31) / 32, merge_warps(u.parts), 0);
-}
-
-template <int DH>
-__global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const Params p, int ctas) {
-  pdl_enter();
-  const bool lost = lost_work(p.status, kLostWait);   // parts may be missing
-  __shared__ MergeShared sh;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  Split u = {0, 0, 0, 0, 0, 0, 0, 0};                 // the unit that starts in CTA tid
-  if (tid < ctas) {
-    u = load_split(p.split + tid);
-    sh.split[tid] = u;
-  }
-  // its tasks with one vector per lane and, packed above them, with two
-  const int all = u.parts > 0 ? u.ntok << p.gshift : 0;
-  const int groups = (all + 31) / 32, vecs = all > 0 ? DH / 4 * merge_pad(all) : 0;
-  long long tasks = static_cast<long long>(groups * ((vecs + 63) / 64)) << 32 | (groups * ((vecs + 31) / 32));
-  long long upto = tasks;
-  int most = u.parts;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += v;
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-  }
-  if (lane == 31) sh.warp_sum[warp] = upto;
-  if (lane == 0) sh.warp_max[warp] = most;
-  if (__syncthreads_or(lost)) return;
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    if (w < warp) upto += sh.warp_sum[w];
-    total += sh.warp_sum[w];
-    most = max(most, sh.warp_max[w]);
-  }
-  const int wp = merge_warps(most), ones = static_cast<int>(total), twos = static_cast<int>(total >> 32);
-  // Two vectors per lane where one leaves more tasks than warps.
-  const bool two = static_cast<long long>(ones) * wp > gridDim.x * kMergeWarps;
-  if (tid < ctas) sh.upto[tid] = static_cast<int>(two ? upto >> 32 : upto);
-  __syncthreads();
-  if (two) merge_tasks<DH, 2, false>(p, sh, u, twos, wp, ctas);
-  else merge_tasks<DH, 1, false>(p, sh, u, ones, wp, ctas);
 }
 
 // Query tiles per unit: two where a unit of d_h = 128 can fill them.
@@ -1463,12 +1383,9 @@ cudaError_t launch_cfg(const CUtensorMap& tq, const CUtensorMap& tq32, const CUt
   if (cudaError_t e = launch_pdl(paged_attn_kernel<DH, NQ, MODE>, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, tq,
                                  tq32, tk, tv, p))
     return e;
-  if (p.rows <= kMergeDirect) {
-    const int tasks = (DH / 4 * kMergeDirect) / 32;   // at most
-    return launch_pdl(paged_merge_few_kernel<DH>, dim3(ctas, std::min(tasks, 4)), dim3(32 * kMergeWarps), 0,
-                      stream, p);
-  }
-  return launch_pdl(paged_merge_kernel<DH>, dim3(3 * ctas), dim3(32 * kMergeWarps), 0, stream, p, ctas);
+  // (of few rows a unit has 16 tasks at most)
+  if (p.rows <= 8) return launch_pdl(paged_merge_kernel<DH, 1>, dim3(ctas, DH == 256 ? 4 : 2), dim3(32 * kMergeWarps), 0, stream, p);
+  return launch_pdl(paged_merge_kernel<DH, 2>, dim3(ctas, 8), dim3(32 * kMergeWarps), 0, stream, p);
 }
 
 // Clusters of `size` CTAs that the device holds at once, asked once per device.
