@@ -299,3 +299,13 @@ def test_units_against_the_masks(tmp_path):
             assert lo == max(0, first) and hi == length + tokens[-1] + 1
             assert tile0 == lo // 128 and tiles == -(-hi // 128) - tile0 >= 1
             total += tiles
+
+
+@pytest.mark.parametrize("name", ["rows", "T_max", "page_size", "n_pages"])
+def test_sizes_beyond_32_bits_are_refused(name):
+    sizes = dict(rows=3, T_max=2, page_size=16, n_pages=8)
+    lens, starts, table = torch.zeros(2).int(), torch.zeros(3).int(), torch.zeros((2, 4)).int()
+    assert G3.paged_batch(lens, starts, table, **sizes).sizes == (2, 3, 2, 16, 8, 4)
+    sizes[name] += 1 << 32                    # the same lower 32 bits
+    with pytest.raises(ValueError, match="32 bits"):
+        G3.paged_batch(lens, starts, table, **sizes)

@@ -518,6 +518,8 @@ class PagedBatch:
         if any(t is not None and t.get_device() != self.device for t in self.tensors):
             raise ValueError("a batch's tensors must live on one device")
         self.sizes = (B, rows, T_max, page_size, n_pages, pages)
+        if any(not -2 ** 31 <= n < 2 ** 31 for n in self.sizes):   # (ctypes would cut them off)
+            raise ValueError("a batch's sizes must fit 32 bits")
         self.struct = gemma3_paged_batch(*self.sizes, *(
             None if t is None else t.data_ptr() for t in self.tensors))
 

@@ -1189,7 +1189,8 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   }
   if (lost_site != 0) record_error(p.status, kDevErrTimeoutBase + lost_site);
   if constexpr (CLUSTER) {
-    // The cluster's parts: each CTA adds a share of the rows' 4-channel vectors.
+    // The cluster's parts: each CTA adds an equal share of the rows' 4-channel
+    // vectors.
     const int cs = cluster_nctarank();
     __syncwarp();
     if (cs > 1) cluster_sync();
@@ -1197,20 +1198,20 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
       const int rank = cluster_ctarank(), head = static_cast<int>(blockIdx.x) / cs / p.units;
       const int j = head % p.H_kv, rows = sh.unit_rows, parts = sh.unit_parts;
       const uint32_t o_at = smem_u32(sP), st_at = o_at + p.rows * DH * 4;
-      const int all = parts > 0 ? rows * (DH / 4) : 0;
+      const int vecs = parts > 0 ? rows * (DH / 4) : 0;
+      const int begin = vecs * rank / cs, all = vecs * (rank + 1) / cs;   // this CTA's
       // I vectors of a thread at once, A parts of each: the loads of a round trip
       // (clusters of two: 21.5 us for 12B-shaped local trees with one vector at a
       // time, 20.7 with four)
       auto add_up = [&](auto items, auto at_once) {
         constexpr int I = decltype(items)::value, A = decltype(at_once)::value;
-        const int stride = cs * 256;
-        for (int i0 = rank * 256 + tid - 128; i0 < all; i0 += I * stride) {
+        for (int i0 = begin + tid - 128; i0 < all; i0 += I * 256) {
           MergeAcc<1> acc[I];
           int c[I], r[I];
 #pragma unroll
           for (int u = 0; u < I; ++u) {
             acc[u].o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int i = min(i0 + u * stride, all - 1);
+            const int i = min(i0 + u * 256, all - 1);
             c[u] = i / rows;
             r[u] = i - c[u] * rows;
           }
@@ -1233,7 +1234,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
           }
 #pragma unroll
           for (int u = 0; u < I; ++u) {
-            if (i0 + u * stride >= all) break;
+            if (i0 + u * 256 >= all) break;
             const float inv = acc[u].l != 0.f ? 1.f / acc[u].l : 0.f;
             const size_t orow = static_cast<size_t>(sh.unit_row0 + (r[u] >> p.gshift)) * p.H + (j << p.gshift) +
                                 (r[u] & ((1 << p.gshift) - 1));
