@@ -665,3 +665,36 @@ def test_many_sequences(B):
     G3.gemma3_paged_positions(T.dev_batch(b), pos)
     assert G3.gemma3_attn_check_status() == 0
     assert torch.equal(pos.cpu().long(), PO.positions(b, b["M"]))
+
+
+# ---------------------------------------------------------------- appends of many rows
+@pytest.mark.parametrize("H_,H_kv,d_h,new", [
+    (4, 1, 256, [1999, 1, 800]), (4, 2, 256, [2500, 33]), (8, 2, 128, [700, 1900]), (3, 3, 128, [2600]),
+    (1, 1, 128, [2432]), (3, 3, 256, [30, 2411]), (8, 4, 256, [2500, 2]), (4, 1, 256, [12000, 8001]), (16, 4, 128, [2500]),
+])
+def test_append_of_prompts(H_, H_kv, d_h, new):
+    """Few heads: a row's vectors in one piece; many rows: several rounds of a CTA."""
+    import transformer_attention_gb300 as G3
+    lens = [17 * i + 5 for i in range(len(new))]
+    b = T.make_batch(lens, new, 64, 83, behind=3)
+    Q, KV, gq, gk = T.append_args(b, H_, H_kv, d_h, 84)
+    M, used, kvd = b["M"], sum(new), H_kv * d_h
+    q, kv, out = Q.cuda(), KV.cuda(), torch.full((b["M"], H_ * d_h + 8), 9.0, dtype=torch.float16, device="cuda")
+    dev = [torch.full((b["n_pages"], 64, H_kv, d_h), 3.0 + i, dtype=torch.float16, device="cuda") for i in range(2)]
+    G3.gemma3_paged_append(T.dev_batch(b), q, H_ * d_h, out, H_ * d_h + 8, kv, kv[:, kvd:], 2 * kvd, gq.cuda(), gk.cuda(),
+                           H_, H_kv, d_h, 1e6, 8.0, 0.17, *dev)
+    assert G3.gemma3_attn_check_status() == 0
+    pos = torch.cat([torch.arange(n) + length for n, length in zip(new, lens)])
+    refq, yq = PO.norm_rope(Q[:used].view(used, H_, d_h), gq, pos, 1e6, 8.0)
+    refk, yk = PO.norm_rope(KV[:used, :kvd].reshape(used, H_kv, d_h), gk, pos, 1e6, 8.0)
+    got = out.cpu()
+    T.near(got[:used, :H_ * d_h].view(used, H_, d_h), refq * 0.17, yq, 0.17)
+    assert bool((got[used:] == 9.0).all()) and bool((got[:, H_ * d_h:] == 9.0).all())
+    seq = torch.repeat_interleave(torch.arange(len(new)), torch.tensor(new))
+    at = b["table"].long()[seq, pos // 64] * 64 + pos % 64
+    k, v = (d.cpu().flatten(0, 1) for d in dev)
+    T.near(k[at], refk, yk)
+    assert torch.equal(v[at], KV[:used, kvd:].view(used, H_kv, d_h))
+    rest = torch.ones(len(k), dtype=torch.bool)
+    rest[at] = False
+    assert bool((k[rest] == 3.0).all()) and bool((v[rest] == 4.0).all())

@@ -8,7 +8,7 @@
 //   sequences, positions and slots together, and its warps take up to 8 steps
 //   of a row's head vectors (Q, K and V), all loads first; d_h / 8 lanes per
 //   vector, each with four channels of both halves, whose pairs it rotates alone.
-//   Measured: 17186 tokens of 64 heads of 128 channels 90 us (85% of the copy
+//   Measured: 17186 tokens of 64 heads of 128 channels 88.6 us (86% of the copy
 //   rate); 16 trees of 5 to 12 tokens, 32 heads of 256, 6.3 us: three round trips.
 // commit: token accepted[b, i] moves to slot lens[b] + i.  accepted ascends, so
 //   accepted[b, i] >= i, and a column of the rows is moved by one thread from
@@ -25,8 +25,8 @@ namespace g3 {
 namespace {
 
 constexpr float kEps = 1e-6f;
-constexpr int kVecUnroll = 8;        // steps of head vectors per item
-constexpr int kAppendRows = 32;      // rows of a CTA at a time
+constexpr int kVecUnroll = 8;        // steps of head vectors per item at most
+constexpr int kAppendRows = 64;      // rows of a CTA at a time
 constexpr int kAppendWarps = 8;
 constexpr int kStartsMax = 1024;     // row_start entries kept in shared memory
 
@@ -85,8 +85,12 @@ struct AppendParams {
   int* status;
 };
 
-// NORM: norm and rotation; else the rows go to the pages as they are.
-template <int DH, bool NORM>
+// NORM: norm and rotation; else the rows go to the pages as they are.  PACKED: a
+// row's steps are one item, else an item has steps of Q, of K or of V alone.  Few
+// heads leave most of such an item empty: 35000 rows of 4 + 1 + 1 heads of 256
+// take 113 us apart and 67 packed, 17186 of 8 + 4 + 4 of 128 45 and 30.  Packed
+// items of a part of a row take 6 to 20% more than those of one kind.
+template <int DH, bool NORM, bool PACKED>
 __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     paged_append_kernel(const PagedBatch p, const AppendParams a, const __grid_constant__ RopeFreqs freqs) {
   pdl_enter();
@@ -114,10 +118,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   const bool in_smem = p.B <= kStartsMax;
   if (in_smem)
     for (int i = tid; i <= p.B; i += blockDim.x) starts[i] = __ldcg(p.row_start + i);
-  // Items of a row: up to chunk_u steps of VPW heads of Q (finished without
-  // gammas), of K or of V.
-  const int iq = NORM ? ((a.H + VPW - 1) / VPW + a.chunk_u - 1) / a.chunk_u : 0;
-  const int ik = ((a.H_kv + VPW - 1) / VPW + a.chunk_u - 1) / a.chunk_u, nch = iq + 2 * ik;
+  // A row's steps are VPW heads of Q (finished without gammas), of K or of V each,
+  // an item up to chunk_u of them.
+  const int sq = NORM ? (a.H + VPW - 1) / VPW : 0, skv = (a.H_kv + VPW - 1) / VPW;
+  const int iq = (sq + a.chunk_u - 1) / a.chunk_u, ik = (skv + a.chunk_u - 1) / a.chunk_u;
+  const int nch = PACKED ? 1 : iq + 2 * ik;
   const int KVD = a.H_kv * DH;
   struct Item {
     int r, kind, head, left;   // row, 0 Q, 1 K, 2 V; this lane's first head, heads from it on
@@ -126,22 +131,40 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     Item t;
     t.r = i / nch;
     const int c = i - t.r * nch;
-    t.kind = c < iq ? 0 : (c < iq + ik ? 1 : 2);
+    t.kind = PACKED || c < iq ? 0 : (c < iq + ik ? 1 : 2);
     t.head = (t.kind == 0 ? c : (t.kind == 1 ? c - iq : c - iq - ik)) * a.chunk_u * VPW + sub;
     t.left = min((t.kind == 0 ? a.H : a.H_kv) - t.head, a.chunk_u * VPW - sub);
     return t;
+  };
+  struct Step {
+    int kind, head;
+    bool live;
+  };
+  auto step_of = [&](const Item& t, int u) -> Step {
+    if constexpr (!PACKED) {
+      return {t.kind, t.head + u * VPW, u * VPW < t.left};
+    } else {
+      const int kind = u < sq ? 0 : (u < sq + skv ? 1 : 2);
+      const int head = (u - (kind == 0 ? 0 : (kind == 1 ? sq : sq + skv))) * VPW + sub;
+      return {kind, head, u < a.chunk_u && head < (kind == 0 ? a.H : a.H_kv)};
+    }
   };
 
   // This lane's two times 8 bytes of the item's vectors.
   uint2 raw[kVecUnroll][2];
   auto load = [&](int m0, const Item& t) {
     const long m = m0 + t.r;
-    const __half* src = (t.kind == 0 ? a.Q + m * a.ldq : (t.kind == 1 ? a.K : a.V) + m * a.ldkv) + t.head * DH + c0;
+    const __half* const q = a.Q + m * a.ldq + c0;
+    const __half* const k = a.K + m * a.ldkv + c0;
+    const __half* const v = a.V + m * a.ldkv + c0;
+    const __half* const one = (t.kind == 0 ? q : (t.kind == 1 ? k : v)) + t.head * DH;
 #pragma unroll
     for (int u = 0; u < kVecUnroll; ++u) {
-      if (u * VPW < t.left) {
-        raw[u][0] = __ldcg(reinterpret_cast<const uint2*>(src + u * VPW * DH));
-        raw[u][1] = __ldcg(reinterpret_cast<const uint2*>(src + u * VPW * DH + DH / 2));
+      const Step s = step_of(t, u);
+      if (s.live) {
+        const __half* src = PACKED ? (s.kind == 0 ? q : (s.kind == 1 ? k : v)) + s.head * DH : one + u * VPW * DH;
+        raw[u][0] = __ldcg(reinterpret_cast<const uint2*>(src));
+        raw[u][1] = __ldcg(reinterpret_cast<const uint2*>(src + DH / 2));
       } else {
         raw[u][0] = raw[u][1] = make_uint2(0, 0);
       }
@@ -194,11 +217,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
           for (int v = lane; v < a.H * LPV; v += 32)
             *reinterpret_cast<uint4*>(a.Qo + m * a.ldqo + v * 8) = make_uint4(0, 0, 0, 0);
       } else {
-        __half* to = (t.kind == 0 ? a.Qo + m * a.ldqo
-                                  : (t.kind == 1 ? a.Kp : a.Vp) + static_cast<size_t>(max(dst, 0)) * KVD) +
-                     t.head * DH + c0;
-        const int left = t.kind != 0 && dst < 0 ? 0 : t.left;   // (no page: nothing is written)
-        if (NORM && t.kind != 2) {
+        __half* const q = a.Qo + m * a.ldqo + c0;
+        const size_t slot = static_cast<size_t>(max(dst, 0)) * KVD + c0;
+        __half* const one = (t.kind == 0 ? q : (t.kind == 1 ? a.Kp : a.Vp) + slot) + t.head * DH;
+        if (NORM && (PACKED || t.kind != 2)) {
           float2 cs[2], sn[2], neg[2], g[4];
           const float pos = pos_sh[t.r];
           rope_sincos2(pos, freqs.f[c0], freqs.f[c0 + 1], sn[0], cs[0]);
@@ -210,6 +232,12 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
 #pragma unroll
           for (int u = 0; u < kVecUnroll; ++u) {
             if (u >= a.chunk_u) break;   // warp-uniform
+            if (PACKED) {
+              const int kind = step_of(t, u).kind;
+              if (kind == 2) break;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) g[e] = kind == 0 ? gq[e] : gk[e];
+            }
             float2 x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -235,11 +263,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
           }
         }
 #pragma unroll
-        for (int u = 0; u < kVecUnroll; ++u)
-          if (u * VPW < left) {
-            *reinterpret_cast<uint2*>(to + u * VPW * DH) = raw[u][0];
-            *reinterpret_cast<uint2*>(to + u * VPW * DH + DH / 2) = raw[u][1];
+        for (int u = 0; u < kVecUnroll; ++u) {
+          const Step s = step_of(t, u);
+          if (s.live && (s.kind == 0 || dst >= 0)) {   // (no page: nothing is written)
+            __half* to = PACKED ? (s.kind == 0 ? q : (s.kind == 1 ? a.Kp : a.Vp) + slot) + s.head * DH : one + u * VPW * DH;
+            *reinterpret_cast<uint2*>(to) = raw[u][0];
+            *reinterpret_cast<uint2*>(to + DH / 2) = raw[u][1];
           }
+        }
       }
       item += kAppendWarps;
       t = item_at(item);
@@ -331,7 +362,7 @@ cudaError_t launch_append_dh(const PagedBatch& batch, const AppendParams& p, boo
                              const RopeFreqs& f, cudaStream_t stream) {
   AppendParams a = p;
   constexpr int vpw = 32 / (DH / 8);
-  const int steps = (norm ? (a.H + vpw - 1) / vpw : 0) + 2 * ((a.H_kv + vpw - 1) / vpw);   // of a row
+  const int sq = norm ? (a.H + vpw - 1) / vpw : 0, skv = (a.H_kv + vpw - 1) / vpw, steps = sq + 2 * skv;   // of a row
   // Few rows: one per CTA, its steps spread over the warps; many: as many as
   // share out the rows over two CTAs per SM.
   const int slots = 2 * num_sms();
@@ -340,8 +371,9 @@ cudaError_t launch_append_dh(const PagedBatch& batch, const AppendParams& p, boo
   a.chunk_u = std::min(kVecUnroll, std::max(1, steps * a.rows / kAppendWarps));
   const int blocks = (batch.M + a.rows - 1) / a.rows;
   const dim3 grid(std::min(blocks, slots)), block(32 * kAppendWarps);
-  return norm ? launch_pdl(paged_append_kernel<DH, true>, grid, block, 0, stream, batch, a, f)
-              : launch_pdl(paged_append_kernel<DH, false>, grid, block, 0, stream, batch, a, f);
+  if (!norm) return launch_pdl(paged_append_kernel<DH, false, false>, grid, block, 0, stream, batch, a, f);
+  return steps <= a.chunk_u ? launch_pdl(paged_append_kernel<DH, true, true>, grid, block, 0, stream, batch, a, f)
+                            : launch_pdl(paged_append_kernel<DH, true, false>, grid, block, 0, stream, batch, a, f);
 }
 
 // The frequencies of the thread's last call (128 powers in double take 6 us of
