@@ -64,7 +64,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_THRESHOLD = 8.0f, P_SHIFT = 7.0f;
 constexpr int kMaxCtas = 160;               // CTAs of a launch at most (workspace)
 constexpr int NPC = 4;                      // ring of pieces
-constexpr int kMaxCluster = 16, kMergeTiles = 4;
+constexpr int kMaxCluster = 16, kMergeTiles = 8;
 constexpr int kMaxSlots = 1 << 30;          // of a sequence (validate_paged_sizes)
 
 enum : int {
@@ -1271,6 +1271,16 @@ __device__ __forceinline__ Split load_split(const Split* from) {
   return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
+// Lanes along the rows of a unit of `all` rows: a power of two.
+__host__ __device__ inline int merge_pad(int all) {
+  int pad = 1;
+  while (pad < all && pad < 32) pad *= 2;
+  return pad;
+}
+__host__ __device__ inline int merge_warps(int parts) {   // of a task
+  return parts >= 32 ? 8 : (parts >= 16 ? 4 : (parts >= 8 ? 2 : 1));
+}
+
 template <int DH, int VV>
 __global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const Params p) {
   pdl_enter();
@@ -1281,10 +1291,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const 
   const Split u = load_split(p.split + blockIdx.x);
   if (__syncthreads_or(lost) || u.parts == 0) return;
   const int all = u.ntok << p.gshift;          // rows of the unit
-  const int pad = all >= 32 ? 32 : 1 << (31 - __clz(2 * all - 1));   // lanes along them: a power of two
+  const int pad = merge_pad(all);
   const int vecs = 32 / pad * VV;              // vectors of a task
   const int chunks = (DH / 4 + vecs - 1) / vecs, total = (all + 31) / 32 * chunks;
-  const int wp = u.parts >= 32 ? 8 : (u.parts >= 16 ? 4 : (u.parts >= 8 ? 2 : 1));   // warps of a task
+  const int wp = merge_warps(u.parts);
   const int sub = warp & (wp - 1), per = kMergeWarps / wp;
   for (int t0 = blockIdx.y * per; t0 < total; t0 += gridDim.y * per) {
     const int task = t0 + warp / wp;
@@ -1384,9 +1394,17 @@ cudaError_t launch_cfg(const CUtensorMap& tq, const CUtensorMap& tq32, const CUt
   if (cudaError_t e = launch_pdl(paged_attn_kernel<DH, NQ, MODE>, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, tq,
                                  tq32, tk, tv, p))
     return e;
-  // (of few rows a unit has 16 tasks at most)
-  if (p.rows <= 8) return launch_pdl(paged_merge_kernel<DH, 1>, dim3(ctas, DH == 256 ? 4 : 2), dim3(32 * kMergeWarps), 0, stream, p);
-  return launch_pdl(paged_merge_kernel<DH, 2>, dim3(ctas, 8), dim3(32 * kMergeWarps), 0, stream, p);
+  // CTAs per unit: one round of its tasks, as far as the host can tell, where units
+  // have many parts (a token over 130000 slots, one kv head of d_h = 256: 38 us with
+  // four CTAs, 35 with eight; a tree of 7 over 60000 44 with eight, 34 with 32); at
+  // most eight where there are many units.
+  const long long units = static_cast<long long>(p.batch.B) * p.H_kv * paged_units(p.batch.T_max, p.ts);
+  const int wp = merge_warps(static_cast<int>(4 * ctas / std::min<long long>(units, ctas)));   // (uneven units: of four times the mean)
+  const int vecs = 32 / merge_pad(p.rows) * (p.rows <= 8 ? 1 : 2);   // of a task
+  const int tasks = (p.rows + 31) / 32 * ((DH / 4 + vecs - 1) / vecs);
+  const dim3 grid(ctas, std::min((tasks * wp + kMergeWarps - 1) / kMergeWarps, wp > 1 ? 32 : 8)), block(32 * kMergeWarps);
+  return p.rows <= 8 ? launch_pdl(paged_merge_kernel<DH, 1>, grid, block, 0, stream, p)
+                     : launch_pdl(paged_merge_kernel<DH, 2>, grid, block, 0, stream, p);
 }
 
 // Clusters of `size` CTAs that the device holds at once, asked once per device.
@@ -1424,7 +1442,9 @@ int clusters_at_once(int size) {
 
 // CTAs of a unit's cluster, or 0: equal shares.  What a unit's tiles can be at
 // most is known here from the window and the page table's width; the equal
-// shares take fewer tiles per CTA and a merge, which costs kMergeTiles of them.
+// shares take fewer tiles per CTA and a merge, which costs kMergeTiles of them (a
+// tree of 7 over 16000 slots, one kv head of d_h = 256, 8 tiles per CTA: 20 us by
+// clusters, 24 shared out).
 template <int DH>
 int cluster_size(const Params& p) {
   const PagedBatch& b = p.batch;
