@@ -653,14 +653,15 @@ def test_t_max_beyond_the_rows(T_max, d_h):
         check_rows(got.cpu(), b, Q, pools, window, torch.float16)
 
 
+@pytest.mark.parametrize("tree", [True, False])
 @pytest.mark.parametrize("B", [31, 32, 33, 1025, 2500])
-def test_many_sequences(B):
+def test_many_sequences(B, tree):
     """Rows find their sequence among many, some of them without new tokens."""
     import transformer_attention_gb300 as G3
     g = torch.Generator().manual_seed(81)
     new = [0, 0] + torch.randint(0, 5, (B - 2,), generator=g).tolist()
     lens = torch.randint(0, 40, (B,), generator=g).tolist()
-    b = T.make_batch(lens, new, 16, 82, tree=True, behind=3)
+    b = T.make_batch(lens, new, 16, 82, tree=tree, behind=3)
     pos = torch.full((b["M"],), -5, dtype=torch.int32, device="cuda")
     G3.gemma3_paged_positions(T.dev_batch(b), pos)
     assert G3.gemma3_attn_check_status() == 0
