@@ -684,13 +684,14 @@ int gemma3_postnorm_residual(const float* a, const void* x, int x_dtype, const v
 
 /* Synchronises `stream`, reads and clears the device status word of the
  * current device.  Returns GEMMA3_OK, GEMMA3_ERR_TIMEOUT (a bounded wait in a
- * kernel expired), GEMMA3_ERR_BAD_INPUT (a kernel found invalid data), or
- * GEMMA3_ERR_CUDA (the stream reported an error). */
+ * kernel expired, whatever else was recorded), GEMMA3_ERR_BAD_INPUT (a kernel
+ * found invalid data), or GEMMA3_ERR_CUDA (the stream reported an error). */
 int gemma3_attn_check_status(void* stream);
 
 /* Raw device status word of the last check (0 = none; 0x1000 + n = wait site
- * n; 0x2000 = a token id outside [0, V); 0x4000 = a paged batch's row, length,
- * page, parent or accepted token out of its range). */
+ * n, of the first that expired; 0x2000 = a token id outside [0, V); 0x4000 = a
+ * paged batch's row, length, page, parent or accepted token out of its range; of
+ * several kinds the sum). */
 int gemma3_last_device_status(void);
 
 /* Human-readable text of a status code. */

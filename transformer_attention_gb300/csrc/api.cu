@@ -1454,7 +1454,7 @@ int gemma3_attn_check_status(void* stream) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g3_device_status, &zero, sizeof(int)) != cudaSuccess)
       return GEMMA3_ERR_CUDA;
-    return v >= kDevErrBadToken ? GEMMA3_ERR_BAD_INPUT : GEMMA3_ERR_TIMEOUT;
+    return (v & kDevErrTimeoutBase) != 0 ? GEMMA3_ERR_TIMEOUT : GEMMA3_ERR_BAD_INPUT;
   }
   return GEMMA3_OK;
 }

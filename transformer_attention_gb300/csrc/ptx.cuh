@@ -94,8 +94,14 @@ __device__ __forceinline__ uint64_t globaltimer() {
   return t;
 }
 
+// Adds `code` to the status word, whatever was recorded before it: an error of
+// the input as a bit, of the waits that gave up the bit that later kernels look
+// for and the first one's site.  (Two additions instead of a loop: the GEMMs'
+// registers stay as they were.)
 __device__ __forceinline__ void record_error(int* status, int code) {
-  atomicCAS(status, 0, code);
+  const int kind = code & (kDevErrTimeoutBase | kDevErrBadToken | kDevErrBadPaged);
+  const int was = atomicOr(status, kind);
+  if (kind != code && (was & kind) == 0) atomicOr(status, code);
 }
 
 // ---------------------------------------------------------------- mbarrier
