@@ -547,10 +547,12 @@ int gemma3_attn_paged_workspace_size(const gemma3_paged_batch* batch, int D, int
  * Projections, QK-norm, RoPE and query scale as gemma3_attn_forward at the
  * positions above; K' and V go to the pages as gemma3_paged_append writes them;
  * the tokens attend as gemma3_paged_attention does; output projection.  Rows of
- * out behind the last sequence are 0.
- *   After an error recorded on the device (by any call, until
+ * out behind the last sequence, and of a sequence that does not fit, are 0; the
+ * other sequences' rows and slots are what they would be without it, or beside
+ * one with a page outside the pool.
+ *   After a wait that gave up or a bad token id (recorded by any call, until
  * gemma3_attn_check_status) out is undefined, and the pages stay as they were
- * if it left the projections without a result. */
+ * if it left the projections without a result: the call can be made again. */
 int gemma3_attn_forward_paged(const gemma3_paged_batch* batch, int D, int H, int H_kv, int d_h,
                               const void* x, const void* Wq, const void* Wkv, const void* Wo,
                               const void* gamma_q, const void* gamma_k, int attn_type, int window,

@@ -989,9 +989,9 @@ int gemma3_attn_forward_cached8(const gemma3_attn_dims* dims, int S, int end_ind
   uint8_t* obuf = weight_sum != nullptr ? kvbuf + w.kv : qbuf;   // O bf16
   uint8_t* aws = kvbuf + w.kv + w.o;
   // More than kSkinnyMaxRows rows: the projections do not run after a recorded
-  // error of any kind, and rows that they did not write must not reach the
+  // bad token id either, and rows that they did not write must not reach the
   // cache (a block's scale would grow, its older numbers be rounded to it).
-  const int lost = M > kSkinnyMaxRows ? kLostAny : kLostWait;
+  const int lost = M > kSkinnyMaxRows ? kLostGemm : kLostWait;
   cudaStream_t s = as_stream(stream);
   const int win = attn_type == GEMMA3_LOCAL_SLIDING ? window : 0;
   if (project_qk(x, d->D, kBF16, Wq, Wkv, qbuf, kvbuf, gamma_q, gamma_k, segment_pos, M, d->D,
@@ -1234,8 +1234,10 @@ int gemma3_attn_forward_paged(const gemma3_paged_batch* batch, int D, int H, int
   cudaStream_t s = as_stream(stream);
   const PagedBatch b = as_batch(batch);
   // Rows that the projections did not write must not reach the pages: with
-  // more than kSkinnyMaxRows rows they do not run after an error of any kind.
-  const int lost = M > kSkinnyMaxRows ? kLostAny : kLostWait;
+  // more than kSkinnyMaxRows rows they do not run after a bad token id either.
+  // (Neither mask has the error that these kernels record themselves, so that a
+  // sequence or page that does not fit costs the others nothing.)
+  const int lost = M > kSkinnyMaxRows ? kLostGemm : kLostWait;
   cudaError_t e;
   if (linear_qknorm_fusable(M, HD, HD, d_h) && linear_qknorm_fusable(M, 2 * KVD, KVD, d_h)) {
     // Norm and rotation in the projections' epilogue; the append only copies.

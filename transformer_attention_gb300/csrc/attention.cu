@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     int* status) {
   pdl_enter();
   using C = Cfg<DH, G>;
-  // After a CTA of this or an earlier launch gave up, the rest do no work.
-  if (*reinterpret_cast<volatile int*>(status) != 0) return;
+  // After a CTA of this or an earlier launch gave up (or a bad token id), the rest do no work.
+  if (lost_work(status, kLostGemm)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   extern __shared__ uint8_t smem_raw[];

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                      int num_items, unsigned int* sched, int* status) {
   pdl_enter();
   constexpr int TQ = BM / G;
-  if (*reinterpret_cast<volatile int*>(status) != 0) return;
+  if (lost_work(status, kLostGemm)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   extern __shared__ uint8_t smem_raw[];

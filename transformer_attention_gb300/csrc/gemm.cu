@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr uint32_t STAGE_BYTES = Ring<HALVES>::STAGE_BYTES;
   constexpr int BN_OUT = GEGLU ? BN / 2 : BN;   // output columns per tile
   constexpr int CW = 128 / static_cast<int>(sizeof(OutT));   // output columns per 128 B chunk
-  // A kernel launched after an earlier one gave up does no work.
-  if (*reinterpret_cast<volatile int*>(status) != 0) return;
+  // A kernel launched after an earlier one gave up, or found a bad token id, does no work.
+  if (lost_work(status, kLostGemm)) return;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));

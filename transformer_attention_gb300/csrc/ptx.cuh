@@ -23,11 +23,13 @@ enum : int {
 };
 
 // What a recorded error may have left undone, as masks of the status word: a
-// wait that gave up, the work behind it; any error, also what the kernels
-// skip that start with the word set (the GEMMs).
+// wait that gave up, the work behind it; that and a bad token id, also what the
+// GEMMs and the prompts' attention skip, which do not start after them.  A paged
+// batch that does not fit stops nothing: its kernels leave out the sequence or
+// page that they found, and compute the rest.
 enum : int {
   kLostWait = kDevErrTimeoutBase,
-  kLostAny = kDevErrTimeoutBase | kDevErrBadToken | kDevErrBadPaged
+  kLostGemm = kDevErrTimeoutBase | kDevErrBadToken
 };
 
 // Has an error of `mask` been recorded?
