@@ -301,6 +301,70 @@ def test_units_against_the_masks(tmp_path):
             total += tiles
 
 
+WHOLE = r"""
+#include "paged.cuh"
+#include <cstdio>
+#include <vector>
+int main() {   // a batch per line: CTAs, kv heads, window, tree, ts, a unit's cost, sequences, their lengths and new tokens
+  int grid, heads, w, tree, ts, unit_cost, B;
+  while (scanf("%d %d %d %d %d %d %d", &grid, &heads, &w, &tree, &ts, &unit_cost, &B) == 7) {
+    std::vector<int> len(B), n(B);
+    long long all = 0, exact = 0, taken = 0;
+    int units = 0, longest = 0;
+    for (int b = 0; b < B; ++b) {
+      if (scanf("%d %d", &len[b], &n[b]) != 2) return 1;
+      if (n[b] == 0) continue;
+      const int nq = g3::paged_units(n[b], ts);
+      all += heads * (g3::kTileCost * g3::paged_prefix(len[b], n[b], w, tree, ts, nq) + (long long)unit_cost * nq);
+      exact += (long long)heads * nq;
+      units += g3::paged_count_units(n[b], ts, heads);
+      const int t = g3::paged_most_tiles(len[b], n[b], w, tree, ts);
+      if (t > longest) longest = t;
+    }
+    const g3::PagedWhole p = g3::paged_whole(all, units, longest, grid, w);
+    for (int b = 0; b < B; ++b)
+      taken += (long long)heads * g3::paged_units(n[b], ts) * g3::paged_whole_shares(p, len[b], n[b], w, tree, ts);
+    printf("%d %lld %lld %d\n", p.uncut, taken, exact, g3::kMaxCtas);
+  }
+}
+"""
+
+
+def test_whole_shares_fit_the_ctas(tmp_path):
+    """What CTAs take whole is no more than there are CTAs: all units where they
+    stay uncut, and else shares that leave a CTA for the rest."""
+    src, exe = tmp_path / "whole.cu", tmp_path / "whole"
+    src.write_text(WHOLE)
+    subprocess.run([_nvcc(), "-std=c++17", "-I", CSRC, "-I", INCLUDE, "-o", str(exe), str(src)], check=True,
+                   capture_output=True, env=dict(os.environ))
+    rng = random.Random(5)
+    lines, grids = [], []
+    for grid in (1, 7, 132, 152, 159, 160):
+        # one sequence of many units, beside ones without new tokens
+        for n in (64 * k + d for k in (1, 9, 10, 11, 32, 200) for d in (-1, 0, 1)):
+            for window in (0, 100):
+                lines.append(f"{grid} 16 {window} 0 6 5 3 0 0 5 {n} 9 0")
+                grids.append(grid)
+        for _ in range(300):
+            tree, B = rng.random() < 0.2, rng.choice([1, 2, 5, 40])
+            top = 64 if tree else rng.choice([1, 60, 300, 5000])
+            lens = [rng.choice([0, 100, 4000, 60000]) + rng.randint(0, 300) for _ in range(B)]
+            new = [rng.choice([0, 1, rng.randint(1, top)]) for _ in range(B)]
+            lines.append(f"{grid} {rng.choice([1, 4, 16])} {rng.choice([0, 0, 1, 700])} {int(tree)} {rng.randint(5, 8)} "
+                         f"5 {B} " + " ".join(f"{a} {c}" for a, c in zip(lens, new)))
+            grids.append(grid)
+    out = subprocess.run([str(exe)], input="\n".join(lines), text=True, capture_output=True,
+                         check=True).stdout.splitlines()
+    assert len(out) == len(lines)
+    seen = set()
+    for line, grid, got in zip(lines, grids, out):
+        uncut, taken, units, most = map(int, got.split())
+        assert grid <= most
+        assert taken == units <= grid if uncut else taken < grid, line
+        seen.add((uncut, taken > 0))
+    assert seen >= {(1, True), (0, True), (0, False)}
+
+
 @pytest.mark.parametrize("name", ["rows", "T_max", "page_size", "n_pages"])
 def test_sizes_beyond_32_bits_are_refused(name):
     sizes = dict(rows=3, T_max=2, page_size=16, n_pages=8)

@@ -182,4 +182,55 @@ __host__ __device__ inline long long paged_prefix(int len, int n, int window, bo
   return sum;
 }
 
+// ---------------------------------------------------------------- whole shares
+constexpr int kTileCost = 2;        // of a tile, in the shares of the work
+constexpr int kMaxCtas = 160;       // CTAs of a launch at most (workspace)
+
+// Units of all heads of a sequence; more than any launch has CTAs count as one more.
+__host__ __device__ inline int paged_count_units(int n, int ts, int H_kv) {
+  constexpr int most = kMaxCtas + 1;
+  const int nq = paged_units(n, ts), units = H_kv * (nq < most ? nq : most);
+  return units < most ? units : most;
+}
+
+// Tiles of a unit of a sequence at most: with a window no unit has more than the
+// slots that its tokens reach.
+__host__ __device__ inline int paged_most_tiles(int len, int n, int window, bool tree, int ts) {
+  const int t = (len + n + kPagedTile - 1) >> kTileShift;
+  if (window <= 0) return t;
+  const int w = static_cast<int>((static_cast<long long>(window) + (tree ? n : 1 << ts) + 2 * kPagedTile) >> kTileShift);
+  return t < w ? t : w;
+}
+
+// Tiles that a CTA does rather than having the units cut into `parts`: a part of
+// 128 x 256 or 256 x 128 sums takes 65 ns of the device, written and added, a
+// tile 1.6 us (128 units of 64 tiles, 27B-shaped: 118 us cut, 115 whole; of 20
+// tiles 59 and 53).
+__host__ __device__ constexpr int uncut_tiles(int parts) { return 3 + parts / 24; }
+
+// What CTAs take whole: every unit (uncut), or shares of so many tiles from the
+// first tile of every unit on (0: nothing).
+struct PagedWhole {
+  int tiles;
+  bool uncut;
+};
+
+// all: the units' cost; units: the sum of paged_count_units; longest: of paged_most_tiles.
+__host__ __device__ inline PagedWhole paged_whole(long long all, int units, int longest, int grid, int window) {
+  const long long per_cta =
+      all < 1 << 30 ? (static_cast<unsigned>(all) + static_cast<unsigned>(grid * kTileCost) - 1) / static_cast<unsigned>(grid * kTileCost)
+                    : (all + grid * kTileCost - 1) / (grid * kTileCost);
+  const long long parts = all / kTileCost < grid + units ? all / kTileCost : grid + units;
+  PagedWhole w;
+  w.uncut = units <= grid && longest <= per_cta + uncut_tiles(static_cast<int>(parts));
+  w.tiles = window == 0 && all > 0 && !w.uncut ? static_cast<int>(per_cta) : 0;
+  return w;
+}
+
+// Whole shares of every unit of a sequence (no window: a unit's tiles grow with its number).
+__host__ __device__ inline int paged_whole_shares(const PagedWhole& w, int len, int n, int window, bool tree, int ts) {
+  if (w.uncut) return n > 0 ? 1 : 0;
+  return w.tiles == 0 || n == 0 ? 0 : paged_unit(len, n, window, tree, ts, 0).tiles / w.tiles;
+}
+
 }  // namespace g3

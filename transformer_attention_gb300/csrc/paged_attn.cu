@@ -54,7 +54,6 @@ constexpr int BM = 128, BN = kPagedTile;
 constexpr uint32_t CHUNK = 128 * 128;       // 128 rows x 64 channels (128 B), swizzled
 constexpr uint32_t PART = 32768;
 constexpr uint32_t QSMALL = 32 * 128;       // 32 rows of a chunk: Q of few rows (the MMA reads on behind them)
-constexpr int kTileCost = 2;                // shares of the work
 constexpr uint32_t O_COL = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 // A row's reference stays P_SHIFT below a past maximum while the present one
@@ -62,7 +61,6 @@ constexpr float LOG2E = 1.4426950408889634f;
 // that are rounded to fp16 reach 2^15, so that those below its normal range, off
 // by 2^-25, are off by 2^-32 at most of the row's largest.
 constexpr float RESCALE_THRESHOLD = 8.0f, P_SHIFT = 7.0f;
-constexpr int kMaxCtas = 160;               // CTAs of a launch at most (workspace)
 constexpr int NPC = 4;                      // ring of pieces
 constexpr int kMaxCluster = 16, kMergeTiles = 8;
 constexpr int kMaxSlots = 1 << 30;          // of a sequence (validate_paged_sizes)
@@ -131,12 +129,6 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   }
   return true;
 }
-
-// Tiles that a CTA does rather than having the units cut into `parts`: a part of
-// 128 x 256 or 256 x 128 sums takes 65 ns of the device, written and added, a
-// tile 1.6 us (128 units of 64 tiles, 27B-shaped: 118 us cut, 115 whole; of 20
-// tiles 59 and 53).
-__host__ __device__ constexpr int uncut_tiles(int parts) { return 3 + parts / 24; }
 
 template <int DH, int NQ_>
 struct Cfg {
@@ -334,12 +326,12 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
   // position kUnitCost + t kTileCost.
   constexpr int TC = kTileCost, UC = ONE ? C::UC1 : C::UCG;
   const int per = CLUSTER ? 0 : (batch.B + C::THREADS - 1) / C::THREADS;   // sequences per thread
-  int S = 0;                  // tiles of a whole share (0: there are none)
-  bool uncut = false;         // every unit is one CTA's share
+  PagedWhole share_of_all = {0, false};   // (ONE: there are no whole shares)
+  const int& S = share_of_all.tiles;
+  const bool& uncut = share_of_all.uncut;
   // whole shares of every unit of a sequence
   auto shares_of = [&](const PagedSeq& s) -> int {
-    if (uncut) return s.n > 0 ? 1 : 0;
-    return ONE || S == 0 || s.n == 0 ? 0 : paged_unit(s.len, s.n, p.window, tree, p.ts, 0).tiles / S;
+    return ONE ? 0 : paged_whole_shares(share_of_all, s.len, s.n, p.window, tree, p.ts);
   };
   // cost of what is left of a kv head's first q units
   auto cost_of = [&](const PagedSeq& s, int whole, int q) -> long long {
@@ -381,12 +373,8 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     mine += p.H_kv * head_cost(seq);
     if constexpr (!ONE) {
       if (seq.n == 0) continue;
-      // (units beyond a CTA's number count as so many; with a window no unit has
-      // more than the slots that its tokens reach)
-      units += min(p.H_kv * min(paged_units(seq.n, p.ts), kMaxCtas), kMaxCtas);
-      int t = (seq.len + seq.n + BN - 1) >> kTileShift;
-      if (p.window > 0) t = min(t, static_cast<int>((static_cast<long long>(p.window) + (tree ? seq.n : 1 << p.ts) + 2 * BN) >> kTileShift));
-      longest = max(longest, t);
+      units += paged_count_units(seq.n, p.ts, p.H_kv);
+      longest = max(longest, paged_most_tiles(seq.len, seq.n, p.window, tree, p.ts));
     }
   }
   long long total = 0;
@@ -424,17 +412,11 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, 1)
     if (tid == 0) p.split[blockIdx.x].parts = 0;   // (the error may be cleared before the merge starts)
     return;
   }
-  // Whole shares: CTAs 0 .. taken - 1.  (No window: a unit's tiles grow with
-  // its number.)  What all shares and units cost leaves at least one CTA over.
+  // Whole shares: CTAs 0 .. taken - 1.  What all shares and units cost leaves at
+  // least one CTA over.
   int taken = 0, grid = gridDim.x, taken_mine = 0, taken_upto = 0;
   if constexpr (!ONE) {
-    const long long all = total;
-    const long long per_cta =
-        all < 1 << 30 ? (static_cast<unsigned>(all) + static_cast<unsigned>(grid * TC) - 1) / static_cast<unsigned>(grid * TC)
-                      : (all + grid * TC - 1) / (grid * TC);
-    uncut = units <= grid &&
-            longest <= per_cta + uncut_tiles(static_cast<int>(min(all / TC, static_cast<long long>(grid + units))));
-    if (p.window == 0 && all > 0 && !uncut) S = static_cast<int>(per_cta);
+    share_of_all = paged_whole(total, units, longest, grid, p.window);
     mine = 0;
     __syncthreads();
     for (int k = 0; k < per; ++k) {
