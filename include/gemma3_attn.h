@@ -480,7 +480,7 @@ typedef struct {
 enum { GEMMA3_TREE_MAX = 64 };
 
 /* segment_pos [M] int32: every row's position (0 behind the last sequence), as
- * the projection entry points take them. */
+ * the projection entry points take them.  It must not overlap the batch's arrays. */
 int gemma3_paged_positions(const gemma3_paged_batch* batch, int32_t* segment_pos, void* stream);
 
 /* The new tokens' K' and V to their slots, with the norm and the rotation on

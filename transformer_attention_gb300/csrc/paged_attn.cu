@@ -11,8 +11,9 @@
 // ring of 32 KB parts, 160 KB in flight per SM, and each 128-slot tile costs 1100
 // (d_h = 128) or 2200 clocks of MMA however few its rows, against 2800 or 5600
 // for its bytes at the HBM rate.  Measured: a token over 131071 slots, 27B-shaped,
-// 161.5 us (1.07 GB: 98% of the copy rate); 1024 tokens over 31744 slots 383 us (1.41 PFLOP/s: of a tile pair's
-// 3100 clocks 2048 are MMA, as in attention_pair.cu).
+// 158 to 163 us (1.07 GB: 97 to 100% of the copy rate); 1024 tokens over 31744 slots
+// 385 to 397 us with the clocks that the power limit leaves (1.36 to 1.41 PFLOP/s:
+// of a tile pair's 3100 clocks 2048 are MMA).
 //
 // Sequences have lengths of their own, known on the device alone: each CTA adds
 // up the work of all units and takes an equal share of it, cut wherever it
@@ -1426,7 +1427,9 @@ int clusters_at_once(int size) {
 // most is known here from the window and the page table's width; the equal
 // shares take fewer tiles per CTA and a merge, which costs kMergeTiles of them (a
 // tree of 7 over 16000 slots, one kv head of d_h = 256, 8 tiles per CTA: 20 us by
-// clusters, 24 shared out).
+// clusters, 24 shared out).  A table wider than the slots are filled looks like
+// longer units: a tree of 7 over 5003 slots takes 13 us by clusters while the table
+// has up to 8192, and 21 to 22 us shared out from 16384 on.
 template <int DH>
 int cluster_size(const Params& p) {
   const PagedBatch& b = p.batch;
@@ -1439,7 +1442,8 @@ int cluster_size(const Params& p) {
   // What equal shares would take per CTA: of an uneven batch at most so many
   // units have tokens, and where only the table bounds the lengths of several
   // sequences, half of it is taken to be filled (8 steps over 100 to 6000 slots,
-  // 12B-shaped: 52 us by clusters, 28 shared out; over 3000 each 24 and 27).
+  // 12B-shaped: 44 us by clusters, 34 shared out; over 3000 each 35 and 40; trees of
+  // 7 over 500, 2000, 7000 and 16000, 4B-shaped: 39 and 31).
   const long long filled = std::min(units, ((b.M >> p.ts) + static_cast<long long>(b.B)) * p.H_kv);
   const bool open = b.B > 1 && p.window == 0;
   const int sms = num_sms();
